@@ -88,6 +88,7 @@ typedef enum pa_status {
 #define PA_DEVERR_SLOT 4     /* slot >= num_blocks * block_size */
 #define PA_DEVERR_PAIR 8     /* copy pair with a block id outside [0, num_blocks) */
 #define PA_DEVERR_TIMEOUT 16 /* an on-chip wait gave up (bounded waits only) */
+#define PA_DEVERR_ROW 32     /* weight row outside [0, num_rows), or an eviction names it twice */
 
 /* Shape of one paged-attention call.  head_dim in {64, 128}; block_size in
  * {16, 32}; num_q_heads a multiple of num_kv_heads with a group of at most 16.
@@ -314,6 +315,151 @@ int pa_paged_attention_mixed(const pa_decode_desc *prefill_desc, const void *pre
                              size_t workspace_bytes, const void *k_pool, const void *v_pool, int32_t *err_flag,
                              void *stream);
 
+/* ------------------------------------------------------------------------
+ * Long contexts: block-sparse decode and eviction [PHASE] (decode reads the
+ * whole cache for each new token, and the cache grows with the context).  No
+ * page describes these calls.
+ *
+ * Block-sparse decode attends, for each (sequence, kv head), only the blocks
+ * that a cheap score of the step's queries selects:
+ *   pa_block_key_bounds  after a cache write: the written blocks' bounds
+ *   pa_select_blocks     each step: the blocks of every (sequence, kv head)
+ *   pa_paged_attention_decode_sparse   attention over those
+ * Eviction shortens the cache itself:
+ *   pa_paged_attention_decode_weights  decode, and every key's weight summed
+ *   pa_evict_tokens      now and then: the heaviest keys stay, compacted
+ *   pa_bm_evict          the block manager's part of it
+ * ------------------------------------------------------------------------ */
+
+/* Channel-wise bounds of every block's keys:
+ *   bounds[b][h][0][d] = min over the block's cached tokens of k[d],
+ *   bounds[b][h][1][d] = max,                      exact bf16 values,
+ * for b the physical block of every logical block of sequence s from
+ * start_lens[s] / B to the last one, tokens 0 .. context_lens[s]-1 counting.
+ * A block that start_lens[s] falls into is taken whole.  A NaN key makes both
+ * bounds of its channel NaN.  Sequences may share blocks (of which they hold
+ * the same tokens).
+ *   k_pool      device bf16 pool; num_q_heads and scale of desc are not used
+ *               (but must be valid: num_q_heads = num_kv_heads will do)
+ *   start_lens  device int32 [num_seqs], tokens whose blocks' bounds are up to
+ *               date (a step's context - 1), or NULL for 0
+ *   max_new_tokens  bound on every context_lens[s] - start_lens[s] (sizes the
+ *               grid)
+ *   bounds      device bf16 [num_blocks][num_kv_heads][2][head_dim], 16-byte
+ *               aligned; blocks that are not touched keep theirs
+ * A bad context, a start outside [0, context] or more than max_new_tokens
+ * tokens set PA_DEVERR_CTX and leave the sequence's bounds as they are; a
+ * block-table entry outside the pool sets PA_DEVERR_PAGE and is skipped. */
+int pa_block_key_bounds(const pa_decode_desc *desc, const void *k_pool, const int32_t *block_tables,
+                        const int32_t *context_lens, const int32_t *start_lens, int max_new_tokens, void *bounds,
+                        int32_t *err_flag, void *stream);
+
+/* Bytes of device workspace pa_select_blocks needs; 0 for an invalid desc. */
+size_t pa_select_blocks_workspace_bytes(const pa_decode_desc *desc);
+
+/* The blocks that each (sequence, kv head) attends this step: its first
+ * sink_blocks, its last recent_blocks, and of the others those with the
+ * largest scores, num_select in all (every block of a context that has no
+ * more).  The score of logical block i for kv head h,
+ *   max over its query heads g of  sum_d  q_gd > 0 ? q_gd hi_d : q_gd < 0 ? q_gd lo_d : 0
+ * with (lo, hi) the block's bounds, is the least upper bound on q_g.k over
+ * keys within the bounds.  Blocks are ranked by the scores' exact values
+ * (fp32 where it can tell two blocks apart, else in 64 bits), ties to the lower
+ * index; a NaN score ranks as +infinity (so that attention reports it).
+ * The desc's scale is taken as positive and not used.
+ *   q         device bf16 [num_seqs][num_q_heads][head_dim]
+ *   bounds    device, of pa_block_key_bounds
+ *   selected  device int32 [num_seqs][num_kv_heads][num_select]: logical block
+ *             indices in increasing order, then -1
+ *   workspace >= pa_select_blocks_workspace_bytes(desc), 16-byte aligned, any
+ *             contents; calls that may overlap on the GPU must not share one
+ * sink_blocks + recent_blocks must not exceed num_select.  A sequence with a
+ * bad context gets -1 throughout and PA_DEVERR_CTX.  A block whose table entry
+ * is outside the pool sets PA_DEVERR_PAGE and ranks below all others.
+ * recent_blocks >= 1 keeps the block being filled in the list. */
+int pa_select_blocks(const pa_decode_desc *desc, const void *q, const void *bounds, const int32_t *block_tables,
+                     const int32_t *context_lens, int num_select, int sink_blocks, int recent_blocks,
+                     int32_t *selected, void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* Bytes of device workspace pa_paged_attention_decode_sparse needs (0 when no
+ * list is split); 0 for an invalid desc. */
+size_t pa_decode_sparse_workspace_bytes(const pa_decode_desc *desc, int num_select);
+
+/* Decode attention over listed blocks: as pa_paged_attention_decode, with the
+ * sum over the keys j < context_lens[s] of the blocks
+ * selected[s][h][0 .. num_select-1] (logical indices, any order; -1 for none)
+ * of each kv head h.  A block listed twice counts twice.  A list without
+ * blocks gives zero rows.  An index that is neither -1 nor one of the
+ * context's blocks is left out and sets PA_DEVERR_PAGE.
+ *   selected   device int32 [num_seqs][num_kv_heads][num_select]
+ *   workspace  >= pa_decode_sparse_workspace_bytes(desc, num_select)
+ * Other arguments and errors as in pa_paged_attention_decode. */
+int pa_paged_attention_decode_sparse(const pa_decode_desc *desc, const void *q, const void *k_pool,
+                                     const void *v_pool, const int32_t *block_tables, const int32_t *context_lens,
+                                     const int32_t *selected, int num_select, void *out, void *workspace,
+                                     size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* Bytes of device workspace pa_paged_attention_decode_weights needs (decode
+ * split-K scratch, and 4 bytes a query head and token of num_seqs contexts of
+ * max_context_len); 0 for an invalid desc. */
+size_t pa_decode_weights_workspace_bytes(const pa_decode_desc *desc);
+
+/* Decode attention that also sums every key's attention weight: out as
+ * pa_paged_attention_decode, and for every kv head h and token j of the
+ * sequences s with row r = weight_rows[s],
+ *   weights_out[r][h][j] = weights[r][h][j] + sum_s sum_g p_sgj,
+ * p the softmax weights (fp32) of h's query heads g, j < context_lens[s].
+ * Positions that no context of the row reaches are not written.  A row is
+ * summed in the order of its sequences: several entries may name one row (the
+ * last queries of a prompt, each with its own context, over one block table).
+ *   weights, weights_out  device fp32 [num_rows][num_kv_heads][max_tokens],
+ *                16-byte aligned; the same pointer updates in place, otherwise
+ *                they must not overlap.  A new sequence's row starts as zeros;
+ *                pa_evict_tokens leaves zeros behind the tokens it keeps.
+ *   weight_rows  device int32 [num_seqs], or NULL: row s (num_rows >= num_seqs)
+ *   max_tokens   >= max_context_len
+ *   workspace    >= pa_decode_weights_workspace_bytes(desc), 16-byte aligned
+ * A row outside [0, num_rows) sets PA_DEVERR_ROW and is not written.  A
+ * sequence with a bad context adds nothing.  Other arguments and errors as in
+ * pa_paged_attention_decode. */
+int pa_paged_attention_decode_weights(const pa_decode_desc *desc, const void *q, const void *k_pool,
+                                      const void *v_pool, const int32_t *block_tables, const int32_t *context_lens,
+                                      const float *weights, float *weights_out, const int32_t *weight_rows,
+                                      int num_rows, int max_tokens, void *out, void *workspace,
+                                      size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* Eviction by accumulated weight.  Every kv head h of sequence s keeps
+ * n = min(keep_lens[s], context_lens[s]) tokens: the first sink_tokens, the last
+ * recent_tokens, and of the others those with the largest
+ * weights[weight_rows[s]][h][j], ties to the lower j (NaN ranks above all).  With
+ * kept[s][h] those tokens in increasing order, for i < n
+ *   slot i of dst_tables[s]        := slot kept[s][h][i] of block_tables[s], K and V
+ *   weights_out[r][h][i]           := weights[r][h][kept[s][h][i]]
+ * and weights_out[r][h][n .. context-1] := 0, new_lens[s] := n.  Each kv head
+ * keeps its own tokens; attention over the n slots is that over those tokens.
+ * Block bounds of the written blocks are stale until pa_block_key_bounds.
+ *   dst_tables  device int32 [num_seqs][max_blocks_per_seq], or NULL: in place.
+ *               Entry i of a row is block_tables' own entry i or a block that no
+ *               table of the call reads (pa_bm_evict hands out such tables: shared
+ *               blocks are replaced, own ones stay).  No block is a destination
+ *               of two sequences, or a destination of one and read by another.
+ *   keep_lens   device int32 [num_seqs], 1 .. max_keep_len
+ *   weights, weights_out, weight_rows, num_rows, max_tokens  as in
+ *               pa_paged_attention_decode_weights
+ *   kept        device int32 [num_seqs][num_kv_heads][max_keep_len], -1 past n
+ *   new_lens    device int32 [num_seqs], not context_lens itself
+ * num_q_heads and scale of desc are not used (but must be valid).  A bad
+ * context, a keep_len outside 1 .. max_keep_len or below sink + recent where
+ * tokens would go (PA_DEVERR_CTX), and a row out of range or named by an earlier
+ * sequence of the call (PA_DEVERR_ROW), leave the sequence as it is: kept -1,
+ * new_lens[s] = context_lens[s].  A token whose source or destination block is
+ * outside the pool is not moved (PA_DEVERR_PAGE). */
+int pa_evict_tokens(const pa_decode_desc *desc, void *k_pool, void *v_pool, const int32_t *block_tables,
+                    const int32_t *dst_tables, const int32_t *context_lens, const int32_t *keep_lens,
+                    int max_keep_len, int sink_tokens, int recent_tokens, const float *weights, float *weights_out,
+                    const int32_t *weight_rows, int num_rows, int max_tokens, int32_t *kept, int32_t *new_lens,
+                    int32_t *err_flag, void *stream);
+
 /* Writes the K/V of num_tokens new tokens into their cache slots [PHASE][SHARE]:
  *   k_pool[slot / B][h][slot % B][:] = k[t][h][:]  (same for v), for t in order.
  * Bit-exact copy.  slot < 0: token skipped.  slot >= num_blocks*B: skipped and
@@ -509,6 +655,22 @@ int pa_bm_swap_out(pa_bm *bm, int seq_id, int64_t *pairs_out, int cap, int *n);
  * block) pairs for pa_swap_blocks (host pools -> device pools); the host
  * blocks are freed.  PA_ERR_OOM leaves everything unchanged. */
 int pa_bm_swap_in(pa_bm *bm, int seq_id, int64_t *pairs_out, int cap, int *n);
+
+/* The block manager's part of an eviction (pa_evict_tokens): seq_id keeps
+ * keep_len (>= 1) tokens.  Writes the table that the kept tokens move into, *n =
+ * ceil(keep_len / B) entries, to dst_out[0..cap-1]: each of the sequence's first
+ * *n blocks, or a fresh block in the place of one with ref_count > 1 (whose count
+ * drops by one).  The sequence then holds those blocks and keep_len tokens; its
+ * other blocks are released, its own blocks among the kept ones leave the prefix
+ * cache (their content changes), and none of its later blocks enters it.  The
+ * source table for pa_evict_tokens is pa_bm_block_table's before this call; its
+ * launches must precede, on the stream, any that writes a released block.
+ * keep_len >= the sequence's length changes nothing and returns its table.
+ * PA_ERR_STATE (unknown or swapped-out id), PA_ERR_INVALID (keep_len < 1, cap < *n
+ * -- *n is set -- or null pointers) and PA_ERR_OOM (not enough free blocks for the
+ * fresh ones, of which none may be a released one: those are still read) leave
+ * everything unchanged. */
+int pa_bm_evict(pa_bm *bm, int seq_id, int keep_len, int32_t *dst_out, int cap, int *n);
 
 /* Number of free host blocks. */
 int pa_bm_num_free_host(const pa_bm *bm);

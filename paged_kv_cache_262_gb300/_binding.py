@@ -18,7 +18,7 @@ _P = _c.c_void_p
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_OOM, PA_ERR_WORKSPACE, PA_ERR_STATE = (
     0, -1, -2, -3, -4, -5, -6)
-DEVERR_CTX, DEVERR_PAGE, DEVERR_SLOT, DEVERR_PAIR, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
+DEVERR_CTX, DEVERR_PAGE, DEVERR_SLOT, DEVERR_PAIR, DEVERR_TIMEOUT, DEVERR_ROW = 1, 2, 4, 8, 16, 32
 
 # Every symbol include/pagedattn.h declares.
 EXPORTS = (
@@ -33,6 +33,9 @@ EXPORTS = (
     "pa_bm_block_table", "pa_bm_seq_len", "pa_bm_ref_count", "pa_bm_num_free", "pa_bm_wasted_slots",
     "pa_bm_append_batch", "pa_bm_block_tables", "pa_bm_append_token", "pa_hbm_probe",
     "pa_selftest_bounded_wait",
+    "pa_block_key_bounds", "pa_select_blocks_workspace_bytes", "pa_select_blocks",
+    "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
+    "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens", "pa_bm_evict",
 )
 
 
@@ -143,6 +146,25 @@ def load(path: Optional[str] = None):
         lib.pa_hbm_probe.argtypes = [_P, _P, sz, i, _P, _P, _P]
         lib.pa_selftest_bounded_wait.restype = i
         lib.pa_selftest_bounded_wait.argtypes = [_c.c_longlong, _P, _P, _P]
+        D = _c.POINTER(DecodeDesc)
+        lib.pa_block_key_bounds.restype = i
+        lib.pa_block_key_bounds.argtypes = [D, _P, _P, _P, _P, i, _P, _P, _P]
+        lib.pa_select_blocks_workspace_bytes.restype = sz
+        lib.pa_select_blocks_workspace_bytes.argtypes = [D]
+        lib.pa_select_blocks.restype = i
+        lib.pa_select_blocks.argtypes = [D, _P, _P, _P, _P, i, i, i, _P, _P, sz, _P, _P]
+        lib.pa_decode_sparse_workspace_bytes.restype = sz
+        lib.pa_decode_sparse_workspace_bytes.argtypes = [D, i]
+        lib.pa_paged_attention_decode_sparse.restype = i
+        lib.pa_paged_attention_decode_sparse.argtypes = [D, _P, _P, _P, _P, _P, _P, i, _P, _P, sz, _P, _P]
+        lib.pa_decode_weights_workspace_bytes.restype = sz
+        lib.pa_decode_weights_workspace_bytes.argtypes = [D]
+        lib.pa_paged_attention_decode_weights.restype = i
+        lib.pa_paged_attention_decode_weights.argtypes = [D, _P, _P, _P, _P, _P, _P, _P, _P, i, i, _P, _P, sz, _P, _P]
+        lib.pa_evict_tokens.restype = i
+        lib.pa_evict_tokens.argtypes = [D, _P, _P, _P, _P, _P, _P, i, i, i, _P, _P, _P, i, i, _P, _P, _P, _P]
+        lib.pa_bm_evict.restype = i
+        lib.pa_bm_evict.argtypes = [_P, i, i, _c.POINTER(_c.c_int32), i, _c.POINTER(i)]
         if path is None:
             _LIB = lib
         return lib
@@ -567,6 +589,234 @@ def swap_blocks(src_k_pools: Sequence, src_v_pools: Sequence, dst_k_pools: Seque
     _check(st, "pa_swap_blocks")
 
 
+# --------------------------------------------------------------- long contexts
+_WS_SELECT, _WS_SPARSE, _WS_WEIGHTS = {}, {}, {}
+
+
+def _new(shape, dtype, device, stream):
+    """An output tensor that belongs to the stream the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call_ws(cache, need, device, stream):
+    """The workspace of a call that was given none: cached per (device,
+    stream), except under graph capture, where the graph's own memory holds
+    it -- a replay must not share the cache with the calls outside it."""
+    import torch
+    if need and torch.cuda.is_current_stream_capturing():
+        return _new((need,), torch.uint8, device, stream)
+    return _cached_ws(cache, need, device, stream) if need else None
+
+
+def _cache_args(k_pool, block_tables, context_lens, v_pool=None):
+    import torch
+    _need(k_pool, torch.bfloat16, "k_pool", 4)
+    if v_pool is not None:
+        _need(v_pool, torch.bfloat16, "v_pool", 4)
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _need(context_lens, torch.int32, "context_lens", 1)
+
+
+def _cache_desc(k_shape, block_tables, S, max_context_len) -> DecodeDesc:
+    """The desc of a call without queries."""
+    nblk, hkv, bs, d = k_shape
+    mb = int(block_tables.shape[1])
+    return DecodeDesc(int(S), int(hkv), int(hkv), int(d), int(bs), int(nblk), mb,
+                      int(max_context_len if max_context_len is not None else mb * bs), 1.0)
+
+
+def _weight_args(weights, weights_out, weight_rows, S, hkv, desc):
+    import torch
+    _need(weights, torch.float32, "weights", 3)
+    if weights_out is None:
+        weights_out = weights
+    _need(weights_out, torch.float32, "weights_out", 3)
+    if tuple(weights_out.shape) != tuple(weights.shape):
+        raise ValueError(f"weights_out must have weights' shape {tuple(weights.shape)}")
+    if weights_out is not weights and weights.numel():
+        a, b, n = weights.data_ptr(), weights_out.data_ptr(), weights.numel() * 4
+        if a != b and a < b + n and b < a + n:
+            raise ValueError("weights and weights_out overlap: pass the same tensor, or another")
+    if weights.shape[1] != hkv:
+        raise ValueError(f"weights has {weights.shape[1]} kv heads, the pools {hkv}")
+    if weights.shape[2] < desc.max_context_len:
+        raise ValueError(f"weights has room for {weights.shape[2]} tokens, max_context_len is {desc.max_context_len}")
+    if weight_rows is not None:
+        _need(weight_rows, torch.int32, "weight_rows", 1)
+        if weight_rows.shape[0] < S:
+            raise ValueError(f"weight_rows has {weight_rows.shape[0]} rows, needs {S}")
+    elif weights.shape[0] < S:
+        raise ValueError(f"weights has {weights.shape[0]} rows, needs {S}")
+    return weights_out
+
+
+def block_key_bounds(k_pool, bounds, block_tables, context_lens, start_lens=None, *, max_new_tokens=None,
+                     max_context_len=None, err_flag=None, stream=None):
+    """Writes the channel-wise minimum and maximum of the keys of every block
+    from start_lens[s] on into bounds [num_blocks][Hkv][2][D] (see
+    pagedattn.h); returns bounds."""
+    import torch
+    _cache_args(k_pool, block_tables, context_lens)
+    _need(bounds, torch.bfloat16, "bounds", 4)
+    nblk, hkv, bs, d = k_pool.shape
+    if tuple(bounds.shape) != (nblk, hkv, 2, d):
+        raise ValueError(f"bounds must be [{nblk}][{hkv}][2][{d}]")
+    S = context_lens.shape[0]
+    rows = [("block_tables", S)]
+    if start_lens is not None:
+        _need(start_lens, torch.int32, "start_lens", 1)
+        rows.append(("start_lens", S))
+    _shapes(k_pool=k_pool, bounds=bounds, block_tables=block_tables, context_lens=context_lens, start_lens=start_lens,
+            rows=rows)
+    desc = _cache_desc(k_pool.shape, block_tables, S, max_context_len)
+    st = load().pa_block_key_bounds(_c.byref(desc), _ptr(k_pool), _ptr(block_tables), _ptr(context_lens),
+                                    _ptr(start_lens),
+                                    int(max_new_tokens if max_new_tokens is not None else desc.max_context_len),
+                                    _ptr(bounds), _flag(err_flag), _stream_ptr(stream))
+    _check(st, "pa_block_key_bounds")
+    return bounds
+
+
+def select_blocks(q, bounds, block_tables, context_lens, num_select, *, block_size, sink_blocks=1, recent_blocks=1,
+                  selected=None, max_context_len=None, workspace=None, err_flag=None, stream=None):
+    """The logical blocks each (sequence, kv head) attends this step, int32
+    [num_seqs][Hkv][num_select], increasing, then -1 (see pagedattn.h)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(bounds, torch.bfloat16, "bounds", 4)
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _need(context_lens, torch.int32, "context_lens", 1)
+    nblk, hkv, two, d = bounds.shape
+    S, k = q.shape[0], int(num_select)
+    if two != 2 or q.shape[2] != d:
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim] of q's head_dim")
+    if selected is None:
+        selected = _new((S, hkv, k), torch.int32, q.device, stream)
+    _need(selected, torch.int32, "selected", 3)
+    if tuple(selected.shape) != (S, hkv, k):
+        raise ValueError(f"selected must be [{S}][{hkv}][{k}]")
+    _shapes(q=q, bounds=bounds, block_tables=block_tables, context_lens=context_lens, selected=selected,
+            rows=(("block_tables", S), ("context_lens", S)))
+    desc = _cache_desc((nblk, hkv, int(block_size), d), block_tables, S, max_context_len)
+    desc.num_q_heads = int(q.shape[1])
+    lib = load()
+    if workspace is None:
+        workspace = _call_ws(_WS_SELECT, int(lib.pa_select_blocks_workspace_bytes(_c.byref(desc))), q.device, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.pa_select_blocks(_c.byref(desc), _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), k,
+                              int(sink_blocks), int(recent_blocks), _ptr(selected), _ws(workspace), ws_bytes,
+                              _flag(err_flag), _stream_ptr(stream))
+    _check(st, "pa_select_blocks")
+    return selected
+
+
+def paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens, selected, out=None, *, scale=None,
+                                  max_context_len=None, workspace=None, err_flag=None, stream=None):
+    """Decode attention over the listed blocks of every (sequence, kv head)
+    (see pagedattn.h)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _cache_args(k_pool, block_tables, context_lens, v_pool)
+    _need(selected, torch.int32, "selected", 3)
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _need(out, torch.bfloat16, "out", 3)
+    S = q.shape[0]
+    _attn_shapes(q, k_pool, v_pool, block_tables, context_lens, out, S)
+    _shapes(q=q, selected=selected, rows=(("selected", S),))
+    if selected.shape[1] != k_pool.shape[1]:
+        raise ValueError(f"selected has {selected.shape[1]} kv heads, the pools {k_pool.shape[1]}")
+    desc = make_desc(q, k_pool, block_tables, scale=scale, max_context_len=max_context_len)
+    k = int(selected.shape[2])
+    lib = load()
+    if workspace is None:
+        workspace = _call_ws(_WS_SPARSE, int(lib.pa_decode_sparse_workspace_bytes(_c.byref(desc), k)), q.device,
+                             stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.pa_paged_attention_decode_sparse(_c.byref(desc), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
+                                              _ptr(context_lens), _ptr(selected), k, _ptr(out), _ws(workspace),
+                                              ws_bytes, _flag(err_flag), _stream_ptr(stream))
+    _check(st, "pa_paged_attention_decode_sparse")
+    return out
+
+
+def paged_attention_decode_weights(q, k_pool, v_pool, block_tables, context_lens, weights, out=None, *,
+                                   weights_out=None, weight_rows=None, scale=None, max_context_len=None,
+                                   workspace=None, err_flag=None, stream=None):
+    """Decode attention that adds every key's attention weight to `weights`
+    [num_rows][Hkv][max_tokens] (in place, or into weights_out; see
+    pagedattn.h); returns (out, weights_out)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _cache_args(k_pool, block_tables, context_lens, v_pool)
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _need(out, torch.bfloat16, "out", 3)
+    S = q.shape[0]
+    _attn_shapes(q, k_pool, v_pool, block_tables, context_lens, out, S)
+    desc = make_desc(q, k_pool, block_tables, scale=scale, max_context_len=max_context_len)
+    weights_out = _weight_args(weights, weights_out, weight_rows, S, k_pool.shape[1], desc)
+    _shapes(q=q, weights=weights, weights_out=weights_out, weight_rows=weight_rows)
+    lib = load()
+    if workspace is None:
+        workspace = _call_ws(_WS_WEIGHTS, int(lib.pa_decode_weights_workspace_bytes(_c.byref(desc))), q.device, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.pa_paged_attention_decode_weights(
+        _c.byref(desc), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), _ptr(weights),
+        _ptr(weights_out), _ptr(weight_rows), int(weights.shape[0]), int(weights.shape[2]), _ptr(out), _ws(workspace),
+        ws_bytes, _flag(err_flag), _stream_ptr(stream))
+    _check(st, "pa_paged_attention_decode_weights")
+    return out, weights_out
+
+
+def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights, *, max_keep_len, sink_tokens=0,
+                 recent_tokens=0, dst_tables=None, weights_out=None, weight_rows=None, kept=None, new_lens=None,
+                 max_context_len=None, err_flag=None, stream=None):
+    """Keeps keep_lens[s] tokens of every (sequence, kv head), those with the
+    largest weights among them, compacted into dst_tables' blocks (None: in
+    place; see pagedattn.h); returns (kept [num_seqs][Hkv][max_keep_len],
+    new_lens [num_seqs])."""
+    import torch
+    _cache_args(k_pool, block_tables, context_lens, v_pool)
+    _need(keep_lens, torch.int32, "keep_lens", 1)
+    hkv = k_pool.shape[1]
+    S, mk = context_lens.shape[0], int(max_keep_len)
+    if mk <= 0:
+        raise ValueError(f"max_keep_len must be positive, got {mk}")
+    rows = [("block_tables", S), ("keep_lens", S)]
+    if dst_tables is not None:
+        _need(dst_tables, torch.int32, "dst_tables", 2)
+        rows.append(("dst_tables", S))
+        if dst_tables.shape[1] != block_tables.shape[1]:
+            raise ValueError("dst_tables must be as wide as block_tables")
+    if kept is None:
+        kept = _new((S, hkv, mk), torch.int32, k_pool.device, stream)
+    if new_lens is None:
+        new_lens = _new((S,), torch.int32, k_pool.device, stream)
+    _need(kept, torch.int32, "kept", 3)
+    _need(new_lens, torch.int32, "new_lens", 1)
+    if tuple(kept.shape) != (S, hkv, mk) or new_lens.shape[0] != S:
+        raise ValueError(f"kept must be [{S}][{hkv}][{mk}] and new_lens [{S}]")
+    if S and new_lens.data_ptr() == context_lens.data_ptr():
+        raise ValueError("new_lens must not be context_lens")
+    desc = _cache_desc(k_pool.shape, block_tables, S, max_context_len)
+    weights_out = _weight_args(weights, weights_out, weight_rows, S, hkv, desc)
+    _shapes(k_pool=k_pool, v_pool=v_pool, block_tables=block_tables, context_lens=context_lens, keep_lens=keep_lens,
+            weights=weights, dst_tables=dst_tables, weights_out=weights_out, weight_rows=weight_rows, kept=kept,
+            new_lens=new_lens, rows=rows)
+    st = load().pa_evict_tokens(_c.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(dst_tables),
+                                _ptr(context_lens), _ptr(keep_lens), mk, int(sink_tokens), int(recent_tokens),
+                                _ptr(weights), _ptr(weights_out), _ptr(weight_rows), int(weights.shape[0]),
+                                int(weights.shape[2]), _ptr(kept), _ptr(new_lens), _flag(err_flag),
+                                _stream_ptr(stream))
+    _check(st, "pa_evict_tokens")
+    return kept, new_lens
+
+
 # --------------------------------------------------------------- block manager
 class BlockManager:
     """Host block manager (free list, block tables, ref counts, copy-on-write)."""
@@ -673,6 +923,21 @@ class BlockManager:
     def swap_in(self, seq_id: int):
         """Returns the (host block, device block) pairs to copy."""
         return self._swap(self._lib.pa_bm_swap_in, seq_id)
+
+    def evict(self, seq_id: int, keep_len: int):
+        """Shortens seq_id to keep_len tokens; returns the block table that
+        evict_tokens moves them into (its source table is block_table() from
+        before this call)."""
+        cap = 64
+        while True:
+            buf = (_c.c_int32 * cap)()
+            n = _c.c_int()
+            st = self._lib.pa_bm_evict(self._h, int(seq_id), int(keep_len), buf, cap, _c.byref(n))
+            if st == PA_ERR_INVALID and n.value > cap:
+                cap = n.value
+                continue
+            _check(st, "pa_bm_evict")
+            return list(buf[:n.value])
 
     def add_seq_tokens(self, seq_id: int, tokens) -> int:
         """New sequence holding the prompt `tokens` (a 1-D sequence of int32

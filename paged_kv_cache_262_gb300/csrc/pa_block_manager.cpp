@@ -587,6 +587,42 @@ int pa_bm_swap_in(pa_bm *bm, int seq_id, int64_t *pairs_out, int cap, int *n) {
   return PA_OK;
 }
 
+int pa_bm_evict(pa_bm *bm, int seq_id, int keep_len, int32_t *dst_out, int cap, int *n) {
+  if (!bm || !n || keep_len < 1) return PA_ERR_INVALID;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end() || it->second.swapped) return PA_ERR_STATE;
+  Seq &s = it->second;
+  const bool all = keep_len >= s.len;
+  const size_t nb =
+      all ? s.blocks.size() : (size_t)(((int64_t)keep_len + bm->block_size - 1) / bm->block_size);
+  *n = (int)nb;
+  if (cap < *n || (!dst_out && *n > 0)) return PA_ERR_INVALID;
+  if (!all) {
+    int fresh = 0;
+    for (size_t i = 0; i < nb; ++i) fresh += bm->ref[s.blocks[i]] > 1;
+    if (fresh > bm->nfree) return PA_ERR_OOM;
+    // Fresh blocks first: the released ones are sources of the same eviction.
+    // Nothing below allocates.
+    for (size_t i = 0; i < nb; ++i) {
+      int32_t &b = s.blocks[i];
+      if (bm->ref[b] > 1) {
+        const int32_t old = b;
+        b = bm->take();
+        bm->drop(old);
+      } else {
+        bm->uncache(b);  // and what continues it: no other sequence holds that either
+      }
+    }
+    for (size_t i = s.blocks.size(); i-- > nb;) bm->drop(s.blocks[i]);
+    s.blocks.resize(nb);
+    s.len = keep_len;
+    s.tracked = false;
+    s.tail.clear();
+  }
+  std::copy(s.blocks.begin(), s.blocks.end(), dst_out);
+  return PA_OK;
+}
+
 int pa_bm_num_free_host(const pa_bm *bm) { return bm ? (int)bm->host_free.size() : -1; }
 
 }  // extern "C"

@@ -1,0 +1,489 @@
+// Block selection for sparse decode attention, sm_103a: per-block bounds of
+// the cached keys, and the choice of the blocks each (sequence, kv head)
+// attends by a cheap score of them.
+//
+//   lo[b][h][d] = min_j k_j[d],  hi[b][h][d] = max_j k_j[d]   over the block's keys
+//   score(s, h, i) = max_g sum_d (q_gd > 0 ? q_gd hi_id : q_gd lo_id)  >=  max_{j in i} q_g.k_j
+//
+// over the G query heads g of kv head h: no key of a block can have a larger
+// product with the query than the block's score.  The score reads 4 D bytes a
+// (block, kv head) where attention reads 4 D B, so choosing costs 1/B of what
+// attending everything would (decode re-reads the whole cache for each token:
+// "Configuring vLLM and PagedAttention for High Throughput Enterprise LLM
+// Serving", "Memory Bottlenecks in Autoregressive LLM Inference").
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pa_decode_body.cuh"
+#include "pa_internal.h"
+#include "pa_select.cuh"
+#include "pagedattn.h"
+
+namespace pa {
+namespace {
+
+// ------------------------------------------------------------- key bounds
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+struct BoundsArgs {
+  const uint4 *k;
+  uint4 *bounds;  // [num_blocks][Hkv][2][D]
+  const int32_t *bt, *ctx, *start;
+  int32_t *err;
+  int Hkv, num_blocks, max_blocks, max_ctx, max_new;
+};
+
+// grid (8 (block, kv head) runs, sequence); a warp reduces one run.  A run is
+// contiguous: every load instruction of the warp covers 512 consecutive bytes.
+template <int D, int B>
+__global__ void __launch_bounds__(256) key_bounds_kernel(const BoundsArgs a) {
+  constexpr int C = D / 8;          // 16-byte chunks of a key
+  constexpr int R = 32 / C;         // keys a load instruction covers
+  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int ctx = __ldg(a.ctx + s), start = a.start ? __ldg(a.start + s) : 0;
+  if (ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx || start < 0 || start > ctx || ctx - start > a.max_new) {
+    if (unit == 0 && lane == 0 && a.err) atomicOr(a.err, PA_DEVERR_CTX);
+    return;
+  }
+  const int i = start / B + unit / a.Hkv, h = unit % a.Hkv;
+  if (i >= (ctx + B - 1) / B) return;
+  const int pg = __ldg(a.bt + (size_t)s * a.max_blocks + i);
+  if (pg < 0 || pg >= a.num_blocks) {
+    if (lane == 0 && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+    return;
+  }
+  const size_t run = (size_t)pg * a.Hkv + h;
+  const uint4 *k = a.k + run * B * C;
+  const int rows = min(B, ctx - i * B);
+  uint4 x[B / R];
+#pragma unroll
+  for (int r = 0; r < B / R; ++r)  // a row past the context: the block's first key once more
+    x[r] = __ldcs(k + (r * R + lane / C < rows ? r * 32 + lane : lane % C));
+  uint4 lo = x[0], hi = x[0];
+#pragma unroll
+  for (int r = 1; r < B / R; ++r) {
+    lo = make_uint4(min2(lo.x, x[r].x), min2(lo.y, x[r].y), min2(lo.z, x[r].z), min2(lo.w, x[r].w));
+    hi = make_uint4(max2(hi.x, x[r].x), max2(hi.y, x[r].y), max2(hi.z, x[r].z), max2(hi.w, x[r].w));
+  }
+#pragma unroll
+  for (int o = C; o < 32; o <<= 1) {
+    lo.x = min2(lo.x, __shfl_xor_sync(0xffffffffu, lo.x, o));
+    lo.y = min2(lo.y, __shfl_xor_sync(0xffffffffu, lo.y, o));
+    lo.z = min2(lo.z, __shfl_xor_sync(0xffffffffu, lo.z, o));
+    lo.w = min2(lo.w, __shfl_xor_sync(0xffffffffu, lo.w, o));
+    hi.x = max2(hi.x, __shfl_xor_sync(0xffffffffu, hi.x, o));
+    hi.y = max2(hi.y, __shfl_xor_sync(0xffffffffu, hi.y, o));
+    hi.z = max2(hi.z, __shfl_xor_sync(0xffffffffu, hi.z, o));
+    hi.w = max2(hi.w, __shfl_xor_sync(0xffffffffu, hi.w, o));
+  }
+  if (lane < 2 * C) a.bounds[run * 2 * C + lane] = lane < C ? lo : hi;
+}
+
+// -------------------------------------------------------------- selection
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelChunk = 128;     // blocks a CTA scores
+constexpr int kSelKeys = 8192;     // keys held in shared memory; more are re-read from the workspace
+constexpr int kSelRefine = 256;    // blocks near the threshold that are ranked in shared memory
+
+struct SelectArgs {
+  const __nv_bfloat16 *q;
+  const uint4 *bounds;
+  const int32_t *bt, *ctx;
+  int32_t *selected;           // [S][Hkv][k]
+  uint32_t *keys;              // [S][Hkv][stride]: scores as ordered keys
+  unsigned long long *keys64;  // [S][Hkv][stride]
+  float *maxabs;               // [S][Hkv][max_chunks]: largest |bound| of a chunk
+  unsigned long long *cnt;     // [S][Hkv] arrivals
+  int32_t *err;
+  int Hq, Hkv, G, num_blocks, max_blocks, max_ctx, k, sink, recent, B, max_chunks;
+  size_t stride;
+  unsigned int epoch;
+};
+
+// A block's score in 64 bits, by one warp: every product of two bf16 values
+// is exact, and blocks of equal bounds get equal sums.
+template <int D>
+__device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int pg, int h, int lane) {
+  constexpr int P = D / 32;
+  const __nv_bfloat16 *lo = reinterpret_cast<const __nv_bfloat16 *>(a.bounds) + ((size_t)pg * a.Hkv + h) * 2 * D;
+  double best = -INFINITY;
+  for (int g = 0; g < a.G; ++g) {
+    double sum = 0.0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int d = lane * P + p;
+      const float x = __bfloat162float(q[g * D + d]);
+      if (x != 0.f) sum += (double)x * (double)__bfloat162float(lo[x > 0.f ? D + d : d]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (sum != sum) sum = INFINITY;
+    best = sum > best ? sum : best;
+  }
+  return best;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+  constexpr int CH = 2 * D / 32;  // 32-element steps over a block's bounds (lo, then hi)
+  __shared__ SelectSmem<kSelThreads> sm;
+  __shared__ uint32_t skeys[kSelKeys];
+  __shared__ double ex[kSelRefine];
+  __shared__ int exi[kSelRefine];
+  __shared__ float fmax_s[kSelWarps];
+  __shared__ int nex, ngt, last;
+  const int chunk = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = a.B;
+  const size_t row = (size_t)s * a.Hkv + h;
+  int32_t *out = a.selected + row * a.k;
+  const int ctx = __ldg(a.ctx + s);
+  const bool bad = ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx;
+  const int n = bad ? 0 : (ctx + B - 1) / B;
+  if (n <= a.k) {  // every block, or none
+    if (chunk == 0) {
+      for (int i = tid; i < a.k; i += kSelThreads) out[i] = i < n ? i : -1;
+      if (bad && h == 0 && tid == 0 && a.err) atomicOr(a.err, PA_DEVERR_CTX);
+    }
+    return;
+  }
+  const int nchunks = (n + kSelChunk - 1) / kSelChunk;
+  if (chunk >= nchunks) return;
+  const int first = a.sink, end = n - a.recent;  // the blocks that compete
+  const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
+  const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
+  uint32_t *keys = a.keys + row * a.stride;
+
+  // ---- scores of this CTA's blocks: S[block][head] = [lo hi] . [q- q+], the
+  // contraction in whatever order of d suits the loads (lane t of a quad takes
+  // the 16-byte chunks t, t + 4, ...), the same for both operands.
+  uint32_t qf[NT][CH / 2][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int g = nt * 8 + (lane >> 2);
+#pragma unroll
+    for (int c = 0; c < CH / 2; ++c) {
+      const uint4 v = g < a.G ? __ldg(reinterpret_cast<const uint4 *>(q + (size_t)g * D) + c * 4 + (lane & 3))
+                              : make_uint4(0u, 0u, 0u, 0u);
+      qf[nt][c][0] = v.x;
+      qf[nt][c][1] = v.y;
+      qf[nt][c][2] = v.z;
+      qf[nt][c][3] = v.w;
+    }
+  }
+  uint32_t big = 0u;  // packed running max of |bound|
+  for (int t = warp; t < kSelChunk / 16; t += kSelWarps) {
+    const int i0 = chunk * kSelChunk + t * 16;
+    if (i0 >= end || i0 + 16 <= first) continue;
+    uint4 x[2][CH];
+    bool have[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = i0 + (lane >> 2) + 8 * r;
+      int pg = i >= first && i < end ? __ldg(bt + i) : -2;
+      if (pg != -2 && (pg < 0 || pg >= a.num_blocks)) {
+        if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+        pg = -1;
+      }
+      have[r] = pg >= 0;
+      const uint4 *src = a.bounds + ((size_t)max(pg, 0) * a.Hkv + h) * (D / 4) + (lane & 3);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) x[r][c] = have[r] ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint4 u = x[0][c], v = x[1][c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t ue = e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
+        const uint32_t ve = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+        big = max2(big, max2(ue & 0x7fff7fffu, ve & 0x7fff7fffu));
+      }
+      const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          b[e] = c < CH / 2 ? min2(qf[nt][c % (CH / 2)][e], 0u) : max2(qf[nt][c % (CH / 2)][e], 0u);
+        mma_16816(acc[nt], a0, b[0], b[1]);
+        mma_16816(acc[nt], a1, b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float best = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int g = nt * 8 + 2 * (lane & 3);
+        if (g < a.G) best = fmaxf(best, acc[nt][2 * r]);
+        if (g + 1 < a.G) best = fmaxf(best, acc[nt][2 * r + 1]);
+      }
+      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+      const int i = i0 + (lane >> 2) + 8 * r;
+      if ((lane & 3) == 0 && i >= first && i < end) keys[i - first] = have[r] ? order_key(best) : 0u;
+    }
+  }
+  float m = fmaxf(bf16_lo(big), bf16_hi(big));
+  if (bf16_lo(big) != bf16_lo(big) || bf16_hi(big) != bf16_hi(big)) m = INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) fmax_s[warp] = m;
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+#pragma unroll
+    for (int w = 1; w < kSelWarps; ++w) m = fmaxf(m, fmax_s[w]);
+    a.maxabs[row * a.max_chunks + chunk] = m;
+    __threadfence();
+    last = arrive_count(a.cnt + row, a.epoch) == (unsigned int)nchunks;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (tid == 0) a.cnt[row] = 0ull;
+
+  // ---- the last CTA of the row selects
+  for (int i = tid; i < a.sink; i += kSelThreads) out[i] = i;
+  for (int i = tid; i < a.recent; i += kSelThreads) out[a.k - a.recent + i] = end + i;
+  const int N = end - first, want = a.k - a.sink - a.recent;
+  if (want == 0) return;
+  // How far an fp32 score may be from the exact one: every one of the 2 D / 16
+  // MMAs adds 17 terms no larger than Q M, Q = max_g sum_d |q_gd|, M = max
+  // |bound|, each cut at 2^-23 or better of the largest: less than 2^-14 Q M
+  // in all.
+  float Q = 0.f;
+  for (int g = 0; g < a.G; ++g) {
+    float x = 0.f;
+    for (int d = lane; d < D; d += 32) x += fabsf(__bfloat162float(q[g * D + d]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    Q = x >= Q ? x : x == x ? Q : INFINITY;
+  }
+  float M = 0.f;
+  for (int c = lane; c < nchunks; c += 32) M = fmaxf(M, __ldcg(a.maxabs + row * a.max_chunks + c));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float slack = 2.f * 6.103515625e-05f * (Q * M);
+  const bool finite = Q * M < INFINITY;  // false for NaN: then no fp32 score is trusted
+
+  const bool in_smem = N <= kSelKeys;
+  if (in_smem)
+    for (int i = tid; i < N; i += kSelThreads) skeys[i] = __ldcg(keys + i);
+  uint32_t *kk = in_smem ? skeys : keys;  // writable; in global memory read past L1
+  __syncthreads();
+  auto key32 = [&](int i) -> uint32_t { return in_smem ? skeys[i] : __ldcg(keys + i); };
+  uint32_t lo = 0u, hi = 0xfffffffeu;  // (no score's key is above it)
+  if (finite) {
+    const Kth<uint32_t> t = kth_largest<kSelThreads, uint32_t>(key32, N, want, sm, tid);
+    if (t.key != 0u) {
+      const float v = key_value(t.key);
+      lo = order_key(__fsub_rd(v, slack));
+      hi = order_key(__fadd_ru(v, slack));
+    } else {
+      hi = 0u;  // blocks outside the pool are among the chosen: those that can be read all are
+    }
+  }
+  // blocks above hi are chosen whatever their rounding, those below lo are not
+  if (tid == 0) nex = ngt = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int i = tid; i < N; i += kSelThreads) {
+    const uint32_t k = key32(i);
+    mine += k > hi;
+    if (k >= lo && k <= hi) {
+      const int at = atomicAdd(&nex, 1);
+      if (at < kSelRefine) exi[at] = i;
+    }
+  }
+  atomicAdd(&ngt, mine);
+  __syncthreads();
+  const int near_ = nex, need = want - ngt;
+  auto emit = [&](int pos, int i) { out[a.sink + pos] = first + i; };
+  if (near_ == need || hi == 0u) {  // (of blocks outside the pool, the first)
+    take_above<kSelThreads, uint32_t>(key32, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, sm, tid, emit);
+    return;
+  }
+  if (near_ <= kSelRefine) {  // few: their exact scores, ranked by counting
+    for (int c = warp; c < near_; c += kSelWarps) {
+      const int pg = __ldg(bt + first + exi[c]);
+      const double e = pg >= 0 && pg < a.num_blocks ? exact_score<D>(a, q, pg, h, lane) : -INFINITY;
+      if (lane == 0) ex[c] = e;
+    }
+    __syncthreads();
+    for (int c = tid; c < near_; c += kSelThreads) {
+      int rank = 0;
+      for (int o = 0; o < near_; ++o) rank += ex[o] > ex[c] || (ex[o] == ex[c] && exi[o] < exi[c]);
+      kk[exi[c]] = rank < need ? 0xffffffffu : 0u;
+    }
+    __syncthreads();
+    take_above<kSelThreads, uint32_t>(key32, N, hi, 0, want, sm, tid, emit);
+    return;
+  }
+  // many (scores that tie in numbers, infinite bounds): 64-bit keys for all of
+  // them in the workspace
+  unsigned long long *k64 = a.keys64 + row * a.stride;
+  for (int i = warp; i < N; i += kSelWarps) {
+    const uint32_t k = key32(i);
+    unsigned long long e = k > hi ? ~0ull : 0ull;
+    if (k >= lo && k <= hi) {
+      const int pg = __ldg(bt + first + i);
+      const double x = pg >= 0 && pg < a.num_blocks ? exact_score<D>(a, q, pg, h, lane) : -INFINITY;
+      e = pg >= 0 && pg < a.num_blocks ? order_key64(x) : 1ull;
+    }
+    if (lane == 0) k64[i] = e;
+  }
+  __threadfence_block();
+  __syncthreads();
+  auto key64 = [&](int i) -> unsigned long long { return k64[i]; };
+  const Kth<unsigned long long> t = kth_largest<kSelThreads, unsigned long long>(key64, N, want, sm, tid);
+  take_above<kSelThreads, unsigned long long>(key64, N, t.key, want - t.above, want, sm, tid, emit);
+}
+
+struct SelectPlan {
+  int max_chunks = 0;
+  size_t stride = 0, keys = 0, keys64 = 0, maxabs = 0, cnt = 0;
+  size_t total() const { return keys + keys64 + maxabs + cnt; }
+};
+
+SelectPlan make_select_plan(const pa_decode_desc *d) {
+  SelectPlan p;
+  const int64_t B = d->block_size;
+  const size_t nblk = (size_t)std::max<int64_t>(1, ((int64_t)d->max_context_len + B - 1) / B);
+  const size_t rows = (size_t)d->num_seqs * d->num_kv_heads;
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  p.max_chunks = (int)((nblk + kSelChunk - 1) / kSelChunk);
+  p.stride = (nblk + 3) & ~(size_t)3;
+  p.keys64 = up(rows * p.stride * 8);
+  p.keys = up(rows * p.stride * 4);
+  p.maxabs = up(rows * p.max_chunks * 4);
+  p.cnt = up(rows * 8);
+  return p;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" int pa_block_key_bounds(const pa_decode_desc *d, const void *k_pool, const int32_t *block_tables,
+                                   const int32_t *context_lens, const int32_t *start_lens, int max_new_tokens,
+                                   void *bounds, int32_t *err_flag, void *stream) {
+  using namespace pa;
+  const int vs = validate_decode_desc(d);
+  if (vs != PA_OK) return vs;
+  if (max_new_tokens < 0) return PA_ERR_INVALID;
+  if (d->num_seqs == 0) return PA_OK;
+  if (!k_pool || !block_tables || !context_lens || !bounds || !aligned16(k_pool) || !aligned16(bounds))
+    return PA_ERR_INVALID;
+  if (d->num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  BoundsArgs a{};
+  a.k = static_cast<const uint4 *>(k_pool);
+  a.bounds = static_cast<uint4 *>(bounds);
+  a.bt = block_tables;
+  a.ctx = context_lens;
+  a.start = start_lens;
+  a.err = err_flag;
+  a.Hkv = d->num_kv_heads;
+  a.num_blocks = d->num_blocks;
+  a.max_blocks = d->max_blocks_per_seq;
+  a.max_ctx = d->max_context_len;
+  a.max_new = max_new_tokens;
+  // most blocks that max_new tokens at the end of a context touch
+  const int64_t B = d->block_size;
+  const int64_t most = std::max<int64_t>(
+      1, std::min<int64_t>((std::min<int64_t>(max_new_tokens, d->max_context_len) + B - 1) / B + 1,
+                           ((int64_t)d->max_context_len + B - 1) / B));
+  const int64_t gx = (most * d->num_kv_heads + 7) / 8;
+  if (gx > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)gx, d->num_seqs);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->head_dim == 128) {
+    if (d->block_size == 16)
+      key_bounds_kernel<128, 16><<<grid, 256, 0, s>>>(a);
+    else
+      key_bounds_kernel<128, 32><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (d->block_size == 16)
+      key_bounds_kernel<64, 16><<<grid, 256, 0, s>>>(a);
+    else
+      key_bounds_kernel<64, 32><<<grid, 256, 0, s>>>(a);
+  }
+  return launch_status(cudaGetLastError());
+}
+
+extern "C" size_t pa_select_blocks_workspace_bytes(const pa_decode_desc *d) {
+  using namespace pa;
+  if (validate_decode_desc(d) != PA_OK) return 0;
+  return make_select_plan(d).total();
+}
+
+extern "C" int pa_select_blocks(const pa_decode_desc *d, const void *q, const void *bounds,
+                                const int32_t *block_tables, const int32_t *context_lens, int num_select,
+                                int sink_blocks, int recent_blocks, int32_t *selected, void *workspace,
+                                size_t workspace_bytes, int32_t *err_flag, void *stream) {
+  using namespace pa;
+  const int vs = validate_decode_desc(d);
+  if (vs != PA_OK) return vs;
+  if (num_select <= 0 || sink_blocks < 0 || recent_blocks < 0 || (int64_t)sink_blocks + recent_blocks > num_select)
+    return PA_ERR_INVALID;
+  if (d->num_seqs == 0) return PA_OK;
+  if (!q || !bounds || !block_tables || !context_lens || !selected || !aligned16(q) || !aligned16(bounds))
+    return PA_ERR_INVALID;
+  if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const SelectPlan p = make_select_plan(d);
+  if (!workspace || workspace_bytes < p.total() || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  SelectArgs a{};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.bounds = static_cast<const uint4 *>(bounds);
+  a.bt = block_tables;
+  a.ctx = context_lens;
+  a.selected = selected;
+  a.keys64 = reinterpret_cast<unsigned long long *>(ws);
+  a.keys = reinterpret_cast<uint32_t *>(ws + p.keys64);
+  a.maxabs = reinterpret_cast<float *>(ws + p.keys64 + p.keys);
+  a.cnt = reinterpret_cast<unsigned long long *>(ws + p.keys64 + p.keys + p.maxabs);
+  a.err = err_flag;
+  a.Hq = d->num_q_heads;
+  a.Hkv = d->num_kv_heads;
+  a.G = d->num_q_heads / d->num_kv_heads;
+  a.num_blocks = d->num_blocks;
+  a.max_blocks = d->max_blocks_per_seq;
+  a.max_ctx = d->max_context_len;
+  a.k = num_select;
+  a.sink = sink_blocks;
+  a.recent = recent_blocks;
+  a.B = d->block_size;
+  a.max_chunks = p.max_chunks;
+  a.stride = p.stride;
+  a.epoch = next_decode_epoch();
+  const dim3 grid(p.max_chunks, d->num_kv_heads, d->num_seqs);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->head_dim == 128) {
+    if (a.G <= 8)
+      select_kernel<128, 1><<<grid, kSelThreads, 0, s>>>(a);
+    else
+      select_kernel<128, 2><<<grid, kSelThreads, 0, s>>>(a);
+  } else {
+    if (a.G <= 8)
+      select_kernel<64, 1><<<grid, kSelThreads, 0, s>>>(a);
+    else
+      select_kernel<64, 2><<<grid, kSelThreads, 0, s>>>(a);
+  }
+  return launch_status(cudaGetLastError());
+}

@@ -81,6 +81,12 @@ bool encode_kv_halves_3d(CUtensorMap *map, const void *base, uint64_t rows, uint
   return r == CUDA_SUCCESS;
 }
 
+bool encode_kv_pages(const pa_decode_desc *d, const void *pool, CUtensorMap *map) {
+  const uint64_t rows = (uint64_t)d->num_blocks * d->num_kv_heads * d->block_size;
+  return d->head_dim == 128 ? encode_kv_halves_3d(map, pool, rows, d->block_size)
+                            : encode_2d_bf16(map, pool, rows, d->head_dim, d->block_size, 64, true);
+}
+
 int validate_decode_desc(const pa_decode_desc *d) {
   if (!d) return PA_ERR_INVALID;
   if (d->num_seqs < 0 || d->num_q_heads <= 0 || d->num_kv_heads <= 0 || d->num_blocks <= 0 ||

@@ -63,6 +63,15 @@ struct DecodeArgs {
   const int64_t *app_slots;
   uint4 *kp;  // the pools, written through for the append
   uint4 *vp;
+  // Block selection (SEL launches): the logical blocks that (s, kv head)
+  // attends, nsel entries each, -1 for none.
+  const int32_t *sel;  // [S][Hkv][nsel]
+  int nsel;
+  // Attention weights (WTS launches): every key's logit (base 2) and every
+  // row's softmax statistics, from which a second kernel takes the weights.
+  float *logits;    // [S][Hkv][max_ctx][G]
+  float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys
+  float *ws_lw;     // [S][Hkv][max_parts][G]: the parts' sums of unrounded probabilities
 };
 
 // Counts one arrival of this call at *c and returns the arrivals so far.  A
@@ -175,11 +184,15 @@ __device__ int seq_of_rank(int r, const int32_t *ctx, int S, int B, int max_bloc
 // unit's shared memory at `smem` (1024-aligned, DecodeSmem<...>::kBytes) and
 // barrier `bar` for its own NW * 32 threads.  The decode kernel runs one unit
 // per CTA; the mixed-step kernel runs several side by side in one CTA.
-template <int D, int B, int NT, int NW, int NST, bool PRE, bool APP, bool GRP = false, bool TMA3 = false>
+// SEL attends the blocks of a list instead of the whole context; WTS also
+// leaves the logits and softmax statistics for the attention weights.
+template <int D, int B, int NT, int NW, int NST, bool PRE, bool APP, bool GRP = false, bool TMA3 = false,
+          bool SEL = false, bool WTS = false>
 __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtensorMap *tmV, const DecodeArgs &a,
                                             int lin, int tid, uint8_t *smem, int bar) {
   using L = DecodeSmem<D, B, NW, NST>;
   static_assert(NW <= 4, "misc holds four warp totals");
+  static_assert(!(SEL || WTS) || !(PRE || APP || GRP), "block lists and weights: plain decode only");
   constexpr int KS = D / 16;  // k-steps of S^T = K Q^T
   constexpr int MT = B / 16;  // 16-token tiles per page
   constexpr int DT = D / 16;  // 16-row d tiles of O^T = V^T P^T
@@ -255,7 +268,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   const bool bad = GRP ? bad_grp
                        : ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx || kstart < 0 || kstart > ctx ||
                              kstart % B != 0;
-  const int npages = GRP ? npages_grp : bad ? 0 : (ctx + B - 1) / B - kstart / B;
+  const int npages = GRP ? npages_grp : bad ? 0 : SEL ? a.nsel : (ctx + B - 1) / B - kstart / B;
   const int kp0 = bad ? 0 : kstart / B;  // first page of this kernel's key range
   const int nparts = (bad || GRP) ? 1 : max(1, (npages + a.part_pages - 1) / a.part_pages);
   if (part >= nparts) return;
@@ -266,6 +279,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
         for (int i = tid; i < ncols * D; i += NW * 32) a.out[row_of(i / D) * D + i % D] = __float2bfloat16(0.f);
     } else
       for (int i = tid; i < G * D; i += NW * 32) out_base[i] = __float2bfloat16(0.f);
+    if (WTS && tid < G) a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] = make_float2(0.f, 0.f);
     if (tid == 0 && a.err) atomicOr(a.err, PA_DEVERR_CTX);
     return;
   }
@@ -289,6 +303,14 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       }
       pg = __ldg(a.bt + (size_t)(s + max(m, 0)) * a.max_blocks + lb);
       meta[i] = ((m + 1) << 24) | lb;
+    } else if constexpr (SEL) {
+      const int lb = __ldg(a.sel + ((size_t)s * a.Hkv + kvh) * a.nsel + p0 + i);
+      meta[i] = lb;
+      if (lb == -1) {  // a list shorter than the rest
+        tbl[i] = -1;
+        continue;
+      }
+      pg = lb >= 0 && lb < (ctx + B - 1) / B ? __ldg(a.bt + (size_t)s * a.max_blocks + lb) : -1;
     } else {
       pg = __ldg(bt_row + i);
     }
@@ -413,11 +435,16 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 
   // Running state.  Lane holds heads 8nt + 2(lane%4) + e (e = 0, 1) and, in o,
   // the O^T rows d = 16dt + lane/4 (+8).
+  // WTS: lw_run sums the probabilities before their rounding to bf16 (the
+  // rounded sum normalises the output, whose products saw rounded values; the
+  // weights are fp32).
   float m_run[NT][2], l_run[NT][2], o[NT][DT][4];
+  float lw_run[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m_run[nt][0] = m_run[nt][1] = -INFINITY;
     l_run[nt][0] = l_run[nt][1] = 0.f;
+    lw_run[nt][0] = lw_run[nt][1] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) o[nt][dt][0] = o[nt][dt][1] = o[nt][dt][2] = o[nt][dt][3] = 0.f;
   }
@@ -443,6 +470,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
         owner = (mt_ >> 24) - 1;
         octx = owner >= 0 ? misc[8 + owner] : kshared;
       }
+      if constexpr (SEL) tok0 = meta[lp] * B;
       if (APP && app_row >= 0 && lp == np - 1) {
         // The gather may have seen the slot before or after the store above:
         // overwrite the row with the staged copy (each lane its own chunks).
@@ -500,18 +528,48 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           t[nt][1] = fmaxf(t[nt][1], fmaxf(sc[mt][nt][1], sc[mt][nt][3]));
         }
       }
+      if constexpr (WTS) {  // a token's G logits lie together: a store covers 8 tokens' rows
+        float *lg = a.logits + ((size_t)s * a.Hkv + kvh) * a.max_ctx * G;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int g = nt * 8 + 2 * (lane & 3);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int j = tok0 + mt * 16 + (lane >> 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (j + 8 * e < octx) {
+                float *to = lg + (size_t)(j + 8 * e) * G + g;
+                if (g + 1 < G && (G & 1) == 0)
+                  *reinterpret_cast<float2 *>(to) = make_float2(sc[mt][nt][2 * e], sc[mt][nt][2 * e + 1]);
+                else {
+                  if (g < G) to[0] = sc[mt][nt][2 * e];
+                  if (g + 1 < G) to[1] = sc[mt][nt][2 * e + 1];
+                }
+              }
+          }
+        }
+      }
       // P (bf16 pairs) against the running maxima; a column that has seen no
       // key yet (maximum -inf) takes 0, so that no -inf - -inf appears
       uint32_t plo[MT][NT], phi[MT][NT];
+      float psum[NT][2];  // WTS: this page's unrounded probabilities, summed
       auto probabilities = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          psum[nt][0] = psum[nt][1] = 0.f;
           const float e0 = m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0];
           const float e1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            plo[mt][nt] = pack_bf16(ex2_ftz(sc[mt][nt][0] - e0), ex2_ftz(sc[mt][nt][1] - e1));
-            phi[mt][nt] = pack_bf16(ex2_ftz(sc[mt][nt][2] - e0), ex2_ftz(sc[mt][nt][3] - e1));
+            const float p0_ = ex2_ftz(sc[mt][nt][0] - e0), p1_ = ex2_ftz(sc[mt][nt][1] - e1);
+            const float p2_ = ex2_ftz(sc[mt][nt][2] - e0), p3_ = ex2_ftz(sc[mt][nt][3] - e1);
+            plo[mt][nt] = pack_bf16(p0_, p1_);
+            phi[mt][nt] = pack_bf16(p2_, p3_);
+            if constexpr (WTS) {
+              psum[nt][0] += p0_ + p2_;
+              psum[nt][1] += p1_ + p3_;
+            }
           }
         }
       };
@@ -536,6 +594,8 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           m_run[nt][1] = mn1;
           l_run[nt][0] *= al0;
           l_run[nt][1] *= al1;
+          lw_run[nt][0] *= al0;
+          lw_run[nt][1] *= al1;
 #pragma unroll
           for (int dt = 0; dt < DT; ++dt) {
             o[nt][dt][0] *= al0;
@@ -545,6 +605,13 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           }
         }
         probabilities();
+      }
+      if constexpr (WTS) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          lw_run[nt][0] += psum[nt][0];
+          lw_run[nt][1] += psum[nt][1];
+        }
       }
 
       // Value rows past the context (the tail of the last page) may hold
@@ -583,6 +650,11 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][dt], af, pb[nt][0], pb[nt][1]);
         }
       }
+    } else if (WTS) {  // a block outside the pool: its keys weigh nothing
+      const int tok0 = (kp0 + p0 + lp) * B;
+      float *lg = a.logits + ((size_t)s * a.Hkv + kvh) * a.max_ctx * G;
+      for (int idx = lane; idx < B * G; idx += 32)
+        if (tok0 + idx / G < ctx) lg[(size_t)tok0 * G + idx] = -INFINITY;
     }
     __syncwarp();
     if (lane == 0 && i + NST < nmine) {
@@ -601,7 +673,10 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], off);
+      for (int off = 4; off < 32; off <<= 1) {
+        l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], off);
+        if constexpr (WTS) lw_run[nt][e] += __shfl_xor_sync(0xffffffffu, lw_run[nt][e], off);
+      }
 
   // ---- merge the warps (ring memory is reused)
   unit_sync<NW * 32>(bar);
@@ -609,6 +684,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   float *red_m = red_o + NW * 16 * D;
   float *red_l = red_m + NW * 16;
   float *wts = red_l + NW * 16;
+  float *red_lw = reinterpret_cast<float *>(meta);  // WTS: [NW][16] (the page list's tags: block lists, sub-groups only)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int g = nt * 8 + 2 * (lane & 3);
@@ -625,12 +701,33 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       red_m[warp * 16 + g + 1] = m_run[nt][1];
       red_l[warp * 16 + g] = l_run[nt][0];
       red_l[warp * 16 + g + 1] = l_run[nt][1];
+      if constexpr (WTS) {
+        red_lw[warp * 16 + g] = lw_run[nt][0];
+        red_lw[warp * 16 + g + 1] = lw_run[nt][1];
+      }
     }
   }
   unit_sync<NW * 32>(bar);
 
   const bool split = nparts > 1;
   const size_t unit = (size_t)s * a.Hkv + kvh;
+  if constexpr (WTS) {
+    static_assert(!WTS || NW * 16 <= kMaxPartPages, "the warps' sums fit the page tags' room");
+    if (tid < G) {
+      float mx = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red_m[w * 16 + tid]);
+      if (mx != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) l += red_lw[w * 16 + tid] * exp2f(red_m[w * 16 + tid] - mx);
+      }
+      if (split)
+        a.ws_lw[(unit * a.max_parts + part) * G + tid] = l;
+      else
+        a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
+            mx != -INFINITY ? make_float2(mx, 1.f / l) : make_float2(0.f, 0.f);
+    }
+  }
   // Whole context in one CTA with a shared prefix before it: per query head,
   // the weight of this CTA's (unnormalised) sum and of each prefix state,
   // both divided by the total weight -- computed once per head, so that every
@@ -758,6 +855,14 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       den += w;
     }
     const float inv = den > 0.f ? 1.f / den : 0.f;
+    if constexpr (WTS) {
+      float lw = 0.f;
+      for (int p = 0; p < nparts; ++p) {
+        const float m = __ldcg(a.ws_ml + 2 * ((ubase + p) * G + g));
+        if (m != -INFINITY) lw += __ldcg(a.ws_lw + (ubase + p) * G + g) * exp2f(m - M);
+      }
+      a.stats[row] = M != -INFINITY ? make_float2(M, 1.f / lw) : make_float2(0.f, 0.f);
+    }
     for (int p = 0; p < nparts; ++p) wts[p * 16 + g] *= inv;
     for (int p = 0; p < npre; ++p) wpre[p * 16 + g] *= inv;
   }

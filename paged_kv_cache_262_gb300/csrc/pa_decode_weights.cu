@@ -1,0 +1,212 @@
+// Paged decode attention that also sums every key's attention weight, for
+// sm_103a: beside out = sum_j p_j v_j (pa_decode.cu), each cached token's
+//   W[row][h][j] += sum over the kv head's query heads g of p_gj,
+//   p_gj = 2^(x_gj - M_g) / L_g,  x = scale log2(e) q.k,
+// the accumulated attention weight by which tokens are evicted (pa_evict.cu)
+// -- the KV cache growing with the context is the bottleneck of "Configuring
+// vLLM and PagedAttention for High Throughput Enterprise LLM Serving"
+// ("Memory Bottlenecks in Autoregressive LLM Inference").
+//
+// p needs the row's final maximum and sum, which exist only once the whole
+// context has been read.  Reading K again would cost half of the call once
+// more; instead the decode unit (pa_decode_body.cuh) leaves its logits, 4 G
+// bytes a (token, kv head) against the 4 D bytes of its K and V, and a second
+// kernel turns them into weights.  The cache streams past L2 (evict first),
+// so the logits of a call mostly stay there in between.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pa_decode_body.cuh"
+#include "pa_internal.h"
+#include "pagedattn.h"
+
+namespace pa {
+namespace {
+
+template <int D, int B, int NT, int NST>
+__global__ void __launch_bounds__(128)
+    decode_logits_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const DecodeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int lin = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, false, true>(&tmK, &tmV, a, lin, threadIdx.x, smem, 0);
+}
+
+struct WeightArgs {
+  const float *logits;    // [S][Hkv][max_ctx][G]
+  const float2 *stats;    // [S][Hq]
+  const int32_t *ctx;
+  const int32_t *rows;    // [S] or null: row s
+  const float *w_in;      // [num_rows][Hkv][max_tokens]
+  float *w_out;
+  int32_t *err;
+  int S, Hkv, G, num_rows, max_ctx, max_tokens_table;
+  size_t max_tokens;
+};
+
+constexpr int kWThreads = 256;
+constexpr int kWTokens = 1024;  // tokens a CTA covers
+
+// grid (token chunk, kv head, sequence).  Sequences that name the same row
+// are summed by the first of them, in sequence order, so that a row has one
+// writer and its sums one order.
+__global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) {
+  extern __shared__ uint32_t members[];  // bit s: sequence s names this CTA's row
+  const int s = blockIdx.z, h = blockIdx.y, j0 = blockIdx.x * kWTokens, tid = threadIdx.x;
+  const int row = a.rows ? __ldg(a.rows + s) : s;
+  if (row < 0 || row >= a.num_rows) {
+    if (a.err && tid == 0 && h == 0 && blockIdx.x == 0) atomicOr(a.err, PA_DEVERR_ROW);
+    return;
+  }
+  if (a.rows) {
+    bool mine = true;
+    for (int base = 0; base < a.S; base += kWThreads) {
+      const int t = base + tid;
+      const bool same = t < a.S && __ldg(a.rows + t) == row;
+      mine &= !(same && t < s);
+      const unsigned int b = __ballot_sync(0xffffffffu, same);
+      if ((tid & 31) == 0) members[t >> 5] = b;
+    }
+    if (!__syncthreads_and(mine)) return;
+  }
+  const size_t wrow = ((size_t)row * a.Hkv + h) * a.max_tokens;
+  float acc[kWTokens / kWThreads];
+  bool any[kWTokens / kWThreads];
+#pragma unroll
+  for (int i = 0; i < kWTokens / kWThreads; ++i) acc[i] = 0.f, any[i] = false;
+  const int words = a.rows ? (a.S + 31) / 32 : 1;
+  for (int w = 0; w < words; ++w) {
+    uint32_t left = a.rows ? members[w] : 1u;
+    while (left) {
+      const int t = a.rows ? w * 32 + __ffs(left) - 1 : s;
+      left &= left - 1;
+      const int ctx = __ldg(a.ctx + t);
+      if (ctx <= j0 || ctx > a.max_ctx || ctx > a.max_tokens_table) continue;
+      const float2 *st = a.stats + ((size_t)t * a.Hkv + h) * a.G;
+      const float *lg = a.logits + ((size_t)t * a.Hkv + h) * a.max_ctx * a.G;
+#pragma unroll
+      for (int i = 0; i < kWTokens / kWThreads; ++i) {
+        const int j = j0 + i * kWThreads + tid;
+        if (j >= ctx) continue;
+        float sum = 0.f;
+        for (int g = 0; g < a.G; ++g) {
+          const float2 ml = __ldg(st + g);
+          sum += ex2_ftz(lg[(size_t)j * a.G + g] - ml.x) * ml.y;
+        }
+        acc[i] += sum;
+        any[i] = true;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kWTokens / kWThreads; ++i) {
+    const int j = j0 + i * kWThreads + tid;
+    if (any[i]) a.w_out[wrow + j] = a.w_in[wrow + j] + acc[i];
+  }
+}
+
+struct WeightPlan {
+  DecodePlan split;
+  size_t lw = 0, stats = 0, logits = 0;
+  size_t total() const { return split.total() + lw + stats + logits; }
+};
+
+WeightPlan make_plan(const pa_decode_desc *d, int sms) {
+  WeightPlan p;
+  p.split = make_decode_plan(d, sms);
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  const size_t G = d->num_q_heads / d->num_kv_heads, units = (size_t)d->num_seqs * d->num_kv_heads;
+  if (p.split.total() > 0) p.lw = up(units * p.split.max_parts * G * sizeof(float));
+  p.stats = up(units * G * sizeof(float2));
+  p.logits = up(units * G * (size_t)d->max_context_len * sizeof(float));
+  return p;
+}
+
+template <int D, int B, int NT>
+int launch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
+  constexpr int NST = B == 16 ? 3 : 1;
+  using L = DecodeSmem<D, B, 4, NST>;
+  auto kern = decode_logits_kernel<D, B, NT, NST>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+    return PA_ERR_CUDA;
+  kern<<<grid, 128, L::kAlloc, st>>>(tk, tv, a);
+  return launch_status(cudaGetLastError());
+}
+
+template <int D, int B>
+int dispatch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
+  return a.G <= 8 ? launch_logits<D, B, 1>(tk, tv, a, grid, st) : launch_logits<D, B, 2>(tk, tv, a, grid, st);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" size_t pa_decode_weights_workspace_bytes(const pa_decode_desc *d) {
+  using namespace pa;
+  if (validate_decode_desc(d) != PA_OK) return 0;
+  return make_plan(d, current_sm_count()).total();
+}
+
+extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const void *q, const void *k_pool,
+                                                 const void *v_pool, const int32_t *block_tables,
+                                                 const int32_t *context_lens, const float *weights, float *weights_out,
+                                                 const int32_t *weight_rows, int num_rows, int max_tokens, void *out,
+                                                 void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                                 void *stream) {
+  using namespace pa;
+  const int vs = validate_decode_desc(d);
+  if (vs != PA_OK) return vs;
+  if (num_rows < 0 || max_tokens < d->max_context_len || (!weight_rows && num_rows < d->num_seqs))
+    return PA_ERR_INVALID;
+  if (d->num_seqs == 0) return PA_OK;
+  if (!q || !k_pool || !v_pool || !block_tables || !context_lens || !weights || !weights_out || !out)
+    return PA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(weights) ||
+      !aligned16(weights_out))
+    return PA_ERR_INVALID;
+  if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  const WeightPlan plan = make_plan(d, sms);
+  if (!workspace || workspace_bytes < plan.total() || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  CUtensorMap tk, tv;
+  if (!encode_kv_pages(d, k_pool, &tk) || !encode_kv_pages(d, v_pool, &tv)) return PA_ERR_CUDA;
+  DecodeArgs a;
+  fill_decode_args(&a, d, plan.split, q, block_tables, context_lens, out, workspace, err_flag,
+                   (long long)sms * (d->block_size == 16 ? 2 : 3));
+  uint8_t *ws = static_cast<uint8_t *>(workspace) + plan.split.total();
+  a.ws_lw = reinterpret_cast<float *>(ws);
+  a.stats = reinterpret_cast<float2 *>(ws + plan.lw);
+  a.logits = reinterpret_cast<float *>(ws + plan.lw + plan.stats);
+  const dim3 grid(plan.split.max_parts, d->num_kv_heads, d->num_seqs);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(tk, tv, a, grid, s)
+                                                           : dispatch_logits<128, 32>(tk, tv, a, grid, s))
+                                    : (d->block_size == 16 ? dispatch_logits<64, 16>(tk, tv, a, grid, s)
+                                                           : dispatch_logits<64, 32>(tk, tv, a, grid, s));
+  if (st != PA_OK) return st;
+  if (d->max_context_len == 0) return PA_OK;
+  WeightArgs w{};
+  w.logits = a.logits;
+  w.stats = a.stats;
+  w.ctx = context_lens;
+  w.rows = weight_rows;
+  w.w_in = weights;
+  w.w_out = weights_out;
+  w.err = err_flag;
+  w.S = d->num_seqs;
+  w.Hkv = d->num_kv_heads;
+  w.G = a.G;
+  w.num_rows = num_rows;
+  w.max_ctx = d->max_context_len;
+  w.max_tokens_table = d->max_blocks_per_seq * d->block_size;
+  w.max_tokens = (size_t)max_tokens;
+  const int chunks = (d->max_context_len + kWTokens - 1) / kWTokens;
+  const size_t smem = weight_rows ? ((size_t)d->num_seqs + kWThreads - 1) / kWThreads * (kWThreads / 8) : 0;
+  weights_kernel<<<dim3(chunks, d->num_kv_heads, d->num_seqs), kWThreads, smem, s>>>(w);
+  return launch_status(cudaGetLastError());
+}

@@ -23,6 +23,9 @@ bool encode_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t 
 // the other, each box_rows x 128 bytes, 128-byte swizzled -- the layout two
 // 64-column 2-D boxes give, in one copy.
 bool encode_kv_halves_3d(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
+// The map by which the decode unit gathers one (block, kv head) run of a
+// validated desc's K or V pool (its TMA3 form for head_dim 128).
+bool encode_kv_pages(const pa_decode_desc *d, const void *pool, CUtensorMap *map);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

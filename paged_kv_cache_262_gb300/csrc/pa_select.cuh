@@ -1,0 +1,164 @@
+// Selection of the largest of n keys by one CTA: the threshold by radix
+// counting in shared memory, then the taken indices in increasing order.
+// Used by the block selection (pa_block_select.cu) and the eviction
+// (pa_evict.cu).
+#pragma once
+
+#include <stdint.h>
+
+namespace pa {
+namespace {
+
+// A 32-bit key that orders as the float does; -0 as +0, NaN above all.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+// The same in 64 bits; NaN as +infinity.
+__device__ __forceinline__ unsigned long long order_key64(double x) {
+  if (x != x) x = INFINITY;
+  const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
+  return (b >> 63) ? ~b : b | (1ull << 63);
+}
+
+constexpr int kDigitBits = 11;
+constexpr int kBins = 1 << kDigitBits;
+
+template <int NT>
+struct SelectSmem {
+  int hist[kBins];
+  unsigned long long lo[NT / 32], hi[NT / 32];
+  int a[NT / 32], b[NT / 32];
+  int bin, above;
+};
+
+// The want-th largest key (1 <= want <= n) and how many keys are above it.
+template <class T>
+struct Kth {
+  T key;
+  int above;
+};
+
+// Whole CTA of NT threads; key(i) for i < n.  A digit is the kDigitBits bits
+// below those that all keys left share, so that the first one already tells
+// keys of one magnitude apart (scores of a context differ in few high bits)
+// and two passes usually end it.
+template <int NT, class T, class KeyF>
+__device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+  unsigned long long lo = ~0ull, hi = 0ull;
+  for (int i = tid; i < n; i += NT) {
+    const unsigned long long k = key(i);
+    lo = k < lo ? k : lo;
+    hi = k > hi ? k : hi;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+    lo = l2 < lo ? l2 : lo;
+    hi = h2 > hi ? h2 : hi;
+  }
+  __syncthreads();  // sm may be in use by a call before
+  if (lane == 0) {
+    sm.lo[warp] = lo;
+    sm.hi[warp] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    lo = sm.lo[w] < lo ? sm.lo[w] : lo;
+    hi = sm.hi[w] > hi ? sm.hi[w] : hi;
+  }
+  int open = 64 - __clzll((long long)(lo ^ hi));  // low bits in which the keys left differ
+  unsigned long long base = open == 64 ? 0ull : (hi >> open) << open;
+  int left = want, above = 0;
+  while (open > 0) {
+    const int w = min(kDigitBits, open), sh = open - w;
+    for (int i = tid; i < kBins; i += NT) sm.hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) {
+      const unsigned long long k = key(i);
+      if (open == 64 || (k ^ base) >> open == 0) atomicAdd(&sm.hist[(int)(k >> sh) & ((1 << w) - 1)], 1);
+    }
+    __syncthreads();
+    // bins from the highest down, kBins / NT consecutive ones a thread
+    constexpr int kPer = kBins / NT;
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) c += sm.hist[kBins - 1 - tid * kPer - j];
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm.a[warp] = incl;
+    __syncthreads();
+    int run = incl - c;
+    for (int v = 0; v < warp; ++v) run += sm.a[v];
+    if (left > run && left <= run + c) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int b = kBins - 1 - tid * kPer - j, cb = sm.hist[b];
+        if (left > run && left <= run + cb) {
+          sm.bin = b;
+          sm.above = run;
+        }
+        run += cb;
+      }
+    }
+    __syncthreads();
+    base |= (unsigned long long)sm.bin << sh;
+    above += sm.above;
+    left -= sm.above;
+    open = sh;
+  }
+  return Kth<T>{(T)base, above};
+}
+
+// Calls emit(position, i) for every i < n with key(i) > t, and for the first
+// need of those with key(i) == t, in increasing order of i, at most `room` of
+// them (keys that another launch overwrites meanwhile must not write past the
+// list).  Whole CTA.
+template <int NT, class T, class KeyF, class Emit>
+__device__ void take_above(KeyF key, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid, Emit emit) {
+  const int lane = tid & 31, warp = tid >> 5;
+  const int seg = (n + NT - 1) / NT * 32;  // a warp's consecutive keys
+  const int beg = min(n, warp * seg), end = min(n, beg + seg);
+  int gt = 0, eq = 0;
+  for (int i = beg + lane; i < beg + seg; i += 32) {
+    const T k = i < end ? key(i) : (T)0;
+    gt += __popc(__ballot_sync(0xffffffffu, i < end && k > t));
+    eq += __popc(__ballot_sync(0xffffffffu, i < end && k == t));
+  }
+  __syncthreads();
+  if (lane == 0) {
+    sm.a[warp] = gt;
+    sm.b[warp] = eq;
+  }
+  __syncthreads();
+  gt = eq = 0;
+  for (int w = 0; w < warp; ++w) {
+    gt += sm.a[w];
+    eq += sm.b[w];
+  }
+  int pos = gt + min(eq, need);
+  const unsigned int below = (1u << lane) - 1u;
+  for (int i = beg + lane; i < beg + seg; i += 32) {
+    const T k = i < end ? key(i) : (T)0;
+    const unsigned int e = __ballot_sync(0xffffffffu, i < end && k == t);
+    const bool in = i < end && (k > t || (k == t && eq + __popc(e & below) < need));
+    const unsigned int b = __ballot_sync(0xffffffffu, in);
+    const int at = pos + __popc(b & below);
+    if (in && at < room) emit(at, i);
+    pos += __popc(b);
+    eq += __popc(e);
+  }
+}
+
+}  // namespace
+}  // namespace pa
