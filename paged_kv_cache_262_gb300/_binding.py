@@ -590,7 +590,50 @@ def swap_blocks(src_k_pools: Sequence, src_v_pools: Sequence, dst_k_pools: Seque
 
 
 # --------------------------------------------------------------- long contexts
+# A step calls these once a layer, with kernels of a few microseconds behind
+# them, so what a call costs on the host counts: the common case of every check
+# is a few attribute reads, and the messages are made only when one fails.
 _WS_SELECT, _WS_SPARSE, _WS_WEIGHTS = {}, {}, {}
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    f = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() builds an object, 3 us
+    return f(device) if f is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _all(device, *specs):
+    """Every (tensor, name, dtype, dims) is a contiguous CUDA tensor of that
+    dtype and rank on the current device."""
+    for t, name, dtype, nd in specs:
+        try:
+            if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.dim() == nd:
+                continue
+        except AttributeError:
+            pass
+        _need(t, dtype, name, nd)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _err_ptr(err_flag, device):
+    if err_flag is None:
+        return None
+    p = _flag(err_flag)
+    if err_flag.get_device() != device:
+        raise ValueError(f"err_flag is on {err_flag.device}, the current device is cuda:{device}")
+    return p
+
+
+def _bad(what):
+    raise ValueError(what)
 
 
 def _new(shape, dtype, device, stream):
@@ -602,56 +645,53 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call_ws(cache, need, device, stream):
-    """The workspace of a call that was given none: cached per (device,
-    stream), except under graph capture, where the graph's own memory holds
-    it -- a replay must not share the cache with the calls outside it."""
+def _call_ws(cache, need, device, stream, raw):
+    """(pointer, bytes, tensor) of the workspace of a call that was given
+    none: cached per (device, stream), except under graph capture, where the
+    graph's own memory holds it -- a replay must not share the cache with the
+    calls outside it."""
+    if need == 0:
+        return None, 0, None
     import torch
-    if need and torch.cuda.is_current_stream_capturing():
-        return _new((need,), torch.uint8, device, stream)
-    return _cached_ws(cache, need, device, stream) if need else None
+    idx = device.index
+    if torch.cuda.is_current_stream_capturing():
+        ws = _new((need,), torch.uint8, device, stream)
+    else:
+        ws = cache.get((idx, raw))
+        if ws is None or ws.numel() < need:
+            ws = _cached_ws(cache, need, device, stream)
+    return ws.data_ptr(), ws.numel(), ws
 
 
-def _cache_args(k_pool, block_tables, context_lens, v_pool=None):
+def _given_ws(workspace):
+    return _ws(workspace), workspace.numel() * workspace.element_size(), workspace
+
+
+def _weight_args(weights, weights_out, weight_rows, S, hkv, max_ctx, dev):
     import torch
-    _need(k_pool, torch.bfloat16, "k_pool", 4)
-    if v_pool is not None:
-        _need(v_pool, torch.bfloat16, "v_pool", 4)
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
-
-
-def _cache_desc(k_shape, block_tables, S, max_context_len) -> DecodeDesc:
-    """The desc of a call without queries."""
-    nblk, hkv, bs, d = k_shape
-    mb = int(block_tables.shape[1])
-    return DecodeDesc(int(S), int(hkv), int(hkv), int(d), int(bs), int(nblk), mb,
-                      int(max_context_len if max_context_len is not None else mb * bs), 1.0)
-
-
-def _weight_args(weights, weights_out, weight_rows, S, hkv, desc):
-    import torch
-    _need(weights, torch.float32, "weights", 3)
     if weights_out is None:
         weights_out = weights
-    _need(weights_out, torch.float32, "weights_out", 3)
-    if tuple(weights_out.shape) != tuple(weights.shape):
-        raise ValueError(f"weights_out must have weights' shape {tuple(weights.shape)}")
-    if weights_out is not weights and weights.numel():
-        a, b, n = weights.data_ptr(), weights_out.data_ptr(), weights.numel() * 4
+        _all(dev, (weights, "weights", torch.float32, 3))
+    else:
+        _all(dev, (weights, "weights", torch.float32, 3), (weights_out, "weights_out", torch.float32, 3))
+        if weights_out.shape != weights.shape:
+            _bad(f"weights_out must have weights' shape {tuple(weights.shape)}")
+        a, b = weights.data_ptr(), weights_out.data_ptr()
+        n = weights.numel() * 4
         if a != b and a < b + n and b < a + n:
-            raise ValueError("weights and weights_out overlap: pass the same tensor, or another")
-    if weights.shape[1] != hkv:
-        raise ValueError(f"weights has {weights.shape[1]} kv heads, the pools {hkv}")
-    if weights.shape[2] < desc.max_context_len:
-        raise ValueError(f"weights has room for {weights.shape[2]} tokens, max_context_len is {desc.max_context_len}")
+            _bad("weights and weights_out overlap: pass the same tensor, or another")
+    nr, wh, width = weights.shape
+    if wh != hkv:
+        _bad(f"weights has {wh} kv heads, the pools {hkv}")
+    if width < max_ctx:
+        _bad(f"weights has room for {width} tokens, max_context_len is {max_ctx}")
     if weight_rows is not None:
-        _need(weight_rows, torch.int32, "weight_rows", 1)
+        _all(dev, (weight_rows, "weight_rows", torch.int32, 1))
         if weight_rows.shape[0] < S:
-            raise ValueError(f"weight_rows has {weight_rows.shape[0]} rows, needs {S}")
-    elif weights.shape[0] < S:
-        raise ValueError(f"weights has {weights.shape[0]} rows, needs {S}")
-    return weights_out
+            _bad(f"weight_rows has {weight_rows.shape[0]} rows, needs {S}")
+    elif nr < S:
+        _bad(f"weights has {nr} rows, needs {S}")
+    return weights_out, nr, width
 
 
 def block_key_bounds(k_pool, bounds, block_tables, context_lens, start_lens=None, *, max_new_tokens=None,
@@ -660,24 +700,28 @@ def block_key_bounds(k_pool, bounds, block_tables, context_lens, start_lens=None
     from start_lens[s] on into bounds [num_blocks][Hkv][2][D] (see
     pagedattn.h); returns bounds."""
     import torch
-    _cache_args(k_pool, block_tables, context_lens)
-    _need(bounds, torch.bfloat16, "bounds", 4)
+    bf, i32, dev = torch.bfloat16, torch.int32, _current_device()
+    _all(dev, (k_pool, "k_pool", bf, 4), (bounds, "bounds", bf, 4), (block_tables, "block_tables", i32, 2),
+         (context_lens, "context_lens", i32, 1))
     nblk, hkv, bs, d = k_pool.shape
-    if tuple(bounds.shape) != (nblk, hkv, 2, d):
-        raise ValueError(f"bounds must be [{nblk}][{hkv}][2][{d}]")
-    S = context_lens.shape[0]
-    rows = [("block_tables", S)]
+    if bounds.shape != (nblk, hkv, 2, d):
+        _bad(f"bounds must be [{nblk}][{hkv}][2][{d}]")
+    (S,), (brows, mb), start = context_lens.shape, block_tables.shape, None
+    if brows < S:
+        _bad(f"block_tables has {brows} rows, needs {S}")
     if start_lens is not None:
-        _need(start_lens, torch.int32, "start_lens", 1)
-        rows.append(("start_lens", S))
-    _shapes(k_pool=k_pool, bounds=bounds, block_tables=block_tables, context_lens=context_lens, start_lens=start_lens,
-            rows=rows)
-    desc = _cache_desc(k_pool.shape, block_tables, S, max_context_len)
-    st = load().pa_block_key_bounds(_c.byref(desc), _ptr(k_pool), _ptr(block_tables), _ptr(context_lens),
-                                    _ptr(start_lens),
-                                    int(max_new_tokens if max_new_tokens is not None else desc.max_context_len),
-                                    _ptr(bounds), _flag(err_flag), _stream_ptr(stream))
-    _check(st, "pa_block_key_bounds")
+        _all(dev, (start_lens, "start_lens", i32, 1))
+        if start_lens.shape[0] < S:
+            _bad(f"start_lens has {start_lens.shape[0]} rows, needs {S}")
+        start = start_lens.data_ptr()
+    most = mb * bs if max_context_len is None else int(max_context_len)
+    desc = DecodeDesc(S, hkv, hkv, d, bs, nblk, mb, most, 1.0)
+    st = load().pa_block_key_bounds(_c.byref(desc), k_pool.data_ptr(), block_tables.data_ptr(),
+                                    context_lens.data_ptr(), start,
+                                    most if max_new_tokens is None else int(max_new_tokens), bounds.data_ptr(),
+                                    _err_ptr(err_flag, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "pa_block_key_bounds")
     return bounds
 
 
@@ -686,32 +730,56 @@ def select_blocks(q, bounds, block_tables, context_lens, num_select, *, block_si
     """The logical blocks each (sequence, kv head) attends this step, int32
     [num_seqs][Hkv][num_select], increasing, then -1 (see pagedattn.h)."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(bounds, torch.bfloat16, "bounds", 4)
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
-    nblk, hkv, two, d = bounds.shape
-    S, k = q.shape[0], int(num_select)
-    if two != 2 or q.shape[2] != d:
-        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim] of q's head_dim")
+    bf, i32, dev = torch.bfloat16, torch.int32, _current_device()
+    _all(dev, (q, "q", bf, 3), (bounds, "bounds", bf, 4), (block_tables, "block_tables", i32, 2),
+         (context_lens, "context_lens", i32, 1))
+    (nblk, hkv, two, d), (S, hq, qd), (brows, mb) = bounds.shape, q.shape, block_tables.shape
+    k, bs = int(num_select), int(block_size)
+    if two != 2 or qd != d:
+        _bad("bounds must be [num_blocks][num_kv_heads][2][head_dim] of q's head_dim")
+    if brows < S or context_lens.shape[0] < S:
+        _bad(f"block_tables has {brows} rows, context_lens {context_lens.shape[0]}, needs {S}")
+    if k <= 0:
+        _bad(f"num_select must be positive, got {k}")
     if selected is None:
-        selected = _new((S, hkv, k), torch.int32, q.device, stream)
-    _need(selected, torch.int32, "selected", 3)
-    if tuple(selected.shape) != (S, hkv, k):
-        raise ValueError(f"selected must be [{S}][{hkv}][{k}]")
-    _shapes(q=q, bounds=bounds, block_tables=block_tables, context_lens=context_lens, selected=selected,
-            rows=(("block_tables", S), ("context_lens", S)))
-    desc = _cache_desc((nblk, hkv, int(block_size), d), block_tables, S, max_context_len)
-    desc.num_q_heads = int(q.shape[1])
-    lib = load()
-    if workspace is None:
-        workspace = _call_ws(_WS_SELECT, int(lib.pa_select_blocks_workspace_bytes(_c.byref(desc))), q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.pa_select_blocks(_c.byref(desc), _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), k,
-                              int(sink_blocks), int(recent_blocks), _ptr(selected), _ws(workspace), ws_bytes,
-                              _flag(err_flag), _stream_ptr(stream))
-    _check(st, "pa_select_blocks")
+        selected = _new((S, hkv, k), i32, q.device, stream)
+    else:
+        _all(dev, (selected, "selected", i32, 3))
+        if selected.shape != (S, hkv, k):
+            _bad(f"selected must be [{S}][{hkv}][{k}]")
+    desc = DecodeDesc(S, hq, hkv, d, bs, nblk, mb, mb * bs if max_context_len is None else int(max_context_len), 1.0)
+    lib, raw = load(), _raw_stream(stream, dev)
+    ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
+        _WS_SELECT, lib.pa_select_blocks_workspace_bytes(_c.byref(desc)), q.device, stream, raw)
+    st = lib.pa_select_blocks(_c.byref(desc), q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(),
+                              context_lens.data_ptr(), k, int(sink_blocks), int(recent_blocks), selected.data_ptr(),
+                              ws, ws_bytes, _err_ptr(err_flag, dev), raw)
+    if st:
+        _check(st, "pa_select_blocks")
     return selected
+
+
+def _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream):
+    """The checks and the desc that the two decode calls share; (out, desc)."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    _all(dev, (q, "q", bf, 3), (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4),
+         (block_tables, "block_tables", i32, 2), (context_lens, "context_lens", i32, 1))
+    (nblk, hkv, bs, d), (S, hq, qd), (brows, mb) = k_pool.shape, q.shape, block_tables.shape
+    if v_pool.shape != k_pool.shape:
+        _bad(f"k_pool {tuple(k_pool.shape)} and v_pool {tuple(v_pool.shape)} differ")
+    if qd != d:
+        _bad(f"q head_dim {qd} != the pools' {d}")
+    if brows < S or context_lens.shape[0] < S:
+        _bad(f"block_tables has {brows} rows, context_lens {context_lens.shape[0]}, needs {S}")
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _new(q.shape, bf, q.device, stream)
+    else:
+        _all(dev, (out, "out", bf, 3))
+        if out.shape != q.shape:
+            _bad(f"out must have q's shape {tuple(q.shape)}")
+    return out, DecodeDesc(S, hq, hkv, d, bs, nblk, mb, mb * bs if max_context_len is None else int(max_context_len),
+                           d**-0.5 if scale is None else float(scale))
 
 
 def paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens, selected, out=None, *, scale=None,
@@ -719,28 +787,20 @@ def paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens,
     """Decode attention over the listed blocks of every (sequence, kv head)
     (see pagedattn.h)."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _cache_args(k_pool, block_tables, context_lens, v_pool)
-    _need(selected, torch.int32, "selected", 3)
-    if out is None:
-        out = _new(q.shape, q.dtype, q.device, stream)
-    _need(out, torch.bfloat16, "out", 3)
-    S = q.shape[0]
-    _attn_shapes(q, k_pool, v_pool, block_tables, context_lens, out, S)
-    _shapes(q=q, selected=selected, rows=(("selected", S),))
-    if selected.shape[1] != k_pool.shape[1]:
-        raise ValueError(f"selected has {selected.shape[1]} kv heads, the pools {k_pool.shape[1]}")
-    desc = make_desc(q, k_pool, block_tables, scale=scale, max_context_len=max_context_len)
-    k = int(selected.shape[2])
-    lib = load()
-    if workspace is None:
-        workspace = _call_ws(_WS_SPARSE, int(lib.pa_decode_sparse_workspace_bytes(_c.byref(desc), k)), q.device,
-                             stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.pa_paged_attention_decode_sparse(_c.byref(desc), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
-                                              _ptr(context_lens), _ptr(selected), k, _ptr(out), _ws(workspace),
-                                              ws_bytes, _flag(err_flag), _stream_ptr(stream))
-    _check(st, "pa_paged_attention_decode_sparse")
+    dev = _current_device()
+    out, desc = _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
+    _all(dev, (selected, "selected", torch.int32, 3))
+    rows, heads, k = selected.shape
+    if rows < desc.num_seqs or heads != desc.num_kv_heads:
+        _bad(f"selected must be [{desc.num_seqs}][{desc.num_kv_heads}][num_select], got {tuple(selected.shape)}")
+    lib, raw = load(), _raw_stream(stream, dev)
+    ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
+        _WS_SPARSE, lib.pa_decode_sparse_workspace_bytes(_c.byref(desc), k), q.device, stream, raw)
+    st = lib.pa_paged_attention_decode_sparse(_c.byref(desc), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                              block_tables.data_ptr(), context_lens.data_ptr(), selected.data_ptr(),
+                                              k, out.data_ptr(), ws, ws_bytes, _err_ptr(err_flag, dev), raw)
+    if st:
+        _check(st, "pa_paged_attention_decode_sparse")
     return out
 
 
@@ -750,26 +810,20 @@ def paged_attention_decode_weights(q, k_pool, v_pool, block_tables, context_lens
     """Decode attention that adds every key's attention weight to `weights`
     [num_rows][Hkv][max_tokens] (in place, or into weights_out; see
     pagedattn.h); returns (out, weights_out)."""
-    import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _cache_args(k_pool, block_tables, context_lens, v_pool)
-    if out is None:
-        out = _new(q.shape, q.dtype, q.device, stream)
-    _need(out, torch.bfloat16, "out", 3)
-    S = q.shape[0]
-    _attn_shapes(q, k_pool, v_pool, block_tables, context_lens, out, S)
-    desc = make_desc(q, k_pool, block_tables, scale=scale, max_context_len=max_context_len)
-    weights_out = _weight_args(weights, weights_out, weight_rows, S, k_pool.shape[1], desc)
-    _shapes(q=q, weights=weights, weights_out=weights_out, weight_rows=weight_rows)
-    lib = load()
-    if workspace is None:
-        workspace = _call_ws(_WS_WEIGHTS, int(lib.pa_decode_weights_workspace_bytes(_c.byref(desc))), q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dev = _current_device()
+    out, desc = _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
+    weights_out, nr, width = _weight_args(weights, weights_out, weight_rows, desc.num_seqs, desc.num_kv_heads,
+                                          desc.max_context_len, dev)
+    lib, raw = load(), _raw_stream(stream, dev)
+    ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
+        _WS_WEIGHTS, lib.pa_decode_weights_workspace_bytes(_c.byref(desc)), q.device, stream, raw)
     st = lib.pa_paged_attention_decode_weights(
-        _c.byref(desc), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), _ptr(weights),
-        _ptr(weights_out), _ptr(weight_rows), int(weights.shape[0]), int(weights.shape[2]), _ptr(out), _ws(workspace),
-        ws_bytes, _flag(err_flag), _stream_ptr(stream))
-    _check(st, "pa_paged_attention_decode_weights")
+        _c.byref(desc), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
+        None if weight_rows is None else weight_rows.data_ptr(), nr, width, out.data_ptr(), ws, ws_bytes,
+        _err_ptr(err_flag, dev), raw)
+    if st:
+        _check(st, "pa_paged_attention_decode_weights")
     return out, weights_out
 
 
@@ -781,39 +835,41 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
     place; see pagedattn.h); returns (kept [num_seqs][Hkv][max_keep_len],
     new_lens [num_seqs])."""
     import torch
-    _cache_args(k_pool, block_tables, context_lens, v_pool)
-    _need(keep_lens, torch.int32, "keep_lens", 1)
-    hkv = k_pool.shape[1]
-    S, mk = context_lens.shape[0], int(max_keep_len)
+    bf, i32, dev = torch.bfloat16, torch.int32, _current_device()
+    _all(dev, (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4), (block_tables, "block_tables", i32, 2),
+         (context_lens, "context_lens", i32, 1), (keep_lens, "keep_lens", i32, 1))
+    (nblk, hkv, bs, d), (S,), (brows, mb), mk = k_pool.shape, context_lens.shape, block_tables.shape, int(max_keep_len)
+    if v_pool.shape != k_pool.shape:
+        _bad(f"k_pool {tuple(k_pool.shape)} and v_pool {tuple(v_pool.shape)} differ")
     if mk <= 0:
-        raise ValueError(f"max_keep_len must be positive, got {mk}")
-    rows = [("block_tables", S), ("keep_lens", S)]
+        _bad(f"max_keep_len must be positive, got {mk}")
+    if brows < S or keep_lens.shape[0] < S:
+        _bad(f"block_tables has {brows} rows, keep_lens {keep_lens.shape[0]}, needs {S}")
+    dst = None
     if dst_tables is not None:
-        _need(dst_tables, torch.int32, "dst_tables", 2)
-        rows.append(("dst_tables", S))
-        if dst_tables.shape[1] != block_tables.shape[1]:
-            raise ValueError("dst_tables must be as wide as block_tables")
+        _all(dev, (dst_tables, "dst_tables", i32, 2))
+        if dst_tables.shape[0] < S or dst_tables.shape[1] != mb:
+            _bad(f"dst_tables must be [{S}][{mb}], as wide as block_tables")
+        dst = dst_tables.data_ptr()
     if kept is None:
-        kept = _new((S, hkv, mk), torch.int32, k_pool.device, stream)
+        kept = _new((S, hkv, mk), i32, k_pool.device, stream)
     if new_lens is None:
-        new_lens = _new((S,), torch.int32, k_pool.device, stream)
-    _need(kept, torch.int32, "kept", 3)
-    _need(new_lens, torch.int32, "new_lens", 1)
-    if tuple(kept.shape) != (S, hkv, mk) or new_lens.shape[0] != S:
-        raise ValueError(f"kept must be [{S}][{hkv}][{mk}] and new_lens [{S}]")
+        new_lens = _new((S,), i32, k_pool.device, stream)
+    _all(dev, (kept, "kept", i32, 3), (new_lens, "new_lens", i32, 1))
+    if kept.shape != (S, hkv, mk) or new_lens.shape[0] != S:
+        _bad(f"kept must be [{S}][{hkv}][{mk}] and new_lens [{S}]")
     if S and new_lens.data_ptr() == context_lens.data_ptr():
-        raise ValueError("new_lens must not be context_lens")
-    desc = _cache_desc(k_pool.shape, block_tables, S, max_context_len)
-    weights_out = _weight_args(weights, weights_out, weight_rows, S, hkv, desc)
-    _shapes(k_pool=k_pool, v_pool=v_pool, block_tables=block_tables, context_lens=context_lens, keep_lens=keep_lens,
-            weights=weights, dst_tables=dst_tables, weights_out=weights_out, weight_rows=weight_rows, kept=kept,
-            new_lens=new_lens, rows=rows)
-    st = load().pa_evict_tokens(_c.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(dst_tables),
-                                _ptr(context_lens), _ptr(keep_lens), mk, int(sink_tokens), int(recent_tokens),
-                                _ptr(weights), _ptr(weights_out), _ptr(weight_rows), int(weights.shape[0]),
-                                int(weights.shape[2]), _ptr(kept), _ptr(new_lens), _flag(err_flag),
-                                _stream_ptr(stream))
-    _check(st, "pa_evict_tokens")
+        _bad("new_lens must not be context_lens")
+    most = mb * bs if max_context_len is None else int(max_context_len)
+    weights_out, nr, width = _weight_args(weights, weights_out, weight_rows, S, hkv, most, dev)
+    desc = DecodeDesc(S, hkv, hkv, d, bs, nblk, mb, most, 1.0)
+    st = load().pa_evict_tokens(_c.byref(desc), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), dst,
+                                context_lens.data_ptr(), keep_lens.data_ptr(), mk, int(sink_tokens),
+                                int(recent_tokens), weights.data_ptr(), weights_out.data_ptr(),
+                                None if weight_rows is None else weight_rows.data_ptr(), nr, width, kept.data_ptr(),
+                                new_lens.data_ptr(), _err_ptr(err_flag, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "pa_evict_tokens")
     return kept, new_lens
 
 

@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(256) key_bounds_kernel(const BoundsArgs a) {
 // -------------------------------------------------------------- selection
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelChunk = 128;     // blocks a CTA scores
 constexpr int kSelKeys = 8192;     // keys held in shared memory; more are re-read from the workspace
 constexpr int kSelRefine = 256;    // blocks near the threshold that are ranked in shared memory
 
@@ -108,24 +107,60 @@ struct SelectArgs {
   unsigned long long *cnt;     // [S][Hkv] arrivals
   int32_t *err;
   int Hq, Hkv, G, num_blocks, max_blocks, max_ctx, k, sink, recent, B, max_chunks;
+  int chunk;                   // blocks a CTA scores, a multiple of 16 kSelWarps
   size_t stride;
   unsigned int epoch;
 };
 
 // A block's score in 64 bits, by one warp: every product of two bf16 values
-// is exact, and blocks of equal bounds get equal sums.
-template <int D>
-__device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int pg, int h, int lane) {
-  constexpr int P = D / 32;
+// is exact, and blocks of equal bounds get equal sums.  The heads whose fp32
+// sum is more than `slack` below the largest cannot be the maximum (slack
+// covers twice the error of a plain fp32 sum; infinite: every head is summed
+// in 64 bits).
+template <int D, int H>  // H: heads, at least G
+__device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int pg, int h, float slack, int lane) {
+  constexpr int P = D / 32;  // elements of a lane, a multiple of two
   const __nv_bfloat16 *lo = reinterpret_cast<const __nv_bfloat16 *>(a.bounds) + ((size_t)pg * a.Hkv + h) * 2 * D;
+  float bl[P], bh[P];
+#pragma unroll
+  for (int p = 0; p < P; p += 2) {
+    const uint32_t l = __ldg(reinterpret_cast<const uint32_t *>(lo + lane * P + p));
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(lo + D + lane * P + p));
+    bl[p] = bf16_lo(l), bl[p + 1] = bf16_hi(l);
+    bh[p] = bf16_lo(u), bh[p + 1] = bf16_hi(u);
+  }
+  float fs[H], top = -INFINITY;
+  uint32_t qv[H][P / 2];
+#pragma unroll
+  for (int g = 0; g < H; ++g) {
+    fs[g] = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; p += 2)
+      qv[g][p / 2] = g < a.G ? __ldg(reinterpret_cast<const uint32_t *>(q + g * D + lane * P + p)) : 0u;
+  }
+#pragma unroll
+  for (int g = 0; g < H; ++g)
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const float x = p & 1 ? bf16_hi(qv[g][p / 2]) : bf16_lo(qv[g][p / 2]);
+      fs[g] += x * (x > 0.f ? bh[p] : bl[p]);
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int g = 0; g < H; ++g) fs[g] += __shfl_xor_sync(0xffffffffu, fs[g], o);
+#pragma unroll
+  for (int g = 0; g < H; ++g)
+    if (g < a.G) top = fmaxf(top, fs[g]);
   double best = -INFINITY;
-  for (int g = 0; g < a.G; ++g) {
+#pragma unroll
+  for (int g = 0; g < H; ++g) {
+    if (g >= a.G || fs[g] < top - slack) continue;  // (the same for every lane)
     double sum = 0.0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int d = lane * P + p;
-      const float x = __bfloat162float(q[g * D + d]);
-      if (x != 0.f) sum += (double)x * (double)__bfloat162float(lo[x > 0.f ? D + d : d]);
+      const float x = p & 1 ? bf16_hi(qv[g][p / 2]) : bf16_lo(qv[g][p / 2]);
+      if (x != 0.f) sum += (double)x * (double)(x > 0.f ? bh[p] : bl[p]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -135,36 +170,178 @@ __device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int p
   return best;
 }
 
+// The last CTA of a row: its candidates' keys are in the workspace.
+struct RowSelect {
+  SelectSmem<kSelThreads> sm;
+  uint32_t keys[kSelKeys];
+  double ex[kSelRefine];
+  int exi[kSelRefine];
+  float mx[kSelWarps];
+  int nex, ngt, last;
+  uint32_t thr;
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+__device__ void select_row(const SelectArgs &a, RowSelect &r, size_t row, int s, int h, int n, int nchunks,
+                           int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+  const int first = a.sink, end = n - a.recent;
+  const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
+  const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
+  uint32_t *keys = a.keys + row * a.stride;
+  int32_t *out = a.selected + row * a.k;
+  const int N = end - first, want = a.k - a.sink - a.recent;
+  const bool in_smem = N <= kSelKeys;
+  if (want > 0 && in_smem) {
+#pragma unroll 8
+    for (int i = tid; i < N; i += kSelThreads) r.keys[i] = __ldcg(keys + i);
+  }
+  for (int i = tid; i < a.sink; i += kSelThreads) out[i] = i;
+  for (int i = tid; i < a.recent; i += kSelThreads) out[a.k - a.recent + i] = end + i;
+  if (want == 0) return;
+  // How far an fp32 score may be from the exact one: every one of the 2 D / 16
+  // MMAs adds 17 terms no larger than Q M, Q = max_g sum_d |q_gd|, M = max
+  // |bound|, each cut at 2^-23 or better of the largest: less than 2^-14 Q M
+  // in all.
+  float x = 0.f, M = 0.f;
+  for (int g = warp; g < a.G; g += kSelWarps) {
+    float y = 0.f;
+#pragma unroll
+    for (int d = 2 * lane; d < D; d += 64) {
+      const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(q + g * D + d));
+      y += fabsf(bf16_lo(v)) + fabsf(bf16_hi(v));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    x = y >= x ? y : y == y ? x : INFINITY;
+  }
+  for (int c = lane; c < nchunks; c += 32) M = fmaxf(M, __ldcg(a.maxabs + row * a.max_chunks + c));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  __syncthreads();
+  if (lane == 0) r.mx[warp] = x;
+  if (tid == 0) r.nex = r.ngt = 0;
+  __syncthreads();
+  float Q = 0.f;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) Q = fmaxf(Q, r.mx[w]);
+  const bool finite = Q * M < INFINITY;  // false for NaN too: then no fp32 score is trusted
+  const float slack = finite ? 2.f * 6.103515625e-05f * (Q * M) : INFINITY;
+
+  auto key32 = [&](int i) -> uint32_t { return in_smem ? r.keys[i] : __ldcg(keys + i); };
+  uint32_t lo = 0u, hi = 0xfffffffeu;  // (no score's key is above it)
+  if (finite) {
+    uint32_t t;
+    if (N <= kSelThreads) {  // few: every key's rank by counting
+      const uint32_t mine = tid < N ? r.keys[tid] : 0u;
+      int gt = 0, ge = 0;
+      for (int j = 0; j < N; ++j) {
+        const uint32_t o = r.keys[j];
+        gt += o > mine;
+        ge += o >= mine;
+      }
+      if (tid < N && gt < want && want <= ge) r.thr = mine;  // (equal keys write the same)
+      __syncthreads();
+      t = r.thr;
+    } else {
+      t = kth_largest<kSelThreads, uint32_t>(key32, N, want, r.sm, tid).key;
+    }
+    if (t != 0u) {
+      const float v = key_value(t);
+      lo = order_key(__fsub_rd(v, slack));
+      hi = order_key(__fadd_ru(v, slack));
+    } else {
+      hi = 0u;  // blocks outside the pool are among the chosen: those that can be read all are
+    }
+  }
+  // blocks above hi are chosen whatever their rounding, those below lo are not
+  int mine = 0;
+  for (int i = tid; i < N; i += kSelThreads) {
+    const uint32_t k = key32(i);
+    mine += k > hi;
+    if (k >= lo && k <= hi) {
+      const int at = atomicAdd(&r.nex, 1);
+      if (at < kSelRefine) r.exi[at] = i;
+    }
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0 && mine) atomicAdd(&r.ngt, mine);
+  __syncthreads();
+  const int near_ = r.nex, need = want - r.ngt;
+  auto emit = [&](int pos, int i) { out[a.sink + pos] = first + i; };
+  if (near_ == need || hi == 0u) {  // (of blocks outside the pool, the first)
+    take_above<kSelThreads, uint32_t>(key32, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, r.sm, tid, emit);
+    return;
+  }
+  if (near_ <= kSelRefine) {  // few: their exact scores, ranked by counting
+    for (int c = warp; c < near_; c += kSelWarps) {
+      const int pg = __ldg(bt + first + r.exi[c]);
+      const double e = pg >= 0 && pg < a.num_blocks ? exact_score<D, 8 * NT>(a, q, pg, h, slack, lane) : -INFINITY;
+      if (lane == 0) r.ex[c] = e;
+    }
+    __syncthreads();
+    for (int c = tid; c < near_; c += kSelThreads) {
+      int rank = 0;
+      for (int o = 0; o < near_; ++o) rank += r.ex[o] > r.ex[c] || (r.ex[o] == r.ex[c] && r.exi[o] < r.exi[c]);
+      (in_smem ? r.keys : keys)[r.exi[c]] = rank < need ? 0xffffffffu : 0u;
+    }
+    __syncthreads();
+    take_above<kSelThreads, uint32_t>(key32, N, hi, 0, want, r.sm, tid, emit);
+    return;
+  }
+  // many (scores that tie in numbers, infinite bounds): 64-bit keys for all of
+  // them in the workspace
+  unsigned long long *k64 = a.keys64 + row * a.stride;
+  for (int i = warp; i < N; i += kSelWarps) {
+    const uint32_t k = key32(i);
+    unsigned long long e = k > hi ? ~0ull : 0ull;
+    if (k >= lo && k <= hi) {
+      const int pg = __ldg(bt + first + i);
+      const bool ok = pg >= 0 && pg < a.num_blocks;
+      e = ok ? order_key64(exact_score<D, 8 * NT>(a, q, pg, h, slack, lane)) : 1ull;
+    }
+    if (lane == 0) k64[i] = e;
+  }
+  __threadfence_block();
+  __syncthreads();
+  auto key64 = [&](int i) -> unsigned long long { return k64[i]; };
+  const Kth<unsigned long long> t = kth_largest<kSelThreads, unsigned long long>(key64, N, want, r.sm, tid);
+  take_above<kSelThreads, unsigned long long>(key64, N, t.key, want - t.above, want, r.sm, tid, emit);
+}
+
+// grid (chunk, kv head, sequence).  Every CTA scores its chunk of a row; the
+// last of a row to finish selects from all of its scores.
+template <int D, int NT>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs a) {
   constexpr int CH = 2 * D / 32;  // 32-element steps over a block's bounds (lo, then hi)
-  __shared__ SelectSmem<kSelThreads> sm;
-  __shared__ uint32_t skeys[kSelKeys];
-  __shared__ double ex[kSelRefine];
-  __shared__ int exi[kSelRefine];
-  __shared__ float fmax_s[kSelWarps];
-  __shared__ int nex, ngt, last;
+  __shared__ RowSelect r;
   const int chunk = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.B;
   const size_t row = (size_t)s * a.Hkv + h;
-  int32_t *out = a.selected + row * a.k;
   const int ctx = __ldg(a.ctx + s);
   const bool bad = ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx;
   const int n = bad ? 0 : (ctx + B - 1) / B;
   if (n <= a.k) {  // every block, or none
     if (chunk == 0) {
+      int32_t *out = a.selected + row * a.k;
       for (int i = tid; i < a.k; i += kSelThreads) out[i] = i < n ? i : -1;
       if (bad && h == 0 && tid == 0 && a.err) atomicOr(a.err, PA_DEVERR_CTX);
     }
     return;
   }
-  const int nchunks = (n + kSelChunk - 1) / kSelChunk;
+  const int nchunks = (n + a.chunk - 1) / a.chunk;
   if (chunk >= nchunks) return;
   const int first = a.sink, end = n - a.recent;  // the blocks that compete
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
   const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
   uint32_t *keys = a.keys + row * a.stride;
+  const int i_end = min(end, (chunk + 1) * a.chunk);
+
+  // lane l's block of a tile: row l / 4 and that + 8; -2: not competing
+  auto page = [&](int i) -> int { return i >= first && i < i_end ? __ldg(bt + i) : -2; };
+  int i0 = chunk * a.chunk + warp * 16;
+  int pg[2] = {page(i0 + (lane >> 2)), page(i0 + 8 + (lane >> 2))};
 
   // ---- scores of this CTA's blocks: S[block][head] = [lo hi] . [q- q+], the
   // contraction in whatever order of d suits the loads (lane t of a quad takes
@@ -184,36 +361,28 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     }
   }
   uint32_t big = 0u;  // packed running max of |bound|
-  for (int t = warp; t < kSelChunk / 16; t += kSelWarps) {
-    const int i0 = chunk * kSelChunk + t * 16;
-    if (i0 >= end || i0 + 16 <= first) continue;
+  for (; i0 < i_end; i0 += 16 * kSelWarps) {
     uint4 x[2][CH];
     bool have[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = i0 + (lane >> 2) + 8 * r;
-      int pg = i >= first && i < end ? __ldg(bt + i) : -2;
-      if (pg != -2 && (pg < 0 || pg >= a.num_blocks)) {
-        if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
-        pg = -1;
-      }
-      have[r] = pg >= 0;
-      const uint4 *src = a.bounds + ((size_t)max(pg, 0) * a.Hkv + h) * (D / 4) + (lane & 3);
+    for (int e = 0; e < 2; ++e) {
+      have[e] = pg[e] >= 0 && pg[e] < a.num_blocks;
+      if (!have[e] && pg[e] != -2 && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+      const uint4 *src = a.bounds + ((size_t)(have[e] ? pg[e] : 0) * a.Hkv + h) * (D / 4) + (lane & 3);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) x[r][c] = have[r] ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < CH; ++c) x[e][c] = have[e] ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
     }
+    const int next = i0 + 16 * kSelWarps + (lane >> 2);
+    pg[0] = page(next);
+    pg[1] = page(next + 8);
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const uint4 u = x[0][c], v = x[1][c];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t ue = e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
-        const uint32_t ve = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
-        big = max2(big, max2(ue & 0x7fff7fffu, ve & 0x7fff7fffu));
-      }
+      big = max2(big, max2(max2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), max2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+      big = max2(big, max2(max2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), max2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
       const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -226,153 +395,68 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
       }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int e = 0; e < 2; ++e) {
       float best = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int g = nt * 8 + 2 * (lane & 3);
-        if (g < a.G) best = fmaxf(best, acc[nt][2 * r]);
-        if (g + 1 < a.G) best = fmaxf(best, acc[nt][2 * r + 1]);
+        if (g < a.G) best = fmaxf(best, acc[nt][2 * e]);
+        if (g + 1 < a.G) best = fmaxf(best, acc[nt][2 * e + 1]);
       }
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-      const int i = i0 + (lane >> 2) + 8 * r;
-      if ((lane & 3) == 0 && i >= first && i < end) keys[i - first] = have[r] ? order_key(best) : 0u;
+      const int i = i0 + (lane >> 2) + 8 * e;
+      if ((lane & 3) == 0 && i >= first && i < i_end) keys[i - first] = have[e] ? order_key(best) : 0u;
     }
   }
   float m = fmaxf(bf16_lo(big), bf16_hi(big));
   if (bf16_lo(big) != bf16_lo(big) || bf16_hi(big) != bf16_hi(big)) m = INFINITY;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) fmax_s[warp] = m;
+  if (lane == 0) r.mx[warp] = m;
   __threadfence();
   __syncthreads();
   if (tid == 0) {
 #pragma unroll
-    for (int w = 1; w < kSelWarps; ++w) m = fmaxf(m, fmax_s[w]);
+    for (int w = 1; w < kSelWarps; ++w) m = fmaxf(m, r.mx[w]);
     a.maxabs[row * a.max_chunks + chunk] = m;
+    if (nchunks > 1) {
+      __threadfence();
+      r.last = arrive_count(a.cnt + row, a.epoch) == (unsigned int)nchunks;
+    }
+  }
+  __syncthreads();
+  if (nchunks > 1) {
+    if (!r.last) return;
     __threadfence();
-    last = arrive_count(a.cnt + row, a.epoch) == (unsigned int)nchunks;
+    if (tid == 0) a.cnt[row] = 0ull;
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  if (tid == 0) a.cnt[row] = 0ull;
-
-  // ---- the last CTA of the row selects
-  for (int i = tid; i < a.sink; i += kSelThreads) out[i] = i;
-  for (int i = tid; i < a.recent; i += kSelThreads) out[a.k - a.recent + i] = end + i;
-  const int N = end - first, want = a.k - a.sink - a.recent;
-  if (want == 0) return;
-  // How far an fp32 score may be from the exact one: every one of the 2 D / 16
-  // MMAs adds 17 terms no larger than Q M, Q = max_g sum_d |q_gd|, M = max
-  // |bound|, each cut at 2^-23 or better of the largest: less than 2^-14 Q M
-  // in all.
-  float Q = 0.f;
-  for (int g = 0; g < a.G; ++g) {
-    float x = 0.f;
-    for (int d = lane; d < D; d += 32) x += fabsf(__bfloat162float(q[g * D + d]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    Q = x >= Q ? x : x == x ? Q : INFINITY;
-  }
-  float M = 0.f;
-  for (int c = lane; c < nchunks; c += 32) M = fmaxf(M, __ldcg(a.maxabs + row * a.max_chunks + c));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float slack = 2.f * 6.103515625e-05f * (Q * M);
-  const bool finite = Q * M < INFINITY;  // false for NaN: then no fp32 score is trusted
-
-  const bool in_smem = N <= kSelKeys;
-  if (in_smem)
-    for (int i = tid; i < N; i += kSelThreads) skeys[i] = __ldcg(keys + i);
-  uint32_t *kk = in_smem ? skeys : keys;  // writable; in global memory read past L1
-  __syncthreads();
-  auto key32 = [&](int i) -> uint32_t { return in_smem ? skeys[i] : __ldcg(keys + i); };
-  uint32_t lo = 0u, hi = 0xfffffffeu;  // (no score's key is above it)
-  if (finite) {
-    const Kth<uint32_t> t = kth_largest<kSelThreads, uint32_t>(key32, N, want, sm, tid);
-    if (t.key != 0u) {
-      const float v = key_value(t.key);
-      lo = order_key(__fsub_rd(v, slack));
-      hi = order_key(__fadd_ru(v, slack));
-    } else {
-      hi = 0u;  // blocks outside the pool are among the chosen: those that can be read all are
-    }
-  }
-  // blocks above hi are chosen whatever their rounding, those below lo are not
-  if (tid == 0) nex = ngt = 0;
-  __syncthreads();
-  int mine = 0;
-  for (int i = tid; i < N; i += kSelThreads) {
-    const uint32_t k = key32(i);
-    mine += k > hi;
-    if (k >= lo && k <= hi) {
-      const int at = atomicAdd(&nex, 1);
-      if (at < kSelRefine) exi[at] = i;
-    }
-  }
-  atomicAdd(&ngt, mine);
-  __syncthreads();
-  const int near_ = nex, need = want - ngt;
-  auto emit = [&](int pos, int i) { out[a.sink + pos] = first + i; };
-  if (near_ == need || hi == 0u) {  // (of blocks outside the pool, the first)
-    take_above<kSelThreads, uint32_t>(key32, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, sm, tid, emit);
-    return;
-  }
-  if (near_ <= kSelRefine) {  // few: their exact scores, ranked by counting
-    for (int c = warp; c < near_; c += kSelWarps) {
-      const int pg = __ldg(bt + first + exi[c]);
-      const double e = pg >= 0 && pg < a.num_blocks ? exact_score<D>(a, q, pg, h, lane) : -INFINITY;
-      if (lane == 0) ex[c] = e;
-    }
-    __syncthreads();
-    for (int c = tid; c < near_; c += kSelThreads) {
-      int rank = 0;
-      for (int o = 0; o < near_; ++o) rank += ex[o] > ex[c] || (ex[o] == ex[c] && exi[o] < exi[c]);
-      kk[exi[c]] = rank < need ? 0xffffffffu : 0u;
-    }
-    __syncthreads();
-    take_above<kSelThreads, uint32_t>(key32, N, hi, 0, want, sm, tid, emit);
-    return;
-  }
-  // many (scores that tie in numbers, infinite bounds): 64-bit keys for all of
-  // them in the workspace
-  unsigned long long *k64 = a.keys64 + row * a.stride;
-  for (int i = warp; i < N; i += kSelWarps) {
-    const uint32_t k = key32(i);
-    unsigned long long e = k > hi ? ~0ull : 0ull;
-    if (k >= lo && k <= hi) {
-      const int pg = __ldg(bt + first + i);
-      const double x = pg >= 0 && pg < a.num_blocks ? exact_score<D>(a, q, pg, h, lane) : -INFINITY;
-      e = pg >= 0 && pg < a.num_blocks ? order_key64(x) : 1ull;
-    }
-    if (lane == 0) k64[i] = e;
-  }
-  __threadfence_block();
-  __syncthreads();
-  auto key64 = [&](int i) -> unsigned long long { return k64[i]; };
-  const Kth<unsigned long long> t = kth_largest<kSelThreads, unsigned long long>(key64, N, want, sm, tid);
-  take_above<kSelThreads, unsigned long long>(key64, N, t.key, want - t.above, want, sm, tid, emit);
+  select_row<D, NT>(a, r, row, s, h, n, nchunks, tid);
 }
 
 struct SelectPlan {
-  int max_chunks = 0;
+  int chunk = 0, max_chunks = 0;
   size_t stride = 0, keys = 0, keys64 = 0, maxabs = 0, cnt = 0;
   size_t total() const { return keys + keys64 + maxabs + cnt; }
 };
 
-SelectPlan make_select_plan(const pa_decode_desc *d) {
+// Chunks of 128 blocks (a tile a warp), or as many more as make the rows fill
+// about two CTAs an SM: a CTA then has its table entries a tile ahead and pays
+// its start once for several tiles.
+SelectPlan make_select_plan(const pa_decode_desc *d, int sms) {
   SelectPlan p;
   const int64_t B = d->block_size;
   const size_t nblk = (size_t)std::max<int64_t>(1, ((int64_t)d->max_context_len + B - 1) / B);
   const size_t rows = (size_t)d->num_seqs * d->num_kv_heads;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
-  p.max_chunks = (int)((nblk + kSelChunk - 1) / kSelChunk);
+  const size_t per = (rows * nblk + 2 * (size_t)std::max(sms, 1) - 1) / (2 * (size_t)std::max(sms, 1));
+  const size_t unit = 16 * kSelWarps;
+  p.chunk = (int)std::min<size_t>(8 * unit, std::max<size_t>(1, (per + unit - 1) / unit) * unit);
+  p.max_chunks = (int)((nblk + p.chunk - 1) / p.chunk);
   p.stride = (nblk + 3) & ~(size_t)3;
   p.keys64 = up(rows * p.stride * 8);
   p.keys = up(rows * p.stride * 4);
-  p.maxabs = up(rows * p.max_chunks * 4);
+  p.maxabs = up(rows * ((nblk + unit - 1) / unit) * 4);  // (whatever the SM count)
   p.cnt = up(rows * 8);
   return p;
 }
@@ -429,7 +513,7 @@ extern "C" int pa_block_key_bounds(const pa_decode_desc *d, const void *k_pool, 
 extern "C" size_t pa_select_blocks_workspace_bytes(const pa_decode_desc *d) {
   using namespace pa;
   if (validate_decode_desc(d) != PA_OK) return 0;
-  return make_select_plan(d).total();
+  return make_select_plan(d, 1).total();
 }
 
 extern "C" int pa_select_blocks(const pa_decode_desc *d, const void *q, const void *bounds,
@@ -445,8 +529,11 @@ extern "C" int pa_select_blocks(const pa_decode_desc *d, const void *q, const vo
   if (!q || !bounds || !block_tables || !context_lens || !selected || !aligned16(q) || !aligned16(bounds))
     return PA_ERR_INVALID;
   if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
-  const SelectPlan p = make_select_plan(d);
-  if (!workspace || workspace_bytes < p.total() || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < make_select_plan(d, 1).total() || !aligned16(workspace))
+    return PA_ERR_WORKSPACE;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  const SelectPlan p = make_select_plan(d, sms);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   SelectArgs a{};
   a.q = static_cast<const __nv_bfloat16 *>(q);
@@ -470,6 +557,7 @@ extern "C" int pa_select_blocks(const pa_decode_desc *d, const void *q, const vo
   a.recent = recent_blocks;
   a.B = d->block_size;
   a.max_chunks = p.max_chunks;
+  a.chunk = p.chunk;
   a.stride = p.stride;
   a.epoch = next_decode_epoch();
   const dim3 grid(p.max_chunks, d->num_kv_heads, d->num_seqs);

@@ -40,12 +40,15 @@ struct EvictArgs {
   size_t max_tokens;
 };
 
-constexpr int kEvThreads = 1024;
-
-// grid (kv head, sequence)
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t skeys[];
-  __shared__ SelectSmem<kEvThreads> sm;
+// grid (kv head, sequence).  A row of weights that fits is held in shared
+// memory as it is (keys are made of it as they are looked at), so that what is
+// kept leaves straight from there, in place or not; a longer one is read again
+// for each pass, and its kept weights move by stretches, read before they are
+// written.
+template <int NT>
+__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
+  extern __shared__ float sw[];
+  __shared__ SelectSmem<NT> sm;
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
   int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int ctx = __ldg(a.ctx + s), keep = __ldg(a.keep + s);
@@ -57,7 +60,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictArg
   if (row < 0 || row >= a.num_rows) bits |= PA_DEVERR_ROW;
   if (a.rows && !bits) {  // a row that an earlier sequence names is that one's
     bool dup = false;
-    for (int t = tid; t < s; t += kEvThreads) dup |= __ldg(a.rows + t) == row;
+    for (int t = tid; t < s; t += NT) dup |= __ldg(a.rows + t) == row;
     if (__syncthreads_or(dup)) bits |= PA_DEVERR_ROW;
   }
   const int n = bits ? 0 : min(keep, ctx);
@@ -65,33 +68,42 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictArg
     a.new_lens[s] = bits ? ctx : n;
     if (bits && a.err) atomicOr(a.err, bits);
   }
-  for (int i = n + tid; i < a.max_keep; i += kEvThreads) kept[i] = -1;
+  for (int i = n + tid; i < a.max_keep; i += NT) kept[i] = -1;
   if (bits) return;
   const size_t wrow = ((size_t)row * a.Hkv + h) * a.max_tokens;
   const float *w = a.w_in + wrow;
-  if (n == ctx) {
-    for (int i = tid; i < n; i += kEvThreads) kept[i] = i;
-  } else {
-    for (int i = tid; i < a.sink; i += kEvThreads) kept[i] = i;
-    for (int i = tid; i < a.recent; i += kEvThreads) kept[n - a.recent + i] = ctx - a.recent + i;
-    const int N = ctx - a.sink - a.recent, want = n - a.sink - a.recent;
-    if (want > 0) {
-      const bool in_smem = N <= a.smem_keys;
-      if (in_smem) {
-        for (int i = tid; i < N; i += kEvThreads) skeys[i] = order_key(w[a.sink + i]);
-        __syncthreads();
-      }
-      auto key = [&](int i) -> uint32_t { return in_smem ? skeys[i] : order_key(w[a.sink + i]); };
-      const Kth<uint32_t> t = kth_largest<kEvThreads, uint32_t>(key, N, want, sm, tid);
-      take_above<kEvThreads, uint32_t>(key, N, t.key, want - t.above, want, sm, tid,
-                                       [&](int pos, int i) { kept[a.sink + pos] = a.sink + i; });
-    }
-  }
-  // the weights, in place or not: a stretch is read before it is written, and
-  // what is written was read (kept increases)
-  __syncthreads();
   float *wo = a.w_out + wrow;
-  for (int base = 0; base < ctx; base += kEvThreads) {
+  if (n == ctx) {
+    for (int i = tid; i < n; i += NT) kept[i] = i;
+    if (wo != w)
+      for (int i = tid; i < n; i += NT) wo[i] = w[i];
+    return;
+  }
+  const int N = ctx - a.sink - a.recent, want = n - a.sink - a.recent;
+  const bool in_smem = ctx <= a.smem_keys;
+  if (in_smem) {
+#pragma unroll 8
+    for (int i = tid; i < ctx; i += NT) sw[i] = __ldcs(w + i);
+    __syncthreads();
+  }
+  auto put = [&](int i, int j) {  // token j is kept, as number i
+    kept[i] = j;
+    if (in_smem) wo[i] = sw[j];
+  };
+  for (int i = tid; i < a.sink; i += NT) put(i, i);
+  for (int i = tid; i < a.recent; i += NT) put(n - a.recent + i, ctx - a.recent + i);
+  if (want > 0) {
+    auto key = [&](int i) -> uint32_t { return order_key(in_smem ? sw[a.sink + i] : w[a.sink + i]); };
+    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key, N, want, sm, tid);
+    take_above<NT, uint32_t>(key, N, t.key, want - t.above, want, sm, tid,
+                             [&](int pos, int i) { put(a.sink + pos, a.sink + i); });
+  }
+  if (in_smem) {
+    for (int i = n + tid; i < ctx; i += NT) wo[i] = 0.f;
+    return;
+  }
+  __syncthreads();
+  for (int base = 0; base < ctx; base += NT) {
     const int i = base + tid;
     const float v = i < n ? w[min(max(kept[i], 0), ctx - 1)] : 0.f;
     __syncthreads();
@@ -100,14 +112,25 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictArg
 }
 
 // Rows of K (even) or V (odd) of one (sequence, kv head), CPS 16-byte chunks
-// of each: grid (2 * slices, kv head, sequence).
+// of each: grid (2 * slices, kv head, sequence).  A stretch's rows are on
+// their way while the one before is stored, and the list and table entries of
+// the one after while both are: sources lie at or behind the stretch, so
+// reading ahead of the stores changes nothing, and the barrier before the
+// stores of a stretch ends its reads.
 constexpr int kMvThreads = 256;
-constexpr int kMvUnroll = 4;
+#ifndef PA_MV_UNROLL
+#define PA_MV_UNROLL 4
+#endif
+#ifndef PA_MV_CPS
+#define PA_MV_CPS 4
+#endif
+constexpr int kMvUnroll = PA_MV_UNROLL;
 
 template <int D, int CPS>
 __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs a) {
   constexpr int C = D / 8;
   constexpr int T = kMvThreads / CPS;  // tokens an access of the CTA covers
+  constexpr int U = kMvUnroll;
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
   const int c = (blockIdx.x >> 1) * CPS + tid % CPS, t0 = tid / CPS;
   const int n = min(__ldg(a.new_lens + s), a.max_keep);
@@ -115,29 +138,49 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
   if (n <= 0 || __ldg(kept) < 0) return;
   uint4 *pool = (blockIdx.x & 1) ? a.vp : a.kp;
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks, *dt = a.dst + (size_t)s * a.max_blocks;
-  const int B = a.B;
+  const int B = a.B, lb = B == 16 ? 4 : 5;
   int bad = 0;
-  for (int base = 0; base < n; base += T * kMvUnroll) {
-    uint4 x[kMvUnroll];
-    int64_t to[kMvUnroll];
+  int j[U], sb[U], db[U];       // list and table entries of the stretch to load
+  int64_t to[U], to_next[U];
+  uint4 x[U], x_next[U];
+  auto entries = [&](int base) {
 #pragma unroll
-    for (int u = 0; u < kMvUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int i = base + u * T + t0;
-      to[u] = -1;
-      if (i < n) {
-        const int j = __ldg(kept + i);
-        const int sb = j >= 0 && j / B < a.max_blocks ? __ldg(bt + j / B) : -1, db = __ldg(dt + i / B);
-        if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
-          bad = 1;
-        } else if (sb != db || j % B != i % B) {
-          to[u] = (((int64_t)db * a.Hkv + h) * B + i % B) * C + c;
-          x[u] = __ldcg(pool + (((int64_t)sb * a.Hkv + h) * B + j % B) * C + c);
-        }
+      j[u] = i < n ? __ldg(kept + i) : -1;
+      db[u] = i < n ? __ldg(dt + (i >> lb)) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) sb[u] = j[u] >= 0 && (j[u] >> lb) < a.max_blocks ? __ldg(bt + (j[u] >> lb)) : -1;
+  };
+  auto load = [&](int base) {  // of the entries at hand
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = base + u * T + t0;
+      to_next[u] = -1;
+      if (i >= n) continue;
+      if (sb[u] < 0 || sb[u] >= a.num_blocks || db[u] < 0 || db[u] >= a.num_blocks) {
+        bad = 1;
+      } else if (sb[u] != db[u] || ((i ^ j[u]) & (B - 1))) {
+        to_next[u] = (((int64_t)db[u] * a.Hkv + h) * B + (i & (B - 1))) * C + c;
+        x_next[u] = __ldcg(pool + (((int64_t)sb[u] * a.Hkv + h) * B + (j[u] & (B - 1))) * C + c);
       }
     }
+  };
+  entries(0);
+  load(0);
+  entries(T * U);
+  for (int base = 0; base < n; base += T * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      to[u] = to_next[u];
+      x[u] = x_next[u];
+    }
+    load(base + T * U);
+    entries(base + 2 * T * U);
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kMvUnroll; ++u)
+    for (int u = 0; u < U; ++u)
       if (to[u] >= 0) pool[to[u]] = x[u];
   }
   if (bad && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
@@ -145,7 +188,7 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
 
 template <int D>
 int launch_move(const EvictArgs &a, cudaStream_t st) {
-  constexpr int CPS = 4;
+  constexpr int CPS = PA_MV_CPS;
   evict_move_kernel<D, CPS><<<dim3(2 * (D / 8) / CPS, a.Hkv, a.S), kMvThreads, 0, st>>>(a);
   return launch_status(cudaGetLastError());
 }
@@ -193,13 +236,19 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
   a.recent = recent_tokens;
   a.num_rows = num_rows;
   a.max_tokens = (size_t)max_tokens;
-  a.smem_keys = std::min(d->max_context_len, 48 * 1024);
+  // Short rows take small CTAs, several an SM.
+  constexpr int kShort = 4096, kLong = 48 * 1024;
+  a.smem_keys = std::min(d->max_context_len, kLong);
   const size_t smem = (size_t)a.smem_keys * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(48 * 1024 * 4)) !=
-      cudaSuccess)
-    return PA_ERR_CUDA;
-  evict_select_kernel<<<dim3(a.Hkv, a.S), kEvThreads, smem, s>>>(a);
+  if (d->max_context_len <= kShort) {
+    evict_select_kernel<256><<<dim3(a.Hkv, a.S), 256, smem, s>>>(a);
+  } else {
+    if (cudaFuncSetAttribute(evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLong * 4) !=
+        cudaSuccess)
+      return PA_ERR_CUDA;
+    evict_select_kernel<1024><<<dim3(a.Hkv, a.S), 1024, smem, s>>>(a);
+  }
   const int st = launch_status(cudaGetLastError());
   if (st != PA_OK) return st;
   return d->head_dim == 128 ? launch_move<128>(a, s) : launch_move<64>(a, s);

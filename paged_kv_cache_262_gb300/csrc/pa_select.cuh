@@ -30,7 +30,7 @@ constexpr int kBins = 1 << kDigitBits;
 
 template <int NT>
 struct SelectSmem {
-  int hist[kBins];
+  int4 hist[kBins / 4];
   unsigned long long lo[NT / 32], hi[NT / 32];
   int a[NT / 32], b[NT / 32];
   int bin, above;
@@ -43,22 +43,28 @@ struct Kth {
   int above;
 };
 
+__device__ __forceinline__ int lead_zeros(uint32_t x) { return __clz((int)x); }
+__device__ __forceinline__ int lead_zeros(unsigned long long x) { return __clzll((long long)x); }
+
 // Whole CTA of NT threads; key(i) for i < n.  A digit is the kDigitBits bits
 // below those that all keys left share, so that the first one already tells
 // keys of one magnitude apart (scores of a context differ in few high bits)
 // and two passes usually end it.
 template <int NT, class T, class KeyF>
 __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int tid) {
+  constexpr int kBits = 8 * sizeof(T);
   const int lane = tid & 31, warp = tid >> 5;
-  unsigned long long lo = ~0ull, hi = 0ull;
+  int *hist = reinterpret_cast<int *>(sm.hist);
+  T lo = ~(T)0, hi = 0;
+#pragma unroll 4
   for (int i = tid; i < n; i += NT) {
-    const unsigned long long k = key(i);
+    const T k = key(i);
     lo = k < lo ? k : lo;
     hi = k > hi ? k : hi;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+    const T l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
     lo = l2 < lo ? l2 : lo;
     hi = h2 > hi ? h2 : hi;
   }
@@ -67,29 +73,29 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
     sm.lo[warp] = lo;
     sm.hi[warp] = hi;
   }
+  for (int i = tid; i < kBins / 4; i += NT) sm.hist[i] = make_int4(0, 0, 0, 0);
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    lo = sm.lo[w] < lo ? sm.lo[w] : lo;
-    hi = sm.hi[w] > hi ? sm.hi[w] : hi;
+    lo = (T)sm.lo[w] < lo ? (T)sm.lo[w] : lo;
+    hi = (T)sm.hi[w] > hi ? (T)sm.hi[w] : hi;
   }
-  int open = 64 - __clzll((long long)(lo ^ hi));  // low bits in which the keys left differ
-  unsigned long long base = open == 64 ? 0ull : (hi >> open) << open;
+  int open = kBits - (lo == hi ? kBits : lead_zeros(lo ^ hi));  // low bits in which the keys left differ
+  T base = open == kBits ? (T)0 : (hi >> open) << open;
   int left = want, above = 0;
   while (open > 0) {
     const int w = min(kDigitBits, open), sh = open - w;
-    for (int i = tid; i < kBins; i += NT) sm.hist[i] = 0;
-    __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < n; i += NT) {
-      const unsigned long long k = key(i);
-      if (open == 64 || (k ^ base) >> open == 0) atomicAdd(&sm.hist[(int)(k >> sh) & ((1 << w) - 1)], 1);
+      const T k = key(i);
+      if (open == kBits || (k ^ base) >> open == 0) atomicAdd(&hist[(int)(k >> sh) & ((1 << w) - 1)], 1);
     }
     __syncthreads();
     // bins from the highest down, kBins / NT consecutive ones a thread
     constexpr int kPer = kBins / NT;
-    int c = 0;
+    int cnt[kPer], c = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) c += sm.hist[kBins - 1 - tid * kPer - j];
+    for (int j = 0; j < kPer; ++j) c += cnt[j] = hist[kBins - 1 - tid * kPer - j];
     int incl = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -103,21 +109,21 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
     if (left > run && left <= run + c) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int b = kBins - 1 - tid * kPer - j, cb = sm.hist[b];
-        if (left > run && left <= run + cb) {
-          sm.bin = b;
+        if (left > run && left <= run + cnt[j]) {
+          sm.bin = kBins - 1 - tid * kPer - j;
           sm.above = run;
         }
-        run += cb;
+        run += cnt[j];
       }
     }
+    for (int i = tid; i < kBins / 4; i += NT) sm.hist[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    base |= (unsigned long long)sm.bin << sh;
+    base |= (T)sm.bin << sh;
     above += sm.above;
     left -= sm.above;
     open = sh;
   }
-  return Kth<T>{(T)base, above};
+  return Kth<T>{base, above};
 }
 
 // Calls emit(position, i) for every i < n with key(i) > t, and for the first

@@ -135,6 +135,8 @@ def fake(monkeypatch):
 
     monkeypatch.setattr(b, "load", lambda path=None: lib)
     monkeypatch.setattr(b, "_need", need)
+    monkeypatch.setattr(b, "_current_device", lambda: -1)  # a host tensor's get_device()
+    monkeypatch.setattr(b, "_raw_stream", lambda stream, device: 7 if stream is None else stream.cuda_stream)
     monkeypatch.setattr(b, "_ws", lambda w: None if w is None else w.data_ptr())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: S())
@@ -244,9 +246,11 @@ def test_wrappers_refuse_what_the_pointers_cannot_show(fake):
     _refused(fake, V, e, t["kp"], t["vp"][:-1], t["bt"], t["ctx"], t["keep"], t["w"], max_keep_len=8)
 
 
-def test_wrappers_refuse_host_tensors():
+def test_wrappers_refuse_host_tensors(monkeypatch):
     import torch
     t = _tensors()
+    from paged_kv_cache_262_gb300 import _binding as b
+    monkeypatch.setattr(b, "_current_device", lambda: 0)
     with pytest.raises(TypeError):
         pa.block_key_bounds(t["kp"], t["bounds"], t["bt"], t["ctx"])
     with pytest.raises(TypeError):
@@ -256,3 +260,17 @@ def test_wrappers_refuse_host_tensors():
     with pytest.raises(TypeError):
         pa.evict_tokens(t["kp"], t["vp"], t["bt"], t["ctx"], t["keep"], t["w"], max_keep_len=8)
     assert isinstance(t["q"], torch.Tensor)
+
+
+def test_wrappers_refuse_what_is_no_tensor_or_on_another_device(fake, monkeypatch):
+    from paged_kv_cache_262_gb300 import _binding as b
+    t = _tensors()
+    with pytest.raises((TypeError, AttributeError)):
+        pa.block_key_bounds(t["kp"], t["bounds"], t["bt"].tolist(), t["ctx"])
+    monkeypatch.setattr(b, "_current_device", lambda: 1)
+    for call in (lambda: pa.block_key_bounds(t["kp"], t["bounds"], t["bt"], t["ctx"]),
+                 lambda: pa.select_blocks(t["q"], t["bounds"], t["bt"], t["ctx"], 3, block_size=16),
+                 lambda: pa.paged_attention_decode_sparse(t["q"], t["kp"], t["vp"], t["bt"], t["ctx"], t["sel"]),
+                 lambda: pa.paged_attention_decode_weights(t["q"], t["kp"], t["vp"], t["bt"], t["ctx"], t["w"]),
+                 lambda: pa.evict_tokens(t["kp"], t["vp"], t["bt"], t["ctx"], t["keep"], t["w"], max_keep_len=8)):
+        _refused(fake, ValueError, call)
