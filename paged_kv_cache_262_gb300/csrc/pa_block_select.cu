@@ -192,9 +192,15 @@ __device__ void select_row(const SelectArgs &a, RowSelect &r, size_t row, int s,
   int32_t *out = a.selected + row * a.k;
   const int N = end - first, want = a.k - a.sink - a.recent;
   const bool in_smem = N <= kSelKeys;
-  if (want > 0 && in_smem) {
+  uint32_t least = ~0u, most = 0u;
+  if (want > 0) {
 #pragma unroll 8
-    for (int i = tid; i < N; i += kSelThreads) r.keys[i] = __ldcg(keys + i);
+    for (int i = tid; i < N; i += kSelThreads) {
+      const uint32_t k = __ldcg(keys + i);
+      if (in_smem) r.keys[i] = k;
+      least = min(least, k);
+      most = max(most, k);
+    }
   }
   for (int i = tid; i < a.sink; i += kSelThreads) out[i] = i;
   for (int i = tid; i < a.recent; i += kSelThreads) out[a.k - a.recent + i] = end + i;
@@ -244,7 +250,7 @@ __device__ void select_row(const SelectArgs &a, RowSelect &r, size_t row, int s,
       __syncthreads();
       t = r.thr;
     } else {
-      t = kth_largest<kSelThreads, uint32_t>(key32, N, want, r.sm, tid).key;
+      t = kth_largest<kSelThreads, uint32_t>(key32, N, want, r.sm, tid, least, most).key;
     }
     if (t != 0u) {
       const float v = key_value(t);
@@ -305,7 +311,13 @@ __device__ void select_row(const SelectArgs &a, RowSelect &r, size_t row, int s,
   __threadfence_block();
   __syncthreads();
   auto key64 = [&](int i) -> unsigned long long { return k64[i]; };
-  const Kth<unsigned long long> t = kth_largest<kSelThreads, unsigned long long>(key64, N, want, r.sm, tid);
+  unsigned long long l64 = ~0ull, m64 = 0ull;
+  for (int i = tid; i < N; i += kSelThreads) {
+    l64 = min(l64, k64[i]);
+    m64 = max(m64, k64[i]);
+  }
+  const Kth<unsigned long long> t =
+      kth_largest<kSelThreads, unsigned long long>(key64, N, want, r.sm, tid, l64, m64);
   take_above<kSelThreads, unsigned long long>(key64, N, t.key, want - t.above, want, r.sm, tid, emit);
 }
 

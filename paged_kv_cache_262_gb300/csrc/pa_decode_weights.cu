@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(128)
     decode_logits_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
+  grid_launch_dependents();
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lin = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, false, true>(&tmK, &tmV, a, lin, threadIdx.x, smem, 0);
@@ -49,21 +50,32 @@ struct WeightArgs {
 };
 
 constexpr int kWThreads = 256;
-constexpr int kWTokens = 1024;  // tokens a CTA covers
+constexpr int kWPer = 4;  // tokens of a thread
+constexpr int kWTokens = kWThreads * kWPer;
+
+template <int V>
+struct FloatVec;
+template <>
+struct FloatVec<1> { using type = float; };
+template <>
+struct FloatVec<2> { using type = float2; };
+template <>
+struct FloatVec<4> { using type = float4; };
 
 // grid (token chunk, kv head, sequence).  Sequences that name the same row
 // are summed by the first of them, in sequence order, so that a row has one
-// writer and its sums one order.
+// writer and its sums one order.  A token's G logits lie together: V of them
+// a load (V divides G), one load of each of the thread's tokens in flight.
+template <int V>
 __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) {
+  using Vec = typename FloatVec<V>::type;
   extern __shared__ uint32_t members[];  // bit s: sequence s names this CTA's row
+  __shared__ float2 sst[2][16];          // statistics of the query heads, of this sequence and the next
   const int s = blockIdx.z, h = blockIdx.y, j0 = blockIdx.x * kWTokens, tid = threadIdx.x;
   const int row = a.rows ? __ldg(a.rows + s) : s;
-  if (row < 0 || row >= a.num_rows) {
-    if (a.err && tid == 0 && h == 0 && blockIdx.x == 0) atomicOr(a.err, PA_DEVERR_ROW);
-    return;
-  }
-  if (a.rows) {
-    bool mine = true;
+  const bool in_range = row >= 0 && row < a.num_rows;
+  bool mine = in_range;
+  if (a.rows && in_range) {
     for (int base = 0; base < a.S; base += kWThreads) {
       const int t = base + tid;
       const bool same = t < a.S && __ldg(a.rows + t) == row;
@@ -71,14 +83,20 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
       const unsigned int b = __ballot_sync(0xffffffffu, same);
       if ((tid & 31) == 0) members[t >> 5] = b;
     }
-    if (!__syncthreads_and(mine)) return;
+    mine = __syncthreads_and(mine);
+  } else if (mine) {
+    mine = __ldg(a.ctx + s) > j0;
   }
+  grid_wait();  // the logits are complete
+  if (!in_range && a.err && tid == 0 && h == 0 && blockIdx.x == 0) atomicOr(a.err, PA_DEVERR_ROW);
+  if (!mine) return;
   const size_t wrow = ((size_t)row * a.Hkv + h) * a.max_tokens;
-  float acc[kWTokens / kWThreads];
-  bool any[kWTokens / kWThreads];
+  float acc[kWPer];
+  bool any[kWPer];
 #pragma unroll
-  for (int i = 0; i < kWTokens / kWThreads; ++i) acc[i] = 0.f, any[i] = false;
+  for (int i = 0; i < kWPer; ++i) acc[i] = 0.f, any[i] = false;
   const int words = a.rows ? (a.S + 31) / 32 : 1;
+  int flip = 0;
   for (int w = 0; w < words; ++w) {
     uint32_t left = a.rows ? members[w] : 1u;
     while (left) {
@@ -86,24 +104,38 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
       left &= left - 1;
       const int ctx = __ldg(a.ctx + t);
       if (ctx <= j0 || ctx > a.max_ctx || ctx > a.max_tokens_table) continue;
-      const float2 *st = a.stats + ((size_t)t * a.Hkv + h) * a.G;
-      const float *lg = a.logits + ((size_t)t * a.Hkv + h) * a.max_ctx * a.G;
+      if (tid < a.G) sst[flip][tid] = __ldcg(a.stats + ((size_t)t * a.Hkv + h) * a.G + tid);
+      __syncthreads();  // (two buffers: who is behind still reads the other)
+      const float2 *st = sst[flip];
+      flip ^= 1;
+      const Vec *lg = reinterpret_cast<const Vec *>(a.logits + ((size_t)t * a.Hkv + h) * a.max_ctx * a.G);
+      float sum[kWPer];
 #pragma unroll
-      for (int i = 0; i < kWTokens / kWThreads; ++i) {
-        const int j = j0 + i * kWThreads + tid;
-        if (j >= ctx) continue;
-        float sum = 0.f;
-        for (int g = 0; g < a.G; ++g) {
-          const float2 ml = __ldg(st + g);
-          sum += ex2_ftz(lg[(size_t)j * a.G + g] - ml.x) * ml.y;
+      for (int i = 0; i < kWPer; ++i) sum[i] = 0.f;
+#pragma unroll 2
+      for (int g = 0; g < a.G; g += V) {
+        Vec x[kWPer];
+#pragma unroll
+        for (int i = 0; i < kWPer; ++i) {
+          const int j = j0 + i * kWThreads + tid;
+          if (j < ctx) x[i] = __ldcs(lg + ((size_t)j * a.G + g) / V);
         }
-        acc[i] += sum;
-        any[i] = true;
+#pragma unroll
+        for (int i = 0; i < kWPer; ++i)
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            sum[i] += ex2_ftz(reinterpret_cast<const float *>(&x[i])[e] - st[g + e].x) * st[g + e].y;
       }
+#pragma unroll
+      for (int i = 0; i < kWPer; ++i)
+        if (j0 + i * kWThreads + tid < ctx) {
+          acc[i] += sum[i];
+          any[i] = true;
+        }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kWTokens / kWThreads; ++i) {
+  for (int i = 0; i < kWPer; ++i) {
     const int j = j0 + i * kWThreads + tid;
     if (any[i]) a.w_out[wrow + j] = a.w_in[wrow + j] + acc[i];
   }
@@ -207,6 +239,7 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   w.max_tokens = (size_t)max_tokens;
   const int chunks = (d->max_context_len + kWTokens - 1) / kWTokens;
   const size_t smem = weight_rows ? ((size_t)d->num_seqs + kWThreads - 1) / kWThreads * (kWThreads / 8) : 0;
-  weights_kernel<<<dim3(chunks, d->num_kv_heads, d->num_seqs), kWThreads, smem, s>>>(w);
-  return launch_status(cudaGetLastError());
+  const dim3 wgrid(chunks, d->num_kv_heads, d->num_seqs);
+  auto kern = a.G % 4 == 0 ? weights_kernel<4> : a.G % 2 == 0 ? weights_kernel<2> : weights_kernel<1>;
+  return launch_dependent(kern, wgrid, kWThreads, smem, s, w);
 }

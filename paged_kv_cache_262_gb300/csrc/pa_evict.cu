@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "pa_internal.h"
+#include "pa_ptx.cuh"
 #include "pa_select.cuh"
 #include "pagedattn.h"
 
@@ -49,6 +50,7 @@ template <int NT>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   extern __shared__ float sw[];
   __shared__ SelectSmem<NT> sm;
+  grid_launch_dependents();
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
   int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int ctx = __ldg(a.ctx + s), keep = __ldg(a.keep + s);
@@ -81,11 +83,18 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   }
   const int N = ctx - a.sink - a.recent, want = n - a.sink - a.recent;
   const bool in_smem = ctx <= a.smem_keys;
-  if (in_smem) {
+  uint32_t least = ~0u, most = 0u;
 #pragma unroll 8
-    for (int i = tid; i < ctx; i += NT) sw[i] = __ldcs(w + i);
-    __syncthreads();
+  for (int i = tid; i < ctx; i += NT) {
+    const float x = __ldcs(w + i);
+    if (in_smem) sw[i] = x;
+    if (i >= a.sink && i < ctx - a.recent) {
+      const uint32_t k = order_key(x);
+      least = min(least, k);
+      most = max(most, k);
+    }
   }
+  __syncthreads();
   auto put = [&](int i, int j) {  // token j is kept, as number i
     kept[i] = j;
     if (in_smem) wo[i] = sw[j];
@@ -94,7 +103,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   for (int i = tid; i < a.recent; i += NT) put(n - a.recent + i, ctx - a.recent + i);
   if (want > 0) {
     auto key = [&](int i) -> uint32_t { return order_key(in_smem ? sw[a.sink + i] : w[a.sink + i]); };
-    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key, N, want, sm, tid);
+    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key, N, want, sm, tid, least, most);
     take_above<NT, uint32_t>(key, N, t.key, want - t.above, want, sm, tid,
                              [&](int pos, int i) { put(a.sink + pos, a.sink + i); });
   }
@@ -111,86 +120,151 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   }
 }
 
-// Rows of K (even) or V (odd) of one (sequence, kv head), CPS 16-byte chunks
-// of each: grid (2 * slices, kv head, sequence).  A stretch's rows are on
-// their way while the one before is stored, and the list and table entries of
-// the one after while both are: sources lie at or behind the stretch, so
-// reading ahead of the stores changes nothing, and the barrier before the
-// stores of a stretch ends its reads.
+// Rows of K (even) or V (odd) of one (sequence, kv head), RB bytes of each:
+// grid (2 * slices, kv head, sequence).  The rows go through a ring of stages
+// in shared memory by asynchronous copies, a 16-byte piece a thread and stage;
+// a thread stores the pieces that it loaded.  A stage is stored when every
+// thread's copies of it, and of all before it, have landed; the later ones on
+// their way read at or behind their own slots, which no earlier stage writes.
 constexpr int kMvThreads = 256;
-#ifndef PA_MV_UNROLL
-#define PA_MV_UNROLL 4
+#ifndef PA_MV_STAGES
+#define PA_MV_STAGES 3
 #endif
-#ifndef PA_MV_CPS
-#define PA_MV_CPS 4
+#ifndef PA_MV_U
+#define PA_MV_U 4
 #endif
-constexpr int kMvUnroll = PA_MV_UNROLL;
+#ifndef PA_MV_WAVE
+#define PA_MV_WAVE 6
+#endif
+constexpr int kMvStages = PA_MV_STAGES;
+constexpr int kMvPieces = PA_MV_U;  // pieces of a thread in a stage
+constexpr int kMvIndex = 2048;  // rows of list and table entries ahead and behind, in shared memory
 
-template <int D, int CPS>
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+struct MoveSmem {
+  uint4 ring[kMvStages][kMvPieces][kMvThreads];
+  int32_t src[kMvIndex], dst[kMvIndex];  // pool rows; dst -1: the row stays where it is
+};
+
+template <int D, int RB>
 __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs a) {
-  constexpr int C = D / 8;
-  constexpr int T = kMvThreads / CPS;  // tokens an access of the CTA covers
-  constexpr int U = kMvUnroll;
+  constexpr int C = D / 8;              // 16-byte pieces of a row
+  constexpr int P = RB / 16;            // of which a CTA moves
+  constexpr int A = kMvThreads / P;     // rows of one piece a thread
+  constexpr int T = A * kMvPieces;      // rows of a stage
+  constexpr int GS = kMvThreads / T;    // stages an index group (a row a thread) covers
+  static_assert(T <= kMvThreads && kMvThreads % T == 0, "whole stages to an index group");
+  static_assert(kMvStages * T + 3 * kMvThreads <= kMvIndex, "the index ring holds what is in flight");
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  MoveSmem &sm = *reinterpret_cast<MoveSmem *>(smem_raw);
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-  const int c = (blockIdx.x >> 1) * CPS + tid % CPS, t0 = tid / CPS;
-  const int n = min(__ldg(a.new_lens + s), a.max_keep);
+  grid_wait();
+  const int n = min(__ldcg(a.new_lens + s), a.max_keep);
   const int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
-  if (n <= 0 || __ldg(kept) < 0) return;
-  uint4 *pool = (blockIdx.x & 1) ? a.vp : a.kp;
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks, *dt = a.dst + (size_t)s * a.max_blocks;
   const int B = a.B, lb = B == 16 ? 4 : 5;
+  uint4 *pool = ((blockIdx.x & 1) ? a.vp : a.kp) + (blockIdx.x >> 1) * P + tid % P;
   int bad = 0;
-  int j[U], sb[U], db[U];       // list and table entries of the stretch to load
-  int64_t to[U], to_next[U];
-  uint4 x[U], x_next[U];
-  auto entries = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = base + u * T + t0;
-      j[u] = i < n ? __ldg(kept + i) : -1;
-      db[u] = i < n ? __ldg(dt + (i >> lb)) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) sb[u] = j[u] >= 0 && (j[u] >> lb) < a.max_blocks ? __ldg(bt + (j[u] >> lb)) : -1;
+
+  // index groups: list entry, then the source block's table entry, then the
+  // rows into shared memory, each a group ahead of the next
+  int j1 = -1, i1 = 0, s1 = -1, d1 = -1, j2 = -1, i2 = 0, d2 = -1;
+  auto step_list = [&](int g) {
+    i2 = g * kMvThreads + tid;
+    j2 = i2 < n ? __ldcg(kept + i2) : -1;
+    d2 = i2 < n ? __ldg(dt + (i2 >> lb)) : -1;
   };
-  auto load = [&](int base) {  // of the entries at hand
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = base + u * T + t0;
-      to_next[u] = -1;
-      if (i >= n) continue;
-      if (sb[u] < 0 || sb[u] >= a.num_blocks || db[u] < 0 || db[u] >= a.num_blocks) {
+  auto step_table = [&]() {
+    i1 = i2, j1 = j2, d1 = d2;
+    s1 = j1 >= 0 && (j1 >> lb) < a.max_blocks ? __ldg(bt + (j1 >> lb)) : -1;
+  };
+  auto step_rows = [&]() {
+    int32_t from = 0, to = -1;
+    if (j1 >= 0) {
+      if (s1 < 0 || s1 >= a.num_blocks || d1 < 0 || d1 >= a.num_blocks) {
         bad = 1;
-      } else if (sb[u] != db[u] || ((i ^ j[u]) & (B - 1))) {
-        to_next[u] = (((int64_t)db[u] * a.Hkv + h) * B + (i & (B - 1))) * C + c;
-        x_next[u] = __ldcg(pool + (((int64_t)sb[u] * a.Hkv + h) * B + (j[u] & (B - 1))) * C + c);
+      } else {
+        from = (s1 * a.Hkv + h) * B + (j1 & (B - 1));
+        const int32_t at = (d1 * a.Hkv + h) * B + (i1 & (B - 1));
+        to = at == from ? -1 : at;
       }
     }
+    sm.src[i1 % kMvIndex] = from;
+    sm.dst[i1 % kMvIndex] = to;
   };
-  entries(0);
-  load(0);
-  entries(T * U);
-  for (int base = 0; base < n; base += T * U) {
+  const uint32_t ring = smem_u32(&sm.ring[0][0][tid]);
+  const int t0 = tid / P;
+  auto load = [&](int st) {  // one group of copies, empty past the end
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      to[u] = to_next[u];
-      x[u] = x_next[u];
+    for (int u = 0; u < kMvPieces; ++u) {
+      const int i = st * T + u * A + t0;
+      if (i < n && sm.dst[i % kMvIndex] >= 0)
+        copy16_async(ring + ((st % kMvStages) * kMvPieces + u) * (kMvThreads * 16),
+                     pool + (int64_t)sm.src[i % kMvIndex] * C);
     }
-    load(base + T * U);
-    entries(base + 2 * T * U);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  step_list(0);
+  if (n <= 0 || __ldcg(kept) < 0) return;  // a refused sequence (the same for the whole CTA)
+  step_table();
+  step_list(1);
+  step_rows();
+  step_table();
+  step_list(2);
+  __syncthreads();
+  const int nst = (n + T - 1) / T;
+  int made = 1;  // index groups in shared memory
+#pragma unroll 1
+  for (int st = 0; st < kMvStages - 1; ++st) {
+    if (st == made * GS) {
+      step_rows();
+      step_table();
+      step_list(++made + 1);
+      __syncthreads();
+    }
+    load(st);
+  }
+#pragma unroll 1
+  for (int st = 0; st < nst; ++st) {
+    const int ahead = st + kMvStages - 1;
+    if (ahead >= made * GS - 1) {  // read behind the barrier
+      step_rows();
+      step_table();
+      step_list(++made + 1);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kMvStages - 2) : "memory");
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (to[u] >= 0) pool[to[u]] = x[u];
+    for (int u = 0; u < kMvPieces; ++u) {
+      const int i = st * T + u * A + t0;
+      const int32_t to = i < n ? sm.dst[i % kMvIndex] : -1;
+      if (to >= 0) pool[(int64_t)to * C] = sm.ring[st % kMvStages][u][tid];
+    }
+    load(ahead);
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (bad && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
 }
 
+template <int D, int RB>
+int launch_move_rows(const EvictArgs &a, cudaStream_t st) {
+  auto kern = evict_move_kernel<D, RB>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(MoveSmem)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return launch_dependent(kern, dim3(2 * (D * 2 / RB), a.Hkv, a.S), kMvThreads, sizeof(MoveSmem), st, a);
+}
+
+// Whole rows where that gives about a CTA an SM, else parts of 128 or 64 bytes.
 template <int D>
-int launch_move(const EvictArgs &a, cudaStream_t st) {
-  constexpr int CPS = PA_MV_CPS;
-  evict_move_kernel<D, CPS><<<dim3(2 * (D / 8) / CPS, a.Hkv, a.S), kMvThreads, 0, st>>>(a);
-  return launch_status(cudaGetLastError());
+int launch_move(const EvictArgs &a, int sms, cudaStream_t st) {
+  const int64_t units = 2ll * a.Hkv * a.S;
+  if constexpr (D == 128)
+    if (4 * units >= (long long)PA_MV_WAVE * sms) return launch_move_rows<D, 256>(a, st);
+  if (units * (D / 64) * 4 >= (long long)PA_MV_WAVE * sms) return launch_move_rows<D, 128>(a, st);
+  return launch_move_rows<D, 64>(a, st);
 }
 
 }  // namespace
@@ -212,6 +286,8 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
       !new_lens || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(weights) || !aligned16(weights_out))
     return PA_ERR_INVALID;
   if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
   EvictArgs a{};
   a.kp = static_cast<uint4 *>(k_pool);
   a.vp = static_cast<uint4 *>(v_pool);
@@ -251,5 +327,5 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
   }
   const int st = launch_status(cudaGetLastError());
   if (st != PA_OK) return st;
-  return d->head_dim == 128 ? launch_move<128>(a, s) : launch_move<64>(a, s);
+  return d->head_dim == 128 ? launch_move<128>(a, sms, s) : launch_move<64>(a, sms, s);
 }

@@ -46,6 +46,26 @@ struct DecodePlan {
   size_t total() const { return ws_o_bytes + ws_ml_bytes + ws_cnt_bytes; }
 };
 
+// Launches `kern` as a programmatic dependent of the kernel before it on the
+// stream: its CTAs may start once that one's have all executed
+// griddepcontrol.launch_dependents, and every one of them executes
+// griddepcontrol.wait before it reads what that kernel writes or writes
+// anything.
+template <class... P, class... A>
+int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+
 // Validates `d` for the decode kernel; PA_OK or an error status.
 int validate_decode_desc(const pa_decode_desc *d);
 

@@ -85,6 +85,12 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   return p;
 }
 
+// --------------------------------------------------- programmatic dependents
+// Lets the next kernel's CTAs start (see launch_dependent).
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+// Waits for the kernel before this one, and for its writes.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------ warp MMA (m16n8k16)
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"

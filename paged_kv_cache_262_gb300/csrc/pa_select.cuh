@@ -25,15 +25,18 @@ __device__ __forceinline__ unsigned long long order_key64(double x) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-constexpr int kDigitBits = 11;
-constexpr int kBins = 1 << kDigitBits;
+// Counting bins of a CTA of NT threads: eight a thread.
+template <int NT>
+constexpr int kDigitBits = NT >= 1024 ? 13 : NT >= 512 ? 12 : 11;
+constexpr int kNearKeys = 256;  // keys of one bin that are ranked by comparing all of them
 
 template <int NT>
 struct SelectSmem {
-  int4 hist[kBins / 4];
+  int4 hist[2 * NT];
   unsigned long long lo[NT / 32], hi[NT / 32];
+  unsigned long long near_[kNearKeys], kth;
   int a[NT / 32], b[NT / 32];
-  int bin, above;
+  int bin, above, count, filled, kth_above;
 };
 
 // The want-th largest key (1 <= want <= n) and how many keys are above it.
@@ -46,22 +49,17 @@ struct Kth {
 __device__ __forceinline__ int lead_zeros(uint32_t x) { return __clz((int)x); }
 __device__ __forceinline__ int lead_zeros(unsigned long long x) { return __clzll((long long)x); }
 
-// Whole CTA of NT threads; key(i) for i < n.  A digit is the kDigitBits bits
-// below those that all keys left share, so that the first one already tells
-// keys of one magnitude apart (scores of a context differ in few high bits)
-// and two passes usually end it.
+// Whole CTA of NT threads; key(i) for i < n; lo and hi: the least and largest
+// key of those that this thread looked at, all of them among the threads.  A
+// digit is the bits below those that all keys left share, so that the first
+// one already tells keys of one magnitude apart (scores of a context differ in
+// few high bits); once a bin's keys are few they are ranked by comparison.
 template <int NT, class T, class KeyF>
-__device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int tid) {
-  constexpr int kBits = 8 * sizeof(T);
+__device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int tid, T lo, T hi) {
+  constexpr int kBits = 8 * sizeof(T), kDigit = kDigitBits<NT>, kBins = 1 << kDigit, kPer = kBins / NT;
+  static_assert(kBins * (int)sizeof(int) == (int)sizeof(sm.hist), "eight bins a thread");
   const int lane = tid & 31, warp = tid >> 5;
   int *hist = reinterpret_cast<int *>(sm.hist);
-  T lo = ~(T)0, hi = 0;
-#pragma unroll 4
-  for (int i = tid; i < n; i += NT) {
-    const T k = key(i);
-    lo = k < lo ? k : lo;
-    hi = k > hi ? k : hi;
-  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const T l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
@@ -74,6 +72,7 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
     sm.hi[warp] = hi;
   }
   for (int i = tid; i < kBins / 4; i += NT) sm.hist[i] = make_int4(0, 0, 0, 0);
+  if (tid == 0) sm.filled = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
@@ -84,15 +83,14 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
   T base = open == kBits ? (T)0 : (hi >> open) << open;
   int left = want, above = 0;
   while (open > 0) {
-    const int w = min(kDigitBits, open), sh = open - w;
+    const int w = min(kDigit, open), sh = open - w;
 #pragma unroll 4
     for (int i = tid; i < n; i += NT) {
       const T k = key(i);
       if (open == kBits || (k ^ base) >> open == 0) atomicAdd(&hist[(int)(k >> sh) & ((1 << w) - 1)], 1);
     }
     __syncthreads();
-    // bins from the highest down, kBins / NT consecutive ones a thread
-    constexpr int kPer = kBins / NT;
+    // bins from the highest down, kPer consecutive ones a thread
     int cnt[kPer], c = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) c += cnt[j] = hist[kBins - 1 - tid * kPer - j];
@@ -112,6 +110,7 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
         if (left > run && left <= run + cnt[j]) {
           sm.bin = kBins - 1 - tid * kPer - j;
           sm.above = run;
+          sm.count = cnt[j];
         }
         run += cnt[j];
       }
@@ -122,6 +121,33 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
     above += sm.above;
     left -= sm.above;
     open = sh;
+    const int count = sm.count;
+    if (open > 0 && count <= kNearKeys) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += NT) {
+        const T k = key(i);
+        if ((k ^ base) >> open == 0) {
+          const int at = atomicAdd(&sm.filled, 1);
+          if (at < kNearKeys) sm.near_[at] = k;
+        }
+      }
+      __syncthreads();
+      if (tid < count) {
+        const T mine = (T)sm.near_[tid];
+        int gt = 0, ge = 0;
+        for (int j = 0; j < count; ++j) {
+          const T o = (T)sm.near_[j];
+          gt += o > mine;
+          ge += o >= mine;
+        }
+        if (gt < left && left <= ge) {  // (equal keys write the same)
+          sm.kth = mine;
+          sm.kth_above = gt;
+        }
+      }
+      __syncthreads();
+      return Kth<T>{(T)sm.kth, above + sm.kth_above};
+    }
   }
   return Kth<T>{base, above};
 }
