@@ -91,34 +91,44 @@ __global__ void __launch_bounds__(256) key_bounds_kernel(const BoundsArgs a) {
 }
 
 // -------------------------------------------------------------- selection
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelKeys = 8192;     // keys held in shared memory; more are re-read from the workspace
-constexpr int kSelRefine = 256;    // blocks near the threshold that are ranked in shared memory
+constexpr int kSelKeys = 8192;   // keys held in shared memory; more are re-read from the workspace
+constexpr int kSelRefine = 128;  // blocks near the threshold that are ranked in shared memory
 
 struct SelectArgs {
   const __nv_bfloat16 *q;
   const uint4 *bounds;
   const int32_t *bt, *ctx;
   int32_t *selected;           // [S][Hkv][k]
-  uint32_t *keys;              // [S][Hkv][stride]: scores as ordered keys
-  unsigned long long *keys64;  // [S][Hkv][stride]
-  float *maxabs;               // [S][Hkv][max_chunks]: largest |bound| of a chunk
-  unsigned long long *cnt;     // [S][Hkv] arrivals
+  unsigned long long *keys64;  // [S][Hkv][stride]: exact scores (many ties only)
+  uint32_t *keys;              // [S][Hkv][stride]: scores as ordered keys (LONG launches only)
+  float *span;                 // [S][Hkv][max_chunks]: largest absolute sum of a chunk (LONG launches only)
+  unsigned long long *cnt;     // [S][Hkv] arrivals (LONG launches only)
   int32_t *err;
   int Hq, Hkv, G, num_blocks, max_blocks, max_ctx, k, sink, recent, B, max_chunks;
-  int chunk;                   // blocks a CTA scores, a multiple of 16 kSelWarps
+  int chunk;                   // blocks a CTA scores, a multiple of 16 blocks a warp
   size_t stride;
   unsigned int epoch;
 };
 
-// A block's score in 64 bits, by one warp: every product of two bf16 values
-// is exact, and blocks of equal bounds get equal sums.  The heads whose fp32
-// sum is more than `slack` below the largest cannot be the maximum (slack
-// covers twice the error of a plain fp32 sum; infinite: every head is summed
-// in 64 bits).
+template <int SW>
+struct RowSelect {
+  SelectSmem<SW * 32> sm;
+  uint4 keys[kSelKeys / 4];
+  unsigned long long ex[kSelRefine];
+  int exi[kSelRefine];
+  float span[8];  // a CTA of the cluster each
+  float mx[SW];
+  int nex, ngt, last;
+};
+
+// A block's score in 64 bits as an ordered key, by one warp: every product of
+// two bf16 values is exact, and blocks of equal bounds get equal sums.  The
+// heads whose fp32 sum is more than `slack` below the largest cannot be the
+// maximum (slack covers twice the error of a plain fp32 sum; infinite: every
+// head is summed in 64 bits).
 template <int D, int H>  // H: heads, at least G
-__device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int pg, int h, float slack, int lane) {
+__device__ unsigned long long exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int pg, int h, float slack,
+                                          int lane) {
   constexpr int P = D / 32;  // elements of a lane, a multiple of two
   const __nv_bfloat16 *lo = reinterpret_cast<const __nv_bfloat16 *>(a.bounds) + ((size_t)pg * a.Hkv + h) * 2 * D;
   float bl[P], bh[P];
@@ -152,7 +162,7 @@ __device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int p
 #pragma unroll
   for (int g = 0; g < H; ++g)
     if (g < a.G) top = fmaxf(top, fs[g]);
-  double best = -INFINITY;
+  unsigned long long best = 0ull;
 #pragma unroll
   for (int g = 0; g < H; ++g) {
     if (g >= a.G || fs[g] < top - slack) continue;  // (the same for every lane)
@@ -164,94 +174,46 @@ __device__ double exact_score(const SelectArgs &a, const __nv_bfloat16 *q, int p
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (sum != sum) sum = INFINITY;
-    best = sum > best ? sum : best;
+    const unsigned long long k = order_key64(sum);
+    best = k > best ? k : best;
   }
   return best;
 }
 
-// The last CTA of a row: its candidates' keys are in the workspace.
-struct RowSelect {
-  SelectSmem<kSelThreads> sm;
-  uint32_t keys[kSelKeys];
-  double ex[kSelRefine];
-  int exi[kSelRefine];
-  float mx[kSelWarps];
-  int nex, ngt, last;
-  uint32_t thr;
-};
+// How far an fp32 score may be from the exact one, as a part of the largest
+// absolute sum A = sum_d |q_gd b_d| of the row: each of the 2 D / 16 MMAs adds
+// 17 terms no larger than A, each, and the sum, cut at 2^-23 of the largest of
+// them or better (and A itself, of the same MMAs, may be short by as much of itself).
+template <int D>
+constexpr float kScoreError = 18.f * (2 * D / 16) * 1.1920929e-07f * 1.001f;
 
-template <int D, int NT>
-__device__ void select_row(const SelectArgs &a, RowSelect &r, size_t row, int s, int h, int n, int nchunks,
-                           int tid) {
+// One CTA selects a row's blocks from its keys (in r.keys, or past kSelKeys of
+// them in the workspace), A the row's largest absolute sum.
+template <int D, int NT, int SW>
+__device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, int s, int h, int n, float A, int tid) {
+  constexpr int kThreads = SW * 32;
   const int lane = tid & 31, warp = tid >> 5;
   const int first = a.sink, end = n - a.recent;
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
   const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
-  uint32_t *keys = a.keys + row * a.stride;
   int32_t *out = a.selected + row * a.k;
   const int N = end - first, want = a.k - a.sink - a.recent;
+  for (int i = tid; i < a.sink; i += kThreads) out[i] = i;
+  for (int i = tid; i < a.recent; i += kThreads) out[a.k - a.recent + i] = end + i;
+  if (want == 0) return;
   const bool in_smem = N <= kSelKeys;
-  uint32_t least = ~0u, most = 0u;
-  if (want > 0) {
-#pragma unroll 8
-    for (int i = tid; i < N; i += kSelThreads) {
-      const uint32_t k = __ldcg(keys + i);
-      if (in_smem) r.keys[i] = k;
+  uint32_t *keys = in_smem ? reinterpret_cast<uint32_t *>(r.keys) : a.keys + row * a.stride;
+  auto key4 = [&](int i) { return keys4(in_smem ? r.keys[i / 4] : __ldcg(reinterpret_cast<const uint4 *>(keys + i))); };
+  const float slack = 2.f * kScoreError<D> * A;
+  const bool finite = slack < INFINITY;  // false for NaN too: then no fp32 score is trusted
+  uint32_t lo = 0u, hi = 0xfffffffeu;    // (no score's key is above it)
+  if (finite) {
+    uint32_t least = ~0u, most = 0u;
+    for_keys<kThreads, uint32_t>(key4, N, tid, [&](int, uint32_t k) {
       least = min(least, k);
       most = max(most, k);
-    }
-  }
-  for (int i = tid; i < a.sink; i += kSelThreads) out[i] = i;
-  for (int i = tid; i < a.recent; i += kSelThreads) out[a.k - a.recent + i] = end + i;
-  if (want == 0) return;
-  // How far an fp32 score may be from the exact one: every one of the 2 D / 16
-  // MMAs adds 17 terms no larger than Q M, Q = max_g sum_d |q_gd|, M = max
-  // |bound|, each cut at 2^-23 or better of the largest: less than 2^-14 Q M
-  // in all.
-  float x = 0.f, M = 0.f;
-  for (int g = warp; g < a.G; g += kSelWarps) {
-    float y = 0.f;
-#pragma unroll
-    for (int d = 2 * lane; d < D; d += 64) {
-      const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(q + g * D + d));
-      y += fabsf(bf16_lo(v)) + fabsf(bf16_hi(v));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    x = y >= x ? y : y == y ? x : INFINITY;
-  }
-  for (int c = lane; c < nchunks; c += 32) M = fmaxf(M, __ldcg(a.maxabs + row * a.max_chunks + c));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  __syncthreads();
-  if (lane == 0) r.mx[warp] = x;
-  if (tid == 0) r.nex = r.ngt = 0;
-  __syncthreads();
-  float Q = 0.f;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) Q = fmaxf(Q, r.mx[w]);
-  const bool finite = Q * M < INFINITY;  // false for NaN too: then no fp32 score is trusted
-  const float slack = finite ? 2.f * 6.103515625e-05f * (Q * M) : INFINITY;
-
-  auto key32 = [&](int i) -> uint32_t { return in_smem ? r.keys[i] : __ldcg(keys + i); };
-  uint32_t lo = 0u, hi = 0xfffffffeu;  // (no score's key is above it)
-  if (finite) {
-    uint32_t t;
-    if (N <= kSelThreads) {  // few: every key's rank by counting
-      const uint32_t mine = tid < N ? r.keys[tid] : 0u;
-      int gt = 0, ge = 0;
-      for (int j = 0; j < N; ++j) {
-        const uint32_t o = r.keys[j];
-        gt += o > mine;
-        ge += o >= mine;
-      }
-      if (tid < N && gt < want && want <= ge) r.thr = mine;  // (equal keys write the same)
-      __syncthreads();
-      t = r.thr;
-    } else {
-      t = kth_largest<kSelThreads, uint32_t>(key32, N, want, r.sm, tid, least, most).key;
-    }
+    });
+    const uint32_t t = kth_largest<kThreads, uint32_t>(key4, N, want, r.sm, tid, least, most).key;
     if (t != 0u) {
       const float v = key_value(t);
       lo = order_key(__fsub_rd(v, slack));
@@ -262,71 +224,80 @@ __device__ void select_row(const SelectArgs &a, RowSelect &r, size_t row, int s,
   }
   // blocks above hi are chosen whatever their rounding, those below lo are not
   int mine = 0;
-  for (int i = tid; i < N; i += kSelThreads) {
-    const uint32_t k = key32(i);
+  for_keys<kThreads, uint32_t>(key4, N, tid, [&](int i, uint32_t k) {
     mine += k > hi;
     if (k >= lo && k <= hi) {
       const int at = atomicAdd(&r.nex, 1);
       if (at < kSelRefine) r.exi[at] = i;
     }
-  }
+  });
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0 && mine) atomicAdd(&r.ngt, mine);
   __syncthreads();
   const int near_ = r.nex, need = want - r.ngt;
-  auto emit = [&](int pos, int i) { out[a.sink + pos] = first + i; };
+  auto emit = [&](int pos, int i, uint32_t) { out[a.sink + pos] = first + i; };
   if (near_ == need || hi == 0u) {  // (of blocks outside the pool, the first)
-    take_above<kSelThreads, uint32_t>(key32, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, r.sm, tid, emit);
+    take_above<kThreads, uint32_t>(key4, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, r.sm, tid, emit);
     return;
   }
   if (near_ <= kSelRefine) {  // few: their exact scores, ranked by counting
-    for (int c = warp; c < near_; c += kSelWarps) {
+    for (int c = warp; c < near_; c += SW) {
       const int pg = __ldg(bt + first + r.exi[c]);
-      const double e = pg >= 0 && pg < a.num_blocks ? exact_score<D, 8 * NT>(a, q, pg, h, slack, lane) : -INFINITY;
-      if (lane == 0) r.ex[c] = e;
+      const bool ok = pg >= 0 && pg < a.num_blocks;
+      const unsigned long long x = ok ? exact_score<D, 8 * NT>(a, q, pg, h, slack, lane) : 0ull;
+      if (lane == 0) r.ex[c] = x;
     }
     __syncthreads();
-    for (int c = tid; c < near_; c += kSelThreads) {
+    for (int c = tid; c < near_; c += kThreads) {
       int rank = 0;
       for (int o = 0; o < near_; ++o) rank += r.ex[o] > r.ex[c] || (r.ex[o] == r.ex[c] && r.exi[o] < r.exi[c]);
-      (in_smem ? r.keys : keys)[r.exi[c]] = rank < need ? 0xffffffffu : 0u;
+      keys[r.exi[c]] = rank < need ? 0xffffffffu : 0u;
     }
     __syncthreads();
-    take_above<kSelThreads, uint32_t>(key32, N, hi, 0, want, r.sm, tid, emit);
+    take_above<kThreads, uint32_t>(key4, N, hi, 0, want, r.sm, tid, emit);
     return;
   }
   // many (scores that tie in numbers, infinite bounds): 64-bit keys for all of
   // them in the workspace
   unsigned long long *k64 = a.keys64 + row * a.stride;
-  for (int i = warp; i < N; i += kSelWarps) {
-    const uint32_t k = key32(i);
-    unsigned long long e = k > hi ? ~0ull : 0ull;
+  for (int i = warp; i < N; i += SW) {
+    const uint32_t k = key4(i & ~3).v[i & 3];
+    unsigned long long x = k > hi ? ~0ull : 0ull;
     if (k >= lo && k <= hi) {
       const int pg = __ldg(bt + first + i);
       const bool ok = pg >= 0 && pg < a.num_blocks;
-      e = ok ? order_key64(exact_score<D, 8 * NT>(a, q, pg, h, slack, lane)) : 1ull;
+      x = ok ? exact_score<D, 8 * NT>(a, q, pg, h, slack, lane) : 1ull;
     }
-    if (lane == 0) k64[i] = e;
+    if (lane == 0) k64[i] = x;
   }
   __threadfence_block();
   __syncthreads();
-  auto key64 = [&](int i) -> unsigned long long { return k64[i]; };
+  auto key64 = [&](int i) {
+    Keys4<unsigned long long> k;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k.v[e] = i + e < N ? k64[i + e] : 0ull;
+    return k;
+  };
   unsigned long long l64 = ~0ull, m64 = 0ull;
-  for (int i = tid; i < N; i += kSelThreads) {
-    l64 = min(l64, k64[i]);
-    m64 = max(m64, k64[i]);
-  }
-  const Kth<unsigned long long> t =
-      kth_largest<kSelThreads, unsigned long long>(key64, N, want, r.sm, tid, l64, m64);
-  take_above<kSelThreads, unsigned long long>(key64, N, t.key, want - t.above, want, r.sm, tid, emit);
+  for_keys<kThreads, unsigned long long>(key64, N, tid, [&](int, unsigned long long k) {
+    l64 = min(l64, k);
+    m64 = max(m64, k);
+  });
+  const Kth<unsigned long long> t = kth_largest<kThreads, unsigned long long>(key64, N, want, r.sm, tid, l64, m64);
+  take_above<kThreads, unsigned long long>(key64, N, t.key, want - t.above, want, r.sm, tid,
+                                           [&](int pos, int i, unsigned long long) { out[a.sink + pos] = first + i; });
 }
 
-// grid (chunk, kv head, sequence).  Every CTA scores its chunk of a row; the
-// last of a row to finish selects from all of its scores.
-template <int D, int NT>
-__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs a) {
+// grid (chunk, kv head, sequence).  Every CTA scores its chunk of a row.  The
+// chunks of a row are a cluster: the scores go straight into the shared memory
+// of its first CTA, which selects (through the workspace and an arrival
+// counter, the last CTA to arrive, this took 4.6 us longer).  LONG: rows of
+// more blocks than that holds, by way of the workspace.
+template <int D, int NT, int SW, bool LONG>
+__global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectArgs a) {
   constexpr int CH = 2 * D / 32;  // 32-element steps over a block's bounds (lo, then hi)
-  __shared__ RowSelect r;
+  constexpr int kThreads = SW * 32;
+  __shared__ RowSelect<SW> r;
   const int chunk = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.B;
@@ -334,20 +305,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
   const int ctx = __ldg(a.ctx + s);
   const bool bad = ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx;
   const int n = bad ? 0 : (ctx + B - 1) / B;
-  if (n <= a.k) {  // every block, or none
+  if (n <= a.k) {  // every block, or none (the same for the whole cluster)
     if (chunk == 0) {
       int32_t *out = a.selected + row * a.k;
-      for (int i = tid; i < a.k; i += kSelThreads) out[i] = i < n ? i : -1;
+      for (int i = tid; i < a.k; i += kThreads) out[i] = i < n ? i : -1;
       if (bad && h == 0 && tid == 0 && a.err) atomicOr(a.err, PA_DEVERR_CTX);
     }
     return;
   }
   const int nchunks = (n + a.chunk - 1) / a.chunk;
-  if (chunk >= nchunks) return;
+  const bool clustered = !LONG && gridDim.x > 1;
+  if (LONG && chunk >= nchunks) return;
+  // the first CTA's shared memory must be there before another writes to it
+  if (clustered) cluster_arrive();
   const int first = a.sink, end = n - a.recent;  // the blocks that compete
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
   const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
-  uint32_t *keys = a.keys + row * a.stride;
   const int i_end = min(end, (chunk + 1) * a.chunk);
 
   // lane l's block of a tile: row l / 4 and that + 8; -2: not competing
@@ -357,7 +330,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
 
   // ---- scores of this CTA's blocks: S[block][head] = [lo hi] . [q- q+], the
   // contraction in whatever order of d suits the loads (lane t of a quad takes
-  // the 16-byte chunks t, t + 4, ...), the same for both operands.
+  // the 16-byte chunks t, t + 4, ...), the same for both operands; and the
+  // same of the absolute values, by which the score's error is bounded.
   uint32_t qf[NT][CH / 2][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -372,8 +346,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
       qf[nt][c][3] = v.w;
     }
   }
-  uint32_t big = 0u;  // packed running max of |bound|
-  for (; i0 < i_end; i0 += 16 * kSelWarps) {
+  if (tid == 0) r.nex = r.ngt = 0;
+  if (clustered) cluster_wait();
+  uint32_t *keys = LONG ? a.keys + row * a.stride : reinterpret_cast<uint32_t *>(r.keys);
+  const uint32_t keys0 = clustered ? cluster_addr(smem_u32(r.keys), 0) : smem_u32(r.keys);
+  float span = 0.f;
+  for (; i0 < i_end; i0 += 16 * SW) {
     uint4 x[2][CH];
     bool have[2];
 #pragma unroll
@@ -384,18 +362,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
 #pragma unroll
       for (int c = 0; c < CH; ++c) x[e][c] = have[e] ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
     }
-    const int next = i0 + 16 * kSelWarps + (lane >> 2);
+    const int next = i0 + 16 * SW + (lane >> 2);
     pg[0] = page(next);
     pg[1] = page(next + 8);
-    float acc[NT][4];
+    float acc[NT][4], abs_[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) {
+      acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+      abs_[nt][0] = abs_[nt][1] = abs_[nt][2] = abs_[nt][3] = 0.f;
+    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const uint4 u = x[0][c], v = x[1][c];
-      big = max2(big, max2(max2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), max2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-      big = max2(big, max2(max2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), max2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
       const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+      uint32_t p0[4], p1[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p0[e] = a0[e] & 0x7fff7fffu, p1[e] = a1[e] & 0x7fff7fffu;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         uint32_t b[4];
@@ -404,6 +386,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
           b[e] = c < CH / 2 ? min2(qf[nt][c % (CH / 2)][e], 0u) : max2(qf[nt][c % (CH / 2)][e], 0u);
         mma_16816(acc[nt], a0, b[0], b[1]);
         mma_16816(acc[nt], a1, b[2], b[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] &= 0x7fff7fffu;
+        mma_16816(abs_[nt], p0, b[0], b[1]);
+        mma_16816(abs_[nt], p1, b[2], b[3]);
       }
     }
 #pragma unroll
@@ -414,63 +400,130 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectArgs
         const int g = nt * 8 + 2 * (lane & 3);
         if (g < a.G) best = fmaxf(best, acc[nt][2 * e]);
         if (g + 1 < a.G) best = fmaxf(best, acc[nt][2 * e + 1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // (heads past G: 0)
+          const float y = abs_[nt][2 * e + k];
+          span = y <= 3.4028235e38f ? fmaxf(span, y) : INFINITY;
+        }
       }
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
       const int i = i0 + (lane >> 2) + 8 * e;
-      if ((lane & 3) == 0 && i >= first && i < i_end) keys[i - first] = have[e] ? order_key(best) : 0u;
+      if ((lane & 3) == 0 && i >= first && i < i_end) {
+        const uint32_t k = have[e] ? order_key(best) : 0u;
+        if (LONG)
+          keys[i - first] = k;
+        else if (clustered)
+          cluster_store(keys0 + 4 * (i - first), k);
+        else
+          keys[i - first] = k;
+      }
     }
   }
-  float m = fmaxf(bf16_lo(big), bf16_hi(big));
-  if (bf16_lo(big) != bf16_lo(big) || bf16_hi(big) != bf16_hi(big)) m = INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) r.mx[warp] = m;
-  __threadfence();
+  for (int o = 16; o > 0; o >>= 1) span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
+  if (lane == 0) r.mx[warp] = span;
+  if (LONG) __threadfence();
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < SW; ++w) span = fmaxf(span, r.mx[w]);
+  if (!LONG) {
+    if (clustered) {
+      if (tid == 0) cluster_store(cluster_addr(smem_u32(&r.span[chunk]), 0), __float_as_uint(span));
+      cluster_arrive();
+      if (chunk != 0) return;
+      cluster_wait();
+      for (int c = 0; c < (int)gridDim.x; ++c) span = fmaxf(span, r.span[c]);
+    }
+    select_row<D, NT, SW>(a, r, row, s, h, n, span, tid);
+    return;
+  }
   if (tid == 0) {
-#pragma unroll
-    for (int w = 1; w < kSelWarps; ++w) m = fmaxf(m, r.mx[w]);
-    a.maxabs[row * a.max_chunks + chunk] = m;
-    if (nchunks > 1) {
-      __threadfence();
-      r.last = arrive_count(a.cnt + row, a.epoch) == (unsigned int)nchunks;
-    }
+    a.span[row * a.max_chunks + chunk] = span;
+    __threadfence();
+    r.last = arrive_count(a.cnt + row, a.epoch) == (unsigned int)nchunks;
   }
   __syncthreads();
-  if (nchunks > 1) {
-    if (!r.last) return;
-    __threadfence();
-    if (tid == 0) a.cnt[row] = 0ull;
+  if (!r.last) return;
+  __threadfence();
+  if (tid == 0) a.cnt[row] = 0ull;
+  const int N = end - first;
+  if (N <= kSelKeys) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.keys + row * a.stride);
+    for (int i = tid; i < (N + 3) / 4; i += kThreads) r.keys[i] = __ldcg(src + i);
   }
-  select_row<D, NT>(a, r, row, s, h, n, nchunks, tid);
+  for (int c = lane; c < nchunks; c += 32) span = fmaxf(span, __ldcg(a.span + row * a.max_chunks + c));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
+  __syncthreads();
+  select_row<D, NT, SW>(a, r, row, s, h, n, span, tid);
 }
 
+// Rows of at most kSelKeys blocks: a cluster of 1, 2, 4 or 8 CTAs a row, as
+// many as make about two CTAs an SM and leave every warp a tile; CTAs of four
+// warps where the rows alone are more than two an SM.  Longer rows: chunks of
+// 128 blocks and more.
 struct SelectPlan {
-  int chunk = 0, max_chunks = 0;
-  size_t stride = 0, keys = 0, keys64 = 0, maxabs = 0, cnt = 0;
-  size_t total() const { return keys + keys64 + maxabs + cnt; }
+  bool rows_long = false;
+  int warps = 8, chunk = 0, max_chunks = 0;
+  size_t stride = 0, keys = 0, keys64 = 0, span = 0, cnt = 0;
+  size_t total() const { return keys + keys64 + span + cnt; }
 };
 
-// Chunks of 128 blocks (a tile a warp), or as many more as make the rows fill
-// about two CTAs an SM: a CTA then has its table entries a tile ahead and pays
-// its start once for several tiles.
 SelectPlan make_select_plan(const pa_decode_desc *d, int sms) {
   SelectPlan p;
   const int64_t B = d->block_size;
   const size_t nblk = (size_t)std::max<int64_t>(1, ((int64_t)d->max_context_len + B - 1) / B);
-  const size_t rows = (size_t)d->num_seqs * d->num_kv_heads;
+  const size_t rows = (size_t)d->num_seqs * d->num_kv_heads, slots = 2 * (size_t)std::max(sms, 1);
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
-  const size_t per = (rows * nblk + 2 * (size_t)std::max(sms, 1) - 1) / (2 * (size_t)std::max(sms, 1));
-  const size_t unit = 16 * kSelWarps;
-  p.chunk = (int)std::min<size_t>(8 * unit, std::max<size_t>(1, (per + unit - 1) / unit) * unit);
-  p.max_chunks = (int)((nblk + p.chunk - 1) / p.chunk);
+  p.rows_long = nblk > kSelKeys;
+  p.warps = !p.rows_long && rows > slots ? 4 : 8;
+  const size_t unit = 16 * p.warps;
+  if (p.rows_long) {  // as many CTAs as fill the slots once, each of up to 8 tiles a warp
+    const size_t per = (rows * nblk + slots - 1) / slots;
+    p.chunk = (int)std::min<size_t>(8 * unit, std::max<size_t>(1, (per + unit - 1) / unit) * unit);
+    p.max_chunks = (int)((nblk + p.chunk - 1) / p.chunk);
+  } else {
+    size_t c = 1;
+    while (c < 8 && rows * c * 2 <= slots && c * unit < nblk) c *= 2;
+    p.chunk = (int)(((nblk + c - 1) / c + unit - 1) / unit * unit);
+    p.max_chunks = (int)c;
+  }
   p.stride = (nblk + 3) & ~(size_t)3;
   p.keys64 = up(rows * p.stride * 8);
-  p.keys = up(rows * p.stride * 4);
-  p.maxabs = up(rows * ((nblk + unit - 1) / unit) * 4);  // (whatever the SM count)
-  p.cnt = up(rows * 8);
+  if (p.rows_long) {
+    p.keys = up(rows * p.stride * 4);
+    p.span = up(rows * ((nblk + unit - 1) / unit) * 4);  // (whatever the SM count)
+    p.cnt = up(rows * 8);
+  }
   return p;
+}
+
+template <int D, int NT, int SW, bool LONG>
+int launch_select(const SelectArgs &a, dim3 grid, cudaStream_t st) {
+  auto kern = select_kernel<D, NT, SW, LONG>;
+  static_assert(sizeof(RowSelect<SW>) <= 48 * 1024, "static shared memory");
+  if (LONG || grid.x == 1) {
+    kern<<<grid, SW * 32, 0, st>>>(a);
+    return launch_status(cudaGetLastError());
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(SW * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = grid.x;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+template <int D, int NT>
+int dispatch_select(const SelectArgs &a, const SelectPlan &p, dim3 grid, cudaStream_t st) {
+  if (p.rows_long) return launch_select<D, NT, 8, true>(a, grid, st);
+  return p.warps == 4 ? launch_select<D, NT, 4, false>(a, grid, st) : launch_select<D, NT, 8, false>(a, grid, st);
 }
 
 }  // namespace
@@ -555,8 +608,8 @@ extern "C" int pa_select_blocks(const pa_decode_desc *d, const void *q, const vo
   a.selected = selected;
   a.keys64 = reinterpret_cast<unsigned long long *>(ws);
   a.keys = reinterpret_cast<uint32_t *>(ws + p.keys64);
-  a.maxabs = reinterpret_cast<float *>(ws + p.keys64 + p.keys);
-  a.cnt = reinterpret_cast<unsigned long long *>(ws + p.keys64 + p.keys + p.maxabs);
+  a.span = reinterpret_cast<float *>(ws + p.keys64 + p.keys);
+  a.cnt = reinterpret_cast<unsigned long long *>(ws + p.keys64 + p.keys + p.span);
   a.err = err_flag;
   a.Hq = d->num_q_heads;
   a.Hkv = d->num_kv_heads;
@@ -574,16 +627,7 @@ extern "C" int pa_select_blocks(const pa_decode_desc *d, const void *q, const vo
   a.epoch = next_decode_epoch();
   const dim3 grid(p.max_chunks, d->num_kv_heads, d->num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d->head_dim == 128) {
-    if (a.G <= 8)
-      select_kernel<128, 1><<<grid, kSelThreads, 0, s>>>(a);
-    else
-      select_kernel<128, 2><<<grid, kSelThreads, 0, s>>>(a);
-  } else {
-    if (a.G <= 8)
-      select_kernel<64, 1><<<grid, kSelThreads, 0, s>>>(a);
-    else
-      select_kernel<64, 2><<<grid, kSelThreads, 0, s>>>(a);
-  }
-  return launch_status(cudaGetLastError());
+  if (d->head_dim == 128)
+    return a.G <= 8 ? dispatch_select<128, 1>(a, p, grid, s) : dispatch_select<128, 2>(a, p, grid, s);
+  return a.G <= 8 ? dispatch_select<64, 1>(a, p, grid, s) : dispatch_select<64, 2>(a, p, grid, s);
 }

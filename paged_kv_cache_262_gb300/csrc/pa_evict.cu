@@ -42,13 +42,13 @@ struct EvictArgs {
 };
 
 // grid (kv head, sequence).  A row of weights that fits is held in shared
-// memory as it is (keys are made of it as they are looked at), so that what is
-// kept leaves straight from there, in place or not; a longer one is read again
-// for each pass, and its kept weights move by stretches, read before they are
-// written.
+// memory as ordered keys, which give the weights back (NaN and -0 as the usual
+// NaN and +0), so that what is kept leaves straight from there, in place or
+// not; a longer one is read again for each pass, and its kept weights move by
+// stretches, read before they are written.
 template <int NT>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
-  extern __shared__ float sw[];
+  extern __shared__ __align__(16) uint32_t skeys[];
   __shared__ SelectSmem<NT> sm;
   grid_launch_dependents();
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
@@ -81,38 +81,74 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
       for (int i = tid; i < n; i += NT) wo[i] = w[i];
     return;
   }
+  // keys of the tokens that compete, N of them behind the sinks
   const int N = ctx - a.sink - a.recent, want = n - a.sink - a.recent;
-  const bool in_smem = ctx <= a.smem_keys;
+  const float *wc = w + a.sink;
+  const bool in_smem = N <= a.smem_keys;
   uint32_t least = ~0u, most = 0u;
-#pragma unroll 8
-  for (int i = tid; i < ctx; i += NT) {
-    const float x = __ldcs(w + i);
-    if (in_smem) sw[i] = x;
-    if (i >= a.sink && i < ctx - a.recent) {
-      const uint32_t k = order_key(x);
-      least = min(least, k);
-      most = max(most, k);
-    }
-  }
-  __syncthreads();
-  auto put = [&](int i, int j) {  // token j is kept, as number i
-    kept[i] = j;
-    if (in_smem) wo[i] = sw[j];
+  auto look = [&](int i, uint32_t k) {
+    if (in_smem) skeys[i] = k;
+    least = min(least, k);
+    most = max(most, k);
   };
-  for (int i = tid; i < a.sink; i += NT) put(i, i);
-  for (int i = tid; i < a.recent; i += NT) put(n - a.recent + i, ctx - a.recent + i);
   if (want > 0) {
-    auto key = [&](int i) -> uint32_t { return order_key(in_smem ? sw[a.sink + i] : w[a.sink + i]); };
-    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key, N, want, sm, tid, least, most);
-    take_above<NT, uint32_t>(key, N, t.key, want - t.above, want, sm, tid,
-                             [&](int pos, int i) { put(a.sink + pos, a.sink + i); });
+    const int head = min(N, (int)(-(reinterpret_cast<uintptr_t>(wc) >> 2) & 3));  // up to a 16-byte boundary
+    if (tid < head) look(tid, order_key(wc[tid]));
+    const float4 *wv = reinterpret_cast<const float4 *>(wc + head);
+    const int nv = (N - head) / 4;
+#pragma unroll 8
+    for (int i = tid; i < nv; i += NT) {
+      const float4 x = __ldcs(wv + i);
+      const uint4 k = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+      least = min(min(least, min(k.x, k.y)), min(k.z, k.w));
+      most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
+      if (!in_smem) continue;
+      uint32_t *to = skeys + head + 4 * i;
+      if (head == 0)
+        *reinterpret_cast<uint4 *>(to) = k;
+      else
+        to[0] = k.x, to[1] = k.y, to[2] = k.z, to[3] = k.w;
+    }
+    const int i = head + 4 * nv + tid;
+    if (i < N) look(i, order_key(wc[i]));
   }
-  if (in_smem) {
+  // the ends: sinks stay where they are, recent tokens are read before any write
+  constexpr int kEnd = 4;
+  float tail[kEnd];
+#pragma unroll
+  for (int e = 0; e < kEnd; ++e)
+    if (e * NT + tid < a.recent) tail[e] = w[ctx - a.recent + e * NT + tid];
+  __syncthreads();
+  for (int i = tid; i < a.sink; i += NT) {
+    kept[i] = i;
+    if (wo != w) wo[i] = w[i];
+  }
+  for (int i = tid; i < a.recent; i += NT) kept[n - a.recent + i] = ctx - a.recent + i;
+  if (want > 0) {
+    auto key4 = [&](int i) {
+      if (in_smem) return keys4(*reinterpret_cast<const uint4 *>(skeys + i));
+      Keys4<uint32_t> k;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k.v[e] = i + e < N ? order_key(wc[i + e]) : 0u;
+      return k;
+    };
+    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key4, N, want, sm, tid, least, most);
+    take_above<NT, uint32_t>(key4, N, t.key, want - t.above, want, sm, tid, [&](int pos, int i, uint32_t k) {
+      kept[a.sink + pos] = a.sink + i;
+      if (in_smem) wo[a.sink + pos] = key_value(k);
+    });
+  }
+  if (in_smem && a.recent <= kEnd * NT) {
+#pragma unroll
+    for (int e = 0; e < kEnd; ++e)
+      if (e * NT + tid < a.recent) wo[n - a.recent + e * NT + tid] = tail[e];
     for (int i = n + tid; i < ctx; i += NT) wo[i] = 0.f;
     return;
   }
   __syncthreads();
-  for (int base = 0; base < ctx; base += NT) {
+  // by stretches; where the competing ones have gone already, the recent ones
+  const int from = in_smem ? n - a.recent : 0;
+  for (int base = from; base < ctx; base += NT) {
     const int i = base + tid;
     const float v = i < n ? w[min(max(kept[i], 0), ctx - 1)] : 0.f;
     __syncthreads();
@@ -315,7 +351,7 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
   // Short rows take small CTAs, several an SM.
   constexpr int kShort = 4096, kLong = 48 * 1024;
   a.smem_keys = std::min(d->max_context_len, kLong);
-  const size_t smem = (size_t)a.smem_keys * 4;
+  const size_t smem = (size_t)((a.smem_keys + 3) & ~3) * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->max_context_len <= kShort) {
     evict_select_kernel<256><<<dim3(a.Hkv, a.S), 256, smem, s>>>(a);

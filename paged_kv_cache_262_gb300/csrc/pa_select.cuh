@@ -25,14 +25,14 @@ __device__ __forceinline__ unsigned long long order_key64(double x) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-// Counting bins of a CTA of NT threads: eight a thread.
+// Counting bins of a CTA of NT threads: eight a thread, or sixteen.
 template <int NT>
 constexpr int kDigitBits = NT >= 1024 ? 13 : NT >= 512 ? 12 : 11;
 constexpr int kNearKeys = 256;  // keys of one bin that are ranked by comparing all of them
 
 template <int NT>
 struct SelectSmem {
-  int4 hist[2 * NT];
+  int4 hist[(1 << kDigitBits<NT>) / 4];
   unsigned long long lo[NT / 32], hi[NT / 32];
   unsigned long long near_[kNearKeys], kth;
   int a[NT / 32], b[NT / 32];
@@ -46,18 +46,39 @@ struct Kth {
   int above;
 };
 
+// Four consecutive keys: key4(i) for i a multiple of 4 below n (what it gives
+// for places past n - 1 is not looked at).
+template <class T>
+struct Keys4 {
+  T v[4];
+};
+
+__device__ __forceinline__ Keys4<uint32_t> keys4(uint4 x) { return Keys4<uint32_t>{{x.x, x.y, x.z, x.w}}; }
+
 __device__ __forceinline__ int lead_zeros(uint32_t x) { return __clz((int)x); }
 __device__ __forceinline__ int lead_zeros(unsigned long long x) { return __clzll((long long)x); }
 
-// Whole CTA of NT threads; key(i) for i < n; lo and hi: the least and largest
-// key of those that this thread looked at, all of them among the threads.  A
-// digit is the bits below those that all keys left share, so that the first
-// one already tells keys of one magnitude apart (scores of a context differ in
-// few high bits); once a bin's keys are few they are ranked by comparison.
-template <int NT, class T, class KeyF>
-__device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int tid, T lo, T hi) {
+// f(i, key) for every key of this thread: four consecutive ones at a time.
+template <int NT, class T, class Key4, class F>
+__device__ __forceinline__ void for_keys(Key4 key4, int n, int tid, F f) {
+#pragma unroll 2
+  for (int i = 4 * tid; i < n; i += 4 * NT) {
+    const Keys4<T> k = key4(i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < n) f(i + e, k.v[e]);
+  }
+}
+
+// Whole CTA of NT threads; lo and hi: the least and largest key of those that
+// this thread looked at, all of them among the threads.  A digit is the bits
+// below those that all keys left share, so that the first one already tells
+// keys of one magnitude apart (scores of a context differ in few high bits);
+// once a bin's keys are few they are ranked by comparison.
+template <int NT, class T, class Key4>
+__device__ Kth<T> kth_largest(Key4 key4, int n, int want, SelectSmem<NT> &sm, int tid, T lo, T hi) {
   constexpr int kBits = 8 * sizeof(T), kDigit = kDigitBits<NT>, kBins = 1 << kDigit, kPer = kBins / NT;
-  static_assert(kBins * (int)sizeof(int) == (int)sizeof(sm.hist), "eight bins a thread");
+  static_assert(kBins * (int)sizeof(int) <= (int)sizeof(sm.hist), "the bins fit");
   const int lane = tid & 31, warp = tid >> 5;
   int *hist = reinterpret_cast<int *>(sm.hist);
 #pragma unroll
@@ -84,16 +105,19 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
   int left = want, above = 0;
   while (open > 0) {
     const int w = min(kDigit, open), sh = open - w;
-#pragma unroll 4
-    for (int i = tid; i < n; i += NT) {
-      const T k = key(i);
-      if (open == kBits || (k ^ base) >> open == 0) atomicAdd(&hist[(int)(k >> sh) & ((1 << w) - 1)], 1);
-    }
+    const bool all = open == kBits;  // (a shift by every bit is none)
+    for_keys<NT, T>(key4, n, tid, [&](int, T k) {
+      if (all || (k ^ base) >> open == 0) atomicAdd(&hist[(int)(k >> sh) & ((1 << w) - 1)], 1);
+    });
     __syncthreads();
     // bins from the highest down, kPer consecutive ones a thread
     int cnt[kPer], c = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) c += cnt[j] = hist[kBins - 1 - tid * kPer - j];
+    for (int j = 0; j < kPer / 4; ++j) {
+      const int4 b = sm.hist[(kBins - tid * kPer) / 4 - 1 - j];
+      cnt[4 * j] = b.w, cnt[4 * j + 1] = b.z, cnt[4 * j + 2] = b.y, cnt[4 * j + 3] = b.x;
+      c += b.x + b.y + b.z + b.w;
+    }
     int incl = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -122,15 +146,13 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
     left -= sm.above;
     open = sh;
     const int count = sm.count;
-    if (open > 0 && count <= kNearKeys) {
-#pragma unroll 4
-      for (int i = tid; i < n; i += NT) {
-        const T k = key(i);
+    if (open > 0 && count <= kNearKeys && count <= NT) {
+      for_keys<NT, T>(key4, n, tid, [&](int, T k) {
         if ((k ^ base) >> open == 0) {
           const int at = atomicAdd(&sm.filled, 1);
           if (at < kNearKeys) sm.near_[at] = k;
         }
-      }
+      });
       __syncthreads();
       if (tid < count) {
         const T mine = (T)sm.near_[tid];
@@ -152,21 +174,27 @@ __device__ Kth<T> kth_largest(KeyF key, int n, int want, SelectSmem<NT> &sm, int
   return Kth<T>{base, above};
 }
 
-// Calls emit(position, i) for every i < n with key(i) > t, and for the first
-// need of those with key(i) == t, in increasing order of i, at most `room` of
-// them (keys that another launch overwrites meanwhile must not write past the
-// list).  Whole CTA.
-template <int NT, class T, class KeyF, class Emit>
-__device__ void take_above(KeyF key, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid, Emit emit) {
+// Calls emit(position, i, key) for every key above t, and for the first need of
+// those equal to t, in increasing order of i, at most `room` of them (keys that
+// another launch overwrites meanwhile must not write past the list).  Whole
+// CTA: every warp counts its consecutive stretch, then lists it.
+template <int NT, class T, class Key4, class Emit>
+__device__ void take_above(Key4 key4, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid, Emit emit) {
   const int lane = tid & 31, warp = tid >> 5;
-  const int seg = (n + NT - 1) / NT * 32;  // a warp's consecutive keys
+  const int seg = (n + 4 * NT - 1) / (4 * NT) * 128;  // keys of a warp
   const int beg = min(n, warp * seg), end = min(n, beg + seg);
   int gt = 0, eq = 0;
-  for (int i = beg + lane; i < beg + seg; i += 32) {
-    const T k = i < end ? key(i) : (T)0;
-    gt += __popc(__ballot_sync(0xffffffffu, i < end && k > t));
-    eq += __popc(__ballot_sync(0xffffffffu, i < end && k == t));
+#pragma unroll 2
+  for (int i = beg + 4 * lane; i < end; i += 128) {
+    const Keys4<T> k = key4(i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += i + e < end && k.v[e] > t;
+      eq += i + e < end && k.v[e] == t;
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   __syncthreads();
   if (lane == 0) {
     sm.a[warp] = gt;
@@ -174,21 +202,61 @@ __device__ void take_above(KeyF key, int n, T t, int need, int room, SelectSmem<
   }
   __syncthreads();
   gt = eq = 0;
-  for (int w = 0; w < warp; ++w) {
-    gt += sm.a[w];
-    eq += sm.b[w];
+  int all_eq = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) {
+      gt += sm.a[w];
+      eq += sm.b[w];
+    }
+    all_eq += sm.b[w];
   }
+  const bool every = need >= all_eq;  // then the order of the equal ones does not matter
   int pos = gt + min(eq, need);
-  const unsigned int below = (1u << lane) - 1u;
-  for (int i = beg + lane; i < beg + seg; i += 32) {
-    const T k = i < end ? key(i) : (T)0;
-    const unsigned int e = __ballot_sync(0xffffffffu, i < end && k == t);
-    const bool in = i < end && (k > t || (k == t && eq + __popc(e & below) < need));
-    const unsigned int b = __ballot_sync(0xffffffffu, in);
-    const int at = pos + __popc(b & below);
-    if (in && at < room) emit(at, i);
-    pos += __popc(b);
-    eq += __popc(e);
+  for (int i0 = beg; i0 < end; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    Keys4<T> k;
+    if (i < end) k = key4(i);
+    unsigned int in = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < end && (k.v[e] > t || (every && k.v[e] == t))) in |= 1u << e;
+    if (!every) {
+      unsigned int same = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < end && k.v[e] == t) same |= 1u << e;
+      const int c = __popc(same);
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      int rank = eq + incl - c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (same >> e & 1) {
+          if (rank < need) in |= 1u << e;
+          ++rank;
+        }
+      eq += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int c = __popc(in);
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int at = pos + incl - c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (in >> e & 1) {
+        if (at < room) emit(at, i + e, k.v[e]);
+        ++at;
+      }
+    pos += __shfl_sync(0xffffffffu, incl, 31);
   }
 }
 

@@ -283,6 +283,13 @@ def test_evict_long_contexts(torch, ctx, keep):
     run_evict(torch, (2, 2, 64, 16), [ctx, ctx // 2], [keep, keep // 2], 4, 64)
 
 
+@pytest.mark.parametrize("ctx,keep,sink,recent", [(3500, 2000, 3, 1500), (3500, 2000, 0, 2000), (9000, 8000, 1, 5000),
+                                                  (60000, 40000, 2, 30000), (700, 600, 600, 0)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_with_long_ends(torch, ctx, keep, sink, recent, in_place):
+    run_evict(torch, (2, 2, 64, 16), [ctx, ctx // 2 + 11], [keep, keep], sink, recent, in_place=in_place)
+
+
 def _ties(w):
     w.copy_((w * 40).round() / 40)  # few values
 
