@@ -189,7 +189,7 @@ constexpr float kScoreError = 18.f * (2 * D / 16) * 1.1920929e-07f * 1.001f;
 
 // One CTA selects a row's blocks from its keys (in r.keys, or past kSelKeys of
 // them in the workspace), A the row's largest absolute sum.
-template <int D, int NT, int SW>
+template <int D, int NT, int SW, bool LONG>
 __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, int s, int h, int n, float A, int tid) {
   constexpr int kThreads = SW * 32;
   const int lane = tid & 31, warp = tid >> 5;
@@ -201,9 +201,12 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
   for (int i = tid; i < a.sink; i += kThreads) out[i] = i;
   for (int i = tid; i < a.recent; i += kThreads) out[a.k - a.recent + i] = end + i;
   if (want == 0) return;
-  const bool in_smem = N <= kSelKeys;
+  const bool in_smem = !LONG || N <= kSelKeys;
   uint32_t *keys = in_smem ? reinterpret_cast<uint32_t *>(r.keys) : a.keys + row * a.stride;
   auto key4 = [&](int i) { return keys4(in_smem ? r.keys[i / 4] : __ldcg(reinterpret_cast<const uint4 *>(keys + i))); };
+  auto key1 = [&](int i) {
+    return in_smem ? reinterpret_cast<const uint32_t *>(r.keys)[i] : __ldcg(keys + i);
+  };
   const float slack = 2.f * kScoreError<D> * A;
   const bool finite = slack < INFINITY;  // false for NaN too: then no fp32 score is trusted
   uint32_t lo = 0u, hi = 0xfffffffeu;    // (no score's key is above it)
@@ -237,7 +240,7 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
   const int near_ = r.nex, need = want - r.ngt;
   auto emit = [&](int pos, int i, uint32_t) { out[a.sink + pos] = first + i; };
   if (near_ == need || hi == 0u) {  // (of blocks outside the pool, the first)
-    take_above<kThreads, uint32_t>(key4, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, r.sm, tid, emit);
+    take_above<kThreads, uint32_t>(key4, key1, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, r.sm, tid, emit);
     return;
   }
   if (near_ <= kSelRefine) {  // few: their exact scores, ranked by counting
@@ -254,14 +257,14 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
       keys[r.exi[c]] = rank < need ? 0xffffffffu : 0u;
     }
     __syncthreads();
-    take_above<kThreads, uint32_t>(key4, N, hi, 0, want, r.sm, tid, emit);
+    take_above<kThreads, uint32_t>(key4, key1, N, hi, 0, want, r.sm, tid, emit);
     return;
   }
   // many (scores that tie in numbers, infinite bounds): 64-bit keys for all of
   // them in the workspace
   unsigned long long *k64 = a.keys64 + row * a.stride;
   for (int i = warp; i < N; i += SW) {
-    const uint32_t k = key4(i & ~3).v[i & 3];
+    const uint32_t k = key1(i);
     unsigned long long x = k > hi ? ~0ull : 0ull;
     if (k >= lo && k <= hi) {
       const int pg = __ldg(bt + first + i);
@@ -284,7 +287,7 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
     m64 = max(m64, k);
   });
   const Kth<unsigned long long> t = kth_largest<kThreads, unsigned long long>(key64, N, want, r.sm, tid, l64, m64);
-  take_above<kThreads, unsigned long long>(key64, N, t.key, want - t.above, want, r.sm, tid,
+  take_above<kThreads, unsigned long long>(key64, [&](int i) { return k64[i]; }, N, t.key, want - t.above, want, r.sm, tid,
                                            [&](int pos, int i, unsigned long long) { out[a.sink + pos] = first + i; });
 }
 
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectAr
       cluster_wait();
       for (int c = 0; c < (int)gridDim.x; ++c) span = fmaxf(span, r.span[c]);
     }
-    select_row<D, NT, SW>(a, r, row, s, h, n, span, tid);
+    select_row<D, NT, SW, LONG>(a, r, row, s, h, n, span, tid);
     return;
   }
   if (tid == 0) {
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectAr
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
   __syncthreads();
-  select_row<D, NT, SW>(a, r, row, s, h, n, span, tid);
+  select_row<D, NT, SW, LONG>(a, r, row, s, h, n, span, tid);
 }
 
 // Rows of at most kSelKeys blocks: a cluster of 1, 2, 4 or 8 CTAs a row, as

@@ -45,8 +45,8 @@ struct EvictArgs {
 // memory as ordered keys, which give the weights back (NaN and -0 as the usual
 // NaN and +0), so that what is kept leaves straight from there, in place or
 // not; a longer one is read again for each pass, and its kept weights move by
-// stretches, read before they are written.
-template <int NT>
+// stretches, read before they are written.  SMEM: every row fits.
+template <int NT, bool SMEM>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t skeys[];
   __shared__ SelectSmem<NT> sm;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   // keys of the tokens that compete, N of them behind the sinks
   const int N = ctx - a.sink - a.recent, want = n - a.sink - a.recent;
   const float *wc = w + a.sink;
-  const bool in_smem = N <= a.smem_keys;
+  const bool in_smem = SMEM || N <= a.smem_keys;
   uint32_t least = ~0u, most = 0u;
   auto look = [&](int i, uint32_t k) {
     if (in_smem) skeys[i] = k;
@@ -96,18 +96,25 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     if (tid < head) look(tid, order_key(wc[tid]));
     const float4 *wv = reinterpret_cast<const float4 *>(wc + head);
     const int nv = (N - head) / 4;
-#pragma unroll 8
-    for (int i = tid; i < nv; i += NT) {
-      const float4 x = __ldcs(wv + i);
-      const uint4 k = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
-      least = min(min(least, min(k.x, k.y)), min(k.z, k.w));
-      most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
-      if (!in_smem) continue;
-      uint32_t *to = skeys + head + 4 * i;
-      if (head == 0)
-        *reinterpret_cast<uint4 *>(to) = k;
-      else
-        to[0] = k.x, to[1] = k.y, to[2] = k.z, to[3] = k.w;
+    for (int base = 0; base < nv; base += 8 * NT) {
+      float4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (base + u * NT + tid < nv) x[u] = __ldcs(wv + base + u * NT + tid);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = base + u * NT + tid;
+        if (i >= nv) break;
+        const uint4 k = make_uint4(order_key(x[u].x), order_key(x[u].y), order_key(x[u].z), order_key(x[u].w));
+        least = min(min(least, min(k.x, k.y)), min(k.z, k.w));
+        most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
+        if (!in_smem) continue;
+        uint32_t *to = skeys + head + 4 * i;
+        if (head == 0)
+          *reinterpret_cast<uint4 *>(to) = k;
+        else
+          to[0] = k.x, to[1] = k.y, to[2] = k.z, to[3] = k.w;
+      }
     }
     const int i = head + 4 * nv + tid;
     if (i < N) look(i, order_key(wc[i]));
@@ -132,8 +139,9 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
       for (int e = 0; e < 4; ++e) k.v[e] = i + e < N ? order_key(wc[i + e]) : 0u;
       return k;
     };
+    auto key1 = [&](int i) { return in_smem ? skeys[i] : order_key(wc[i]); };
     const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key4, N, want, sm, tid, least, most);
-    take_above<NT, uint32_t>(key4, N, t.key, want - t.above, want, sm, tid, [&](int pos, int i, uint32_t k) {
+    take_above<NT, uint32_t>(key4, key1, N, t.key, want - t.above, want, sm, tid, [&](int pos, int i, uint32_t k) {
       kept[a.sink + pos] = a.sink + i;
       if (in_smem) wo[a.sink + pos] = key_value(k);
     });
@@ -353,13 +361,14 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
   a.smem_keys = std::min(d->max_context_len, kLong);
   const size_t smem = (size_t)((a.smem_keys + 3) & ~3) * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(a.Hkv, a.S);
   if (d->max_context_len <= kShort) {
-    evict_select_kernel<256><<<dim3(a.Hkv, a.S), 256, smem, s>>>(a);
+    evict_select_kernel<256, true><<<grid, 256, smem, s>>>(a);
   } else {
-    if (cudaFuncSetAttribute(evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLong * 4) !=
-        cudaSuccess)
+    auto kern = d->max_context_len <= kLong ? evict_select_kernel<1024, true> : evict_select_kernel<1024, false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLong * 4) != cudaSuccess)
       return PA_ERR_CUDA;
-    evict_select_kernel<1024><<<dim3(a.Hkv, a.S), 1024, smem, s>>>(a);
+    kern<<<grid, 1024, smem, s>>>(a);
   }
   const int st = launch_status(cudaGetLastError());
   if (st != PA_OK) return st;

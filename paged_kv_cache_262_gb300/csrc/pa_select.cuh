@@ -174,12 +174,12 @@ __device__ Kth<T> kth_largest(Key4 key4, int n, int want, SelectSmem<NT> &sm, in
   return Kth<T>{base, above};
 }
 
-// Calls emit(position, i, key) for every key above t, and for the first need of
+// (key1(i): one of them.)  Calls emit(position, i, key) for every key above t, and for the first need of
 // those equal to t, in increasing order of i, at most `room` of them (keys that
 // another launch overwrites meanwhile must not write past the list).  Whole
 // CTA: every warp counts its consecutive stretch, then lists it.
-template <int NT, class T, class Key4, class Emit>
-__device__ void take_above(Key4 key4, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid, Emit emit) {
+template <int NT, class T, class Key4, class Key1, class Emit>
+__device__ void take_above(Key4 key4, Key1 key1, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid, Emit emit) {
   const int lane = tid & 31, warp = tid >> 5;
   const int seg = (n + 4 * NT - 1) / (4 * NT) * 128;  // keys of a warp
   const int beg = min(n, warp * seg), end = min(n, beg + seg);
@@ -212,51 +212,22 @@ __device__ void take_above(Key4 key4, int n, T t, int need, int room, SelectSmem
     all_eq += sm.b[w];
   }
   const bool every = need >= all_eq;  // then the order of the equal ones does not matter
+  const unsigned int below = (1u << lane) - 1u;
   int pos = gt + min(eq, need);
-  for (int i0 = beg; i0 < end; i0 += 128) {
-    const int i = i0 + 4 * lane;
-    Keys4<T> k;
-    if (i < end) k = key4(i);
-    unsigned int in = 0u;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < end && (k.v[e] > t || (every && k.v[e] == t))) in |= 1u << e;
+#pragma unroll 4
+  for (int i0 = beg; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const T k = i < end ? key1(i) : (T)0;
+    bool in = i < end && (k > t || (every && k == t));
     if (!every) {
-      unsigned int same = 0u;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < end && k.v[e] == t) same |= 1u << e;
-      const int c = __popc(same);
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      int rank = eq + incl - c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (same >> e & 1) {
-          if (rank < need) in |= 1u << e;
-          ++rank;
-        }
-      eq += __shfl_sync(0xffffffffu, incl, 31);
+      const unsigned int same = __ballot_sync(0xffffffffu, i < end && k == t);
+      in |= (same >> lane & 1u) && eq + __popc(same & below) < need;
+      eq += __popc(same);
     }
-    const int c = __popc(in);
-    int incl = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    int at = pos + incl - c;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (in >> e & 1) {
-        if (at < room) emit(at, i + e, k.v[e]);
-        ++at;
-      }
-    pos += __shfl_sync(0xffffffffu, incl, 31);
+    const unsigned int b = __ballot_sync(0xffffffffu, in);
+    const int at = pos + __popc(b & below);
+    if (in && at < room) emit(at, i, k);
+    pos += __popc(b);
   }
 }
 
