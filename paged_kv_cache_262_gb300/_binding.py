@@ -594,70 +594,81 @@ def swap_blocks(src_k_pools: Sequence, src_v_pools: Sequence, dst_k_pools: Seque
 # them, so what a call costs on the host counts: the common case of every check
 # is a few attribute reads, and the messages are made only when one fails.
 _WS_SELECT, _WS_SPARSE, _WS_WEIGHTS = {}, {}, {}
+_T = None  # what the calls use of torch, looked up once
 
 
-def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+class _Torch:
+    def __init__(self):
+        import torch
+        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.capturing = torch.cuda.is_current_stream_capturing
+        # the public forms build a device or stream object a call (3 us)
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _raw_stream(stream, device: int) -> int:
-    """The handle of `stream`, or of the device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    f = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() builds an object, 3 us
-    return f(device) if f is not None else torch.cuda.current_stream(device).cuda_stream
+def _torch():
+    global _T
+    _T = _Torch()
+    return _T
+
+
+def _on_device(device, t, name, dtype, nd):
+    """The reason why t is not a contiguous CUDA tensor of that dtype and rank
+    on the current device, raised; nothing if it is one."""
+    _need(t, dtype, name, nd)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
 def _all(device, *specs):
     """Every (tensor, name, dtype, dims) is a contiguous CUDA tensor of that
     dtype and rank on the current device."""
-    for t, name, dtype, nd in specs:
-        try:
-            if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.dim() == nd:
-                continue
-        except AttributeError:
-            pass
-        _need(t, dtype, name, nd)
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    try:
+        for t, name, dtype, nd in specs:
+            if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or t.dim() != nd:
+                _on_device(device, t, name, dtype, nd)
+    except AttributeError:
+        _on_device(device, t, name, dtype, nd)
+        raise
 
 
-def _err_ptr(err_flag, device):
+def _err_ptr(err_flag, device, i32):
     if err_flag is None:
         return None
-    p = _flag(err_flag)
-    if err_flag.get_device() != device:
-        raise ValueError(f"err_flag is on {err_flag.device}, the current device is cuda:{device}")
-    return p
+    _all(device, (err_flag, "err_flag", i32, err_flag.dim() if hasattr(err_flag, "dim") else None))
+    if err_flag.numel() < 1:
+        raise ValueError("err_flag needs one int32")
+    return err_flag.data_ptr()
 
 
 def _bad(what):
     raise ValueError(what)
 
 
-def _new(shape, dtype, device, stream):
+def _new(T, shape, dtype, device, stream):
     """An output tensor that belongs to the stream the call runs on."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return T.empty(shape, dtype=dtype, device=device)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return T.empty(shape, dtype=dtype, device=device)
 
 
-def _call_ws(cache, need, device, stream, raw):
+def _call_ws(T, cache, need, device, stream, raw):
     """(pointer, bytes, tensor) of the workspace of a call that was given
     none: cached per (device, stream), except under graph capture, where the
     graph's own memory holds it -- a replay must not share the cache with the
-    calls outside it."""
+    calls outside it.  (The legacy stream, handle 0, cannot be captured.)"""
     if need == 0:
         return None, 0, None
-    import torch
-    idx = device.index
-    if torch.cuda.is_current_stream_capturing():
-        ws = _new((need,), torch.uint8, device, stream)
+    if raw and T.capturing():
+        import torch
+        ws = _new(T, (need,), torch.uint8, device, stream)
     else:
-        ws = cache.get((idx, raw))
+        ws = cache.get((device.index, raw))
         if ws is None or ws.numel() < need:
             ws = _cached_ws(cache, need, device, stream)
     return ws.data_ptr(), ws.numel(), ws
@@ -667,13 +678,12 @@ def _given_ws(workspace):
     return _ws(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
-def _weight_args(weights, weights_out, weight_rows, S, hkv, max_ctx, dev):
-    import torch
+def _weight_args(T, weights, weights_out, weight_rows, S, hkv, max_ctx, dev):
     if weights_out is None:
         weights_out = weights
-        _all(dev, (weights, "weights", torch.float32, 3))
+        _all(dev, (weights, "weights", T.f32, 3))
     else:
-        _all(dev, (weights, "weights", torch.float32, 3), (weights_out, "weights_out", torch.float32, 3))
+        _all(dev, (weights, "weights", T.f32, 3), (weights_out, "weights_out", T.f32, 3))
         if weights_out.shape != weights.shape:
             _bad(f"weights_out must have weights' shape {tuple(weights.shape)}")
         a, b = weights.data_ptr(), weights_out.data_ptr()
@@ -686,7 +696,7 @@ def _weight_args(weights, weights_out, weight_rows, S, hkv, max_ctx, dev):
     if width < max_ctx:
         _bad(f"weights has room for {width} tokens, max_context_len is {max_ctx}")
     if weight_rows is not None:
-        _all(dev, (weight_rows, "weight_rows", torch.int32, 1))
+        _all(dev, (weight_rows, "weight_rows", T.i32, 1))
         if weight_rows.shape[0] < S:
             _bad(f"weight_rows has {weight_rows.shape[0]} rows, needs {S}")
     elif nr < S:
@@ -699,8 +709,8 @@ def block_key_bounds(k_pool, bounds, block_tables, context_lens, start_lens=None
     """Writes the channel-wise minimum and maximum of the keys of every block
     from start_lens[s] on into bounds [num_blocks][Hkv][2][D] (see
     pagedattn.h); returns bounds."""
-    import torch
-    bf, i32, dev = torch.bfloat16, torch.int32, _current_device()
+    T = _T or _torch()
+    bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (k_pool, "k_pool", bf, 4), (bounds, "bounds", bf, 4), (block_tables, "block_tables", i32, 2),
          (context_lens, "context_lens", i32, 1))
     nblk, hkv, bs, d = k_pool.shape
@@ -716,10 +726,10 @@ def block_key_bounds(k_pool, bounds, block_tables, context_lens, start_lens=None
         start = start_lens.data_ptr()
     most = mb * bs if max_context_len is None else int(max_context_len)
     desc = DecodeDesc(S, hkv, hkv, d, bs, nblk, mb, most, 1.0)
-    st = load().pa_block_key_bounds(_c.byref(desc), k_pool.data_ptr(), block_tables.data_ptr(),
+    st = (_LIB or load()).pa_block_key_bounds(_c.byref(desc), k_pool.data_ptr(), block_tables.data_ptr(),
                                     context_lens.data_ptr(), start,
                                     most if max_new_tokens is None else int(max_new_tokens), bounds.data_ptr(),
-                                    _err_ptr(err_flag, dev), _raw_stream(stream, dev))
+                                    _err_ptr(err_flag, dev, T.i32), T.stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "pa_block_key_bounds")
     return bounds
@@ -729,8 +739,8 @@ def select_blocks(q, bounds, block_tables, context_lens, num_select, *, block_si
                   selected=None, max_context_len=None, workspace=None, err_flag=None, stream=None):
     """The logical blocks each (sequence, kv head) attends this step, int32
     [num_seqs][Hkv][num_select], increasing, then -1 (see pagedattn.h)."""
-    import torch
-    bf, i32, dev = torch.bfloat16, torch.int32, _current_device()
+    T = _T or _torch()
+    bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (q, "q", bf, 3), (bounds, "bounds", bf, 4), (block_tables, "block_tables", i32, 2),
          (context_lens, "context_lens", i32, 1))
     (nblk, hkv, two, d), (S, hq, qd), (brows, mb) = bounds.shape, q.shape, block_tables.shape
@@ -742,27 +752,26 @@ def select_blocks(q, bounds, block_tables, context_lens, num_select, *, block_si
     if k <= 0:
         _bad(f"num_select must be positive, got {k}")
     if selected is None:
-        selected = _new((S, hkv, k), i32, q.device, stream)
+        selected = _new(T, (S, hkv, k), i32, q.device, stream)
     else:
         _all(dev, (selected, "selected", i32, 3))
         if selected.shape != (S, hkv, k):
             _bad(f"selected must be [{S}][{hkv}][{k}]")
     desc = DecodeDesc(S, hq, hkv, d, bs, nblk, mb, mb * bs if max_context_len is None else int(max_context_len), 1.0)
-    lib, raw = load(), _raw_stream(stream, dev)
+    lib, raw = _LIB or load(), T.stream(dev) if stream is None else stream.cuda_stream
     ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
-        _WS_SELECT, lib.pa_select_blocks_workspace_bytes(_c.byref(desc)), q.device, stream, raw)
+        T, _WS_SELECT, lib.pa_select_blocks_workspace_bytes(_c.byref(desc)), q.device, stream, raw)
     st = lib.pa_select_blocks(_c.byref(desc), q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(),
                               context_lens.data_ptr(), k, int(sink_blocks), int(recent_blocks), selected.data_ptr(),
-                              ws, ws_bytes, _err_ptr(err_flag, dev), raw)
+                              ws, ws_bytes, _err_ptr(err_flag, dev, T.i32), raw)
     if st:
         _check(st, "pa_select_blocks")
     return selected
 
 
-def _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream):
+def _decode_args(T, q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream):
     """The checks and the desc that the two decode calls share; (out, desc)."""
-    import torch
-    bf, i32 = torch.bfloat16, torch.int32
+    bf, i32 = T.bf16, T.i32
     _all(dev, (q, "q", bf, 3), (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4),
          (block_tables, "block_tables", i32, 2), (context_lens, "context_lens", i32, 1))
     (nblk, hkv, bs, d), (S, hq, qd), (brows, mb) = k_pool.shape, q.shape, block_tables.shape
@@ -773,7 +782,7 @@ def _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_
     if brows < S or context_lens.shape[0] < S:
         _bad(f"block_tables has {brows} rows, context_lens {context_lens.shape[0]}, needs {S}")
     if out is None:
-        out = torch.empty_like(q) if stream is None else _new(q.shape, bf, q.device, stream)
+        out = T.empty_like(q) if stream is None else _new(T, q.shape, bf, q.device, stream)
     else:
         _all(dev, (out, "out", bf, 3))
         if out.shape != q.shape:
@@ -786,19 +795,19 @@ def paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens,
                                   max_context_len=None, workspace=None, err_flag=None, stream=None):
     """Decode attention over the listed blocks of every (sequence, kv head)
     (see pagedattn.h)."""
-    import torch
-    dev = _current_device()
-    out, desc = _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
-    _all(dev, (selected, "selected", torch.int32, 3))
+    T = _T or _torch()
+    dev = T.device()
+    out, desc = _decode_args(T, q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
+    _all(dev, (selected, "selected", T.i32, 3))
     rows, heads, k = selected.shape
     if rows < desc.num_seqs or heads != desc.num_kv_heads:
         _bad(f"selected must be [{desc.num_seqs}][{desc.num_kv_heads}][num_select], got {tuple(selected.shape)}")
-    lib, raw = load(), _raw_stream(stream, dev)
+    lib, raw = _LIB or load(), T.stream(dev) if stream is None else stream.cuda_stream
     ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
-        _WS_SPARSE, lib.pa_decode_sparse_workspace_bytes(_c.byref(desc), k), q.device, stream, raw)
+        T, _WS_SPARSE, lib.pa_decode_sparse_workspace_bytes(_c.byref(desc), k), q.device, stream, raw)
     st = lib.pa_paged_attention_decode_sparse(_c.byref(desc), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                               block_tables.data_ptr(), context_lens.data_ptr(), selected.data_ptr(),
-                                              k, out.data_ptr(), ws, ws_bytes, _err_ptr(err_flag, dev), raw)
+                                              k, out.data_ptr(), ws, ws_bytes, _err_ptr(err_flag, dev, T.i32), raw)
     if st:
         _check(st, "pa_paged_attention_decode_sparse")
     return out
@@ -810,18 +819,19 @@ def paged_attention_decode_weights(q, k_pool, v_pool, block_tables, context_lens
     """Decode attention that adds every key's attention weight to `weights`
     [num_rows][Hkv][max_tokens] (in place, or into weights_out; see
     pagedattn.h); returns (out, weights_out)."""
-    dev = _current_device()
-    out, desc = _decode_args(q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
-    weights_out, nr, width = _weight_args(weights, weights_out, weight_rows, desc.num_seqs, desc.num_kv_heads,
+    T = _T or _torch()
+    dev = T.device()
+    out, desc = _decode_args(T, q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
+    weights_out, nr, width = _weight_args(T, weights, weights_out, weight_rows, desc.num_seqs, desc.num_kv_heads,
                                           desc.max_context_len, dev)
-    lib, raw = load(), _raw_stream(stream, dev)
+    lib, raw = _LIB or load(), T.stream(dev) if stream is None else stream.cuda_stream
     ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
-        _WS_WEIGHTS, lib.pa_decode_weights_workspace_bytes(_c.byref(desc)), q.device, stream, raw)
+        T, _WS_WEIGHTS, lib.pa_decode_weights_workspace_bytes(_c.byref(desc)), q.device, stream, raw)
     st = lib.pa_paged_attention_decode_weights(
         _c.byref(desc), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
         None if weight_rows is None else weight_rows.data_ptr(), nr, width, out.data_ptr(), ws, ws_bytes,
-        _err_ptr(err_flag, dev), raw)
+        _err_ptr(err_flag, dev, T.i32), raw)
     if st:
         _check(st, "pa_paged_attention_decode_weights")
     return out, weights_out
@@ -834,8 +844,8 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
     largest weights among them, compacted into dst_tables' blocks (None: in
     place; see pagedattn.h); returns (kept [num_seqs][Hkv][max_keep_len],
     new_lens [num_seqs])."""
-    import torch
-    bf, i32, dev = torch.bfloat16, torch.int32, _current_device()
+    T = _T or _torch()
+    bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4), (block_tables, "block_tables", i32, 2),
          (context_lens, "context_lens", i32, 1), (keep_lens, "keep_lens", i32, 1))
     (nblk, hkv, bs, d), (S,), (brows, mb), mk = k_pool.shape, context_lens.shape, block_tables.shape, int(max_keep_len)
@@ -852,22 +862,22 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
             _bad(f"dst_tables must be [{S}][{mb}], as wide as block_tables")
         dst = dst_tables.data_ptr()
     if kept is None:
-        kept = _new((S, hkv, mk), i32, k_pool.device, stream)
+        kept = _new(T, (S, hkv, mk), i32, k_pool.device, stream)
     if new_lens is None:
-        new_lens = _new((S,), i32, k_pool.device, stream)
+        new_lens = _new(T, (S,), i32, k_pool.device, stream)
     _all(dev, (kept, "kept", i32, 3), (new_lens, "new_lens", i32, 1))
     if kept.shape != (S, hkv, mk) or new_lens.shape[0] != S:
         _bad(f"kept must be [{S}][{hkv}][{mk}] and new_lens [{S}]")
     if S and new_lens.data_ptr() == context_lens.data_ptr():
         _bad("new_lens must not be context_lens")
     most = mb * bs if max_context_len is None else int(max_context_len)
-    weights_out, nr, width = _weight_args(weights, weights_out, weight_rows, S, hkv, most, dev)
+    weights_out, nr, width = _weight_args(T, weights, weights_out, weight_rows, S, hkv, most, dev)
     desc = DecodeDesc(S, hkv, hkv, d, bs, nblk, mb, most, 1.0)
-    st = load().pa_evict_tokens(_c.byref(desc), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), dst,
+    st = (_LIB or load()).pa_evict_tokens(_c.byref(desc), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), dst,
                                 context_lens.data_ptr(), keep_lens.data_ptr(), mk, int(sink_tokens),
                                 int(recent_tokens), weights.data_ptr(), weights_out.data_ptr(),
                                 None if weight_rows is None else weight_rows.data_ptr(), nr, width, kept.data_ptr(),
-                                new_lens.data_ptr(), _err_ptr(err_flag, dev), _raw_stream(stream, dev))
+                                new_lens.data_ptr(), _err_ptr(err_flag, dev, T.i32), T.stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "pa_evict_tokens")
     return kept, new_lens

@@ -107,6 +107,10 @@ struct DecodeSmem {
   static constexpr int kMetaOff = kStageOff + 2 * D * 2;  // GRP: per page, owner + 1 << 24 | logical block
   static constexpr int kBytes = kMetaOff + kMaxPartPages * 4;
   static constexpr int kAlloc = kBytes + 1024;  // base re-aligned to 1024 in the kernel
+  // CL: behind all that, the part's result for the cluster: o [16][D], m [16], l [16], lw [16]
+  static constexpr int kPartOff = (kBytes + 15) & ~15;
+  static constexpr int kPartBytes = (16 * D + 3 * 16) * 4;
+  static constexpr int kAllocCl = kPartOff + kPartBytes + 1024;
 };
 
 // Length class of a sequence for longest-first ordering: quarter-octave
@@ -185,14 +189,17 @@ __device__ int seq_of_rank(int r, const int32_t *ctx, int S, int B, int max_bloc
 // barrier `bar` for its own NW * 32 threads.  The decode kernel runs one unit
 // per CTA; the mixed-step kernel runs several side by side in one CTA.
 // SEL attends the blocks of a list instead of the whole context; WTS also
-// leaves the logits and softmax statistics for the attention weights.
+// leaves the logits and softmax statistics for the attention weights.  CL: the
+// parts of a (sequence, kv head) are the CTAs of a cluster (launched with
+// max_parts along x), and join through one another's shared memory instead of
+// the workspace: no fence, no counter, no second trip to L2.
 template <int D, int B, int NT, int NW, int NST, bool PRE, bool APP, bool GRP = false, bool TMA3 = false,
-          bool SEL = false, bool WTS = false>
+          bool SEL = false, bool WTS = false, bool CL = false>
 __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtensorMap *tmV, const DecodeArgs &a,
                                             int lin, int tid, uint8_t *smem, int bar) {
   using L = DecodeSmem<D, B, NW, NST>;
   static_assert(NW <= 4, "misc holds four warp totals");
-  static_assert(!(SEL || WTS) || !(PRE || APP || GRP), "block lists and weights: plain decode only");
+  static_assert(!(SEL || WTS || CL) || !(PRE || APP || GRP), "block lists and weights: plain decode only");
   constexpr int KS = D / 16;  // k-steps of S^T = K Q^T
   constexpr int MT = B / 16;  // 16-token tiles per page
   constexpr int DT = D / 16;  // 16-row d tiles of O^T = V^T P^T
@@ -209,8 +216,11 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   // a.lpt is set; s is the sub-group's first member.
   const int per_seq = a.max_parts * a.Hkv;
   const int rank = GRP ? lin / a.Hkv : lin / per_seq;
-  const int part = GRP ? 0 : (lin - rank * per_seq) / a.Hkv;
-  const int kvh = GRP ? lin - rank * a.Hkv : lin - rank * per_seq - part * a.Hkv;
+  // CL: the parts of one kv head follow one another (a cluster)
+  const int part = GRP ? 0 : CL ? (lin - rank * per_seq) % a.max_parts : (lin - rank * per_seq) / a.Hkv;
+  const int kvh = GRP  ? lin - rank * a.Hkv
+                  : CL ? (lin - rank * per_seq) / a.max_parts
+                       : lin - rank * per_seq - part * a.Hkv;
   const bool rank_it = a.lpt && (GRP ? a.nsub : a.S) > 1;
   const int sg = GRP && rank_it
                      ? seq_of_rank<NW * 32>(rank, a.sub_shared, a.nsub, B, a.max_blocks, a.max_ctx, misc, tid, bar)
@@ -271,7 +281,9 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   const int npages = GRP ? npages_grp : bad ? 0 : SEL ? a.nsel : (ctx + B - 1) / B - kstart / B;
   const int kp0 = bad ? 0 : kstart / B;  // first page of this kernel's key range
   const int nparts = (bad || GRP) ? 1 : max(1, (npages + a.part_pages - 1) / a.part_pages);
-  if (part >= nparts) return;
+  if (part >= nparts) {  // CL: the others neither read this CTA's part nor wait for it once it has left
+    return;
+  }
   __nv_bfloat16 *out_base = a.out + ((size_t)s * a.Hq + (size_t)kvh * G) * D;
   if (bad) {
     if (GRP) {
@@ -330,6 +342,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   uint8_t *ring = smem + warp * NST * L::kSlotBytes;
   const int nmine = np > warp ? (np - warp + NW - 1) / NW : 0;
   const uint64_t pol = policy_evict_first();
+  const uint64_t keep = WTS ? policy_evict_last() : 0;  // the logits, until the second pass has read them
   auto issue = [&](int i) {  // lane 0: gather local page i of this warp into its slot
     const int pg = tbl[warp + i * NW];
     uint64_t *bar = &my_bars[i % NST];
@@ -528,7 +541,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           t[nt][1] = fmaxf(t[nt][1], fmaxf(sc[mt][nt][1], sc[mt][nt][3]));
         }
       }
-      if constexpr (WTS) {  // a token's G logits lie together: a store covers 8 tokens' rows
+      if constexpr (WTS) {  // a token's G logits lie together: a store covers 8 tokens' rows; kept in L2 for the second pass
         float *lg = a.logits + ((size_t)s * a.Hkv + kvh) * a.max_ctx * G;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -541,7 +554,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
               if (j + 8 * e < octx) {
                 float *to = lg + (size_t)(j + 8 * e) * G + g;
                 if (g + 1 < G && (G & 1) == 0)
-                  *reinterpret_cast<float2 *>(to) = make_float2(sc[mt][nt][2 * e], sc[mt][nt][2 * e + 1]);
+                  store2_hint(to, sc[mt][nt][2 * e], sc[mt][nt][2 * e + 1], keep);
                 else {
                   if (g < G) to[0] = sc[mt][nt][2 * e];
                   if (g + 1 < G) to[1] = sc[mt][nt][2 * e + 1];
@@ -721,8 +734,10 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 #pragma unroll
         for (int w = 0; w < NW; ++w) l += red_lw[w * 16 + tid] * exp2f(red_m[w * 16 + tid] - mx);
       }
-      if (split)
+      if (split && !CL)
         a.ws_lw[(unit * a.max_parts + part) * G + tid] = l;
+      else if (split)
+        reinterpret_cast<float *>(smem + L::kPartOff)[16 * D + 32 + tid] = l;
       else
         a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
             mx != -INFINITY ? make_float2(mx, 1.f / l) : make_float2(0.f, 0.f);
@@ -807,6 +822,13 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
         a.out[row_of(g) * D + d] = __float2bfloat16(res);
       else
         out_base[idx] = __float2bfloat16(res);
+    } else if constexpr (CL) {
+      float *mine = reinterpret_cast<float *>(smem + L::kPartOff);
+      mine[idx] = l > 0.f ? acc / l : 0.f;
+      if (d == 0) {
+        mine[16 * D + g] = mx;
+        mine[16 * D + 16 + g] = l;
+      }
     } else {
       const size_t u = (unit * a.max_parts + part) * G + g;
       a.ws_o[u * D + d] = l > 0.f ? acc / l : 0.f;
@@ -817,6 +839,44 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
     }
   }
   if (!split) return;
+
+  if constexpr (CL) {
+    // ---- split-K in a cluster: every part joins a share of the outputs
+    cluster_arrive();
+    cluster_wait();
+    const uint32_t base = smem_u32(smem + L::kPartOff);
+    if (tid < G) {
+      float M = -INFINITY, den = 0.f, lw = 0.f;
+      for (int p = 0; p < nparts; ++p) {
+        const uint32_t at = cluster_addr(base, p) + (16 * D + tid) * 4;
+        const float m = cluster_load(at), l = cluster_load(at + 64);
+        if (l > 0.f) M = fmaxf(M, m);
+      }
+      for (int p = 0; p < nparts; ++p) {
+        const uint32_t at = cluster_addr(base, p) + (16 * D + tid) * 4;
+        const float m = cluster_load(at), l = cluster_load(at + 64);
+        const float w = l > 0.f ? l * exp2f(m - M) : 0.f;
+        wts[p * 16 + tid] = w;
+        den += w;
+        if (WTS && m != -INFINITY) lw += cluster_load(at + 128) * exp2f(m - M);
+      }
+      const float inv = den > 0.f ? 1.f / den : 0.f;
+      for (int p = 0; p < nparts; ++p) wts[p * 16 + tid] *= inv;
+      if (WTS && part == 0)
+        a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
+            M != -INFINITY ? make_float2(M, 1.f / lw) : make_float2(0.f, 0.f);
+    }
+    unit_sync<NW * 32>(bar);
+    for (int idx = part * (NW * 32) + tid; idx < G * D; idx += nparts * (NW * 32)) {
+      const int g = idx / D;
+      float acc = 0.f;
+      for (int p = 0; p < nparts; ++p) acc += wts[p * 16 + g] * cluster_load(cluster_addr(base, p) + idx * 4);
+      out_base[idx] = __float2bfloat16(acc);
+    }
+    cluster_arrive();  // nobody leaves while its part is being read
+    cluster_wait();
+    return;
+  }
 
   // ---- split-K: the last part of this (sequence, kv head) merges all parts
   __threadfence();
@@ -877,6 +937,33 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
     out_base[idx] = __float2bfloat16(acc);
   }
   if (tid == 0) a.ws_cnt[unit] = 0ull;
+}
+
+// Host: launches a decode kernel over grid (parts, kv heads, sequences): as one
+// cluster a (sequence, kv head) when a context has 2 .. 8 parts (`in_cluster`,
+// with smem_cl bytes of shared memory), else `plain`, joined through the
+// workspace.
+constexpr int kMaxClusterParts = 8;
+template <class K>
+int launch_parts(K plain, K in_cluster, int smem, int smem_cl, dim3 grid, int threads, const CUtensorMap &tk,
+                 const CUtensorMap &tv, const DecodeArgs &a, cudaStream_t st) {
+  const bool cl = grid.x > 1 && grid.x <= kMaxClusterParts;
+  K kern = cl ? in_cluster : plain;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = cl ? smem_cl : smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = grid.x;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cl ? 1 : 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, tk, tv, a));
 }
 
 // Host: the argument block of a decode launch over a validated desc with

@@ -23,25 +23,22 @@
 namespace pa {
 namespace {
 
-template <int D, int B, int NT, int NST>
+template <int D, int B, int NT, int NST, bool CL>
 __global__ void __launch_bounds__(128)
     sparse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int lin = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
-  decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, true, false>(&tmK, &tmV, a, lin, threadIdx.x, smem, 0);
+  const int lin = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, true, false, CL>(&tmK, &tmV, a, lin, threadIdx.x, smem,
+                                                                                0);
 }
 
 template <int D, int B, int NT>
 int launch_sparse(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
   constexpr int NST = B == 16 ? 2 : 1;
-  using L = DecodeSmem<D, B, 4, NST>;
-  auto kern = sparse_kernel<D, B, NT, NST>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
-    return PA_ERR_CUDA;
-  kern<<<grid, 128, L::kAlloc, st>>>(tk, tv, a);
-  return launch_status(cudaGetLastError());
+  return launch_parts(sparse_kernel<D, B, NT, NST, false>, sparse_kernel<D, B, NT, NST, true>,
+                      DecodeSmem<D, B, 4, NST>::kAlloc, DecodeSmem<D, B, 4, NST>::kAllocCl, grid, 128, tk, tv, a, st);
 }
 
 // The desc whose split plan a list of num_select blocks takes.

@@ -26,15 +26,16 @@
 namespace pa {
 namespace {
 
-template <int D, int B, int NT, int NST>
+template <int D, int B, int NT, int NST, bool CL>
 __global__ void __launch_bounds__(128)
     decode_logits_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   grid_launch_dependents();
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int lin = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
-  decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, false, true>(&tmK, &tmV, a, lin, threadIdx.x, smem, 0);
+  const int lin = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, false, true, CL>(&tmK, &tmV, a, lin, threadIdx.x, smem,
+                                                                                0);
 }
 
 struct WeightArgs {
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
   bool any[kWPer];
 #pragma unroll
   for (int i = 0; i < kWPer; ++i) acc[i] = 0.f, any[i] = false;
+  const uint64_t done = policy_evict_first();  // the logits leave L2 first once read
   const int words = a.rows ? (a.S + 31) / 32 : 1;
   int flip = 0;
   for (int w = 0; w < words; ++w) {
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
 #pragma unroll
         for (int i = 0; i < kWPer; ++i) {
           const int j = j0 + i * kWThreads + tid;
-          if (j < ctx) x[i] = __ldcs(lg + ((size_t)j * a.G + g) / V);
+          if (j < ctx) x[i] = load_hint(lg + ((size_t)j * a.G + g) / V, done);
         }
 #pragma unroll
         for (int i = 0; i < kWPer; ++i)
@@ -158,20 +160,24 @@ WeightPlan make_plan(const pa_decode_desc *d, int sms) {
   return p;
 }
 
-template <int D, int B, int NT>
+template <int D, int B, int NT, int NST>
 int launch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
-  constexpr int NST = B == 16 ? 3 : 1;
-  using L = DecodeSmem<D, B, 4, NST>;
-  auto kern = decode_logits_kernel<D, B, NT, NST>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
-    return PA_ERR_CUDA;
-  kern<<<grid, 128, L::kAlloc, st>>>(tk, tv, a);
-  return launch_status(cudaGetLastError());
+  return launch_parts(decode_logits_kernel<D, B, NT, NST, false>, decode_logits_kernel<D, B, NT, NST, true>,
+                      DecodeSmem<D, B, 4, NST>::kAlloc, DecodeSmem<D, B, 4, NST>::kAllocCl, grid, 128, tk, tv, a, st);
 }
 
+// Slots of a warp as in the plain decode: 16-token pages two when the units fit
+// one wave, else three; 32-token pages one.
 template <int D, int B>
-int dispatch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
-  return a.G <= 8 ? launch_logits<D, B, 1>(tk, tv, a, grid, st) : launch_logits<D, B, 2>(tk, tv, a, grid, st);
+int dispatch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, int sms,
+                    cudaStream_t st) {
+  if constexpr (B == 16) {
+    if (a.G <= 8 && (long long)grid.x * grid.y * grid.z <= 2ll * sms)
+      return launch_logits<D, B, 1, 2>(tk, tv, a, grid, st);
+    return a.G <= 8 ? launch_logits<D, B, 1, 3>(tk, tv, a, grid, st) : launch_logits<D, B, 2, 3>(tk, tv, a, grid, st);
+  } else {
+    return a.G <= 8 ? launch_logits<D, B, 1, 1>(tk, tv, a, grid, st) : launch_logits<D, B, 2, 1>(tk, tv, a, grid, st);
+  }
 }
 
 }  // namespace
@@ -216,10 +222,10 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   a.logits = reinterpret_cast<float *>(ws + plan.lw + plan.stats);
   const dim3 grid(plan.split.max_parts, d->num_kv_heads, d->num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(tk, tv, a, grid, s)
-                                                           : dispatch_logits<128, 32>(tk, tv, a, grid, s))
-                                    : (d->block_size == 16 ? dispatch_logits<64, 16>(tk, tv, a, grid, s)
-                                                           : dispatch_logits<64, 32>(tk, tv, a, grid, s));
+  const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(tk, tv, a, grid, sms, s)
+                                                           : dispatch_logits<128, 32>(tk, tv, a, grid, sms, s))
+                                    : (d->block_size == 16 ? dispatch_logits<64, 16>(tk, tv, a, grid, sms, s)
+                                                           : dispatch_logits<64, 32>(tk, tv, a, grid, sms, s));
   if (st != PA_OK) return st;
   if (d->max_context_len == 0) return PA_OK;
   WeightArgs w{};

@@ -92,13 +92,13 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ----------------------------------------------------------------- clusters
-// Barrier of every thread of the cluster, in two halves: writes before the
-// arrival are seen behind the wait.
+// Barrier of every thread of the cluster that has not exited, in two halves:
+// writes before the arrival are seen behind the wait.
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 // The shared-memory address of CTA `rank` of the cluster that corresponds to
 // this CTA's `addr`.
@@ -109,6 +109,42 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// --------------------------------------------------------- L2 eviction hints
+__device__ __forceinline__ uint64_t policy_evict_last() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void store2_hint(float *to, float x, float y, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1,%2}, %3;" ::"l"(to), "f"(x), "f"(y), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ float load_hint(const float *from, uint64_t policy) {
+  float v;
+  asm volatile("ld.global.L2::cache_hint.f32 %0, [%1], %2;" : "=f"(v) : "l"(from), "l"(policy) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 load_hint(const float2 *from, uint64_t policy) {
+  float2 v;
+  asm volatile("ld.global.L2::cache_hint.v2.f32 {%0,%1}, [%2], %3;" : "=f"(v.x), "=f"(v.y) : "l"(from), "l"(policy)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_hint(const float4 *from, uint64_t policy) {
+  float4 v;
+  asm volatile("ld.global.L2::cache_hint.v4.f32 {%0,%1,%2,%3}, [%4], %5;"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(from), "l"(policy)
+               : "memory");
+  return v;
 }
 
 // ------------------------------------------------------ warp MMA (m16n8k16)

@@ -1,7 +1,6 @@
 """Block-sparse decode and eviction: every refusal that needs no GPU, by the
 C calls (before any launch) and by the binding, and the wrappers' marshalling
 against a recording stand-in for the library."""
-import contextlib
 import ctypes
 
 import pytest
@@ -106,6 +105,8 @@ def test_workspaces_are_checked(lib):
 
 
 class _Lib:
+    capturing = False
+
     def __init__(self):
         self.calls = []
 
@@ -124,27 +125,25 @@ def fake(monkeypatch):
     from paged_kv_cache_262_gb300 import _binding as b
     lib = _Lib()
 
-    class S:
-        cuda_stream = 7
-
     def need(t, dtype, name, ndim=None):  # _need without the device check
         if t.dtype != dtype:
             raise TypeError(name)
         if not t.is_contiguous() or (ndim is not None and t.dim() != ndim):
             raise ValueError(name)
 
-    monkeypatch.setattr(b, "load", lambda path=None: lib)
+    T = b._Torch()
+    T.device = lambda: -1  # a host tensor's get_device()
+    T.stream = lambda device: 7
+    T.capturing = lambda: lib.capturing
+    T.empty = lambda *a, **k: torch.empty(*a, **{x: y for x, y in k.items() if x != "device"})
+    monkeypatch.setattr(b, "_T", T)
+    monkeypatch.setattr(b, "_LIB", lib)
     monkeypatch.setattr(b, "_need", need)
-    monkeypatch.setattr(b, "_current_device", lambda: -1)  # a host tensor's get_device()
-    monkeypatch.setattr(b, "_raw_stream", lambda stream, device: 7 if stream is None else stream.cuda_stream)
     monkeypatch.setattr(b, "_ws", lambda w: None if w is None else w.data_ptr())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: S())
-    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: lib.capturing)
-    real_empty = torch.empty
-    monkeypatch.setattr(torch, "empty", lambda *a, **k: real_empty(*a, **{x: y for x, y in k.items() if x != "device"}))
+    monkeypatch.setattr(b, "_cached_ws", lambda cache, n, device, stream: cache.setdefault(
+        (device.index, 7), torch.empty(n, dtype=torch.uint8)))
     lib.capturing = False
+    lib.T = T
     lib.caches = {}
     for name in ("_WS_SELECT", "_WS_SPARSE", "_WS_WEIGHTS"):
         lib.caches[name] = {}
@@ -250,7 +249,9 @@ def test_wrappers_refuse_host_tensors(monkeypatch):
     import torch
     t = _tensors()
     from paged_kv_cache_262_gb300 import _binding as b
-    monkeypatch.setattr(b, "_current_device", lambda: 0)
+    T = b._Torch()
+    T.device = lambda: 0
+    monkeypatch.setattr(b, "_T", T)
     with pytest.raises(TypeError):
         pa.block_key_bounds(t["kp"], t["bounds"], t["bt"], t["ctx"])
     with pytest.raises(TypeError):
@@ -262,12 +263,11 @@ def test_wrappers_refuse_host_tensors(monkeypatch):
     assert isinstance(t["q"], torch.Tensor)
 
 
-def test_wrappers_refuse_what_is_no_tensor_or_on_another_device(fake, monkeypatch):
-    from paged_kv_cache_262_gb300 import _binding as b
+def test_wrappers_refuse_what_is_no_tensor_or_on_another_device(fake):
     t = _tensors()
     with pytest.raises((TypeError, AttributeError)):
         pa.block_key_bounds(t["kp"], t["bounds"], t["bt"].tolist(), t["ctx"])
-    monkeypatch.setattr(b, "_current_device", lambda: 1)
+    fake.T.device = lambda: 1
     for call in (lambda: pa.block_key_bounds(t["kp"], t["bounds"], t["bt"], t["ctx"]),
                  lambda: pa.select_blocks(t["q"], t["bounds"], t["bt"], t["ctx"], 3, block_size=16),
                  lambda: pa.paged_attention_decode_sparse(t["q"], t["kp"], t["vp"], t["bt"], t["ctx"], t["sel"]),
