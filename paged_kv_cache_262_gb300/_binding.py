@@ -595,6 +595,29 @@ def swap_blocks(src_k_pools: Sequence, src_v_pools: Sequence, dst_k_pools: Seque
 # is a few attribute reads, and the messages are made only when one fails.
 _WS_SELECT, _WS_SPARSE, _WS_WEIGHTS = {}, {}, {}
 _T = None  # what the calls use of torch, looked up once
+# The quick way (fastcall/): a call's common form in one C call, which returns
+# None whenever something is not as it must be or not as it handles; the
+# Python below is the whole of every call and says what is wrong.
+_FAST = None  # the module; False without it
+
+
+def _fast():
+    global _FAST
+    _FAST = False
+    if os.path.exists(_build.FAST):
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries first)
+        lib = load()
+        loader = importlib.machinery.ExtensionFileLoader("_pa_fastcall", _build.FAST)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_fastcall", loader))
+        loader.exec_module(mod)
+        mod.bind(*(_c.cast(getattr(lib, n), _P).value for n in (
+            "pa_block_key_bounds", "pa_select_blocks_workspace_bytes", "pa_select_blocks",
+            "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
+            "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens")))
+        _FAST = mod
+    return _FAST
 
 
 class _Torch:
@@ -709,6 +732,10 @@ def block_key_bounds(k_pool, bounds, block_tables, context_lens, start_lens=None
     """Writes the channel-wise minimum and maximum of the keys of every block
     from start_lens[s] on into bounds [num_blocks][Hkv][2][D] (see
     pagedattn.h); returns bounds."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and stream is None and F.bounds(k_pool, bounds, block_tables, context_lens, start_lens, max_new_tokens,
+                                         max_context_len, err_flag):
+        return bounds
     T = _T or _torch()
     bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (k_pool, "k_pool", bf, 4), (bounds, "bounds", bf, 4), (block_tables, "block_tables", i32, 2),
@@ -739,6 +766,12 @@ def select_blocks(q, bounds, block_tables, context_lens, num_select, *, block_si
                   selected=None, max_context_len=None, workspace=None, err_flag=None, stream=None):
     """The logical blocks each (sequence, kv head) attends this step, int32
     [num_seqs][Hkv][num_select], increasing, then -1 (see pagedattn.h)."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and selected is None and workspace is None and stream is None:
+        r = F.select(q, bounds, block_tables, context_lens, num_select, block_size, sink_blocks, recent_blocks,
+                     max_context_len, err_flag, _WS_SELECT)
+        if r is not None:
+            return r
     T = _T or _torch()
     bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (q, "q", bf, 3), (bounds, "bounds", bf, 4), (block_tables, "block_tables", i32, 2),
@@ -795,6 +828,12 @@ def paged_attention_decode_sparse(q, k_pool, v_pool, block_tables, context_lens,
                                   max_context_len=None, workspace=None, err_flag=None, stream=None):
     """Decode attention over the listed blocks of every (sequence, kv head)
     (see pagedattn.h)."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and out is None and workspace is None and stream is None:
+        r = F.sparse(q, k_pool, v_pool, block_tables, context_lens, selected, scale, max_context_len, err_flag,
+                     _WS_SPARSE)
+        if r is not None:
+            return r
     T = _T or _torch()
     dev = T.device()
     out, desc = _decode_args(T, q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
@@ -819,6 +858,12 @@ def paged_attention_decode_weights(q, k_pool, v_pool, block_tables, context_lens
     """Decode attention that adds every key's attention weight to `weights`
     [num_rows][Hkv][max_tokens] (in place, or into weights_out; see
     pagedattn.h); returns (out, weights_out)."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and out is None and workspace is None and stream is None:
+        r = F.weights(q, k_pool, v_pool, block_tables, context_lens, weights, weights_out, weight_rows, scale,
+                      max_context_len, err_flag, _WS_WEIGHTS)
+        if r is not None:
+            return r, weights if weights_out is None else weights_out
     T = _T or _torch()
     dev = T.device()
     out, desc = _decode_args(T, q, k_pool, v_pool, block_tables, context_lens, out, scale, max_context_len, dev, stream)
@@ -844,6 +889,12 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
     largest weights among them, compacted into dst_tables' blocks (None: in
     place; see pagedattn.h); returns (kept [num_seqs][Hkv][max_keep_len],
     new_lens [num_seqs])."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and kept is None and new_lens is None and stream is None:
+        r = F.evict(k_pool, v_pool, block_tables, context_lens, keep_lens, weights, max_keep_len, sink_tokens,
+                    recent_tokens, dst_tables, weights_out, weight_rows, max_context_len, err_flag)
+        if r is not None:
+            return r
     T = _T or _torch()
     bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4), (block_tables, "block_tables", i32, 2),

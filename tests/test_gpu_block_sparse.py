@@ -395,3 +395,68 @@ def test_offsets_beyond_32_bits(torch):
         res.append((b[-n:], sel, pa.paged_attention_decode_sparse(q, k, v, t, c["ctx"], sel, max_context_len=100)))
     assert same_bits(torch, res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
     assert same_bits(torch, res[0][2], res[1][2])
+
+
+# ------------------------------------------------- the two ways into the calls
+def test_both_ways_into_the_calls_agree(torch, monkeypatch):
+    """Every call by the extension module and by the Python beside it: the
+    same bits, the same refusals; the extension module was built here and
+    takes the common form."""
+    from paged_kv_cache_262_gb300 import _binding as b
+    R = _ref()
+    F = b._FAST if b._FAST is not None else b._fast()
+    assert F, "the extension module is not built"
+    c = R.make_cache([700, 33, 1], 2, 128, 16, seed=71)
+    q = torch.randn(3, 8, 128, device="cuda").to(torch.bfloat16)
+    keep = torch.tensor([300, 20, 5], dtype=torch.int32, device="cuda")
+    w0 = torch.rand(3, 2, c["mb"] * 16, device="cuda")
+    rows = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    k0, v0 = c["k"].clone(), c["v"].clone()
+
+    def all_calls():
+        c["k"].copy_(k0), c["v"].copy_(v0)
+        w, err = w0.clone(), err_of(torch)
+        bd = torch.zeros(k0.shape[0], 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+        pa.block_key_bounds(c["k"], bd, c["bt"], c["ctx"], c["ctx"] - 1, max_new_tokens=1, err_flag=err)
+        pa.block_key_bounds(c["k"], bd, c["bt"], c["ctx"])
+        sel = pa.select_blocks(q, bd, c["bt"], c["ctx"], 5, block_size=16, sink_blocks=2, recent_blocks=1,
+                               max_context_len=700, err_flag=err)
+        o1 = pa.paged_attention_decode_sparse(q, c["k"], c["v"], c["bt"], c["ctx"], sel, scale=0.125)
+        o2, w2 = pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w, weight_rows=rows,
+                                                   max_context_len=700, err_flag=err)
+        assert w2 is w
+        o3, w3 = pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w,
+                                                   weights_out=torch.zeros_like(w))
+        kept, new = pa.evict_tokens(c["k"], c["v"], c["bt"], c["ctx"], keep, w, max_keep_len=300, sink_tokens=1,
+                                    recent_tokens=2, weight_rows=rows, err_flag=err)
+        assert int(err) == 0
+        return [bd, sel, o1, o2, o3, w3, kept, new, w, c["k"].clone(), c["v"].clone()]
+
+    def refusals():
+        got = []
+        for f in (lambda: pa.block_key_bounds(c["k"], w0, c["bt"], c["ctx"]),
+                  lambda: pa.block_key_bounds(c["k"], torch.zeros_like(c["k"]), c["bt"], c["ctx"]),
+                  lambda: pa.select_blocks(q, torch.zeros(9, 2, 2, 64, dtype=torch.bfloat16, device="cuda"), c["bt"],
+                                           c["ctx"], 5, block_size=16),
+                  lambda: pa.select_blocks(q, torch.zeros(9, 2, 2, 128, dtype=torch.bfloat16, device="cuda"), c["bt"],
+                                           c["ctx"], 5, block_size=8),
+                  lambda: pa.select_blocks(q, torch.zeros(9, 2, 2, 128, dtype=torch.bfloat16, device="cuda"), c["bt"],
+                                           c["ctx"], 2, block_size=16, sink_blocks=2),
+                  lambda: pa.paged_attention_decode_sparse(q, c["k"], c["v"][:-1], c["bt"], c["ctx"], rows),
+                  lambda: pa.paged_attention_decode_sparse(q, c["k"], c["v"], c["bt"], c["ctx"].cpu(),
+                                                           torch.zeros(3, 2, 4, dtype=torch.int32, device="cuda")),
+                  lambda: pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w0[:2]),
+                  lambda: pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w0[:, :, ::2]),
+                  lambda: pa.evict_tokens(c["k"], c["v"], c["bt"], c["ctx"], keep, w0, max_keep_len=0),
+                  lambda: pa.evict_tokens(c["k"], c["v"], c["bt"], c["ctx"], keep, w0, max_keep_len=8,
+                                          sink_tokens=-1)):
+            with pytest.raises((TypeError, ValueError, pa.PaError)) as e:
+                f()
+            got.append((type(e.value), str(e.value)))
+        return got
+
+    quick, said = all_calls(), refusals()
+    assert F.sparse(q, c["k"], c["v"], c["bt"], c["ctx"], quick[1], None, None, None, b._WS_SPARSE) is not None
+    monkeypatch.setattr(b, "_FAST", False)
+    assert all(torch.equal(x, y) for x, y in zip(quick, all_calls()))
+    assert said == refusals()

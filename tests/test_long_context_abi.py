@@ -137,6 +137,7 @@ def fake(monkeypatch):
     T.capturing = lambda: lib.capturing
     T.empty = lambda *a, **k: torch.empty(*a, **{x: y for x, y in k.items() if x != "device"})
     monkeypatch.setattr(b, "_T", T)
+    monkeypatch.setattr(b, "_FAST", False)
     monkeypatch.setattr(b, "_LIB", lib)
     monkeypatch.setattr(b, "_need", need)
     monkeypatch.setattr(b, "_ws", lambda w: None if w is None else w.data_ptr())
@@ -274,3 +275,28 @@ def test_wrappers_refuse_what_is_no_tensor_or_on_another_device(fake):
                  lambda: pa.paged_attention_decode_weights(t["q"], t["kp"], t["vp"], t["bt"], t["ctx"], t["w"]),
                  lambda: pa.evict_tokens(t["kp"], t["vp"], t["bt"], t["ctx"], t["keep"], t["w"], max_keep_len=8)):
         _refused(fake, ValueError, call)
+
+
+def test_the_quick_way_leaves_everything_unusual_to_the_other(lib):
+    """The extension module, where it is built: None, without a launch and
+    without an error, for host tensors, for what is no tensor, for a wrong
+    number of arguments -- and for anything at all where there is no GPU."""
+    from paged_kv_cache_262_gb300 import _binding as b
+    F = b._FAST if b._FAST is not None else b._fast()
+    if not F:
+        pytest.skip("the extension module is not built")
+    t = _tensors()
+    calls = [(F.bounds, (t["kp"], t["bounds"], t["bt"], t["ctx"], None, None, None, None)),
+             (F.select, (t["q"], t["bounds"], t["bt"], t["ctx"], 3, 16, 1, 1, None, None, {})),
+             (F.sparse, (t["q"], t["kp"], t["vp"], t["bt"], t["ctx"], t["sel"], None, None, None, {})),
+             (F.weights, (t["q"], t["kp"], t["vp"], t["bt"], t["ctx"], t["w"], None, None, None, None, None, {})),
+             (F.evict, (t["kp"], t["vp"], t["bt"], t["ctx"], t["keep"], t["w"], 8, 0, 0, None, None, None, None,
+                        None))]
+    for f, args in calls:
+        assert f(*args) is None
+        assert f(*args[:-1]) is None and f() is None
+        for i in range(len(args)):
+            for x in (None, "q", 1.5, [1], 2**40, -2**40, object()):
+                assert f(*args[:i], x, *args[i + 1:]) is None
+    with pytest.raises(TypeError):
+        F.bind(1, 2)
