@@ -116,9 +116,11 @@ struct RowSelect {
   uint4 keys[kSelKeys / 4];
   unsigned long long ex[kSelRefine];
   int exi[kSelRefine];
-  float span[8];  // a CTA of the cluster each
+  float span[8];              // a CTA of the cluster each:
+  uint32_t least[8], most[8];  // its least and largest key
   float mx[SW];
-  int nex, ngt, last;
+  uint32_t wl[SW], wm[SW];
+  int nex, last;
 };
 
 // A block's score in 64 bits as an ordered key, by one warp: every product of
@@ -188,9 +190,11 @@ template <int D>
 constexpr float kScoreError = 18.f * (2 * D / 16) * 1.1920929e-07f * 1.001f;
 
 // One CTA selects a row's blocks from its keys (in r.keys, or past kSelKeys of
-// them in the workspace), A the row's largest absolute sum.
+// them in the workspace), A the row's largest absolute sum; least and most: the
+// least and largest key of some of them, all among the threads.
 template <int D, int NT, int SW, bool LONG>
-__device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, int s, int h, int n, float A, int tid) {
+__device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, int s, int h, int n, float A,
+                           uint32_t least, uint32_t most, int tid) {
   constexpr int kThreads = SW * 32;
   const int lane = tid & 31, warp = tid >> 5;
   const int first = a.sink, end = n - a.recent;
@@ -210,37 +214,54 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
   const float slack = 2.f * kScoreError<D> * A;
   const bool finite = slack < INFINITY;  // false for NaN too: then no fp32 score is trusted
   uint32_t lo = 0u, hi = 0xfffffffeu;    // (no score's key is above it)
+  int above = 0;
   if (finite) {
-    uint32_t least = ~0u, most = 0u;
-    for_keys<kThreads, uint32_t>(key4, N, tid, [&](int, uint32_t k) {
-      least = min(least, k);
-      most = max(most, k);
-    });
-    const uint32_t t = kth_largest<kThreads, uint32_t>(key4, N, want, r.sm, tid, least, most).key;
-    if (t != 0u) {
-      const float v = key_value(t);
+    const Kth<uint32_t> t = kth_largest<kThreads, uint32_t>(key4, N, want, r.sm, tid, least, most);
+    above = t.above;
+    if (t.key != 0u) {
+      const float v = key_value(t.key);
       lo = order_key(__fsub_rd(v, slack));
       hi = order_key(__fadd_ru(v, slack));
     } else {
       hi = 0u;  // blocks outside the pool are among the chosen: those that can be read all are
     }
   }
-  // blocks above hi are chosen whatever their rounding, those below lo are not
-  int mine = 0;
-  for_keys<kThreads, uint32_t>(key4, N, tid, [&](int i, uint32_t k) {
-    mine += k > hi;
-    if (k >= lo && k <= hi) {
-      const int at = atomicAdd(&r.nex, 1);
-      if (at < kSelRefine) r.exi[at] = i;
-    }
-  });
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0 && mine) atomicAdd(&r.ngt, mine);
-  __syncthreads();
-  const int near_ = r.nex, need = want - r.ngt;
   auto emit = [&](int pos, int i, uint32_t) { out[a.sink + pos] = first + i; };
-  if (near_ == need || hi == 0u) {  // (of blocks outside the pool, the first)
-    take_above<kThreads, uint32_t>(key4, key1, N, hi == 0u ? 0u : lo - 1u, hi == 0u ? need : 0, want, r.sm, tid, emit);
+  if (hi == 0u) {  // (of blocks outside the pool, the first)
+    take_above<kThreads, uint32_t>(key4, key1, N, 0u, want - above, want, r.sm, tid, emit);
+    return;
+  }
+  // blocks above hi are chosen whatever their rounding, those below lo are not:
+  // a count of either kind for each warp's stretch, and a list of those between
+  const Stretch<kThreads> w(N, warp);
+  int gt = 0, nr = 0;
+#pragma unroll 2
+  for (int i = w.beg + 4 * lane; i < w.end; i += 128) {
+    const Keys4<uint32_t> k = key4(i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i + e >= w.end || k.v[e] < lo) continue;
+      if (k.v[e] > hi) {
+        ++gt;
+      } else {
+        ++nr;
+        const int at = atomicAdd(&r.nex, 1);
+        if (at < kSelRefine) r.exi[at] = i + e;
+      }
+    }
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  nr = __reduce_add_sync(0xffffffffu, nr);
+  if (lane == 0) {
+    r.sm.a[warp] = gt;
+    r.sm.b[warp] = nr;
+  }
+  __syncthreads();
+  const int near_ = r.nex, need = want - sum_all<kThreads>(r.sm.a, lane);
+  int pos = sum_before<kThreads>(r.sm.a, lane, warp);
+  if (near_ == need) {
+    pos += sum_before<kThreads>(r.sm.b, lane, warp);
+    list_stretch<kThreads, uint32_t>(key1, w, lo, true, 0, 0, pos, want, lane, emit);
     return;
   }
   if (near_ <= kSelRefine) {  // few: their exact scores, ranked by counting
@@ -251,13 +272,21 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
       if (lane == 0) r.ex[c] = x;
     }
     __syncthreads();
-    for (int c = tid; c < near_; c += kThreads) {
-      int rank = 0;
-      for (int o = 0; o < near_; ++o) rank += r.ex[o] > r.ex[c] || (r.ex[o] == r.ex[c] && r.exi[o] < r.exi[c]);
-      keys[r.exi[c]] = rank < need ? 0xffffffffu : 0u;
+    static_assert(kSelRefine <= kThreads, "a thread a block");
+    int rank = 0;
+    if (tid < near_) {
+      const unsigned long long x = r.ex[tid];
+      const int xi = r.exi[tid];
+      for (int o = 0; o < near_; ++o) rank += r.ex[o] > x || (r.ex[o] == x && r.exi[o] < xi);
+      keys[xi] = rank < need ? 0xffffffffu : 0u;
     }
     __syncthreads();
-    take_above<kThreads, uint32_t>(key4, key1, N, hi, 0, want, r.sm, tid, emit);
+    if (tid < near_ && rank >= need) r.exi[tid] = N;  // not one of the chosen
+    __syncthreads();
+    int before = 0;  // chosen ones in the stretches before this warp's
+    for (int c = lane; c < near_; c += 32) before += r.exi[c] < w.beg;
+    pos += __reduce_add_sync(0xffffffffu, before);
+    list_stretch<kThreads, uint32_t>(key1, w, hi + 1u, true, 0, 0, pos, want, lane, emit);
     return;
   }
   // many (scores that tie in numbers, infinite bounds): 64-bit keys for all of
@@ -349,11 +378,12 @@ __global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectAr
       qf[nt][c][3] = v.w;
     }
   }
-  if (tid == 0) r.nex = r.ngt = 0;
+  if (tid == 0) r.nex = 0;
   if (clustered) cluster_wait();
   uint32_t *keys = LONG ? a.keys + row * a.stride : reinterpret_cast<uint32_t *>(r.keys);
   const uint32_t keys0 = clustered ? cluster_addr(smem_u32(r.keys), 0) : smem_u32(r.keys);
   float span = 0.f;
+  uint32_t least = ~0u, most = 0u;
   for (; i0 < i_end; i0 += 16 * SW) {
     uint4 x[2][CH];
     bool have[2];
@@ -414,6 +444,8 @@ __global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectAr
       const int i = i0 + (lane >> 2) + 8 * e;
       if ((lane & 3) == 0 && i >= first && i < i_end) {
         const uint32_t k = have[e] ? order_key(best) : 0u;
+        least = min(least, k);
+        most = max(most, k);
         if (LONG)
           keys[i - first] = k;
         else if (clustered)
@@ -423,22 +455,38 @@ __global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectAr
       }
     }
   }
+  const bool one = !LONG && !clustered;  // then the threads' own least and largest keys will do
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
   if (lane == 0) r.mx[warp] = span;
+  if (!LONG && !one) {
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) r.wl[warp] = least, r.wm[warp] = most;
+  }
   if (LONG) __threadfence();
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < SW; ++w) span = fmaxf(span, r.mx[w]);
   if (!LONG) {
     if (clustered) {
-      if (tid == 0) cluster_store(cluster_addr(smem_u32(&r.span[chunk]), 0), __float_as_uint(span));
+      if (tid == 0) {
+#pragma unroll
+        for (int w = 0; w < SW; ++w) least = min(least, r.wl[w]), most = max(most, r.wm[w]);
+        cluster_store(cluster_addr(smem_u32(&r.span[chunk]), 0), __float_as_uint(span));
+        cluster_store(cluster_addr(smem_u32(&r.least[chunk]), 0), least);
+        cluster_store(cluster_addr(smem_u32(&r.most[chunk]), 0), most);
+      }
       cluster_arrive();
       if (chunk != 0) return;
       cluster_wait();
-      for (int c = 0; c < (int)gridDim.x; ++c) span = fmaxf(span, r.span[c]);
+      for (int c = 0; c < (int)gridDim.x; ++c) {
+        span = fmaxf(span, r.span[c]);
+        least = min(least, r.least[c]);
+        most = max(most, r.most[c]);
+      }
     }
-    select_row<D, NT, SW, LONG>(a, r, row, s, h, n, span, tid);
+    select_row<D, NT, SW, LONG>(a, r, row, s, h, n, span, least, most, tid);
     return;
   }
   if (tid == 0) {
@@ -458,8 +506,14 @@ __global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectAr
   for (int c = lane; c < nchunks; c += 32) span = fmaxf(span, __ldcg(a.span + row * a.max_chunks + c));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
+  least = ~0u, most = 0u;
+  for (int i = tid; i < N; i += kThreads) {
+    const uint32_t k = __ldcg(a.keys + row * a.stride + i);
+    least = min(least, k);
+    most = max(most, k);
+  }
   __syncthreads();
-  select_row<D, NT, SW, LONG>(a, r, row, s, h, n, span, tid);
+  select_row<D, NT, SW, LONG>(a, r, row, s, h, n, span, least, most, tid);
 }
 
 // Rows of at most kSelKeys blocks: a cluster of 1, 2, 4 or 8 CTAs a row, as

@@ -171,17 +171,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
 // thread's copies of it, and of all before it, have landed; the later ones on
 // their way read at or behind their own slots, which no earlier stage writes.
 constexpr int kMvThreads = 256;
-#ifndef PA_MV_STAGES
-#define PA_MV_STAGES 3
-#endif
-#ifndef PA_MV_U
-#define PA_MV_U 4
-#endif
-#ifndef PA_MV_WAVE
-#define PA_MV_WAVE 6
-#endif
-constexpr int kMvStages = PA_MV_STAGES;
-constexpr int kMvPieces = PA_MV_U;  // pieces of a thread in a stage
+constexpr int kMvStages = 3;
+constexpr int kMvPieces = 4;     // pieces of a thread in a stage
 constexpr int kMvIndex = 2048;  // rows of list and table entries ahead and behind, in shared memory
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
@@ -306,8 +297,8 @@ template <int D>
 int launch_move(const EvictArgs &a, int sms, cudaStream_t st) {
   const int64_t units = 2ll * a.Hkv * a.S;
   if constexpr (D == 128)
-    if (4 * units >= (long long)PA_MV_WAVE * sms) return launch_move_rows<D, 256>(a, st);
-  if (units * (D / 64) * 4 >= (long long)PA_MV_WAVE * sms) return launch_move_rows<D, 128>(a, st);
+    if (4 * units >= 6ll * sms) return launch_move_rows<D, 256>(a, st);
+  if (units * (D / 64) * 4 >= 6ll * sms) return launch_move_rows<D, 128>(a, st);
   return launch_move_rows<D, 64>(a, st);
 }
 

@@ -58,6 +58,16 @@ __device__ __forceinline__ Keys4<uint32_t> keys4(uint4 x) { return Keys4<uint32_
 __device__ __forceinline__ int lead_zeros(uint32_t x) { return __clz((int)x); }
 __device__ __forceinline__ int lead_zeros(unsigned long long x) { return __clzll((long long)x); }
 
+// Sum of v[0 .. warp - 1], a value a warp of the CTA.
+template <int NT>
+__device__ __forceinline__ int sum_before(const int *v, int lane, int warp) {
+  return __reduce_add_sync(0xffffffffu, lane < warp && lane < NT / 32 ? v[lane] : 0);
+}
+template <int NT>
+__device__ __forceinline__ int sum_all(const int *v, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? v[lane] : 0);
+}
+
 // f(i, key) for every key of this thread: four consecutive ones at a time.
 template <int NT, class T, class Key4, class F>
 __device__ __forceinline__ void for_keys(Key4 key4, int n, int tid, F f) {
@@ -95,10 +105,13 @@ __device__ Kth<T> kth_largest(Key4 key4, int n, int want, SelectSmem<NT> &sm, in
   for (int i = tid; i < kBins / 4; i += NT) sm.hist[i] = make_int4(0, 0, 0, 0);
   if (tid == 0) sm.filled = 0;
   __syncthreads();
+  lo = (T)sm.lo[lane % (NT / 32)];
+  hi = (T)sm.hi[lane % (NT / 32)];
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    lo = (T)sm.lo[w] < lo ? (T)sm.lo[w] : lo;
-    hi = (T)sm.hi[w] > hi ? (T)sm.hi[w] : hi;
+  for (int o = NT / 64; o > 0; o >>= 1) {
+    const T l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+    lo = l2 < lo ? l2 : lo;
+    hi = h2 > hi ? h2 : hi;
   }
   int open = kBits - (lo == hi ? kBits : lead_zeros(lo ^ hi));  // low bits in which the keys left differ
   T base = open == kBits ? (T)0 : (hi >> open) << open;
@@ -126,8 +139,7 @@ __device__ Kth<T> kth_largest(Key4 key4, int n, int want, SelectSmem<NT> &sm, in
     }
     if (lane == 31) sm.a[warp] = incl;
     __syncthreads();
-    int run = incl - c;
-    for (int v = 0; v < warp; ++v) run += sm.a[v];
+    int run = incl - c + sum_before<NT>(sm.a, lane, warp);
     if (left > run && left <= run + c) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -174,23 +186,67 @@ __device__ Kth<T> kth_largest(Key4 key4, int n, int want, SelectSmem<NT> &sm, in
   return Kth<T>{base, above};
 }
 
-// (key1(i): one of them.)  Calls emit(position, i, key) for every key above t, and for the first need of
-// those equal to t, in increasing order of i, at most `room` of them (keys that
-// another launch overwrites meanwhile must not write past the list).  Whole
-// CTA: every warp counts its consecutive stretch, then lists it.
+// A warp's stretch of consecutive keys when the CTA's warps share n of them.
+template <int NT>
+struct Stretch {
+  int beg, end;
+  __device__ Stretch(int n, int warp) {
+    const int seg = (n + 4 * NT - 1) / (4 * NT) * 128;
+    beg = min(n, warp * seg);
+    end = min(n, beg + seg);
+  }
+};
+
+// Calls emit(position, i, key) for the keys of the warp's stretch that are at
+// least t (eq_before + those equal to t before them < need, unless `every`
+// equal one is taken), in increasing order of i, from position pos on and below
+// `room` (keys that another launch overwrites meanwhile must not write past the
+// list).  key1(i): a key.
+template <int NT, class T, class Key1, class Emit>
+__device__ __forceinline__ void list_stretch(Key1 key1, Stretch<NT> w, T t, bool every, int eq_before, int need,
+                                             int pos, int room, int lane, Emit emit) {
+  const unsigned int below = (1u << lane) - 1u;
+  if (every) {
+#pragma unroll 4
+    for (int i0 = w.beg; i0 < w.end; i0 += 32) {
+      const int i = i0 + lane;
+      const T k = i < w.end ? key1(i) : (T)0;
+      const bool in = i < w.end && k >= t;
+      const unsigned int b = __ballot_sync(0xffffffffu, in);
+      const int at = pos + __popc(b & below);
+      if (in && at < room) emit(at, i, k);
+      pos += __popc(b);
+    }
+    return;
+  }
+  for (int i0 = w.beg; i0 < w.end; i0 += 32) {
+    const int i = i0 + lane;
+    const T k = i < w.end ? key1(i) : (T)0;
+    const unsigned int same = __ballot_sync(0xffffffffu, i < w.end && k == t);
+    const bool in = i < w.end && (k > t || (k == t && eq_before + __popc(same & below) < need));
+    const unsigned int b = __ballot_sync(0xffffffffu, in);
+    const int at = pos + __popc(b & below);
+    if (in && at < room) emit(at, i, k);
+    pos += __popc(b);
+    eq_before += __popc(same);
+  }
+}
+
+// The same over the whole CTA: emit for every key above t, and for the first
+// need of those equal to t.
 template <int NT, class T, class Key4, class Key1, class Emit>
-__device__ void take_above(Key4 key4, Key1 key1, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid, Emit emit) {
+__device__ void take_above(Key4 key4, Key1 key1, int n, T t, int need, int room, SelectSmem<NT> &sm, int tid,
+                           Emit emit) {
   const int lane = tid & 31, warp = tid >> 5;
-  const int seg = (n + 4 * NT - 1) / (4 * NT) * 128;  // keys of a warp
-  const int beg = min(n, warp * seg), end = min(n, beg + seg);
+  const Stretch<NT> w(n, warp);
   int gt = 0, eq = 0;
 #pragma unroll 2
-  for (int i = beg + 4 * lane; i < end; i += 128) {
+  for (int i = w.beg + 4 * lane; i < w.end; i += 128) {
     const Keys4<T> k = key4(i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      gt += i + e < end && k.v[e] > t;
-      eq += i + e < end && k.v[e] == t;
+      gt += i + e < w.end && k.v[e] > t;
+      eq += i + e < w.end && k.v[e] == t;
     }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
@@ -201,34 +257,10 @@ __device__ void take_above(Key4 key4, Key1 key1, int n, T t, int need, int room,
     sm.b[warp] = eq;
   }
   __syncthreads();
-  gt = eq = 0;
-  int all_eq = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) {
-      gt += sm.a[w];
-      eq += sm.b[w];
-    }
-    all_eq += sm.b[w];
-  }
-  const bool every = need >= all_eq;  // then the order of the equal ones does not matter
-  const unsigned int below = (1u << lane) - 1u;
-  int pos = gt + min(eq, need);
-#pragma unroll 4
-  for (int i0 = beg; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    const T k = i < end ? key1(i) : (T)0;
-    bool in = i < end && (k > t || (every && k == t));
-    if (!every) {
-      const unsigned int same = __ballot_sync(0xffffffffu, i < end && k == t);
-      in |= (same >> lane & 1u) && eq + __popc(same & below) < need;
-      eq += __popc(same);
-    }
-    const unsigned int b = __ballot_sync(0xffffffffu, in);
-    const int at = pos + __popc(b & below);
-    if (in && at < room) emit(at, i, k);
-    pos += __popc(b);
-  }
+  gt = sum_before<NT>(sm.a, lane, warp);
+  eq = sum_before<NT>(sm.b, lane, warp);
+  const bool every = need >= sum_all<NT>(sm.b, lane);  // then the order of the equal ones does not matter
+  list_stretch<NT, T>(key1, w, t, every, eq, need, gt + min(eq, need), room, lane, emit);
 }
 
 }  // namespace
