@@ -88,10 +88,16 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
   } else if (mine) {
     mine = __ldg(a.ctx + s) > j0;
   }
+  const size_t wrow = ((size_t)(mine ? row : 0) * a.Hkv + h) * a.max_tokens;
+  float w[kWPer];  // on their way while the logits are still written
+#pragma unroll
+  for (int i = 0; i < kWPer; ++i) {
+    const int j = j0 + i * kWThreads + tid;
+    w[i] = mine && j < a.max_ctx ? a.w_in[wrow + j] : 0.f;
+  }
   grid_wait();  // the logits are complete
   if (!in_range && a.err && tid == 0 && h == 0 && blockIdx.x == 0) atomicOr(a.err, PA_DEVERR_ROW);
   if (!mine) return;
-  const size_t wrow = ((size_t)row * a.Hkv + h) * a.max_tokens;
   float acc[kWPer];
   bool any[kWPer];
 #pragma unroll
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
 #pragma unroll
   for (int i = 0; i < kWPer; ++i) {
     const int j = j0 + i * kWThreads + tid;
-    if (any[i]) a.w_out[wrow + j] = a.w_in[wrow + j] + acc[i];
+    if (any[i]) a.w_out[wrow + j] = w[i] + acc[i];
   }
 }
 

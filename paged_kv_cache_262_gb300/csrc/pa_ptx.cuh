@@ -129,21 +129,19 @@ __device__ __forceinline__ void store2_hint(float *to, float x, float y, uint64_
 }
 __device__ __forceinline__ float load_hint(const float *from, uint64_t policy) {
   float v;
-  asm volatile("ld.global.L2::cache_hint.f32 %0, [%1], %2;" : "=f"(v) : "l"(from), "l"(policy) : "memory");
+  asm volatile("ld.global.L2::cache_hint.f32 %0, [%1], %2;" : "=f"(v) : "l"(from), "l"(policy));
   return v;
 }
 __device__ __forceinline__ float2 load_hint(const float2 *from, uint64_t policy) {
   float2 v;
-  asm volatile("ld.global.L2::cache_hint.v2.f32 {%0,%1}, [%2], %3;" : "=f"(v.x), "=f"(v.y) : "l"(from), "l"(policy)
-               : "memory");
+  asm volatile("ld.global.L2::cache_hint.v2.f32 {%0,%1}, [%2], %3;" : "=f"(v.x), "=f"(v.y) : "l"(from), "l"(policy));
   return v;
 }
 __device__ __forceinline__ float4 load_hint(const float4 *from, uint64_t policy) {
   float4 v;
   asm volatile("ld.global.L2::cache_hint.v4.f32 {%0,%1,%2,%3}, [%4], %5;"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "l"(from), "l"(policy)
-               : "memory");
+               : "l"(from), "l"(policy));
   return v;
 }
 
