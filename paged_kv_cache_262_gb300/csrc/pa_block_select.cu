@@ -326,7 +326,7 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
 // counter, the last CTA to arrive, this took 4.6 us longer).  LONG: rows of
 // more blocks than that holds, by way of the workspace.
 template <int D, int NT, int SW, bool LONG>
-__global__ void __launch_bounds__(SW * 32, 16 / SW) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kernel(const SelectArgs a) {
   constexpr int CH = 2 * D / 32;  // 32-element steps over a block's bounds (lo, then hi)
   constexpr int kThreads = SW * 32;
   __shared__ RowSelect<SW> r;

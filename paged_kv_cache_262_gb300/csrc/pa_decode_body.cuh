@@ -231,6 +231,12 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   const int nm = GRP ? __ldg(a.sub_start + sg + 1) - s : 1;  // members (query-row groups) of the unit
   const int warp = tid >> 5, lane = tid & 31;
   const int G = a.G;
+  // SEL: this thread's first list entry, loaded beside the context length
+  int sel0 = -1;
+  if constexpr (SEL) {
+    if (part * a.part_pages + tid < a.nsel)
+      sel0 = __ldg(a.sel + ((size_t)s * a.Hkv + kvh) * a.nsel + part * a.part_pages + tid);
+  }
   const int ncols = nm * G;  // query rows of the unit: member g / G, head g % G
   // GRP: a sub-group outside the batch is refused before anything is read
   const bool in_range = !GRP || (s >= 0 && nm > 0 && s + nm <= a.S);
@@ -316,7 +322,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       pg = __ldg(a.bt + (size_t)(s + max(m, 0)) * a.max_blocks + lb);
       meta[i] = ((m + 1) << 24) | lb;
     } else if constexpr (SEL) {
-      const int lb = __ldg(a.sel + ((size_t)s * a.Hkv + kvh) * a.nsel + p0 + i);
+      const int lb = i == tid ? sel0 : __ldg(a.sel + ((size_t)s * a.Hkv + kvh) * a.nsel + p0 + i);
       meta[i] = lb;
       if (lb == -1) {  // a list shorter than the rest
         tbl[i] = -1;

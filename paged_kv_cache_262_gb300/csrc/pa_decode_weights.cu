@@ -50,7 +50,7 @@ struct WeightArgs {
   size_t max_tokens;
 };
 
-constexpr int kWThreads = 256;
+constexpr int kWThreads = 128;
 constexpr int kWPer = 4;  // tokens of a thread
 constexpr int kWTokens = kWThreads * kWPer;
 
@@ -210,7 +210,7 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   if (!q || !k_pool || !v_pool || !block_tables || !context_lens || !weights || !weights_out || !out)
     return PA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(weights) ||
-      !aligned16(weights_out))
+      !aligned16(weights_out) || !same_or_apart(weights, weights_out, num_rows, d->num_kv_heads, max_tokens))
     return PA_ERR_INVALID;
   if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   const int sms = current_sm_count();

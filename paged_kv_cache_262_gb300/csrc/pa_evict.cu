@@ -318,7 +318,8 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
     return PA_ERR_INVALID;
   if (d->num_seqs == 0) return PA_OK;
   if (!k_pool || !v_pool || !block_tables || !context_lens || !keep_lens || !weights || !weights_out || !kept ||
-      !new_lens || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(weights) || !aligned16(weights_out))
+      !new_lens || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(weights) || !aligned16(weights_out) ||
+      new_lens == context_lens || !same_or_apart(weights, weights_out, num_rows, d->num_kv_heads, max_tokens))
     return PA_ERR_INVALID;
   if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   const int sms = current_sm_count();

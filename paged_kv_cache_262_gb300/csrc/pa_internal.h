@@ -29,6 +29,13 @@ bool encode_kv_pages(const pa_decode_desc *d, const void *pool, CUtensorMap *map
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two rows x heads x tokens fp32 arrays are one array or apart.
+inline bool same_or_apart(const float *a, const float *b, int rows, int heads, int tokens) {
+  const size_t bytes = (size_t)rows * heads * tokens * sizeof(float);
+  const char *x = reinterpret_cast<const char *>(a), *y = reinterpret_cast<const char *>(b);
+  return x == y || x + bytes <= y || y + bytes <= x;
+}
+
 inline int launch_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
 // Longest context part one decode CTA streams, and most parts per sequence.

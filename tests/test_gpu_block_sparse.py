@@ -373,6 +373,69 @@ def test_a_step_of_select_and_attend_in_graphs_and_on_streams(torch):
     assert int(err) == 0
 
 
+def test_long_rows_in_a_graph(torch):
+    """Rows that go through the workspace and its arrival counters: replays,
+    and eager calls on the same workspace between them."""
+    R = _ref()
+    n, Hkv, G, D, B = 9000, 2, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    b = torch.randn(n, Hkv, 2, D, generator=g, device="cuda").sort(dim=2).values.to(torch.bfloat16)
+    bt = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[None].expand(3, -1).contiguous()
+    lens = [n * B, 300, 5000 * B]
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qs = [torch.randn(3, Hkv * G, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    want = [R.ref_select(x, b, bt, lens, B, G, 50, 1, 1) for x in qs]
+    desc = pa.DecodeDesc(3, Hkv * G, Hkv, D, B, n, n, n * B, 1.0)
+    import ctypes
+    ws = torch.full((int(pa.load().pa_select_blocks_workspace_bytes(ctypes.byref(desc))),), 255, dtype=torch.uint8,
+                    device="cuda")
+    q, sel = qs[0].clone(), torch.empty(3, Hkv, 50, dtype=torch.int32, device="cuda")
+    call = lambda: pa.select_blocks(q, b, bt, ctx, 50, block_size=B, workspace=ws, selected=sel)  # noqa: E731
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        call()
+    for i in (0, 1, 1, 0):
+        q.copy_(qs[i])
+        graph.replay()
+        assert torch.equal(sel, want[i])
+        sel.zero_()
+        call()
+        assert torch.equal(sel, want[i])
+
+
+def test_calls_on_two_streams_at_once(torch):
+    """Default workspaces belong to their stream: two steps in flight at the
+    same time do not meet."""
+    R = _ref()
+    c = R.make_cache([4000, 1500], 4, 128, 16, seed=33)
+    b = torch.zeros(c["k"].shape[0], 4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    pa.block_key_bounds(c["k"], b, c["bt"], c["ctx"])
+    qs = [torch.randn(2, 16, 128, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    w = [torch.zeros(2, 4, c["mb"] * 16, device="cuda") for _ in range(2)]
+
+    def step(x, w):
+        sel = pa.select_blocks(x, b, c["bt"], c["ctx"], 130, block_size=16)
+        out, _ = pa.paged_attention_decode_weights(x, c["k"], c["v"], c["bt"], c["ctx"], w)
+        return sel, pa.paged_attention_decode_sparse(x, c["k"], c["v"], c["bt"], c["ctx"], sel), out
+
+    want = [step(x, y) for x, y in zip(qs, w)]
+    once = [y.clone() for y in w]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for r in range(10):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                w[i].zero_()
+                got[i].append(step(qs[i], w[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert torch.equal(w[i], once[i])
+        for r in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(r, want[i]))
+
+
 def test_offsets_beyond_32_bits(torch):
     """Blocks at the end of a pool of more than 2^31 elements."""
     R = _ref()
@@ -393,6 +456,12 @@ def test_offsets_beyond_32_bits(torch):
         pa.block_key_bounds(k, b, t, c["ctx"], max_context_len=100)
         sel = pa.select_blocks(q, b, t, c["ctx"], 3, block_size=B, max_context_len=100)
         res.append((b[-n:], sel, pa.paged_attention_decode_sparse(q, k, v, t, c["ctx"], sel, max_context_len=100)))
+    w, keep = [torch.zeros(2, Hkv, 112, device="cuda") for _ in range(2)], torch.full((2,), 20, dtype=torch.int32,
+                                                                                      device="cuda")
+    for (k, v, t), x in zip(((c["k"], c["v"], c["bt"]), (kp, vp, bt)), w):
+        pa.paged_attention_decode_weights(q, k, v, t, c["ctx"], x, max_context_len=100)
+        pa.evict_tokens(k, v, t, c["ctx"], keep, x, max_keep_len=20, max_context_len=100)
+    assert torch.equal(w[0], w[1]) and same_bits(torch, c["k"], kp[-n:]) and same_bits(torch, c["v"], vp[-n:])
     assert same_bits(torch, res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
     assert same_bits(torch, res[0][2], res[1][2])
 

@@ -44,7 +44,7 @@ def weights(lib, d, q=16, kp=16, vp=16, bt=16, ctx=16, w=16, wo=16, rows=None, n
 
 
 def evict(lib, d, kp=16, vp=16, bt=16, dst=None, ctx=16, keep=16, mk=8, sink=1, recent=1, w=16, wo=16, rows=None,
-          nr=2, mt=64, kept=16, new=16):
+          nr=2, mt=64, kept=16, new=32):
     return lib.pa_evict_tokens(d, kp, vp, bt, dst, ctx, keep, mk, sink, recent, w, wo, rows, nr, mt, kept, new, None,
                                None)
 
@@ -88,7 +88,10 @@ INVALID = pa.PA_ERR_INVALID
     (evict, dict(kp=None)), (evict, dict(vp=None)), (evict, dict(bt=None)), (evict, dict(ctx=None)),
     (evict, dict(keep=None)), (evict, dict(w=None)), (evict, dict(wo=None)), (evict, dict(kept=None)),
     (evict, dict(new=None)), (evict, dict(kp=18)), (evict, dict(w=20)), (evict, dict(mk=0)), (evict, dict(sink=-1)),
-    (evict, dict(recent=-1)), (evict, dict(mt=63)), (evict, dict(nr=1)),
+    (evict, dict(recent=-1)), (evict, dict(mt=63)), (evict, dict(nr=1)), (evict, dict(new=16)),
+    # (2 rows x 2 heads x 64 tokens x 4 bytes = 1024: arrays less than that apart overlap)
+    (evict, dict(w=4096, wo=4096 + 1008)), (evict, dict(w=4096 + 16, wo=4096)),
+    (weights, dict(w=4096, wo=4096 + 1008)), (weights, dict(w=4096 + 16, wo=4096)),
 ])
 def test_bad_arguments(lib, call, kw):
     assert call(lib, _desc(), **kw) == INVALID
