@@ -50,7 +50,6 @@ template <int NT, bool SMEM>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t skeys[];
   __shared__ SelectSmem<NT> sm;
-  grid_launch_dependents();
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
   int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int ctx = __ldg(a.ctx + s), keep = __ldg(a.keep + s);
@@ -156,11 +155,18 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   __syncthreads();
   // by stretches; where the competing ones have gone already, the recent ones
   const int from = in_smem ? n - a.recent : 0;
-  for (int base = from; base < ctx; base += NT) {
-    const int i = base + tid;
-    const float v = i < n ? w[min(max(kept[i], 0), ctx - 1)] : 0.f;
+  constexpr int kBatch = 8;
+  for (int base = from; base < ctx; base += kBatch * NT) {
+    float v[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = base + e * NT + tid;
+      v[e] = i < n ? w[min(max(kept[i], 0), ctx - 1)] : 0.f;
+    }
     __syncthreads();
-    if (i < ctx) wo[i] = v;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (base + e * NT + tid < ctx) wo[base + e * NT + tid] = v[e];
   }
 }
 
@@ -171,33 +177,34 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
 // thread's copies of it, and of all before it, have landed; the later ones on
 // their way read at or behind their own slots, which no earlier stage writes.
 constexpr int kMvThreads = 256;
-constexpr int kMvStages = 3;
-constexpr int kMvPieces = 4;     // pieces of a thread in a stage
-constexpr int kMvIndex = 2048;  // rows of list and table entries ahead and behind, in shared memory
+constexpr int kMvPieces = 4;  // pieces of a thread in a stage
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// ST stages; IX rows of list and table entries, ahead and behind, looked up IR
+// rows a thread at a time.
+template <int ST, int IX>
 struct MoveSmem {
-  uint4 ring[kMvStages][kMvPieces][kMvThreads];
-  int32_t src[kMvIndex], dst[kMvIndex];  // pool rows; dst -1: the row stays where it is
+  uint4 ring[ST][kMvPieces][kMvThreads];
+  int32_t src[IX], dst[IX];  // pool rows; dst -1: the row stays where it is
 };
 
-template <int D, int RB>
+template <int D, int RB, int ST, int IX, int IR>
 __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs a) {
   constexpr int C = D / 8;              // 16-byte pieces of a row
   constexpr int P = RB / 16;            // of which a CTA moves
   constexpr int A = kMvThreads / P;     // rows of one piece a thread
   constexpr int T = A * kMvPieces;      // rows of a stage
-  constexpr int GS = kMvThreads / T;    // stages an index group (a row a thread) covers
-  static_assert(T <= kMvThreads && kMvThreads % T == 0, "whole stages to an index group");
-  static_assert(kMvStages * T + 3 * kMvThreads <= kMvIndex, "the index ring holds what is in flight");
+  constexpr int IG = IR * kMvThreads;   // rows of an index group
+  constexpr int GS = IG / T;            // stages it covers
+  static_assert(T <= IG && IG % T == 0, "whole stages to an index group");
+  static_assert(ST * T + 3 * IG <= IX, "the index ring holds what is in flight");
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  MoveSmem &sm = *reinterpret_cast<MoveSmem *>(smem_raw);
+  auto &sm = *reinterpret_cast<MoveSmem<ST, IX> *>(smem_raw);
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-  grid_wait();
-  const int n = min(__ldcg(a.new_lens + s), a.max_keep);
+  const int n = min(__ldg(a.new_lens + s), a.max_keep);
   const int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks, *dt = a.dst + (size_t)s * a.max_blocks;
   const int B = a.B, lb = B == 16 ? 4 : 5;
@@ -206,29 +213,41 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
 
   // index groups: list entry, then the source block's table entry, then the
   // rows into shared memory, each a group ahead of the next
-  int j1 = -1, i1 = 0, s1 = -1, d1 = -1, j2 = -1, i2 = 0, d2 = -1;
+  int g1 = 0, g2 = 0, j1[IR], s1[IR], d1[IR], j2[IR], d2[IR];
   auto step_list = [&](int g) {
-    i2 = g * kMvThreads + tid;
-    j2 = i2 < n ? __ldcg(kept + i2) : -1;
-    d2 = i2 < n ? __ldg(dt + (i2 >> lb)) : -1;
+    g2 = g;
+#pragma unroll
+    for (int r = 0; r < IR; ++r) {
+      const int i = g * IG + r * kMvThreads + tid;
+      j2[r] = i < n ? __ldg(kept + i) : -1;
+      d2[r] = i < n ? __ldg(dt + (i >> lb)) : -1;
+    }
   };
   auto step_table = [&]() {
-    i1 = i2, j1 = j2, d1 = d2;
-    s1 = j1 >= 0 && (j1 >> lb) < a.max_blocks ? __ldg(bt + (j1 >> lb)) : -1;
+    g1 = g2;
+#pragma unroll
+    for (int r = 0; r < IR; ++r) {
+      j1[r] = j2[r], d1[r] = d2[r];
+      s1[r] = j1[r] >= 0 && (j1[r] >> lb) < a.max_blocks ? __ldg(bt + (j1[r] >> lb)) : -1;
+    }
   };
   auto step_rows = [&]() {
-    int32_t from = 0, to = -1;
-    if (j1 >= 0) {
-      if (s1 < 0 || s1 >= a.num_blocks || d1 < 0 || d1 >= a.num_blocks) {
-        bad = 1;
-      } else {
-        from = (s1 * a.Hkv + h) * B + (j1 & (B - 1));
-        const int32_t at = (d1 * a.Hkv + h) * B + (i1 & (B - 1));
-        to = at == from ? -1 : at;
+#pragma unroll
+    for (int r = 0; r < IR; ++r) {
+      const int i = g1 * IG + r * kMvThreads + tid;
+      int32_t from = 0, to = -1;
+      if (j1[r] >= 0) {
+        if (s1[r] < 0 || s1[r] >= a.num_blocks || d1[r] < 0 || d1[r] >= a.num_blocks) {
+          bad = 1;
+        } else {
+          from = (s1[r] * a.Hkv + h) * B + (j1[r] & (B - 1));
+          const int32_t at = (d1[r] * a.Hkv + h) * B + (i & (B - 1));
+          to = at == from ? -1 : at;
+        }
       }
+      sm.src[i % IX] = from;
+      sm.dst[i % IX] = to;
     }
-    sm.src[i1 % kMvIndex] = from;
-    sm.dst[i1 % kMvIndex] = to;
   };
   const uint32_t ring = smem_u32(&sm.ring[0][0][tid]);
   const int t0 = tid / P;
@@ -236,14 +255,14 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
 #pragma unroll
     for (int u = 0; u < kMvPieces; ++u) {
       const int i = st * T + u * A + t0;
-      if (i < n && sm.dst[i % kMvIndex] >= 0)
-        copy16_async(ring + ((st % kMvStages) * kMvPieces + u) * (kMvThreads * 16),
-                     pool + (int64_t)sm.src[i % kMvIndex] * C);
+      if (i < n && sm.dst[i % IX] >= 0)
+        copy16_async(ring + ((st % ST) * kMvPieces + u) * (kMvThreads * 16),
+                     pool + (int64_t)sm.src[i % IX] * C);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   step_list(0);
-  if (n <= 0 || __ldcg(kept) < 0) return;  // a refused sequence (the same for the whole CTA)
+  if (n <= 0 || __ldg(kept) < 0) return;  // a refused sequence (the same for the whole CTA)
   step_table();
   step_list(1);
   step_rows();
@@ -253,7 +272,7 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
   const int nst = (n + T - 1) / T;
   int made = 1;  // index groups in shared memory
 #pragma unroll 1
-  for (int st = 0; st < kMvStages - 1; ++st) {
+  for (int st = 0; st < ST - 1; ++st) {
     if (st == made * GS) {
       step_rows();
       step_table();
@@ -264,19 +283,19 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
   }
 #pragma unroll 1
   for (int st = 0; st < nst; ++st) {
-    const int ahead = st + kMvStages - 1;
+    const int ahead = st + ST - 1;
     if (ahead >= made * GS - 1) {  // read behind the barrier
       step_rows();
       step_table();
       step_list(++made + 1);
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kMvStages - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMvPieces; ++u) {
       const int i = st * T + u * A + t0;
-      const int32_t to = i < n ? sm.dst[i % kMvIndex] : -1;
-      if (to >= 0) pool[(int64_t)to * C] = sm.ring[st % kMvStages][u][tid];
+      const int32_t to = i < n ? sm.dst[i % IX] : -1;
+      if (to >= 0) pool[(int64_t)to * C] = sm.ring[st % ST][u][tid];
     }
     load(ahead);
   }
@@ -284,22 +303,33 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
   if (bad && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
 }
 
-template <int D, int RB>
+template <int D, int RB, int ST, int IX, int IR>
 int launch_move_rows(const EvictArgs &a, cudaStream_t st) {
-  auto kern = evict_move_kernel<D, RB>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(MoveSmem)) != cudaSuccess)
+  using Smem = MoveSmem<ST, IX>;
+  auto kern = evict_move_kernel<D, RB, ST, IX, IR>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) != cudaSuccess)
     return PA_ERR_CUDA;
-  return launch_dependent(kern, dim3(2 * (D * 2 / RB), a.Hkv, a.S), kMvThreads, sizeof(MoveSmem), st, a);
+  kern<<<dim3(2 * (D * 2 / RB), a.Hkv, a.S), kMvThreads, sizeof(Smem), st>>>(a);
+  return launch_status(cudaGetLastError());
 }
 
-// Whole rows where that gives about a CTA an SM, else parts of 128 or 64 bytes.
+// Whole rows where that gives three CTAs to two SMs, else parts of 128 or 64
+// bytes; a CTA with an SM to itself takes more stages and larger index groups,
+// and where parts of 64 bytes leave half the SMs idle, parts of a sector.  (us
+// at 16384 of 32768 tokens, 8 kv heads: 8 sequences 194 by 128 bytes, 210 by
+// 256; 1 sequence 60 by 32 bytes, 73 by 64.)  Launched behind the selection,
+// not as its programmatic dependent: CTAs that start while the selection still
+// holds some SMs pile up on the others (205 us instead of 194).
 template <int D>
 int launch_move(const EvictArgs &a, int sms, cudaStream_t st) {
   const int64_t units = 2ll * a.Hkv * a.S;
   if constexpr (D == 128)
-    if (4 * units >= 6ll * sms) return launch_move_rows<D, 256>(a, st);
-  if (units * (D / 64) * 4 >= 6ll * sms) return launch_move_rows<D, 128>(a, st);
-  return launch_move_rows<D, 64>(a, st);
+    if (2 * units >= 3ll * sms) return launch_move_rows<D, 256, 3, 2048, 1>(a, st);
+  if (2 * units * (D / 64) >= 3ll * sms) return launch_move_rows<D, 128, 3, 2048, 1>(a, st);
+  const int64_t ctas = units * (D / 32);
+  if (ctas > sms) return launch_move_rows<D, 64, 3, 2048, 1>(a, st);
+  if (2 * ctas > sms) return launch_move_rows<D, 64, 4, 8192, 8>(a, st);
+  return launch_move_rows<D, 32, 4, 8192, 8>(a, st);
 }
 
 }  // namespace

@@ -71,7 +71,7 @@ __device__ __forceinline__ int sum_all(const int *v, int lane) {
 // f(i, key) for every key of this thread: four consecutive ones at a time.
 template <int NT, class T, class Key4, class F>
 __device__ __forceinline__ void for_keys(Key4 key4, int n, int tid, F f) {
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 4 * tid; i < n; i += 4 * NT) {
     const Keys4<T> k = key4(i);
 #pragma unroll
@@ -240,7 +240,7 @@ __device__ void take_above(Key4 key4, Key1 key1, int n, T t, int need, int room,
   const int lane = tid & 31, warp = tid >> 5;
   const Stretch<NT> w(n, warp);
   int gt = 0, eq = 0;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = w.beg + 4 * lane; i < w.end; i += 128) {
     const Keys4<T> k = key4(i);
 #pragma unroll

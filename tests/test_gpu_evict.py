@@ -283,6 +283,23 @@ def test_evict_long_contexts(torch, ctx, keep):
     run_evict(torch, (2, 2, 64, 16), [ctx, ctx // 2], [keep, keep // 2], 4, 64)
 
 
+def test_evict_many_long_rows(torch):
+    """Rows enough to fill the GPU without clusters."""
+    lens = [4200 + 37 * i for i in range(40)]
+    run_evict(torch, (8, 8, 64, 16), lens, [3000 + 11 * i for i in range(40)], 3, 40)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_a_row_longer_than_any_shared_memory(torch, in_place):
+    run_evict(torch, (1, 1, 64, 32), [200001, 9], [120000, 9], 1, 64, in_place=in_place)
+
+
+@pytest.mark.parametrize("fill", ["_ties", "_zeros", "_odd", "_same", "_steps"])
+@pytest.mark.parametrize("ctx,keep", [(5000, 77), (9999, 9000), (33000, 16001)])
+def test_evict_weights_of_every_kind_in_clusters(torch, fill, ctx, keep):
+    run_evict(torch, (1, 1, 64, 16), [ctx, ctx - 640], [keep, keep // 2], 1, 2, weights=globals()[fill])
+
+
 @pytest.mark.parametrize("ctx,keep,sink,recent", [(3500, 2000, 3, 1500), (3500, 2000, 0, 2000), (9000, 8000, 1, 5000),
                                                   (60000, 40000, 2, 30000), (700, 600, 600, 0)])
 @pytest.mark.parametrize("in_place", [True, False])
@@ -298,6 +315,16 @@ def _zeros(w):
     w.zero_()
     w[:, :, ::7] = -0.0
     w[:, :, 5::11] = 1e-20
+
+
+def _same(w):
+    w.fill_(0.25)
+
+
+def _steps(w):  # a few values that differ in their last bits, in blocks
+    n = w.shape[2]
+    i = w.new_tensor(range(n)).long()
+    w.copy_((1.0 + (i // 700 * 5 % 7) * 2.0**-23).expand_as(w))
 
 
 def _odd(w):
