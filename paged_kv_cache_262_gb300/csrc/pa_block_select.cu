@@ -49,6 +49,8 @@ template <int D, int B>
 __global__ void __launch_bounds__(256) key_bounds_kernel(const BoundsArgs a) {
   constexpr int C = D / 8;          // 16-byte chunks of a key
   constexpr int R = 32 / C;         // keys a load instruction covers
+  grid_wait();
+  grid_launch_dependents();
   const int s = blockIdx.y, lane = threadIdx.x & 31;
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int ctx = __ldg(a.ctx + s), start = a.start ? __ldg(a.start + s) : 0;
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.B;
   const size_t row = (size_t)s * a.Hkv + h;
+  grid_wait();
   const int ctx = __ldg(a.ctx + s);
   const bool bad = ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx;
   const int n = bad ? 0 : (ctx + B - 1) / B;
@@ -455,6 +458,7 @@ __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kerne
       }
     }
   }
+  grid_launch_dependents();
   const bool one = !LONG && !clustered;  // then the threads' own least and largest keys will do
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
@@ -560,21 +564,7 @@ template <int D, int NT, int SW, bool LONG>
 int launch_select(const SelectArgs &a, dim3 grid, cudaStream_t st) {
   auto kern = select_kernel<D, NT, SW, LONG>;
   static_assert(sizeof(RowSelect<SW>) <= 48 * 1024, "static shared memory");
-  if (LONG || grid.x == 1) {
-    kern<<<grid, SW * 32, 0, st>>>(a);
-    return launch_status(cudaGetLastError());
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(SW * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = grid.x;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
+  return launch_dependent(kern, grid, SW * 32, 0, LONG ? 1 : (int)grid.x, st, a);
 }
 
 template <int D, int NT>
@@ -618,18 +608,9 @@ extern "C" int pa_block_key_bounds(const pa_decode_desc *d, const void *k_pool, 
   if (gx > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)gx, d->num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d->head_dim == 128) {
-    if (d->block_size == 16)
-      key_bounds_kernel<128, 16><<<grid, 256, 0, s>>>(a);
-    else
-      key_bounds_kernel<128, 32><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (d->block_size == 16)
-      key_bounds_kernel<64, 16><<<grid, 256, 0, s>>>(a);
-    else
-      key_bounds_kernel<64, 32><<<grid, 256, 0, s>>>(a);
-  }
-  return launch_status(cudaGetLastError());
+  auto kern = d->head_dim == 128 ? (d->block_size == 16 ? key_bounds_kernel<128, 16> : key_bounds_kernel<128, 32>)
+                                 : (d->block_size == 16 ? key_bounds_kernel<64, 16> : key_bounds_kernel<64, 32>);
+  return launch_dependent(kern, grid, 256, 0, 1, s, a);
 }
 
 extern "C" size_t pa_select_blocks_workspace_bytes(const pa_decode_desc *d) {

@@ -955,21 +955,10 @@ int launch_parts(K plain, K in_cluster, int smem, int smem_cl, dim3 grid, int th
                  const CUtensorMap &tv, const DecodeArgs &a, cudaStream_t st) {
   const bool cl = grid.x > 1 && grid.x <= kMaxClusterParts;
   K kern = cl ? in_cluster : plain;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = cl ? smem_cl : smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = grid.x;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cl ? 1 : 0;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
-      cudaSuccess)
+  const int bytes = cl ? smem_cl : smem;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return PA_ERR_CUDA;
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, tk, tv, a));
+  return launch_dependent(kern, grid, threads, (size_t)bytes, cl ? (int)grid.x : 1, st, tk, tv, a);
 }
 
 // Host: the argument block of a decode launch over a validated desc with

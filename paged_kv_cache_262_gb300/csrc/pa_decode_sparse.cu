@@ -28,6 +28,8 @@ __global__ void __launch_bounds__(128)
     sparse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
+  grid_wait();
+  grid_launch_dependents();
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lin = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
   decode_unit<D, B, NT, 4, NST, false, false, false, D == 128, true, false, CL>(&tmK, &tmV, a, lin, threadIdx.x, smem,

@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(128)
     decode_logits_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
+  grid_wait();
   grid_launch_dependents();
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lin = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
@@ -253,5 +254,5 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   const size_t smem = weight_rows ? ((size_t)d->num_seqs + kWThreads - 1) / kWThreads * (kWThreads / 8) : 0;
   const dim3 wgrid(chunks, d->num_kv_heads, d->num_seqs);
   auto kern = a.G % 4 == 0 ? weights_kernel<4> : a.G % 2 == 0 ? weights_kernel<2> : weights_kernel<1>;
-  return launch_dependent(kern, wgrid, kWThreads, smem, s, w);
+  return launch_dependent(kern, wgrid, kWThreads, smem, 1, s, w);
 }

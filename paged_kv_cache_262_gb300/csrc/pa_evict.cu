@@ -50,6 +50,7 @@ template <int NT, bool SMEM>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t skeys[];
   __shared__ SelectSmem<NT> sm;
+  grid_wait();
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
   int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int ctx = __ldg(a.ctx + s), keep = __ldg(a.keep + s);
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   auto &sm = *reinterpret_cast<MoveSmem<ST, IX> *>(smem_raw);
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  grid_wait();
   const int n = min(__ldg(a.new_lens + s), a.max_keep);
   const int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks, *dt = a.dst + (size_t)s * a.max_blocks;
@@ -309,17 +311,16 @@ int launch_move_rows(const EvictArgs &a, cudaStream_t st) {
   auto kern = evict_move_kernel<D, RB, ST, IX, IR>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) != cudaSuccess)
     return PA_ERR_CUDA;
-  kern<<<dim3(2 * (D * 2 / RB), a.Hkv, a.S), kMvThreads, sizeof(Smem), st>>>(a);
-  return launch_status(cudaGetLastError());
+  return launch_dependent(kern, dim3(2 * (D * 2 / RB), a.Hkv, a.S), kMvThreads, sizeof(Smem), 1, st, a);
 }
 
 // Whole rows where that gives three CTAs to two SMs, else parts of 128 or 64
 // bytes; a CTA with an SM to itself takes more stages and larger index groups,
 // and where parts of 64 bytes leave half the SMs idle, parts of a sector.  (us
 // at 16384 of 32768 tokens, 8 kv heads: 8 sequences 194 by 128 bytes, 210 by
-// 256; 1 sequence 60 by 32 bytes, 73 by 64.)  Launched behind the selection,
-// not as its programmatic dependent: CTAs that start while the selection still
-// holds some SMs pile up on the others (205 us instead of 194).
+// 256; 1 sequence 60 by 32 bytes, 73 by 64.)  The selection does not let it start
+// early: CTAs that start while the selection still holds some SMs pile up on the
+// others (205 us instead of 194).
 template <int D>
 int launch_move(const EvictArgs &a, int sms, cudaStream_t st) {
   const int64_t units = 2ll * a.Hkv * a.S;
@@ -384,15 +385,15 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
   const size_t smem = (size_t)((a.smem_keys + 3) & ~3) * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(a.Hkv, a.S);
+  int st;
   if (d->max_context_len <= kShort) {
-    evict_select_kernel<256, true><<<grid, 256, smem, s>>>(a);
+    st = launch_dependent(evict_select_kernel<256, true>, grid, 256, smem, 1, s, a);
   } else {
     auto kern = d->max_context_len <= kLong ? evict_select_kernel<1024, true> : evict_select_kernel<1024, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLong * 4) != cudaSuccess)
       return PA_ERR_CUDA;
-    kern<<<grid, 1024, smem, s>>>(a);
+    st = launch_dependent(kern, grid, 1024, smem, 1, s, a);
   }
-  const int st = launch_status(cudaGetLastError());
   if (st != PA_OK) return st;
   return d->head_dim == 128 ? launch_move<128>(a, sms, s) : launch_move<64>(a, sms, s);
 }

@@ -54,22 +54,27 @@ struct DecodePlan {
 };
 
 // Launches `kern` as a programmatic dependent of the kernel before it on the
-// stream: its CTAs may start once that one's have all executed
-// griddepcontrol.launch_dependents, and every one of them executes
-// griddepcontrol.wait before it reads what that kernel writes or writes
-// anything.
+// stream, whatever that is: its CTAs may start before that one has ended (from
+// when all of its CTAs have executed griddepcontrol.launch_dependents or
+// exited), so that the launch itself is off the path, and every one of them
+// executes griddepcontrol.wait before it reads or writes global memory.  With
+// `cluster` > 1, in clusters of that many CTAs along x.
 template <class... P, class... A>
-int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream,
+                     A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return launch_status(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
