@@ -218,7 +218,8 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
   uint32_t lo = 0u, hi = 0xfffffffeu;    // (no score's key is above it)
   int above = 0;
   if (finite) {
-    const Kth<uint32_t> t = kth_largest<kThreads, uint32_t>(key4, N, want, r.sm, tid, least, most);
+    const Kth<uint32_t> t = N <= kThreads ? kth_of_few<kThreads, uint32_t>(key4, key1, N, want, r.sm, tid)
+                                          : kth_largest<kThreads, uint32_t>(key4, N, want, r.sm, tid, least, most);
     above = t.above;
     if (t.key != 0u) {
       const float v = key_value(t.key);

@@ -956,7 +956,8 @@ int launch_parts(K plain, K in_cluster, int smem, int smem_cl, dim3 grid, int th
   const bool cl = grid.x > 1 && grid.x <= kMaxClusterParts;
   K kern = cl ? in_cluster : plain;
   const int bytes = cl ? smem_cl : smem;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+  if (bytes > 48 * 1024 &&  // (what a kernel may have without being asked)
+          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return PA_ERR_CUDA;
   return launch_dependent(kern, grid, threads, (size_t)bytes, cl ? (int)grid.x : 1, st, tk, tv, a);
 }

@@ -186,6 +186,31 @@ __device__ Kth<T> kth_largest(Key4 key4, int n, int want, SelectSmem<NT> &sm, in
   return Kth<T>{base, above};
 }
 
+// The same for n <= NT keys, a thread a key: the least key that fewer than want
+// are above (300 instructions and two barriers where the bins take 1.5 us).
+template <int NT, class T, class Key4, class Key1>
+__device__ Kth<T> kth_of_few(Key4 key4, Key1 key1, int n, int want, SelectSmem<NT> &sm, int tid) {
+  static_assert(sizeof(T) == 4, "32-bit keys");
+  const T mine = tid < n ? key1(tid) : (T)0;
+  int gt = 0;
+#pragma unroll 4
+  for (int j = 0; j + 4 <= n; j += 4) {
+    const Keys4<T> k = key4(j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gt += k.v[e] > mine;
+  }
+  for (int j = n & ~3; j < n; ++j) gt += key1(j) > mine;
+  T t = __reduce_min_sync(0xffffffffu, tid < n && gt < want ? mine : ~(T)0);
+  const int lane = tid & 31;
+  __syncthreads();  // sm may be in use by a call before
+  if (lane == 0) sm.lo[tid >> 5] = t;
+  __syncthreads();
+  t = __reduce_min_sync(0xffffffffu, lane < NT / 32 ? (T)sm.lo[lane] : ~(T)0);
+  if (tid < n && mine == t) sm.kth_above = gt;  // (equal keys write the same)
+  __syncthreads();
+  return Kth<T>{t, sm.kth_above};
+}
+
 // A warp's stretch of consecutive keys when the CTA's warps share n of them.
 template <int NT>
 struct Stretch {
