@@ -11,6 +11,13 @@
 // attending everything would (decode re-reads the whole cache for each token:
 // "Configuring vLLM and PagedAttention for High Throughput Enterprise LLM
 // Serving", "Memory Bottlenecks in Autoregressive LLM Inference").
+//
+// Both read more than they compute.  Bounds of 8 x 32768 tokens (8 kv heads, D
+// 128): 92.5 us, 6.5 TB/s; of one step of 64 sequences 2.8 us, a launch.
+// Selection of 128 of 2048 blocks for 8 sequences and 64 query heads: 22 us for
+// 67 MB, about 12 reading (5.8 TB/s) and 5 selecting, which one CTA a row does
+// after the rest; 32 of up to 128 blocks for 64 sequences 9.4 us and 33 of 256
+// for one sequence 6.4 us, in which the steps of the selection bind.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -325,8 +332,8 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
 
 // grid (chunk, kv head, sequence).  Every CTA scores its chunk of a row.  The
 // chunks of a row are a cluster: the scores go straight into the shared memory
-// of its first CTA, which selects (through the workspace and an arrival
-// counter, the last CTA to arrive, this took 4.6 us longer).  LONG: rows of
+// of its first CTA, which selects (by way of the workspace, an arrival counter
+// and the last CTA to arrive this handing over took 4.6 us, not 0.7).  LONG: rows of
 // more blocks than that holds, by way of the workspace.
 template <int D, int NT, int SW, bool LONG>
 __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kernel(const SelectArgs a) {

@@ -11,7 +11,15 @@
 // resolved through the block table once and streamed by TMA into per-warp
 // rings, warp MMAs, online softmax in fp32.  A list has the same length for
 // every sequence, so the split plan is that of contexts of num_select blocks
-// and no unit is longer than another.
+// and no unit is longer than another; the parts of a unit are a cluster and
+// join through shared memory (through the workspace: 22 us for the first case
+// below).
+//
+// The bytes bind: 240 sequences, 24 blocks of 32 tokens each at most, 8 kv heads
+// of 128: 103 us, 6.8 TB/s.  128 blocks of 16 for 8 sequences, 67 MB: 17.1 us,
+// 3.9 TB/s -- one wave of 256 CTAs, of which starting, three dependent loads,
+// the first gathers and the join are 7 us; more slots a warp or other parts
+// (16, 22, 43, 64 pages) are no faster.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

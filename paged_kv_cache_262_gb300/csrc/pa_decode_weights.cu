@@ -11,8 +11,14 @@
 // context has been read.  Reading K again would cost half of the call once
 // more; instead the decode unit (pa_decode_body.cuh) leaves its logits, 4 G
 // bytes a (token, kv head) against the 4 D bytes of its K and V, and a second
-// kernel turns them into weights.  The cache streams past L2 (evict first),
-// so the logits of a call mostly stay there in between.
+// kernel turns them into weights.  The cache streams past L2 (evict first)
+// while the logits are kept there (evict last) and let go as they are read.
+//
+// 8 x 32768 tokens, 64 query and 8 kv heads of 128 (1.09 GB): 181 us, 6.0 TB/s,
+// 167 the first kernel (67 MB of logits written, 7 MB of them reach HBM; without
+// the hint 204 us in all) and the rest the second, which starts while the first
+// runs and has the old sums loaded when it ends.  64 sequences of 128 .. 2048
+// tokens: 51 us, 5.9 TB/s.  Four sequences of up to 100: 5.8 us, two launches.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
