@@ -72,6 +72,11 @@ struct DecodeArgs {
   float *logits;    // [S][Hkv][max_ctx][G]
   float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys
   float *ws_lw;     // [S][Hkv][max_parts][G]: the parts' sums of unrounded probabilities
+  // Where a unit is one CTA or one cluster, it adds the weights itself: w_out
+  // [S][Hkv][max_tokens] = w_in + weights (null: a second kernel does).
+  const float *w_in;
+  float *w_out;
+  size_t max_tokens;
 };
 
 // Counts one arrival of this call at *c and returns the arrivals so far.  A
@@ -86,6 +91,52 @@ __device__ __forceinline__ unsigned int arrive_count(unsigned long long *c, unsi
     if (prev == old) return (unsigned int)(nv & 0xffffffffull);
     old = prev;
   }
+}
+
+// Adds the attention weights of tokens beg .. end - 1 of one (sequence, kv
+// head): w_out[j] = w_in[j] + sum_g 2^(x_jg - st[g].x) st[g].y, x the logits
+// [token][G].  NT threads; V of a token's G logits a load (V divides G), four
+// tokens a thread on their way.
+template <int V, int NT>
+__device__ __forceinline__ void add_weights(const float *logits, const float2 *st, int G, const float *w_in,
+                                            float *w_out, int beg, int end, int tid) {
+  using Vec = typename FloatVec<V>::type;
+  const Vec *lg = reinterpret_cast<const Vec *>(logits);
+  const uint64_t done = policy_evict_first();  // the logits leave L2 first once read
+  constexpr int kPer = 4;
+  for (int j0 = beg + tid; j0 < end; j0 += kPer * NT) {
+    float w[kPer], sum[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      w[i] = j0 + i * NT < end ? w_in[j0 + i * NT] : 0.f;
+      sum[i] = 0.f;
+    }
+#pragma unroll 2
+    for (int g = 0; g < G; g += V) {
+      Vec x[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (j0 + i * NT < end) x[i] = load_hint(lg + ((size_t)(j0 + i * NT) * G + g) / V, done);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          sum[i] += ex2_ftz(reinterpret_cast<const float *>(&x[i])[e] - st[g + e].x) * st[g + e].y;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (j0 + i * NT < end) w_out[j0 + i * NT] = w[i] + sum[i];
+  }
+}
+template <int NT>
+__device__ __forceinline__ void add_weights(const float *logits, const float2 *st, int G, const float *w_in,
+                                            float *w_out, int beg, int end, int tid) {
+  if (G % 4 == 0)
+    add_weights<4, NT>(logits, st, G, w_in, w_out, beg, end, tid);
+  else if (G % 2 == 0)
+    add_weights<2, NT>(logits, st, G, w_in, w_out, beg, end, tid);
+  else
+    add_weights<1, NT>(logits, st, G, w_in, w_out, beg, end, tid);
 }
 
 template <int D, int B, int NW, int NST>
@@ -704,6 +755,13 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   float *red_l = red_m + NW * 16;
   float *wts = red_l + NW * 16;
   float *red_lw = reinterpret_cast<float *>(meta);  // WTS: [NW][16] (the page list's tags: block lists, sub-groups only)
+  float2 *st_s = reinterpret_cast<float2 *>(red_lw + NW * 16);  // WTS: [16] the heads' statistics
+  // WTS: this CTA's tokens, once st_s is there
+  auto own_weights = [&]() {
+    const size_t u = (size_t)s * a.Hkv + kvh;
+    add_weights<NW * 32>(a.logits + u * a.max_ctx * G, st_s, G, a.w_in + u * a.max_tokens, a.w_out + u * a.max_tokens,
+                         p0 * B, min(ctx, (p0 + np) * B), tid);
+  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int g = nt * 8 + 2 * (lane & 3);
@@ -731,7 +789,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   const bool split = nparts > 1;
   const size_t unit = (size_t)s * a.Hkv + kvh;
   if constexpr (WTS) {
-    static_assert(!WTS || NW * 16 <= kMaxPartPages, "the warps' sums fit the page tags' room");
+    static_assert(!WTS || NW * 16 + 32 <= kMaxPartPages, "the warps' sums fit the page tags' room");
     if (tid < G) {
       float mx = -INFINITY, l = 0.f;
 #pragma unroll
@@ -745,7 +803,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       else if (split)
         reinterpret_cast<float *>(smem + L::kPartOff)[16 * D + 32 + tid] = l;
       else
-        a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
+        st_s[tid] = a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
             mx != -INFINITY ? make_float2(mx, 1.f / l) : make_float2(0.f, 0.f);
     }
   }
@@ -844,7 +902,15 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       }
     }
   }
-  if (!split) return;
+  if (!split) {
+    if constexpr (WTS) {
+      if (a.w_out) {
+        unit_sync<NW * 32>(bar);
+        own_weights();
+      }
+    }
+    return;
+  }
 
   if constexpr (CL) {
     // ---- split-K in a cluster: every part joins a share of the outputs
@@ -868,9 +934,10 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       }
       const float inv = den > 0.f ? 1.f / den : 0.f;
       for (int p = 0; p < nparts; ++p) wts[p * 16 + tid] *= inv;
-      if (WTS && part == 0)
-        a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
-            M != -INFINITY ? make_float2(M, 1.f / lw) : make_float2(0.f, 0.f);
+      if (WTS) {
+        st_s[tid] = M != -INFINITY ? make_float2(M, 1.f / lw) : make_float2(0.f, 0.f);
+        if (part == 0) a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] = st_s[tid];
+      }
     }
     unit_sync<NW * 32>(bar);
     for (int idx = part * (NW * 32) + tid; idx < G * D; idx += nparts * (NW * 32)) {
@@ -880,6 +947,9 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       out_base[idx] = __float2bfloat16(acc);
     }
     cluster_arrive();  // nobody leaves while its part is being read
+    if constexpr (WTS) {
+      if (a.w_out) own_weights();
+    }
     cluster_wait();
     return;
   }

@@ -14,11 +14,14 @@
 // kernel turns them into weights.  The cache streams past L2 (evict first)
 // while the logits are kept there (evict last) and let go as they are read.
 //
-// 8 x 32768 tokens, 64 query and 8 kv heads of 128 (1.09 GB): 181 us, 6.0 TB/s,
+// Where a CTA's own logits are few it adds their weights itself at its end, in
+// the one launch.
+//
+// 8 x 32768 tokens, 64 query and 8 kv heads of 128 (1.09 GB): 182 us, 6.0 TB/s,
 // 167 the first kernel (67 MB of logits written, 7 MB of them reach HBM; without
 // the hint 204 us in all) and the rest the second, which starts while the first
 // runs and has the old sums loaded when it ends.  64 sequences of 128 .. 2048
-// tokens: 51 us, 5.9 TB/s.  Four sequences of up to 100: 5.8 us, two launches.
+// tokens: 49 us, 6.1 TB/s.  Four sequences of up to 100: 4.6 us, the launch.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -60,15 +63,6 @@ struct WeightArgs {
 constexpr int kWThreads = 128;
 constexpr int kWPer = 4;  // tokens of a thread
 constexpr int kWTokens = kWThreads * kWPer;
-
-template <int V>
-struct FloatVec;
-template <>
-struct FloatVec<1> { using type = float; };
-template <>
-struct FloatVec<2> { using type = float2; };
-template <>
-struct FloatVec<4> { using type = float4; };
 
 // grid (token chunk, kv head, sequence).  Sequences that name the same row
 // are summed by the first of them, in sequence order, so that a row has one
@@ -233,6 +227,16 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   a.ws_lw = reinterpret_cast<float *>(ws);
   a.stats = reinterpret_cast<float2 *>(ws + plan.lw);
   a.logits = reinterpret_cast<float *>(ws + plan.lw + plan.stats);
+  // One launch where every (sequence, kv head) is a CTA or a cluster, rows are
+  // not shared and a CTA's logits are at most 64 KB; else a second kernel, on
+  // the whole GPU, adds the weights.  (us, one launch and two: 64 sequences up to
+  // 2048 tokens, 32 KB a CTA, 49.2 and 51.6; four short ones 4.6 and 5.7; 8 x
+  // 32768 tokens, 256 KB, 187 and 182.)
+  const int64_t cta_bytes = (int64_t)plan.split.part_pages * d->block_size * a.G * (int64_t)sizeof(float);
+  const bool one = !weight_rows && plan.split.max_parts <= kMaxClusterParts && cta_bytes <= 64 * 1024;
+  a.w_in = weights;
+  a.w_out = one ? weights_out : nullptr;
+  a.max_tokens = (size_t)max_tokens;
   const dim3 grid(plan.split.max_parts, d->num_kv_heads, d->num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(tk, tv, a, grid, sms, s)
@@ -240,7 +244,7 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
                                     : (d->block_size == 16 ? dispatch_logits<64, 16>(tk, tv, a, grid, sms, s)
                                                            : dispatch_logits<64, 32>(tk, tv, a, grid, sms, s));
   if (st != PA_OK) return st;
-  if (d->max_context_len == 0) return PA_OK;
+  if (one || d->max_context_len == 0) return PA_OK;
   WeightArgs w{};
   w.logits = a.logits;
   w.stats = a.stats;

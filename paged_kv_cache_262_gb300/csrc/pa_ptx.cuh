@@ -127,19 +127,27 @@ __device__ __forceinline__ void store2_hint(float *to, float x, float y, uint64_
   asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1,%2}, %3;" ::"l"(to), "f"(x), "f"(y), "l"(policy)
                : "memory");
 }
+template <int V>
+struct FloatVec;
+template <>
+struct FloatVec<1> { using type = float; };
+template <>
+struct FloatVec<2> { using type = float2; };
+template <>
+struct FloatVec<4> { using type = float4; };
 __device__ __forceinline__ float load_hint(const float *from, uint64_t policy) {
   float v;
-  asm volatile("ld.global.L2::cache_hint.f32 %0, [%1], %2;" : "=f"(v) : "l"(from), "l"(policy));
+  asm volatile("ld.global.cg.L2::cache_hint.f32 %0, [%1], %2;" : "=f"(v) : "l"(from), "l"(policy));
   return v;
 }
 __device__ __forceinline__ float2 load_hint(const float2 *from, uint64_t policy) {
   float2 v;
-  asm volatile("ld.global.L2::cache_hint.v2.f32 {%0,%1}, [%2], %3;" : "=f"(v.x), "=f"(v.y) : "l"(from), "l"(policy));
+  asm volatile("ld.global.cg.L2::cache_hint.v2.f32 {%0,%1}, [%2], %3;" : "=f"(v.x), "=f"(v.y) : "l"(from), "l"(policy));
   return v;
 }
 __device__ __forceinline__ float4 load_hint(const float4 *from, uint64_t policy) {
   float4 v;
-  asm volatile("ld.global.L2::cache_hint.v4.f32 {%0,%1,%2,%3}, [%4], %5;"
+  asm volatile("ld.global.cg.L2::cache_hint.v4.f32 {%0,%1,%2,%3}, [%4], %5;"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "l"(from), "l"(policy));
   return v;

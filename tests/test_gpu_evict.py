@@ -109,6 +109,33 @@ def test_weights_attention_is_decodes(torch):
     assert bool((w[0, :, 700:] == 0).all())
 
 
+@pytest.mark.parametrize("shape", [(8, 2, 128, 16), (16, 1, 64, 32), (3, 1, 64, 16)], ids=ids)
+@pytest.mark.parametrize("lens", [[1], [700], [1500, 3, 40], [9000], [30000, 100]])
+def test_weights_by_one_launch_and_by_two(torch, shape, lens):
+    """Few sequences of every length: units of one CTA, clusters, splits
+    through the workspace, the weights added by the CTAs and (with rows) by
+    the second kernel -- both within tolerance, and each its own bits again."""
+    R = _ref()
+    Hq, Hkv, D, B = shape
+    c = R.make_cache(lens, Hkv, D, B, seed=57, junk=float("nan"))
+    q = random_q(torch, len(lens), Hq, D)
+    w0 = random_weights(torch, len(lens), Hkv, c["mb"] * B)
+    rows = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    outs = []
+    for r in (None, rows):
+        again = []
+        for _ in range(2):
+            w, err = w0.clone(), err_of(torch)
+            out, _ = pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w, weight_rows=r,
+                                                       max_context_len=max(lens), err_flag=err)
+            assert int(err) == 0
+            again.append(w)
+        check_weights(torch, c, q, out, w0, w, 1 / math.sqrt(D))
+        assert torch.equal(*again)
+        outs.append(out)
+    assert same_bits(torch, *outs)
+
+
 def test_weights_summed_over_steps(torch):
     """Steps accumulate; a token added by a step starts from the zeros
     behind the context."""
