@@ -117,6 +117,22 @@ unsigned int next_decode_epoch() {
   return e;
 }
 
+namespace {
+
+// The workspace of a plan with max_parts parts a context.
+void size_plan(const pa_decode_desc *d, int max_parts, DecodePlan *p) {
+  p->ws_o_bytes = p->ws_ml_bytes = p->ws_cnt_bytes = 0;
+  if (max_parts <= 1 || d->num_seqs <= 0) return;
+  const size_t G = d->num_q_heads / d->num_kv_heads;
+  const size_t n = (size_t)d->num_seqs * d->num_kv_heads * max_parts * G;
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  p->ws_o_bytes = up(n * d->head_dim * sizeof(float));
+  p->ws_ml_bytes = up(n * 2 * sizeof(float));
+  p->ws_cnt_bytes = up((size_t)d->num_seqs * d->num_kv_heads * sizeof(unsigned long long));
+}
+
+}  // namespace
+
 // Split policy.  Each CTA streams one part (part_pages pages of one
 // (sequence, kv head)); two CTAs (16-token pages) or three (32-token pages)
 // are resident per SM.  The host knows only the longest-context bound, so it
@@ -160,14 +176,37 @@ DecodePlan make_decode_plan(const pa_decode_desc *d, int sm_count) {
   pp = std::max<int64_t>(pp, 1);
   p.part_pages = (int)pp;
   p.max_parts = (int)((max_pages + pp - 1) / pp);
-  if (p.max_parts > 1 && d->num_seqs > 0) {
-    const size_t G = d->num_q_heads / d->num_kv_heads;
-    const size_t n = (size_t)d->num_seqs * d->num_kv_heads * p.max_parts * G;
-    auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
-    p.ws_o_bytes = up(n * d->head_dim * sizeof(float));
-    p.ws_ml_bytes = up(n * 2 * sizeof(float));
-    p.ws_cnt_bytes = up((size_t)d->num_seqs * d->num_kv_heads * sizeof(unsigned long long));
+  size_plan(d, p.max_parts, &p);
+  return p;
+}
+
+// Units that leave room are cut into parts for one wave again, but parts that
+// join in a cluster are worth less work than those that join through the
+// workspace: down to 8 pages for up to 8 parts, and past those (each cluster of
+// 8 then goes through the workspace, about 2.5 us) 32, where 8 parts would be
+// longer than 48 pages.  (us for attention weights, by this plan and by the one
+// above with the workspace: one sequence of 32000 tokens, 8 kv heads, 29.7 and
+// 54.7; of 8000 18.3 and 29.3; of 1000, 1 kv head, 6.8 and 14.9.)
+// PA_PARTITION_PAGES as above.
+DecodePlan make_cluster_plan(const pa_decode_desc *d, int sm_count) {
+  DecodePlan p = make_decode_plan(d, sm_count);
+  const char *env = getenv("PA_PARTITION_PAGES");
+  const int64_t max_pages = std::max<int64_t>(1, ((int64_t)d->max_context_len + d->block_size - 1) / d->block_size);
+  const int64_t units = std::max<int64_t>(1, (int64_t)d->num_seqs * d->num_kv_heads);
+  const int64_t room = 2 * (int64_t)std::max(sm_count, 1) / units;  // parts a unit in one wave, two CTAs an SM
+  const int64_t least = (max_pages + kMaxPartPages - 1) / kMaxPartPages;
+  if (!(env && atoi(env) > 0) && room >= least && room >= 1) {
+    int64_t np = std::min<int64_t>(std::min<int64_t>(room, kClusterParts), std::max<int64_t>(1, max_pages / 8));
+    if (room >= 2 * kClusterParts && max_pages > 48 * np) {
+      np = std::min<int64_t>(std::min<int64_t>(room, kMaxParts), max_pages / 32);
+      np = std::max<int64_t>(kClusterParts, np / kClusterParts * kClusterParts);  // whole clusters
+    }
+    np = std::max(np, least);
+    p.part_pages = (int)((max_pages + np - 1) / np);
+    p.max_parts = (int)((max_pages + p.part_pages - 1) / p.part_pages);
+    size_plan(d, p.max_parts, &p);
   }
+  if (p.max_parts <= kClusterParts) p.ws_o_bytes = p.ws_ml_bytes = p.ws_cnt_bytes = 0;
   return p;
 }
 

@@ -10,6 +10,8 @@
 #include <math.h>
 #include <stdlib.h>
 
+#include <algorithm>
+
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "pagedattn.h"
@@ -71,7 +73,6 @@ struct DecodeArgs {
   // row's softmax statistics, from which a second kernel takes the weights.
   float *logits;    // [S][Hkv][max_ctx][G]
   float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys
-  float *ws_lw;     // [S][Hkv][max_parts][G]: the parts' sums of unrounded probabilities
   // Where a unit is one CTA or one cluster, it adds the weights itself: w_out
   // [S][Hkv][max_tokens] = w_in + weights (null: a second kernel does).
   const float *w_in;
@@ -158,10 +159,11 @@ struct DecodeSmem {
   static constexpr int kMetaOff = kStageOff + 2 * D * 2;  // GRP: per page, owner + 1 << 24 | logical block
   static constexpr int kBytes = kMetaOff + kMaxPartPages * 4;
   static constexpr int kAlloc = kBytes + 1024;  // base re-aligned to 1024 in the kernel
-  // CL: behind all that, the part's result for the cluster: o [16][D], m [16], l [16], lw [16]
-  static constexpr int kPartOff = (kBytes + 15) & ~15;
-  static constexpr int kPartBytes = (16 * D + 3 * 16) * 4;
-  static constexpr int kAllocCl = kPartOff + kPartBytes + 1024;
+  // CL: in the ring's room too, behind the merge buffers (with wts for a
+  // cluster a lane): the part's result for the cluster, o [16][D], m [16], l [16]
+  static constexpr int kPartOff = (NW * 16 * D + 2 * NW * 16 + 32 * 16) * 4;
+  static constexpr int kPartBytes = (16 * D + 2 * 16) * 4;
+  static_assert(kPartOff % 16 == 0 && kPartOff + kPartBytes <= kRegion0, "the part's result fits");
 };
 
 // Length class of a sequence for longest-first ordering: quarter-octave
@@ -240,10 +242,16 @@ __device__ int seq_of_rank(int r, const int32_t *ctx, int S, int B, int max_bloc
 // barrier `bar` for its own NW * 32 threads.  The decode kernel runs one unit
 // per CTA; the mixed-step kernel runs several side by side in one CTA.
 // SEL attends the blocks of a list instead of the whole context; WTS also
-// leaves the logits and softmax statistics for the attention weights.  CL: the
-// parts of a (sequence, kv head) are the CTAs of a cluster (launched with
-// max_parts along x), and join through one another's shared memory instead of
-// the workspace: no fence, no counter, no second trip to L2.
+// leaves the logits and softmax statistics for the attention weights.  Both take
+// the PV product with the probabilities as a bf16 value and a bf16 remainder
+// (2^-16 of a probability left) and sum them unrounded: the weights are fp32
+// and need that sum, and the second product, in kernels that wait for HBM, keeps
+// the output's error at its own rounding (0.0017 of the norm, 0.0023 with the
+// probabilities rounded once).  CL: the
+// parts of a (sequence, kv head) are the CTAs of clusters along x and join
+// through one another's shared memory (by way of the workspace a part costs the
+// last CTA to arrive about 0.5 us), more than eight of them then cluster by
+// cluster through the workspace.
 template <int D, int B, int NT, int NW, int NST, bool PRE, bool APP, bool GRP = false, bool TMA3 = false,
           bool SEL = false, bool WTS = false, bool CL = false>
 __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtensorMap *tmV, const DecodeArgs &a,
@@ -256,6 +264,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   constexpr int DT = D / 16;  // 16-row d tiles of O^T = V^T P^T
 
   constexpr bool FOLD = PRE || GRP;  // shared-prefix states to fold in at the end
+  constexpr bool FINE = SEL || WTS;  // probabilities in two bf16 terms
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
   int32_t *tbl = reinterpret_cast<int32_t *>(smem + L::kTblOff);
   int *misc = reinterpret_cast<int *>(smem + L::kMiscOff);
@@ -505,16 +514,11 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 
   // Running state.  Lane holds heads 8nt + 2(lane%4) + e (e = 0, 1) and, in o,
   // the O^T rows d = 16dt + lane/4 (+8).
-  // WTS: lw_run sums the probabilities before their rounding to bf16 (the
-  // rounded sum normalises the output, whose products saw rounded values; the
-  // weights are fp32).
   float m_run[NT][2], l_run[NT][2], o[NT][DT][4];
-  float lw_run[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m_run[nt][0] = m_run[nt][1] = -INFINITY;
     l_run[nt][0] = l_run[nt][1] = 0.f;
-    lw_run[nt][0] = lw_run[nt][1] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) o[nt][dt][0] = o[nt][dt][1] = o[nt][dt][2] = o[nt][dt][3] = 0.f;
   }
@@ -623,7 +627,8 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       // P (bf16 pairs) against the running maxima; a column that has seen no
       // key yet (maximum -inf) takes 0, so that no -inf - -inf appears
       uint32_t plo[MT][NT], phi[MT][NT];
-      float psum[NT][2];  // WTS: this page's unrounded probabilities, summed
+      uint32_t qlo[MT][NT], qhi[MT][NT];  // FINE: what the rounding to bf16 leaves of them
+      float psum[NT][2];                  // FINE: this page's unrounded probabilities, summed
       auto probabilities = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -636,9 +641,11 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
             const float p2_ = ex2_ftz(sc[mt][nt][2] - e0), p3_ = ex2_ftz(sc[mt][nt][3] - e1);
             plo[mt][nt] = pack_bf16(p0_, p1_);
             phi[mt][nt] = pack_bf16(p2_, p3_);
-            if constexpr (WTS) {
+            if constexpr (FINE) {
               psum[nt][0] += p0_ + p2_;
               psum[nt][1] += p1_ + p3_;
+              qlo[mt][nt] = pack_bf16(p0_ - bf16_lo(plo[mt][nt]), p1_ - bf16_hi(plo[mt][nt]));
+              qhi[mt][nt] = pack_bf16(p2_ - bf16_lo(phi[mt][nt]), p3_ - bf16_hi(phi[mt][nt]));
             }
           }
         }
@@ -664,8 +671,6 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           m_run[nt][1] = mn1;
           l_run[nt][0] *= al0;
           l_run[nt][1] *= al1;
-          lw_run[nt][0] *= al0;
-          lw_run[nt][1] *= al1;
 #pragma unroll
           for (int dt = 0; dt < DT; ++dt) {
             o[nt][dt][0] *= al0;
@@ -676,11 +681,11 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
         }
         probabilities();
       }
-      if constexpr (WTS) {
+      if constexpr (FINE) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          lw_run[nt][0] += psum[nt][0];
-          lw_run[nt][1] += psum[nt][1];
+          l_run[nt][0] += psum[nt][0];
+          l_run[nt][1] += psum[nt][1];
         }
       }
 
@@ -702,13 +707,19 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       // O^T[d][head] += V^T P^T, one 16-token k-tile at a time
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        uint32_t pb[NT][2];
+        uint32_t pb[NT][2], qb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          l_run[nt][0] += bf16_lo(plo[mt][nt]) + bf16_lo(phi[mt][nt]);
-          l_run[nt][1] += bf16_hi(plo[mt][nt]) + bf16_hi(phi[mt][nt]);
+          if constexpr (!FINE) {
+            l_run[nt][0] += bf16_lo(plo[mt][nt]) + bf16_lo(phi[mt][nt]);
+            l_run[nt][1] += bf16_hi(plo[mt][nt]) + bf16_hi(phi[mt][nt]);
+          }
           pb[nt][0] = movmatrix_t(plo[mt][nt]);
           pb[nt][1] = movmatrix_t(phi[mt][nt]);
+          if constexpr (FINE) {
+            qb[nt][0] = movmatrix_t(qlo[mt][nt]);
+            qb[nt][1] = movmatrix_t(qhi[mt][nt]);
+          }
         }
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
@@ -717,7 +728,10 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
           uint32_t af[4];
           ldsm_x4_t(vb + (c >> 3) * L::kBoxBytes + sw128(r, c & 7), af);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][dt], af, pb[nt][0], pb[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(o[nt][dt], af, pb[nt][0], pb[nt][1]);
+            if constexpr (FINE) mma_16816(o[nt][dt], af, qb[nt][0], qb[nt][1]);
+          }
         }
       }
     } else if (WTS) {  // a block outside the pool: its keys weigh nothing
@@ -743,10 +757,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], off);
-        if constexpr (WTS) lw_run[nt][e] += __shfl_xor_sync(0xffffffffu, lw_run[nt][e], off);
-      }
+      for (int off = 4; off < 32; off <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], off);
 
   // ---- merge the warps (ring memory is reused)
   unit_sync<NW * 32>(bar);
@@ -754,8 +765,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   float *red_m = red_o + NW * 16 * D;
   float *red_l = red_m + NW * 16;
   float *wts = red_l + NW * 16;
-  float *red_lw = reinterpret_cast<float *>(meta);  // WTS: [NW][16] (the page list's tags: block lists, sub-groups only)
-  float2 *st_s = reinterpret_cast<float2 *>(red_lw + NW * 16);  // WTS: [16] the heads' statistics
+  float2 *st_s = reinterpret_cast<float2 *>(meta);  // WTS: [16] the heads' statistics (in the page list's tags' room)
   // WTS: this CTA's tokens, once st_s is there
   auto own_weights = [&]() {
     const size_t u = (size_t)s * a.Hkv + kvh;
@@ -778,10 +788,6 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       red_m[warp * 16 + g + 1] = m_run[nt][1];
       red_l[warp * 16 + g] = l_run[nt][0];
       red_l[warp * 16 + g + 1] = l_run[nt][1];
-      if constexpr (WTS) {
-        red_lw[warp * 16 + g] = lw_run[nt][0];
-        red_lw[warp * 16 + g + 1] = lw_run[nt][1];
-      }
     }
   }
   unit_sync<NW * 32>(bar);
@@ -789,22 +795,16 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   const bool split = nparts > 1;
   const size_t unit = (size_t)s * a.Hkv + kvh;
   if constexpr (WTS) {
-    static_assert(!WTS || NW * 16 + 32 <= kMaxPartPages, "the warps' sums fit the page tags' room");
-    if (tid < G) {
+    if (tid < G && !split) {
       float mx = -INFINITY, l = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red_m[w * 16 + tid]);
       if (mx != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) l += red_lw[w * 16 + tid] * exp2f(red_m[w * 16 + tid] - mx);
+        for (int w = 0; w < NW; ++w) l += red_l[w * 16 + tid] * exp2f(red_m[w * 16 + tid] - mx);
       }
-      if (split && !CL)
-        a.ws_lw[(unit * a.max_parts + part) * G + tid] = l;
-      else if (split)
-        reinterpret_cast<float *>(smem + L::kPartOff)[16 * D + 32 + tid] = l;
-      else
-        st_s[tid] = a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
-            mx != -INFINITY ? make_float2(mx, 1.f / l) : make_float2(0.f, 0.f);
+      st_s[tid] = a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
+          mx != -INFINITY ? make_float2(mx, 1.f / l) : make_float2(0.f, 0.f);
     }
   }
   // Whole context in one CTA with a shared prefix before it: per query head,
@@ -913,44 +913,102 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   }
 
   if constexpr (CL) {
-    // ---- split-K in a cluster: every part joins a share of the outputs
+    // ---- split-K in clusters: the parts of one join, each a share of the
+    // outputs.  More than a cluster's parts: the clusters' results go to the
+    // workspace, and the last cluster to arrive joins those.
+    const int q = part / kClusterParts, nq = (nparts + kClusterParts - 1) / kClusterParts;
+    const int members = min(kClusterParts, nparts - q * kClusterParts), rank_ = part % kClusterParts;
+    const size_t slot = unit * (size_t)((a.max_parts + kClusterParts - 1) / kClusterParts) + q;  // of the workspace
     cluster_arrive();
     cluster_wait();
     const uint32_t base = smem_u32(smem + L::kPartOff);
     if (tid < G) {
-      float M = -INFINITY, den = 0.f, lw = 0.f;
-      for (int p = 0; p < nparts; ++p) {
-        const uint32_t at = cluster_addr(base, p) + (16 * D + tid) * 4;
-        const float m = cluster_load(at), l = cluster_load(at + 64);
-        if (l > 0.f) M = fmaxf(M, m);
+      float m[kClusterParts], l[kClusterParts];
+      float M = -INFINITY, den = 0.f;
+#pragma unroll
+      for (int p = 0; p < kClusterParts; ++p) {
+        const uint32_t at = cluster_addr(base, p < members ? p : 0) + (16 * D + tid) * 4;
+        m[p] = cluster_load(at);
+        l[p] = cluster_load(at + 64);
+        if (p < members && l[p] > 0.f) M = fmaxf(M, m[p]);
       }
-      for (int p = 0; p < nparts; ++p) {
-        const uint32_t at = cluster_addr(base, p) + (16 * D + tid) * 4;
-        const float m = cluster_load(at), l = cluster_load(at + 64);
-        const float w = l > 0.f ? l * exp2f(m - M) : 0.f;
-        wts[p * 16 + tid] = w;
-        den += w;
-        if (WTS && m != -INFINITY) lw += cluster_load(at + 128) * exp2f(m - M);
+#pragma unroll
+      for (int p = 0; p < kClusterParts; ++p) {
+        l[p] = p < members && l[p] > 0.f ? l[p] * exp2f(m[p] - M) : 0.f;
+        den += l[p];
       }
       const float inv = den > 0.f ? 1.f / den : 0.f;
-      for (int p = 0; p < nparts; ++p) wts[p * 16 + tid] *= inv;
-      if (WTS) {
-        st_s[tid] = M != -INFINITY ? make_float2(M, 1.f / lw) : make_float2(0.f, 0.f);
-        if (part == 0) a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] = st_s[tid];
+#pragma unroll
+      for (int p = 0; p < kClusterParts; ++p) wts[p * 16 + tid] = l[p] * inv;
+      if (nq > 1) {
+        if (rank_ == 0) reinterpret_cast<float2 *>(a.ws_ml)[slot * G + tid] = make_float2(M, den);
+      } else if constexpr (WTS) {
+        st_s[tid] = M != -INFINITY ? make_float2(M, inv) : make_float2(0.f, 0.f);
+        if (rank_ == 0) a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] = st_s[tid];
       }
     }
     unit_sync<NW * 32>(bar);
-    for (int idx = part * (NW * 32) + tid; idx < G * D; idx += nparts * (NW * 32)) {
+    for (int idx = rank_ * (NW * 32) + tid; idx < G * D; idx += members * (NW * 32)) {
       const int g = idx / D;
-      float acc = 0.f;
-      for (int p = 0; p < nparts; ++p) acc += wts[p * 16 + g] * cluster_load(cluster_addr(base, p) + idx * 4);
-      out_base[idx] = __float2bfloat16(acc);
+      float v[kClusterParts], acc = 0.f;
+#pragma unroll
+      for (int p = 0; p < kClusterParts; ++p)
+        v[p] = p < members ? cluster_load(cluster_addr(base, p) + idx * 4) : 0.f;
+#pragma unroll
+      for (int p = 0; p < kClusterParts; ++p) acc += wts[p * 16 + g] * v[p];
+      if (nq > 1)
+        a.ws_o[slot * G * D + idx] = acc;
+      else
+        out_base[idx] = __float2bfloat16(acc);
     }
+    if (nq > 1) __threadfence();
     cluster_arrive();  // nobody leaves while its part is being read
     if constexpr (WTS) {
       if (a.w_out) own_weights();
     }
     cluster_wait();
+    if (nq == 1 || rank_ != 0) return;
+    if (tid == 0) misc[0] = (arrive_count(a.ws_cnt + unit, a.epoch) == (unsigned int)nq);
+    unit_sync<NW * 32>(bar);
+    if (!misc[0]) return;
+    __threadfence();
+    const size_t first = slot - q;
+    for (int g = warp; g < G; g += NW) {  // a warp a head, a lane a cluster
+      static_assert(kMaxParts / kClusterParts <= 32, "a lane a cluster");
+      const float2 ml = lane < nq ? __ldcg(reinterpret_cast<const float2 *>(a.ws_ml) + (first + lane) * G + g)
+                                  : make_float2(-INFINITY, 0.f);
+      float M = ml.y > 0.f ? ml.x : -INFINITY;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float w = ml.y > 0.f ? ml.y * exp2f(ml.x - M) : 0.f;
+      float den = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      const float inv = den > 0.f ? 1.f / den : 0.f;
+      wts[lane * 16 + g] = w * inv;
+      if (WTS && lane == 0)
+        a.stats[(size_t)s * a.Hq + (size_t)kvh * G + g] =
+            M != -INFINITY ? make_float2(M, inv) : make_float2(0.f, 0.f);
+    }
+    unit_sync<NW * 32>(bar);
+    const float4 *po = reinterpret_cast<const float4 *>(a.ws_o + first * G * D);
+    for (int idx = tid; idx < G * D / 4; idx += NW * 32) {
+      const int g = idx / (D / 4);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p0 = 0; p0 < nq; p0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          v[p] = p0 + p < nq ? __ldcg(po + (size_t)(p0 + p) * (G * D / 4) + idx) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const float w = wts[(p0 + p) * 16 + g];  // (0 past nq)
+          acc.x += w * v[p].x, acc.y += w * v[p].y, acc.z += w * v[p].z, acc.w += w * v[p].w;
+        }
+      }
+      *reinterpret_cast<uint2 *>(out_base + 4 * idx) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    }
+    if (tid == 0) a.ws_cnt[unit] = 0ull;
     return;
   }
 
@@ -991,14 +1049,6 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       den += w;
     }
     const float inv = den > 0.f ? 1.f / den : 0.f;
-    if constexpr (WTS) {
-      float lw = 0.f;
-      for (int p = 0; p < nparts; ++p) {
-        const float m = __ldcg(a.ws_ml + 2 * ((ubase + p) * G + g));
-        if (m != -INFINITY) lw += __ldcg(a.ws_lw + (ubase + p) * G + g) * exp2f(m - M);
-      }
-      a.stats[row] = M != -INFINITY ? make_float2(M, 1.f / lw) : make_float2(0.f, 0.f);
-    }
     for (int p = 0; p < nparts; ++p) wts[p * 16 + g] *= inv;
     for (int p = 0; p < npre; ++p) wpre[p * 16 + g] *= inv;
   }
@@ -1015,21 +1065,25 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   if (tid == 0) a.ws_cnt[unit] = 0ull;
 }
 
-// Host: launches a decode kernel over grid (parts, kv heads, sequences): as one
-// cluster a (sequence, kv head) when a context has 2 .. 8 parts (`in_cluster`,
-// with smem_cl bytes of shared memory), else `plain`, joined through the
-// workspace.
-constexpr int kMaxClusterParts = 8;
+// Host: launches a decode kernel over a cluster plan's (parts, kv heads,
+// sequences) with `smem` bytes of shared memory: in clusters of up to
+// kClusterParts parts of a (sequence, kv head) when a context has more than one
+// (`in_cluster`), else `plain`.
 template <class K>
-int launch_parts(K plain, K in_cluster, int smem, int smem_cl, dim3 grid, int threads, const CUtensorMap &tk,
-                 const CUtensorMap &tv, const DecodeArgs &a, cudaStream_t st) {
-  const bool cl = grid.x > 1 && grid.x <= kMaxClusterParts;
-  K kern = cl ? in_cluster : plain;
-  const int bytes = cl ? smem_cl : smem;
-  if (bytes > 48 * 1024 &&  // (what a kernel may have without being asked)
-          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+int launch_parts(K plain, K in_cluster, int smem, const pa_decode_desc *d, int threads, const CUtensorMap &tk,
+                 const CUtensorMap &tv, DecodeArgs a, cudaStream_t st) {
+  const int parts = a.max_parts;
+  if (parts > kClusterParts) a.max_parts = (parts + kClusterParts - 1) / kClusterParts * kClusterParts;
+  K kern = parts > 1 ? in_cluster : plain;
+  // A wave of at most two CTAs an SM spreads over all of them only where a
+  // third does not fit (8 x 128 listed blocks: 16.9 us, 17.8 otherwise).
+  if (parts > 1 && (long long)a.max_parts * d->num_kv_heads * d->num_seqs <= 2ll * current_sm_count())
+    smem = std::max(smem, 77 * 1024);
+  if (smem > 48 * 1024 &&  // (what a kernel may have without being asked)
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return PA_ERR_CUDA;
-  return launch_dependent(kern, grid, threads, (size_t)bytes, cl ? (int)grid.x : 1, st, tk, tv, a);
+  return launch_dependent(kern, dim3(a.max_parts, d->num_kv_heads, d->num_seqs), threads, (size_t)smem,
+                          std::min(a.max_parts, kClusterParts), st, tk, tv, a);
 }
 
 // Host: the argument block of a decode launch over a validated desc with

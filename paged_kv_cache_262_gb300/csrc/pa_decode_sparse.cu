@@ -9,17 +9,19 @@
 //
 // The unit is the decode kernel's (pa_decode_body.cuh): the list's blocks are
 // resolved through the block table once and streamed by TMA into per-warp
-// rings, warp MMAs, online softmax in fp32.  A list has the same length for
-// every sequence, so the split plan is that of contexts of num_select blocks
-// and no unit is longer than another; the parts of a unit are a cluster and
-// join through shared memory (through the workspace: 22 us for the first case
-// below).
+// rings, warp MMAs, online softmax in fp32, the probabilities in two bf16 terms.
+// A list has the same length for every sequence, so the split plan is that of
+// contexts of num_select blocks and no unit is longer than another; the parts of
+// a unit are a cluster and join through shared memory (through the workspace:
+// 22 us for the second case below).
 //
 // The bytes bind: 240 sequences, 24 blocks of 32 tokens each at most, 8 kv heads
-// of 128: 103 us, 6.8 TB/s.  128 blocks of 16 for 8 sequences, 67 MB: 17.1 us,
-// 3.9 TB/s -- one wave of 256 CTAs, of which starting, three dependent loads,
-// the first gathers and the join are 7 us; more slots a warp or other parts
-// (16, 22, 43, 64 pages) are no faster.
+// of 128: 107 us, 6.5 TB/s (103 with the probabilities rounded once: with one
+// slot a warp the second product is not hidden).  128 blocks of 16 for 8
+// sequences, 67 MB: 16.9 us, 4.0 TB/s -- one wave of 256 CTAs, of which starting,
+// three dependent loads, the first gathers and the join are 7 us; more slots a
+// warp or other parts (16, 22, 43, 64 pages) are no faster.  One sequence, 256
+// blocks, 32 query and 8 kv heads: 10.3 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,10 +47,11 @@ __global__ void __launch_bounds__(128)
 }
 
 template <int D, int B, int NT>
-int launch_sparse(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
+int launch_sparse(const pa_decode_desc *d, const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a,
+                  cudaStream_t st) {
   constexpr int NST = B == 16 ? 2 : 1;
   return launch_parts(sparse_kernel<D, B, NT, NST, false>, sparse_kernel<D, B, NT, NST, true>,
-                      DecodeSmem<D, B, 4, NST>::kAlloc, DecodeSmem<D, B, 4, NST>::kAllocCl, grid, 128, tk, tv, a, st);
+                      DecodeSmem<D, B, 4, NST>::kAlloc, d, 128, tk, tv, a, st);
 }
 
 // The desc whose split plan a list of num_select blocks takes.
@@ -73,7 +76,7 @@ extern "C" size_t pa_decode_sparse_workspace_bytes(const pa_decode_desc *d, int 
   using namespace pa;
   if (validate_sparse(d, num_select) != PA_OK) return 0;
   const pa_decode_desc l = list_desc(d, num_select);
-  return make_decode_plan(&l, current_sm_count()).total();
+  return make_cluster_plan(&l, current_sm_count()).total();
 }
 
 extern "C" int pa_paged_attention_decode_sparse(const pa_decode_desc *d, const void *q, const void *k_pool,
@@ -91,7 +94,7 @@ extern "C" int pa_paged_attention_decode_sparse(const pa_decode_desc *d, const v
   const int sms = current_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   const pa_decode_desc l = list_desc(d, num_select);
-  const DecodePlan plan = make_decode_plan(&l, sms);
+  const DecodePlan plan = make_cluster_plan(&l, sms);
   if (plan.total() > 0 && (!workspace || workspace_bytes < plan.total() || !aligned16(workspace)))
     return PA_ERR_WORKSPACE;
   CUtensorMap tk, tv;
@@ -101,15 +104,14 @@ extern "C" int pa_paged_attention_decode_sparse(const pa_decode_desc *d, const v
   a.lpt = 0;  // every list has the same length
   a.sel = selected;
   a.nsel = num_select;
-  const dim3 grid(plan.max_parts, d->num_kv_heads, d->num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = a.G > 8;
   if (d->head_dim == 128) {
     if (d->block_size == 16)
-      return wide ? launch_sparse<128, 16, 2>(tk, tv, a, grid, s) : launch_sparse<128, 16, 1>(tk, tv, a, grid, s);
-    return wide ? launch_sparse<128, 32, 2>(tk, tv, a, grid, s) : launch_sparse<128, 32, 1>(tk, tv, a, grid, s);
+      return wide ? launch_sparse<128, 16, 2>(d, tk, tv, a, s) : launch_sparse<128, 16, 1>(d, tk, tv, a, s);
+    return wide ? launch_sparse<128, 32, 2>(d, tk, tv, a, s) : launch_sparse<128, 32, 1>(d, tk, tv, a, s);
   }
   if (d->block_size == 16)
-    return wide ? launch_sparse<64, 16, 2>(tk, tv, a, grid, s) : launch_sparse<64, 16, 1>(tk, tv, a, grid, s);
-  return wide ? launch_sparse<64, 32, 2>(tk, tv, a, grid, s) : launch_sparse<64, 32, 1>(tk, tv, a, grid, s);
+    return wide ? launch_sparse<64, 16, 2>(d, tk, tv, a, s) : launch_sparse<64, 16, 1>(d, tk, tv, a, s);
+  return wide ? launch_sparse<64, 32, 2>(d, tk, tv, a, s) : launch_sparse<64, 32, 1>(d, tk, tv, a, s);
 }

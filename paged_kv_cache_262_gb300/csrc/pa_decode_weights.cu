@@ -152,38 +152,38 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightArgs a) 
 
 struct WeightPlan {
   DecodePlan split;
-  size_t lw = 0, stats = 0, logits = 0;
-  size_t total() const { return split.total() + lw + stats + logits; }
+  size_t stats = 0, logits = 0;
+  size_t total() const { return split.total() + stats + logits; }
 };
 
 WeightPlan make_plan(const pa_decode_desc *d, int sms) {
   WeightPlan p;
-  p.split = make_decode_plan(d, sms);
+  p.split = make_cluster_plan(d, sms);
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const size_t G = d->num_q_heads / d->num_kv_heads, units = (size_t)d->num_seqs * d->num_kv_heads;
-  if (p.split.total() > 0) p.lw = up(units * p.split.max_parts * G * sizeof(float));
   p.stats = up(units * G * sizeof(float2));
   p.logits = up(units * G * (size_t)d->max_context_len * sizeof(float));
   return p;
 }
 
 template <int D, int B, int NT, int NST>
-int launch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, cudaStream_t st) {
+int launch_logits(const pa_decode_desc *d, const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a,
+                  cudaStream_t st) {
   return launch_parts(decode_logits_kernel<D, B, NT, NST, false>, decode_logits_kernel<D, B, NT, NST, true>,
-                      DecodeSmem<D, B, 4, NST>::kAlloc, DecodeSmem<D, B, 4, NST>::kAllocCl, grid, 128, tk, tv, a, st);
+                      DecodeSmem<D, B, 4, NST>::kAlloc, d, 128, tk, tv, a, st);
 }
 
 // Slots of a warp as in the plain decode: 16-token pages two when the units fit
 // one wave, else three; 32-token pages one.
 template <int D, int B>
-int dispatch_logits(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a, dim3 grid, int sms,
-                    cudaStream_t st) {
+int dispatch_logits(const pa_decode_desc *d, const CUtensorMap &tk, const CUtensorMap &tv, const DecodeArgs &a,
+                    int sms, cudaStream_t st) {
   if constexpr (B == 16) {
-    if (a.G <= 8 && (long long)grid.x * grid.y * grid.z <= 2ll * sms)
-      return launch_logits<D, B, 1, 2>(tk, tv, a, grid, st);
-    return a.G <= 8 ? launch_logits<D, B, 1, 3>(tk, tv, a, grid, st) : launch_logits<D, B, 2, 3>(tk, tv, a, grid, st);
+    if (a.G <= 8 && (long long)a.max_parts * a.Hkv * a.S <= 2ll * sms)
+      return launch_logits<D, B, 1, 2>(d, tk, tv, a, st);
+    return a.G <= 8 ? launch_logits<D, B, 1, 3>(d, tk, tv, a, st) : launch_logits<D, B, 2, 3>(d, tk, tv, a, st);
   } else {
-    return a.G <= 8 ? launch_logits<D, B, 1, 1>(tk, tv, a, grid, st) : launch_logits<D, B, 2, 1>(tk, tv, a, grid, st);
+    return a.G <= 8 ? launch_logits<D, B, 1, 1>(d, tk, tv, a, st) : launch_logits<D, B, 2, 1>(d, tk, tv, a, st);
   }
 }
 
@@ -224,25 +224,23 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   fill_decode_args(&a, d, plan.split, q, block_tables, context_lens, out, workspace, err_flag,
                    (long long)sms * (d->block_size == 16 ? 2 : 3));
   uint8_t *ws = static_cast<uint8_t *>(workspace) + plan.split.total();
-  a.ws_lw = reinterpret_cast<float *>(ws);
-  a.stats = reinterpret_cast<float2 *>(ws + plan.lw);
-  a.logits = reinterpret_cast<float *>(ws + plan.lw + plan.stats);
+  a.stats = reinterpret_cast<float2 *>(ws);
+  a.logits = reinterpret_cast<float *>(ws + plan.stats);
   // One launch where every (sequence, kv head) is a CTA or a cluster, rows are
   // not shared and a CTA's logits are at most 64 KB; else a second kernel, on
   // the whole GPU, adds the weights.  (us, one launch and two: 64 sequences up to
   // 2048 tokens, 32 KB a CTA, 49.2 and 51.6; four short ones 4.6 and 5.7; 8 x
   // 32768 tokens, 256 KB, 187 and 182.)
   const int64_t cta_bytes = (int64_t)plan.split.part_pages * d->block_size * a.G * (int64_t)sizeof(float);
-  const bool one = !weight_rows && plan.split.max_parts <= kMaxClusterParts && cta_bytes <= 64 * 1024;
+  const bool one = !weight_rows && plan.split.max_parts <= kClusterParts && cta_bytes <= 64 * 1024;
   a.w_in = weights;
   a.w_out = one ? weights_out : nullptr;
   a.max_tokens = (size_t)max_tokens;
-  const dim3 grid(plan.split.max_parts, d->num_kv_heads, d->num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(tk, tv, a, grid, sms, s)
-                                                           : dispatch_logits<128, 32>(tk, tv, a, grid, sms, s))
-                                    : (d->block_size == 16 ? dispatch_logits<64, 16>(tk, tv, a, grid, sms, s)
-                                                           : dispatch_logits<64, 32>(tk, tv, a, grid, sms, s));
+  const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(d, tk, tv, a, sms, s)
+                                                           : dispatch_logits<128, 32>(d, tk, tv, a, sms, s))
+                                    : (d->block_size == 16 ? dispatch_logits<64, 16>(d, tk, tv, a, sms, s)
+                                                           : dispatch_logits<64, 32>(d, tk, tv, a, sms, s));
   if (st != PA_OK) return st;
   if (one || d->max_context_len == 0) return PA_OK;
   WeightArgs w{};

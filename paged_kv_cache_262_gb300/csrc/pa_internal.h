@@ -84,6 +84,11 @@ int validate_decode_desc(const pa_decode_desc *d);
 // The plan used by both pa_decode_workspace_bytes and the launcher.
 DecodePlan make_decode_plan(const pa_decode_desc *d, int sm_count);
 
+// The plan of the kernels whose parts join in clusters of up to kClusterParts
+// (block lists, attention weights).  A workspace only past one cluster's parts.
+constexpr int kClusterParts = 8;
+DecodePlan make_cluster_plan(const pa_decode_desc *d, int sm_count);
+
 // A new tag for the split-K arrival counters of one decode launch: unique
 // (never 0) across every launcher that may share a workspace.
 unsigned int next_decode_epoch();

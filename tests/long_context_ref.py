@@ -85,17 +85,19 @@ def ref_select(q, bounds, bt, lens, B, G, k, sink, recent):
     return out
 
 
-def ref_attend(q, k, v, scale):
+def ref_attend(q, k, v, scale, once=False):
     """Softmax weights, outputs and their tolerances for [G][D] queries over
     [n][D] keys.
 
-    The kernel rounds the probabilities p to bf16 and divides by the sum of the
-    rounded ones: relative errors of at most 2^-8 each move the output by at
-    most 2^-8 sum p |v - out| <= 2^-8 (A + |out|), A = sum p |v|; its own
-    rounding is at most 2^-8 |out|.  Both rounded values and their products
-    are then of fp32: the logits x (base 2) are off by e_x (below), which moves
-    p by 2 ln2 e_x relative, ex2 by 2^-22, the sums by n terms cut at 2^-23 on
-    the partial sums, covered by 2^-12 of A + |out|.
+    The kernel takes each probability p as a bf16 value and a bf16 remainder,
+    which leave at most 2^-16 of it, and divides by the sum of the unrounded
+    ones: the output moves by at most 2^-16 A, A = sum p |v|.  (`once`: rounded
+    once, by 2^-8 each, and divided by the sum of the rounded ones: at most
+    2^-8 sum p |v - out| <= 2^-8 (A + |out|).)  The output's own rounding is at
+    most 2^-8 |out|.  The values and products are of fp32: the logits x (base
+    2) are off by e_x (below), which moves p by 2 ln2 e_x relative, ex2 by
+    2^-22, the sums by n terms cut at 2^-23 on the partial sums, covered by
+    2^-12 of A + |out|.
     """
     x = (q.double() @ k.T) * scale
     if x.shape[1] == 0:
@@ -109,7 +111,7 @@ def ref_attend(q, k, v, scale):
     ex = (q.double().abs() @ k.abs().T) * (abs(scale) * LOG2E * 17 * (q.shape[1] // 16) * 2.0**-23)
     ex = ex + x.abs() * LOG2E * 2.0**-22
     rel = 2 * math.log(2) * ex.amax(-1, keepdim=True)
-    tol = (2.0**-8 + 2.0**-12 + rel) * (A + out.abs()) + 2.0**-8 * out.abs() + 1e-30
+    tol = ((2.0**-8 if once else 2.0**-16) + 2.0**-12 + rel) * (A + out.abs()) + 2.0**-8 * out.abs() + 1e-30
     return p, out, tol, p * (rel + 2.0**-19)
 
 
