@@ -607,11 +607,16 @@ def _fast():
     if os.path.exists(_build.FAST):
         import importlib.machinery
         import importlib.util
-        import torch  # noqa: F401  (its libraries first)
+        import torch
         lib = load()
         loader = importlib.machinery.ExtensionFileLoader("_pa_fastcall", _build.FAST)
-        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_fastcall", loader))
-        loader.exec_module(mod)
+        try:
+            mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_fastcall", loader))
+            loader.exec_module(mod)
+        except ImportError:  # built for another torch
+            return _FAST
+        if mod.torch_version != torch.__version__:
+            return _FAST
         mod.bind(*(_c.cast(getattr(lib, n), _P).value for n in (
             "pa_block_key_bounds", "pa_select_blocks_workspace_bytes", "pa_select_blocks",
             "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",

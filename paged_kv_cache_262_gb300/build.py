@@ -57,7 +57,8 @@ def _fast_command(out: str) -> Optional[List[str]]:
            os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-w",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc], FAST_SRC,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DPA_TORCH_VERSION="{torch.__version__}"', *[f"-I{i}" for i in inc], FAST_SRC,
             "-o", out, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
             f"-Wl,-rpath,{libs}"]
 

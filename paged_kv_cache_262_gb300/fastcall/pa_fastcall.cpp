@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <cmath>
 
 #include "pagedattn.h"
 
@@ -304,4 +305,12 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_pa_fastcall", nullptr, -1, me
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pa_fastcall(void) { return PyModule_Create(&module_def); }
+PyMODINIT_FUNC PyInit__pa_fastcall(void) {
+  PyObject *m = PyModule_Create(&module_def);
+  // the torch that it was compiled against, and may be used with
+  if (m && PyModule_AddStringConstant(m, "torch_version", PA_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

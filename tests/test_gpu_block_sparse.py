@@ -372,6 +372,16 @@ def test_a_step_of_select_and_attend_in_graphs_and_on_streams(torch):
             step(qs[2 - i if i < 3 else 0])  # an eager call in between shares nothing with the graph
             torch.cuda.synchronize()
             assert torch.equal(r[0], want[i][0]) and same_bits(torch, r[1], want[i][1])
+    # the queries made in the graph, by other kernels between the calls
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = [step(q * 1 + 0) for _ in range(3)]
+    for i in (2, 0, 1):
+        q.copy_(qs[i])
+        g.replay()
+        torch.cuda.synchronize()
+        for x in r:
+            assert torch.equal(x[0], want[i][0]) and same_bits(torch, x[1], want[i][1])
     assert int(err) == 0
 
 
