@@ -220,7 +220,7 @@ __device__ void select_row(const SelectArgs &a, RowSelect<SW> &r, size_t row, in
   auto key1 = [&](int i) {
     return in_smem ? reinterpret_cast<const uint32_t *>(r.keys)[i] : __ldcg(keys + i);
   };
-  const float slack = 2.f * kScoreError<D> * A;
+  const float slack = 2.f * kScoreError<D> * A + 1e-30f;  // (and what products below fp32's normal range lose)
   const bool finite = slack < INFINITY;  // false for NaN too: then no fp32 score is trusted
   uint32_t lo = 0u, hi = 0xfffffffeu;    // (no score's key is above it)
   int above = 0;
@@ -366,8 +366,9 @@ __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kerne
   const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
   const int i_end = min(end, (chunk + 1) * a.chunk);
 
-  // lane l's block of a tile: row l / 4 and that + 8; -2: not competing
-  auto page = [&](int i) -> int { return i >= first && i < i_end ? __ldg(bt + i) : -2; };
+  // lane l's block of a tile: row l / 4 and that + 8; -1: outside the pool, -2:
+  // not competing
+  auto page = [&](int i) -> int { return i >= first && i < i_end ? max(__ldg(bt + i), -1) : -2; };
   int i0 = chunk * a.chunk + warp * 16;
   int pg[2] = {page(i0 + (lane >> 2)), page(i0 + 8 + (lane >> 2))};
 

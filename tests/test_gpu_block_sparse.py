@@ -182,6 +182,17 @@ def test_select_near_ties(torch):
         assert torch.equal(got, R.ref_select(q, b, bt, [n * 16], 16, 1, k, 0, 0))
 
 
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-20, 1e20])
+def test_select_at_the_ends_of_the_range(torch, size):
+    R = _ref()
+    c, b, q, G = select_case(torch, (8, 2, 128, 16), [2000, 333], seed=15)
+    b = (b.float() * size).to(torch.bfloat16)
+    for scale in (1.0, 1e-6):
+        x = (q.float() * scale).to(torch.bfloat16)
+        got = pa.select_blocks(x, b, c["bt"], c["ctx"], 9, block_size=16, sink_blocks=1, recent_blocks=1)
+        assert torch.equal(got, R.ref_select(x, b, c["bt"], c["lens"], 16, G, 9, 1, 1))
+
+
 @pytest.mark.parametrize("what", ["inf_bound", "nan_bound", "inf_query", "nan_query", "overflow", "minus"])
 def test_select_with_values_that_are_not_finite(torch, what):
     R = _ref()
@@ -220,6 +231,11 @@ def test_select_refusals_on_the_device(torch):
     bt[0, top] = c["k"].shape[0] + 3
     got = pa.select_blocks(q, b, bt, c["ctx"], 6, block_size=16, err_flag=err)
     assert int(err) == pa.DEVERR_PAGE and top not in got[0, 0].tolist() and torch.equal(got[1:], want[1:])
+    for entry in (-1, -2, -3, -2**31, 2**31 - 1):
+        bt[0, top] = entry
+        err.zero_()
+        assert torch.equal(pa.select_blocks(q, b, bt, c["ctx"], 6, block_size=16, err_flag=err), got)
+        assert int(err) == pa.DEVERR_PAGE, entry
     # fewer readable blocks than asked for: all of them, then the first unreadable ones
     bt = c["bt"].clone()
     bt[0, 3:37] = -5
