@@ -464,6 +464,91 @@ def test_calls_on_two_streams_at_once(torch):
             assert all(torch.equal(x, y) for x, y in zip(r, want[i]))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("quick", [True, False])
+def test_the_first_call_of_a_thread(torch, monkeypatch, D, quick):
+    """A new host thread has no context of its own yet."""
+    import threading
+
+    if not quick:
+        monkeypatch.setattr(pa._binding, "_FAST", False)
+    c = _ref().make_cache([300, 40], 2, D, 16, seed=35)
+    q = torch.randn(2, 8, D, device="cuda").to(torch.bfloat16)
+    b = torch.zeros(c["k"].shape[0], 2, 2, D, dtype=torch.bfloat16, device="cuda")
+    pa.block_key_bounds(c["k"], b, c["bt"], c["ctx"])
+    fresh = torch.zeros_like(b)
+    w = [torch.zeros(2, 2, c["mb"] * 16, device="cuda") for _ in range(2)]
+    sel = pa.select_blocks(q, b, c["bt"], c["ctx"], 6, block_size=16)
+    calls = [
+        lambda i: pa.block_key_bounds(c["k"], fresh if i else b, c["bt"], c["ctx"]),
+        lambda i: pa.select_blocks(q, b, c["bt"], c["ctx"], 6, block_size=16),
+        lambda i: pa.paged_attention_decode_sparse(q, c["k"], c["v"], c["bt"], c["ctx"], sel),
+        lambda i: pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w[i])[0],
+        lambda i: pa.paged_attention_decode(q, c["k"], c["v"], c["bt"], c["ctx"]),
+    ]
+    for f in calls:
+        want, got = f(0), []
+
+        def run():
+            try:
+                got.append(f(1))
+            except Exception as e:  # noqa: BLE001
+                got.append(e)
+
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        assert isinstance(got[0], torch.Tensor) and torch.equal(got[0], want), got
+    assert torch.equal(w[0], w[1])
+
+
+def test_calls_from_two_threads_on_one_stream(torch):
+    """The two launches of a call with weights share a default workspace with
+    every other such call on the stream: no other thread's come between them."""
+    import threading
+
+    R = _ref()
+    c = R.make_cache([5000, 900, 40], 2, 64, 16, seed=34)
+    rows = torch.tensor([1, 0, 1], dtype=torch.int32, device="cuda")  # a shared row: by two launches
+    qs = [torch.randn(3, 8, 64, device="cuda").to(torch.bfloat16) for _ in range(2)]
+
+    def step(x, w, out):
+        return pa.paged_attention_decode_weights(x, c["k"], c["v"], c["bt"], c["ctx"], w, out, weight_rows=rows)
+
+    def zeros():
+        return torch.zeros(2, 2, c["mb"] * 16, device="cuda")
+
+    want = [zeros() for _ in qs]
+    outs = [step(x, w, None)[0] for x, w in zip(qs, want)]
+    torch.cuda.synchronize()
+    ws = [[zeros() for _ in range(200)] for _ in qs]
+    got = [[torch.empty_like(x) for _ in range(200)] for x in qs]
+    start = threading.Barrier(2)
+    failed = []
+
+    def run(i):
+        try:
+            start.wait(60)
+            for n, (w, out) in enumerate(zip(ws[i], got[i])):
+                if n % 2:
+                    step(qs[i], w, out)  # the way through ctypes
+                else:
+                    out.copy_(step(qs[i], w, None)[0])
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i in range(2):
+        assert all(torch.equal(w, want[i]) for w in ws[i])
+        assert all(torch.equal(o, outs[i]) for o in got[i])
+
+
 def test_offsets_beyond_32_bits(torch):
     """Blocks at the end of a pool of more than 2^31 elements."""
     R = _ref()
