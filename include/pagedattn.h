@@ -328,7 +328,7 @@ int pa_paged_attention_mixed(const pa_decode_desc *prefill_desc, const void *pre
  * Eviction shortens the cache itself:
  *   pa_paged_attention_decode_weights  decode, and every key's weight summed
  *   pa_evict_tokens      now and then: the heaviest keys stay, compacted
- *   pa_bm_evict          the block manager's part of it
+ *   pa_bm_evict, pa_bm_evict_batch  the block manager's part of it
  * ------------------------------------------------------------------------ */
 
 /* Channel-wise bounds of every block's keys:
@@ -440,8 +440,9 @@ int pa_paged_attention_decode_weights(const pa_decode_desc *desc, const void *q,
  * Block bounds of the written blocks are stale until pa_block_key_bounds.
  *   dst_tables  device int32 [num_seqs][max_blocks_per_seq], or NULL: in place.
  *               Entry i of a row is block_tables' own entry i or a block that no
- *               table of the call reads (pa_bm_evict hands out such tables: shared
- *               blocks are replaced, own ones stay).  No block is a destination
+ *               table of the call reads (pa_bm_evict hands out such a table for one
+ *               sequence, pa_bm_evict_batch for several: shared blocks are
+ *               replaced, own ones stay).  No block is a destination
  *               of two sequences, or a destination of one and read by another.
  *   keep_lens   device int32 [num_seqs], 1 .. max_keep_len
  *   weights, weights_out, weight_rows, num_rows, max_tokens  as in
@@ -671,6 +672,19 @@ int pa_bm_swap_in(pa_bm *bm, int seq_id, int64_t *pairs_out, int cap, int *n);
  * fresh ones, of which none may be a released one: those are still read) leave
  * everything unchanged. */
 int pa_bm_evict(pa_bm *bm, int seq_id, int keep_len, int32_t *dst_out, int cap, int *n);
+
+/* The evictions of seq_ids[0..n-1] (distinct) to keep_lens[0..n-1] tokens, for
+ * one pa_evict_tokens call over all of them.  As pa_bm_evict for each, except
+ * that fresh blocks replace all that were shared before the call, for every
+ * holder in it, and none is released before the last is taken: no sequence's
+ * destination is another's source, which tables from several pa_bm_evict calls
+ * do not promise (those go to a pa_evict_tokens call each, in order).  Row i
+ * of dst_out[n][max_blocks] is sequence i's table, then pad; new_lens_out (may be
+ * NULL) its length.  Source tables: pa_bm_block_tables before this call.
+ * PA_ERR_STATE, PA_ERR_INVALID (a repeated id, a keep_len < 1, a table longer than
+ * max_blocks, null pointers, n < 0) and PA_ERR_OOM leave everything unchanged. */
+int pa_bm_evict_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *keep_lens, int n, int32_t *dst_out,
+                      int max_blocks, int32_t pad, int32_t *new_lens_out);
 
 /* Number of free host blocks. */
 int pa_bm_num_free_host(const pa_bm *bm);

@@ -36,6 +36,7 @@ EXPORTS = (
     "pa_block_key_bounds", "pa_select_blocks_workspace_bytes", "pa_select_blocks",
     "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
     "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens", "pa_bm_evict",
+    "pa_bm_evict_batch",
 )
 
 
@@ -166,6 +167,8 @@ def load(path: Optional[str] = None):
         lib.pa_paged_attention_decode_weights.argtypes = [D, _P, _P, _P, _P, _P, _P, _P, _P, i, i, _P, _P, sz, _P, _P]
         lib.pa_evict_tokens.restype = i
         lib.pa_evict_tokens.argtypes = [D, _P, _P, _P, _P, _P, _P, i, i, i, _P, _P, _P, i, i, _P, _P, _P, _P]
+        lib.pa_bm_evict_batch.restype = i
+        lib.pa_bm_evict_batch.argtypes = [_P, _P, _P, i, _P, i, i, _P]
         lib.pa_bm_evict.restype = i
         lib.pa_bm_evict.argtypes = [_P, i, i, _c.POINTER(_c.c_int32), i, _c.POINTER(i)]
         if path is None:
@@ -1052,7 +1055,8 @@ class BlockManager:
     def evict(self, seq_id: int, keep_len: int):
         """Shortens seq_id to keep_len tokens; returns the block table that
         evict_tokens moves them into (its source table is block_table() from
-        before this call)."""
+        before this call).  For several sequences in one evict_tokens call:
+        evict_batch."""
         cap = 64
         while True:
             buf = (_c.c_int32 * cap)()
@@ -1063,6 +1067,23 @@ class BlockManager:
                 continue
             _check(st, "pa_bm_evict")
             return list(buf[:n.value])
+
+    def evict_batch(self, seq_ids, keep_lens, max_blocks: int, pad: int = -1):
+        """Shortens each of `seq_ids` (distinct) to its keep_lens tokens, for
+        one evict_tokens call over all of them; returns its dst_tables int32
+        [n, max_blocks] and the new lengths int32 [n] (the source tables are
+        block_tables() from before this call).  On an error nothing has
+        changed."""
+        import numpy as np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32).reshape(-1)
+        keep = np.ascontiguousarray(keep_lens, dtype=np.int32).reshape(-1)
+        if keep.size != ids.size:
+            raise ValueError("keep_lens needs one length per sequence")
+        out = np.empty((ids.size, int(max_blocks)), np.int32)
+        lens = np.empty(ids.size, np.int32)
+        _check(self._lib.pa_bm_evict_batch(self._h, ids.ctypes.data, keep.ctypes.data, int(ids.size), out.ctypes.data,
+                                           int(max_blocks), int(pad), lens.ctypes.data), "pa_bm_evict_batch")
+        return out, lens
 
     def add_seq_tokens(self, seq_id: int, tokens) -> int:
         """New sequence holding the prompt `tokens` (a 1-D sequence of int32

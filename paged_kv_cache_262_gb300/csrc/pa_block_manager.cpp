@@ -196,6 +196,22 @@ struct pa_bm {
       ++nfree;
     }
   }
+  // s goes down to len tokens in dst[0..nb-1]: its own blocks, whose content
+  // changes, or blocks taken for it.
+  void shorten(Seq &s, int len, const int32_t *dst, size_t nb) {
+    for (size_t i = 0; i < nb; ++i) {
+      if (dst[i] != s.blocks[i])
+        drop(s.blocks[i]);
+      else
+        uncache(dst[i]);  // and what continues it: no other sequence holds that either
+      s.blocks[i] = dst[i];
+    }
+    for (size_t i = s.blocks.size(); i-- > nb;) drop(s.blocks[i]);
+    s.blocks.resize(nb);
+    s.len = len;
+    s.tracked = false;
+    s.tail.clear();
+  }
   bool needs_block(const Seq &s) const {  // appending to s takes a free block
     return s.len % block_size == 0 || ref[s.blocks[s.len / block_size]] > 1;
   }
@@ -603,24 +619,57 @@ int pa_bm_evict(pa_bm *bm, int seq_id, int keep_len, int32_t *dst_out, int cap, 
     if (fresh > bm->nfree) return PA_ERR_OOM;
     // Fresh blocks first: the released ones are sources of the same eviction.
     // Nothing below allocates.
-    for (size_t i = 0; i < nb; ++i) {
-      int32_t &b = s.blocks[i];
-      if (bm->ref[b] > 1) {
-        const int32_t old = b;
-        b = bm->take();
-        bm->drop(old);
-      } else {
-        bm->uncache(b);  // and what continues it: no other sequence holds that either
-      }
-    }
-    for (size_t i = s.blocks.size(); i-- > nb;) bm->drop(s.blocks[i]);
-    s.blocks.resize(nb);
-    s.len = keep_len;
-    s.tracked = false;
-    s.tail.clear();
+    for (size_t i = 0; i < nb; ++i) dst_out[i] = bm->ref[s.blocks[i]] > 1 ? bm->take() : s.blocks[i];
+    bm->shorten(s, keep_len, dst_out, nb);
+    return PA_OK;
   }
   std::copy(s.blocks.begin(), s.blocks.end(), dst_out);
   return PA_OK;
+}
+
+int pa_bm_evict_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *keep_lens, int n, int32_t *dst_out,
+                      int max_blocks, int32_t pad, int32_t *new_lens_out) {
+  if (!bm || n < 0 || max_blocks < 0 || (n > 0 && (!seq_ids || !keep_lens || (!dst_out && max_blocks > 0))))
+    return PA_ERR_INVALID;
+  if (n == 0) return PA_OK;
+  return guarded([&]() -> int {
+    // every check and allocation first: a failure leaves no trace
+    bm->batch_seqs.resize(n);
+    Seq **sq = bm->batch_seqs.data();
+    const uint64_t call = ++bm->batch_no;
+    const int64_t B = bm->block_size;
+    auto blocks_of = [&](int i) -> size_t {
+      return keep_lens[i] < sq[i]->len ? (size_t)((keep_lens[i] + B - 1) / B) : sq[i]->blocks.size();
+    };
+    int64_t fresh = 0;
+    for (int i = 0; i < n; ++i) {
+      auto it = bm->seqs.find(seq_ids[i]);
+      if (it == bm->seqs.end() || it->second.swapped) return PA_ERR_STATE;
+      Seq &s = it->second;
+      if (s.stamp == call || keep_lens[i] < 1) return PA_ERR_INVALID;  // listed twice
+      s.stamp = call;
+      sq[i] = &s;
+      const size_t nb = blocks_of(i);
+      if ((int64_t)nb > max_blocks) return PA_ERR_INVALID;
+      if (keep_lens[i] < s.len)
+        for (size_t j = 0; j < nb; ++j) fresh += bm->ref[s.blocks[j]] > 1;
+    }
+    if (fresh > (int64_t)bm->nfree) return PA_ERR_OOM;
+    // All the tables before anything is released: what is shared now is a
+    // source of another sequence, and so is what will be released.
+    for (int i = 0; i < n; ++i) {
+      const Seq &s = *sq[i];
+      const size_t nb = blocks_of(i);
+      int32_t *row = dst_out + (size_t)i * max_blocks;
+      for (size_t j = 0; j < nb; ++j)
+        row[j] = keep_lens[i] < s.len && bm->ref[s.blocks[j]] > 1 ? bm->take() : s.blocks[j];
+      std::fill(row + nb, row + max_blocks, pad);
+      if (new_lens_out) new_lens_out[i] = std::min(keep_lens[i], s.len);
+    }
+    for (int i = 0; i < n; ++i)
+      if (keep_lens[i] < sq[i]->len) bm->shorten(*sq[i], keep_lens[i], dst_out + (size_t)i * max_blocks, blocks_of(i));
+    return PA_OK;
+  });
 }
 
 int pa_bm_num_free_host(const pa_bm *bm) { return bm ? (int)bm->host_free.size() : -1; }

@@ -156,3 +156,148 @@ def test_among_the_other_calls(seed):
                 held[b] = held.get(b, 0) + 1
         assert [bm.ref_count(b) for b in range(N)] == [held.get(b, 0) for b in range(N)]
         assert bm.num_free() == N - len(held)
+
+
+# ---------------------------------------------------------------- several at once
+def test_a_batch_replaces_what_any_of_it_reads():
+    """Two holders of the same blocks and a third sequence: one by one, the
+    last holder would stay in place over the first one's source, and released
+    tails would come back as fresh blocks."""
+    bm = pa.BlockManager(32, 4)
+    bm.add_seq(0, 16)
+    bm.fork(0, 1)
+    bm.append(1)
+    bm.add_seq(2, 30)
+    tables, lens = bm.block_tables([0, 1, 2], 10)
+    assert lens.tolist() == [16, 17, 30]
+    dst, new = bm.evict_batch([0, 1, 2], [6, 9, 13], 10, pad=-7)
+    assert new.tolist() == [6, 9, 13] and dst.shape == (3, 10)
+    rows = [dst[i, :n].tolist() for i, n in enumerate((2, 3, 4))]
+    assert [(dst[i, n:] == -7).all() for i, n in enumerate((2, 3, 4))] == [True] * 3
+    assert rows[2] == tables[2, :4].tolist()  # its own, in place
+    assert not (set(rows[0]) | set(rows[1])) & set(tables[tables >= 0].tolist())
+    assert len(set(sum(rows, []))) == 9
+    assert [bm.block_table(s) for s in range(3)] == rows and [bm.seq_len(s) for s in range(3)] == [6, 9, 13]
+    assert bm.num_free() == 32 - 9
+
+
+def test_a_batch_of_one_is_the_single_call():
+    for keep in (1, 4, 5, 16, 17, 40):
+        a, b = pa.BlockManager(32, 4), pa.BlockManager(32, 4)
+        for m in (a, b):
+            m.add_seq(0, 16)
+            m.fork(0, 1)
+            m.append(1)
+        dst, new = a.evict_batch([1], [keep], 8)
+        one = b.evict(1, keep)
+        assert dst[0, :len(one)].tolist() == one and (dst[0, len(one):] == -1).all()
+        assert new.tolist() == [b.seq_len(1)] and a.num_free() == b.num_free()
+    dst, new = a.evict_batch([], [], 4)
+    assert dst.shape == (0, 4) and new.shape == (0,)
+
+
+def test_a_batch_with_sequences_that_stay():
+    bm = pa.BlockManager(16, 4)
+    bm.add_seq(0, 12)
+    bm.fork(0, 1)
+    t = bm.block_table(0)
+    dst, new = bm.evict_batch([0, 1], [12, 5], 3)
+    assert dst[0].tolist() == t and new.tolist() == [12, 5]
+    assert not set(dst[1, :2].tolist()) & set(t) and bm.block_table(0) == t and bm.num_free() == 16 - 5
+
+
+def test_a_refused_batch_leaves_everything():
+    import numpy as np
+    bm = pa.BlockManager(8, 4, 8)
+    bm.add_seq(0, 16)
+    bm.fork(0, 1)
+    bm.append(1)
+    bm.add_seq(2, 3)
+    state = lambda: ([bm.block_table(s) for s in (0, 1, 2)], [bm.seq_len(s) for s in (0, 1, 2)],  # noqa: E731
+                     bm.num_free())
+    was = state()
+    for ids, keep, mb, status in (([0, 9], [4, 4], 8, pa.PA_ERR_STATE), ([0, 0], [4, 4], 8, pa.PA_ERR_INVALID),
+                                  ([0, 1], [4, 0], 8, pa.PA_ERR_INVALID), ([0, 1], [4, -3], 8, pa.PA_ERR_INVALID),
+                                  ([2, 1], [1, 9], 2, pa.PA_ERR_INVALID), ([0, 1], [6, 6], 8, pa.PA_ERR_OOM)):
+        with pytest.raises(pa.PaError) as e:
+            bm.evict_batch(ids, keep, mb)
+        assert e.value.status == status and state() == was
+    with pytest.raises(ValueError):
+        bm.evict_batch([0, 1], [4], 8)
+    f = pa.load().pa_bm_evict_batch
+    i, k, o = (np.array(x, np.int32) for x in ([0], [4], [0, 0]))
+    P = lambda x: x.ctypes.data  # noqa: E731
+    assert f(None, P(i), P(k), 1, P(o), 2, -1, None) == pa.PA_ERR_INVALID
+    assert f(bm._h, None, P(k), 1, P(o), 2, -1, None) == pa.PA_ERR_INVALID
+    assert f(bm._h, P(i), None, 1, P(o), 2, -1, None) == pa.PA_ERR_INVALID
+    assert f(bm._h, P(i), P(k), 1, None, 2, -1, None) == pa.PA_ERR_INVALID
+    assert f(bm._h, P(i), P(k), -1, P(o), 2, -1, None) == pa.PA_ERR_INVALID
+    assert f(bm._h, P(i), P(k), 1, P(o), -1, -1, None) == pa.PA_ERR_INVALID
+    assert f(bm._h, None, None, 0, None, 0, -1, None) == pa.PA_OK and state() == was
+    bm.swap_out(2)
+    with pytest.raises(pa.PaError) as e:
+        bm.evict_batch([0, 2], [1, 1], 8)
+    assert e.value.status == pa.PA_ERR_STATE
+    assert f(bm._h, P(i), P(k), 1, P(o), 2, -1, None) == pa.PA_OK and bm.seq_len(0) == 4
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_batches_among_the_other_calls(seed):
+    """Random calls: a batch's destinations are distinct, each its sequence's
+    own entry or a block that no table of the batch held; the counts, the free
+    blocks and the prefix cache's answers fit the tables afterwards."""
+    r = random.Random(100 + seed)
+    B, N = 4, 64
+    bm, lens, nxt = pa.BlockManager(N, B), {}, 0
+    for _ in range(300):
+        op = r.random()
+        try:
+            if op < 0.25 or not lens:
+                n = r.randint(0, 30)
+                bm.add_seq_tokens(nxt, [r.randint(0, 1) for _ in range(n)])
+                lens[nxt], nxt = n, nxt + 1
+            elif op < 0.4:
+                s = r.choice(list(lens))
+                bm.fork(s, nxt)
+                lens[nxt], nxt = lens[s], nxt + 1
+            elif op < 0.6:
+                ids = r.sample(list(lens), r.randint(1, len(lens)))
+                bm.append_batch(ids, [r.randint(0, 1) for _ in ids])
+                for s in ids:
+                    lens[s] += 1
+            elif op < 0.9:
+                ids = r.sample(list(lens), r.randint(1, len(lens)))
+                keep = [r.randint(1, 30) for _ in ids]
+                src, _ = bm.block_tables(ids, 40)
+                dst, new = bm.evict_batch(ids, keep, 40)
+                read = set(src[src >= 0].tolist())
+                written = []
+                for i, s in enumerate(ids):
+                    n = -(-min(keep[i], lens[s]) // B)
+                    assert new[i] == min(keep[i], lens[s]) and (dst[i, n:] == -1).all()
+                    assert all(d == src[i, j] or d not in read for j, d in enumerate(dst[i, :n].tolist()))
+                    if keep[i] < lens[s]:
+                        written += dst[i, :n].tolist()
+                        assert not set(dst[i, :n].tolist()) & {int(x) for j in range(len(ids)) if j != i
+                                                               for x in src[j] if x >= 0}
+                        lens[s] = keep[i]
+                    assert bm.block_table(s) == dst[i, :n].tolist()
+                assert len(set(written)) == len(written)
+            else:
+                s = r.choice(list(lens))
+                bm.free_seq(s)
+                del lens[s]
+        except pa.PaError as e:
+            assert e.status == pa.PA_ERR_OOM
+            if r.random() < 0.5:
+                s = r.choice(list(lens))
+                bm.free_seq(s)
+                del lens[s]
+        held = {}
+        for s in lens:
+            t = bm.block_table(s)
+            assert bm.seq_len(s) == lens[s] and len(t) == -(-lens[s] // B) and len(set(t)) == len(t)
+            for b in t:
+                held[b] = held.get(b, 0) + 1
+        assert [bm.ref_count(b) for b in range(N)] == [held.get(b, 0) for b in range(N)]
+        assert bm.num_free() == N - len(held) and 0 <= bm.num_cached_blocks() <= N

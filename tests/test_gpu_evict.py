@@ -557,3 +557,34 @@ def test_long_context_loop(torch):
         for s in (0, 1):
             check(s, out[s], sel[s])
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("max_blocks", [40, 64])
+def test_several_sequences_of_a_block_manager_in_one_eviction(torch, max_blocks):
+    """Samples of one prompt and other sequences, shortened together: every
+    kept row comes from its sequence's blocks as they were before the call."""
+    R = _ref()
+    B, Hkv, D, N = 16, 2, 128, 150
+    bm = pa.BlockManager(N, B)
+    bm.add_seq(0, 300)
+    bm.fork(0, 1)
+    bm.fork(0, 2)
+    bm.append_batch([1, 2])
+    bm.add_seq(3, 500)
+    bm.add_seq(4, 40)
+    bm.fork(4, 5)
+    ids, keep = [3, 1, 0, 2, 5], [200, 150, 299, 301, 17]
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k, v = (torch.randn(N, Hkv, B, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    bt, lens = bm.block_tables(ids, max_blocks)
+    dst, new = bm.evict_batch(ids, keep, max_blocks)
+    assert new.tolist() == [200, 150, 299, 301, 17] and lens.tolist() == [500, 301, 300, 301, 40]
+    c = dict(k=k, v=v, bt=torch.as_tensor(bt).cuda(), ctx=torch.as_tensor(lens).cuda(), lens=lens.tolist(), B=B, D=D,
+             Hkv=Hkv, mb=max_blocks)
+    w0 = random_weights(torch, len(ids), Hkv, max_blocks * B)
+    w, before, err = w0.clone(), (k.clone(), v.clone()), err_of(torch)
+    dt = torch.as_tensor(dst).cuda()
+    got = pa.evict_tokens(k, v, c["bt"], c["ctx"], torch.as_tensor(keep, dtype=torch.int32).cuda(), w, max_keep_len=301,
+                          sink_tokens=2, recent_tokens=9, dst_tables=dt, err_flag=err)
+    assert int(err) == 0 and got[1].tolist() == new.tolist()
+    check_evict(torch, c, before, got, w0, w, keep, 2, 9, dt, 301)
