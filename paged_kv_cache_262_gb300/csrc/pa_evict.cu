@@ -48,6 +48,19 @@ struct EvictArgs {
   size_t max_tokens;
 };
 
+// Weights that nothing has written yet in this kernel: the compiler may order
+// these loads as it likes, and so has several on their way.
+__device__ __forceinline__ float4 load_weights(const float *p) {
+  float4 x;
+  asm("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float load_weight(const float *p) {
+  float x;
+  asm("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+
 // grid (kv head, sequence).  A row of weights that fits is held in shared
 // memory as ordered keys, which give the weights back (NaN and -0 as the usual
 // NaN and +0), so that what is kept leaves straight from there, in place or
@@ -139,19 +152,33 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
   }
   for (int i = tid; i < a.recent; i += NT) kept[n - a.recent + i] = ctx - a.recent + i;
   if (want > 0) {
+    // Not held: four weights a load, from a 16-byte boundary on; the `lead` ones
+    // before the first get key 0, which is below every weight's.
+    const int lead = in_smem ? 0 : (int)(reinterpret_cast<uintptr_t>(wc) >> 2) & 3;
+    const float *wa = wc - lead;
+    const int n_keys = N + lead;
     auto key4 = [&](int i) {
       if (in_smem) return keys4(*reinterpret_cast<const uint4 *>(skeys + i));
       Keys4<uint32_t> k;
+      if (i + 4 <= n_keys) {
+        const float4 x = load_weights(wa + i);
+        k = Keys4<uint32_t>{{order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w)}};
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) k.v[e] = i + e < N ? order_key(wc[i + e]) : 0u;
+        for (int e = 0; e < 4; ++e) k.v[e] = i + e < n_keys ? order_key(load_weight(wa + i + e)) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (i + e < lead) k.v[e] = 0u;
       return k;
     };
-    auto key1 = [&](int i) { return in_smem ? skeys[i] : order_key(wc[i]); };
-    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key4, N, want, sm, tid, least, most);
-    take_above<NT, uint32_t>(key4, key1, N, t.key, want - t.above, want, sm, tid, [&](int pos, int i, uint32_t k) {
-      kept[a.sink + pos] = a.sink + i;
-      if (in_smem) wo[a.sink + pos] = key_value(k);
-    });
+    auto key1 = [&](int i) { return in_smem ? skeys[i] : i < lead ? 0u : order_key(load_weight(wa + i)); };
+    const Kth<uint32_t> t = kth_largest<NT, uint32_t>(key4, n_keys, want, sm, tid, least, most);
+    take_above<NT, uint32_t>(key4, key1, n_keys, t.key, want - t.above, want, sm, tid,
+                             [&](int pos, int i, uint32_t k) {
+                               kept[a.sink + pos] = a.sink + i - lead;
+                               if (in_smem) wo[a.sink + pos] = key_value(k);
+                             });
   }
   if (in_smem && a.recent <= kEnd * NT) {
 #pragma unroll
