@@ -390,7 +390,9 @@ size_t pa_decode_sparse_workspace_bytes(const pa_decode_desc *desc, int num_sele
  * selected[s][h][0 .. num_select-1] (logical indices, any order; -1 for none)
  * of each kv head h.  A block listed twice counts twice.  A list without
  * blocks gives zero rows.  An index that is neither -1 nor one of the
- * context's blocks is left out and sets PA_DEVERR_PAGE.
+ * context's blocks is left out and sets PA_DEVERR_PAGE.  A NaN or +infinite
+ * logit of a listed key makes its query head's row NaN, a key whose logit is
+ * -infinity weighs nothing (a row of nothing else is zeros).
  *   selected   device int32 [num_seqs][num_kv_heads][num_select]
  *   workspace  >= pa_decode_sparse_workspace_bytes(desc, num_select)
  * Other arguments and errors as in pa_paged_attention_decode. */
@@ -409,7 +411,9 @@ size_t pa_decode_weights_workspace_bytes(const pa_decode_desc *desc);
  * sequences s with row r = weight_rows[s],
  *   weights_out[r][h][j] = weights[r][h][j] + sum_s sum_g p_sgj,
  * p the softmax weights (fp32) of h's query heads g, j < context_lens[s].
- * Positions that no context of the row reaches are not written.  A row is
+ * Positions that no context of the row reaches are not written.  Logits that
+ * are not finite: as in pa_paged_attention_decode_sparse; the weights of a head
+ * with a NaN row are NaN over its whole context.  A row is
  * summed in the order of its sequences: several entries may name one row (the
  * last queries of a prompt, each with its own context, over one block table).
  *   weights, weights_out  device fp32 [num_rows][num_kv_heads][max_tokens],

@@ -72,7 +72,7 @@ struct DecodeArgs {
   // Attention weights (WTS launches): every key's logit (base 2) and every
   // row's softmax statistics, from which a second kernel takes the weights.
   float *logits;    // [S][Hkv][max_ctx][G]
-  float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys
+  float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys, (., NaN) for a NaN sum
   // Where a unit is one CTA or one cluster, it adds the weights itself: w_out
   // [S][Hkv][max_tokens] = w_in + weights (null: a second kernel does).
   const float *w_in;
@@ -93,6 +93,10 @@ __device__ __forceinline__ unsigned int arrive_count(unsigned long long *c, unsi
     old = prev;
   }
 }
+
+// The maximum to take exponents against: 0 for a row that has none (-infinity),
+// where 2^(-inf - -inf) would be NaN.
+__device__ __forceinline__ float max_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
 // Adds the attention weights of tokens beg .. end - 1 of one (sequence, kv
 // head): w_out[j] = w_in[j] + sum_g 2^(x_jg - st[g].x) st[g].y, x the logits
@@ -247,8 +251,9 @@ __device__ int seq_of_rank(int r, const int32_t *ctx, int S, int B, int max_bloc
 // (2^-16 of a probability left) and sum them unrounded: the weights are fp32
 // and need that sum, and the second product, in kernels that wait for HBM, keeps
 // the output's error at its own rounding (0.0017 of the norm, 0.0023 with the
-// probabilities rounded once).  CL: the
-// parts of a (sequence, kv head) are the CTAs of clusters along x and join
+// probabilities rounded once).  In both a logit of NaN or +infinity makes its
+// row's sum NaN, and every join passes that on: only a sum of 0 stands for no
+// keys.  CL: the parts of a (sequence, kv head) are the CTAs of clusters along x and join
 // through one another's shared memory (by way of the workspace a part costs the
 // last CTA to arrive about 0.5 us), more than eight of them then cluster by
 // cluster through the workspace.
@@ -259,6 +264,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
   using L = DecodeSmem<D, B, NW, NST>;
   static_assert(NW <= 4, "misc holds four warp totals");
   static_assert(!(SEL || WTS || CL) || !(PRE || APP || GRP), "block lists and weights: plain decode only");
+  static_assert(!CL || SEL || WTS, "the join in clusters passes NaN on");
   constexpr int KS = D / 16;  // k-steps of S^T = K Q^T
   constexpr int MT = B / 16;  // 16-token tiles per page
   constexpr int DT = D / 16;  // 16-row d tiles of O^T = V^T P^T
@@ -799,12 +805,10 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       float mx = -INFINITY, l = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red_m[w * 16 + tid]);
-      if (mx != -INFINITY) {
+      mx = max_or_0(mx);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) l += red_l[w * 16 + tid] * exp2f(red_m[w * 16 + tid] - mx);
-      }
-      st_s[tid] = a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] =
-          mx != -INFINITY ? make_float2(mx, 1.f / l) : make_float2(0.f, 0.f);
+      for (int w = 0; w < NW; ++w) l += red_l[w * 16 + tid] * exp2f(red_m[w * 16 + tid] - mx);
+      st_s[tid] = a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] = make_float2(mx, l == 0.f ? 0.f : 1.f / l);
     }
   }
   // Whole context in one CTA with a shared prefix before it: per query head,
@@ -853,14 +857,16 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 #pragma unroll
     for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red_m[w * 16 + g]);
     float l = 0.f, acc = 0.f;
-    if (mx != -INFINITY) {
+    if (FINE || mx != -INFINITY) {
+      const float base = FINE ? max_or_0(mx) : mx;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float f = exp2f(red_m[w * 16 + g] - mx);
+        const float f = exp2f(red_m[w * 16 + g] - base);
         l += red_l[w * 16 + g] * f;
         acc += red_o[(w * 16 + g) * D + d] * f;
       }
     }
+    const bool some = FINE ? l != 0.f : l > 0.f;  // FINE: a NaN sum is no empty one
     if (!split) {
       float res;
       if (npre > 0) {  // fold in the shared prefix's partial states
@@ -880,7 +886,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
 #pragma unroll
         for (int p = 0; p < kMaxPrefixParts; ++p) res += coef[16 * (p + 1) + g] * po[p];
       } else {
-        res = l > 0.f ? acc / l : 0.f;
+        res = some ? acc / l : 0.f;
       }
       if (GRP)
         a.out[row_of(g) * D + d] = __float2bfloat16(res);
@@ -888,7 +894,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
         out_base[idx] = __float2bfloat16(res);
     } else if constexpr (CL) {
       float *mine = reinterpret_cast<float *>(smem + L::kPartOff);
-      mine[idx] = l > 0.f ? acc / l : 0.f;
+      mine[idx] = some ? acc / l : 0.f;
       if (d == 0) {
         mine[16 * D + g] = mx;
         mine[16 * D + 16 + g] = l;
@@ -930,20 +936,21 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
         const uint32_t at = cluster_addr(base, p < members ? p : 0) + (16 * D + tid) * 4;
         m[p] = cluster_load(at);
         l[p] = cluster_load(at + 64);
-        if (p < members && l[p] > 0.f) M = fmaxf(M, m[p]);
+        if (p < members && l[p] != 0.f) M = fmaxf(M, m[p]);
       }
+      M = max_or_0(M);
 #pragma unroll
       for (int p = 0; p < kClusterParts; ++p) {
-        l[p] = p < members && l[p] > 0.f ? l[p] * exp2f(m[p] - M) : 0.f;
+        l[p] = p < members && l[p] != 0.f ? l[p] * exp2f(m[p] - M) : 0.f;
         den += l[p];
       }
-      const float inv = den > 0.f ? 1.f / den : 0.f;
+      const float inv = den != 0.f ? 1.f / den : 0.f;
 #pragma unroll
       for (int p = 0; p < kClusterParts; ++p) wts[p * 16 + tid] = l[p] * inv;
       if (nq > 1) {
         if (rank_ == 0) reinterpret_cast<float2 *>(a.ws_ml)[slot * G + tid] = make_float2(M, den);
       } else if constexpr (WTS) {
-        st_s[tid] = M != -INFINITY ? make_float2(M, inv) : make_float2(0.f, 0.f);
+        st_s[tid] = make_float2(M, inv);
         if (rank_ == 0) a.stats[(size_t)s * a.Hq + (size_t)kvh * G + tid] = st_s[tid];
       }
     }
@@ -977,18 +984,17 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap *tmK, const CUtens
       static_assert(kMaxParts / kClusterParts <= 32, "a lane a cluster");
       const float2 ml = lane < nq ? __ldcg(reinterpret_cast<const float2 *>(a.ws_ml) + (first + lane) * G + g)
                                   : make_float2(-INFINITY, 0.f);
-      float M = ml.y > 0.f ? ml.x : -INFINITY;
+      float M = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float w = ml.y > 0.f ? ml.y * exp2f(ml.x - M) : 0.f;
+      M = max_or_0(M);
+      const float w = ml.y != 0.f ? ml.y * exp2f(ml.x - M) : 0.f;
       float den = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-      const float inv = den > 0.f ? 1.f / den : 0.f;
+      const float inv = den != 0.f ? 1.f / den : 0.f;
       wts[lane * 16 + g] = w * inv;
-      if (WTS && lane == 0)
-        a.stats[(size_t)s * a.Hq + (size_t)kvh * G + g] =
-            M != -INFINITY ? make_float2(M, inv) : make_float2(0.f, 0.f);
+      if (WTS && lane == 0) a.stats[(size_t)s * a.Hq + (size_t)kvh * G + g] = make_float2(M, inv);
     }
     unit_sync<NW * 32>(bar);
     const float4 *po = reinterpret_cast<const float4 *>(a.ws_o + first * G * D);

@@ -115,6 +115,24 @@ def ref_attend(q, k, v, scale, once=False):
     return p, out, tol, p * (rel + 2.0**-19)
 
 
+def ref_attend_any(q, k, v, scale):
+    """ref_attend for any keys: a head with a NaN or +infinite logit has NaN
+    weights and a NaN row, a key of -infinity weighs nothing (a head that has
+    no others gives zeros)."""
+    x = (q.double() @ k.T) * scale
+    p, tp = torch.zeros_like(x), torch.zeros_like(x)
+    out = torch.zeros(q.shape[0], v.shape[1], dtype=torch.float64, device=q.device)
+    tol = torch.zeros_like(out)
+    for g in range(q.shape[0]):
+        if bool((torch.isnan(x[g]) | (x[g] == math.inf)).any()):
+            p[g], out[g] = math.nan, math.nan
+            continue
+        live = x[g] != -math.inf
+        r = ref_attend(q[g:g + 1], k[live], v[live], scale)
+        p[g, live], out[g], tol[g], tp[g, live] = (y[0] for y in r)
+    return p, out, tol, tp
+
+
 def ref_evict(w, n, sink, recent, ctx):
     """Kept tokens of one row of weights [ctx]."""
     if n >= ctx:

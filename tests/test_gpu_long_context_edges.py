@@ -1,0 +1,118 @@
+"""The long-context calls at their edges: logits and values that are not
+finite, refused sequences, calls from several host threads, launches that
+fail."""
+import math
+
+import pytest
+
+import paged_kv_cache_262_gb300 as pa
+from gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return need_gpu()
+
+
+def _ref():
+    import long_context_ref
+    return long_context_ref
+
+
+def err_of(torch):
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------ values that are not finite
+NOT_FINITE = ["nan_key", "nan_query", "inf_key", "all_nan", "nan_value"]
+#: (query heads, kv heads, head_dim, block), contexts, PA_PARTITION_PAGES: one
+#: CTA a (sequence, kv head), clusters, and several clusters joined
+SPLITS = [((8, 2, 64, 16), [1, 40, 1000, 300], None), ((8, 2, 128, 16), [1, 40, 1000, 300], "1"),
+          ((16, 1, 64, 32), [1, 40, 1000, 300], "3"), ((6, 2, 128, 32), [1, 40, 1000, 300], "512"),
+          ((4, 1, 64, 16), [30000, 20], None), ((20, 2, 128, 16), [9000, 20], None)]
+
+
+def not_finite_case(torch, what, shape, lens):
+    """Caches and queries with such a value in every sequence but the second."""
+    R = _ref()
+    Hq, Hkv, D, B = shape
+    c = R.make_cache(lens, Hkv, D, B, seed=81, junk=float("nan"))
+    q = torch.randn(len(lens), Hq, D, device="cuda",
+                    generator=torch.Generator(device="cuda").manual_seed(82)).to(torch.bfloat16)
+    for s, n in enumerate(lens):
+        if s == 1:
+            continue
+        j = n // 2
+        blk, at = int(c["bt"][s, j // B]), j % B
+        if what == "nan_key":
+            c["k"][blk, Hkv - 1, at, 3] = math.nan
+        elif what == "nan_query":
+            q[s, Hq - 1, 5] = math.nan
+        elif what == "inf_key":  # +infinity for some heads, -infinity for others
+            c["k"][blk, 0, at, 7] = math.inf
+        elif what == "all_nan":
+            c["k"][c["bt"][s, :-(-n // B)].long(), 0] = math.nan
+        else:
+            c["v"][blk, 0, at, 9] = math.nan
+    return c, q
+
+
+def as_wanted(torch, got, want, tol):
+    nan = torch.isnan(want)
+    return torch.equal(torch.isnan(got), nan) and bool(((got - want).abs() <= tol)[~nan].all())
+
+
+@pytest.mark.parametrize("what", NOT_FINITE)
+@pytest.mark.parametrize("shape,lens,pp", SPLITS)
+def test_sparse_reports_what_is_not_finite(torch, monkeypatch, what, shape, lens, pp):
+    """A NaN or +infinite logit makes its head's row NaN, however the list is
+    split; -infinity weighs nothing."""
+    R = _ref()
+    monkeypatch.delenv("PA_PARTITION_PAGES", raising=False)
+    if pp:
+        monkeypatch.setenv("PA_PARTITION_PAGES", pp)
+    Hq, Hkv, D, B = shape
+    G = Hq // Hkv
+    c, q = not_finite_case(torch, what, shape, lens)
+    k = max(-(-n // B) for n in lens)
+    sel = torch.full((len(lens), Hkv, k), -1, dtype=torch.int32, device="cuda")
+    for s, n in enumerate(lens):
+        sel[s, :, :-(-n // B)] = torch.arange(-(-n // B), dtype=torch.int32, device="cuda")
+    err = err_of(torch)
+    out = pa.paged_attention_decode_sparse(q, c["k"], c["v"], c["bt"], c["ctx"], sel, err_flag=err)
+    assert int(err) == 0
+    for s, n in enumerate(lens):
+        for h in range(Hkv):
+            _, want, tol, _ = R.ref_attend_any(q[s, h * G:(h + 1) * G], R.rows(c["k"], c["bt"][s], n, B, h),
+                                               R.rows(c["v"], c["bt"][s], n, B, h), 1 / math.sqrt(D))
+            assert as_wanted(torch, out[s, h * G:(h + 1) * G].double(), want, tol), (s, h)
+
+
+@pytest.mark.parametrize("what", NOT_FINITE)
+@pytest.mark.parametrize("shape,lens,pp", SPLITS)
+@pytest.mark.parametrize("with_rows", [False, True])
+def test_weights_report_what_is_not_finite(torch, monkeypatch, what, shape, lens, pp, with_rows):
+    """The same for decode with weights; the weights of a kv head with such a
+    row are NaN, by one launch and by two (with_rows)."""
+    R = _ref()
+    monkeypatch.delenv("PA_PARTITION_PAGES", raising=False)
+    if pp:
+        monkeypatch.setenv("PA_PARTITION_PAGES", pp)
+    Hq, Hkv, D, B = shape
+    G = Hq // Hkv
+    c, q = not_finite_case(torch, what, shape, lens)
+    rows = torch.arange(len(lens), dtype=torch.int32, device="cuda") if with_rows else None
+    w, err = torch.zeros(len(lens), Hkv, c["mb"] * B, device="cuda"), err_of(torch)
+    out, _ = pa.paged_attention_decode_weights(q, c["k"], c["v"], c["bt"], c["ctx"], w, weight_rows=rows,
+                                               max_context_len=max(lens), err_flag=err)
+    assert int(err) == 0
+    for s, n in enumerate(lens):
+        for h in range(Hkv):
+            p, want, tol, tp = R.ref_attend_any(q[s, h * G:(h + 1) * G], R.rows(c["k"], c["bt"][s], n, B, h),
+                                                R.rows(c["v"], c["bt"][s], n, B, h), 1 / math.sqrt(D))
+            assert as_wanted(torch, out[s, h * G:(h + 1) * G].double(), want, tol), (s, h)
+            # (the tolerance of the weights: their probabilities', and 2^-24 an addition)
+            assert as_wanted(torch, w[s, h, :n].double(), p.sum(0), tp.sum(0) + 2.0**-20 * p.sum(0)), (s, h)
+            assert bool((w[s, h, n:] == 0).all())
