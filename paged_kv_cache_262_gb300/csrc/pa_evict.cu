@@ -240,7 +240,9 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvictArgs 
   auto &sm = *reinterpret_cast<MoveSmem<ST, IX> *>(smem_raw);
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
   grid_wait();
-  const int n = min(__ldcg(a.new_lens + s), a.max_keep);  // (the kernel before writes these)
+  // (The kernel before writes these; of a refused sequence it is the context, which
+  // may be past the table.)
+  const int n = min(min(__ldcg(a.new_lens + s), a.max_keep), a.max_blocks * a.B);
   const int32_t *kept = a.kept + ((size_t)s * a.Hkv + h) * a.max_keep;
   const int32_t *bt = a.bt + (size_t)s * a.max_blocks, *dt = a.dst + (size_t)s * a.max_blocks;
   const int B = a.B, lb = B == 16 ? 4 : 5;

@@ -116,3 +116,38 @@ def test_weights_report_what_is_not_finite(torch, monkeypatch, what, shape, lens
             # (the tolerance of the weights: their probabilities', and 2^-24 an addition)
             assert as_wanted(torch, w[s, h, :n].double(), p.sum(0), tp.sum(0) + 2.0**-20 * p.sum(0)), (s, h)
             assert bool((w[s, h, n:] == 0).all())
+
+
+# ---------------------------------------------------------- refused sequences
+@pytest.mark.parametrize("S,Hkv,D", [(2, 2, 64), (3, 8, 128), (40, 8, 128)])
+@pytest.mark.parametrize("blocks", [4, 9])
+def test_evict_refuses_a_context_past_its_table(torch, S, Hkv, D, blocks):
+    """max_keep_len above the table's capacity, and in the last row a context
+    past it: refused, and nothing behind the tables' rows is read (tables that
+    end their allocation; every form of the row kernel)."""
+    R = _ref()
+    B = 16
+    lens = [blocks * B - s % 7 for s in range(S)]
+    c = R.make_cache(lens, Hkv, D, B, seed=86)
+    bt = c["bt"][:, :blocks].contiguous()
+    dst, ctx = bt.clone(), c["ctx"].clone()
+    ctx[S - 1] = 5000
+    max_keep, keep = 4096, torch.full((S,), 20, dtype=torch.int32, device="cuda")
+    keep[S - 1] = 4096
+    k0, v0 = c["k"].clone(), c["v"].clone()
+    w0 = torch.rand(S, Hkv, 5000, device="cuda")
+    w, err = w0.clone(), err_of(torch)
+    kept, new = pa.evict_tokens(c["k"], c["v"], bt, ctx, keep, w, max_keep_len=max_keep, dst_tables=dst,
+                                max_context_len=5000, err_flag=err)
+    assert int(err) == pa.DEVERR_CTX and new.tolist() == [20] * (S - 1) + [5000]
+    assert bool((kept[S - 1] == -1).all()) and torch.equal(w[S - 1], w0[S - 1])
+    for s, n in enumerate(lens[:-1]):
+        for h in range(Hkv):
+            at = R.ref_evict(w0[s, h, :n], 20, 0, 0, n)
+            assert torch.equal(kept[s, h, :20].long(), at) and bool((kept[s, h, 20:] == -1).all())
+            i = torch.arange(20, device="cuda")
+            src, to = bt[s].long()[at // B], bt[s].long()[i // B]
+            for pool, old in ((c["k"], k0), (c["v"], v0)):
+                assert torch.equal(pool[to, h, i % B], old[src, h, at % B])
+    last = bt[S - 1].long()
+    assert torch.equal(c["k"][last], k0[last]) and torch.equal(c["v"][last], v0[last])
