@@ -1083,11 +1083,14 @@ int launch_parts(K plain, K in_cluster, int smem, const pa_decode_desc *d, int t
   K kern = parts > 1 ? in_cluster : plain;
   // A wave of at most two CTAs an SM spreads over all of them only where a
   // third does not fit (8 x 128 listed blocks: 16.9 us, 17.8 otherwise).
-  if (parts > 1 && (long long)a.max_parts * d->num_kv_heads * d->num_seqs <= 2ll * current_sm_count())
-    smem = std::max(smem, 77 * 1024);
-  if (smem > 48 * 1024 &&  // (what a kernel may have without being asked)
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  constexpr int kSpread = 77 * 1024;
+  // What the kernel may have is its own, not a launch's: always the most that any
+  // launch takes, so that host threads that launch it at once set the same.
+  const int most = parts > 1 ? std::max(smem, kSpread) : smem;
+  if (most > 48 * 1024 &&  // (what a kernel may have without being asked)
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
     return PA_ERR_CUDA;
+  if (parts > 1 && (long long)a.max_parts * d->num_kv_heads * d->num_seqs <= 2ll * current_sm_count()) smem = most;
   return launch_dependent(kern, dim3(a.max_parts, d->num_kv_heads, d->num_seqs), threads, (size_t)smem,
                           std::min(a.max_parts, kClusterParts), st, tk, tv, a);
 }

@@ -151,3 +151,46 @@ def test_evict_refuses_a_context_past_its_table(torch, S, Hkv, D, blocks):
                 assert torch.equal(pool[to, h, i % B], old[src, h, at % B])
     last = bt[S - 1].long()
     assert torch.equal(c["k"][last], k0[last]) and torch.equal(c["v"][last], v0[last])
+
+
+# ------------------------------------------------------ several host threads
+def test_small_and_large_grids_from_several_threads(torch, monkeypatch):
+    """Launches of one kernel with unlike amounts of shared memory, made at
+    the same time: a grid of a wave asks for more than a larger one does."""
+    import ctypes
+    import threading
+
+    R = _ref()
+    monkeypatch.setenv("PA_PARTITION_PAGES", "1")  # three parts a list
+    Hkv, Hq, D, B = 2, 8, 128, 16
+    c = R.make_cache([48], Hkv, D, B, seed=83)
+    lib, stream = pa.load(), torch.cuda.current_stream().cuda_stream
+    calls, outs, want, keep = [], [], [], []
+    for S in (1, 120, 2, 90):  # 6, 720, 12 and 540 CTAs
+        q = torch.randn(S, Hq, D, device="cuda").to(torch.bfloat16)
+        sel = torch.arange(3, dtype=torch.int32, device="cuda").expand(S, Hkv, 3).contiguous()
+        bt, ctx, out = c["bt"].expand(S, -1).contiguous(), c["ctx"].expand(S).contiguous(), torch.empty_like(q)
+        want.append(pa.paged_attention_decode_sparse(q, c["k"], c["v"], bt, ctx, sel))
+        desc = pa.DecodeDesc(S, Hq, Hkv, D, B, c["k"].shape[0], bt.shape[1], 48, D**-0.5)
+        assert lib.pa_decode_sparse_workspace_bytes(ctypes.byref(desc), 3) == 0
+        calls.append((ctypes.byref(desc), q.data_ptr(), c["k"].data_ptr(), c["v"].data_ptr(), bt.data_ptr(),
+                      ctx.data_ptr(), sel.data_ptr(), 3, out.data_ptr(), None, 0, None, stream))
+        outs.append(out)
+        keep.append((q, sel, bt, ctx))
+    torch.cuda.synchronize()
+    start, status = threading.Barrier(len(calls)), [set() for _ in calls]
+
+    def run(i):
+        f, args, seen = lib.pa_paged_attention_decode_sparse, calls[i], status[i]
+        start.wait(60)
+        for _ in range(4000):  # (the interpreter lock is free while the C call runs)
+            seen.add(f(*args))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{pa.PA_OK}] * len(calls), status
+    assert all(torch.equal(x, y) for x, y in zip(outs, want))
