@@ -452,7 +452,8 @@ int pa_paged_attention_decode_weights(const pa_decode_desc *desc, const void *q,
  *   weights, weights_out, weight_rows, num_rows, max_tokens  as in
  *               pa_paged_attention_decode_weights
  *   kept        device int32 [num_seqs][num_kv_heads][max_keep_len], -1 past n
- *   new_lens    device int32 [num_seqs], not context_lens itself
+ *   new_lens    device int32 [num_seqs]; it and kept overlap neither each other
+ *               nor context_lens, keep_lens, weight_rows or a table
  * num_q_heads and scale of desc are not used (but must be valid).  A bad
  * context, a keep_len outside 1 .. max_keep_len or below sink + recent where
  * tokens would go (PA_DEVERR_CTX), and a row out of range or named by an earlier

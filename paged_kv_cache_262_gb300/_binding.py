@@ -930,10 +930,16 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
     _all(dev, (kept, "kept", i32, 3), (new_lens, "new_lens", i32, 1))
     if kept.shape != (S, hkv, mk) or new_lens.shape[0] != S:
         _bad(f"kept must be [{S}][{hkv}][{mk}] and new_lens [{S}]")
-    if S and new_lens.data_ptr() == context_lens.data_ptr():
-        _bad("new_lens must not be context_lens")
     most = mb * bs if max_context_len is None else int(max_context_len)
     weights_out, nr, width = _weight_args(T, weights, weights_out, weight_rows, S, hkv, most, dev)
+    spans = [(name, t.data_ptr(), t.data_ptr() + 4 * n) for name, t, n in (
+        ("new_lens", new_lens, S), ("kept", kept, S * hkv * mk), ("context_lens", context_lens, S),
+        ("keep_lens", keep_lens, S), ("weight_rows", weight_rows, S), ("block_tables", block_tables, S * mb),
+        ("dst_tables", dst_tables, S * mb)) if t is not None]
+    for i, (name, beg, end) in enumerate(spans[:2]):  # the outputs
+        for other, obeg, oend in spans[i + 1:]:
+            if beg < oend and obeg < end:
+                _bad(f"{name} must not overlap {other}")
     desc = DecodeDesc(S, hkv, hkv, d, bs, nblk, mb, most, 1.0)
     st = (_LIB or load()).pa_evict_tokens(_c.byref(desc), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), dst,
                                 context_lens.data_ptr(), keep_lens.data_ptr(), mk, int(sink_tokens),

@@ -386,8 +386,17 @@ extern "C" int pa_evict_tokens(const pa_decode_desc *d, void *k_pool, void *v_po
   if (d->num_seqs == 0) return PA_OK;
   if (!k_pool || !v_pool || !block_tables || !context_lens || !keep_lens || !weights || !weights_out || !kept ||
       !new_lens || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(weights) || !aligned16(weights_out) ||
-      new_lens == context_lens || !same_or_apart(weights, weights_out, num_rows, d->num_kv_heads, max_tokens))
+      !same_or_apart(weights, weights_out, num_rows, d->num_kv_heads, max_tokens))
     return PA_ERR_INVALID;
+  // One kv head's CTA writes what the others' may not have read yet.
+  const size_t S = d->num_seqs, tables = S * d->max_blocks_per_seq, list = S * d->num_kv_heads * max_keep_len;
+  const struct {
+    const int32_t *p;
+    size_t n;
+  } read[] = {{context_lens, S}, {keep_lens, S}, {weight_rows, S}, {block_tables, tables}, {dst_tables, tables}};
+  for (const auto &r : read)
+    if (!apart(new_lens, S, r.p, r.n) || !apart(kept, list, r.p, r.n)) return PA_ERR_INVALID;
+  if (!apart(new_lens, S, kept, list)) return PA_ERR_INVALID;
   if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   const int sms = current_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;

@@ -36,6 +36,12 @@ inline bool same_or_apart(const float *a, const float *b, int rows, int heads, i
   return x == y || x + bytes <= y || y + bytes <= x;
 }
 
+// Whether two arrays (null: none) of so many int32 are apart.
+inline bool apart(const int32_t *a, size_t na, const int32_t *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return !a || !b || x + na * sizeof(int32_t) <= y || y + nb * sizeof(int32_t) <= x;
+}
+
 inline int launch_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
 // Longest context part one decode CTA streams, and most parts per sequence.

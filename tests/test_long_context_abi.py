@@ -303,3 +303,59 @@ def test_the_quick_way_leaves_everything_unusual_to_the_other(lib):
                 assert f(*args[:i], x, *args[i + 1:]) is None
     with pytest.raises(TypeError):
         F.bind(1, 2)
+
+
+# (2 sequences, 2 kv heads, 4 blocks a table, max_keep_len 8: new_lens 8 bytes, kept 128, a table 32)
+APART = dict(bt=4096, ctx=8192, keep=12288, kept=16384, new=20480)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(new=8192), dict(new=8196), dict(new=8188), dict(new=12288), dict(new=12292), dict(new=12284),
+    dict(new=4096), dict(new=4124), dict(rows=24576, new=24576), dict(rows=24576, new=24580),
+    dict(dst=28672, new=28672), dict(dst=28672, new=28700), dict(new=16384), dict(new=16508), dict(new=16380),
+    dict(kept=8192), dict(kept=8068), dict(kept=12288), dict(kept=4096 + 28), dict(kept=4096 - 124),
+    dict(rows=24576, kept=24576), dict(dst=28672, kept=28672 - 124),
+])
+def test_outputs_of_an_eviction_that_overlap_what_it_reads(lib, kw):
+    """Another kv head's CTA may still have to read what the first one
+    writes: refused, whole or in part."""
+    assert evict(lib, _desc(), **{**APART, **kw}) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(new=8200), dict(new=8184), dict(new=4128), dict(new=16512),
+                                dict(rows=24576, new=24584), dict(dst=28672, kept=28672 - 128), dict(dst=4096)])
+def test_outputs_of_an_eviction_beside_what_it_reads(lib, kw):
+    """Not refused: the call goes on to ask for the GPU (and, having one,
+    would launch, so only where there is none)."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("addresses of no memory")
+    assert evict(lib, _desc(), **{**APART, **kw}) == pa.PA_ERR_CUDA
+
+
+def test_the_wrapper_refuses_outputs_that_overlap(fake):
+    import torch
+    t = _tensors()
+    ok = (t["kp"], t["vp"], t["bt"], t["ctx"])
+
+    def refused(**kw):
+        args = dict(keep_lens=t["keep"])
+        args.update(kw)
+        keep = args.pop("keep_lens")
+        _refused(fake, ValueError, pa.evict_tokens, *ok, keep, t["w"], max_keep_len=8, **args)
+
+    both = torch.zeros(7, dtype=torch.int32)  # [0:4] and [3:7]
+    rows = torch.arange(4, dtype=torch.int32)
+    refused(new_lens=t["keep"])
+    refused(keep_lens=both[:4], new_lens=both[3:])
+    refused(new_lens=rows, weight_rows=rows)
+    refused(new_lens=t["bt"].view(-1)[:4])
+    flat = torch.zeros(4 * 2 * 8 + 4, dtype=torch.int32)
+    refused(kept=flat[:64].view(4, 2, 8), new_lens=flat[60:64])
+    dst = torch.zeros(64 + 24, dtype=torch.int32)
+    refused(kept=dst[:64].view(4, 2, 8), dst_tables=dst[63:87].view(4, 6))
+    # side by side: taken
+    one = torch.zeros(64 + 4 + 4, dtype=torch.int32)
+    kept, new = pa.evict_tokens(*ok, one[64:68], t["w"], max_keep_len=8, kept=one[:64].view(4, 2, 8),
+                                new_lens=one[68:])
+    assert fake.calls[-1][0] == "pa_evict_tokens" and kept.data_ptr() == one.data_ptr()
