@@ -59,7 +59,8 @@
  *    replays need no workspace clearing; the allocation-free decode wants its
  *    first call outside a capture (see below).
  *  - Thread safety: calls are re-entrant; the only global state is a
- *    per-device cache of SM count and of the driver's tensor-map encoder.
+ *    per-device cache of SM count and of the driver's tensor-map encoder, and
+ *    the lock under which pa_paged_attention_decode_weights makes its launches.
  */
 #ifndef PAGEDATTN_H
 #define PAGEDATTN_H
@@ -422,7 +423,13 @@ size_t pa_decode_weights_workspace_bytes(const pa_decode_desc *desc);
  *                pa_evict_tokens leaves zeros behind the tokens it keeps.
  *   weight_rows  device int32 [num_seqs], or NULL: row s (num_rows >= num_seqs)
  *   max_tokens   >= max_context_len
- *   workspace    >= pa_decode_weights_workspace_bytes(desc), 16-byte aligned
+ *   workspace    >= pa_decode_weights_workspace_bytes(desc), 16-byte aligned, any
+ *                contents.  The call may be two kernels that hand over through
+ *                it: calls that may overlap on the GPU must not share one, and no
+ *                other host thread may put a call of another kind that uses it on
+ *                the stream meanwhile (calls of this kind keep out of each
+ *                other's way, so several threads may share a stream and a
+ *                workspace for them)
  * A row outside [0, num_rows) sets PA_DEVERR_ROW and is not written.  A
  * sequence with a bad context adds nothing.  Other arguments and errors as in
  * pa_paged_attention_decode. */

@@ -160,9 +160,6 @@ def load(path: Optional[str] = None):
         lib.pa_paged_attention_decode_sparse.argtypes = [D, _P, _P, _P, _P, _P, _P, i, _P, _P, sz, _P, _P]
         lib.pa_decode_weights_workspace_bytes.restype = sz
         lib.pa_decode_weights_workspace_bytes.argtypes = [D]
-        # two launches that hand over by way of the workspace: with the interpreter
-        # lock held, so that no other thread's call comes between them
-        lib.pa_paged_attention_decode_weights = _c.PyDLL(p).pa_paged_attention_decode_weights
         lib.pa_paged_attention_decode_weights.restype = i
         lib.pa_paged_attention_decode_weights.argtypes = [D, _P, _P, _P, _P, _P, _P, _P, _P, i, i, _P, _P, sz, _P, _P]
         lib.pa_evict_tokens.restype = i

@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "pa_decode_body.cuh"
 #include "pa_internal.h"
@@ -237,6 +238,10 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   a.w_out = one ? weights_out : nullptr;
   a.max_tokens = (size_t)max_tokens;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // The second kernel reads what the first left in the workspace: no other such
+  // call may come between the two on the stream, whatever thread makes it.
+  static std::mutex both;
+  const std::lock_guard<std::mutex> lock(both);
   const int st = d->head_dim == 128 ? (d->block_size == 16 ? dispatch_logits<128, 16>(d, tk, tv, a, sms, s)
                                                            : dispatch_logits<128, 32>(d, tk, tv, a, sms, s))
                                     : (d->block_size == 16 ? dispatch_logits<64, 16>(d, tk, tv, a, sms, s)

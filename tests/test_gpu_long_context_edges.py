@@ -194,3 +194,56 @@ def test_small_and_large_grids_from_several_threads(torch, monkeypatch):
     torch.cuda.synchronize()
     assert status == [{pa.PA_OK}] * len(calls), status
     assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+@pytest.mark.parametrize("with_rows", [True, False])
+def test_weights_calls_of_several_threads_share_a_workspace(torch, with_rows):
+    """C calls from threads that share a stream and a workspace: two kernels
+    each (with rows, or for the long context), of which no other thread's call
+    comes between."""
+    import ctypes
+    import threading
+
+    R = _ref()
+    Hq, Hkv, D, B, lens = 8, 2, 64, 16, [40000, 900, 40]
+    c = R.make_cache(lens, Hkv, D, B, seed=87)
+    lib, stream = pa.load(), torch.cuda.current_stream().cuda_stream
+    rows = torch.tensor([1, 0, 1], dtype=torch.int32, device="cuda") if with_rows else None
+    desc = pa.DecodeDesc(3, Hq, Hkv, D, B, c["k"].shape[0], c["mb"], max(lens), D**-0.5)
+    n = int(lib.pa_decode_weights_workspace_bytes(ctypes.byref(desc)))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    width, N, T = c["mb"] * B, 150, 4
+
+    def arrays():
+        return [(torch.zeros(3, Hkv, width, device="cuda"), torch.empty(3, Hq, D, dtype=torch.bfloat16, device="cuda"))
+                for _ in range(T)]
+
+    qs = [torch.randn(3, Hq, D, device="cuda").to(torch.bfloat16) for _ in range(T)]
+
+    def call(i, w, out):
+        return lib.pa_paged_attention_decode_weights(
+            ctypes.byref(desc), qs[i].data_ptr(), c["k"].data_ptr(), c["v"].data_ptr(), c["bt"].data_ptr(),
+            c["ctx"].data_ptr(), w.data_ptr(), w.data_ptr(), None if rows is None else rows.data_ptr(), 3, width,
+            out.data_ptr(), ws.data_ptr(), n, None, stream)
+
+    want, got = arrays(), arrays()
+    for i in range(T):
+        for _ in range(N):
+            assert call(i, *want[i]) == pa.PA_OK
+    torch.cuda.synchronize()
+    start, status = threading.Barrier(T), [set() for _ in range(T)]
+
+    def run(i):
+        start.wait(60)
+        for _ in range(N):
+            status[i].add(call(i, *got[i]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(T)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{pa.PA_OK}] * T
+    for x, y in zip(want, got):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
