@@ -7,7 +7,9 @@
 // workspace and stream) and returns its result, or None when anything is not
 // as it must be or not as it is handled here.  The caller (_binding.py) then
 // takes its own way, which makes every check again, by name, and handles the
-// rest: nothing is launched before a None.
+// rest: nothing is launched before a None.  Once the library's call has been made
+// it is not made again: its failure is raised, and the results are Python objects
+// before it.
 #include <Python.h>
 
 #include <ATen/Functions.h>
@@ -103,6 +105,33 @@ at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int device) {
   return at::empty(sizes, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (at::DeviceIndex)device)));
 }
 
+// A reference of its own.
+struct Ref {
+  PyObject *p;
+  explicit Ref(PyObject *o) : p(o) {
+    if (!p) throw No{};
+  }
+  Ref(const Ref &) = delete;
+  ~Ref() { Py_XDECREF(p); }
+  // The result of a call that returned `status`, or its failure raised as the
+  // binding raises it.
+  PyObject *after(int status, const char *call) {
+    PyObject *r = p;
+    if (status == PA_OK) {
+      p = nullptr;
+      return r;
+    }
+    PyObject *m = PyImport_ImportModule("paged_kv_cache_262_gb300._binding");
+    PyObject *x = m ? PyObject_CallMethod(m, "_check", "is", status, call) : nullptr;
+    Py_XDECREF(m);
+    if (x) {  // (it raises)
+      Py_DECREF(x);
+      PyErr_SetString(PyExc_RuntimeError, call);
+    }
+    return nullptr;
+  }
+};
+
 template <class F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   try {
@@ -130,12 +159,15 @@ PyObject *bounds(PyObject *, PyObject *const *a, Py_ssize_t n) {
       need(size(t, 0) >= S);
       start = static_cast<const int32_t *>(t.data_ptr());
     }
-    const int most = integer_or(a[6], (int64_t)size(bt, 1) * B);
+    const int most = integer_or(a[6], (int64_t)size(bt, 1) * B), max_new = integer_or(a[5], most);
     const pa_decode_desc d{S, size(k, 1), size(k, 1), size(k, 3), B, size(k, 0), size(bt, 1), most, 1.f};
-    need(lib.bounds(&d, k.data_ptr(), static_cast<const int32_t *>(bt.data_ptr()),
-                    static_cast<const int32_t *>(ctx.data_ptr()), start, integer_or(a[5], most), b.data_ptr(),
-                    dev.err(a[7]), c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream()) == PA_OK);
-    Py_RETURN_TRUE;
+    int32_t *err = dev.err(a[7]);
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
+    Py_INCREF(Py_True);
+    Ref r(Py_True);
+    return r.after(lib.bounds(&d, k.data_ptr(), static_cast<const int32_t *>(bt.data_ptr()),
+                              static_cast<const int32_t *>(ctx.data_ptr()), start, max_new, b.data_ptr(), err, st),
+                   "pa_block_key_bounds");
   });
 }
 
@@ -152,11 +184,13 @@ PyObject *select(PyObject *, PyObject *const *a, Py_ssize_t n) {
     cudaStream_t st = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
     int32_t *err = dev.err(a[9]);
     const Workspace ws = workspace(a[10], lib.select_bytes(&d), dev.index, st);
+    const int sink = integer(a[6]), recent = integer(a[7]);
     at::Tensor out = fresh({S, Hkv, k}, kI, dev.index);
-    need(lib.select(&d, q.data_ptr(), b.data_ptr(), static_cast<const int32_t *>(bt.data_ptr()),
-                    static_cast<const int32_t *>(ctx.data_ptr()), k, integer(a[6]), integer(a[7]),
-                    static_cast<int32_t *>(out.data_ptr()), ws.p, ws.bytes, err, st) == PA_OK);
-    return THPVariable_Wrap(out);
+    Ref r(THPVariable_Wrap(out));
+    return r.after(lib.select(&d, q.data_ptr(), b.data_ptr(), static_cast<const int32_t *>(bt.data_ptr()),
+                              static_cast<const int32_t *>(ctx.data_ptr()), k, sink, recent,
+                              static_cast<int32_t *>(out.data_ptr()), ws.p, ws.bytes, err, st),
+                   "pa_select_blocks");
   });
 }
 
@@ -194,10 +228,12 @@ PyObject *sparse(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *err = dev.err(a[8]);
     const Workspace ws = workspace(a[9], lib.sparse_bytes(&x.d, k), dev.index, st);
     at::Tensor out = fresh(x.q.sizes(), kBf, dev.index);
-    need(lib.sparse(&x.d, x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(),
-                    static_cast<const int32_t *>(x.bt.data_ptr()), static_cast<const int32_t *>(x.ctx.data_ptr()),
-                    static_cast<const int32_t *>(sel.data_ptr()), k, out.data_ptr(), ws.p, ws.bytes, err, st) == PA_OK);
-    return THPVariable_Wrap(out);
+    Ref r(THPVariable_Wrap(out));
+    return r.after(lib.sparse(&x.d, x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(),
+                              static_cast<const int32_t *>(x.bt.data_ptr()),
+                              static_cast<const int32_t *>(x.ctx.data_ptr()),
+                              static_cast<const int32_t *>(sel.data_ptr()), k, out.data_ptr(), ws.p, ws.bytes, err, st),
+                   "pa_paged_attention_decode_sparse");
   });
 }
 
@@ -233,11 +269,13 @@ PyObject *weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *err = dev.err(a[10]);
     const Workspace ws = workspace(a[11], lib.weights_bytes(&x.d), dev.index, st);
     at::Tensor out = fresh(x.q.sizes(), kBf, dev.index);
-    need(lib.weights(&x.d, x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(),
-                     static_cast<const int32_t *>(x.bt.data_ptr()), static_cast<const int32_t *>(x.ctx.data_ptr()),
-                     static_cast<const float *>(w.in.data_ptr()), static_cast<float *>(w.out.data_ptr()), w.rows,
-                     size(w.in, 0), size(w.in, 2), out.data_ptr(), ws.p, ws.bytes, err, st) == PA_OK);
-    return THPVariable_Wrap(out);
+    Ref r(THPVariable_Wrap(out));
+    return r.after(lib.weights(&x.d, x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(),
+                               static_cast<const int32_t *>(x.bt.data_ptr()),
+                               static_cast<const int32_t *>(x.ctx.data_ptr()),
+                               static_cast<const float *>(w.in.data_ptr()), static_cast<float *>(w.out.data_ptr()),
+                               w.rows, size(w.in, 0), size(w.in, 2), out.data_ptr(), ws.p, ws.bytes, err, st),
+                   "pa_paged_attention_decode_weights");
   });
 }
 
@@ -261,18 +299,16 @@ PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Weights w = weight_rows(dev, a[5], a[10], a[11], d);
     cudaStream_t st = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
     int32_t *err = dev.err(a[13]);
+    const int sink = integer(a[7]), recent = integer(a[8]);
     at::Tensor kept = fresh({S, Hkv, mk}, kI, dev.index), lens = fresh({S}, kI, dev.index);
-    need(lib.evict(&d, k.data_ptr(), v.data_ptr(), static_cast<const int32_t *>(bt.data_ptr()), dst,
-                   static_cast<const int32_t *>(ctx.data_ptr()), static_cast<const int32_t *>(keep.data_ptr()), mk,
-                   integer(a[7]), integer(a[8]), static_cast<const float *>(w.in.data_ptr()),
-                   static_cast<float *>(w.out.data_ptr()), w.rows, size(w.in, 0), size(w.in, 2),
-                   static_cast<int32_t *>(kept.data_ptr()), static_cast<int32_t *>(lens.data_ptr()), err,
-                   st) == PA_OK);
-    PyObject *p = THPVariable_Wrap(kept), *r = THPVariable_Wrap(lens);
-    PyObject *pair = p && r ? PyTuple_Pack(2, p, r) : nullptr;
-    Py_XDECREF(p);
-    Py_XDECREF(r);
-    return pair;  // (a failure here, behind the launch, is raised: memory for a tuple)
+    Ref k_(THPVariable_Wrap(kept)), l_(THPVariable_Wrap(lens)), r(PyTuple_Pack(2, k_.p, l_.p));
+    return r.after(lib.evict(&d, k.data_ptr(), v.data_ptr(), static_cast<const int32_t *>(bt.data_ptr()), dst,
+                             static_cast<const int32_t *>(ctx.data_ptr()),
+                             static_cast<const int32_t *>(keep.data_ptr()), mk, sink, recent,
+                             static_cast<const float *>(w.in.data_ptr()), static_cast<float *>(w.out.data_ptr()),
+                             w.rows, size(w.in, 0), size(w.in, 2), static_cast<int32_t *>(kept.data_ptr()),
+                             static_cast<int32_t *>(lens.data_ptr()), err, st),
+                   "pa_evict_tokens");
   });
 }
 

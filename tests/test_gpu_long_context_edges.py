@@ -247,3 +247,64 @@ def test_weights_calls_of_several_threads_share_a_workspace(torch, with_rows):
     assert status == [{pa.PA_OK}] * T
     for x, y in zip(want, got):
         assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+# ------------------------------------------------------- launches that fail
+def test_a_call_that_failed_is_not_made_again(torch, monkeypatch):
+    """Every call by the extension module against a library whose calls fail
+    as a launch does (the first of two kernels may be on its way by then): the
+    failure is raised, and no call is made twice."""
+    import ctypes
+
+    from paged_kv_cache_262_gb300 import _binding as b
+    R = _ref()
+    F = b._FAST if b._FAST is not None else b._fast()
+    assert F, "the extension module is not built"
+    lib = pa.load()
+    names = ("pa_block_key_bounds", "pa_select_blocks_workspace_bytes", "pa_select_blocks",
+             "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
+             "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens")
+    made, keep = [], []
+
+    def failing(name):
+        def call(*_):
+            made.append(name)
+            return pa.PA_ERR_CUDA
+        f = ctypes.CFUNCTYPE(ctypes.c_int, *getattr(lib, name).argtypes)(call)
+        keep.append(f)
+        return f
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes") or name == "pa_status_string":
+                return getattr(lib, name)
+            return made.append(name) or (lambda *_: 0)
+
+    c = R.make_cache([100, 40], 2, 64, 16, seed=84)
+    q = torch.randn(2, 4, 64, device="cuda").to(torch.bfloat16)
+    bd = torch.zeros(c["k"].shape[0], 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    sel = torch.zeros(2, 2, 3, dtype=torch.int32, device="cuda")
+    w = torch.zeros(2, 2, c["mb"] * 16, device="cuda")
+    cache = (c["k"], c["v"], c["bt"], c["ctx"])
+    calls = [("pa_block_key_bounds", lambda: pa.block_key_bounds(c["k"], bd, c["bt"], c["ctx"])),
+             ("pa_select_blocks", lambda: pa.select_blocks(q, bd, c["bt"], c["ctx"], 3, block_size=16)),
+             ("pa_paged_attention_decode_sparse", lambda: pa.paged_attention_decode_sparse(q, *cache, sel)),
+             ("pa_paged_attention_decode_weights", lambda: pa.paged_attention_decode_weights(q, *cache, w)),
+             ("pa_evict_tokens", lambda: pa.evict_tokens(*cache, torch.full_like(c["ctx"], 8), w, max_keep_len=8))]
+    for _, call in calls:
+        call()  # (so that the default workspaces are there)
+    real = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names]
+    F.bind(*(a if n.endswith("_bytes") else ctypes.cast(failing(n), ctypes.c_void_p).value
+             for n, a in zip(names, real)))
+    try:
+        monkeypatch.setattr(b, "_LIB", Lib())
+        for name, call in calls:
+            made.clear()
+            with pytest.raises(pa.PaError) as e:
+                call()
+            assert made == [name] and e.value.status == pa.PA_ERR_CUDA and name in str(e.value)
+    finally:
+        F.bind(*real)
+    monkeypatch.undo()
+    for _, call in calls:
+        call()
