@@ -376,7 +376,9 @@ size_t pa_select_blocks_workspace_bytes(const pa_decode_desc *desc);
  *             contents; calls that may overlap on the GPU must not share one
  * sink_blocks + recent_blocks must not exceed num_select.  A sequence with a
  * bad context gets -1 throughout and PA_DEVERR_CTX.  A block whose table entry
- * is outside the pool sets PA_DEVERR_PAGE and ranks below all others.
+ * is outside the pool sets PA_DEVERR_PAGE and ranks below all others; it is still
+ * listed as one of the first or the last, or where the list has room for every
+ * block (attention leaves it out).
  * recent_blocks >= 1 keeps the block being filled in the list. */
 int pa_select_blocks(const pa_decode_desc *desc, const void *q, const void *bounds, const int32_t *block_tables,
                      const int32_t *context_lens, int num_select, int sink_blocks, int recent_blocks,

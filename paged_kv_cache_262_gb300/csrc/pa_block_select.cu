@@ -348,7 +348,19 @@ __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kerne
   const int ctx = __ldg(a.ctx + s);
   const bool bad = ctx <= 0 || ctx > a.max_blocks * B || ctx > a.max_ctx;
   const int n = bad ? 0 : (ctx + B - 1) / B;
+  // The blocks listed whatever their score, the first `lead` and those from `tail`
+  // on, have their entries looked at once a sequence, by its first CTA; those that
+  // compete, where they are scored.
+  const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
+  auto look = [&](int lead, int tail) {
+    if (chunk != 0 || h != 0 || !a.err) return;
+    for (int i = tid; i < lead + n - tail; i += kThreads) {
+      const int pg = __ldg(bt + (i < lead ? i : tail + i - lead));
+      if (pg < 0 || pg >= a.num_blocks) atomicOr(a.err, PA_DEVERR_PAGE);
+    }
+  };
   if (n <= a.k) {  // every block, or none (the same for the whole cluster)
+    look(0, 0);
     if (chunk == 0) {
       int32_t *out = a.selected + row * a.k;
       for (int i = tid; i < a.k; i += kThreads) out[i] = i < n ? i : -1;
@@ -362,7 +374,6 @@ __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kerne
   // the first CTA's shared memory must be there before another writes to it
   if (clustered) cluster_arrive();
   const int first = a.sink, end = n - a.recent;  // the blocks that compete
-  const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
   const __nv_bfloat16 *q = a.q + ((size_t)s * a.Hq + (size_t)h * a.G) * D;
   const int i_end = min(end, (chunk + 1) * a.chunk);
 
@@ -467,6 +478,7 @@ __global__ void __launch_bounds__(SW * 32, (NT == 1 ? 16 : 8) / SW) select_kerne
       }
     }
   }
+  look(first, end);  // (here the scores have left the table in L1: 0.1 us less than before them)
   grid_launch_dependents();
   const bool one = !LONG && !clustered;  // then the threads' own least and largest keys will do
 #pragma unroll

@@ -308,3 +308,29 @@ def test_a_call_that_failed_is_not_made_again(torch, monkeypatch):
     monkeypatch.undo()
     for _, call in calls:
         call()
+
+
+# ------------------------------------------------ table entries of the ends
+@pytest.mark.parametrize("entry", ["above", -1, -2**31])
+@pytest.mark.parametrize("where", ["sink", "recent", "short", "all_listed"])
+@pytest.mark.parametrize("blocks", [40, 9000])
+def test_selection_reports_every_unreadable_block(torch, entry, where, blocks):
+    """A block with an entry outside the pool is reported also where it is
+    listed whatever its score: a sink, a recent block, any block of a context
+    with no more of them than the list has places."""
+    R = _ref()
+    Hkv, G, D, B, k = 2, 2, 64, 16, 12
+    lens = [blocks * B, 9 * B - 3, k * B]
+    g = torch.Generator(device="cuda").manual_seed(85)
+    b = torch.randn(blocks, Hkv, 2, D, generator=g, device="cuda").sort(dim=2).values.to(torch.bfloat16)
+    bt = torch.randperm(blocks, generator=g, device="cuda").to(torch.int32)[None].expand(3, -1).contiguous()
+    bt[1, 9:], bt[2, k:] = blocks + 1, -1  # past a context: not looked at
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(3, Hkv * G, D, generator=g, device="cuda").to(torch.bfloat16)
+    want, err = R.ref_select(q, b, bt, lens, B, G, k, 2, 3), err_of(torch)
+    got = pa.select_blocks(q, b, bt, ctx, k, block_size=B, sink_blocks=2, recent_blocks=3, err_flag=err)
+    assert torch.equal(got, want) and int(err) == 0
+    s, i = {"sink": (0, 1), "recent": (0, blocks - 2), "short": (1, 8), "all_listed": (2, 5)}[where]
+    bt[s, i] = blocks if entry == "above" else entry
+    got = pa.select_blocks(q, b, bt, ctx, k, block_size=B, sink_blocks=2, recent_blocks=3, err_flag=err)
+    assert torch.equal(got, want) and int(err) == pa.DEVERR_PAGE
