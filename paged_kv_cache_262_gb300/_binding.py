@@ -865,7 +865,10 @@ def paged_attention_decode_weights(q, k_pool, v_pool, block_tables, context_lens
                                    workspace=None, err_flag=None, stream=None):
     """Decode attention that adds every key's attention weight to `weights`
     [num_rows][Hkv][max_tokens] (in place, or into weights_out; see
-    pagedattn.h); returns (out, weights_out)."""
+    pagedattn.h); returns (out, weights_out).  The workspace, kept for the
+    stream when none is given, holds 4 bytes for each query head and token of
+    every sequence's max_context_len (default: the table's capacity): give the
+    step's longest context."""
     F = _FAST if _FAST is not None else _fast()
     if F and out is None and workspace is None and stream is None:
         r = F.weights(q, k_pool, v_pool, block_tables, context_lens, weights, weights_out, weight_rows, scale,

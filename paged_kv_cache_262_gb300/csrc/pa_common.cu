@@ -196,9 +196,12 @@ DecodePlan make_decode_plan(const pa_decode_desc *d, int sm_count) {
 // join in a cluster are worth less work than those that join through the
 // workspace: down to 8 pages for up to 8 parts, and past those (each cluster of
 // 8 then goes through the workspace, about 2.5 us) 32, where 8 parts would be
-// longer than 48 pages.  (us for attention weights, by this plan and by the one
+// longer than 48 pages (which takes effect from 64 on, where 32 pages a part make
+// two whole clusters).  (us for attention weights, by this plan and by the one
 // above with the workspace: one sequence of 32000 tokens, 8 kv heads, 29.7 and
-// 54.7; of 8000 18.3 and 29.3; of 1000, 1 kv head, 6.8 and 14.9.)
+// 54.7; of 8000 18.3 and 29.3; of 1000, 1 kv head, 6.8 and 14.9.  More clusters and
+// one, in a graph: 64 pages a part of eight 16.5 and 18.0, 80 18.1 and 21.3, 128
+// 20.4 and 30.7; two sequences, 64 pages, 19.8 and 20.1.)
 // PA_PARTITION_PAGES as above.
 DecodePlan make_cluster_plan(const pa_decode_desc *d, int sm_count) {
   DecodePlan p = make_decode_plan(d, sm_count);

@@ -18,7 +18,7 @@
 // The bytes bind: 240 sequences, 24 blocks of 32 tokens each at most, 8 kv heads
 // of 128: 107 us, 6.5 TB/s (103 with the probabilities rounded once: with one
 // slot a warp the second product is not hidden).  128 blocks of 16 for 8
-// sequences, 67 MB: 16.9 us, 4.0 TB/s -- one wave of 256 CTAs, of which starting,
+// sequences, 67 MB: 17.1 us, 3.9 TB/s (16.3 in a graph) -- one wave of 256 CTAs, of which starting,
 // three dependent loads, the first gathers and the join are 7 us; more slots a
 // warp or other parts (16, 22, 43, 64 pages) are no faster.  One sequence, 256
 // blocks, 32 query and 8 kv heads: 10.3 us.

@@ -21,7 +21,8 @@
 // 167 the first kernel (67 MB of logits written, 7 MB of them reach HBM; without
 // the hint 204 us in all) and the rest the second, which starts while the first
 // runs and has the old sums loaded when it ends.  64 sequences of 128 .. 2048
-// tokens: 49 us, 6.1 TB/s.  Four sequences of up to 100: 4.6 us, the launch.
+// tokens: 49 us, 6.1 TB/s.  Four sequences of up to 100: 4.4 us in a graph, the
+// launch, and 5-6 a call from Python, the host's.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -229,9 +230,11 @@ extern "C" int pa_paged_attention_decode_weights(const pa_decode_desc *d, const 
   a.logits = reinterpret_cast<float *>(ws + plan.stats);
   // One launch where every (sequence, kv head) is a CTA or a cluster, rows are
   // not shared and a CTA's logits are at most 64 KB; else a second kernel, on
-  // the whole GPU, adds the weights.  (us, one launch and two: 64 sequences up to
-  // 2048 tokens, 32 KB a CTA, 49.2 and 51.6; four short ones 4.6 and 5.7; 8 x
-  // 32768 tokens, 256 KB, 187 and 182.)
+  // the whole GPU, adds the weights.  (us in a graph, one launch and two, 8 heads a
+  // kv head: four short sequences 4.3 and 5.5; 64 x 1024 tokens, 32 KB a CTA, 50.8
+  // and 52.3; 64 x 2048, 64 KB, 91.9 and 93.6; 64 x 4096, 128 KB, 185.0 and 185.7;
+  // 64 x 8192 with 4 heads, 128 KB, 344.6 and 341.8; 40 x 8192, 256 KB, 311 and 298;
+  // 8 x 32768, 256 KB, 189 and 184: they meet near 128 KB, within 1 % there.)
   const int64_t cta_bytes = (int64_t)plan.split.part_pages * d->block_size * a.G * (int64_t)sizeof(float);
   const bool one = !weight_rows && plan.split.max_parts <= kClusterParts && cta_bytes <= 64 * 1024;
   a.w_in = weights;
