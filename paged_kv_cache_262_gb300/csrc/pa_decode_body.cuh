@@ -72,7 +72,7 @@ struct DecodeArgs {
   // Attention weights (WTS launches): every key's logit (base 2) and every
   // row's softmax statistics, from which a second kernel takes the weights.
   float *logits;    // [S][Hkv][max_ctx][G]
-  float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys, (., NaN) for a NaN sum
+  float2 *stats;    // [S][Hq]: maximum, 1 / sum of 2^(logit - maximum); (0, 0) for a row without keys
   // Where a unit is one CTA or one cluster, it adds the weights itself: w_out
   // [S][Hkv][max_tokens] = w_in + weights (null: a second kernel does).
   const float *w_in;
