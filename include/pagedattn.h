@@ -60,7 +60,8 @@
  *    first call outside a capture (see below).
  *  - Thread safety: calls are re-entrant; the only global state is a
  *    per-device cache of SM count and of the driver's tensor-map encoder, and
- *    the lock under which pa_paged_attention_decode_weights makes its launches.
+ *    the locks under which pa_paged_attention_decode_weights and
+ *    pa_paged_attention_decode_tree make their launches.
  */
 #ifndef PAGEDATTN_H
 #define PAGEDATTN_H
@@ -90,6 +91,7 @@ typedef enum pa_status {
 #define PA_DEVERR_PAIR 8     /* copy pair with a block id outside [0, num_blocks) */
 #define PA_DEVERR_TIMEOUT 16 /* an on-chip wait gave up (bounded waits only) */
 #define PA_DEVERR_ROW 32     /* weight row outside [0, num_rows), or an eviction names it twice */
+#define PA_DEVERR_TREE 64    /* tree's nodes outside the packed arrays or too many, bad parent or path entry */
 
 /* Shape of one paged-attention call.  head_dim in {64, 128}; block_size in
  * {16, 32}; num_q_heads a multiple of num_kv_heads with a group of at most 16.
@@ -475,6 +477,127 @@ int pa_evict_tokens(const pa_decode_desc *desc, void *k_pool, void *v_pool, cons
                     const int32_t *weight_rows, int num_rows, int max_tokens, int32_t *kept, int32_t *new_lens,
                     int32_t *err_flag, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens [PHASE]: decode reads the whole cache for each new
+ * token, so a step that checks several drafted tokens at once reads it once
+ * for all of them.  No page describes these calls.
+ *
+ * Sequence s has context_lens[s] tokens in the cache and a tree of drafted
+ * tokens behind them: node i (0 <= i < T_s) of the tree is row
+ * cu_nodes[s] + i of the packed arrays (T_s = cu_nodes[s+1] - cu_nodes[s]), and
+ * parents[row] is the index of its parent in the tree, an earlier node
+ * (0 .. i-1), or -1 for none.  Its K/V are cached at position
+ * context_lens[s] + i of the sequence (pa_reshape_and_cache; the slots are
+ * those of pa_bm_reserve_batch).  A chain of drafted tokens is a tree with
+ * parents -1, 0, 1, ...; a tree may have no nodes.  A step:
+ *   pa_bm_reserve_batch             room for the drafted tokens
+ *   pa_paged_attention_decode_tree  each layer, after its cache write
+ *   pa_verify_tree                  the path that the model agrees with
+ *   pa_commit_tree                  its K/V moved up behind the context
+ *   pa_bm_commit_batch              its tokens become the sequence's
+ * ------------------------------------------------------------------------ */
+
+/* Most nodes of a tree. */
+#define PA_MAX_TREE_NODES 256
+
+/* Bytes of device workspace pa_paged_attention_decode_tree needs for `desc`
+ * and trees of at most max_tree_nodes nodes on the current device; 0 for an
+ * invalid desc or bound. */
+size_t pa_decode_tree_workspace_bytes(const pa_decode_desc *desc, int max_tree_nodes);
+
+/* Decode attention of every node of every sequence's tree: node i attends the
+ * context and its own chain of ancestors, itself included,
+ *   out[n][h] = sum_j softmax_j(scale * q[n][h] . k_j) v_j,  n = cu_nodes[s] + i,
+ *   j = 0 .. context_lens[s]-1 and context_lens[s] + a for a = i, parent of i, ...
+ *   q, out        device bf16 [total_nodes][num_q_heads][head_dim]
+ *   context_lens  device int32 [num_seqs], tokens before the tree, >= 0;
+ *                 desc's max_context_len bounds context_lens[s] + T_s
+ *   cu_nodes      device int32 [num_seqs + 1], non-decreasing, within
+ *                 [0, total_nodes]
+ *   parents       device int32 [total_nodes]
+ *   max_tree_nodes  bound on every T_s, 1 .. PA_MAX_TREE_NODES
+ *   workspace     >= pa_decode_tree_workspace_bytes(desc, max_tree_nodes), 16-byte
+ *                 aligned, any contents.  The call may be two kernels that hand
+ *                 over through it: calls that may overlap on the GPU must not
+ *                 share one, and no other host thread may put a call of another
+ *                 kind that uses it on the stream meanwhile (calls of this kind
+ *                 keep out of each other's way)
+ * Only keys that a node attends reach its row: the other nodes' K/V may hold any
+ * bits.  A NaN or +infinite logit of an attended key makes the row NaN, a key
+ * whose logit is -infinity weighs nothing (a row of nothing else is zeros).
+ * A tree whose node range is not within [0, total_nodes] or that has more than
+ * max_tree_nodes nodes sets PA_DEVERR_TREE, a context that is negative or that
+ * leaves its tree no room (T_s more tokens than max_context_len or the table
+ * hold) PA_DEVERR_CTX; its rows (those in range) are zeros.  So is the row of a
+ * node whose chain meets a parent that is neither -1 nor an earlier node
+ * (PA_DEVERR_TREE).  A block-table entry outside the pool sets PA_DEVERR_PAGE and
+ * its keys are left out.  Rows outside every tree are not written.  Other
+ * arguments and errors as in pa_paged_attention_decode. */
+int pa_paged_attention_decode_tree(const pa_decode_desc *desc, const void *q, const void *k_pool,
+                                   const void *v_pool, const int32_t *block_tables, const int32_t *context_lens,
+                                   const int32_t *cu_nodes, const int32_t *parents, int max_tree_nodes,
+                                   int total_nodes, void *out, void *workspace, size_t workspace_bytes,
+                                   int32_t *err_flag, void *stream);
+
+/* Types of pa_verify_tree's logits. */
+#define PA_LOGITS_BF16 0
+#define PA_LOGITS_F32 1
+
+/* Bytes of device workspace pa_verify_tree needs; 0 for bad sizes. */
+size_t pa_verify_tree_workspace_bytes(int num_seqs, int max_tree_nodes, int vocab_size);
+
+/* The path of every tree that greedy decoding would have taken.  Each node's
+ * target is its logits' largest token,
+ *   targets[n] = argmax_v logits[n][v], ties to the lower v, a NaN above all,
+ * and the path begins at node 0 and goes on from a node to its child (a later
+ * node whose parent it is) with tokens[child] == targets[node], the lowest such
+ * child; path_lens[s] nodes in all.  next_tokens[s] is the last one's target,
+ * the token that follows the path.
+ *   logits       device [total_nodes][logits_stride] of logits_type, the first
+ *                vocab_size of each row counting; aligned to its elements
+ *   tokens       device int32 [total_nodes], the drafted tokens (a tree's node 0
+ *                needs none)
+ *   parents, cu_nodes, max_tree_nodes, total_nodes  as in
+ *                pa_paged_attention_decode_tree
+ *   targets      device int32 [total_nodes]; rows outside every tree are not
+ *                written
+ *   path         device int32 [num_seqs][max_tree_nodes], indices in the tree in
+ *                increasing order, then -1
+ *   path_lens, next_tokens  device int32 [num_seqs]; 0 and -1 for a tree without
+ *                nodes
+ *   workspace    >= pa_verify_tree_workspace_bytes(...), 16-byte aligned, any
+ *                contents; calls that may overlap on the GPU must not share one
+ * A node range as refused there, or a node 0 with a parent, sets PA_DEVERR_TREE
+ * and gives path_lens 0 and next_tokens -1 (and, of a refused range, no targets);
+ * another node's bad parent sets it too, and that node is on no path.  No output
+ * overlaps another or an input. */
+int pa_verify_tree(const void *logits, int logits_type, int64_t logits_stride, int vocab_size,
+                   const int32_t *tokens, const int32_t *parents, const int32_t *cu_nodes, int num_seqs,
+                   int max_tree_nodes, int total_nodes, int32_t *targets, int32_t *path, int32_t *path_lens,
+                   int32_t *next_tokens, void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* Moves the accepted paths' K/V up behind the contexts, in place, in every
+ * layer: with c = context_lens[s] and n = path_lens[s], for i < n
+ *   slot c + i of block_tables[s] := slot c + path[s][i], K and V,
+ * bit-exact, and new_lens[s] := c + n.  What the other nodes left behind them
+ * stays as it is.  Bounds of the written blocks are stale until
+ * pa_block_key_bounds (start_lens = context_lens).
+ *   k_pools, v_pools  HOST arrays of num_layers device pointers (1..256 layers)
+ *   path         device int32 [num_seqs][max_path_len], increasing within a row;
+ *                max_path_len 1 .. PA_MAX_TREE_NODES
+ *   path_lens    device int32 [num_seqs], 0 .. max_path_len
+ *   new_lens     device int32 [num_seqs]; overlaps no input
+ * num_q_heads and scale of desc are not used (but must be valid).  No block that
+ * holds a tree's node belongs to another sequence of the call.  A negative
+ * context or a path_lens[s] out of range (PA_DEVERR_CTX), and a path that is not
+ * increasing from 0 on or that leaves the table or max_context_len
+ * (PA_DEVERR_TREE), leave the sequence as it is: new_lens[s] = context_lens[s].
+ * A token whose source or destination block is outside the pool is not moved
+ * (PA_DEVERR_PAGE). */
+int pa_commit_tree(const pa_decode_desc *desc, void *const *k_pools, void *const *v_pools, int num_layers,
+                   const int32_t *block_tables, const int32_t *context_lens, const int32_t *path,
+                   const int32_t *path_lens, int max_path_len, int32_t *new_lens, int32_t *err_flag, void *stream);
+
 /* Writes the K/V of num_tokens new tokens into their cache slots [PHASE][SHARE]:
  *   k_pool[slot / B][h][slot % B][:] = k[t][h][:]  (same for v), for t in order.
  * Bit-exact copy.  slot < 0: token skipped.  slot >= num_blocks*B: skipped and
@@ -699,6 +822,30 @@ int pa_bm_evict(pa_bm *bm, int seq_id, int keep_len, int32_t *dst_out, int cap, 
  * max_blocks, null pointers, n < 0) and PA_ERR_OOM leave everything unchanged. */
 int pa_bm_evict_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *keep_lens, int n, int32_t *dst_out,
                       int max_blocks, int32_t pad, int32_t *new_lens_out);
+
+/* Room for drafted tokens (pa_paged_attention_decode_tree): each of
+ * seq_ids[0..n-1] (distinct) gets blocks for counts[i] >= 0 tokens past its
+ * length, and slots_out gets their slots, in order, sequence after sequence
+ * (sum of counts entries).  The length stays; the table holds the blocks, which
+ * later appends and pa_bm_commit_batch fill; of blocks that an earlier call
+ * reserved, those that this one does not need are released.  A partly filled
+ * last block with ref_count > 1 is copied on write as by pa_bm_append (unless
+ * counts[i] is 0): cow_pairs_out[n][2], {-1, -1} for none.  A fork does not share
+ * reserved blocks.
+ * PA_ERR_STATE (an unknown or swapped-out id), PA_ERR_INVALID (a repeated id, a
+ * negative count, a length that would pass INT_MAX, null pointers, n < 0) and
+ * PA_ERR_OOM leave the manager and the outputs untouched. */
+int pa_bm_reserve_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *counts, int n, int64_t *slots_out,
+                        int64_t *cow_pairs_out);
+
+/* The accepted tokens become the sequences': counts[i] >= 0 tokens onto each of
+ * seq_ids[0..n-1] (distinct), into the blocks that pa_bm_reserve_batch reserved
+ * (tokens[sum of counts], their ids, sequence after sequence, or NULL; as
+ * counts[i] calls of pa_bm_append_token or pa_bm_append).  Their K/V are valid
+ * once pa_commit_tree has run in every layer.  PA_ERR_STATE (an unknown or
+ * swapped-out id, more tokens than were reserved, or a shared block in their
+ * way), PA_ERR_INVALID and PA_ERR_OOM as above. */
+int pa_bm_commit_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *counts, const int32_t *tokens, int n);
 
 /* Number of free host blocks. */
 int pa_bm_num_free_host(const pa_bm *bm);

@@ -18,7 +18,9 @@ _P = _c.c_void_p
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_OOM, PA_ERR_WORKSPACE, PA_ERR_STATE = (
     0, -1, -2, -3, -4, -5, -6)
-DEVERR_CTX, DEVERR_PAGE, DEVERR_SLOT, DEVERR_PAIR, DEVERR_TIMEOUT, DEVERR_ROW = 1, 2, 4, 8, 16, 32
+DEVERR_CTX, DEVERR_PAGE, DEVERR_SLOT, DEVERR_PAIR, DEVERR_TIMEOUT, DEVERR_ROW, DEVERR_TREE = (
+    1, 2, 4, 8, 16, 32, 64)
+MAX_TREE_NODES = 256
 
 # Every symbol include/pagedattn.h declares.
 EXPORTS = (
@@ -37,6 +39,8 @@ EXPORTS = (
     "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
     "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens", "pa_bm_evict",
     "pa_bm_evict_batch",
+    "pa_decode_tree_workspace_bytes", "pa_paged_attention_decode_tree", "pa_verify_tree_workspace_bytes",
+    "pa_verify_tree", "pa_commit_tree", "pa_bm_reserve_batch", "pa_bm_commit_batch",
 )
 
 
@@ -166,6 +170,20 @@ def load(path: Optional[str] = None):
         lib.pa_evict_tokens.argtypes = [D, _P, _P, _P, _P, _P, _P, i, i, i, _P, _P, _P, i, i, _P, _P, _P, _P]
         lib.pa_bm_evict_batch.restype = i
         lib.pa_bm_evict_batch.argtypes = [_P, _P, _P, i, _P, i, i, _P]
+        lib.pa_decode_tree_workspace_bytes.restype = sz
+        lib.pa_decode_tree_workspace_bytes.argtypes = [D, i]
+        lib.pa_paged_attention_decode_tree.restype = i
+        lib.pa_paged_attention_decode_tree.argtypes = [D, _P, _P, _P, _P, _P, _P, _P, i, i, _P, _P, sz, _P, _P]
+        lib.pa_verify_tree_workspace_bytes.restype = sz
+        lib.pa_verify_tree_workspace_bytes.argtypes = [i, i, i]
+        lib.pa_verify_tree.restype = i
+        lib.pa_verify_tree.argtypes = [_P, i, i64, i, _P, _P, _P, i, i, i, _P, _P, _P, _P, _P, sz, _P, _P]
+        lib.pa_commit_tree.restype = i
+        lib.pa_commit_tree.argtypes = [D, _c.POINTER(_P), _c.POINTER(_P), i, _P, _P, _P, _P, i, _P, _P, _P]
+        lib.pa_bm_reserve_batch.restype = i
+        lib.pa_bm_reserve_batch.argtypes = [_P, _P, _P, i, _P, _P]
+        lib.pa_bm_commit_batch.restype = i
+        lib.pa_bm_commit_batch.argtypes = [_P, _P, _P, _P, i]
         lib.pa_bm_evict.restype = i
         lib.pa_bm_evict.argtypes = [_P, i, i, _c.POINTER(_c.c_int32), i, _c.POINTER(i)]
         if path is None:
@@ -951,6 +969,156 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
     return kept, new_lens
 
 
+# --------------------------------------------------------------- trees of drafted tokens
+_WS_TREE, _WS_VERIFY = {}, {}
+
+
+def _tree_args(T, dev, S, N, cu_nodes, parents, max_tree_nodes):
+    _all(dev, (cu_nodes, "cu_nodes", T.i32, 1), (parents, "parents", T.i32, 1))
+    if cu_nodes.shape[0] < S + 1:
+        _bad(f"cu_nodes has {cu_nodes.shape[0]} entries, needs {S + 1}")
+    if parents.shape[0] < N:
+        _bad(f"parents has {parents.shape[0]} entries, needs {N}")
+    most = int(max_tree_nodes)
+    if not 1 <= most <= MAX_TREE_NODES:
+        _bad(f"max_tree_nodes must be 1 .. {MAX_TREE_NODES}, got {most}")
+    return most
+
+
+def paged_attention_decode_tree(q, k_pool, v_pool, block_tables, context_lens, cu_nodes, parents, out=None, *,
+                                max_tree_nodes, scale=None, max_context_len=None, workspace=None, err_flag=None,
+                                stream=None):
+    """Decode attention of every node of every sequence's tree of drafted
+    tokens: q [total_nodes][Hq][D], node i of sequence s at row
+    cu_nodes[s] + i, its K/V cached at position context_lens[s] + i; it
+    attends the context and its chain of ancestors (parents, indices in the
+    tree, -1: none; see pagedattn.h).  max_context_len bounds the contexts
+    with their trees."""
+    T = _T or _torch()
+    bf, i32, dev = T.bf16, T.i32, T.device()
+    _all(dev, (q, "q", bf, 3), (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4),
+         (block_tables, "block_tables", i32, 2), (context_lens, "context_lens", i32, 1))
+    (nblk, hkv, bs, d), (N, hq, qd), (S,), (brows, mb) = k_pool.shape, q.shape, context_lens.shape, block_tables.shape
+    if v_pool.shape != k_pool.shape:
+        _bad(f"k_pool {tuple(k_pool.shape)} and v_pool {tuple(v_pool.shape)} differ")
+    if qd != d:
+        _bad(f"q head_dim {qd} != the pools' {d}")
+    if brows < S:
+        _bad(f"block_tables has {brows} rows, needs {S}")
+    most = _tree_args(T, dev, S, N, cu_nodes, parents, max_tree_nodes)
+    if out is None:
+        out = T.empty_like(q) if stream is None else _new(T, q.shape, bf, q.device, stream)
+    else:
+        _all(dev, (out, "out", bf, 3))
+        if out.shape != q.shape:
+            _bad(f"out must have q's shape {tuple(q.shape)}")
+    desc = DecodeDesc(S, hq, hkv, d, bs, nblk, mb, mb * bs if max_context_len is None else int(max_context_len),
+                      d**-0.5 if scale is None else float(scale))
+    lib, raw = _LIB or load(), T.stream(dev) if stream is None else stream.cuda_stream
+    ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
+        T, _WS_TREE, lib.pa_decode_tree_workspace_bytes(_c.byref(desc), most), q.device, stream, raw)
+    st = lib.pa_paged_attention_decode_tree(
+        _c.byref(desc), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), cu_nodes.data_ptr(), parents.data_ptr(), most, N, out.data_ptr(), ws, ws_bytes,
+        _err_ptr(err_flag, dev, i32), raw)
+    if st:
+        _check(st, "pa_paged_attention_decode_tree")
+    return out
+
+
+def verify_tree(logits, tokens, parents, cu_nodes, *, max_tree_nodes, targets=None, path=None, path_lens=None,
+                next_tokens=None, workspace=None, err_flag=None, stream=None):
+    """The path of every tree that greedy decoding would have taken: logits
+    [total_nodes][vocabulary] bf16 or fp32 (rows may lie apart), tokens int32
+    [total_nodes].  Returns (targets [total_nodes], path [num_seqs]
+    [max_tree_nodes], path_lens [num_seqs], next_tokens [num_seqs]), int32 (see
+    pagedattn.h)."""
+    T = _T or _torch()
+    i32, dev = T.i32, T.device()
+    if getattr(logits, "dtype", None) is not T.f32:
+        kind = 0
+        if getattr(logits, "dtype", None) is not T.bf16:
+            raise TypeError(f"logits must be a bf16 or fp32 CUDA tensor, got {getattr(logits, 'dtype', type(logits))}")
+    else:
+        kind = 1
+    if logits.dim() != 2:
+        _bad(f"logits must have 2 dims, got {logits.dim()}")
+    if not logits.is_cuda or logits.get_device() != dev:
+        _bad(f"logits is on {logits.device}, the current device is cuda:{dev}")
+    N, V = logits.shape
+    stride = logits.stride(0) if N > 1 else V
+    if V < 1 or (V > 1 and logits.stride(1) != 1) or stride < V:
+        _bad("each row of logits must be contiguous, and rows apart")
+    _all(dev, (tokens, "tokens", i32, 1))
+    if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
+        _bad("cu_nodes must be [num_seqs + 1]")
+    if tokens.shape[0] < N:
+        _bad(f"tokens has {tokens.shape[0]} entries, needs {N}")
+    S = cu_nodes.shape[0] - 1
+    most = _tree_args(T, dev, S, N, cu_nodes, parents, max_tree_nodes)
+    made = []
+    for t, name, shape in ((targets, "targets", (N,)), (path, "path", (S, most)), (path_lens, "path_lens", (S,)),
+                           (next_tokens, "next_tokens", (S,))):
+        if t is None:
+            t = _new(T, shape, i32, logits.device, stream)
+        else:
+            _all(dev, (t, name, i32, len(shape)))
+            if tuple(t.shape) != shape:
+                _bad(f"{name} must be {list(shape)}")
+        made.append(t)
+    lib, raw = _LIB or load(), T.stream(dev) if stream is None else stream.cuda_stream
+    ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
+        T, _WS_VERIFY, lib.pa_verify_tree_workspace_bytes(S, most, V), logits.device, stream, raw)
+    st = lib.pa_verify_tree(logits.data_ptr(), kind, stride, V, tokens.data_ptr(), parents.data_ptr(),
+                            cu_nodes.data_ptr(), S, most, N, *(t.data_ptr() for t in made), ws, ws_bytes,
+                            _err_ptr(err_flag, dev, i32), raw)
+    if st:
+        _check(st, "pa_verify_tree")
+    return tuple(made)
+
+
+def commit_tree(k_pools: Sequence, v_pools: Sequence, block_tables, context_lens, path, path_lens, new_lens=None, *,
+                max_context_len=None, err_flag=None, stream=None):
+    """Moves the accepted paths' K/V (path, path_lens of verify_tree) up
+    behind the contexts in every layer's pools, in place; returns new_lens
+    [num_seqs] = context_lens + path_lens (see pagedattn.h)."""
+    T = _T or _torch()
+    bf, i32, dev, L = T.bf16, T.i32, T.device(), len(k_pools)
+    if L == 0 or len(v_pools) != L:
+        _bad("k_pools and v_pools must be non-empty and of equal length")
+    shape = k_pools[0].shape
+    for pools, name in ((k_pools, "k_pools"), (v_pools, "v_pools")):
+        for t in pools:
+            _all(dev, (t, name, bf, 4))
+            if t.shape != shape:
+                _bad("the pools must all have the same shape")
+    _all(dev, (block_tables, "block_tables", i32, 2), (context_lens, "context_lens", i32, 1), (path, "path", i32, 2),
+         (path_lens, "path_lens", i32, 1))
+    (nblk, hkv, bs, d), (S,), (brows, mb), (prows, most) = shape, context_lens.shape, block_tables.shape, path.shape
+    if brows < S or prows < S or path_lens.shape[0] < S:
+        _bad(f"block_tables has {brows} rows, path {prows}, path_lens {path_lens.shape[0]}, needs {S}")
+    if new_lens is None:
+        new_lens = _new(T, (S,), i32, context_lens.device, stream)
+    _all(dev, (new_lens, "new_lens", i32, 1))
+    if new_lens.shape[0] != S:
+        _bad(f"new_lens must be [{S}]")
+    beg = new_lens.data_ptr()
+    for t, name in ((context_lens, "context_lens"), (path, "path"), (path_lens, "path_lens"),
+                    (block_tables, "block_tables")):
+        if beg < t.data_ptr() + 4 * t.numel() and t.data_ptr() < beg + 4 * S:
+            _bad(f"new_lens must not overlap {name}")
+    desc = DecodeDesc(S, hkv, hkv, d, bs, nblk, mb, mb * bs if max_context_len is None else int(max_context_len), 1.0)
+    kp = (_P * L)(*[t.data_ptr() for t in k_pools])
+    vp = (_P * L)(*[t.data_ptr() for t in v_pools])
+    st = (_LIB or load()).pa_commit_tree(_c.byref(desc), kp, vp, L, block_tables.data_ptr(), context_lens.data_ptr(),
+                                         path.data_ptr(), path_lens.data_ptr(), most, new_lens.data_ptr(),
+                                         _err_ptr(err_flag, dev, i32),
+                                         T.stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "pa_commit_tree")
+    return new_lens
+
+
 # --------------------------------------------------------------- block manager
 class BlockManager:
     """Host block manager (free list, block tables, ref counts, copy-on-write)."""
@@ -1090,6 +1258,41 @@ class BlockManager:
         _check(self._lib.pa_bm_evict_batch(self._h, ids.ctypes.data, keep.ctypes.data, int(ids.size), out.ctypes.data,
                                            int(max_blocks), int(pad), lens.ctypes.data), "pa_bm_evict_batch")
         return out, lens
+
+    def reserve(self, seq_ids, counts):
+        """Room for counts[i] drafted tokens past each of `seq_ids` (distinct);
+        the lengths stay.  Returns (slots int64 [sum of counts], sequence after
+        sequence, cow_pairs int64 [n, 2]; -1 rows: no copy); on an error
+        nothing has changed.  commit() makes the accepted tokens theirs; a
+        later reserve releases what it does not need itself."""
+        import numpy as np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32).reshape(-1)
+        cnt = np.ascontiguousarray(counts, dtype=np.int32).reshape(-1)
+        if cnt.size != ids.size:
+            raise ValueError("counts needs one number per sequence")
+        slots = np.empty(int(cnt[cnt > 0].sum(dtype=np.int64)), np.int64)
+        cows = np.empty((ids.size, 2), np.int64)
+        _check(self._lib.pa_bm_reserve_batch(self._h, ids.ctypes.data, cnt.ctypes.data, int(ids.size),
+                                             slots.ctypes.data, cows.ctypes.data), "pa_bm_reserve_batch")
+        return slots, cows
+
+    def commit(self, seq_ids, counts, tokens=None):
+        """counts[i] accepted tokens onto each of `seq_ids` (distinct), into
+        the reserved blocks; `tokens` (optional): their ids, sequence after
+        sequence.  On an error nothing has changed."""
+        import numpy as np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32).reshape(-1)
+        cnt = np.ascontiguousarray(counts, dtype=np.int32).reshape(-1)
+        if cnt.size != ids.size:
+            raise ValueError("counts needs one number per sequence")
+        tok = None
+        if tokens is not None:
+            tok = np.ascontiguousarray(tokens, dtype=np.int32).reshape(-1)
+            if tok.size != int(cnt[cnt > 0].sum(dtype=np.int64)):
+                raise ValueError("tokens needs one id per accepted token")
+        _check(self._lib.pa_bm_commit_batch(self._h, ids.ctypes.data, cnt.ctypes.data,
+                                            None if tok is None else tok.ctypes.data, int(ids.size)),
+               "pa_bm_commit_batch")
 
     def add_seq_tokens(self, seq_id: int, tokens) -> int:
         """New sequence holding the prompt `tokens` (a 1-D sequence of int32

@@ -24,7 +24,9 @@
 namespace {
 
 struct Seq {
-  std::vector<int32_t> blocks;  // device block ids, or host block ids while swapped out
+  // Device block ids, or host block ids while swapped out: those of the len
+  // tokens, then the reserved ones (pa_bm_reserve_batch; no other sequence's).
+  std::vector<int32_t> blocks;
   int len = 0;
   bool swapped = false;
   uint64_t stamp = 0;  // last batch call that listed this sequence
@@ -213,9 +215,15 @@ struct pa_bm {
     s.tail.clear();
   }
   bool needs_block(const Seq &s) const {  // appending to s takes a free block
-    return s.len % block_size == 0 || ref[s.blocks[s.len / block_size]] > 1;
+    return opens_block(s) || ref[s.blocks[s.len / block_size]] > 1;
   }
-  void grow(Seq &s) { s.blocks.reserve(std::max<size_t>(8, 2 * s.blocks.size())); }
+  bool opens_block(const Seq &s) const {  // the next token has no block yet
+    return (size_t)(s.len / block_size) == s.blocks.size();
+  }
+  size_t blocks_for(int64_t tokens) const { return (size_t)((tokens + block_size - 1) / block_size); }
+  void grow(Seq &s, size_t to = 0) {
+    if (to > s.blocks.capacity() || to == 0) s.blocks.reserve(std::max({(size_t)8, 2 * s.blocks.size(), to}));
+  }
   // Appending `token` (nullptr: an id not given) to s fills a block that is
   // then registered, so the cache's key store must exist first.
   bool fills_tracked(const Seq &s, const int32_t *token) const {
@@ -224,6 +232,39 @@ struct pa_bm {
   void ensure_keys() {  // allocates once
     if (c_tok.empty()) c_tok.assign((size_t)num_blocks * block_size, 0);
   }
+  // A block about to be written that others hold too is copied on write.
+  void unshare(int32_t &b, int64_t *cow_pair_out) {
+    if (ref[b] < 2) return;
+    const int32_t fresh = take();
+    cow_pair_out[0] = b;
+    cow_pair_out[1] = fresh;
+    drop(b);
+    b = fresh;
+  }
+  // Whether unsharing b once more, in batch call `call`, takes a free block: k
+  // of the call's sequences writing a block of ref_count r copy it min(k, r - 1)
+  // times (after r - 1 copies the last holder owns it alone).
+  bool counts_copy(int32_t b, uint64_t call) {
+    if (ref[b] < 2) return false;
+    if (blk_stamp[b] != call) {
+      blk_stamp[b] = call;
+      blk_count[b] = 0;
+    }
+    return blk_count[b]++ < ref[b] - 1;
+  }
+  // The sequences of a batch call into batch_seqs: PA_ERR_STATE for an id
+  // that is unknown or swapped out, PA_ERR_INVALID for one listed twice.
+  int find_batch(const int32_t *seq_ids, int n, uint64_t call) {
+    batch_seqs.resize(n);
+    for (int i = 0; i < n; ++i) {
+      auto it = seqs.find(seq_ids[i]);
+      if (it == seqs.end() || it->second.swapped) return PA_ERR_STATE;
+      if (it->second.stamp == call) return PA_ERR_INVALID;
+      it->second.stamp = call;
+      batch_seqs[i] = &it->second;
+    }
+    return PA_OK;
+  }
   // One token onto s; the caller checked that a block is free if one is
   // needed, that s.blocks has room for a new one and, when the token fills a
   // tracked block, that the key store exists.  Never allocates.
@@ -231,18 +272,10 @@ struct pa_bm {
     const int B = block_size;
     const int j = s.len;
     cow_pair_out[0] = cow_pair_out[1] = -1;
-    if (j % B == 0) {  // the token opens a new block
+    if (opens_block(s))
       s.blocks.push_back(take());
-    } else {
-      int32_t &last = s.blocks[j / B];
-      if (ref[last] > 1) {  // shared partial block: copy on write
-        const int32_t fresh = take();
-        cow_pair_out[0] = last;
-        cow_pair_out[1] = fresh;
-        drop(last);
-        last = fresh;
-      }
-    }
+    else
+      unshare(s.blocks[j / B], cow_pair_out);
     *slot_out = (int64_t)s.blocks[j / B] * B + (j % B);
     s.len = j + 1;
     if (!token) {  // an id not given: from here on nothing of s is registered
@@ -253,8 +286,7 @@ struct pa_bm {
     if (!s.tracked) return;
     s.tail.push_back(*token);  // within the reserved block's room
     if (s.len % B == 0) {      // the token filled its block: findable by later prompts
-      const size_t nb = s.blocks.size();
-      const int32_t b = s.blocks[nb - 1], parent = nb >= 2 ? s.blocks[nb - 2] : -1;
+      const int32_t b = s.blocks[j / B], parent = j >= B ? s.blocks[j / B - 1] : -1;
       // only reachable when the chain before it is cached; its K/V are valid
       // once this step's cache write of the token has run
       if ((parent < 0 || c_parent[parent] != -2) && c_parent[b] == -2) register_block(b, parent, s.tail.data());
@@ -300,7 +332,7 @@ int append_single(pa_bm *bm, int seq_id, const int32_t *token, int64_t *slot_out
   if (s.len == INT_MAX) return PA_ERR_INVALID;
   if (bm->needs_block(s) && bm->nfree == 0) return PA_ERR_OOM;
   const int st = guarded([&]() -> int {  // allocations first
-    if (s.len % bm->block_size == 0 && s.blocks.size() == s.blocks.capacity()) bm->grow(s);
+    if (bm->opens_block(s) && s.blocks.size() == s.blocks.capacity()) bm->grow(s);
     if (bm->fills_tracked(s, token)) bm->ensure_keys();
     return PA_OK;
   });
@@ -376,6 +408,7 @@ int pa_bm_fork(pa_bm *bm, int parent_id, int child_id) {
     auto it = bm->seqs.find(parent_id);
     if (it == bm->seqs.end() || bm->seqs.count(child_id) || it->second.swapped) return PA_ERR_STATE;
     auto c = bm->seqs.emplace(child_id, it->second).first;  // copies
+    c->second.blocks.resize(bm->blocks_for(c->second.len));  // (not the reserved blocks)
     if (c->second.tracked) {
       try {
         c->second.tail.reserve(bm->block_size);  // a copy keeps only the ids' own room
@@ -415,26 +448,14 @@ int pa_bm_append_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *tokens,
       s.stamp = call;
       sq[i] = &s;
     }
-    // k of the batch appending into a partial block of ref_count r copy it
-    // min(k, r - 1) times: after r - 1 copies the last holder owns it alone
     int64_t need = 0;
     for (int i = 0; i < n; ++i) {
       const Seq &s = *sq[i];
-      if (s.len % B == 0) {
-        ++need;
-        continue;
-      }
-      const int32_t x = s.blocks[s.len / B];
-      if (bm->ref[x] < 2) continue;
-      if (bm->blk_stamp[x] != call) {
-        bm->blk_stamp[x] = call;
-        bm->blk_count[x] = 0;
-      }
-      if (bm->blk_count[x]++ < bm->ref[x] - 1) ++need;
+      need += bm->opens_block(s) || bm->counts_copy(s.blocks[s.len / B], call);
     }
     if (need > (int64_t)bm->nfree) return PA_ERR_OOM;
     for (int i = 0; i < n; ++i) {
-      if (sq[i]->len % B == 0 && sq[i]->blocks.size() == sq[i]->blocks.capacity()) bm->grow(*sq[i]);
+      if (bm->opens_block(*sq[i]) && sq[i]->blocks.size() == sq[i]->blocks.capacity()) bm->grow(*sq[i]);
       if (bm->fills_tracked(*sq[i], tokens ? tokens + i : nullptr)) bm->ensure_keys();
     }
     for (int i = 0; i < n; ++i) bm->append_one(*sq[i], slots_out + i, cow_pairs_out + 2 * i, tokens ? tokens + i : nullptr);
@@ -672,6 +693,78 @@ int pa_bm_evict_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *keep_len
   });
 }
 
+int pa_bm_reserve_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *counts, int n, int64_t *slots_out,
+                        int64_t *cow_pairs_out) {
+  if (!bm || n < 0 || (n > 0 && (!seq_ids || !counts || !cow_pairs_out))) return PA_ERR_INVALID;
+  if (n == 0) return PA_OK;
+  return guarded([&]() -> int {
+    // every check and allocation first: a failure leaves no trace
+    const uint64_t call = ++bm->batch_no;
+    const int st = bm->find_batch(seq_ids, n, call);
+    if (st != PA_OK) return st;
+    Seq **sq = bm->batch_seqs.data();
+    const int B = bm->block_size;
+    int64_t need = 0, back = 0;  // blocks taken, and reserved ones given back
+    for (int i = 0; i < n; ++i) {
+      const Seq &s = *sq[i];
+      if (counts[i] < 0 || counts[i] > INT_MAX - s.len || (counts[i] > 0 && !slots_out)) return PA_ERR_INVALID;
+      const size_t want = bm->blocks_for((int64_t)s.len + counts[i]);
+      if (want > s.blocks.size())
+        need += (int64_t)(want - s.blocks.size());
+      else
+        back += (int64_t)(s.blocks.size() - want);
+      need += counts[i] > 0 && !bm->opens_block(s) && bm->counts_copy(s.blocks[s.len / B], call);
+    }
+    if (need > (int64_t)bm->nfree + back) return PA_ERR_OOM;
+    for (int i = 0; i < n; ++i) bm->grow(*sq[i], std::max<size_t>(1, bm->blocks_for((int64_t)sq[i]->len + counts[i])));
+    for (int i = 0; i < n; ++i) {
+      Seq &s = *sq[i];
+      for (const size_t want = bm->blocks_for((int64_t)s.len + counts[i]); s.blocks.size() > want; s.blocks.pop_back())
+        bm->drop(s.blocks.back());
+    }
+    for (int i = 0; i < n; ++i) {
+      Seq &s = *sq[i];
+      const size_t want = bm->blocks_for((int64_t)s.len + counts[i]);
+      cow_pairs_out[2 * i] = cow_pairs_out[2 * i + 1] = -1;
+      if (counts[i] > 0 && !bm->opens_block(s)) bm->unshare(s.blocks[s.len / B], cow_pairs_out + 2 * i);
+      while (s.blocks.size() < want) s.blocks.push_back(bm->take());
+      for (int64_t j = s.len; j < (int64_t)s.len + counts[i]; ++j) *slots_out++ = (int64_t)s.blocks[j / B] * B + j % B;
+    }
+    return PA_OK;
+  });
+}
+
+int pa_bm_commit_batch(pa_bm *bm, const int32_t *seq_ids, const int32_t *counts, const int32_t *tokens, int n) {
+  if (!bm || n < 0 || (n > 0 && (!seq_ids || !counts))) return PA_ERR_INVALID;
+  if (n == 0) return PA_OK;
+  return guarded([&]() -> int {
+    const uint64_t call = ++bm->batch_no;
+    const int st = bm->find_batch(seq_ids, n, call);
+    if (st != PA_OK) return st;
+    Seq **sq = bm->batch_seqs.data();
+    const int B = bm->block_size;
+    bool fills = false;
+    for (int i = 0; i < n; ++i) {
+      const Seq &s = *sq[i];
+      if (counts[i] < 0 || counts[i] > INT_MAX - s.len) return PA_ERR_INVALID;
+      const size_t want = bm->blocks_for((int64_t)s.len + counts[i]);
+      if (want > s.blocks.size()) return PA_ERR_STATE;
+      if (counts[i] > 0)
+        for (size_t j = s.len / B; j < want; ++j)
+          if (bm->ref[s.blocks[j]] > 1) return PA_ERR_STATE;
+      fills |= tokens && s.tracked && (s.len + counts[i]) / B > s.len / B;
+    }
+    if (fills) bm->ensure_keys();
+    for (int i = 0; i < n; ++i)
+      for (int k = 0; k < counts[i]; ++k) {
+        int64_t slot, cow[2];
+        bm->append_one(*sq[i], &slot, cow, tokens);
+        if (tokens) ++tokens;
+      }
+    return PA_OK;
+  });
+}
+
 int pa_bm_num_free_host(const pa_bm *bm) { return bm ? (int)bm->host_free.size() : -1; }
 
 }  // extern "C"
@@ -679,18 +772,19 @@ int pa_bm_num_free_host(const pa_bm *bm) { return bm ? (int)bm->host_free.size()
 namespace {
 
 int64_t wasted_slots(const pa_bm *bm) {
-  // Only a sequence's last block can be partly filled.  A block shared by
-  // several sequences is counted once, with the largest fill among them.
+  // Only a sequence's last block can be partly filled, and the reserved ones
+  // behind it are empty.  A block shared by several sequences is counted once,
+  // with the largest fill among them.
   std::unordered_map<int32_t, int> fill;
   for (const auto &kv : bm->seqs) {
     const Seq &s = kv.second;
     if (s.blocks.empty() || s.swapped) continue;
-    int f = s.len - (int)(s.blocks.size() - 1) * bm->block_size;
-    auto it = fill.find(s.blocks.back());
-    if (it == fill.end())
-      fill.emplace(s.blocks.back(), f);
-    else
+    const size_t B = bm->block_size, len = s.len;
+    for (size_t i = len > 0 ? (len - 1) / B : 0; i < s.blocks.size(); ++i) {
+      const int f = (int)(len > i * B ? std::min(B, len - i * B) : 0);
+      auto it = fill.emplace(s.blocks[i], f).first;
       it->second = std::max(it->second, f);
+    }
   }
   int64_t w = 0;
   for (const auto &kv : fill) w += bm->block_size - kv.second;

@@ -1,0 +1,31 @@
+// Trees of drafted tokens, device side: where a sequence's nodes lie in the
+// packed arrays and which parents are good.
+#pragma once
+
+#include "pa_internal.h"
+#include "pagedattn.h"
+
+namespace pa {
+namespace {
+
+// A sequence's nodes: rows first .. first + count - 1 of the packed arrays.
+struct TreeRange {
+  int first, count;
+  bool bad;  // not within [0, total], decreasing, or more nodes than the call takes
+};
+
+__device__ __forceinline__ TreeRange tree_range(const int32_t *cu, int s, int total, int max_nodes) {
+  TreeRange r;
+  r.first = __ldg(cu + s);
+  const int end = __ldg(cu + s + 1);
+  r.bad = r.first < 0 || end < r.first || end > total;
+  r.count = r.bad ? 0 : end - r.first;
+  r.bad = r.bad || r.count > max_nodes;
+  return r;
+}
+
+// A node's parent is an earlier node of its tree, or -1.
+__device__ __forceinline__ bool good_parent(int node, int parent) { return parent >= -1 && parent < node; }
+
+}  // namespace
+}  // namespace pa

@@ -1,0 +1,259 @@
+"""The block manager's part of decoding with trees: reserve and commit."""
+import random
+
+import numpy as np
+import pytest
+
+import paged_kv_cache_262_gb300 as pa
+from paged_kv_cache_262_gb300 import build as pbuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    pbuild.build()
+    return pa.load()
+
+
+def status(f, *args):
+    with pytest.raises(pa.PaError) as e:
+        f(*args)
+    return e.value.status
+
+
+def slots_of(bm, s, first, n):
+    t, B = bm.block_table(s), bm.block_size
+    return [t[j // B] * B + j % B for j in range(first, first + n)]
+
+
+def test_reserve_gives_slots_and_keeps_the_length():
+    bm = pa.BlockManager(20, 16)
+    bm.add_seq(0, 10)
+    bm.add_seq(1, 32)
+    bm.add_seq(2, 0)
+    slots, cows = bm.reserve([1, 0, 2], [3, 30, 0])
+    assert (cows == -1).all()
+    assert [bm.seq_len(s) for s in (0, 1, 2)] == [10, 32, 0]
+    assert slots.tolist() == slots_of(bm, 1, 32, 3) + slots_of(bm, 0, 10, 30)
+    assert [len(bm.block_table(s)) for s in (0, 1, 2)] == [3, 3, 0]
+    assert bm.num_free() == 14
+    # asked again for less: what is not needed goes back
+    slots, _ = bm.reserve([0, 1], [2, 0])
+    assert slots.tolist() == slots_of(bm, 0, 10, 2)
+    assert [len(bm.block_table(s)) for s in (0, 1)] == [1, 2] and bm.num_free() == 17
+    assert bm.wasted_slots() == 6
+
+
+def test_commit_is_the_appends_into_the_reserved_slots():
+    for ids in (False, True):
+        a, b = pa.BlockManager(30, 4), pa.BlockManager(30, 4)
+        prompt = [5, 6, 7, 8, 9, 1]
+        for m in (a, b):
+            m.add_seq_tokens(0, prompt)
+        rng = random.Random(1)
+        for _ in range(8):
+            n, k = 9, rng.randrange(0, 7)
+            slots, cows = a.reserve([0], [n])
+            toks = [rng.randrange(50) for _ in range(k)]
+            a.commit([0], [k], toks if ids else None)
+            want = [b.append(0, t if ids else None)[0] for t in toks]
+            assert len(want) == k and a.seq_len(0) == b.seq_len(0)
+            # the tokens lie where the reservation said
+            assert slots.tolist()[:k] == slots_of(a, 0, a.seq_len(0) - k, k)
+            assert a.num_cached_blocks() == b.num_cached_blocks()
+        a.reserve([0], [0])
+        assert len(a.block_table(0)) == len(b.block_table(0)) == -(-a.seq_len(0) // 4)
+        assert a.num_free() == b.num_free() and a.wasted_slots() == b.wasted_slots()
+
+
+def test_committed_blocks_are_found_by_later_prompts():
+    bm = pa.BlockManager(30, 4)
+    bm.add_seq_tokens(0, [1, 2, 3])
+    bm.reserve([0], [12])
+    bm.commit([0], [6], [4, 5, 6, 7, 8, 9])
+    assert bm.num_cached_blocks() == 2
+    assert bm.add_seq_tokens(1, [1, 2, 3, 4, 5, 6, 7, 8, 10]) == 8
+    assert bm.block_table(1)[:2] == bm.block_table(0)[:2]
+    # an id not given ends it
+    bm.commit([0], [2])
+    bm.reserve([0], [12])
+    bm.commit([0], [8], list(range(8)))
+    assert bm.num_cached_blocks() == 2
+
+
+def test_appends_fill_reserved_blocks():
+    bm = pa.BlockManager(8, 4)
+    bm.add_seq(0, 4)
+    bm.add_seq(1, 3)
+    slots, _ = bm.reserve([0, 1], [6, 1])
+    free = bm.num_free()
+    got = [bm.append(0) for _ in range(4)]
+    assert [g[0] for g in got] == slots.tolist()[:4] and all(g[1] is None for g in got)
+    s, c = bm.append_batch([0, 1])
+    assert s.tolist() == [slots[4], slots[6]] and (c == -1).all()
+    assert bm.num_free() == free
+
+
+def test_a_shared_last_block_is_copied_on_write():
+    bm = pa.BlockManager(20, 16)
+    bm.add_seq(0, 20)
+    bm.fork(0, 1)
+    bm.fork(0, 2)
+    before = bm.block_table(0)
+    slots, cows = bm.reserve([0, 1, 2], [2, 3, 20])
+    # the last holder keeps the block
+    assert [tuple(c) for c in cows.tolist()] == [(before[1], bm.block_table(0)[1]), (before[1], bm.block_table(1)[1]),
+                                                 (-1, -1)]
+    assert bm.block_table(2)[1] == before[1] and bm.ref_count(before[1]) == 1 and bm.ref_count(before[0]) == 3
+    assert slots.tolist() == slots_of(bm, 0, 20, 2) + slots_of(bm, 1, 20, 3) + slots_of(bm, 2, 20, 20)
+    bm.commit([0, 1, 2], [2, 1, 0])
+    assert [bm.seq_len(s) for s in range(3)] == [22, 21, 20]
+
+
+def test_no_tokens_no_copy():
+    bm = pa.BlockManager(20, 16)
+    bm.add_seq(0, 20)
+    bm.fork(0, 1)
+    slots, cows = bm.reserve([0, 1], [0, 0])
+    assert slots.size == 0 and (cows == -1).all() and bm.block_table(0) == bm.block_table(1)
+
+
+def test_forks_do_not_share_reserved_blocks():
+    bm = pa.BlockManager(20, 16)
+    bm.add_seq(0, 16)
+    bm.reserve([0], [40])
+    bm.fork(0, 1)
+    assert bm.block_table(1) == bm.block_table(0)[:1]
+    assert [bm.ref_count(b) for b in bm.block_table(0)] == [2, 1, 1, 1]
+    bm.commit([0], [3])  # the full block is shared, the reserved ones are its own
+    slot, cow = bm.append(1)
+    assert cow is None and slot // 16 not in bm.block_table(0)
+    bm.free_seq(0)
+    bm.free_seq(1)
+    assert bm.num_free() == 20
+    # a partly filled block forked after its reservation stands in the way
+    bm.add_seq(0, 10)
+    bm.reserve([0], [3])
+    bm.fork(0, 1)
+    assert status(bm.commit, [0], [2]) == pa.PA_ERR_STATE
+    _, cows = bm.reserve([0], [3])
+    assert cows[0, 0] >= 0
+    bm.commit([0], [2])
+    assert bm.seq_len(0) == 12 and bm.seq_len(1) == 10
+
+
+def snapshot(bm, ids):
+    return [(bm.block_table(s), bm.seq_len(s)) for s in ids], bm.num_free(), bm.num_cached_blocks(), bm.wasted_slots()
+
+
+def test_errors_change_nothing():
+    bm = pa.BlockManager(10, 4, 10)
+    for s, n in ((0, 6), (1, 8), (2, 4)):
+        bm.add_seq(s, n)
+    bm.fork(0, 3)
+    bm.swap_out(2)
+    bm.reserve([1], [4])
+    ids = [0, 1, 3]
+    before = snapshot(bm, ids)
+    S, I, M = pa.PA_ERR_STATE, pa.PA_ERR_INVALID, pa.PA_ERR_OOM
+    for want, a, n in ((S, [0, 9], [1, 1]), (S, [0, 2], [1, 1]), (I, [0, 1, 0], [1, 1, 1]), (I, [0, 1], [1, -1]),
+                       (M, [0, 1], [4, 30]), (I, [0], [2**31 - 1])):
+        out = np.full(64, -7, np.int64)
+        cow = np.full(64, -7, np.int64)
+        a_, n_ = np.array(a, np.int32), np.array(n, np.int32)
+        st = pa.load().pa_bm_reserve_batch(bm._h, a_.ctypes.data, n_.ctypes.data, len(a), out.ctypes.data,
+                                           cow.ctypes.data)
+        assert st == want, (a, n)
+        assert snapshot(bm, ids) == before and (out == -7).all() and (cow == -7).all()
+    for want, a, n in ((S, [1, 9], [1, 1]), (S, [1, 2], [1, 1]), (I, [1, 1], [1, 1]), (I, [1], [-1]), (S, [1], [5]),
+                       (S, [0], [1]), (I, [1], [2**31 - 1])):
+        assert status(bm.commit, a, n) == want, (a, n)
+        assert snapshot(bm, ids) == before
+    with pytest.raises(ValueError):
+        bm.reserve([0, 1], [1])
+    with pytest.raises(ValueError):
+        bm.commit([1], [2], [5])
+    lib = pa.load()
+    assert lib.pa_bm_reserve_batch(None, None, None, 0, None, None) == I
+    assert lib.pa_bm_reserve_batch(bm._h, None, None, 1, None, None) == I
+    assert lib.pa_bm_reserve_batch(bm._h, None, None, 0, None, None) == pa.PA_OK
+    assert lib.pa_bm_commit_batch(bm._h, None, None, None, 1) == I
+    assert lib.pa_bm_commit_batch(bm._h, None, None, None, 0) == pa.PA_OK
+
+
+def test_released_blocks_serve_the_same_call():
+    bm = pa.BlockManager(6, 4)
+    bm.add_seq(0, 4)
+    bm.add_seq(1, 4)
+    bm.reserve([0], [16])
+    assert bm.num_free() == 0
+    slots, _ = bm.reserve([1, 0], [16, 0])
+    assert slots.tolist() == slots_of(bm, 1, 4, 16) and bm.num_free() == 0
+    assert len(bm.block_table(0)) == 1
+
+
+def test_swap_evict_and_free_with_reserved_blocks():
+    bm = pa.BlockManager(12, 4, 12)
+    bm.add_seq(0, 10)
+    bm.reserve([0], [9])
+    assert len(bm.swap_out(0)) == 5 and bm.num_free() == 12
+    assert len(bm.swap_in(0)) == 5 and bm.num_free() == 7
+    assert len(bm.evict(0, 5)) == 2 and bm.num_free() == 10 and bm.seq_len(0) == 5
+    bm.reserve([0], [9])
+    dst, lens = bm.evict_batch([0], [99], 8)
+    assert lens.tolist() == [5] and bm.block_table(0) == dst[0, :4].tolist()
+    bm.free_seq(0)
+    assert bm.num_free() == 12 and bm.wasted_slots() == 0
+
+
+def test_random_steps_against_a_model():
+    rng = random.Random(7)
+    bm = pa.BlockManager(60, 4)
+    lens, n = {}, 0
+    for _ in range(1500):
+        op = rng.random()
+        ids = list(lens)
+        if op < 0.1 and len(ids) < 8:
+            k = rng.randrange(12)
+            try:
+                bm.add_seq_tokens(n, [rng.randrange(3) for _ in range(k)])
+                lens[n] = k
+                n += 1
+            except pa.PaError as e:
+                assert e.status == pa.PA_ERR_OOM
+        elif op < 0.15 and ids:
+            s = rng.choice(ids)
+            bm.fork(s, n)
+            lens[n] = lens[s]
+            n += 1
+        elif op < 0.22 and ids:
+            s = rng.choice(ids)
+            bm.free_seq(s)
+            del lens[s]
+        elif ids:
+            some = rng.sample(ids, rng.randrange(1, len(ids) + 1))
+            counts = [rng.randrange(0, 9) for _ in some]
+            try:
+                slots, cows = bm.reserve(some, counts)
+            except pa.PaError as e:
+                assert e.status == pa.PA_ERR_OOM
+                continue
+            at = 0
+            for s, c in zip(some, counts):
+                assert slots[at:at + c].tolist() == slots_of(bm, s, lens[s], c)
+                at += c
+                assert len(bm.block_table(s)) == -(-(lens[s] + c) // 4)
+            assert len(set(slots.tolist())) == len(slots)
+            take = [rng.randrange(0, c + 1) for c in counts]
+            bm.commit(some, take, [rng.randrange(3) for _ in range(sum(take))])
+            for s, k in zip(some, take):
+                lens[s] += k
+        refs = {}
+        for s in lens:
+            assert bm.seq_len(s) == lens[s]
+            for b in bm.block_table(s):
+                refs[b] = refs.get(b, 0) + 1
+        assert all(bm.ref_count(b) == refs.get(b, 0) for b in range(60))
+        assert bm.num_free() == 60 - len(refs)
+    for s in list(lens):
+        bm.free_seq(s)
+    assert bm.num_free() == 60

@@ -1,0 +1,463 @@
+"""Verification of trees of drafted tokens, compaction of their accepted
+paths, and whole steps with the block manager, on the GPU."""
+import math
+import random
+
+import numpy as np
+import pytest
+
+import gpu_util
+import long_context_ref as lc
+import tree_ref as tr
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return gpu_util.need_gpu()
+
+
+@pytest.fixture(scope="module")
+def pa(torch):
+    import paged_kv_cache_262_gb300 as pa
+    return pa
+
+
+def i32(torch, x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def make_verify(torch, nodes, V, dtype, seed, kind="any", right=0.6, coarse=False, pad=0, spare=2):
+    rng = random.Random(seed)
+    trees = [tr.make_tree(t, kind, rng) for t in nodes]
+    cu = [0]
+    for t in nodes:
+        cu.append(cu[-1] + t)
+    N = cu[-1] + spare
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(N, V + pad, generator=g, device="cuda")
+    if coarse:  # ties everywhere
+        x = x.round()
+    x[:, V:] = math.inf  # padding behind the vocabulary
+    x = x.to(dtype)
+    best = x[:, :V].float().argmax(1).tolist()
+    tokens = []
+    for c, tree in zip(cu, trees):
+        for p in tree:
+            tokens.append(best[c + p] if p >= 0 and rng.random() < right else rng.randrange(V))
+    return dict(x=x, tokens=tokens + [0] * spare, trees=trees, cu=cu, V=V, most=max(max(nodes), 1), N=N)
+
+
+def verify(pa, torch, m, logits=None, most=None, cu=None, trees=None, expect_err=0):
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = m["x"][:, :m["V"]] if logits is None else logits
+    trees = m["trees"] if trees is None else trees
+    flat = [p for t in trees for p in t]
+    targets = torch.full((m["N"],), -5, dtype=torch.int32, device="cuda")
+    got = pa.verify_tree(x, i32(torch, m["tokens"]), i32(torch, flat + [-1] * (m["N"] - len(flat))),
+                         i32(torch, m["cu"] if cu is None else cu), max_tree_nodes=most or m["most"],
+                         targets=targets, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == expect_err
+    return [t.cpu().tolist() for t in got]
+
+
+def check_verify(pa, torch, m, **kw):
+    targets, path, lens, nexts = verify(pa, torch, m, **kw)
+    rt, rp, rn = tr.ref_verify(m["x"], m["tokens"], m["trees"], m["cu"], m["V"])
+    n = m["cu"][-1]
+    assert targets[:n] == rt[:n] and all(t == -5 for t in targets[n:])
+    most = kw.get("most") or m["most"]
+    assert path == [p + [-1] * (most - len(p)) for p in rp]
+    assert lens == [len(p) for p in rp] and nexts == rn
+    return rp
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("nodes,V", [([1], 1), ([1], 7), ([3, 0, 2], 33), ([8], 32000), ([5, 1, 40, 0, 17], 50001),
+                                     ([256, 3], 1000), ([26] * 12, 4096), ([2], 300007), ([0, 0], 10)])
+def test_verify(pa, torch, dtype, nodes, V):
+    paths = check_verify(pa, torch, make_verify(torch, nodes, V, getattr(torch, dtype), seed=V + len(nodes)))
+    assert sum(map(len, paths)) >= sum(t > 0 for t in nodes)
+
+
+@pytest.mark.parametrize("kind", ["chain", "star", "roots"])
+def test_verify_kinds(pa, torch, kind):
+    check_verify(pa, torch, make_verify(torch, [64, 256, 1], 200, torch.bfloat16, 5, kind, right=0.95), most=256)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_verify_ties_go_to_the_lowest(pa, torch, dtype):
+    check_verify(pa, torch, make_verify(torch, [9, 4, 30], 5000, getattr(torch, dtype), 6, coarse=True))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("pad,shift", [(1, 0), (3, 1), (8, 5), (0, 3)])
+def test_verify_strides_and_alignment(pa, torch, dtype, pad, shift):
+    """Rows whose ends and starts lie anywhere, with infinities in the padding."""
+    m = make_verify(torch, [9, 4, 30], 1021, getattr(torch, dtype), 7, pad=pad)
+    flat = torch.full((shift + m["N"] * (1021 + pad),), math.inf, dtype=m["x"].dtype, device="cuda")
+    rows = flat[shift:].view(m["N"], 1021 + pad)
+    rows.copy_(m["x"])
+    check_verify(pa, torch, m, logits=rows[:, :1021])
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_verify_special_values(pa, torch, dtype):
+    m = make_verify(torch, [12], 3000, getattr(torch, dtype), 8)
+    x = m["x"]
+    x[0] = -math.inf                                   # nothing but -infinity: token 0
+    x[1, 1000], x[1, 2000], x[1, 500] = math.nan, math.nan, math.inf  # the first NaN
+    x[2] = -x[2].abs()                                 # only negative values
+    x[3] = 0.0
+    x[3, ::2] = -0.0                                   # -0 equals 0
+    x[4, 2999] = math.inf
+    x[5] = -math.inf
+    x[5, 2998] = torch.finfo(x.dtype).min
+    x[6, 77] = -math.nan
+    check_verify(pa, torch, m)
+
+
+def test_verify_duplicate_children(pa, torch):
+    """Two children with the target's token: the lower one."""
+    m = make_verify(torch, [6], 50, torch.bfloat16, 9)
+    m["trees"] = [[-1, 0, 0, 0, 1, 2]]
+    best = [int(m["x"][i, :50].float().argmax()) for i in range(6)]
+    m["tokens"] = [0, 49 if best[0] != 49 else 48, best[0], best[0], best[1], best[2], 0, 0]
+    assert check_verify(pa, torch, m) == [[0, 2, 5]]
+
+
+def test_verify_bad_trees(pa, torch):
+    m = make_verify(torch, [4, 5, 6], 90, torch.bfloat16, 10, "chain", right=1.0)
+    good = tr.ref_verify(m["x"], m["tokens"], m["trees"], m["cu"], 90)
+    # too many nodes in the last
+    targets, path, lens, nexts = verify(pa, torch, m, most=5, expect_err=pa.DEVERR_TREE)
+    assert lens == [4, 5, 0] and nexts[2] == -1 and path[2] == [-1] * 5 and targets[9:] == [-5] * 8
+    for cu in ([0, 4, 9, 99], [0, 4, 9, 3], [0, 4, 9, -1]):
+        targets, path, lens, nexts = verify(pa, torch, m, cu=cu, expect_err=pa.DEVERR_TREE)
+        assert lens == [4, 5, 0] and nexts[:2] == good[2][:2] and nexts[2] == -1 and targets[9:] == [-5] * 8
+    for node, parent in ((2, 2), (2, 3), (2, -2), (2, 2**31 - 1)):  # the chain ends before it
+        trees = [list(t) for t in m["trees"]]
+        trees[1][node] = parent
+        _, path, lens, _ = verify(pa, torch, m, trees=trees, expect_err=pa.DEVERR_TREE)
+        assert lens == [4, 2, 6] and path[1] == [0, 1, -1, -1, -1, -1]
+    trees = [list(t) for t in m["trees"]]
+    trees[1][0] = 0
+    _, path, lens, nexts = verify(pa, torch, m, trees=trees, expect_err=pa.DEVERR_TREE)
+    assert lens == [4, 0, 6] and nexts[1] == -1
+
+
+def test_verify_graph_and_streams(pa, torch):
+    a = make_verify(torch, [9, 4, 30], 9000, torch.bfloat16, 11)
+    b = make_verify(torch, [9, 4, 30], 9000, torch.bfloat16, 12)
+    x, tok, par, cu = a["x"].clone(), i32(torch, a["tokens"]), i32(torch, [0] * a["N"]), i32(torch, a["cu"])
+    s = torch.cuda.Stream()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(pa.verify_tree(x, tok, par, cu, max_tree_nodes=30))
+        graphs.append(g)
+    for m in (a, b, a):
+        x.copy_(m["x"])
+        tok.copy_(i32(torch, m["tokens"]))
+        flat = [p for t in m["trees"] for p in t]
+        par.copy_(i32(torch, flat + [-1] * (m["N"] - len(flat))))
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        rt, rp, rn = tr.ref_verify(m["x"], m["tokens"], m["trees"], m["cu"], 9000)
+        for o in outs:
+            assert o[0][:m["cu"][-1]].tolist() == rt[:m["cu"][-1]]
+            assert o[1].tolist() == [p + [-1] * (30 - len(p)) for p in rp] and o[3].tolist() == rn
+
+
+def test_verify_refusals(pa, torch):
+    m = make_verify(torch, [3, 2], 64, torch.bfloat16, 13, spare=0)
+    args = [m["x"], i32(torch, m["tokens"]), i32(torch, [p for t in m["trees"] for p in t]), i32(torch, m["cu"])]
+
+    def refused(i, x, **kw):
+        a = list(args)
+        a[i] = x
+        with pytest.raises((TypeError, ValueError)):
+            pa.verify_tree(*a, **{"max_tree_nodes": 3, **kw})
+
+    refused(0, m["x"].half())
+    refused(0, m["x"].cpu())
+    refused(0, m["x"].t())
+    refused(0, m["x"][0])
+    refused(0, m["x"][:1].expand(5, 64))
+    refused(0, None)
+    refused(1, args[1].long())
+    refused(1, args[1][:4])
+    refused(2, args[2][:4])
+    refused(3, args[3][:0])
+    refused(0, args[0], max_tree_nodes=0)
+    refused(0, args[0], max_tree_nodes=257)
+    refused(0, args[0], path=torch.empty(2, 2, dtype=torch.int32, device="cuda"))
+    # no sequences
+    got = pa.verify_tree(m["x"][:0], args[1][:0], args[2][:0], args[3][:1], max_tree_nodes=3)
+    assert [tuple(t.shape) for t in got] == [(0,), (0, 3), (0,), (0,)]
+
+
+# ------------------------------------------------------------------ commit
+def make_commit(torch, ctx, nodes, paths, Hkv, D, B, L, seed, most=None):
+    c = lc.make_cache([a + b for a, b in zip(ctx, nodes)], Hkv, D, B, seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    # any bits, NaN among them
+    c["pools"] = [torch.randint(-32768, 32768, c["k"].shape, generator=g, device="cuda", dtype=torch.int16)
+                  .view(torch.bfloat16) for _ in range(2 * L)]
+    most = most or max([len(p) for p in paths] + [1])
+    c.update(ctx=i32(torch, ctx), path=i32(torch, [p + [-1] * (most - len(p)) for p in paths]),
+             path_lens=i32(torch, [len(p) for p in paths]), contexts=ctx, paths=paths, L=L)
+    return c
+
+
+def ref_commit(c, skip=(), drop=()):
+    """The pools after the call; `drop`: (sequence, logical block) outside the pool."""
+    B, out = c["B"], [p.clone() for p in c["pools"]]
+    for s, path in enumerate(c["paths"]):
+        if s in skip:
+            continue
+        at = lambda j: (int(c["bt"][s, j // B]), j % B)  # noqa: E731
+        for i, p in enumerate(path):
+            if (s, (c["contexts"][s] + p) // B) in drop or (s, (c["contexts"][s] + i) // B) in drop:
+                continue
+            (fb, fo), (tb, to) = at(c["contexts"][s] + p), at(c["contexts"][s] + i)
+            for old, new in zip(c["pools"], out):
+                new[tb, :, to] = old[fb, :, fo]
+    return out
+
+
+def commit(pa, torch, c, **kw):
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new = pa.commit_tree(c["pools"][:c["L"]], c["pools"][c["L"]:], c["bt"], c["ctx"], c["path"], c["path_lens"],
+                         err_flag=err, **kw)
+    torch.cuda.synchronize()
+    return new.tolist(), int(err.item())
+
+
+def same(a, b):
+    import torch
+    return all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(a, b))
+
+
+def random_path(rng, t, n):
+    return sorted(rng.sample(range(t), n))
+
+
+@pytest.mark.parametrize("ctx,nodes,lens,hkv,d,b,L", [
+    ([0], [1], [1], 1, 64, 16, 1),
+    ([0, 5], [3, 4], [0, 4], 2, 128, 16, 2),
+    ([15, 16, 17, 31], [8, 8, 8, 8], [3, 8, 1, 5], 8, 128, 16, 3),
+    ([100, 0, 37], [256, 200, 255], [256, 77, 130], 3, 64, 32, 2),
+    ([33] * 20, [26] * 20, list(range(20)), 5, 128, 32, 1),
+    ([9], [12], [6], 1, 128, 16, 130),
+])
+def test_commit(pa, torch, ctx, nodes, lens, hkv, d, b, L):
+    rng = random.Random(len(ctx) + L)
+    paths = [random_path(rng, t, n) for t, n in zip(nodes, lens)]
+    c = make_commit(torch, ctx, nodes, paths, hkv, d, b, L, seed=L)
+    want = ref_commit(c)
+    new, err = commit(pa, torch, c)
+    assert err == 0 and new == [a + n for a, n in zip(ctx, lens)]
+    assert same(c["pools"], want)
+
+
+def test_commit_overlapping_moves(pa, torch):
+    """Every other node accepted: each row's source is a later row's destination."""
+    path = list(range(0, 250, 2))
+    c = make_commit(torch, [7], [250], [path], 4, 128, 16, 2, seed=3, most=256)
+    want = ref_commit(c)
+    assert commit(pa, torch, c) == ([7 + 125], 0) and same(c["pools"], want)
+    path = [i + 1 for i in range(249)]  # all but the first, each moving up by one
+    c = make_commit(torch, [7], [250], [path], 4, 128, 16, 2, seed=4)
+    want = ref_commit(c)
+    assert commit(pa, torch, c) == ([7 + 249], 0) and same(c["pools"], want)
+
+
+def test_commit_bad_sequences_stay(pa, torch):
+    ctx, nodes = [50, 60, 70], [8, 8, 8]
+    for s, what, value, bit in ((1, "ctx", -1, "CTX"), (1, "path_lens", -1, "CTX"), (1, "path_lens", 9, "CTX"),
+                                (1, "path", -1, "TREE"), (1, "path", 2, "TREE"), (1, "path", 500, "TREE"),
+                                (1, "path", 2**31 - 1, "TREE"), (1, "ctx", 2**31 - 1, "TREE")):
+        paths = [[0, 3, 5], [0, 2, 6, 7], [1, 4]]
+        c = make_commit(torch, ctx, nodes, paths, 2, 128, 16, 2, seed=5, most=8)
+        want = ref_commit(c, skip=(s,))
+        if what == "path":
+            c["path"][s, 2] = value
+        else:
+            c[what][s] = value
+        new, err = commit(pa, torch, c)
+        assert err == getattr(pa, "DEVERR_" + bit), (what, value)
+        assert new == [53, value if what == "ctx" else 60, 72] and same(c["pools"], want)
+    c = make_commit(torch, ctx, nodes, paths, 2, 128, 16, 2, seed=5, most=8)
+    want = ref_commit(c, skip=(2,))
+    assert commit(pa, torch, c, max_context_len=74) == ([53, 64, 70], pa.DEVERR_TREE)  # 70 + 4 is past it
+    assert same(c["pools"], want)
+
+
+def test_commit_pages_outside_the_pool(pa, torch):
+    c = make_commit(torch, [10], [40], [[0, 3, 9, 10, 20, 30, 39]], 2, 128, 16, 1, seed=6)
+    want = ref_commit(c, drop=((0, 1),))
+    c["bt"][0, 1] = c["k"].shape[0]
+    assert commit(pa, torch, c) == ([17], pa.DEVERR_PAGE) and same(c["pools"], want)
+
+
+def test_commit_pool_past_32_bit_offsets(pa, torch):
+    hkv, d, b = 8, 128, 32
+    nblk = (1 << 31) // (hkv * d * b) + 40
+    c = make_commit(torch, [40], [40], [[0, 3, 9, 30]], hkv, d, b, 1, seed=7)
+    want = ref_commit(c)
+    big = [torch.zeros(nblk, hkv, b, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    old = c["bt"].clone()
+    for i in range(3):
+        for x, p in zip(big, c["pools"]):
+            x[nblk - 1 - 5 * i] = p[int(old[0, i])]
+        c["bt"][0, i] = nblk - 1 - 5 * i
+    c["pools"] = big
+    assert commit(pa, torch, c) == ([44], 0)
+    for i in range(3):
+        assert same([x[nblk - 1 - 5 * i] for x in big], [w[int(old[0, i])] for w in want])
+
+
+def test_commit_refusals(pa, torch):
+    c = make_commit(torch, [50, 60], [8, 8], [[0, 1], [0]], 2, 128, 16, 2, seed=8)
+    K, V = c["pools"][:2], c["pools"][2:]
+    args = [K, V, c["bt"], c["ctx"], c["path"], c["path_lens"]]
+
+    def refused(i, x, *more):
+        a = list(args)
+        a[i] = x
+        with pytest.raises((TypeError, ValueError)):
+            pa.commit_tree(*a, *more)
+
+    refused(0, [])
+    refused(1, V[:1])
+    refused(1, [V[0], V[1][:-1]])
+    refused(0, [K[0].float(), K[1]])
+    refused(2, c["bt"][:1])
+    refused(4, c["path"][:1])
+    refused(5, c["path_lens"][:1])
+    refused(5, c["path_lens"].long())
+    refused(3, c["ctx"], c["ctx"])         # new_lens over an input
+    refused(3, c["ctx"], c["path_lens"])
+    refused(3, c["ctx"], torch.empty(3, dtype=torch.int32, device="cuda"))
+    wide = torch.full((2, 257), -1, dtype=torch.int32, device="cuda")
+    with pytest.raises(pa.PaError):
+        pa.commit_tree(K, V, c["bt"], c["ctx"], wide, c["path_lens"])
+
+
+# ------------------------------------------------------------------ whole steps
+def test_steps_together(pa, torch):
+    """Sequences decoded by trees with a toy model of one attention layer: the
+    accepted tokens are those of token-by-token decoding of the same model,
+    and so is the cache."""
+    B, Hkv, Hq, D, V = 16, 2, 8, 64, 97
+    g = torch.Generator(device="cuda").manual_seed(1)
+    emb = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    wk, wv, wq, wo = emb(V, Hkv, D), emb(V, Hkv, D), emb(V, Hq, D), emb(Hq * D, V)
+    L = 2  # the second layer's cache holds the same rows with another sign
+    bm = pa.BlockManager(64, B)
+    pools = [torch.zeros(64, Hkv, B, D, dtype=torch.bfloat16, device="cuda") for _ in range(2 * L)]
+    rng = random.Random(2)
+    prompts = {0: [rng.randrange(V) for _ in range(21)], 1: [rng.randrange(V) for _ in range(16)], 2: [3]}
+
+    def write(tokens, slots):
+        t = torch.tensor(tokens, dtype=torch.int64, device="cuda")
+        s = torch.tensor(np.asarray(slots), dtype=torch.int64, device="cuda")
+        for layer in range(L):
+            sign = 1 - 2 * layer
+            pa.reshape_and_cache(wk[t] * sign, wv[t] * sign, pools[layer], pools[L + layer], s)
+
+    def logits_of(attn):
+        return (attn.reshape(attn.shape[0], -1).float() @ wo.float()).to(torch.bfloat16)
+
+    # token by token, in a cache of its own
+    def greedy(prompt, n):
+        toks, out = list(prompt), []
+        for _ in range(n):
+            t = torch.tensor(toks, device="cuda")
+            blocks = -(-len(toks) // B)
+            kp = torch.zeros(blocks, Hkv, B, D, dtype=torch.bfloat16, device="cuda")
+            vp = torch.zeros_like(kp)
+            pa.reshape_and_cache(wk[t].contiguous(), wv[t].contiguous(), kp, vp, torch.arange(len(toks), device="cuda"))
+            bt = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+            o = pa.paged_attention_decode(wq[t[-1:]].contiguous(), kp, vp, bt, i32(torch, [len(toks)]))
+            x = logits_of(o)[0].float()
+            top = x.topk(2).values
+            out.append((int(x.argmax()), float(top[0] - top[1])))
+            toks.append(out[-1][0])
+        return out
+
+    want = {s: greedy(p, 14) for s, p in prompts.items()}
+    # Up to the first narrow choice: the two ways' attention outputs differ by about 2^-8 of 0.3, rms, so their
+    # logits (sums of Hq D = 512 products with values of about 1) by about 0.03, and each is rounded to bf16 by at
+    # most 2^-3 (values under 64).
+    limit = {s: next((i for i, (_, m) in enumerate(w) if m < 0.75), len(w)) for s, w in want.items()}
+    # the prompt's last token is each first tree's root: it is not in the cache yet
+    for s, p in prompts.items():
+        bm.add_seq_tokens(s, p[:-1])
+        table = bm.block_table(s)
+        if len(p) > 1:
+            write(p[:-1], [table[j // B] * B + j % B for j in range(len(p) - 1)])
+    root = {s: p[-1] for s, p in prompts.items()}
+    done = {s: [] for s in prompts}
+    ids = list(prompts)
+    accepted_any = 0
+    for step in range(6):
+        trees, tokens, counts = [], [], []
+        for s in ids:
+            have = len(done[s])
+            future = [w[0] for w in want[s]][have:]
+            t = rng.choice((1, 4, 7))
+            tree, toks = [-1], [root[s]]
+            for i in range(1, t):
+                parent = rng.randrange(i)
+                tree.append(parent)
+                depth, at = 0, parent
+                while tree[at] >= 0:
+                    at, depth = tree[at], depth + 1
+                guess = future[depth] if depth < len(future) and rng.random() < 0.8 else rng.randrange(V)
+                toks.append(guess)
+            trees.append(tree)
+            tokens += toks
+            counts.append(t)
+        slots, cows = bm.reserve(ids, counts)
+        assert (cows == -1).all()
+        write(tokens, slots)
+        tables, lens = bm.block_tables(ids, 16)
+        bt, ctx = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+        cu = i32(torch, [0] + list(np.cumsum(counts)))
+        par, tok = i32(torch, [p for t in trees for p in t]), i32(torch, tokens)
+        err = i32(torch, [0])
+        o = pa.paged_attention_decode_tree(wq[tok.long()].contiguous(), pools[0], pools[L], bt, ctx, cu, par,
+                                           max_tree_nodes=7, err_flag=err)
+        targets, path, plen, nexts = pa.verify_tree(logits_of(o), tok, par, cu, max_tree_nodes=7, err_flag=err)
+        new = pa.commit_tree(pools[:L], pools[L:], bt, ctx, path, plen, err_flag=err)
+        assert int(err.item()) == 0
+        n = plen.tolist()
+        kept = []
+        for s, k, row, t, base in zip(ids, n, path.tolist(), counts, cu.tolist()):
+            kept += [tokens[base + i] for i in row[:k]]
+            done[s] += [tokens[base + i] for i in row[1:k]] + [nexts.tolist()[ids.index(s)]]
+            accepted_any += k - 1
+        bm.commit(ids, n, kept)
+        assert new.tolist() == [bm.seq_len(s) for s in ids]
+        for s, x in zip(ids, nexts.tolist()):
+            root[s] = x
+    assert accepted_any > 5
+    for s in ids:
+        got, upto = done[s], min(len(done[s]), limit[s])
+        assert got[:upto] == [w[0] for w in want[s]][:upto]
+        # the cache: every committed token's rows, in every layer
+        toks = torch.tensor((prompts[s] + got)[:bm.seq_len(s)], device="cuda")
+        table = torch.tensor(bm.block_table(s), device="cuda")
+        j = torch.arange(len(toks), device="cuda")
+        for layer in range(L):
+            sign = 1 - 2 * layer
+            assert torch.equal(pools[layer][table[j // B], :, j % B], wk[toks] * sign)
+            assert torch.equal(pools[L + layer][table[j // B], :, j % B], wv[toks] * sign)
