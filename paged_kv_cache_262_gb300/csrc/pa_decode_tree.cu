@@ -1,18 +1,47 @@
-// Decode attention of trees of drafted tokens over the paged cache, for
-// sm_103a: every node of every sequence's tree attends the sequence's context
-// and its own chain of ancestors,
+// Decode attention of trees of drafted tokens over the paged cache, on the
+// tcgen05 tensor cores of sm_103a: every node of every sequence's tree attends
+// the sequence's context and its own chain of ancestors,
 //   out = sum_j softmax_j(scale * q.k_j) v_j,  j < c and j = c + a, a on the chain.
 // It serves the decode phase of "Configuring vLLM and PagedAttention for High
 // Throughput Enterprise LLM Serving" ("Memory Bottlenecks in Autoregressive
 // LLM Inference": decode reads the whole cache for every token): the tokens of
-// a tree share one reading of it.
+// a tree share one reading of it.  A tree of T nodes gives R = T G query rows a
+// kv head, 4 D R operations a key against the 4 D bytes of its K and V: up to
+// about 280 rows the cache's bytes bind, past that the tensor cores.
 //
-// A CTA per (node, kv head): its four warps take the keys in turn, a lane
-// D / 32 of a key's dimensions, each of the kv head's query heads with its own
-// running maximum and sum in fp32; the warps' states are joined at the end.
+// A unit is (sequence, kv head) with its keys in tiles of 128; the units' tiles,
+// one unit after another, are cut into equal shares, one for each CTA (persistent,
+// one an SM), whatever the lengths.  A share's pieces of units that other shares
+// go on with leave partial softmax states, which a second kernel joins.  The rows
+// are the MMA's M side: a CTA holds one tile of 128 rows (floor(128 / G) nodes),
+// or two where the trees have more, and more rows than that are further CTAs that
+// read the same keys at the same time.  Roles:
+//   warps 0-3   (4-7 with two tiles) a row a thread (TMEM lane): softmax, P (bf16)
+//               back over S in TMEM, the piece's end
+//   next warp   takes the share's pieces, posts them to the others, loads their
+//               query rows and gathers K and V tiles (2-D TMA, 128-byte swizzle)
+//               into one ring, across pieces
+//   next warp   owns TMEM and issues the MMAs: S = Q K^T, O += P V
+// MMAs issued by one thread complete in order.  With one row tile S has two
+// buffers and S of the next key tile is issued before P V of this one, and the
+// probabilities are kept as a bf16 value and a bf16 remainder (2^-16 of them
+// left) in two products, which the tensor cores have the time for; with two tiles
+// these alternate, and the probabilities are rounded to bf16 once.  The running maximum moves
+// only when it grows by more than 8 (2^8), so O is seldom rescaled.
+//
+// Only tiles at and behind the context's end, or with a page outside the pool, are
+// masked.  There a key's value row meets a probability of 0 in the rows that do
+// not attend it: value rows past the tree are cleared in shared memory, and the
+// rare node whose values are not all finite is taken out of the product and added
+// to the rows that attend it one by one.  Every wait is bounded; a timeout sets
+// PA_DEVERR_TIMEOUT.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
@@ -23,120 +52,812 @@ namespace pa {
 namespace {
 
 struct TreeArgs {
-  const __nv_bfloat16 *q, *k, *v;
   const int32_t *bt, *ctx, *cu, *parents;
   __nv_bfloat16 *out;
+  float4 *ws_o;   // [share][row tile][2][D / 4][prow], sums of p v; slot 0 a piece that began before the share, 1 one that goes on past it
+  float2 *ws_ml;  // [share][row tile][2][prow], maximum and sum
+  int4 *ws_next;  // [share][row tile]: of a piece that goes on: first row, kv head, nodes, last share (-1: none)
   int32_t *err;
-  int S, Hq, Hkv, G, B, num_blocks, max_blocks, max_ctx, max_nodes, total;
+  int S, Hq, Hkv, G, num_blocks, max_blocks, max_ctx, max_nodes, total;
+  int nodes_tile;  // nodes of a row tile
+  int box;         // nodes of a query load
+  int tiles_x;     // CTAs (of one or two row tiles) a unit's rows take
+  int shares, prow;
   float scale_log2;
 };
 
-constexpr int kTrWarps = 4;
+constexpr int kTM = 128;                 // rows of a row tile
+constexpr int kTN = 128;                 // keys of a key tile
+constexpr int kTHalf = kTN * 128;        // 64 columns of a tile
+constexpr int kTPosts = 4;               // pieces posted ahead
+constexpr int kTPostWords = 16;
+constexpr int kTRegsLaunch = 168, kTRegsSoftmax = 216, kTRegsOther = 72;  // two row tiles (see pa_prefill_body.cuh)
+static_assert(256 * kTRegsSoftmax + 128 * kTRegsOther <= 384 * kTRegsLaunch, "register split");
 
-template <int D>
-__global__ void __launch_bounds__(kTrWarps * 32) tree_kernel(const TreeArgs a) {
-  constexpr int E = D / 32;
-  __shared__ int chain[PA_MAX_TREE_NODES];
-  __shared__ int len;
-  __shared__ float so[kTrWarps][16][D], sm[kTrWarps][16], sl[kTrWarps][16];
-  const int i = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+template <int D, int NT>
+struct TreeSmem {
+  static constexpr int kTile = D / 64 * kTHalf;          // 128 rows
+  static constexpr int kSets = NT == 1 ? 2 : 1;          // of query rows
+  static constexpr int kSlots = D == 128 ? 5 : 10;       // K and V tiles in flight
+  static constexpr int kOffRing = kSets * NT * kTile;
+  static constexpr int kOffBar = kOffRing + kSlots * kTile;
+  static constexpr int kFull = 0, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots, kPFull = kSFull + 2,
+                       kPV = kPFull + 2, kQFull = kPV + 2, kQEmpty = kQFull + 2, kUFull = kQEmpty + 2,
+                       kUEmpty = kUFull + kTPosts, kVote = kUEmpty + kTPosts, kRead = kVote + 2, kDone = kRead + 1,
+                       kBars = kDone + 1;
+  static constexpr int kOffPost = kOffBar + kBars * 8;
+  static constexpr int kOffPages = kOffPost + kTPosts * kTPostWords * 4;  // [8] valid pages of the latest key tiles
+  static constexpr int kOffBad = kOffPages + 8 * 4;                       // [4][4] keys of a tree tile that are not finite
+  static constexpr int kOffScan = (kOffBad + 16 * 4 + 7) & ~7;            // [12] sums of the warps, total
+  static constexpr int kOffMisc = kOffScan + 14 * 8;                      // TMEM address, dead, first sequence, its tiles' offset
+  static constexpr int kBytes = kOffMisc + 32;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+  static constexpr int kThreads = NT == 1 ? 192 : 384;
+};
+
+// Words of a posted piece.
+enum { PP_KIND = 0, PP_ROW0, PP_NODES, PP_BASE, PP_CTX, PP_HEAD, PP_TILE, PP_TILES, PP_SLOT, PP_LIVE, PP_FIRST };
+enum { kPieceStop = 0, kPieceZero = 1, kPiece = 2 };
+
+// A sequence's tree, its context and its key tiles for each kv head: none
+// without nodes, one (whose rows become zeros) where it is refused.
+struct TreeSeq {
+  int first, count, ctx, tiles;
+  int why;  // PA_DEVERR_* bits
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int s, int B) {
   const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
-  if (r.bad && tid == 0 && a.err) atomicOr(a.err, PA_DEVERR_TREE);
-  if (i >= r.count) return;
-  const int c = __ldg(a.ctx + s);
-  const bool room = c >= 0 && c <= a.max_ctx - r.count && c <= a.max_blocks * a.B - r.count;
-  if (tid == 0) {
-    int n = 0, at = i;
-    if (r.bad || !room) {
-      at = -1;
-      if (!room && !r.bad && a.err) atomicOr(a.err, PA_DEVERR_CTX);
+  TreeSeq q{r.first, r.count, __ldg(a.ctx + s), 0, r.bad ? PA_DEVERR_TREE : 0};
+  if (r.count == 0) return q;
+  if (!q.why && (q.ctx < 0 || q.ctx > a.max_ctx - r.count || q.ctx > a.max_blocks * B - r.count)) q.why = PA_DEVERR_CTX;
+  q.tiles = q.why ? 1 : (q.ctx + r.count + kTN - 1) / kTN;
+  return q;
+}
+
+__device__ __forceinline__ long long share_begin(long long total, int shares, int i) { return total * i / shares; }
+
+// The bits of keys [key0, key0 + 128) below `n`.
+__device__ __forceinline__ uint32_t bits_below(int n, int word) {
+  const int k = n - word * 32;
+  return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+}
+
+// P of one row: 2^(x - base) for its 128 scores x = s * sc, as bf16 pairs into
+// TMEM columns [col, col + 64) and, FINE, what that rounding leaves into
+// [col + 64, col + 128); their sum, unrounded.
+template <bool FINE>
+__device__ __forceinline__ float tree_probabilities(const float (&s)[kTN], float sc, float base, uint32_t col) {
+  const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t hi[32], lo[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const int k = c * 64 + 2 * e;
+      const float2 t = fma2(make_float2(s[k], s[k + 1]), sc2, nb2);
+      const float2 p = make_float2(ex2_ftz(t.x), ex2_ftz(t.y));
+      hi[e] = pack_bf16(p.x, p.y);
+      if constexpr (FINE) lo[e] = pack_bf16(p.x - bf16_lo(hi[e]), p.y - bf16_hi(hi[e]));
+      acc[e & 3] = add2(acc[e & 3], p);
     }
-    while (at >= 0) {
-      chain[n++] = at;
-      const int p = __ldg(a.parents + r.first + at);
-      if (!good_parent(at, p)) {
-        if (a.err) atomicOr(a.err, PA_DEVERR_TREE);
-        n = 0;
+    tmem_st32(col + c * 32, hi);
+    if constexpr (FINE) tmem_st32(col + 64 + c * 32, lo);
+  }
+  const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+  return x.x + x.y;
+}
+
+template <int D, int B, int NT>
+__global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+  using L = TreeSmem<D, NT>;
+  constexpr bool FINE = NT == 1;
+  constexpr int kHalves = D / 64, PAGES = kTN / B, NS = L::kSlots, kThreads = L::kThreads;
+  constexpr uint32_t kAllPages = (1u << PAGES) - 1u;
+  constexpr uint32_t kIdS = umma_idesc_bf16(128, 128, false, false);
+  constexpr uint32_t kIdPV = umma_idesc_bf16(128, D, false, true);
+  constexpr uint32_t kColO = 256;  // S: columns 0 and 128 (two buffers, or two row tiles); O: 256 and 256 + 128
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+  int *posts = reinterpret_cast<int *>(smem + L::kOffPost);
+  volatile uint32_t *pages_of = reinterpret_cast<uint32_t *>(smem + L::kOffPages);
+  uint32_t *bad_of = reinterpret_cast<uint32_t *>(smem + L::kOffBad);
+  long long *scan = reinterpret_cast<long long *>(smem + L::kOffScan);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+  volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 4);
+  int *start_s = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
+  long long *start_off = reinterpret_cast<long long *>(smem + L::kOffMisc + 16);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kProducer = 4 * NT, kIssuer = kProducer + 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars[L::kFull + i], 1);
+      mbar_init(&bars[L::kEmpty + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[L::kSFull + i], 2);
+      mbar_init(&bars[L::kPFull + i], 128);
+      mbar_init(&bars[L::kPV + i], 1);
+      mbar_init(&bars[L::kQFull + i], 1);
+      mbar_init(&bars[L::kQEmpty + i], 128 * NT);
+      mbar_init(&bars[L::kVote + i], 128);
+    }
+    for (int i = 0; i < kTPosts; ++i) {
+      mbar_init(&bars[L::kUFull + i], 1);
+      mbar_init(&bars[L::kUEmpty + i], 128 * NT + 1);
+    }
+    mbar_init(&bars[L::kRead], 128 * NT);
+    mbar_init(&bars[L::kDone], 1);
+    for (int i = 0; i < 16; ++i) bad_of[i] = 0;
+    *dead = 0;
+    *start_s = a.S;
+    fence_mbar_init();
+  }
+  if (warp == kIssuer) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  grid_wait();
+  grid_launch_dependents();
+
+  // ---- this CTA's share of all units' key tiles
+  long long mine = 0;
+  const int per = (a.S + kThreads - 1) / kThreads;
+  for (int s = tid * per; s < min(a.S, (tid + 1) * per); ++s) {
+    const TreeSeq q = tree_seq(a, s, B);
+    mine += (long long)q.tiles * a.Hkv;
+    if (q.why && blockIdx.x == 0 && a.err) atomicOr(a.err, q.why);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const int share = blockIdx.x / a.tiles_x, tx = blockIdx.x % a.tiles_x;
+  const int shares = (int)min((long long)a.shares, total);
+  const long long beg = share < shares ? share_begin(total, shares, share) : 0;
+  const long long end = share < shares ? share_begin(total, shares, share + 1) : 0;
+  if (beg < end && beg >= before && beg < before + mine) {
+    long long at = before;
+    for (int s = tid * per;; ++s) {
+      const long long n = (long long)tree_seq(a, s, B).tiles * a.Hkv;
+      if (beg < at + n) {
+        *start_s = s;
+        *start_off = beg - at;
         break;
       }
-      at = p;
+      at += n;
     }
-    len = n;
   }
   __syncthreads();
-  // (a tree past max_nodes has rows past the grid: they are zeros too)
-  if (len == 0) {
-    for (int row = i; row < r.count; row += a.max_nodes)
-      for (int d = tid; d < a.G * D; d += kTrWarps * 32)
-        a.out[((size_t)(r.first + row) * a.Hq + (size_t)h * a.G) * D + d] = __float2bfloat16(0.f);
-    return;
-  }
-  const int keys = c + len;
-  float q[16][E], o[16][E], m[16], l[16];
+  const uint32_t tmem = *tslot;
+  auto fail = [&]() {
+    *dead = 1;
+    if (a.err) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+  };
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    if (*dead) return false;
+    if (mbar_wait(&bars[b], parity)) return true;
+    fail();
+    return false;
+  };
+  // uniform over the warp (warp collectives follow)
+  auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
+
+  if (warp >= kProducer) {
+    if constexpr (NT == 2) setmaxnreg_dec<kTRegsOther>();
+    if (warp == kProducer) {
+      // ------------------------------------------------------------ producer
+      // (the rows of further CTAs read the same keys: they stay in L2 for them)
+      const uint64_t pol = a.tiles_x > 1 ? policy_evict_normal() : policy_evict_first();
+      const int base = tx * NT * a.nodes_tile;  // first node of this CTA's rows
+      long long pos = beg;
+      int s = *start_s, window = -1;
+      TreeSeq near{};  // of sequence window + lane
+      long long off = beg < end ? *start_off : 0;
+      int u = 0, qn = 0, item = 0, jall = 0;
+      bool ok = true, goes_on = false;
+      while (ok && pos < end) {
+        if (s >> 5 != window) {
+          window = s >> 5;
+          near = TreeSeq{};
+          if (window * 32 + lane < a.S) near = tree_seq(a, window * 32 + lane, B);
+        }
+        const int tiles = __shfl_sync(0xffffffffu, near.tiles, s & 31);
+        if (tiles == 0) {
+          ++s;
+          continue;
+        }
+        const int first = __shfl_sync(0xffffffffu, near.first, s & 31), T = __shfl_sync(0xffffffffu, near.count, s & 31);
+        const int c = __shfl_sync(0xffffffffu, near.ctx, s & 31), why = __shfl_sync(0xffffffffu, near.why, s & 31);
+        const int h = (int)(off / tiles), t0 = (int)(off - (long long)h * tiles);
+        const int nt = (int)min((long long)(tiles - t0), end - pos);
+        const int left = T - base;  // nodes from this CTA's first on
+        if (why ? tx == 0 : left > 0) {
+          const int live = NT == 1 || left <= a.nodes_tile ? 1 : 2;
+          const int slot = t0 > 0 ? 0 : nt < tiles ? 1 : -1;
+          const int pb = u % kTPosts;
+          if (u >= kTPosts && !wait_warp(L::kUEmpty + pb, (uint32_t)((u / kTPosts - 1) & 1))) break;
+          if (lane == 0) {
+            int *p = posts + pb * kTPostWords;
+            p[PP_KIND] = why ? kPieceZero : kPiece;
+            p[PP_ROW0] = first + base;
+            p[PP_NODES] = T;
+            p[PP_BASE] = base;
+            p[PP_CTX] = c;
+            p[PP_HEAD] = h;
+            p[PP_TILE] = t0;
+            p[PP_TILES] = nt;
+            p[PP_SLOT] = slot;
+            p[PP_LIVE] = live;
+            p[PP_FIRST] = first;
+            mbar_arrive(&bars[L::kUFull + pb]);
+            if (slot == 1) {  // the share that has the unit's last tile
+              const long long unit_end = pos + tiles;
+              a.ws_next[blockIdx.x] = make_int4(first + base, h, left, (int)((unit_end * shares - 1) / total));
+            }
+          }
+          goes_on |= slot == 1;
+          ++u;
+          if (!why) {
+            const int set = qn % L::kSets, first_item = item;
+            bool q_due = true;
+            // the piece's query rows, as soon as the set is free; at the latest when a K or V
+            // tile would have to wait for this piece's own
+            auto queries = [&](bool now) -> bool {
+              if (qn >= L::kSets) {
+                const uint32_t par = (uint32_t)((qn / L::kSets - 1) & 1);
+                if (now) {
+                  if (!wait_warp(L::kQEmpty + set, par)) return false;
+                } else if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[L::kQEmpty + set], par))) {
+                  return true;
+                }
+              }
+              q_due = false;
+              if (lane == 0) {
+                uint64_t *bar = &bars[L::kQFull + set];
+                mbar_arrive_expect_tx(bar, (uint32_t)(live * kHalves * a.box * a.G * 128));
+                for (int x = 0; x < live; ++x)
+                  for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load_4d(smem + (set * NT + x) * L::kTile + hf * kTHalf, &tmQ, hf * 64, 0, h,
+                                first + base + x * a.nodes_tile, bar);
+              }
+              __syncwarp();
+              return true;
+            };
+            const int npages = (c + T + B - 1) / B;
+            const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
+            auto page_id = [&](int t) {  // this lane's page of key tile t (-1: none)
+              const int i = t * PAGES + lane % PAGES;
+              int pg = -1;
+              if (lane < PAGES * kHalves && i < npages) {
+                pg = __ldg(bt + i);
+                if (pg < 0 || pg >= a.num_blocks) {
+                  if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+                  pg = -1;
+                }
+              }
+              return pg;
+            };
+            int cur = page_id(t0);
+            for (int t = t0; ok && t < t0 + nt; ++t, ++jall) {
+              const int nxt = t + 1 < t0 + nt ? page_id(t + 1) : -1;  // on its way meanwhile
+              const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0) & kAllPages;
+              for (int kv = 0; kv < 2; ++kv, ++item) {
+                if (q_due && !(ok = queries(item - NS >= first_item))) break;
+                const int sl = item % NS;
+                uint64_t *bar = &bars[L::kFull + sl];
+                if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
+                if (lane == 0) {
+                  if (kv == 0) pages_of[jall & 7] = have;
+                  if (have)
+                    mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * B * D * 2);
+                  else
+                    mbar_arrive(bar);
+                }
+                __syncwarp();
+                if (cur >= 0) {
+                  const int hf = lane / PAGES;
+                  tma_load_2d_hint(smem + L::kOffRing + sl * L::kTile + hf * kTHalf + (lane % PAGES) * B * 128,
+                                   kv ? &tmV : &tmK, hf * 64, (cur * a.Hkv + h) * B, bar, pol);
+                }
+              }
+              cur = nxt;
+            }
+            if (ok && q_due) ok = queries(true);
+            if (!q_due) ++qn;
+          }
+        }
+        pos += nt;
+        off += nt;
+        if (off == (long long)tiles * a.Hkv) {
+          off = 0;
+          ++s;
+        }
+      }
+      if (ok && !(u >= kTPosts && !wait_warp(L::kUEmpty + u % kTPosts, (uint32_t)((u / kTPosts - 1) & 1))) && lane == 0) {
+        posts[u % kTPosts * kTPostWords + PP_KIND] = kPieceStop;
+        mbar_arrive(&bars[L::kUFull + u % kTPosts]);
+      }
+      if (lane == 0 && a.ws_next && !goes_on) a.ws_next[blockIdx.x] = make_int4(0, 0, 0, -1);
+      // what is still in flight lands before the CTA leaves
+      for (int i = max(0, item - NS); i < item; ++i) mbar_wait(&bars[L::kFull + i % NS], (uint32_t)((i / NS) & 1));
+      for (int i = max(0, qn - L::kSets); i < qn; ++i)
+        mbar_wait(&bars[L::kQFull + i % L::kSets], (uint32_t)((i / L::kSets) & 1));
+    } else if (warp == kIssuer && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      int u = 0, qn = 0, item = 0, n0 = 0, n1 = 0;  // n0, n1: key tiles of the row tiles
+      bool ok = true;
+      while (ok) {
+        const int pb = u % kTPosts;
+        if (!wait(L::kUFull + pb, (uint32_t)((u / kTPosts) & 1))) break;
+        const int *p = posts + pb * kTPostWords;
+        const int kind = p[PP_KIND], nt = p[PP_TILES], live = p[PP_LIVE];
+        if (kind == kPieceStop) break;
+        ++u;
+        if (kind == kPieceZero) {
+          mbar_arrive(&bars[L::kUEmpty + pb]);
+          continue;
+        }
+        const int set = qn % L::kSets;
+        if (!wait(L::kQFull + set, (uint32_t)((qn / L::kSets) & 1))) break;
+        ++qn;
+        const uint32_t sq = smem_u32(smem + set * NT * L::kTile), ring = smem_u32(smem + L::kOffRing);
+        // S of row tile x against the K tile of key tile j into S columns `buf`
+        auto issue_s = [&](int x, int j, int buf) {
+          const uint32_t kb = ring + (item + 2 * j) % NS * L::kTile, qb = sq + x * L::kTile;
 #pragma unroll
-  for (int g = 0; g < 16; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * kTHalf + (kk & 3) * 32;
+            umma_bf16(tmem + buf * 128, umma_desc_sw128(qb + o, 16, 1024), umma_desc_sw128(kb + o, 16, 1024), kIdS,
+                      kk > 0);
+          }
+          umma_commit(&bars[L::kSFull + buf]);
+          mbar_arrive(&bars[L::kSFull + buf]);  // (what the producer wrote with the tile is seen behind it)
+        };
+        auto issue_pv = [&](int x, int j, int buf) {  // O_x += P V
+          const uint32_t vb = ring + (item + 2 * j + 1) % NS * L::kTile;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[g][e] = 0.f;
-      q[g][e] = g < a.G ? __bfloat162float(
-                              a.q[((size_t)(r.first + i) * a.Hq + (size_t)h * a.G + g) * D + lane * E + e])
-                        : 0.f;
+          for (int f = 0; f < (FINE ? 2 : 1); ++f)
+#pragma unroll
+            for (int kk = 0; kk < kTN / 16; ++kk)
+              umma_bf16_ts(tmem + kColO + x * 128, tmem + buf * 128 + f * 64 + kk * 8,
+                           umma_desc_sw128(vb + kk * 2048, kTHalf, 1024), kIdPV, 1u);
+          umma_commit(&bars[L::kPV + (NT == 1 ? buf : x)]);
+        };
+        auto full = [&](int i) { return wait(L::kFull + i % NS, (uint32_t)((i / NS) & 1)); };
+        if constexpr (NT == 1) {
+          ok = full(item);
+          if (ok) {
+            tc_fence_after();
+            issue_s(0, 0, n0 & 1);
+            umma_commit(&bars[L::kEmpty + item % NS]);
+          }
+          for (int j = 0; ok && j < nt; ++j, ++n0) {
+            if (j + 1 < nt) {
+              if (!(ok = full(item + 2 * j + 2))) break;
+              tc_fence_after();
+              issue_s(0, j + 1, (n0 + 1) & 1);
+              umma_commit(&bars[L::kEmpty + (item + 2 * j + 2) % NS]);
+            }
+            if (!(ok = full(item + 2 * j + 1) && wait(L::kPFull + (n0 & 1), (uint32_t)((n0 >> 1) & 1)))) break;
+            tc_fence_after();
+            issue_pv(0, j, n0 & 1);
+            umma_commit(&bars[L::kEmpty + (item + 2 * j + 1) % NS]);
+          }
+        } else {
+          ok = full(item);
+          if (ok) {
+            tc_fence_after();
+            issue_s(0, 0, 0);
+            if (live > 1) issue_s(1, 0, 1);
+            umma_commit(&bars[L::kEmpty + item % NS]);
+          }
+          for (int j = 0; ok && j < nt; ++j) {
+            const bool more = j + 1 < nt;
+            if (!(ok = full(item + 2 * j + 1) && wait(L::kPFull, (uint32_t)(n0++ & 1)))) break;
+            tc_fence_after();
+            issue_pv(0, j, 0);
+            if (more) {
+              if (!(ok = full(item + 2 * j + 2))) break;
+              tc_fence_after();
+              issue_s(0, j + 1, 0);
+            }
+            if (live > 1) {
+              if (!(ok = wait(L::kPFull + 1, (uint32_t)(n1++ & 1)))) break;
+              tc_fence_after();
+              issue_pv(1, j, 1);
+            }
+            umma_commit(&bars[L::kEmpty + (item + 2 * j + 1) % NS]);
+            if (more) {
+              if (live > 1) issue_s(1, j + 1, 1);
+              umma_commit(&bars[L::kEmpty + (item + 2 * j + 2) % NS]);
+            }
+          }
+        }
+        item += 2 * nt;
+        mbar_arrive(&bars[L::kUEmpty + pb]);
+      }
+      umma_commit(&bars[L::kDone]);
+      mbar_wait(&bars[L::kDone], 0);  // every MMA complete before TMEM is freed
+    }
+  } else {
+    // ----------------------------------- softmax: row tile x, row m = TMEM lane
+    if constexpr (NT == 2) setmaxnreg_inc<kTRegsSoftmax>();
+    const int x = warp >> 2, m = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16), o_col = kColO + x * 128;
+    const int nl = m / a.G;  // node within the row tile
+    const bool positive = a.scale_log2 > 0.f;
+    const float sc = positive ? a.scale_log2 : 1.f;
+    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads = 0;
+    bool ok = true;
+    // P V of this row tile's key tile n.  (With one row tile the one before it may
+    // not be complete either, so each S buffer has a barrier.)
+    auto wait_pv = [&](int n) -> bool {
+      return NT == 1 ? wait_warp(L::kPV + (n & 1), (uint32_t)((n >> 1) & 1)) : wait_warp(L::kPV + x, (uint32_t)(n & 1));
+    };
+    while (ok) {
+      const int pb = u % kTPosts;
+      if (!wait_warp(L::kUFull + pb, (uint32_t)((u / kTPosts) & 1))) break;
+      const int *p = posts + pb * kTPostWords;
+      const int kind = p[PP_KIND];
+      if (kind == kPieceStop) break;
+      const int row0 = p[PP_ROW0], T = p[PP_NODES], c = p[PP_CTX], h = p[PP_HEAD], t0 = p[PP_TILE], nt = p[PP_TILES];
+      const int slot = p[PP_SLOT], live = p[PP_LIVE], first = p[PP_FIRST], base = p[PP_BASE];
+      ++u;
+      if (kind == kPieceZero) {
+        for (int i = tid; i < T * a.G * (D / 8); i += 128 * NT) {
+          const int node = i / (a.G * (D / 8)), rest = i - node * (a.G * (D / 8));
+          reinterpret_cast<uint4 *>(a.out + ((size_t)(first + node) * a.Hq + (size_t)h * a.G) * D)[rest] =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        mbar_arrive(&bars[L::kUEmpty + pb]);
+        continue;
+      }
+      const int set = qn % L::kSets, tree0 = c / kTN;  // first key tile with a node
+      ++qn;
+      if (x >= live) {  // no rows of this tile
+        jall += nt;
+        votes += max(0, t0 + nt - max(t0, tree0));
+        mbar_arrive(&bars[L::kUEmpty + pb]);
+        continue;
+      }
+      const int node = base + x * a.nodes_tile + nl;
+      const bool valid = nl < a.nodes_tile && node < T;
+      const bool some = __any_sync(0xffffffffu, valid);  // rows of this warp
+      bool refused = false;
+      if (valid)
+        for (int at = node; at >= 0;) {
+          const int up = __ldg(a.parents + first + at);
+          if (!good_parent(at, up)) {
+            refused = true;
+            break;
+          }
+          at = up;
+        }
+      if (refused && a.err) atomicOr(a.err, PA_DEVERR_TREE);
+      if (some) {
+        uint32_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) tmem_st32(lane_base + o_col + i * 32, z);
+      }
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < nt; ++j, ++jall, ++jx) {
+        const int t = t0 + j, key0 = t * kTN, buf = NT == 1 ? jx & 1 : x;
+        const bool tree = t >= tree0;
+        uint32_t allow[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) allow[w] = bits_below(c - key0, w);
+        if (tree && valid && !refused)
+          for (int at = node; at >= 0 && c + at >= key0; at = __ldg(a.parents + first + at)) {
+            const int k = c + at - key0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (k >> 5 == w) allow[w] |= 1u << (k & 31);
+          }
+        if (!wait_warp(L::kSFull + buf, (uint32_t)((NT == 1 ? jx >> 1 : jx) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t pages = pages_of[jall & 7], s_col = buf * 128;
+        const bool masked = tree || pages != kAllPages;
+        const int v_item = 2 * jall + 1;
+        uint8_t *vt = smem + L::kOffRing + v_item % NS * L::kTile;
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < PAGES; ++i)
+            if (!((pages >> i) & 1u)) {
+              const uint32_t run = B == 32 ? 0xffffffffu : 0xffffu << (i * B % 32);
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if (i * B / 32 == w) allow[w] &= ~run;
+            }
+          if (x == 0) {  // value rows that no row attends, and nodes whose values are not finite
+            if (!wait_warp(L::kFull + v_item % NS, (uint32_t)((v_item / NS) & 1))) {
+              ok = false;
+              break;
+            }
+            uint4 *row = reinterpret_cast<uint4 *>(vt + m * 128);
+            const bool none = key0 + m >= c + T || !((pages >> (m / B)) & 1u);
+            if (none) {
+#pragma unroll
+              for (int i = 0; i < kHalves * 8; ++i) row[(i >> 3) * (kTHalf / 16) + ((i ^ lane) & 7)] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            } else if (tree && key0 + m >= c) {
+              uint32_t odd = 0;
+#pragma unroll
+              for (int i = 0; i < kHalves * 8; ++i) {
+                const uint4 v = row[(i >> 3) * (kTHalf / 16) + ((i ^ lane) & 7)];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  odd |= (uint32_t)((w[e] & 0x7f80u) == 0x7f80u) | (uint32_t)((w[e] & 0x7f800000u) == 0x7f800000u);
+              }
+              if (odd) atomicOr(&bad_of[(votes & 3) * 4 + (m >> 5)], 1u << (m & 31));
+            }
+            if (tree) {
+              if (m < 4) bad_of[((votes + 2) & 3) * 4 + m] = 0;  // (two votes ago: everyone has read it)
+              mbar_arrive(&bars[L::kVote + (votes & 1)]);  // (the second tile's threads may be one vote behind)
+            }
+          }
+        }
+        if (some) {
+          float s[kTN];
+          {
+            uint32_t v[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(lane_base + s_col + i * 32, v[i]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[i * 32 + e] = __uint_as_float(v[i][e]);
+          }
+          if (!positive) {
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) s[i] *= a.scale_log2;
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) s[i] = (allow[i >> 5] >> (i & 31)) & 1u ? s[i] : -INFINITY;
+          }
+          float mx;
+          {
+            float pm[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pm[i] = s[i];
+#pragma unroll
+            for (int i = 8; i < kTN; i += 2) pm[(i >> 1) & 7] = max3f(pm[(i >> 1) & 7], s[i], s[i + 1]);
+            mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+          }
+          const float m_new = fmaxf(m_run, mx * sc);
+          const bool grow = valid && m_new > m_run + 8.f;
+          const float m_use = grow ? m_new : m_run;
+          const float alpha = grow ? exp2f(m_run - m_new) : 1.f;
+          const float lsum = tree_probabilities<FINE>(s, sc, m_use == -INFINITY ? 0.f : m_use, lane_base + s_col);
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            if (NT == 1 && !wait_pv(jx - 1)) {  // (two tiles: S came behind that product)
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t v[32];
+              tmem_ld32(lane_base + o_col + i * 32, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st32(lane_base + o_col + i * 32, v);
+            }
+          }
+          tmem_wait_st();
+          l_run = l_run * alpha + lsum;
+          m_run = m_use;
+        }
+        if (tree) {
+          if (!wait_warp(L::kVote + (votes & 1), (uint32_t)((votes >> 1) & 1))) {
+            ok = false;
+            break;
+          }
+          const volatile uint32_t *bad = bad_of + (votes & 3) * 4;
+          ++votes;
+          if (bad[0] | bad[1] | bad[2] | bad[3]) {
+            // a node's values that are not finite: p v added to the rows that attend them, then a cleared row
+            if (j > 0 && !wait_pv(jx - 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              for (uint32_t left = some ? bad[w] : 0u; left; left &= left - 1) {
+                const int k = w * 32 + __ffs(left) - 1;
+                const uint32_t hi = tmem_ld1(lane_base + s_col + (k >> 1));
+                const uint32_t lo = FINE ? tmem_ld1(lane_base + s_col + 64 + (k >> 1)) : 0u;
+                tmem_wait_ld();
+                const float pk = k & 1 ? bf16_hi(hi) + bf16_hi(lo) : bf16_lo(hi) + bf16_lo(lo);
+                const bool attends = (allow[w] >> (k & 31)) & 1u;
+#pragma unroll 1
+                for (int i = 0; i < D / 32; ++i) {
+                  uint32_t v[32];
+                  tmem_ld32(lane_base + o_col + i * 32, v);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 32; e += 2) {
+                    const int ch = (i & 1) * 4 + e / 8;  // 16-byte chunk of the half
+                    const uint32_t y = *reinterpret_cast<const uint32_t *>(vt + (i >> 1) * kTHalf + sw128(k, ch) + (e & 7) * 2);
+                    if (attends) {
+                      v[e] = __float_as_uint(__uint_as_float(v[e]) + pk * bf16_lo(y));
+                      v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + pk * bf16_hi(y));
+                    }
+                  }
+                  tmem_st32(lane_base + o_col + i * 32, v);
+                }
+                tmem_wait_st();
+              }
+            mbar_arrive_n(&bars[L::kRead], NT == 2 && live == 1 ? 2u : 1u);
+            if (x == 0) {
+              const uint32_t par = (uint32_t)(reads++ & 1);
+              if (!wait_warp(L::kRead, par)) {
+                ok = false;
+                break;
+              }
+              if ((bad[m >> 5] >> (m & 31)) & 1u) {
+                uint4 *row = reinterpret_cast<uint4 *>(vt + m * 128);
+#pragma unroll
+                for (int i = 0; i < kHalves * 8; ++i) row[(i >> 3) * (kTHalf / 16) + (i & 7)] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&bars[L::kPFull + buf]);  // (a warp may be at the next key tile while another is here)
+      }
+      if (!ok || !wait_pv(jx - 1)) break;
+      tc_fence_after();
+
+      // ---- the piece's end
+      if (some) {
+        const bool full = l_run != 0.f && !refused;  // (a NaN sum is no empty one)
+        if (slot < 0) {
+          const float inv = full ? 1.f / l_run : 0.f;
+          constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
+          uint8_t *stage = smem + (set * NT + x) * L::kTile + (warp & 3) * 32 * RB;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t v[32];
+            tmem_ld32(lane_base + o_col + i * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if (full) {
+                y.x = pack_bf16(__uint_as_float(v[8 * k]) * inv, __uint_as_float(v[8 * k + 1]) * inv);
+                y.y = pack_bf16(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv);
+                y.z = pack_bf16(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
+                y.w = pack_bf16(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
+              }
+              *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 4 + k) ^ lane) & (CH - 1)) * 16) = y;
+            }
+          }
+          __syncwarp();
+#pragma unroll 4
+          for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
+            const int r = r0 + lane / CH, ch = lane % CH;
+            const int mr = (warp & 3) * 32 + r, n = mr / a.G;
+            if (n >= a.nodes_tile || base + x * a.nodes_tile + n >= T) continue;
+            const size_t row = (size_t)(row0 + x * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (mr - n * a.G);
+            reinterpret_cast<uint4 *>(a.out + row * D)[ch] =
+                *reinterpret_cast<const uint4 *>(stage + r * RB + ((ch ^ r) & (CH - 1)) * 16);
+          }
+          fence_proxy_async_smem();  // the next queries come by TMA
+        } else {
+          const size_t at = (size_t)blockIdx.x * 2 + slot;
+          const int r = x * 128 + m;
+          float4 *o = a.ws_o + at * (D / 4) * a.prow + r;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t v[32];
+            tmem_ld32(lane_base + o_col + i * 32, v);
+            tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                o[(size_t)(i * 8 + k) * a.prow] =
+                    make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
+                                __uint_as_float(v[4 * k + 3]));
+            }
+          }
+          if (valid) a.ws_ml[at * a.prow + r] = make_float2(m_run, full ? l_run : 0.f);
+        }
+        tc_fence_before();
+      }
+      mbar_arrive_n(&bars[L::kQEmpty + set], NT == 2 && live == 1 ? 2u : 1u);  // (for the other tile's threads too)
+      mbar_arrive(&bars[L::kUEmpty + pb]);
     }
   }
-  for (int j = warp; j < keys; j += kTrWarps) {
-    const int pos = j < c ? j : c + chain[j - c];
-    const int pg = __ldg(a.bt + (size_t)s * a.max_blocks + pos / a.B);
-    if (pg < 0 || pg >= a.num_blocks) {
-      if (lane == 0 && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
-      continue;
-    }
-    const size_t at = (((size_t)pg * a.Hkv + h) * a.B + pos % a.B) * D + lane * E;
-    float k[E], v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      k[e] = __bfloat162float(a.k[at + e]);
-      v[e] = __bfloat162float(a.v[at + e]);
-    }
-#pragma unroll
-    for (int g = 0; g < 16; ++g) {
-      if (g >= a.G) break;
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x += q[g][e] * k[e];
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-      x *= a.scale_log2;
-      const float mn = fmaxf(m[g], x), base = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m[g] - base), p = exp2f(x - base);
-      m[g] = mn;
-      l[g] = l[g] * f + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[g][e] = o[g][e] * f + (p == 0.f ? 0.f : p * v[e]);
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < 16; ++g) {
-    if (g >= a.G) break;
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][g][lane * E + e] = o[g][e];
-    if (lane == 0) sm[warp][g] = m[g], sl[warp][g] = l[g];
-  }
+  tc_fence_before();
   __syncthreads();
-  for (int idx = tid; idx < a.G * D; idx += kTrWarps * 32) {
-    const int g = idx / D, d = idx % D;
-    float mx = -INFINITY, den = 0.f, acc = 0.f;
-    for (int w = 0; w < kTrWarps; ++w) mx = fmaxf(mx, sm[w][g]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    for (int w = 0; w < kTrWarps; ++w) {
-      const float f = exp2f(sm[w][g] - base);
-      den += sl[w][g] * f;
-      acc += so[w][g][d] * f;
+  if (warp == kIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of units that several shares hold.  grid (32 rows, share and
+// row tile): the CTA of the share that a unit begins in; a lane a row, a warp 16
+// of its values.
+template <int D>
+__global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
+  grid_wait();
+  const int4 next = a.ws_next[blockIdx.y];
+  if (next.w < 0) return;
+  const int share = blockIdx.y / a.tiles_x, tx = blockIdx.y % a.tiles_x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x * 32 + lane;
+  const int x = r / 128, m = r % 128, n = m / a.G;
+  if (n >= a.nodes_tile || x * a.nodes_tile + n >= next.z) return;
+  const int pieces = next.w - share + 1;
+  // piece i: share + i's, where the unit began (0) or went on
+  auto at = [&](int i) { return ((size_t)(share + i) * a.tiles_x + tx) * 2 + (i == 0); };
+  float M = -INFINITY, den = 0.f;
+  for (int i = 0; i < pieces; ++i) {
+    const float2 ml = a.ws_ml[at(i) * a.prow + r];
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+  if (M == -INFINITY) M = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < pieces; ++i) {
+    const float2 ml = a.ws_ml[at(i) * a.prow + r];
+    const float4 *o = a.ws_o + (at(i) * (D / 4) + warp * 4) * a.prow + r;
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = o[(size_t)k * a.prow];
+    if (ml.y == 0.f) continue;
+    const float w = exp2f(ml.x - M);
+    den += w * ml.y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[k].x += w * v[k].x, acc[k].y += w * v[k].y;
+      acc[k].z += w * v[k].z, acc[k].w += w * v[k].w;
     }
-    a.out[((size_t)(r.first + i) * a.Hq + (size_t)h * a.G) * D + idx] =
-        __float2bfloat16(den != 0.f ? acc / den : 0.f);
+  }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  const size_t row = (size_t)(next.x + x * a.nodes_tile + n) * a.Hq + (size_t)next.y * a.G + (m - n * a.G);
+  uint4 *out = reinterpret_cast<uint4 *>(a.out + row * D + warp * 16);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (den != 0.f) {
+      const float4 p = acc[2 * k], q = acc[2 * k + 1];
+      y = make_uint4(pack_bf16(p.x * inv, p.y * inv), pack_bf16(p.z * inv, p.w * inv), pack_bf16(q.x * inv, q.y * inv),
+                     pack_bf16(q.z * inv, q.w * inv));
+    }
+    out[k] = y;
   }
 }
 
@@ -147,13 +868,60 @@ int validate_tree(const pa_decode_desc *d, int max_nodes) {
   return max_nodes > PA_MAX_TREE_NODES ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
+// How a call is laid out; the workspace is for pieces, so none where a unit is one tile.
+struct TreePlan {
+  int nodes_tile, row_tiles, tiles_x, shares, prow;
+  bool split;
+  size_t o_bytes, ml_bytes, next_bytes;
+  size_t total() const { return o_bytes + ml_bytes + next_bytes; }
+};
+
+TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
+  TreePlan p{};
+  const int G = d->num_q_heads / d->num_kv_heads;
+  p.nodes_tile = kTM / G;
+  p.row_tiles = max_nodes <= p.nodes_tile ? 1 : 2;
+  p.tiles_x = (max_nodes + p.row_tiles * p.nodes_tile - 1) / (p.row_tiles * p.nodes_tile);
+  const long long tiles = std::max<long long>(1, ((long long)d->max_context_len + kTN - 1) / kTN);
+  const long long units = std::max<long long>(1, (long long)d->num_seqs * d->num_kv_heads);
+  p.shares = (int)std::max<long long>(1, std::min<long long>(sms / p.tiles_x, units * tiles));
+  p.split = tiles > 1;
+  p.prow = p.row_tiles == 2 ? 2 * kTM : (std::min(kTM, max_nodes * G) + 31) / 32 * 32;
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  if (p.split) {
+    const size_t n = (size_t)p.shares * p.tiles_x;
+    p.o_bytes = up(n * 2 * p.prow * d->head_dim * sizeof(float));
+    p.ml_bytes = up(n * 2 * p.prow * sizeof(float2));
+    p.next_bytes = up(n * sizeof(int4));
+  }
+  return p;
+}
+
+template <int D, int B, int NT>
+int launch_tree(const TreePlan &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                const TreeArgs &a, cudaStream_t st) {
+  using L = TreeSmem<D, NT>;
+  auto kern = tree_kernel<D, B, NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (NT == 2) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PA_ERR_CUDA;
+    if (fa.numRegs < kTRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
+  }
+  int r = launch_dependent(kern, dim3(p.shares * p.tiles_x), L::kThreads, L::kAlloc, 1, st, tq, tk, tv, a);
+  if (r == PA_OK && p.split)
+    r = launch_dependent(tree_join_kernel<D>, dim3(p.prow / 32, p.shares * p.tiles_x), D * 2, 0, 1, st, a);
+  return r;
+}
+
 }  // namespace
 }  // namespace pa
 
 extern "C" size_t pa_decode_tree_workspace_bytes(const pa_decode_desc *d, int max_tree_nodes) {
   using namespace pa;
   if (validate_tree(d, max_tree_nodes) != PA_OK) return 0;
-  return 0;
+  return make_tree_plan(d, max_tree_nodes, current_sm_count()).total();
 }
 
 extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const void *q, const void *k_pool,
@@ -171,32 +939,52 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
     return PA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return PA_ERR_INVALID;
   if (d->num_seqs > 65535 || d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  const TreePlan p = make_tree_plan(d, max_tree_nodes, sms);
+  if (p.total() > 0 && (!workspace || workspace_bytes < p.total() || !aligned16(workspace))) return PA_ERR_WORKSPACE;
   TreeArgs a{};
-  a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.k = static_cast<const __nv_bfloat16 *>(k_pool);
-  a.v = static_cast<const __nv_bfloat16 *>(v_pool);
   a.bt = block_tables;
   a.ctx = context_lens;
   a.cu = cu_nodes;
   a.parents = parents;
   a.out = static_cast<__nv_bfloat16 *>(out);
+  if (p.split) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.ws_o = reinterpret_cast<float4 *>(ws);
+    a.ws_ml = reinterpret_cast<float2 *>(ws + p.o_bytes);
+    a.ws_next = reinterpret_cast<int4 *>(ws + p.o_bytes + p.ml_bytes);
+  }
   a.err = err_flag;
   a.S = d->num_seqs;
   a.Hq = d->num_q_heads;
   a.Hkv = d->num_kv_heads;
   a.G = d->num_q_heads / d->num_kv_heads;
-  a.B = d->block_size;
   a.num_blocks = d->num_blocks;
   a.max_blocks = d->max_blocks_per_seq;
   a.max_ctx = d->max_context_len;
   a.max_nodes = max_tree_nodes;
   a.total = total_nodes;
+  a.nodes_tile = p.nodes_tile;
+  a.box = std::min(p.nodes_tile, std::min(max_tree_nodes, total_nodes));
+  a.tiles_x = p.tiles_x;
+  a.shares = p.shares;
+  a.prow = p.prow;
   a.scale_log2 = d->scale * 1.4426950408889634f;
-  const dim3 grid(max_tree_nodes, d->num_kv_heads, d->num_seqs);
+  const uint64_t rows = (uint64_t)d->num_blocks * d->num_kv_heads * d->block_size;
+  CUtensorMap tq, tk, tv;
+  if (!encode_q_nodes(&tq, q, total_nodes, d->num_kv_heads, a.G, d->head_dim, a.box) ||
+      !encode_2d_bf16(&tk, k_pool, rows, d->head_dim, d->block_size, 64, true) ||
+      !encode_2d_bf16(&tv, v_pool, rows, d->head_dim, d->block_size, 64, true))
+    return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d->head_dim == 128)
-    tree_kernel<128><<<grid, kTrWarps * 32, 0, st>>>(a);
-  else
-    tree_kernel<64><<<grid, kTrWarps * 32, 0, st>>>(a);
-  return launch_status(cudaGetLastError());
+  // The join reads what the first kernel left in the workspace: no other such
+  // call may come between the two on the stream, whatever thread makes it.
+  static std::mutex both;
+  const std::lock_guard<std::mutex> lock(both);
+#define PA_TREE(D_, B_)                                                            \
+  (p.row_tiles == 1 ? launch_tree<D_, B_, 1>(p, tq, tk, tv, a, st) : launch_tree<D_, B_, 2>(p, tq, tk, tv, a, st))
+  if (d->head_dim == 128) return d->block_size == 16 ? PA_TREE(128, 16) : PA_TREE(128, 32);
+  return d->block_size == 16 ? PA_TREE(64, 16) : PA_TREE(64, 32);
+#undef PA_TREE
 }

@@ -23,6 +23,11 @@ bool encode_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t 
 // the other, each box_rows x 128 bytes, 128-byte swizzled -- the layout two
 // 64-column 2-D boxes give, in one copy.
 bool encode_kv_halves_3d(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
+// Query rows [nodes][kv heads][group][head_dim] as a 4-D map whose boxes of
+// box_nodes nodes of one kv head land as box_nodes * group rows of 64 columns
+// (128 bytes), 128-byte swizzled.
+bool encode_q_nodes(CUtensorMap *map, const void *q, uint64_t nodes, uint32_t kv_heads, uint32_t group,
+                    uint32_t head_dim, uint32_t box_nodes);
 // The map by which the decode unit gathers one (block, kv head) run of a
 // validated desc's K or V pool (its TMA3 form for head_dim 128).
 bool encode_kv_pages(const pa_decode_desc *d, const void *pool, CUtensorMap *map);
