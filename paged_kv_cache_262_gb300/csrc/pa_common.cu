@@ -109,6 +109,21 @@ bool encode_q_nodes(CUtensorMap *map, const void *q, uint64_t nodes, uint32_t kv
   });
 }
 
+bool encode_kv_groups(CUtensorMap *map, const void *base, uint64_t rows, uint32_t head_dim, uint32_t box_rows) {
+  EncodeTiledFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)head_dim * 2;
+  cuuint64_t dims[4] = {64, 8, head_dim / 64, rows / 8};
+  cuuint64_t strides[3] = {row, 128, 8 * row};
+  cuuint32_t box[4] = {64, 8, head_dim / 64, box_rows / 8};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encoded([&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
+}
+
 bool encode_kv_pages(const pa_decode_desc *d, const void *pool, CUtensorMap *map) {
   const uint64_t rows = (uint64_t)d->num_blocks * d->num_kv_heads * d->block_size;
   return d->head_dim == 128 ? encode_kv_halves_3d(map, pool, rows, d->block_size)

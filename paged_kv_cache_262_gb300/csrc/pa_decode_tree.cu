@@ -13,20 +13,23 @@
 // one unit after another, are cut into equal shares, one for each CTA (persistent,
 // one an SM), whatever the lengths.  A share's pieces of units that other shares
 // go on with leave partial softmax states, which a second kernel joins.  The rows
-// are the MMA's M side: a CTA holds one tile of 128 rows (floor(128 / G) nodes),
-// or two where the trees have more, and more rows than that are further CTAs that
-// read the same keys at the same time.  Roles:
-//   warps 0-3   (4-7 with two tiles) a row a thread (TMEM lane): softmax, P (bf16)
-//               back over S in TMEM, the piece's end
-//   next warp   takes the share's pieces, posts them to the others, loads their
-//               query rows and gathers K and V tiles (2-D TMA, 128-byte swizzle)
-//               into one ring, across pieces
-//   next warp   owns TMEM and issues the MMAs: S = Q K^T, O += P V
-// MMAs issued by one thread complete in order.  With one row tile S has two
-// buffers and S of the next key tile is issued before P V of this one, and the
-// probabilities are kept as a bf16 value and a bf16 remainder (2^-16 of them
-// left) in two products, which the tensor cores have the time for; with two tiles
-// these alternate, and the probabilities are rounded to bf16 once.  The running maximum moves
+// are the MMA's M side: a row tile is 128 rows (floor(128 / G) nodes).  Trees of
+// one row tile have the CTA's two softmax warpgroups take half of every key tile
+// each, with a running state of its own, joined at the piece's end (so that a
+// tile's V is let go early: with whole tiles in turn 64 x 5 nodes took 143 us);
+// trees of more have a row tile for each, and more than two row tiles are further
+// CTAs that read the same keys at the same time.  Roles:
+//   warps 0-3, 4-7  a row a thread (TMEM lane): softmax, P (bf16) back over S in
+//                   TMEM, the piece's end
+//   warp 8, 10  take the share's pieces and gather K (8) and V (10) tiles, a page
+//               a copy (4-D TMA, 128-byte swizzle), into one ring across pieces;
+//               8 posts the pieces to the other roles and loads their query rows
+//   warp 9      owns TMEM and issues the MMAs: S = Q K^T, O += P V (one row tile: S
+//               of the next key tile before P V of this one; two: theirs in turn)
+// MMAs issued by one thread complete in order.  Where the bytes bind, with one row
+// tile, the probabilities are kept as a bf16 value and a bf16 remainder (2^-16 of
+// them left) in two products, which the tensor cores have the time for; with two
+// tiles they are rounded to bf16 once.  The running maximum moves
 // only when it grows by more than 8 (2^8), so O is seldom rescaled.
 //
 // Only tiles at and behind the context's end, or with a page outside the pool, are
@@ -68,36 +71,40 @@ struct TreeArgs {
 
 constexpr int kTM = 128;                 // rows of a row tile
 constexpr int kTN = 128;                 // keys of a key tile
-constexpr int kTHalf = kTN * 128;        // 64 columns of a tile
+constexpr int kTHalf = kTM * 128;        // 64 columns of a row tile
 constexpr int kTPosts = 4;               // pieces posted ahead
 constexpr int kTPostWords = 16;
-constexpr int kTRegsLaunch = 168, kTRegsSoftmax = 216, kTRegsOther = 72;  // two row tiles (see pa_prefill_body.cuh)
-static_assert(256 * kTRegsSoftmax + 128 * kTRegsOther <= 384 * kTRegsLaunch, "register split");
+constexpr int kTThreads = 384;
+// as in pa_prefill_body.cuh: the softmax warpgroups take the third one's registers
+constexpr int kTRegsLaunch = 168, kTRegsSoftmax = 216, kTRegsOther = 72;
+static_assert(256 * kTRegsSoftmax + 128 * kTRegsOther <= kTThreads * kTRegsLaunch, "register split");
+constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10;  // warps
 
-template <int D, int NT>
+template <int D, bool ROWS2>
 struct TreeSmem {
   static constexpr int kTile = D / 64 * kTHalf;          // 128 rows
-  static constexpr int kSets = NT == 1 ? 2 : 1;          // of query rows
+  static constexpr int kSets = ROWS2 ? 1 : 2;            // of query rows
+  static constexpr int kSet = ROWS2 ? 2 * kTile : kTile;
   static constexpr int kSlots = D == 128 ? 5 : 10;       // K and V tiles in flight
-  static constexpr int kOffRing = kSets * NT * kTile;
+  static constexpr int kOffRing = kSets * kSet;
   static constexpr int kOffBar = kOffRing + kSlots * kTile;
   static constexpr int kFull = 0, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots, kPFull = kSFull + 2,
                        kPV = kPFull + 2, kQFull = kPV + 2, kQEmpty = kQFull + 2, kUFull = kQEmpty + 2,
-                       kUEmpty = kUFull + kTPosts, kVote = kUEmpty + kTPosts, kRead = kVote + 2, kDone = kRead + 1,
-                       kBars = kDone + 1;
+                       kUEmpty = kUFull + kTPosts, kVote = kUEmpty + kTPosts, kRead = kVote + 4, kXFull = kRead + 2,
+                       kXEmpty = kXFull + 1, kDone = kXEmpty + 1, kBars = kDone + 1;
   static constexpr int kOffPost = kOffBar + kBars * 8;
   static constexpr int kOffPages = kOffPost + kTPosts * kTPostWords * 4;  // [8] valid pages of the latest key tiles
-  static constexpr int kOffBad = kOffPages + 8 * 4;                       // [4][4] keys of a tree tile that are not finite
-  static constexpr int kOffScan = (kOffBad + 16 * 4 + 7) & ~7;            // [12] sums of the warps, total
-  static constexpr int kOffMisc = kOffScan + 14 * 8;                      // TMEM address, dead, first sequence, its tiles' offset
-  static constexpr int kBytes = kOffMisc + 32;
+  static constexpr int kOffBad = kOffPages + 8 * 4;                       // [2][4][2], ROWS2 [4][4]: keys of a tree tile that are not finite
+  static constexpr int kOffScan = (kOffBad + 16 * 4 + 7) & ~7;            // [12] sums of the warps
+  static constexpr int kOffX = kOffScan + 12 * 8;                         // [128] the second warpgroup's maximum and sum
+  static constexpr int kOffMisc = kOffX + 128 * 8;                        // TMEM address, dead, first sequence, its tiles' offset
+  static constexpr int kBytes = kOffMisc + 24;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  static constexpr int kThreads = NT == 1 ? 192 : 384;
 };
 
 // Words of a posted piece.
-enum { PP_KIND = 0, PP_ROW0, PP_NODES, PP_BASE, PP_CTX, PP_HEAD, PP_TILE, PP_TILES, PP_SLOT, PP_LIVE, PP_FIRST };
+enum { PP_KIND = 0, PP_ROW0, PP_NODES, PP_BASE, PP_CTX, PP_HEAD, PP_TILE, PP_TILES, PP_SLOT, PP_LIVE, PP_FIRST, PP_LAST };
 enum { kPieceStop = 0, kPieceZero = 1, kPiece = 2 };
 
 // A sequence's tree, its context and its key tiles for each kv head: none
@@ -124,43 +131,53 @@ __device__ __forceinline__ uint32_t bits_below(int n, int word) {
   return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
 }
 
-// P of one row: 2^(x - base) for its 128 scores x = s * sc, as bf16 pairs into
-// TMEM columns [col, col + 64) and, FINE, what that rounding leaves into
-// [col + 64, col + 128); their sum, unrounded.
-template <bool FINE>
-__device__ __forceinline__ float tree_probabilities(const float (&s)[kTN], float sc, float base, uint32_t col) {
+// P of one row: 2^(x - base) for KN scores x = s * sc, as bf16 pairs into TMEM
+// columns [col, col + KN / 2) and, FINE, what that rounding leaves into the KN / 2
+// behind; their sum, unrounded.
+template <bool FINE, int KN>
+__device__ __forceinline__ float tree_probabilities(const float (&s)[KN], float sc, float base, uint32_t col) {
   const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t hi[32], lo[32];
+  for (int c = 0; c < KN / 32; ++c) {
+    uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int k = c * 64 + 2 * e;
+    for (int e = 0; e < 16; ++e) {
+      const int k = c * 32 + 2 * e;
       const float2 t = fma2(make_float2(s[k], s[k + 1]), sc2, nb2);
       const float2 p = make_float2(ex2_ftz(t.x), ex2_ftz(t.y));
       hi[e] = pack_bf16(p.x, p.y);
       if constexpr (FINE) lo[e] = pack_bf16(p.x - bf16_lo(hi[e]), p.y - bf16_hi(hi[e]));
       acc[e & 3] = add2(acc[e & 3], p);
     }
-    tmem_st32(col + c * 32, hi);
-    if constexpr (FINE) tmem_st32(col + 64 + c * 32, lo);
+    tmem_st16(col + c * 16, hi);
+    if constexpr (FINE) tmem_st16(col + KN / 2 + c * 16, lo);
   }
   const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
   return x.x + x.y;
 }
 
-template <int D, int B, int NT>
-__global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
+// A piece: key tiles t0 .. t0 + nt - 1 of a unit.
+struct TreePiece {
+  int s, first, T, ctx, why, h, tiles, t0, nt;
+};
+
+// ROWS2: the softmax warpgroups have a row tile each, else half of each key tile.
+template <int D, int B, bool ROWS2>
+__global__ void __launch_bounds__(kTThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
-  using L = TreeSmem<D, NT>;
-  constexpr bool FINE = NT == 1;
-  constexpr int kHalves = D / 64, PAGES = kTN / B, NS = L::kSlots, kThreads = L::kThreads;
+  using L = TreeSmem<D, ROWS2>;
+  constexpr bool FINE = !ROWS2;
+  constexpr int kHalves = D / 64, PAGES = kTN / B, NS = L::kSlots;
+  constexpr int kGroup = kHalves * 1024;  // 8 keys of a K or V tile: 8 x 128 bytes of each half
   constexpr uint32_t kAllPages = (1u << PAGES) - 1u;
   constexpr uint32_t kIdS = umma_idesc_bf16(128, 128, false, false);
   constexpr uint32_t kIdPV = umma_idesc_bf16(128, D, false, true);
-  constexpr uint32_t kColO = 256;  // S: columns 0 and 128 (two buffers, or two row tiles); O: 256 and 256 + 128
+  constexpr int KN = ROWS2 ? kTN : kTN / 2;  // keys of a tile for a warpgroup
+  // S: columns 0 and 128 (of the two row tiles, or two key tiles in turn); O of the
+  // warpgroups: 256 and 256 + 128
+  constexpr uint32_t kColO = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
@@ -168,12 +185,12 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
   volatile uint32_t *pages_of = reinterpret_cast<uint32_t *>(smem + L::kOffPages);
   uint32_t *bad_of = reinterpret_cast<uint32_t *>(smem + L::kOffBad);
   long long *scan = reinterpret_cast<long long *>(smem + L::kOffScan);
+  float2 *xml = reinterpret_cast<float2 *>(smem + L::kOffX);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 4);
   int *start_s = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
   long long *start_off = reinterpret_cast<long long *>(smem + L::kOffMisc + 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = 4 * NT, kIssuer = kProducer + 1;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -182,24 +199,27 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[L::kSFull + i], 2);
-      mbar_init(&bars[L::kPFull + i], 128);
+      mbar_init(&bars[L::kPFull + i], ROWS2 ? 128 : 256);
       mbar_init(&bars[L::kPV + i], 1);
       mbar_init(&bars[L::kQFull + i], 1);
-      mbar_init(&bars[L::kQEmpty + i], 128 * NT);
+      mbar_init(&bars[L::kQEmpty + i], ROWS2 ? 256 : 128);
       mbar_init(&bars[L::kVote + i], 128);
+      mbar_init(&bars[L::kVote + 2 + i], 128);
+      mbar_init(&bars[L::kRead + i], ROWS2 ? 256 : 128);
     }
     for (int i = 0; i < kTPosts; ++i) {
       mbar_init(&bars[L::kUFull + i], 1);
-      mbar_init(&bars[L::kUEmpty + i], 128 * NT + 1);
+      mbar_init(&bars[L::kUEmpty + i], 256 + 1);
     }
-    mbar_init(&bars[L::kRead], 128 * NT);
+    mbar_init(&bars[L::kXFull], 128);
+    mbar_init(&bars[L::kXEmpty], 128);
     mbar_init(&bars[L::kDone], 1);
     for (int i = 0; i < 16; ++i) bad_of[i] = 0;
     *dead = 0;
     *start_s = a.S;
     fence_mbar_init();
   }
-  if (warp == kIssuer) {
+  if (warp == kTIssuer) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -208,7 +228,7 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
 
   // ---- this CTA's share of all units' key tiles
   long long mine = 0;
-  const int per = (a.S + kThreads - 1) / kThreads;
+  const int per = (a.S + kTThreads - 1) / kTThreads;
   for (int s = tid * per; s < min(a.S, (tid + 1) * per); ++s) {
     const TreeSeq q = tree_seq(a, s, B);
     mine += (long long)q.tiles * a.Hkv;
@@ -226,7 +246,7 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
   tc_fence_after();
   long long total = 0, before = incl - mine;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kTThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
@@ -261,149 +281,172 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
   // uniform over the warp (warp collectives follow)
   auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
-  if (warp >= kProducer) {
-    if constexpr (NT == 2) setmaxnreg_dec<kTRegsOther>();
-    if (warp == kProducer) {
-      // ------------------------------------------------------------ producer
+  if (warp >= 8) {
+    setmaxnreg_dec<kTRegsOther>();
+    if (warp == kTProducerK || warp == kTProducerV) {
+      // ----------------------------------------------------------- producers
       // (the rows of further CTAs read the same keys: they stay in L2 for them)
       const uint64_t pol = a.tiles_x > 1 ? policy_evict_normal() : policy_evict_first();
-      const int base = tx * NT * a.nodes_tile;  // first node of this CTA's rows
-      long long pos = beg;
+      const int kv = warp == kTProducerV;  // K tiles are the ring's even items, V tiles the odd ones
+      const CUtensorMap *map = kv ? &tmV : &tmK;
+      const int base = ROWS2 ? tx * 2 * a.nodes_tile : 0;  // first node of this CTA's rows
+      long long pos = beg, off = beg < end ? *start_off : 0;
       int s = *start_s, window = -1;
       TreeSeq near{};  // of sequence window + lane
-      long long off = beg < end ? *start_off : 0;
-      int u = 0, qn = 0, item = 0, jall = 0;
+      // the share's next piece of a unit that has rows for this CTA (nt == 0: no more)
+      auto next_piece = [&]() {
+        TreePiece p{};
+        while (pos < end) {
+          if (s >> 5 != window) {
+            window = s >> 5;
+            near = TreeSeq{};
+            if (window * 32 + lane < a.S) near = tree_seq(a, window * 32 + lane, B);
+          }
+          const int tiles = __shfl_sync(0xffffffffu, near.tiles, s & 31);
+          if (tiles == 0) {
+            ++s;
+            continue;
+          }
+          p.s = s;
+          p.first = __shfl_sync(0xffffffffu, near.first, s & 31);
+          p.T = __shfl_sync(0xffffffffu, near.count, s & 31);
+          p.ctx = __shfl_sync(0xffffffffu, near.ctx, s & 31);
+          p.why = __shfl_sync(0xffffffffu, near.why, s & 31);
+          p.tiles = tiles;
+          p.h = (int)(off / tiles);
+          p.t0 = (int)(off - (long long)p.h * tiles);
+          const int nt = (int)min((long long)(tiles - p.t0), end - pos);
+          pos += nt;
+          off += nt;
+          if (off == (long long)tiles * a.Hkv) {
+            off = 0;
+            ++s;
+          }
+          if (p.why ? tx == 0 : p.T > base) {
+            p.nt = nt;
+            return p;
+          }
+        }
+        p.nt = 0;
+        return p;
+      };
+      auto page_id = [&](const TreePiece &p, int t) {  // this lane's page of key tile t (-1: none)
+        const int i = t * PAGES + lane;
+        int pg = -1;
+        if (lane < PAGES && i < (p.ctx + p.T + B - 1) / B) {
+          pg = __ldg(a.bt + (size_t)p.s * a.max_blocks + i);
+          if (pg < 0 || pg >= a.num_blocks) {
+            if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+            pg = -1;
+          }
+        }
+        return pg;
+      };
+      int u = 0, qn = 0, jall = 0;
       bool ok = true, goes_on = false;
-      while (ok && pos < end) {
-        if (s >> 5 != window) {
-          window = s >> 5;
-          near = TreeSeq{};
-          if (window * 32 + lane < a.S) near = tree_seq(a, window * 32 + lane, B);
-        }
-        const int tiles = __shfl_sync(0xffffffffu, near.tiles, s & 31);
-        if (tiles == 0) {
-          ++s;
-          continue;
-        }
-        const int first = __shfl_sync(0xffffffffu, near.first, s & 31), T = __shfl_sync(0xffffffffu, near.count, s & 31);
-        const int c = __shfl_sync(0xffffffffu, near.ctx, s & 31), why = __shfl_sync(0xffffffffu, near.why, s & 31);
-        const int h = (int)(off / tiles), t0 = (int)(off - (long long)h * tiles);
-        const int nt = (int)min((long long)(tiles - t0), end - pos);
-        const int left = T - base;  // nodes from this CTA's first on
-        if (why ? tx == 0 : left > 0) {
-          const int live = NT == 1 || left <= a.nodes_tile ? 1 : 2;
-          const int slot = t0 > 0 ? 0 : nt < tiles ? 1 : -1;
-          const int pb = u % kTPosts;
-          if (u >= kTPosts && !wait_warp(L::kUEmpty + pb, (uint32_t)((u / kTPosts - 1) & 1))) break;
+      TreePiece p = next_piece();
+      int cur = p.nt > 0 && !p.why ? page_id(p, p.t0) : -1;
+      while (p.nt > 0) {
+        const long long unit_end = pos - p.nt - p.t0 + p.tiles;  // (of the piece that next_piece gave last)
+        const TreePiece n = next_piece();
+        const int left = p.T - base, live = !ROWS2 || left <= a.nodes_tile ? 1 : 2;
+        if (!kv) {
+          const int slot = p.t0 > 0 ? 0 : p.nt < p.tiles ? 1 : -1, pb = u % kTPosts;
+          if (u >= kTPosts && !(ok = wait_warp(L::kUEmpty + pb, (uint32_t)((u / kTPosts - 1) & 1)))) break;
           if (lane == 0) {
-            int *p = posts + pb * kTPostWords;
-            p[PP_KIND] = why ? kPieceZero : kPiece;
-            p[PP_ROW0] = first + base;
-            p[PP_NODES] = T;
-            p[PP_BASE] = base;
-            p[PP_CTX] = c;
-            p[PP_HEAD] = h;
-            p[PP_TILE] = t0;
-            p[PP_TILES] = nt;
-            p[PP_SLOT] = slot;
-            p[PP_LIVE] = live;
-            p[PP_FIRST] = first;
+            int *w = posts + pb * kTPostWords;
+            w[PP_KIND] = p.why ? kPieceZero : kPiece;
+            w[PP_ROW0] = p.first + base;
+            w[PP_NODES] = p.T;
+            w[PP_BASE] = base;
+            w[PP_CTX] = p.ctx;
+            w[PP_HEAD] = p.h;
+            w[PP_TILE] = p.t0;
+            w[PP_TILES] = p.nt;
+            w[PP_SLOT] = slot;
+            w[PP_LIVE] = live;
+            w[PP_FIRST] = p.first;
+            w[PP_LAST] = p.t0 + p.nt == p.tiles;
             mbar_arrive(&bars[L::kUFull + pb]);
-            if (slot == 1) {  // the share that has the unit's last tile
-              const long long unit_end = pos + tiles;
-              a.ws_next[blockIdx.x] = make_int4(first + base, h, left, (int)((unit_end * shares - 1) / total));
-            }
+            // the share that has the unit's last tile
+            if (slot == 1)
+              a.ws_next[blockIdx.x] = make_int4(p.first + base, p.h, left, (int)((unit_end * shares - 1) / total));
           }
           goes_on |= slot == 1;
           ++u;
-          if (!why) {
-            const int set = qn % L::kSets, first_item = item;
-            bool q_due = true;
-            // the piece's query rows, as soon as the set is free; at the latest when a K or V
-            // tile would have to wait for this piece's own
-            auto queries = [&](bool now) -> bool {
-              if (qn >= L::kSets) {
-                const uint32_t par = (uint32_t)((qn / L::kSets - 1) & 1);
-                if (now) {
-                  if (!wait_warp(L::kQEmpty + set, par)) return false;
-                } else if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[L::kQEmpty + set], par))) {
-                  return true;
-                }
+        }
+        if (!p.why) {
+          const int set = qn % L::kSets, first = jall;
+          bool q_due = !kv;
+          // the piece's query rows, as soon as the set is free; at the latest when a K or V
+          // tile would have to wait for this piece's own
+          auto queries = [&](bool now) -> bool {
+            if (qn >= L::kSets) {
+              const uint32_t par = (uint32_t)((qn / L::kSets - 1) & 1);
+              if (now) {
+                if (!wait_warp(L::kQEmpty + set, par)) return false;
+              } else if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[L::kQEmpty + set], par))) {
+                return true;
               }
-              q_due = false;
-              if (lane == 0) {
-                uint64_t *bar = &bars[L::kQFull + set];
-                mbar_arrive_expect_tx(bar, (uint32_t)(live * kHalves * a.box * a.G * 128));
-                for (int x = 0; x < live; ++x)
-                  for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_4d(smem + (set * NT + x) * L::kTile + hf * kTHalf, &tmQ, hf * 64, 0, h,
-                                first + base + x * a.nodes_tile, bar);
-              }
-              __syncwarp();
-              return true;
-            };
-            const int npages = (c + T + B - 1) / B;
-            const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
-            auto page_id = [&](int t) {  // this lane's page of key tile t (-1: none)
-              const int i = t * PAGES + lane % PAGES;
-              int pg = -1;
-              if (lane < PAGES * kHalves && i < npages) {
-                pg = __ldg(bt + i);
-                if (pg < 0 || pg >= a.num_blocks) {
-                  if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
-                  pg = -1;
-                }
-              }
-              return pg;
-            };
-            int cur = page_id(t0);
-            for (int t = t0; ok && t < t0 + nt; ++t, ++jall) {
-              const int nxt = t + 1 < t0 + nt ? page_id(t + 1) : -1;  // on its way meanwhile
-              const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0) & kAllPages;
-              for (int kv = 0; kv < 2; ++kv, ++item) {
-                if (q_due && !(ok = queries(item - NS >= first_item))) break;
-                const int sl = item % NS;
-                uint64_t *bar = &bars[L::kFull + sl];
-                if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
-                if (lane == 0) {
-                  if (kv == 0) pages_of[jall & 7] = have;
-                  if (have)
-                    mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * B * D * 2);
-                  else
-                    mbar_arrive(bar);
-                }
-                __syncwarp();
-                if (cur >= 0) {
-                  const int hf = lane / PAGES;
-                  tma_load_2d_hint(smem + L::kOffRing + sl * L::kTile + hf * kTHalf + (lane % PAGES) * B * 128,
-                                   kv ? &tmV : &tmK, hf * 64, (cur * a.Hkv + h) * B, bar, pol);
-                }
-              }
-              cur = nxt;
             }
-            if (ok && q_due) ok = queries(true);
-            if (!q_due) ++qn;
+            q_due = false;
+            if (lane == 0) {
+              uint64_t *bar = &bars[L::kQFull + set];
+              mbar_arrive_expect_tx(bar, (uint32_t)(live * kHalves * a.box * a.G * 128));
+              for (int x = 0; x < live; ++x)
+                for (int hf = 0; hf < kHalves; ++hf)
+                  tma_load_4d(smem + set * L::kSet + x * L::kTile + hf * kTHalf, &tmQ, hf * 64, 0, p.h,
+                              p.first + base + x * a.nodes_tile, bar);
+            }
+            __syncwarp();
+            return true;
+          };
+          for (int t = p.t0; ok && t < p.t0 + p.nt; ++t, ++jall) {
+            const int item = 2 * jall + kv, sl = item % NS;
+            // the next tile's page on its way meanwhile, or that of the next piece's first
+            const int nxt = t + 1 < p.t0 + p.nt ? page_id(p, t + 1) : n.nt > 0 && !n.why ? page_id(n, n.t0) : -1;
+            const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0);
+            if (q_due && !(ok = queries(item + 1 - NS >= 2 * first))) break;
+            uint64_t *bar = &bars[L::kFull + sl];
+            if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
+            if (lane == 0) {
+              if (!kv) pages_of[jall & 7] = have;
+              if (have)
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * B * D * 2);
+              else
+                mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (cur >= 0)
+              tma_load_4d_hint(smem + L::kOffRing + sl * L::kTile + lane * B * D * 2, map, 0, 0, 0,
+                               (cur * a.Hkv + p.h) * (B / 8), bar, pol);
+            cur = nxt;
           }
+          if (ok && q_due) ok = queries(true);
+          if (!q_due) ++qn;
+          if (!ok) break;
+        } else {
+          cur = n.nt > 0 && !n.why ? page_id(n, n.t0) : -1;
         }
-        pos += nt;
-        off += nt;
-        if (off == (long long)tiles * a.Hkv) {
-          off = 0;
-          ++s;
+        p = n;
+      }
+      if (!kv) {
+        if (ok && !(u >= kTPosts && !wait_warp(L::kUEmpty + u % kTPosts, (uint32_t)((u / kTPosts - 1) & 1))) && lane == 0) {
+          posts[u % kTPosts * kTPostWords + PP_KIND] = kPieceStop;
+          mbar_arrive(&bars[L::kUFull + u % kTPosts]);
         }
+        if (lane == 0 && a.ws_next && !goes_on) a.ws_next[blockIdx.x] = make_int4(0, 0, 0, -1);
+        for (int i = max(0, qn - L::kSets); i < qn; ++i)
+          mbar_wait(&bars[L::kQFull + i % L::kSets], (uint32_t)((i / L::kSets) & 1));
       }
-      if (ok && !(u >= kTPosts && !wait_warp(L::kUEmpty + u % kTPosts, (uint32_t)((u / kTPosts - 1) & 1))) && lane == 0) {
-        posts[u % kTPosts * kTPostWords + PP_KIND] = kPieceStop;
-        mbar_arrive(&bars[L::kUFull + u % kTPosts]);
-      }
-      if (lane == 0 && a.ws_next && !goes_on) a.ws_next[blockIdx.x] = make_int4(0, 0, 0, -1);
       // what is still in flight lands before the CTA leaves
-      for (int i = max(0, item - NS); i < item; ++i) mbar_wait(&bars[L::kFull + i % NS], (uint32_t)((i / NS) & 1));
-      for (int i = max(0, qn - L::kSets); i < qn; ++i)
-        mbar_wait(&bars[L::kQFull + i % L::kSets], (uint32_t)((i / L::kSets) & 1));
-    } else if (warp == kIssuer && lane == 0) {
+      for (int j = max(0, jall - (NS + 1) / 2); j < jall; ++j) {
+        const int item = 2 * j + kv;
+        if (item >= 2 * jall - NS) mbar_wait(&bars[L::kFull + item % NS], (uint32_t)((item / NS) & 1));
+      }
+    } else if (warp == kTIssuer && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
-      int u = 0, qn = 0, item = 0, n0 = 0, n1 = 0;  // n0, n1: key tiles of the row tiles
+      int u = 0, qn = 0, item = 0, n[2] = {0, 0};  // n: key tiles of the warpgroups
       bool ok = true;
       while (ok) {
         const int pb = u % kTPosts;
@@ -419,77 +462,81 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
         const int set = qn % L::kSets;
         if (!wait(L::kQFull + set, (uint32_t)((qn / L::kSets) & 1))) break;
         ++qn;
-        const uint32_t sq = smem_u32(smem + set * NT * L::kTile), ring = smem_u32(smem + L::kOffRing);
-        // S of row tile x against the K tile of key tile j into S columns `buf`
-        auto issue_s = [&](int x, int j, int buf) {
-          const uint32_t kb = ring + (item + 2 * j) % NS * L::kTile, qb = sq + x * L::kTile;
+        const uint32_t sq = smem_u32(smem + set * L::kSet), ring = smem_u32(smem + L::kOffRing);
+        // S of the rows at sq + q against the K tile of key tile j, into S columns `buf`
+        auto issue_s = [&](int q, int j, int buf) {
+          const uint32_t kb = ring + (item + 2 * j) % NS * L::kTile, qb = sq + q;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * kTHalf + (kk & 3) * 32;
-            umma_bf16(tmem + buf * 128, umma_desc_sw128(qb + o, 16, 1024), umma_desc_sw128(kb + o, 16, 1024), kIdS,
-                      kk > 0);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16(tmem + buf * 128, umma_desc_sw128(qb + (kk >> 2) * kTHalf + (kk & 3) * 32, 16, 1024),
+                      umma_desc_sw128(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, kGroup), kIdS, kk > 0);
           umma_commit(&bars[L::kSFull + buf]);
           mbar_arrive(&bars[L::kSFull + buf]);  // (what the producer wrote with the tile is seen behind it)
         };
-        auto issue_pv = [&](int x, int j, int buf) {  // O_x += P V
-          const uint32_t vb = ring + (item + 2 * j + 1) % NS * L::kTile;
+        auto issue_pv = [&](int x, int j, int buf) {  // O of warpgroup x += P V
+          const uint32_t vb = ring + (item + 2 * j + 1) % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
+          const uint32_t pc = tmem + buf * 128 + (ROWS2 ? 0 : x * 64);
 #pragma unroll
           for (int f = 0; f < (FINE ? 2 : 1); ++f)
 #pragma unroll
-            for (int kk = 0; kk < kTN / 16; ++kk)
-              umma_bf16_ts(tmem + kColO + x * 128, tmem + buf * 128 + f * 64 + kk * 8,
-                           umma_desc_sw128(vb + kk * 2048, kTHalf, 1024), kIdPV, 1u);
-          umma_commit(&bars[L::kPV + (NT == 1 ? buf : x)]);
+            for (int kk = 0; kk < KN / 16; ++kk)
+              umma_bf16_ts(tmem + kColO + x * 128, pc + f * (KN / 2) + kk * 8,
+                           umma_desc_sw128(vb + kk * 2 * kGroup, 1024, kGroup), kIdPV, 1u);
         };
-        auto full = [&](int i) { return wait(L::kFull + i % NS, (uint32_t)((i / NS) & 1)); };
-        if constexpr (NT == 1) {
-          ok = full(item);
-          if (ok) {
-            tc_fence_after();
-            issue_s(0, 0, n0 & 1);
-            umma_commit(&bars[L::kEmpty + item % NS]);
-          }
-          for (int j = 0; ok && j < nt; ++j, ++n0) {
-            if (j + 1 < nt) {
-              if (!(ok = full(item + 2 * j + 2))) break;
-              tc_fence_after();
-              issue_s(0, j + 1, (n0 + 1) & 1);
-              umma_commit(&bars[L::kEmpty + (item + 2 * j + 2) % NS]);
-            }
-            if (!(ok = full(item + 2 * j + 1) && wait(L::kPFull + (n0 & 1), (uint32_t)((n0 >> 1) & 1)))) break;
-            tc_fence_after();
-            issue_pv(0, j, n0 & 1);
-            umma_commit(&bars[L::kEmpty + (item + 2 * j + 1) % NS]);
-          }
-        } else {
-          ok = full(item);
-          if (ok) {
-            tc_fence_after();
+        auto full = [&](int i) {
+          if (!wait(L::kFull + i % NS, (uint32_t)((i / NS) & 1))) return false;
+          tc_fence_after();
+          return true;
+        };
+        auto written = [&](int b, uint32_t parity) {  // P
+          if (!wait(L::kPFull + b, parity)) return false;
+          tc_fence_after();
+          return true;
+        };
+        auto release = [&](int i) { umma_commit(&bars[L::kEmpty + (item + i) % NS]); };
+        if constexpr (ROWS2) {
+          if ((ok = full(item))) {
             issue_s(0, 0, 0);
-            if (live > 1) issue_s(1, 0, 1);
-            umma_commit(&bars[L::kEmpty + item % NS]);
+            if (live > 1) issue_s(L::kTile, 0, 1);
+            release(0);
           }
           for (int j = 0; ok && j < nt; ++j) {
             const bool more = j + 1 < nt;
-            if (!(ok = full(item + 2 * j + 1) && wait(L::kPFull, (uint32_t)(n0++ & 1)))) break;
-            tc_fence_after();
+            if (!(ok = full(item + 2 * j + 1) && written(0, (uint32_t)(n[0]++ & 1)))) break;
             issue_pv(0, j, 0);
+            umma_commit(&bars[L::kPV]);
             if (more) {
               if (!(ok = full(item + 2 * j + 2))) break;
-              tc_fence_after();
               issue_s(0, j + 1, 0);
             }
             if (live > 1) {
-              if (!(ok = wait(L::kPFull + 1, (uint32_t)(n1++ & 1)))) break;
-              tc_fence_after();
+              if (!(ok = written(1, (uint32_t)(n[1]++ & 1)))) break;
               issue_pv(1, j, 1);
+              umma_commit(&bars[L::kPV + 1]);
             }
-            umma_commit(&bars[L::kEmpty + (item + 2 * j + 1) % NS]);
+            release(2 * j + 1);
             if (more) {
-              if (live > 1) issue_s(1, j + 1, 1);
-              umma_commit(&bars[L::kEmpty + (item + 2 * j + 2) % NS]);
+              if (live > 1) issue_s(L::kTile, j + 1, 1);
+              release(2 * j + 2);
             }
+          }
+        } else {
+          if ((ok = full(item))) {
+            issue_s(0, 0, n[0] & 1);
+            release(0);
+          }
+          for (int j = 0; ok && j < nt; ++j, ++n[0]) {
+            const int buf = n[0] & 1;
+            if (j + 1 < nt) {
+              if (!(ok = full(item + 2 * j + 2))) break;
+              issue_s(0, j + 1, buf ^ 1);
+              release(2 * j + 2);
+            }
+            if (!(ok = full(item + 2 * j + 1) && written(buf, (uint32_t)((n[0] >> 1) & 1)))) break;
+            issue_pv(0, j, buf);
+            issue_pv(1, j, buf);
+            release(2 * j + 1);
+            umma_commit(&bars[L::kPV + buf]);
           }
         }
         item += 2 * nt;
@@ -499,19 +546,21 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
       mbar_wait(&bars[L::kDone], 0);  // every MMA complete before TMEM is freed
     }
   } else {
-    // ----------------------------------- softmax: row tile x, row m = TMEM lane
-    if constexpr (NT == 2) setmaxnreg_inc<kTRegsSoftmax>();
+    // ------------------------------- softmax: warpgroup x, row m = TMEM lane
+    setmaxnreg_inc<kTRegsSoftmax>();
     const int x = warp >> 2, m = tid & 127;
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16), o_col = kColO + x * 128;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t o_col = kColO + x * 128;
     const int nl = m / a.G;  // node within the row tile
+    const int xr = ROWS2 ? x : 0;  // row tile
     const bool positive = a.scale_log2 > 0.f;
     const float sc = positive ? a.scale_log2 : 1.f;
-    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads = 0;
+    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads = 0, handed = 0;  // jx: this warpgroup's key tiles
     bool ok = true;
-    // P V of this row tile's key tile n.  (With one row tile the one before it may
-    // not be complete either, so each S buffer has a barrier.)
+    // P V of this warpgroup's key tile n (one row tile: the one before it may not
+    // be complete either, so each S buffer has a barrier)
     auto wait_pv = [&](int n) -> bool {
-      return NT == 1 ? wait_warp(L::kPV + (n & 1), (uint32_t)((n >> 1) & 1)) : wait_warp(L::kPV + x, (uint32_t)(n & 1));
+      return ROWS2 ? wait_warp(L::kPV + x, (uint32_t)(n & 1)) : wait_warp(L::kPV + (n & 1), (uint32_t)((n >> 1) & 1));
     };
     while (ok) {
       const int pb = u % kTPosts;
@@ -520,10 +569,10 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
       const int kind = p[PP_KIND];
       if (kind == kPieceStop) break;
       const int row0 = p[PP_ROW0], T = p[PP_NODES], c = p[PP_CTX], h = p[PP_HEAD], t0 = p[PP_TILE], nt = p[PP_TILES];
-      const int slot = p[PP_SLOT], live = p[PP_LIVE], first = p[PP_FIRST], base = p[PP_BASE];
+      const int slot = p[PP_SLOT], live = p[PP_LIVE], first = p[PP_FIRST], base = p[PP_BASE], last = p[PP_LAST];
       ++u;
       if (kind == kPieceZero) {
-        for (int i = tid; i < T * a.G * (D / 8); i += 128 * NT) {
+        for (int i = tid; i < T * a.G * (D / 8); i += 256) {
           const int node = i / (a.G * (D / 8)), rest = i - node * (a.G * (D / 8));
           reinterpret_cast<uint4 *>(a.out + ((size_t)(first + node) * a.Hq + (size_t)h * a.G) * D)[rest] =
               make_uint4(0u, 0u, 0u, 0u);
@@ -533,113 +582,84 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
       }
       const int set = qn % L::kSets, tree0 = c / kTN;  // first key tile with a node
       ++qn;
-      if (x >= live) {  // no rows of this tile
+      if (ROWS2 && x >= live) {  // no rows for this warpgroup
         jall += nt;
         votes += max(0, t0 + nt - max(t0, tree0));
         mbar_arrive(&bars[L::kUEmpty + pb]);
         continue;
       }
-      const int node = base + x * a.nodes_tile + nl;
+      const int node = base + xr * a.nodes_tile + nl;
       const bool valid = nl < a.nodes_tile && node < T;
       const bool some = __any_sync(0xffffffffu, valid);  // rows of this warp
-      bool refused = false;
-      if (valid)
-        for (int at = node; at >= 0;) {
-          const int up = __ldg(a.parents + first + at);
-          if (!good_parent(at, up)) {
-            refused = true;
-            break;
-          }
-          at = up;
-        }
-      if (refused && a.err) atomicOr(a.err, PA_DEVERR_TREE);
+      // the second warpgroup's state of the last piece has been taken
+      if (!ROWS2 && x == 1 && handed > 0 && !wait_warp(L::kXEmpty, (uint32_t)((handed - 1) & 1))) break;
       if (some) {
-        uint32_t z[32];
+        uint32_t z[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0u;
+        for (int i = 0; i < 16; ++i) z[i] = 0u;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) tmem_st32(lane_base + o_col + i * 32, z);
+        for (int i = 0; i < D / 16; ++i) tmem_st16(lane_base + o_col + i * 16, z);
       }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < nt; ++j, ++jall, ++jx) {
-        const int t = t0 + j, key0 = t * kTN, buf = NT == 1 ? jx & 1 : x;
+      bool refused = false;  // known where the piece has the tree's last key tile
+      for (int j = 0; j < nt; ++j, ++jx) {
+        const int t = t0 + j, key0 = t * kTN + (ROWS2 ? 0 : x * KN);  // of the keys of this warpgroup
+        const int buf = ROWS2 ? x : jx & 1;
+        const uint32_t s_col = buf * 128 + (ROWS2 ? 0 : x * 64);
         const bool tree = t >= tree0;
-        uint32_t allow[4];
+        uint32_t allow[KN / 32];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) allow[w] = bits_below(c - key0, w);
-        if (tree && valid && !refused)
-          for (int at = node; at >= 0 && c + at >= key0; at = __ldg(a.parents + first + at)) {
+        for (int w = 0; w < KN / 32; ++w) allow[w] = bits_below(c - key0, w);
+        if (tree && valid) {
+          const bool to_root = last && j == nt - 1;
+          for (int at = node; at >= 0 && (to_root || c + at >= key0);) {
             const int k = c + at - key0;
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int w = 0; w < KN / 32; ++w)
               if (k >> 5 == w) allow[w] |= 1u << (k & 31);
+            const int up = __ldg(a.parents + first + at);
+            if (!good_parent(at, up)) {
+              refused = true;
+              break;
+            }
+            at = up;
           }
-        if (!wait_warp(L::kSFull + buf, (uint32_t)((NT == 1 ? jx >> 1 : jx) & 1))) {
+        }
+        if (!wait_warp(L::kSFull + buf, (uint32_t)((ROWS2 ? jx : jx >> 1) & 1))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t pages = pages_of[jall & 7], s_col = buf * 128;
-        const bool masked = tree || pages != kAllPages;
-        const int v_item = 2 * jall + 1;
-        uint8_t *vt = smem + L::kOffRing + v_item % NS * L::kTile;
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < PAGES; ++i)
-            if (!((pages >> i) & 1u)) {
-              const uint32_t run = B == 32 ? 0xffffffffu : 0xffffu << (i * B % 32);
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                if (i * B / 32 == w) allow[w] &= ~run;
-            }
-          if (x == 0) {  // value rows that no row attends, and nodes whose values are not finite
-            if (!wait_warp(L::kFull + v_item % NS, (uint32_t)((v_item / NS) & 1))) {
-              ok = false;
-              break;
-            }
-            uint4 *row = reinterpret_cast<uint4 *>(vt + m * 128);
-            const bool none = key0 + m >= c + T || !((pages >> (m / B)) & 1u);
-            if (none) {
-#pragma unroll
-              for (int i = 0; i < kHalves * 8; ++i) row[(i >> 3) * (kTHalf / 16) + ((i ^ lane) & 7)] = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            } else if (tree && key0 + m >= c) {
-              uint32_t odd = 0;
-#pragma unroll
-              for (int i = 0; i < kHalves * 8; ++i) {
-                const uint4 v = row[(i >> 3) * (kTHalf / 16) + ((i ^ lane) & 7)];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  odd |= (uint32_t)((w[e] & 0x7f80u) == 0x7f80u) | (uint32_t)((w[e] & 0x7f800000u) == 0x7f800000u);
-              }
-              if (odd) atomicOr(&bad_of[(votes & 3) * 4 + (m >> 5)], 1u << (m & 31));
-            }
-            if (tree) {
-              if (m < 4) bad_of[((votes + 2) & 3) * 4 + m] = 0;  // (two votes ago: everyone has read it)
-              mbar_arrive(&bars[L::kVote + (votes & 1)]);  // (the second tile's threads may be one vote behind)
-            }
-          }
-        }
+        const uint32_t pages_t = pages_of[(jall + j) & 7];
+        const bool masked = tree || pages_t != kAllPages;
+        const uint32_t pages = ROWS2 ? pages_t : pages_t >> (x * PAGES / 2);  // of this warpgroup's keys
         if (some) {
-          float s[kTN];
+          float s[KN];
           {
-            uint32_t v[4][32];
+            uint32_t v[KN / 32][32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(lane_base + s_col + i * 32, v[i]);
+            for (int i = 0; i < KN / 32; ++i) tmem_ld32(lane_base + s_col + i * 32, v[i]);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < KN / 32; ++i)
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[i * 32 + e] = __uint_as_float(v[i][e]);
           }
           if (!positive) {
 #pragma unroll
-            for (int i = 0; i < kTN; ++i) s[i] *= a.scale_log2;
+            for (int i = 0; i < KN; ++i) s[i] *= a.scale_log2;
           }
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < kTN; ++i) s[i] = (allow[i >> 5] >> (i & 31)) & 1u ? s[i] : -INFINITY;
+            for (int i = 0; i < KN / B; ++i)
+              if (!((pages >> i) & 1u)) {
+                const uint32_t run = B == 32 ? 0xffffffffu : 0xffffu << (i * B % 32);
+#pragma unroll
+                for (int w = 0; w < KN / 32; ++w)
+                  if (i * B / 32 == w) allow[w] &= ~run;
+              }
+#pragma unroll
+            for (int i = 0; i < KN; ++i) s[i] = (allow[i >> 5] >> (i & 31)) & 1u ? s[i] : -INFINITY;
           }
           float mx;
           {
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) pm[i] = s[i];
 #pragma unroll
-            for (int i = 8; i < kTN; i += 2) pm[(i >> 1) & 7] = max3f(pm[(i >> 1) & 7], s[i], s[i + 1]);
+            for (int i = 8; i < KN; i += 2) pm[(i >> 1) & 7] = max3f(pm[(i >> 1) & 7], s[i], s[i + 1]);
             mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
           }
           const float m_new = fmaxf(m_run, mx * sc);
@@ -656,7 +676,7 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
           const float alpha = grow ? exp2f(m_run - m_new) : 1.f;
           const float lsum = tree_probabilities<FINE>(s, sc, m_use == -INFINITY ? 0.f : m_use, lane_base + s_col);
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
-            if (NT == 1 && !wait_pv(jx - 1)) {  // (two tiles: S came behind that product)
+            if (!ROWS2 && !wait_pv(jx - 1)) {  // (two row tiles: S came behind that product)
               ok = false;
               break;
             }
@@ -675,132 +695,200 @@ __global__ void __launch_bounds__(TreeSmem<D, NT>::kThreads, 1)
           l_run = l_run * alpha + lsum;
           m_run = m_use;
         }
-        if (tree) {
-          if (!wait_warp(L::kVote + (votes & 1), (uint32_t)((votes >> 1) & 1))) {
-            ok = false;
-            break;
-          }
-          const volatile uint32_t *bad = bad_of + (votes & 3) * 4;
-          ++votes;
-          if (bad[0] | bad[1] | bad[2] | bad[3]) {
-            // a node's values that are not finite: p v added to the rows that attend them, then a cleared row
-            if (j > 0 && !wait_pv(jx - 1)) {
+        if (masked) {
+          // Value rows that no row attends are cleared; a node whose values are not finite is
+          // voted on.  (ROWS2: by the first warpgroup, whose product comes first.)
+          const int v_item = 2 * (jall + j) + 1, vote = ROWS2 ? votes & 1 : x * 2 + (votes & 1);
+          uint8_t *vt = smem + L::kOffRing + v_item % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
+          auto bad_at = [&](int v) { return bad_of + (ROWS2 ? (v & 3) * 4 : x * 8 + (v & 3) * 2); };
+          uint32_t *bad_w = bad_at(votes);
+          // this thread's value row, that of key key0 + r, or (two threads a row) its part of it
+          const int r = m & (KN - 1);
+          constexpr int kChunks = kHalves * 8 / (ROWS2 ? 1 : 2);  // 16 bytes each
+          uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
+          auto chunk = [&](int i) {
+            const int ch = ROWS2 ? i : kChunks * (m >> 6) + i;
+            return reinterpret_cast<uint4 *>(row + (ch >> 3) * 1024 + ((ch ^ (lane & (kChunks < 8 ? 3 : 7))) & 7) * 16);
+          };
+          if (!ROWS2 || x == 0) {
+            if (!wait_warp(L::kFull + v_item % NS, (uint32_t)((v_item / NS) & 1))) {
               ok = false;
               break;
             }
-            tc_fence_after();
+            if (key0 + r >= c + T || !((pages >> (r / B)) & 1u)) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              for (uint32_t left = some ? bad[w] : 0u; left; left &= left - 1) {
-                const int k = w * 32 + __ffs(left) - 1;
-                const uint32_t hi = tmem_ld1(lane_base + s_col + (k >> 1));
-                const uint32_t lo = FINE ? tmem_ld1(lane_base + s_col + 64 + (k >> 1)) : 0u;
-                tmem_wait_ld();
-                const float pk = k & 1 ? bf16_hi(hi) + bf16_hi(lo) : bf16_lo(hi) + bf16_lo(lo);
-                const bool attends = (allow[w] >> (k & 31)) & 1u;
-#pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
-                  uint32_t v[32];
-                  tmem_ld32(lane_base + o_col + i * 32, v);
-                  tmem_wait_ld();
+              for (int i = 0; i < kChunks; ++i) *chunk(i) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            } else if (tree && key0 + r >= c) {
+              uint32_t odd = 0;
 #pragma unroll
-                  for (int e = 0; e < 32; e += 2) {
-                    const int ch = (i & 1) * 4 + e / 8;  // 16-byte chunk of the half
-                    const uint32_t y = *reinterpret_cast<const uint32_t *>(vt + (i >> 1) * kTHalf + sw128(k, ch) + (e & 7) * 2);
-                    if (attends) {
-                      v[e] = __float_as_uint(__uint_as_float(v[e]) + pk * bf16_lo(y));
-                      v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + pk * bf16_hi(y));
-                    }
-                  }
-                  tmem_st32(lane_base + o_col + i * 32, v);
-                }
-                tmem_wait_st();
+              for (int i = 0; i < kChunks; ++i) {
+                const uint4 v = *chunk(i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  odd |= (uint32_t)((w[e] & 0x7f80u) == 0x7f80u) | (uint32_t)((w[e] & 0x7f800000u) == 0x7f800000u);
               }
-            mbar_arrive_n(&bars[L::kRead], NT == 2 && live == 1 ? 2u : 1u);
-            if (x == 0) {
-              const uint32_t par = (uint32_t)(reads++ & 1);
-              if (!wait_warp(L::kRead, par)) {
+              if (odd) atomicOr(&bad_w[r >> 5], 1u << (r & 31));
+            }
+            if (tree) {
+              // the buffer of the vote after next: everyone has read what was there
+              if (m < KN / 32) bad_at(votes + 2)[m] = 0;
+              mbar_arrive(&bars[L::kVote + vote]);
+            }
+          }
+          if (tree) {
+            if (!wait_warp(L::kVote + vote, (uint32_t)((votes >> 1) & 1))) {
+              ok = false;
+              break;
+            }
+            const volatile uint32_t *bad = bad_w;
+            ++votes;
+            if (bad[0] | bad[1] | (ROWS2 ? bad[2] | bad[3] : 0u)) {
+              // p v added to the rows that attend such a node, then its row cleared
+              if (!ROWS2 && j > 0 && !wait_pv(jx - 1)) {
                 ok = false;
                 break;
               }
-              if ((bad[m >> 5] >> (m & 31)) & 1u) {
-                uint4 *row = reinterpret_cast<uint4 *>(vt + m * 128);
+              tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < kHalves * 8; ++i) row[(i >> 3) * (kTHalf / 16) + (i & 7)] = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
+              for (int w = 0; w < KN / 32; ++w)
+                for (uint32_t todo = some ? bad[w] : 0u; todo; todo &= todo - 1) {
+                  const int k = w * 32 + __ffs(todo) - 1;
+                  const uint32_t hi = tmem_ld1(lane_base + s_col + (k >> 1));
+                  const uint32_t lo = FINE ? tmem_ld1(lane_base + s_col + KN / 2 + (k >> 1)) : 0u;
+                  tmem_wait_ld();
+                  const float pk = k & 1 ? bf16_hi(hi) + bf16_hi(lo) : bf16_lo(hi) + bf16_lo(lo);
+                  const bool attends = (allow[w] >> (k & 31)) & 1u;
+#pragma unroll 1
+                  for (int i = 0; i < D / 32; ++i) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_base + o_col + i * 32, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                      const int ch = (i & 1) * 4 + e / 8;  // 16-byte chunk of the half
+                      const uint32_t y = *reinterpret_cast<const uint32_t *>(
+                          vt + (k >> 3) * kGroup + (i >> 1) * 1024 + sw128(k & 7, ch) + (e & 7) * 2);
+                      if (attends) {
+                        v[e] = __float_as_uint(__uint_as_float(v[e]) + pk * bf16_lo(y));
+                        v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + pk * bf16_hi(y));
+                      }
+                    }
+                    tmem_st32(lane_base + o_col + i * 32, v);
+                  }
+                  tmem_wait_st();
+                }
+              const int rb = L::kRead + (ROWS2 ? 0 : x);
+              mbar_arrive_n(&bars[rb], ROWS2 && live == 1 ? 2u : 1u);
+              if (!ROWS2 || x == 0) {
+                const uint32_t par = (uint32_t)(reads++ & 1);
+                if (!wait_warp(rb, par)) {
+                  ok = false;
+                  break;
+                }
+                if ((bad[r >> 5] >> (r & 31)) & 1u) {
+#pragma unroll
+                  for (int i = 0; i < kChunks; ++i) *chunk(i) = make_uint4(0, 0, 0, 0);
+                  fence_proxy_async_smem();
+                }
               }
             }
           }
         }
         tc_fence_before();
-        mbar_arrive(&bars[L::kPFull + buf]);  // (a warp may be at the next key tile while another is here)
+        mbar_arrive(&bars[L::kPFull + buf]);  // (one row tile: a warp may be at the next key tile while another is here)
       }
       if (!ok || !wait_pv(jx - 1)) break;
       tc_fence_after();
+      jall += nt;
 
       // ---- the piece's end
-      if (some) {
-        const bool full = l_run != 0.f && !refused;  // (a NaN sum is no empty one)
-        if (slot < 0) {
-          const float inv = full ? 1.f / l_run : 0.f;
-          constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
-          uint8_t *stage = smem + (set * NT + x) * L::kTile + (warp & 3) * 32 * RB;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t v[32];
-            tmem_ld32(lane_base + o_col + i * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 y = make_uint4(0u, 0u, 0u, 0u);
-              if (full) {
-                y.x = pack_bf16(__uint_as_float(v[8 * k]) * inv, __uint_as_float(v[8 * k + 1]) * inv);
-                y.y = pack_bf16(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv);
-                y.z = pack_bf16(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
-                y.w = pack_bf16(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
-              }
-              *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 4 + k) ^ lane) & (CH - 1)) * 16) = y;
-            }
-          }
-          __syncwarp();
-#pragma unroll 4
-          for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
-            const int r = r0 + lane / CH, ch = lane % CH;
-            const int mr = (warp & 3) * 32 + r, n = mr / a.G;
-            if (n >= a.nodes_tile || base + x * a.nodes_tile + n >= T) continue;
-            const size_t row = (size_t)(row0 + x * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (mr - n * a.G);
-            reinterpret_cast<uint4 *>(a.out + row * D)[ch] =
-                *reinterpret_cast<const uint4 *>(stage + r * RB + ((ch ^ r) & (CH - 1)) * 16);
-          }
-          fence_proxy_async_smem();  // the next queries come by TMA
-        } else {
-          const size_t at = (size_t)blockIdx.x * 2 + slot;
-          const int r = x * 128 + m;
-          float4 *o = a.ws_o + at * (D / 4) * a.prow + r;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t v[32];
-            tmem_ld32(lane_base + o_col + i * 32, v);
-            tmem_wait_ld();
-            if (valid) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                o[(size_t)(i * 8 + k) * a.prow] =
-                    make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
-                                __uint_as_float(v[4 * k + 3]));
-            }
-          }
-          if (valid) a.ws_ml[at * a.prow + r] = make_float2(m_run, full ? l_run : 0.f);
-        }
-        tc_fence_before();
+      if (refused && a.err) atomicOr(a.err, PA_DEVERR_TREE);
+      if (!ROWS2 && x == 1) {  // the second warpgroup's state goes to the first
+        xml[m] = make_float2(m_run, l_run);
+        ++handed;
+        mbar_arrive(&bars[L::kXFull]);
+        mbar_arrive(&bars[L::kUEmpty + pb]);
+        continue;
       }
-      mbar_arrive_n(&bars[L::kQEmpty + set], NT == 2 && live == 1 ? 2u : 1u);  // (for the other tile's threads too)
+      float f0 = 1.f, f1 = 0.f;  // factors of the two states
+      if constexpr (!ROWS2) {
+        if (!wait_warp(L::kXFull, (uint32_t)(handed++ & 1))) break;
+        tc_fence_after();
+        const float2 o = xml[m];
+        const float M = fmaxf(l_run != 0.f ? m_run : -INFINITY, o.y != 0.f ? o.x : -INFINITY);
+        const float b0 = M == -INFINITY ? 0.f : M;
+        f0 = l_run != 0.f ? exp2f(m_run - b0) : 0.f;
+        f1 = o.y != 0.f ? exp2f(o.x - b0) : 0.f;
+        l_run = l_run * f0 + o.y * f1;
+        m_run = M;
+      }
+      const bool empty = l_run == 0.f || refused;  // (a NaN sum is no empty one)
+      // 16 values of this row, of both states
+      auto values = [&](int i, float (&v)[16]) {
+        uint32_t p0[16], p1[16];
+        tmem_ld16(lane_base + o_col + i * 16, p0);
+        if constexpr (!ROWS2) tmem_ld16(lane_base + o_col + 128 + i * 16, p1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          v[e] = ROWS2 ? __uint_as_float(p0[e]) : __uint_as_float(p0[e]) * f0 + __uint_as_float(p1[e]) * f1;
+      };
+      if (some && slot < 0) {
+        const float inv = empty ? 0.f : 1.f / l_run;
+        constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
+        uint8_t *stage = smem + set * L::kSet + xr * L::kTile + (warp & 3) * 32 * RB;
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
+          float v[16];
+          values(i, v);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (!empty)
+              y = make_uint4(pack_bf16(v[8 * k] * inv, v[8 * k + 1] * inv), pack_bf16(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                             pack_bf16(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                             pack_bf16(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+            *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 2 + k) ^ lane) & (CH - 1)) * 16) = y;
+          }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
+          const int r = r0 + lane / CH, ch = lane % CH;
+          const int mr = (warp & 3) * 32 + r, n = mr / a.G;
+          if (n >= a.nodes_tile || base + xr * a.nodes_tile + n >= T) continue;
+          const size_t at = (size_t)(row0 + xr * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (mr - n * a.G);
+          reinterpret_cast<uint4 *>(a.out + at * D)[ch] =
+              *reinterpret_cast<const uint4 *>(stage + r * RB + ((ch ^ r) & (CH - 1)) * 16);
+        }
+        fence_proxy_async_smem();  // the next queries come by TMA
+      } else if (some) {
+        const size_t at = (size_t)blockIdx.x * 2 + slot;
+        const int r = xr * 128 + m;
+        float4 *o = a.ws_o + at * (D / 4) * a.prow + r;
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
+          float v[16];
+          values(i, v);
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[(size_t)(i * 4 + k) * a.prow] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+        }
+        if (valid) a.ws_ml[at * a.prow + r] = make_float2(m_run, refused ? -1.f : l_run);
+      }
+      tc_fence_before();
+      if constexpr (!ROWS2) mbar_arrive(&bars[L::kXEmpty]);
+      mbar_arrive_n(&bars[L::kQEmpty + set], ROWS2 && live == 1 ? 2u : 1u);  // (for the other row tile's threads too)
       mbar_arrive(&bars[L::kUEmpty + pb]);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer) {
+  if (warp == kTIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -822,9 +910,11 @@ __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
   // piece i: share + i's, where the unit began (0) or went on
   auto at = [&](int i) { return ((size_t)(share + i) * a.tiles_x + tx) * 2 + (i == 0); };
   float M = -INFINITY, den = 0.f;
+  bool refused = false;  // the piece with the tree's last keys says so: a sum below 0
   for (int i = 0; i < pieces; ++i) {
     const float2 ml = a.ws_ml[at(i) * a.prow + r];
     if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    refused |= ml.y < 0.f;
   }
   if (M == -INFINITY) M = 0.f;
   float4 acc[4];
@@ -852,7 +942,7 @@ __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     uint4 y = make_uint4(0u, 0u, 0u, 0u);
-    if (den != 0.f) {
+    if (den != 0.f && !refused) {
       const float4 p = acc[2 * k], q = acc[2 * k + 1];
       y = make_uint4(pack_bf16(p.x * inv, p.y * inv), pack_bf16(p.z * inv, p.w * inv), pack_bf16(q.x * inv, q.y * inv),
                      pack_bf16(q.z * inv, q.w * inv));
@@ -897,19 +987,17 @@ TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   return p;
 }
 
-template <int D, int B, int NT>
+template <int D, int B, bool ROWS2>
 int launch_tree(const TreePlan &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                 const TreeArgs &a, cudaStream_t st) {
-  using L = TreeSmem<D, NT>;
-  auto kern = tree_kernel<D, B, NT>;
+  using L = TreeSmem<D, ROWS2>;
+  auto kern = tree_kernel<D, B, ROWS2>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (NT == 2) {
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PA_ERR_CUDA;
-    if (fa.numRegs < kTRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
-  }
-  int r = launch_dependent(kern, dim3(p.shares * p.tiles_x), L::kThreads, L::kAlloc, 1, st, tq, tk, tv, a);
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PA_ERR_CUDA;
+  if (fa.numRegs < kTRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
+  int r = launch_dependent(kern, dim3(p.shares * p.tiles_x), kTThreads, L::kAlloc, 1, st, tq, tk, tv, a);
   if (r == PA_OK && p.split)
     r = launch_dependent(tree_join_kernel<D>, dim3(p.prow / 32, p.shares * p.tiles_x), D * 2, 0, 1, st, a);
   return r;
@@ -974,8 +1062,8 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
   const uint64_t rows = (uint64_t)d->num_blocks * d->num_kv_heads * d->block_size;
   CUtensorMap tq, tk, tv;
   if (!encode_q_nodes(&tq, q, total_nodes, d->num_kv_heads, a.G, d->head_dim, a.box) ||
-      !encode_2d_bf16(&tk, k_pool, rows, d->head_dim, d->block_size, 64, true) ||
-      !encode_2d_bf16(&tv, v_pool, rows, d->head_dim, d->block_size, 64, true))
+      !encode_kv_groups(&tk, k_pool, rows, d->head_dim, d->block_size) ||
+      !encode_kv_groups(&tv, v_pool, rows, d->head_dim, d->block_size))
     return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // The join reads what the first kernel left in the workspace: no other such
@@ -983,7 +1071,7 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
   static std::mutex both;
   const std::lock_guard<std::mutex> lock(both);
 #define PA_TREE(D_, B_)                                                            \
-  (p.row_tiles == 1 ? launch_tree<D_, B_, 1>(p, tq, tk, tv, a, st) : launch_tree<D_, B_, 2>(p, tq, tk, tv, a, st))
+  (p.row_tiles == 1 ? launch_tree<D_, B_, false>(p, tq, tk, tv, a, st) : launch_tree<D_, B_, true>(p, tq, tk, tv, a, st))
   if (d->head_dim == 128) return d->block_size == 16 ? PA_TREE(128, 16) : PA_TREE(128, 32);
   return d->block_size == 16 ? PA_TREE(64, 16) : PA_TREE(64, 32);
 #undef PA_TREE

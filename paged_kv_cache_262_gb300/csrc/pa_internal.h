@@ -28,6 +28,10 @@ bool encode_kv_halves_3d(CUtensorMap *map, const void *base, uint64_t rows, uint
 // (128 bytes), 128-byte swizzled.
 bool encode_q_nodes(CUtensorMap *map, const void *q, uint64_t nodes, uint32_t kv_heads, uint32_t group,
                     uint32_t head_dim, uint32_t box_nodes);
+// K or V pool rows as (64 columns, 8 rows, 64-column half, 8-row group): one
+// box of box_rows rows lands as 8-row groups one after another, each its halves
+// of 8 x 128 bytes, 128-byte swizzled -- boxes laid end to end are one operand.
+bool encode_kv_groups(CUtensorMap *map, const void *base, uint64_t rows, uint32_t head_dim, uint32_t box_rows);
 // The map by which the decode unit gathers one (block, kv head) run of a
 // validated desc's K or V pool (its TMA3 form for head_dim 128).
 bool encode_kv_pages(const pa_decode_desc *d, const void *pool, CUtensorMap *map);
