@@ -543,9 +543,6 @@ int pa_paged_attention_decode_tree(const pa_decode_desc *desc, const void *q, co
 #define PA_LOGITS_BF16 0
 #define PA_LOGITS_F32 1
 
-/* Bytes of device workspace pa_verify_tree needs; 0 for bad sizes. */
-size_t pa_verify_tree_workspace_bytes(int num_seqs, int max_tree_nodes, int vocab_size);
-
 /* The path of every tree that greedy decoding would have taken.  Each node's
  * target is its logits' largest token,
  *   targets[n] = argmax_v logits[n][v], ties to the lower v, a NaN above all,
@@ -565,8 +562,6 @@ size_t pa_verify_tree_workspace_bytes(int num_seqs, int max_tree_nodes, int voca
  *                increasing order, then -1
  *   path_lens, next_tokens  device int32 [num_seqs]; 0 and -1 for a tree without
  *                nodes
- *   workspace    >= pa_verify_tree_workspace_bytes(...), 16-byte aligned, any
- *                contents; calls that may overlap on the GPU must not share one
  * A node range as refused there, or a node 0 with a parent, sets PA_DEVERR_TREE
  * and gives path_lens 0 and next_tokens -1 (and, of a refused range, no targets);
  * another node's bad parent sets it too, and that node is on no path.  No output
@@ -574,7 +569,7 @@ size_t pa_verify_tree_workspace_bytes(int num_seqs, int max_tree_nodes, int voca
 int pa_verify_tree(const void *logits, int logits_type, int64_t logits_stride, int vocab_size,
                    const int32_t *tokens, const int32_t *parents, const int32_t *cu_nodes, int num_seqs,
                    int max_tree_nodes, int total_nodes, int32_t *targets, int32_t *path, int32_t *path_lens,
-                   int32_t *next_tokens, void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+                   int32_t *next_tokens, int32_t *err_flag, void *stream);
 
 /* Moves the accepted paths' K/V up behind the contexts, in place, in every
  * layer: with c = context_lens[s] and n = path_lens[s], for i < n

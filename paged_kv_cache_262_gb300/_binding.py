@@ -39,8 +39,8 @@ EXPORTS = (
     "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
     "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens", "pa_bm_evict",
     "pa_bm_evict_batch",
-    "pa_decode_tree_workspace_bytes", "pa_paged_attention_decode_tree", "pa_verify_tree_workspace_bytes",
-    "pa_verify_tree", "pa_commit_tree", "pa_bm_reserve_batch", "pa_bm_commit_batch",
+    "pa_decode_tree_workspace_bytes", "pa_paged_attention_decode_tree", "pa_verify_tree",
+    "pa_commit_tree", "pa_bm_reserve_batch", "pa_bm_commit_batch",
 )
 
 
@@ -174,10 +174,8 @@ def load(path: Optional[str] = None):
         lib.pa_decode_tree_workspace_bytes.argtypes = [D, i]
         lib.pa_paged_attention_decode_tree.restype = i
         lib.pa_paged_attention_decode_tree.argtypes = [D, _P, _P, _P, _P, _P, _P, _P, i, i, _P, _P, sz, _P, _P]
-        lib.pa_verify_tree_workspace_bytes.restype = sz
-        lib.pa_verify_tree_workspace_bytes.argtypes = [i, i, i]
         lib.pa_verify_tree.restype = i
-        lib.pa_verify_tree.argtypes = [_P, i, i64, i, _P, _P, _P, i, i, i, _P, _P, _P, _P, _P, sz, _P, _P]
+        lib.pa_verify_tree.argtypes = [_P, i, i64, i, _P, _P, _P, i, i, i, _P, _P, _P, _P, _P, _P]
         lib.pa_commit_tree.restype = i
         lib.pa_commit_tree.argtypes = [D, _c.POINTER(_P), _c.POINTER(_P), i, _P, _P, _P, _P, i, _P, _P, _P]
         lib.pa_bm_reserve_batch.restype = i
@@ -642,6 +640,8 @@ def _fast():
             "pa_block_key_bounds", "pa_select_blocks_workspace_bytes", "pa_select_blocks",
             "pa_decode_sparse_workspace_bytes", "pa_paged_attention_decode_sparse",
             "pa_decode_weights_workspace_bytes", "pa_paged_attention_decode_weights", "pa_evict_tokens")))
+        mod.bind_trees(*(_c.cast(getattr(lib, n), _P).value for n in (
+            "pa_decode_tree_workspace_bytes", "pa_paged_attention_decode_tree", "pa_verify_tree", "pa_commit_tree")))
         _FAST = mod
     return _FAST
 
@@ -970,7 +970,7 @@ def evict_tokens(k_pool, v_pool, block_tables, context_lens, keep_lens, weights,
 
 
 # --------------------------------------------------------------- trees of drafted tokens
-_WS_TREE, _WS_VERIFY = {}, {}
+_WS_TREE = {}
 
 
 def _tree_args(T, dev, S, N, cu_nodes, parents, max_tree_nodes):
@@ -994,6 +994,12 @@ def paged_attention_decode_tree(q, k_pool, v_pool, block_tables, context_lens, c
     attends the context and its chain of ancestors (parents, indices in the
     tree, -1: none; see pagedattn.h).  max_context_len bounds the contexts
     with their trees."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and out is None and workspace is None and stream is None:
+        r = F.tree(q, k_pool, v_pool, block_tables, context_lens, cu_nodes, parents, max_tree_nodes, scale,
+                   max_context_len, err_flag, _WS_TREE)
+        if r is not None:
+            return r
     T = _T or _torch()
     bf, i32, dev = T.bf16, T.i32, T.device()
     _all(dev, (q, "q", bf, 3), (k_pool, "k_pool", bf, 4), (v_pool, "v_pool", bf, 4),
@@ -1027,12 +1033,17 @@ def paged_attention_decode_tree(q, k_pool, v_pool, block_tables, context_lens, c
 
 
 def verify_tree(logits, tokens, parents, cu_nodes, *, max_tree_nodes, targets=None, path=None, path_lens=None,
-                next_tokens=None, workspace=None, err_flag=None, stream=None):
+                next_tokens=None, err_flag=None, stream=None):
     """The path of every tree that greedy decoding would have taken: logits
     [total_nodes][vocabulary] bf16 or fp32 (rows may lie apart), tokens int32
     [total_nodes].  Returns (targets [total_nodes], path [num_seqs]
     [max_tree_nodes], path_lens [num_seqs], next_tokens [num_seqs]), int32 (see
     pagedattn.h)."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and targets is None and path is None and path_lens is None and next_tokens is None and stream is None:
+        r = F.verify(logits, tokens, parents, cu_nodes, max_tree_nodes, err_flag)
+        if r is not None:
+            return r
     T = _T or _torch()
     i32, dev = T.i32, T.device()
     if getattr(logits, "dtype", None) is not T.f32:
@@ -1067,10 +1078,8 @@ def verify_tree(logits, tokens, parents, cu_nodes, *, max_tree_nodes, targets=No
                 _bad(f"{name} must be {list(shape)}")
         made.append(t)
     lib, raw = _LIB or load(), T.stream(dev) if stream is None else stream.cuda_stream
-    ws, ws_bytes, keep = _given_ws(workspace) if workspace is not None else _call_ws(
-        T, _WS_VERIFY, lib.pa_verify_tree_workspace_bytes(S, most, V), logits.device, stream, raw)
     st = lib.pa_verify_tree(logits.data_ptr(), kind, stride, V, tokens.data_ptr(), parents.data_ptr(),
-                            cu_nodes.data_ptr(), S, most, N, *(t.data_ptr() for t in made), ws, ws_bytes,
+                            cu_nodes.data_ptr(), S, most, N, *(t.data_ptr() for t in made),
                             _err_ptr(err_flag, dev, i32), raw)
     if st:
         _check(st, "pa_verify_tree")
@@ -1082,6 +1091,11 @@ def commit_tree(k_pools: Sequence, v_pools: Sequence, block_tables, context_lens
     """Moves the accepted paths' K/V (path, path_lens of verify_tree) up
     behind the contexts in every layer's pools, in place; returns new_lens
     [num_seqs] = context_lens + path_lens (see pagedattn.h)."""
+    F = _FAST if _FAST is not None else _fast()
+    if F and new_lens is None and stream is None:
+        r = F.commit(k_pools, v_pools, block_tables, context_lens, path, path_lens, max_context_len, err_flag)
+        if r is not None:
+            return r
     T = _T or _torch()
     bf, i32, dev, L = T.bf16, T.i32, T.device(), len(k_pools)
     if L == 0 or len(v_pools) != L:

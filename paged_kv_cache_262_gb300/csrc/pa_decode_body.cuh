@@ -80,20 +80,6 @@ struct DecodeArgs {
   size_t max_tokens;
 };
 
-// Counts one arrival of this call at *c and returns the arrivals so far.  A
-// counter whose epoch tag is not this call's (left by another call or holding
-// stale data) restarts at 1, so the workspace needs no zero-fill.
-__device__ __forceinline__ unsigned int arrive_count(unsigned long long *c, unsigned int epoch) {
-  const unsigned long long tag = (unsigned long long)epoch << 32;
-  unsigned long long old = atomicAdd(c, 0ull), prev;
-  for (;;) {
-    const unsigned long long nv = ((old >> 32) == epoch) ? old + 1 : (tag | 1ull);
-    prev = atomicCAS(c, old, nv);
-    if (prev == old) return (unsigned int)(nv & 0xffffffffull);
-    old = prev;
-  }
-}
-
 // The maximum to take exponents against: 0 for a row that has none (-infinity),
 // where 2^(-inf - -inf) would be NaN.
 __device__ __forceinline__ float max_or_0(float m) { return m == -INFINITY ? 0.f : m; }

@@ -19,13 +19,20 @@
 // tile's V is let go early: with whole tiles in turn 64 x 5 nodes took 143 us);
 // trees of more have a row tile for each, and more than two row tiles are further
 // CTAs that read the same keys at the same time.  Roles:
-//   warps 0-3, 4-7  a row a thread (TMEM lane): softmax, P (bf16) back over S in
-//                   TMEM, the piece's end
-//   warp 8, 10  take the share's pieces and gather K (8) and V (10) tiles, a page
-//               a copy (4-D TMA, 128-byte swizzle), into one ring across pieces;
-//               8 posts the pieces to the other roles and loads their query rows
+//   warps 0-3, 4-7  a row a thread (TMEM lane): softmax, P (bf16) back over S in TMEM
+//   warp 8      takes the share's pieces, posts them to the other roles, loads their
+//               query rows and gathers K tiles, a page a copy (4-D TMA, 128-byte
+//               swizzle), into a ring of K and V tiles that runs across pieces
+//   warp 10     the V tiles likewise (one warp issues a page copy in about 100
+//               cycles, too slow for both where the bytes bind)
 //   warp 9      owns TMEM and issues the MMAs: S = Q K^T, O += P V (one row tile: S
-//               of the next key tile before P V of this one; two: theirs in turn)
+//               of the next key tile before P V of this one; two: theirs in turn --
+//               with an issuer for each, 8 x 64 nodes over 32K tokens took 514 us)
+//   warp 11     looks through the value rows of the tiles with a tree (below)
+//   warps 12-15 one row tile: the piece's end, beside the softmax of the next piece
+//               (in the softmax warps' hands it held up everything for up to 7000
+//               cycles a piece; a key tile takes 2500).  Two row tiles, whose pieces
+//               are long: the softmax warps' own.
 // MMAs issued by one thread complete in order.  Where the bytes bind, with one row
 // tile, the probabilities are kept as a bf16 value and a bf16 remainder (2^-16 of
 // them left) in two products, which the tensor cores have the time for; with two
@@ -74,14 +81,20 @@ constexpr int kTN = 128;                 // keys of a key tile
 constexpr int kTHalf = kTM * 128;        // 64 columns of a row tile
 constexpr int kTPosts = 4;               // pieces posted ahead
 constexpr int kTPostWords = 16;
-constexpr int kTThreads = 384;
-// as in pa_prefill_body.cuh: the softmax warpgroups take the third one's registers
-constexpr int kTRegsLaunch = 168, kTRegsSoftmax = 216, kTRegsOther = 72;
-static_assert(256 * kTRegsSoftmax + 128 * kTRegsOther <= kTThreads * kTRegsLaunch, "register split");
-constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10;  // warps
+constexpr int kTVotes = 4;               // tiles with a tree under way at once
+constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTChecker = 11, kTEnd = 12;  // warps
+// A unit counts as so many key tiles more than it has when the shares are cut:
+// what its pieces cost besides (64 x 5 nodes: FIGURE).
+constexpr int kTUnitCost = 1;
 
 template <int D, bool ROWS2>
 struct TreeSmem {
+  static constexpr int kThreads = ROWS2 ? 384 : 512;
+  // Register split (setmaxnreg): the softmax warpgroups take what the others give
+  // back.  The sum is within the launch's threads x kRegsLaunch, which the host
+  // checks before every launch (a larger sum would wait forever).
+  static constexpr int kRegsLaunch = ROWS2 ? 168 : 128, kRegsSoftmax = ROWS2 ? 216 : 152, kRegsOther = ROWS2 ? 72 : 104;
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register split");
   static constexpr int kTile = D / 64 * kTHalf;          // 128 rows
   static constexpr int kSets = ROWS2 ? 1 : 2;            // of query rows
   static constexpr int kSet = ROWS2 ? 2 * kTile : kTile;
@@ -90,14 +103,13 @@ struct TreeSmem {
   static constexpr int kOffBar = kOffRing + kSlots * kTile;
   static constexpr int kFull = 0, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots, kPFull = kSFull + 2,
                        kPV = kPFull + 2, kQFull = kPV + 2, kQEmpty = kQFull + 2, kUFull = kQEmpty + 2,
-                       kUEmpty = kUFull + kTPosts, kVote = kUEmpty + kTPosts, kRead = kVote + 4, kXFull = kRead + 2,
-                       kXEmpty = kXFull + 1, kDone = kXEmpty + 1, kBars = kDone + 1;
+                       kUEmpty = kUFull + kTPosts, kVote = kUEmpty + kTPosts, kKick = kVote + kTVotes, kRead = kKick + kTVotes,
+                       kXFull = kRead + 2, kOFree = kXFull + 2, kDone = kOFree + 1, kBars = kDone + 1;
   static constexpr int kOffPost = kOffBar + kBars * 8;
-  static constexpr int kOffPages = kOffPost + kTPosts * kTPostWords * 4;  // [8] valid pages of the latest key tiles
-  static constexpr int kOffBad = kOffPages + 8 * 4;                       // [2][4][2], ROWS2 [4][4]: keys of a tree tile that are not finite
-  static constexpr int kOffScan = (kOffBad + 16 * 4 + 7) & ~7;            // [12] sums of the warps
-  static constexpr int kOffX = kOffScan + 12 * 8;                         // [128] the second warpgroup's maximum and sum
-  static constexpr int kOffMisc = kOffX + 128 * 8;                        // TMEM address, dead, first sequence, its tiles' offset
+  static constexpr int kOffPages = kOffPost + kTPosts * kTPostWords * 4;  // [2][8] valid pages of the latest K, V tiles
+  static constexpr int kOffBad = kOffPages + 2 * 8 * 4;                   // [votes][4] keys of a tile that are not finite
+  static constexpr int kOffScan = (kOffBad + kTVotes * 16 + 7) & ~7;      // [16] sums of the warps
+  static constexpr int kOffMisc = kOffScan + 16 * 8;                      // TMEM address, dead, first sequence, its tiles' offset
   static constexpr int kBytes = kOffMisc + 24;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -122,6 +134,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int s, int B) {
   q.tiles = q.why ? 1 : (q.ctx + r.count + kTN - 1) / kTN;
   return q;
 }
+
+__device__ __forceinline__ int unit_cost(int tiles) { return tiles ? tiles + kTUnitCost : 0; }
 
 __device__ __forceinline__ long long share_begin(long long total, int shares, int i) { return total * i / shares; }
 
@@ -160,16 +174,48 @@ __device__ __forceinline__ float tree_probabilities(const float (&s)[KN], float 
 // A piece: key tiles t0 .. t0 + nt - 1 of a unit.
 struct TreePiece {
   int s, first, T, ctx, why, h, tiles, t0, nt;
+  long long unit_end;  // behind the unit, in the shares' count
 };
+
+// Zeros into the rows of a kv head of T nodes from packed row `row0` on, by `n` threads.
+template <int D>
+__device__ __forceinline__ void zero_rows(const TreeArgs &a, int row0, int T, int h, int tid, int n) {
+  const int chunks = a.G * (D / 8);
+  for (int i = tid; i < T * chunks; i += n) {
+    const int node = i / chunks, rest = i - node * chunks;
+    reinterpret_cast<uint4 *>(a.out + ((size_t)(row0 + node) * a.Hq + (size_t)h * a.G) * D)[rest] =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Row m of a row tile whose first node has packed row `row0` (nl: its node there): its row of q and out, or -1.
+__device__ __forceinline__ long long row_of(const TreeArgs &a, int row0, int nl, int h, int m, bool valid) {
+  return valid ? (long long)(row0 + nl) * a.Hq + h * a.G + (m - nl * a.G) : -1;
+}
+
+// A warp's 32 rows of RB bytes, staged with their 16-byte chunks swizzled, to
+// their places in out (`own`: the lane's row of it; columns from `col` on).
+template <int D, int RB>
+__device__ __forceinline__ void store_rows(const TreeArgs &a, const uint8_t *stage, long long own, int col, int lane) {
+  constexpr int CH = RB / 16;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
+    const int r = r0 + lane / CH, ch = lane % CH;
+    const long long to = __shfl_sync(0xffffffffu, own, r);
+    if (to >= 0)
+      reinterpret_cast<uint4 *>(a.out + to * D + col)[ch] =
+          *reinterpret_cast<const uint4 *>(stage + r * RB + ((ch ^ r) & (CH - 1)) * 16);
+  }
+}
 
 // ROWS2: the softmax warpgroups have a row tile each, else half of each key tile.
 template <int D, int B, bool ROWS2>
-__global__ void __launch_bounds__(kTThreads, 1)
+__global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
   using L = TreeSmem<D, ROWS2>;
   constexpr bool FINE = !ROWS2;
-  constexpr int kHalves = D / 64, PAGES = kTN / B, NS = L::kSlots;
+  constexpr int kHalves = D / 64, PAGES = kTN / B, NS = L::kSlots, kThreads = L::kThreads;
   constexpr int kGroup = kHalves * 1024;  // 8 keys of a K or V tile: 8 x 128 bytes of each half
   constexpr uint32_t kAllPages = (1u << PAGES) - 1u;
   constexpr uint32_t kIdS = umma_idesc_bf16(128, 128, false, false);
@@ -182,10 +228,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
   int *posts = reinterpret_cast<int *>(smem + L::kOffPost);
-  volatile uint32_t *pages_of = reinterpret_cast<uint32_t *>(smem + L::kOffPages);
-  uint32_t *bad_of = reinterpret_cast<uint32_t *>(smem + L::kOffBad);
+  volatile uint32_t *pages_of = reinterpret_cast<uint32_t *>(smem + L::kOffPages);  // [K, V][8]
+  volatile uint32_t *bad_of = reinterpret_cast<uint32_t *>(smem + L::kOffBad);
   long long *scan = reinterpret_cast<long long *>(smem + L::kOffScan);
-  float2 *xml = reinterpret_cast<float2 *>(smem + L::kOffX);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 4);
   int *start_s = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -203,18 +248,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(&bars[L::kPV + i], 1);
       mbar_init(&bars[L::kQFull + i], 1);
       mbar_init(&bars[L::kQEmpty + i], ROWS2 ? 256 : 128);
-      mbar_init(&bars[L::kVote + i], 128);
-      mbar_init(&bars[L::kVote + 2 + i], 128);
-      mbar_init(&bars[L::kRead + i], ROWS2 ? 256 : 128);
+      mbar_init(&bars[L::kRead + i], ROWS2 && i == 0 ? 256 : 128);
     }
     for (int i = 0; i < kTPosts; ++i) {
       mbar_init(&bars[L::kUFull + i], 1);
-      mbar_init(&bars[L::kUEmpty + i], 256 + 1);
+      mbar_init(&bars[L::kUEmpty + i], 256 + 2 + (ROWS2 ? 0 : 128));
     }
-    mbar_init(&bars[L::kXFull], 128);
-    mbar_init(&bars[L::kXEmpty], 128);
+    for (int i = 0; i < kTVotes; ++i) {
+      mbar_init(&bars[L::kKick + i], 1);
+      mbar_init(&bars[L::kVote + i], 1);
+    }
+    mbar_init(&bars[L::kXFull], 256);
+    mbar_init(&bars[L::kXFull + 1], 256);
+    mbar_init(&bars[L::kOFree], 128);
     mbar_init(&bars[L::kDone], 1);
-    for (int i = 0; i < 16; ++i) bad_of[i] = 0;
     *dead = 0;
     *start_s = a.S;
     fence_mbar_init();
@@ -228,10 +275,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   // ---- this CTA's share of all units' key tiles
   long long mine = 0;
-  const int per = (a.S + kTThreads - 1) / kTThreads;
+  const int per = (a.S + kThreads - 1) / kThreads;
   for (int s = tid * per; s < min(a.S, (tid + 1) * per); ++s) {
     const TreeSeq q = tree_seq(a, s, B);
-    mine += (long long)q.tiles * a.Hkv;
+    mine += (long long)unit_cost(q.tiles) * a.Hkv;
     if (q.why && blockIdx.x == 0 && a.err) atomicOr(a.err, q.why);
   }
   long long incl = mine;
@@ -246,7 +293,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_fence_after();
   long long total = 0, before = incl - mine;
 #pragma unroll
-  for (int w = 0; w < kTThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
@@ -257,7 +304,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (beg < end && beg >= before && beg < before + mine) {
     long long at = before;
     for (int s = tid * per;; ++s) {
-      const long long n = (long long)tree_seq(a, s, B).tiles * a.Hkv;
+      const long long n = (long long)unit_cost(tree_seq(a, s, B).tiles) * a.Hkv;
       if (beg < at + n) {
         *start_s = s;
         *start_off = beg - at;
@@ -282,12 +329,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
   auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
   if (warp >= 8) {
-    setmaxnreg_dec<kTRegsOther>();
+    setmaxnreg_dec<L::kRegsOther>();
     if (warp == kTProducerK || warp == kTProducerV) {
       // ----------------------------------------------------------- producers
       // (the rows of further CTAs read the same keys: they stay in L2 for them)
       const uint64_t pol = a.tiles_x > 1 ? policy_evict_normal() : policy_evict_first();
-      const int kv = warp == kTProducerV;  // K tiles are the ring's even items, V tiles the odd ones
+      // K tiles are the ring's even items, V tiles the odd ones
+      const int kv = warp == kTProducerV;
       const CUtensorMap *map = kv ? &tmV : &tmK;
       const int base = ROWS2 ? tx * 2 * a.nodes_tile : 0;  // first node of this CTA's rows
       long long pos = beg, off = beg < end ? *start_off : 0;
@@ -313,19 +361,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
           p.ctx = __shfl_sync(0xffffffffu, near.ctx, s & 31);
           p.why = __shfl_sync(0xffffffffu, near.why, s & 31);
           p.tiles = tiles;
-          p.h = (int)(off / tiles);
-          p.t0 = (int)(off - (long long)p.h * tiles);
-          const int nt = (int)min((long long)(tiles - p.t0), end - pos);
-          pos += nt;
-          off += nt;
-          if (off == (long long)tiles * a.Hkv) {
+          // the unit's first kTUnitCost places stand for what it costs besides its tiles
+          const int cost = unit_cost(tiles);
+          p.h = (int)(off / cost);
+          const int from = (int)(off - (long long)p.h * cost), n = (int)min((long long)(cost - from), end - pos);
+          p.t0 = max(from - kTUnitCost, 0);
+          p.nt = max(from + n - kTUnitCost, 0) - p.t0;
+          pos += n;
+          off += n;
+          p.unit_end = pos + (cost - from - n);
+          if (off == (long long)cost * a.Hkv) {
             off = 0;
             ++s;
           }
-          if (p.why ? tx == 0 : p.T > base) {
-            p.nt = nt;
-            return p;
-          }
+          if (p.nt > 0 && (p.why ? tx == 0 : p.T > base)) return p;
         }
         p.nt = 0;
         return p;
@@ -347,7 +396,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
       TreePiece p = next_piece();
       int cur = p.nt > 0 && !p.why ? page_id(p, p.t0) : -1;
       while (p.nt > 0) {
-        const long long unit_end = pos - p.nt - p.t0 + p.tiles;  // (of the piece that next_piece gave last)
         const TreePiece n = next_piece();
         const int left = p.T - base, live = !ROWS2 || left <= a.nodes_tile ? 1 : 2;
         if (!kv) {
@@ -370,7 +418,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             mbar_arrive(&bars[L::kUFull + pb]);
             // the share that has the unit's last tile
             if (slot == 1)
-              a.ws_next[blockIdx.x] = make_int4(p.first + base, p.h, left, (int)((unit_end * shares - 1) / total));
+              a.ws_next[blockIdx.x] = make_int4(p.first + base, p.h, left, (int)((p.unit_end * shares - 1) / total));
           }
           goes_on |= slot == 1;
           ++u;
@@ -402,15 +450,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
             return true;
           };
           for (int t = p.t0; ok && t < p.t0 + p.nt; ++t, ++jall) {
-            const int item = 2 * jall + kv, sl = item % NS;
             // the next tile's page on its way meanwhile, or that of the next piece's first
             const int nxt = t + 1 < p.t0 + p.nt ? page_id(p, t + 1) : n.nt > 0 && !n.why ? page_id(n, n.t0) : -1;
             const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0);
-            if (q_due && !(ok = queries(item + 1 - NS >= 2 * first))) break;
+            if (q_due && !(ok = queries(2 * jall + 1 - NS >= 2 * first))) break;
+            const int item = 2 * jall + kv, sl = item % NS;
             uint64_t *bar = &bars[L::kFull + sl];
             if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
             if (lane == 0) {
-              if (!kv) pages_of[jall & 7] = have;
+              pages_of[kv * 8 + (jall & 7)] = have;
               if (have)
                 mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * B * D * 2);
               else
@@ -439,14 +487,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         for (int i = max(0, qn - L::kSets); i < qn; ++i)
           mbar_wait(&bars[L::kQFull + i % L::kSets], (uint32_t)((i / L::kSets) & 1));
       }
-      // what is still in flight lands before the CTA leaves
-      for (int j = max(0, jall - (NS + 1) / 2); j < jall; ++j) {
-        const int item = 2 * j + kv;
-        if (item >= 2 * jall - NS) mbar_wait(&bars[L::kFull + item % NS], (uint32_t)((item / NS) & 1));
-      }
+      // what is still in flight lands before the CTA leaves: the last item of each slot (an
+      // earlier one's phase may be two behind by now, which its parity does not tell)
+      for (int i = max(0, 2 * jall - NS); i < 2 * jall; ++i)
+        if ((i & 1) == kv) mbar_wait(&bars[L::kFull + i % NS], (uint32_t)((i / NS) & 1));
     } else if (warp == kTIssuer && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
-      int u = 0, qn = 0, item = 0, n[2] = {0, 0};  // n: key tiles of the warpgroups
+      int u = 0, qn = 0, item = 0, n = 0, n1 = 0;  // n, n1: key tiles (of the row tiles)
       bool ok = true;
       while (ok) {
         const int pb = u % kTPosts;
@@ -459,9 +506,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           mbar_arrive(&bars[L::kUEmpty + pb]);
           continue;
         }
-        const int set = qn % L::kSets;
-        if (!wait(L::kQFull + set, (uint32_t)((qn / L::kSets) & 1))) break;
-        ++qn;
+        const int set = qn++ % L::kSets;
+        if (!wait(L::kQFull + set, (uint32_t)(((qn - 1) / L::kSets) & 1))) break;
         const uint32_t sq = smem_u32(smem + set * L::kSet), ring = smem_u32(smem + L::kOffRing);
         // S of the rows at sq + q against the K tile of key tile j, into S columns `buf`
         auto issue_s = [&](int q, int j, int buf) {
@@ -502,7 +548,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           for (int j = 0; ok && j < nt; ++j) {
             const bool more = j + 1 < nt;
-            if (!(ok = full(item + 2 * j + 1) && written(0, (uint32_t)(n[0]++ & 1)))) break;
+            if (!(ok = full(item + 2 * j + 1) && written(0, (uint32_t)(n++ & 1)))) break;
             issue_pv(0, j, 0);
             umma_commit(&bars[L::kPV]);
             if (more) {
@@ -510,7 +556,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               issue_s(0, j + 1, 0);
             }
             if (live > 1) {
-              if (!(ok = written(1, (uint32_t)(n[1]++ & 1)))) break;
+              if (!(ok = written(1, (uint32_t)(n1++ & 1)))) break;
               issue_pv(1, j, 1);
               umma_commit(&bars[L::kPV + 1]);
             }
@@ -522,17 +568,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
         } else {
           if ((ok = full(item))) {
-            issue_s(0, 0, n[0] & 1);
+            issue_s(0, 0, n & 1);
             release(0);
           }
-          for (int j = 0; ok && j < nt; ++j, ++n[0]) {
-            const int buf = n[0] & 1;
+          for (int j = 0; ok && j < nt; ++j, ++n) {
+            const int buf = n & 1;
             if (j + 1 < nt) {
               if (!(ok = full(item + 2 * j + 2))) break;
               issue_s(0, j + 1, buf ^ 1);
               release(2 * j + 2);
             }
-            if (!(ok = full(item + 2 * j + 1) && written(buf, (uint32_t)((n[0] >> 1) & 1)))) break;
+            if (!(ok = full(item + 2 * j + 1) && written(buf, (uint32_t)((n >> 1) & 1)) &&
+                       (j > 0 || wait(L::kOFree, (uint32_t)((qn - 1) & 1)))))
+              break;
+            tc_fence_after();
             issue_pv(0, j, buf);
             issue_pv(1, j, buf);
             release(2 * j + 1);
@@ -544,10 +593,163 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       umma_commit(&bars[L::kDone]);
       mbar_wait(&bars[L::kDone], 0);  // every MMA complete before TMEM is freed
+    } else if (warp == kTChecker) {
+      // ------------- value rows of the tiles with a tree, once their scores are there
+      int u = 0, jall = 0, votes = 0;
+      while (true) {
+        const int pb = u % kTPosts;
+        if (!wait_warp(L::kUFull + pb, (uint32_t)((u / kTPosts) & 1))) break;
+        const int *p = posts + pb * kTPostWords;
+        const int kind = p[PP_KIND], nt = p[PP_TILES], c = p[PP_CTX], T = p[PP_NODES], t0 = p[PP_TILE];
+        if (kind == kPieceStop) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kUEmpty + pb]);
+        ++u;
+        if (kind == kPieceZero) continue;
+        bool ok = true;
+        for (int t = max(t0, c / kTN); ok && t < t0 + nt; ++t, ++votes) {
+          const int tile = jall + t - t0, item = 2 * tile + 1, key0 = t * kTN;
+          // (what is behind the scores' barrier has left the V tile's slot to it)
+          if (!(ok = wait_warp(L::kKick + votes % kTVotes, (uint32_t)((votes / kTVotes) & 1)) &&
+                     wait_warp(L::kFull + item % NS, (uint32_t)((item / NS) & 1))))
+            break;
+          const uint32_t pages = pages_of[8 + (tile & 7)];
+          uint8_t *vt = smem + L::kOffRing + item % NS * L::kTile;
+          for (int g = 0; g < kTN / 32; ++g) {
+            const int r = g * 32 + lane;
+            uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
+            bool odd = false;
+            if (key0 + r >= c + T || !((pages >> (r / B)) & 1u)) {  // no row attends it
+#pragma unroll
+              for (int i = 0; i < kHalves * 8; ++i)
+                *reinterpret_cast<uint4 *>(row + (i >> 3) * 1024 + ((i ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+            } else if (key0 + r >= c) {
+#pragma unroll
+              for (int i = 0; i < kHalves * 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(row + (i >> 3) * 1024 + ((i ^ lane) & 7) * 16);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+            const uint32_t b = __ballot_sync(0xffffffffu, odd);
+            if (lane == 0) bad_of[votes % kTVotes * 4 + g] = b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::kVote + votes % kTVotes]);
+        }
+        if (!ok) break;
+        jall += nt;
+      }
+    } else if (!ROWS2 && warp >= kTEnd) {
+      // --------------------- a piece's end: the two states of every row joined
+      const int w = warp & 3, m = tid & 127;
+      const uint32_t lane_base = tmem + ((uint32_t)(w * 32) << 16);
+      const int nl = m / a.G;
+      int u = 0, qn = 0, jall = 0;
+      auto clear = [&]() {  // both states, for the next piece
+        uint32_t z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          tmem_st16(lane_base + kColO + i * 16, z);
+          tmem_st16(lane_base + kColO + 128 + i * 16, z);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars[L::kOFree]);
+      };
+      clear();
+      while (true) {
+        const int pb = u % kTPosts;
+        if (!wait_warp(L::kUFull + pb, (uint32_t)((u / kTPosts) & 1))) break;
+        const int *p = posts + pb * kTPostWords;
+        const int kind = p[PP_KIND];
+        if (kind == kPieceStop) break;
+        const int row0 = p[PP_ROW0], T = p[PP_NODES], h = p[PP_HEAD], nt = p[PP_TILES], slot = p[PP_SLOT];
+        ++u;
+        mbar_arrive(&bars[L::kUEmpty + pb]);
+        if (kind == kPieceZero) {
+          zero_rows<D>(a, row0, T, h, m, 128);
+          continue;
+        }
+        const int set = qn % L::kSets;
+        ++qn;
+        jall += nt;
+        const int last = jall - 1;
+        const bool valid = nl < a.nodes_tile && nl < T, some = __any_sync(0xffffffffu, valid);
+        // the row's states, left in the piece's query rows' room (which nothing reads any more), then the products
+        uint8_t *stage = smem + set * L::kSet + w * 32 * D * 2;
+        if (!wait_warp(L::kXFull + set, (uint32_t)(((qn - 1) >> 1) & 1)) ||
+            !wait_warp(L::kPV + (last & 1), (uint32_t)((last >> 1) & 1)))
+          break;
+        tc_fence_after();
+        const float2 s0 = reinterpret_cast<const float2 *>(stage)[lane], s1 = reinterpret_cast<const float2 *>(stage)[32 + lane];
+        __syncwarp();
+        const bool refused = s0.y < 0.f;
+        const float M = fmaxf(s0.y != 0.f ? s0.x : -INFINITY, s1.y != 0.f ? s1.x : -INFINITY);
+        const float b0 = M == -INFINITY ? 0.f : M;
+        float f0 = s0.y != 0.f ? exp2f(s0.x - b0) : 0.f, f1 = s1.y != 0.f ? exp2f(s1.x - b0) : 0.f;
+        const float l = s0.y * f0 + s1.y * f1;
+        auto values = [&](int i, float (&v)[16]) {  // 16 i .. 16 i + 15, of both states
+          uint32_t p0[16], p1[16];
+          tmem_ld16(lane_base + kColO + i * 16, p0);
+          tmem_ld16(lane_base + kColO + 128 + i * 16, p1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(p0[e]) * f0 + __uint_as_float(p1[e]) * f1;
+        };
+        if (some && slot < 0) {
+          const bool empty = l == 0.f || refused;  // (a NaN sum is no empty one)
+          const float inv = 1.f / l;
+          f0 *= inv, f1 *= inv;
+          constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
+#pragma unroll 2
+          for (int i = 0; i < D / 16; ++i) {
+            float v[16];
+            values(i, v);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if (!empty)
+                y = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
+                               pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
+              *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 2 + k) ^ lane) & (CH - 1)) * 16) = y;
+            }
+            __syncwarp();
+          }
+          clear();
+          store_rows<D, RB>(a, stage, row_of(a, row0, nl, h, m, valid), 0, lane);
+          fence_proxy_async_smem();  // the next queries come by TMA
+        } else {
+          if (some) {
+            const size_t at = (size_t)blockIdx.x * 2 + slot;
+            float4 *o = a.ws_o + at * (D / 4) * a.prow + m;
+#pragma unroll 2
+            for (int i = 0; i < D / 16; ++i) {
+              float v[16];
+              values(i, v);
+              if (valid) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  o[(size_t)(i * 4 + k) * a.prow] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              }
+              __syncwarp();
+            }
+            if (valid) a.ws_ml[at * a.prow + m] = make_float2(M, refused ? -1.f : l);
+            __syncwarp();
+          }
+          clear();
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(&bars[L::kQEmpty + set]);
+      }
     }
   } else {
     // ------------------------------- softmax: warpgroup x, row m = TMEM lane
-    setmaxnreg_inc<kTRegsSoftmax>();
+    setmaxnreg_inc<L::kRegsSoftmax>();
     const int x = warp >> 2, m = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_col = kColO + x * 128;
@@ -555,7 +757,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int xr = ROWS2 ? x : 0;  // row tile
     const bool positive = a.scale_log2 > 0.f;
     const float sc = positive ? a.scale_log2 : 1.f;
-    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads = 0, handed = 0;  // jx: this warpgroup's key tiles
+    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads[2] = {0, 0};  // jx: this warpgroup's key tiles
     bool ok = true;
     // P V of this warpgroup's key tile n (one row tile: the one before it may not
     // be complete either, so each S buffer has a barrier)
@@ -572,11 +774,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int slot = p[PP_SLOT], live = p[PP_LIVE], first = p[PP_FIRST], base = p[PP_BASE], last = p[PP_LAST];
       ++u;
       if (kind == kPieceZero) {
-        for (int i = tid; i < T * a.G * (D / 8); i += 256) {
-          const int node = i / (a.G * (D / 8)), rest = i - node * (a.G * (D / 8));
-          reinterpret_cast<uint4 *>(a.out + ((size_t)(first + node) * a.Hq + (size_t)h * a.G) * D)[rest] =
-              make_uint4(0u, 0u, 0u, 0u);
-        }
+        if constexpr (ROWS2) zero_rows<D>(a, first, T, h, tid, 256);
         mbar_arrive(&bars[L::kUEmpty + pb]);
         continue;
       }
@@ -591,9 +789,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int node = base + xr * a.nodes_tile + nl;
       const bool valid = nl < a.nodes_tile && node < T;
       const bool some = __any_sync(0xffffffffu, valid);  // rows of this warp
-      // the second warpgroup's state of the last piece has been taken
-      if (!ROWS2 && x == 1 && handed > 0 && !wait_warp(L::kXEmpty, (uint32_t)((handed - 1) & 1))) break;
-      if (some) {
+      if (valid && last)  // the chains to be walked behind the last key tile
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.parents + first + node));
+      __syncwarp();
+      if (ROWS2 && some) {
         uint32_t z[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) z[i] = 0u;
@@ -630,6 +829,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           break;
         }
         tc_fence_after();
+        if (tree && x == 0 && m == 0) mbar_arrive(&bars[L::kKick + votes % kTVotes]);
+        __syncwarp();
         const uint32_t pages_t = pages_of[(jall + j) & 7];
         const bool masked = tree || pages_t != kAllPages;
         const uint32_t pages = ROWS2 ? pages_t : pages_t >> (x * PAGES / 2);  // of this warpgroup's keys
@@ -695,194 +896,136 @@ __global__ void __launch_bounds__(kTThreads, 1)
           l_run = l_run * alpha + lsum;
           m_run = m_use;
         }
-        if (masked) {
-          // Value rows that no row attends are cleared; a node whose values are not finite is
-          // voted on.  (ROWS2: by the first warpgroup, whose product comes first.)
-          const int v_item = 2 * (jall + j) + 1, vote = ROWS2 ? votes & 1 : x * 2 + (votes & 1);
-          uint8_t *vt = smem + L::kOffRing + v_item % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
-          auto bad_at = [&](int v) { return bad_of + (ROWS2 ? (v & 3) * 4 : x * 8 + (v & 3) * 2); };
-          uint32_t *bad_w = bad_at(votes);
-          // this thread's value row, that of key key0 + r, or (two threads a row) its part of it
-          const int r = m & (KN - 1);
-          constexpr int kChunks = kHalves * 8 / (ROWS2 ? 1 : 2);  // 16 bytes each
-          uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
-          auto chunk = [&](int i) {
-            const int ch = ROWS2 ? i : kChunks * (m >> 6) + i;
-            return reinterpret_cast<uint4 *>(row + (ch >> 3) * 1024 + ((ch ^ (lane & (kChunks < 8 ? 3 : 7))) & 7) * 16);
-          };
-          if (!ROWS2 || x == 0) {
-            if (!wait_warp(L::kFull + v_item % NS, (uint32_t)((v_item / NS) & 1))) {
-              ok = false;
-              break;
-            }
-            if (key0 + r >= c + T || !((pages >> (r / B)) & 1u)) {
+        const int v_item = 2 * (jall + j) + 1;
+        uint8_t *vt = smem + L::kOffRing + v_item % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
+        // clears the value rows r < KN of this warpgroup's keys that `which` says
+        auto clear_rows = [&](auto which) {
+          for (int r = m; r < KN; r += 128)
+            if (which(r)) {
+              uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
 #pragma unroll
-              for (int i = 0; i < kChunks; ++i) *chunk(i) = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < kHalves * 8; ++i)
+                *reinterpret_cast<uint4 *>(row + (i >> 3) * 1024 + ((i ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
-            } else if (tree && key0 + r >= c) {
-              uint32_t odd = 0;
-#pragma unroll
-              for (int i = 0; i < kChunks; ++i) {
-                const uint4 v = *chunk(i);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  odd |= (uint32_t)((w[e] & 0x7f80u) == 0x7f80u) | (uint32_t)((w[e] & 0x7f800000u) == 0x7f800000u);
-              }
-              if (odd) atomicOr(&bad_w[r >> 5], 1u << (r & 31));
             }
-            if (tree) {
-              // the buffer of the vote after next: everyone has read what was there
-              if (m < KN / 32) bad_at(votes + 2)[m] = 0;
-              mbar_arrive(&bars[L::kVote + vote]);
-            }
+        };
+        if (tree) {
+          if (!wait_warp(L::kVote + votes % kTVotes, (uint32_t)((votes / kTVotes) & 1))) {
+            ok = false;
+            break;
           }
-          if (tree) {
-            if (!wait_warp(L::kVote + vote, (uint32_t)((votes >> 1) & 1))) {
+          const volatile uint32_t *bad = bad_of + votes % kTVotes * 4 + (ROWS2 ? 0 : x * 2);
+          ++votes;
+          if (bad[0] | bad[1] | (ROWS2 ? bad[2] | bad[3] : 0u)) {
+            // p v added to the rows that attend such a node, then its row cleared
+            if (!ROWS2 && !(j > 0 ? wait_pv(jx - 1) : wait_warp(L::kOFree, (uint32_t)((qn - 1) & 1)))) {
               ok = false;
               break;
             }
-            const volatile uint32_t *bad = bad_w;
-            ++votes;
-            if (bad[0] | bad[1] | (ROWS2 ? bad[2] | bad[3] : 0u)) {
-              // p v added to the rows that attend such a node, then its row cleared
-              if (!ROWS2 && j > 0 && !wait_pv(jx - 1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+            tc_fence_after();
 #pragma unroll
-              for (int w = 0; w < KN / 32; ++w)
-                for (uint32_t todo = some ? bad[w] : 0u; todo; todo &= todo - 1) {
-                  const int k = w * 32 + __ffs(todo) - 1;
-                  const uint32_t hi = tmem_ld1(lane_base + s_col + (k >> 1));
-                  const uint32_t lo = FINE ? tmem_ld1(lane_base + s_col + KN / 2 + (k >> 1)) : 0u;
-                  tmem_wait_ld();
-                  const float pk = k & 1 ? bf16_hi(hi) + bf16_hi(lo) : bf16_lo(hi) + bf16_lo(lo);
-                  const bool attends = (allow[w] >> (k & 31)) & 1u;
+            for (int w = 0; w < KN / 32; ++w)
+              for (uint32_t todo = some ? bad[w] : 0u; todo; todo &= todo - 1) {
+                const int k = w * 32 + __ffs(todo) - 1;
+                const uint32_t hi = tmem_ld1(lane_base + s_col + (k >> 1));
+                const uint32_t lo = FINE ? tmem_ld1(lane_base + s_col + KN / 2 + (k >> 1)) : 0u;
+                tmem_wait_ld();
+                const float pk = k & 1 ? bf16_hi(hi) + bf16_hi(lo) : bf16_lo(hi) + bf16_lo(lo);
+                const bool attends = (allow[w] >> (k & 31)) & 1u;
 #pragma unroll 1
-                  for (int i = 0; i < D / 32; ++i) {
-                    uint32_t v[32];
-                    tmem_ld32(lane_base + o_col + i * 32, v);
-                    tmem_wait_ld();
+                for (int i = 0; i < D / 32; ++i) {
+                  uint32_t v[32];
+                  tmem_ld32(lane_base + o_col + i * 32, v);
+                  tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                      const int ch = (i & 1) * 4 + e / 8;  // 16-byte chunk of the half
-                      const uint32_t y = *reinterpret_cast<const uint32_t *>(
-                          vt + (k >> 3) * kGroup + (i >> 1) * 1024 + sw128(k & 7, ch) + (e & 7) * 2);
-                      if (attends) {
-                        v[e] = __float_as_uint(__uint_as_float(v[e]) + pk * bf16_lo(y));
-                        v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + pk * bf16_hi(y));
-                      }
+                  for (int e = 0; e < 32; e += 2) {
+                    const int ch = (i & 1) * 4 + e / 8;  // 16-byte chunk of the half
+                    const uint32_t y = *reinterpret_cast<const uint32_t *>(vt + (k >> 3) * kGroup + (i >> 1) * 1024 +
+                                                                           sw128(k & 7, ch) + (e & 7) * 2);
+                    if (attends) {
+                      v[e] = __float_as_uint(__uint_as_float(v[e]) + pk * bf16_lo(y));
+                      v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + pk * bf16_hi(y));
                     }
-                    tmem_st32(lane_base + o_col + i * 32, v);
                   }
-                  tmem_wait_st();
+                  tmem_st32(lane_base + o_col + i * 32, v);
                 }
-              const int rb = L::kRead + (ROWS2 ? 0 : x);
-              mbar_arrive_n(&bars[rb], ROWS2 && live == 1 ? 2u : 1u);
-              if (!ROWS2 || x == 0) {
-                const uint32_t par = (uint32_t)(reads++ & 1);
-                if (!wait_warp(rb, par)) {
-                  ok = false;
-                  break;
-                }
-                if ((bad[r >> 5] >> (r & 31)) & 1u) {
-#pragma unroll
-                  for (int i = 0; i < kChunks; ++i) *chunk(i) = make_uint4(0, 0, 0, 0);
-                  fence_proxy_async_smem();
-                }
+                tmem_wait_st();
               }
+            const int rb = ROWS2 ? live == 1 : x;  // everyone has read them (two row tiles: both warpgroups)
+            mbar_arrive(&bars[L::kRead + rb]);
+            if (!wait_warp(L::kRead + rb, (uint32_t)(reads[rb]++ & 1))) {
+              ok = false;
+              break;
             }
+            clear_rows([&](int r) { return (bad[r >> 5] >> (r & 31)) & 1u; });
           }
+        } else if (masked) {  // pages outside the pool
+          if (!wait_warp(L::kFull + v_item % NS, (uint32_t)((v_item / NS) & 1))) {
+            ok = false;
+            break;
+          }
+          clear_rows([&](int r) { return !((pages >> (r / B)) & 1u); });
         }
         tc_fence_before();
         mbar_arrive(&bars[L::kPFull + buf]);  // (one row tile: a warp may be at the next key tile while another is here)
       }
-      if (!ok || !wait_pv(jx - 1)) break;
-      tc_fence_after();
+      if (!ok) break;
       jall += nt;
-
-      // ---- the piece's end
       if (refused && a.err) atomicOr(a.err, PA_DEVERR_TREE);
-      if (!ROWS2 && x == 1) {  // the second warpgroup's state goes to the first
-        xml[m] = make_float2(m_run, l_run);
-        ++handed;
-        mbar_arrive(&bars[L::kXFull]);
-        mbar_arrive(&bars[L::kUEmpty + pb]);
-        continue;
-      }
-      float f0 = 1.f, f1 = 0.f;  // factors of the two states
-      if constexpr (!ROWS2) {
-        if (!wait_warp(L::kXFull, (uint32_t)(handed++ & 1))) break;
+      if constexpr (!ROWS2) {  // to the warps that end the piece
+        float2 *to = reinterpret_cast<float2 *>(smem + set * L::kSet + (warp & 3) * 32 * D * 2);
+        to[x * 32 + lane] = make_float2(m_run, refused && x == 0 ? -1.f : l_run);
+        mbar_arrive(&bars[L::kXFull + set]);  // (the softmax may end the next piece before these have ended this one)
+      } else {
+        if (!wait_pv(jx - 1)) break;
         tc_fence_after();
-        const float2 o = xml[m];
-        const float M = fmaxf(l_run != 0.f ? m_run : -INFINITY, o.y != 0.f ? o.x : -INFINITY);
-        const float b0 = M == -INFINITY ? 0.f : M;
-        f0 = l_run != 0.f ? exp2f(m_run - b0) : 0.f;
-        f1 = o.y != 0.f ? exp2f(o.x - b0) : 0.f;
-        l_run = l_run * f0 + o.y * f1;
-        m_run = M;
-      }
-      const bool empty = l_run == 0.f || refused;  // (a NaN sum is no empty one)
-      // 16 values of this row, of both states
-      auto values = [&](int i, float (&v)[16]) {
-        uint32_t p0[16], p1[16];
-        tmem_ld16(lane_base + o_col + i * 16, p0);
-        if constexpr (!ROWS2) tmem_ld16(lane_base + o_col + 128 + i * 16, p1);
-        tmem_wait_ld();
+        auto values = [&](int i, float f, float (&v)[16]) {
+          uint32_t p0[16];
+          __syncwarp();
+          tmem_ld16(lane_base + o_col + i * 16, p0);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          v[e] = ROWS2 ? __uint_as_float(p0[e]) : __uint_as_float(p0[e]) * f0 + __uint_as_float(p1[e]) * f1;
-      };
-      if (some && slot < 0) {
-        const float inv = empty ? 0.f : 1.f / l_run;
-        constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
-        uint8_t *stage = smem + set * L::kSet + xr * L::kTile + (warp & 3) * 32 * RB;
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(p0[e]) * f;
+        };
+        if (some && slot < 0) {
+          constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
+          uint8_t *stage = smem + x * L::kTile + (warp & 3) * 32 * RB;
+          const bool empty = l_run == 0.f || refused;  // (a NaN sum is no empty one)
+          const float inv = 1.f / l_run;
 #pragma unroll 2
-        for (int i = 0; i < D / 16; ++i) {
-          float v[16];
-          values(i, v);
+          for (int i = 0; i < D / 16; ++i) {
+            float v[16];
+            values(i, inv, v);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint4 y = make_uint4(0u, 0u, 0u, 0u);
-            if (!empty)
-              y = make_uint4(pack_bf16(v[8 * k] * inv, v[8 * k + 1] * inv), pack_bf16(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                             pack_bf16(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                             pack_bf16(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-            *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 2 + k) ^ lane) & (CH - 1)) * 16) = y;
+            for (int k = 0; k < 2; ++k) {
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if (!empty)
+                y = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
+                               pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
+              *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 2 + k) ^ lane) & (CH - 1)) * 16) = y;
+            }
           }
-        }
-        __syncwarp();
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
-          const int r = r0 + lane / CH, ch = lane % CH;
-          const int mr = (warp & 3) * 32 + r, n = mr / a.G;
-          if (n >= a.nodes_tile || base + xr * a.nodes_tile + n >= T) continue;
-          const size_t at = (size_t)(row0 + xr * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (mr - n * a.G);
-          reinterpret_cast<uint4 *>(a.out + at * D)[ch] =
-              *reinterpret_cast<const uint4 *>(stage + r * RB + ((ch ^ r) & (CH - 1)) * 16);
-        }
-        fence_proxy_async_smem();  // the next queries come by TMA
-      } else if (some) {
-        const size_t at = (size_t)blockIdx.x * 2 + slot;
-        const int r = xr * 128 + m;
-        float4 *o = a.ws_o + at * (D / 4) * a.prow + r;
+          __syncwarp();
+          store_rows<D, RB>(a, stage, row_of(a, row0 + x * a.nodes_tile, nl, h, m, valid), 0, lane);
+          fence_proxy_async_smem();  // the next queries come by TMA
+        } else if (some) {
+          const size_t at = (size_t)blockIdx.x * 2 + slot;
+          float4 *o = a.ws_o + at * (D / 4) * a.prow + x * 128 + m;
 #pragma unroll 2
-        for (int i = 0; i < D / 16; ++i) {
-          float v[16];
-          values(i, v);
-          if (valid) {
+          for (int i = 0; i < D / 16; ++i) {
+            float v[16];
+            values(i, 1.f, v);
+            if (valid) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[(size_t)(i * 4 + k) * a.prow] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 4; ++k)
+                o[(size_t)(i * 4 + k) * a.prow] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
           }
+          if (valid) a.ws_ml[at * a.prow + x * 128 + m] = make_float2(m_run, refused ? -1.f : l_run);
         }
-        if (valid) a.ws_ml[at * a.prow + r] = make_float2(m_run, refused ? -1.f : l_run);
+        tc_fence_before();
+        mbar_arrive_n(&bars[L::kQEmpty + set], live == 1 ? 2u : 1u);  // (for the other row tile's threads too)
       }
-      tc_fence_before();
-      if constexpr (!ROWS2) mbar_arrive(&bars[L::kXEmpty]);
-      mbar_arrive_n(&bars[L::kQEmpty + set], ROWS2 && live == 1 ? 2u : 1u);  // (for the other row tile's threads too)
       mbar_arrive(&bars[L::kUEmpty + pb]);
     }
   }
@@ -975,7 +1118,7 @@ TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   const long long tiles = std::max<long long>(1, ((long long)d->max_context_len + kTN - 1) / kTN);
   const long long units = std::max<long long>(1, (long long)d->num_seqs * d->num_kv_heads);
   p.shares = (int)std::max<long long>(1, std::min<long long>(sms / p.tiles_x, units * tiles));
-  p.split = tiles > 1;
+  p.split = tiles > 1;  // (a unit of one tile is in one share)
   p.prow = p.row_tiles == 2 ? 2 * kTM : (std::min(kTM, max_nodes * G) + 31) / 32 * 32;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   if (p.split) {
@@ -996,8 +1139,8 @@ int launch_tree(const TreePlan &p, const CUtensorMap &tq, const CUtensorMap &tk,
     return PA_ERR_CUDA;
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PA_ERR_CUDA;
-  if (fa.numRegs < kTRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
-  int r = launch_dependent(kern, dim3(p.shares * p.tiles_x), kTThreads, L::kAlloc, 1, st, tq, tk, tv, a);
+  if (fa.numRegs < L::kRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
+  int r = launch_dependent(kern, dim3(p.shares * p.tiles_x), L::kThreads, L::kAlloc, 1, st, tq, tk, tv, a);
   if (r == PA_OK && p.split)
     r = launch_dependent(tree_join_kernel<D>, dim3(p.prow / 32, p.shares * p.tiles_x), D * 2, 0, 1, st, a);
   return r;

@@ -115,6 +115,21 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 // Waits for the kernel before this one, and for its writes.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ----------------------------------------------------------- arrival counters
+// Counts one arrival of this call at *c and returns the arrivals so far.  A
+// counter whose epoch tag is not this call's (left by another call or holding
+// stale data) restarts at 1, so the workspace needs no zero-fill.
+__device__ __forceinline__ unsigned int arrive_count(unsigned long long *c, unsigned int epoch) {
+  const unsigned long long tag = (unsigned long long)epoch << 32;
+  unsigned long long old = atomicAdd(c, 0ull), prev;
+  for (;;) {
+    const unsigned long long nv = ((old >> 32) == epoch) ? old + 1 : (tag | 1ull);
+    prev = atomicCAS(c, old, nv);
+    if (prev == old) return (unsigned int)(nv & 0xffffffffull);
+    old = prev;
+  }
+}
+
 // ----------------------------------------------------------------- clusters
 // Barrier of every thread of the cluster that has not exited, in two halves:
 // writes before the arrival are seen behind the wait.

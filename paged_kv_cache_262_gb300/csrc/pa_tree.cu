@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "pa_internal.h"
+#include "pa_ptx.cuh"
 #include "pa_tree.cuh"
 #include "pagedattn.h"
 
@@ -34,63 +35,177 @@ struct VerifyArgs {
   const int32_t *tokens, *parents, *cu;
   int32_t *targets, *path, *path_lens, *next;
   int32_t *err;
-  int S, V, max_nodes, total;
+  int S, V, max_nodes, total, parts;
 };
 
 constexpr int kVThreads = 256;
+constexpr int kVLoads = 8;     // 16-byte loads of a thread on their way
+constexpr int kVMaxParts = 8;  // of a row
 
-// grid (node, sequence): the node's target.
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float logit(const __nv_bfloat16 *, const uint4 &v, int e) {
+  const uint32_t w = (&v.x)[e >> 1];
+  return e & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+__device__ __forceinline__ float logit(const float *, const uint4 &v, int e) { return __uint_as_float((&v.x)[e]); }
+
+// grid (part of a row, node, sequence), the parts of a row a cluster: the node's
+// target.  A maximum over the tokens is a running one that few values change, so a
+// warp takes that of a batch of 16-byte words first (packed, for bf16) and looks
+// closer, for the token, only where a batch is not at or below what it has: each
+// of its later words lies behind all of its earlier ones, so an equal value there
+// is no better.  (Every thread by its own running maximum instead: 32 of them
+// disagree so often that 426 MB took 137 us.)
+//
+// The bytes bind: FIGURE.
 template <class T>
 __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
-  const int i = blockIdx.x, s = blockIdx.y;
+  constexpr int E = 16 / sizeof(T);
+  __shared__ unsigned long long best_w[kVThreads / 32];
+  __shared__ uint32_t best_p[kVMaxParts][2];  // of the cluster's parts, in its first CTA
+  grid_wait();
+  grid_launch_dependents();
+  const int i = blockIdx.y, s = blockIdx.z, part = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
   if (r.bad || i >= r.count) return;
-  const T *x = static_cast<const T *>(a.logits) + (size_t)(r.first + i) * a.stride;
-  unsigned long long best = 0;
-  for (int v = threadIdx.x; v < a.V; v += kVThreads) {
-    const unsigned long long k = rank_of((float)x[v], v);
+  const T *row = static_cast<const T *>(a.logits) + (size_t)(r.first + i) * a.stride;
+  // this CTA's logits: 16-byte words of the row, and (part 0) the elements before the first, (the last) behind the last
+  const int head = min(a.V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
+  const int words = (a.V - head) / E;
+  const int w0 = (int)((long long)words * part / a.parts), w1 = (int)((long long)words * (part + 1) / a.parts);
+  const uint4 *vec = reinterpret_cast<const uint4 *>(row + head);
+  unsigned long long best = 0;  // below every logit's rank
+  float top = -INFINITY;        // the warp's best logit so far
+  bool some = false, nan = false;
+  auto one = [&](float x, int v) {
+    const unsigned long long k = rank_of(x, v);
+    best = k > best ? k : best;
+  };
+  auto largest = [&](const uint4 &w) {
+    if constexpr (E == 8) {
+      const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
+      const __nv_bfloat162 y = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+      return max_nan(__low2float(y), __high2float(y));
+    } else {
+      return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
+  };
+  // words at, at + kVThreads, ... of this thread, `n` of them there (the warp's lanes together)
+  auto batch = [&](const uint4 (&w)[kVLoads], int at, int n) {
+    float m[kVLoads], most = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kVLoads; ++u) {
+      m[u] = u < n ? largest(w[u]) : -INFINITY;
+      most = max_nan(most, m[u]);
+    }
+    if (!__any_sync(0xffffffffu, n > 0 && (!some || !(most <= top)))) return;
+#pragma unroll
+    for (int u = 0; u < kVLoads; ++u)
+      if (u < n && (!some || !(m[u] <= top))) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) one(logit(row, w[u], e), head + (at + u * kVThreads) * E + e);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    top = max_nan(top, most);
+    some = true;
+    nan = top != top;  // (nothing behind the first NaN is better)
+  };
+  if (part == 0 && tid < head) one((float)row[tid], tid);
+  int at = w0 + warp * 32;  // the warp's first word
+  for (; at + 31 + (kVLoads - 1) * kVThreads < w1 && !nan; at += kVLoads * kVThreads) {
+    uint4 w[kVLoads];
+#pragma unroll
+    for (int u = 0; u < kVLoads; ++u) w[u] = __ldcs(vec + at + lane + u * kVThreads);
+    batch(w, at + lane, kVLoads);
+  }
+  for (; at < w1 && !nan; at += kVLoads * kVThreads) {
+    uint4 w[kVLoads];
+    const int left = w1 - at - lane, n = left <= 0 ? 0 : min(kVLoads, (left + kVThreads - 1) / kVThreads);
+#pragma unroll
+    for (int u = 0; u < kVLoads; ++u) w[u] = u < n ? __ldcs(vec + at + lane + u * kVThreads) : make_uint4(0u, 0u, 0u, 0u);
+    batch(w, at + lane, n);
+  }
+  const int tail = head + words * E + tid;
+  if (part == a.parts - 1 && tail < a.V) one((float)row[tail], tail);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
     best = k > best ? k : best;
   }
-  __shared__ unsigned long long red[kVThreads];
-  red[threadIdx.x] = best;
+  if (lane == 0) best_w[warp] = best;
   __syncthreads();
-  for (int o = kVThreads / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o && red[threadIdx.x + o] > red[threadIdx.x]) red[threadIdx.x] = red[threadIdx.x + o];
-    __syncthreads();
+  if (tid == 0) {
+#pragma unroll
+    for (int w = 1; w < kVThreads / 32; ++w) best = best_w[w] > best ? best_w[w] : best;
+    if (a.parts > 1) {
+      const uint32_t to = cluster_addr(smem_u32(&best_p[part][0]), 0);
+      cluster_store(to, (uint32_t)best);
+      cluster_store(to + 4, (uint32_t)(best >> 32));
+    }
   }
-  if (threadIdx.x == 0) a.targets[r.first + i] = (int32_t)~(unsigned int)red[0];
+  if (a.parts > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (part > 0) return;
+    if (tid == 0)
+      for (int p = 0; p < a.parts; ++p) {
+        const unsigned long long k = (unsigned long long)best_p[p][1] << 32 | best_p[p][0];
+        best = k > best ? k : best;
+      }
+  }
+  if (tid == 0) a.targets[r.first + i] = (int32_t)~(unsigned int)best;
 }
 
-// One warp a sequence: the walk.
-__global__ void __launch_bounds__(32) walk_kernel(const VerifyArgs a) {
-  const int s = blockIdx.x, lane = threadIdx.x;
+// One CTA a sequence: the walk, by one warp in shared memory.
+__global__ void __launch_bounds__(PA_MAX_TREE_NODES) walk_kernel(const VerifyArgs a) {
+  __shared__ int32_t par[PA_MAX_TREE_NODES], tok[PA_MAX_TREE_NODES], tgt[PA_MAX_TREE_NODES];
+  const int s = blockIdx.x, k = threadIdx.x, lane = k & 31;
+  grid_wait();  // the targets are there (and what the caller's own kernels wrote)
+  grid_launch_dependents();
   const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
-  if (r.bad && lane == 0 && a.err) atomicOr(a.err, PA_DEVERR_TREE);
-  const int T = r.bad ? 0 : r.count;
-  int32_t *path = a.path + (size_t)s * a.max_nodes;
-  bool bad = false;
-  for (int i = lane; i < T; i += 32) bad |= !good_parent(i, a.parents[r.first + i]);
+  const int n = r.bad ? 0 : r.count;
+  bool bad = r.bad;
+  if (k < n) {
+    tgt[k] = a.targets[r.first + k];
+    par[k] = __ldg(a.parents + r.first + k);
+    tok[k] = __ldg(a.tokens + r.first + k);
+    bad = !good_parent(k, par[k]);
+  }
   if (bad && a.err) atomicOr(a.err, PA_DEVERR_TREE);
-  int n = 0, next = -1;
-  int node = T > 0 && a.parents[r.first] == -1 ? 0 : -1;
+  __syncthreads();
+  if (k >= 32) return;
+  int32_t *path = a.path + (size_t)s * a.max_nodes;
+  int len = 0, next = -1, node = n > 0 && par[0] == -1 ? 0 : -1;
   while (node >= 0) {
-    if (lane == 0) path[n] = node;
-    ++n;
-    next = a.targets[r.first + node];
+    if (lane == 0) path[len] = node;
+    ++len;
+    next = tgt[node];
     int found = -1;
-    for (int base = node + 1; base < T && found < 0; base += 32) {
-      const int i = base + lane;
-      const unsigned fits = __ballot_sync(
-          0xffffffffu, i < T && a.parents[r.first + i] == node && a.tokens[r.first + i] == next);
+    for (int base = node + 1; base < n && found < 0; base += 32) {
+      const int c = base + lane;
+      const unsigned fits = __ballot_sync(0xffffffffu, c < n && par[c] == node && tok[c] == next);
       if (fits) found = base + __ffs(fits) - 1;
     }
     node = found;
   }
-  for (int i = n + lane; i < a.max_nodes; i += 32) path[i] = -1;
+  for (int c = len + lane; c < a.max_nodes; c += 32) path[c] = -1;
   if (lane == 0) {
-    a.path_lens[s] = n;
+    a.path_lens[s] = len;
     a.next[s] = next;
   }
+}
+
+// Parts of a row: CTAs for a few waves, of 2048 logits at least, in one cluster.
+int verify_parts(int num_seqs, int max_nodes, int vocab, int sms) {
+  const long long rows = std::max<long long>(1, (long long)num_seqs * max_nodes);
+  const long long want = (8ll * std::max(sms, 1) + rows - 1) / rows;
+  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, kVMaxParts), vocab / 2048));
 }
 
 constexpr int kCommitLayers = 128;  // layers per launch (kernel-parameter space)
@@ -101,49 +216,73 @@ struct CommitArgs {
   int32_t *new_lens;
   int32_t *err;
   int Hkv, B, C, num_blocks, max_blocks, max_ctx, max_path;
-  int first;  // the launch that reports and writes new_lens
+  int layers, pools;  // of the launch, and of a CTA
+  int first;          // the launch that reports and writes new_lens
 };
 
-constexpr int kCThreads = 128;
+constexpr int kCThreads = 256;
+constexpr int kCRows = 8;  // rows of a thread on their way
+static_assert(kCThreads >= PA_MAX_TREE_NODES, "a thread a path entry");
 
-// grid (sequence, layer, K|V).  path[i] >= i, so a row's source lies at or
-// behind its destination, and rows moved in order never meet one that is
-// still to be read.
+// grid (group of pools, sequence): the rows that move, then every 16-byte column
+// of the group's pools.  path[i] >= i, so a row's source lies at or behind its
+// destination, and rows moved in order never meet one that is still to be read.
 __global__ void __launch_bounds__(kCThreads) commit_kernel(const __grid_constant__ CommitArgs a) {
-  __shared__ int src[PA_MAX_TREE_NODES];
-  const int s = blockIdx.x, tid = threadIdx.x;
-  const bool told = a.first && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0;
-  const int c = __ldg(a.ctx + s), n = __ldg(a.path_lens + s);
-  int why = c < 0 || n < 0 || n > a.max_path ? PA_DEVERR_CTX : 0;
-  const int limit = min(a.max_ctx, a.max_blocks * a.B);
+  __shared__ int64_t from[PA_MAX_TREE_NODES], to[PA_MAX_TREE_NODES];  // offsets of the moved rows, head 0
+  __shared__ int counts[kCThreads / 32];
+  grid_wait();
+  grid_launch_dependents();
+  const int s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool told = a.first && blockIdx.x == 0;
   const int32_t *path = a.path + (size_t)s * a.max_path;
-  bool bad = false;
-  if (!why)
-    for (int i = tid; i < n; i += kCThreads) {
-      const int p = __ldg(path + i), before = i > 0 ? __ldg(path + i - 1) : -1;
-      src[i] = p;
-      bad |= p <= before || p < 0 || p >= limit - c;
-    }
-  if (__syncthreads_or(bad)) why = PA_DEVERR_TREE;
-  if (told) {
+  const int c = __ldg(a.ctx + s), n = __ldg(a.path_lens + s);
+  const int p = tid < a.max_path ? __ldg(path + tid) : 0, before = tid > 0 && tid < a.max_path ? __ldg(path + tid - 1) : -1;
+  const bool sound = c >= 0 && n >= 0 && n <= a.max_path;
+  const bool mine = sound && tid < n;
+  const bool bad = mine && (p <= before || p < 0 || p >= min(a.max_ctx, a.max_blocks * a.B) - c);
+  const int why = __syncthreads_or(bad) ? PA_DEVERR_TREE : sound ? 0 : PA_DEVERR_CTX;
+  if (told && tid == 0) {
     a.new_lens[s] = why ? c : c + n;
     if (why && a.err) atomicOr(a.err, why);
   }
   if (why) return;
-  uint4 *pool = blockIdx.z ? a.v[blockIdx.y] : a.k[blockIdx.y];
-  for (int x = tid; x < a.Hkv * a.C; x += kCThreads) {
-    const int h = x / a.C, ch = x - h * a.C;
-    for (int i = 0; i < n; ++i) {
-      if (src[i] == i) continue;
-      const int from = c + src[i], to = c + i;
-      const int fp = __ldg(a.bt + (size_t)s * a.max_blocks + from / a.B);
-      const int tp = __ldg(a.bt + (size_t)s * a.max_blocks + to / a.B);
-      if (fp < 0 || fp >= a.num_blocks || tp < 0 || tp >= a.num_blocks) {
-        if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
-        continue;
-      }
-      pool[(((size_t)tp * a.Hkv + h) * a.B + to % a.B) * a.C + ch] =
-          pool[(((size_t)fp * a.Hkv + h) * a.B + from % a.B) * a.C + ch];
+  bool moves = mine && p != tid;
+  int64_t src = 0, dst = 0;
+  if (moves) {
+    const int32_t *bt = a.bt + (size_t)s * a.max_blocks;
+    const int x = c + p, y = c + tid;
+    const int xp = __ldg(bt + x / a.B), yp = __ldg(bt + y / a.B);
+    if (xp < 0 || xp >= a.num_blocks || yp < 0 || yp >= a.num_blocks) {
+      if (told && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+      moves = false;
+    }
+    src = ((int64_t)xp * a.Hkv * a.B + x % a.B) * a.C;
+    dst = ((int64_t)yp * a.Hkv * a.B + y % a.B) * a.C;
+  }
+  const unsigned b = __ballot_sync(0xffffffffu, moves);
+  if (lane == 0) counts[warp] = __popc(b);
+  __syncthreads();
+  int rows = 0, at = __popc(b & ((1u << lane) - 1u));
+#pragma unroll
+  for (int w = 0; w < kCThreads / 32; ++w) {
+    if (w < warp) at += counts[w];
+    rows += counts[w];
+  }
+  if (moves) from[at] = src, to[at] = dst;
+  __syncthreads();
+  const int cols = a.Hkv * a.C, first = blockIdx.x * a.pools, pools = min(a.pools, 2 * a.layers - first);
+  for (int x = tid; x < pools * cols; x += kCThreads) {
+    const int q = x / cols, rest = x - q * cols, h = rest / a.C, ch = rest - h * a.C;
+    const int which = first + q;  // K pools, then V pools
+    uint4 *pool = (which < a.layers ? a.k[which] : a.v[which - a.layers]) + (int64_t)h * a.B * a.C + ch;
+    for (int i = 0; i < rows; i += kCRows) {
+      uint4 v[kCRows];
+#pragma unroll
+      for (int u = 0; u < kCRows; ++u)
+        if (i + u < rows) v[u] = __ldcg(pool + from[i + u]);
+#pragma unroll
+      for (int u = 0; u < kCRows; ++u)
+        if (i + u < rows) __stcg(pool + to[i + u], v[u]);
     }
   }
 }
@@ -153,15 +292,10 @@ bool valid_verify(int num_seqs, int max_nodes, int vocab) { return num_seqs >= 0
 }  // namespace
 }  // namespace pa
 
-extern "C" size_t pa_verify_tree_workspace_bytes(int num_seqs, int max_tree_nodes, int vocab_size) {
-  return 0;
-}
-
 extern "C" int pa_verify_tree(const void *logits, int logits_type, int64_t logits_stride, int vocab_size,
                               const int32_t *tokens, const int32_t *parents, const int32_t *cu_nodes, int num_seqs,
                               int max_tree_nodes, int total_nodes, int32_t *targets, int32_t *path,
-                              int32_t *path_lens, int32_t *next_tokens, void *workspace, size_t workspace_bytes,
-                              int32_t *err_flag, void *stream) {
+                              int32_t *path_lens, int32_t *next_tokens, int32_t *err_flag, void *stream) {
   using namespace pa;
   if (!valid_verify(num_seqs, max_tree_nodes, vocab_size) || total_nodes < 0 || logits_stride < vocab_size ||
       (logits_type != PA_LOGITS_BF16 && logits_type != PA_LOGITS_F32))
@@ -172,6 +306,8 @@ extern "C" int pa_verify_tree(const void *logits, int logits_type, int64_t logit
       (total_nodes > 0 && (!logits || !tokens || !parents || !targets)))
     return PA_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(logits) % (logits_type == PA_LOGITS_BF16 ? 2 : 4)) return PA_ERR_INVALID;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
   VerifyArgs a{};
   a.logits = logits;
   a.stride = logits_stride;
@@ -187,14 +323,14 @@ extern "C" int pa_verify_tree(const void *logits, int logits_type, int64_t logit
   a.V = vocab_size;
   a.max_nodes = max_tree_nodes;
   a.total = total_nodes;
+  a.parts = verify_parts(num_seqs, max_tree_nodes, vocab_size, sms);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(max_tree_nodes, num_seqs);
-  if (logits_type == PA_LOGITS_BF16)
-    target_kernel<__nv_bfloat16><<<grid, kVThreads, 0, st>>>(a);
-  else
-    target_kernel<float><<<grid, kVThreads, 0, st>>>(a);
-  walk_kernel<<<num_seqs, 32, 0, st>>>(a);
-  return launch_status(cudaGetLastError());
+  if (total_nodes > 0) {
+    auto kern = logits_type == PA_LOGITS_BF16 ? target_kernel<__nv_bfloat16> : target_kernel<float>;
+    const int r = launch_dependent(kern, dim3(a.parts, max_tree_nodes, num_seqs), kVThreads, 0, a.parts, st, a);
+    if (r != PA_OK) return r;
+  }
+  return launch_dependent(walk_kernel, dim3(num_seqs), PA_MAX_TREE_NODES, 0, 1, st, a);
 }
 
 extern "C" int pa_commit_tree(const pa_decode_desc *d, void *const *k_pools, void *const *v_pools, int num_layers,
@@ -214,6 +350,9 @@ extern "C" int pa_commit_tree(const pa_decode_desc *d, void *const *k_pools, voi
   if (!apart(new_lens, S, context_lens, S) || !apart(new_lens, S, path_lens, S) ||
       !apart(new_lens, S, path, S * max_path_len) || !apart(new_lens, S, block_tables, S * d->max_blocks_per_seq))
     return PA_ERR_INVALID;
+  if (d->num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
   CommitArgs a{};
   a.bt = block_tables;
   a.ctx = context_lens;
@@ -235,8 +374,11 @@ extern "C" int pa_commit_tree(const pa_decode_desc *d, void *const *k_pools, voi
       a.v[l] = static_cast<uint4 *>(v_pools[l0 + l]);
     }
     a.first = l0 == 0;
-    commit_kernel<<<dim3(d->num_seqs, nl, 2), kCThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    const int st = launch_status(cudaGetLastError());
+    a.layers = nl;
+    // one wave, of 8 CTAs an SM
+    a.pools = (int)((2ll * nl * d->num_seqs + 8ll * sms - 1) / (8ll * sms));
+    const int st = launch_dependent(commit_kernel, dim3((2 * nl + a.pools - 1) / a.pools, d->num_seqs), kCThreads, 0, 1,
+                                    static_cast<cudaStream_t>(stream), a);
     if (st != PA_OK) return st;
   }
   return PA_OK;

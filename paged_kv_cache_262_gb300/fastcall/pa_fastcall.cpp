@@ -1,4 +1,5 @@
-// The quick way into the long-context calls from Python: one C call checks the
+// The quick way into the long-context calls and those for trees of drafted
+// tokens from Python: one C call checks the
 // tensors, allocates the outputs and calls libpagedattn, in 2-3 us besides the
 // launches, where the same steps in Python take 8-15 us -- more than the
 // kernels of a small step.
@@ -35,6 +36,13 @@ struct Library {
   decltype(&pa_paged_attention_decode_weights) weights;
   decltype(&pa_evict_tokens) evict;
 } lib;
+
+struct TreeLibrary {
+  decltype(&pa_decode_tree_workspace_bytes) tree_bytes;
+  decltype(&pa_paged_attention_decode_tree) tree;
+  decltype(&pa_verify_tree) verify;
+  decltype(&pa_commit_tree) commit;
+} trees;
 
 struct No {};  // not for the quick way
 
@@ -312,6 +320,117 @@ PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+const int32_t *ints(const at::Tensor &t) { return static_cast<const int32_t *>(t.data_ptr()); }
+
+// q, k_pool, v_pool, block_tables, context_lens, cu_nodes, parents, max_tree_nodes, scale, max_context_len, err_flag,
+// workspaces -> out
+PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject * {
+    const Dev dev{c10::cuda::current_device()};
+    const at::Tensor &q = dev(a[0], kBf, 3), &k = dev(a[1], kBf, 4), &v = dev(a[2], kBf, 4), &bt = dev(a[3], kI, 2),
+                     &ctx = dev(a[4], kI, 1), &cu = dev(a[5], kI, 1), &parents = dev(a[6], kI, 1);
+    const int N = size(q, 0), S = size(ctx, 0), B = size(k, 2), D = size(k, 3), most = integer(a[7]);
+    need(v.sizes() == k.sizes() && size(q, 2) == D && D > 0 && size(bt, 0) >= S && size(cu, 0) > S &&
+         size(parents, 0) >= N && most >= 1 && most <= PA_MAX_TREE_NODES && trees.tree);
+    double sc = 1.0 / std::sqrt((double)D);
+    if (a[8] != Py_None) {
+      need(PyFloat_CheckExact(a[8]));
+      sc = PyFloat_AS_DOUBLE(a[8]);
+    }
+    const pa_decode_desc d{S, size(q, 1), size(k, 1), D, B, size(k, 0), size(bt, 1),
+                           integer_or(a[9], (int64_t)size(bt, 1) * B), (float)sc};
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
+    int32_t *err = dev.err(a[10]);
+    const Workspace ws = workspace(a[11], trees.tree_bytes(&d, most), dev.index, st);
+    at::Tensor out = fresh(q.sizes(), kBf, dev.index);
+    Ref r(THPVariable_Wrap(out));
+    return r.after(trees.tree(&d, q.data_ptr(), k.data_ptr(), v.data_ptr(), ints(bt), ints(ctx), ints(cu), ints(parents),
+                              most, N, out.data_ptr(), ws.p, ws.bytes, err, st),
+                   "pa_paged_attention_decode_tree");
+  });
+}
+
+// logits, tokens, parents, cu_nodes, max_tree_nodes, err_flag -> (targets, path, path_lens, next_tokens)
+PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject * {
+    const Dev dev{c10::cuda::current_device()};
+    need(THPVariable_CheckExact(a[0]));
+    const at::Tensor &x = THPVariable_Unpack(a[0]);
+    need(x.is_cuda() && x.get_device() == dev.index && x.dim() == 2 && !x.requires_grad() &&
+         (x.scalar_type() == kBf || x.scalar_type() == kF));
+    need(x.size(0) <= INT_MAX && x.size(1) >= 1 && x.size(1) <= INT_MAX && (x.size(1) == 1 || x.stride(1) == 1));
+    const int N = size(x, 0), V = size(x, 1), most = integer(a[4]);
+    const int64_t stride = N > 1 ? x.stride(0) : V;
+    const at::Tensor &tokens = dev(a[1], kI, 1), &parents = dev(a[2], kI, 1), &cu = dev(a[3], kI, 1);
+    need(stride >= V && size(tokens, 0) >= N && size(parents, 0) >= N && size(cu, 0) >= 1 && most >= 1 &&
+         most <= PA_MAX_TREE_NODES && trees.verify);
+    const int S = size(cu, 0) - 1;
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
+    int32_t *err = dev.err(a[5]);
+    at::Tensor out[4] = {fresh({N}, kI, dev.index), fresh({S, most}, kI, dev.index), fresh({S}, kI, dev.index),
+                         fresh({S}, kI, dev.index)};
+    Ref t_(THPVariable_Wrap(out[0])), p_(THPVariable_Wrap(out[1])), l_(THPVariable_Wrap(out[2])),
+        n_(THPVariable_Wrap(out[3])), r(PyTuple_Pack(4, t_.p, p_.p, l_.p, n_.p));
+    auto to = [&](int i) { return static_cast<int32_t *>(out[i].data_ptr()); };
+    return r.after(trees.verify(x.data_ptr(), x.scalar_type() == kF ? PA_LOGITS_F32 : PA_LOGITS_BF16, stride, V,
+                                ints(tokens), ints(parents), ints(cu), S, most, N, to(0), to(1), to(2), to(3), err, st),
+                   "pa_verify_tree");
+  });
+}
+
+// k_pools, v_pools (lists), block_tables, context_lens, path, path_lens, max_context_len, err_flag -> new_lens
+PyObject *commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject * {
+    const Dev dev{c10::cuda::current_device()};
+    constexpr int kMost = 256;  // layers of a call
+    void *pools[2][kMost];
+    int L = 0;
+    const at::Tensor *k = nullptr;
+    for (int w = 0; w < 2; ++w) {
+      need(PyList_CheckExact(a[w]));
+      const Py_ssize_t len = PyList_GET_SIZE(a[w]);
+      need(len >= 1 && len <= kMost && (w == 0 || len == L));
+      L = (int)len;
+      for (int l = 0; l < L; ++l) {
+        const at::Tensor &t = dev(PyList_GET_ITEM(a[w], l), kBf, 4);
+        if (!k) k = &t;
+        need(t.sizes() == k->sizes());
+        pools[w][l] = t.data_ptr();
+      }
+    }
+    const at::Tensor &bt = dev(a[2], kI, 2), &ctx = dev(a[3], kI, 1), &path = dev(a[4], kI, 2), &lens = dev(a[5], kI, 1);
+    const int S = size(ctx, 0), Hkv = size(*k, 1), B = size(*k, 2);
+    need(size(bt, 0) >= S && size(path, 0) >= S && size(lens, 0) >= S && trees.commit);
+    const pa_decode_desc d{S, Hkv, Hkv, size(*k, 3), B, size(*k, 0), size(bt, 1),
+                           integer_or(a[6], (int64_t)size(bt, 1) * B), 1.f};
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
+    int32_t *err = dev.err(a[7]);
+    at::Tensor out = fresh({S}, kI, dev.index);
+    Ref r(THPVariable_Wrap(out));
+    return r.after(trees.commit(&d, pools[0], pools[1], L, ints(bt), ints(ctx), ints(path), ints(lens), size(path, 1),
+                                static_cast<int32_t *>(out.data_ptr()), err, st),
+                   "pa_commit_tree");
+  });
+}
+
+// bind_trees(addresses of the library's calls, in the order of TreeLibrary)
+PyObject *bind_trees(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  void *p[4];
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "bind_trees takes 4 addresses");
+    return nullptr;
+  }
+  for (int i = 0; i < 4; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  trees.tree_bytes = reinterpret_cast<decltype(trees.tree_bytes)>(p[0]);
+  trees.tree = reinterpret_cast<decltype(trees.tree)>(p[1]);
+  trees.verify = reinterpret_cast<decltype(trees.verify)>(p[2]);
+  trees.commit = reinterpret_cast<decltype(trees.commit)>(p[3]);
+  Py_RETURN_NONE;
+}
+
 // bind(addresses of the library's calls, in the order of Library)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   void *p[8];
@@ -336,7 +455,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define PA_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_FAST(bounds),  PA_FAST(select), PA_FAST(sparse), PA_FAST(weights),
-                         PA_FAST(evict),   PA_FAST(bind),   {nullptr, nullptr, 0, nullptr}};
+                         PA_FAST(evict),   PA_FAST(bind),   PA_FAST(tree),   PA_FAST(verify),
+                         PA_FAST(commit),  PA_FAST(bind_trees), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_pa_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -59,9 +59,9 @@ def test_attention_arguments(lib):
 
 
 def verify(lib, logits=P, kind=0, stride=100, V=100, tokens=P, parents=P, cu=P, S=2, most=8, total=10, targets=P,
-           path=P, lens=P, nexts=P, ws=None, n=0):
+           path=P, lens=P, nexts=P):
     return lib.pa_verify_tree(logits, kind, stride, V, tokens, parents, cu, S, most, total, targets, path, lens, nexts,
-                              ws, n, None, None)
+                              None, None)
 
 
 def test_verify_arguments(lib):
@@ -79,8 +79,6 @@ def test_verify_arguments(lib):
     assert verify(lib, logits=P + 2, kind=1) == pa.PA_ERR_INVALID
     none = dict(logits=None, tokens=None, parents=None, cu=None, targets=None, path=None, lens=None, nexts=None)
     assert verify(lib, S=0, **none) == pa.PA_OK
-    for bad in ((-1, 8, 100), (2, 0, 100), (2, 8, 0), (2, 257, 100)):
-        assert lib.pa_verify_tree_workspace_bytes(*bad) == 0
 
 
 def commit(lib, d, k=(P,), v=(P,), L=1, bt=P, ctx=P, path=P, lens=P, most=8, new=1 << 20):
