@@ -33,11 +33,12 @@
 //               (in the softmax warps' hands it held up everything for up to 7000
 //               cycles a piece; a key tile takes 2500).  Two row tiles, whose pieces
 //               are long: the softmax warps' own.
-// MMAs issued by one thread complete in order.  Where the bytes bind, with one row
-// tile, the probabilities are kept as a bf16 value and a bf16 remainder (2^-16 of
-// them left) in two products, which the tensor cores have the time for; with two
-// tiles they are rounded to bf16 once.  The running maximum moves
-// only when it grows by more than 8 (2^8), so O is seldom rescaled.
+// MMAs issued by one thread complete in order.  The probabilities are rounded to
+// bf16 once, as in the decode and prefill kernels (error against 64 bits 0.0023 of
+// the norm, 0.0017 of which is the output's own rounding): kept in two terms, with
+// a second product each, they made the tensor cores as busy as HBM (32 x 16..32
+// nodes 106 us, 94 so).  The running maximum moves only when it grows by more than 8 (2^8), so O is
+// seldom rescaled.
 //
 // Only tiles at and behind the context's end, or with a page outside the pool, are
 // masked.  There a key's value row meets a probability of 0 in the rows that do
@@ -85,7 +86,7 @@ constexpr int kTVotes = 4;               // tiles with a tree under way at once
 constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTChecker = 11, kTEnd = 12;  // warps
 // A unit counts as so many key tiles more than it has when the shares are cut:
 // what its pieces cost besides (64 x 5 nodes: FIGURE).
-constexpr int kTUnitCost = 1;
+constexpr int kTUnitCost = 3;
 
 template <int D, bool ROWS2>
 struct TreeSmem {
@@ -109,8 +110,8 @@ struct TreeSmem {
   static constexpr int kOffPages = kOffPost + kTPosts * kTPostWords * 4;  // [2][8] valid pages of the latest K, V tiles
   static constexpr int kOffBad = kOffPages + 2 * 8 * 4;                   // [votes][4] keys of a tile that are not finite
   static constexpr int kOffScan = (kOffBad + kTVotes * 16 + 7) & ~7;      // [16] sums of the warps
-  static constexpr int kOffMisc = kOffScan + 16 * 8;                      // TMEM address, dead, first sequence, its tiles' offset
-  static constexpr int kBytes = kOffMisc + 24;
+  static constexpr int kOffMisc = kOffScan + 16 * 8;                      // TMEM address, dead, first sequence, its tiles' offset, O put by hand [2]
+  static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
@@ -146,26 +147,23 @@ __device__ __forceinline__ uint32_t bits_below(int n, int word) {
 }
 
 // P of one row: 2^(x - base) for KN scores x = s * sc, as bf16 pairs into TMEM
-// columns [col, col + KN / 2) and, FINE, what that rounding leaves into the KN / 2
-// behind; their sum, unrounded.
-template <bool FINE, int KN>
+// columns [col, col + KN / 2); their sum, unrounded.
+template <int KN>
 __device__ __forceinline__ float tree_probabilities(const float (&s)[KN], float sc, float base, uint32_t col) {
   const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < KN / 32; ++c) {
-    uint32_t hi[16], lo[16];
+    uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int k = c * 32 + 2 * e;
       const float2 t = fma2(make_float2(s[k], s[k + 1]), sc2, nb2);
       const float2 p = make_float2(ex2_ftz(t.x), ex2_ftz(t.y));
-      hi[e] = pack_bf16(p.x, p.y);
-      if constexpr (FINE) lo[e] = pack_bf16(p.x - bf16_lo(hi[e]), p.y - bf16_hi(hi[e]));
+      w[e] = pack_bf16(p.x, p.y);
       acc[e & 3] = add2(acc[e & 3], p);
     }
-    tmem_st16(col + c * 16, hi);
-    if constexpr (FINE) tmem_st16(col + KN / 2 + c * 16, lo);
+    tmem_st16(col + c * 16, w);
   }
   const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
   return x.x + x.y;
@@ -214,7 +212,6 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
   using L = TreeSmem<D, ROWS2>;
-  constexpr bool FINE = !ROWS2;
   constexpr int kHalves = D / 64, PAGES = kTN / B, NS = L::kSlots, kThreads = L::kThreads;
   constexpr int kGroup = kHalves * 1024;  // 8 keys of a K or V tile: 8 x 128 bytes of each half
   constexpr uint32_t kAllPages = (1u << PAGES) - 1u;
@@ -232,11 +229,17 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
   volatile uint32_t *bad_of = reinterpret_cast<uint32_t *>(smem + L::kOffBad);
   long long *scan = reinterpret_cast<long long *>(smem + L::kOffScan);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+  volatile int *put_of = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 24);
   volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 4);
   int *start_s = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
   long long *start_off = reinterpret_cast<long long *>(smem + L::kOffMisc + 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (warp == kTProducerV && lane == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bars[L::kFull + i], 1);
@@ -493,13 +496,13 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         if ((i & 1) == kv) mbar_wait(&bars[L::kFull + i % NS], (uint32_t)((i / NS) & 1));
     } else if (warp == kTIssuer && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
-      int u = 0, qn = 0, item = 0, n = 0, n1 = 0;  // n, n1: key tiles (of the row tiles)
+      int u = 0, qn = 0, item = 0, n = 0, n1 = 0, votes = 0;  // n, n1: key tiles (of the row tiles)
       bool ok = true;
       while (ok) {
         const int pb = u % kTPosts;
         if (!wait(L::kUFull + pb, (uint32_t)((u / kTPosts) & 1))) break;
         const int *p = posts + pb * kTPostWords;
-        const int kind = p[PP_KIND], nt = p[PP_TILES], live = p[PP_LIVE];
+        const int kind = p[PP_KIND], nt = p[PP_TILES], live = p[PP_LIVE], tree0 = p[PP_CTX] / kTN - p[PP_TILE];
         if (kind == kPieceStop) break;
         ++u;
         if (kind == kPieceZero) {
@@ -522,16 +525,20 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         auto issue_pv = [&](int x, int j, int buf) {  // O of warpgroup x += P V
           const uint32_t vb = ring + (item + 2 * j + 1) % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
           const uint32_t pc = tmem + buf * 128 + (ROWS2 ? 0 : x * 64);
+          const bool put = j == 0 && put_of[x];  // the first product adds to what is there
 #pragma unroll
-          for (int f = 0; f < (FINE ? 2 : 1); ++f)
-#pragma unroll
-            for (int kk = 0; kk < KN / 16; ++kk)
-              umma_bf16_ts(tmem + kColO + x * 128, pc + f * (KN / 2) + kk * 8,
-                           umma_desc_sw128(vb + kk * 2 * kGroup, 1024, kGroup), kIdPV, 1u);
+          for (int kk = 0; kk < KN / 16; ++kk)
+            umma_bf16_ts(tmem + kColO + x * 128, pc + kk * 8, umma_desc_sw128(vb + kk * 2 * kGroup, 1024, kGroup),
+                         kIdPV, j > 0 || kk > 0 || put);
         };
         auto full = [&](int i) {
           if (!wait(L::kFull + i % NS, (uint32_t)((i / NS) & 1))) return false;
           tc_fence_after();
+          return true;
+        };
+        auto key_tile = [&](int j) {  // its K tile is there; one with a tree: to the checking warp
+          if (!full(item + 2 * j)) return false;
+          if (j >= tree0) mbar_arrive(&bars[L::kKick + votes++ % kTVotes]);
           return true;
         };
         auto written = [&](int b, uint32_t parity) {  // P
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         };
         auto release = [&](int i) { umma_commit(&bars[L::kEmpty + (item + i) % NS]); };
         if constexpr (ROWS2) {
-          if ((ok = full(item))) {
+          if ((ok = key_tile(0))) {
             issue_s(0, 0, 0);
             if (live > 1) issue_s(L::kTile, 0, 1);
             release(0);
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             issue_pv(0, j, 0);
             umma_commit(&bars[L::kPV]);
             if (more) {
-              if (!(ok = full(item + 2 * j + 2))) break;
+              if (!(ok = key_tile(j + 1))) break;
               issue_s(0, j + 1, 0);
             }
             if (live > 1) {
@@ -567,26 +574,33 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             }
           }
         } else {
-          if ((ok = full(item))) {
-            issue_s(0, 0, n & 1);
-            release(0);
-          }
-          for (int j = 0; ok && j < nt; ++j, ++n) {
-            const int buf = n & 1;
-            if (j + 1 < nt) {
-              if (!(ok = full(item + 2 * j + 2))) break;
-              issue_s(0, j + 1, buf ^ 1);
-              release(2 * j + 2);
+          // S of up to one key tile more than P V, whichever can go first: a P V that waited for the
+          // next K tile would keep its V tile's slot from the loads (32 x 16..32 nodes: FIGURE)
+          int js = 0, jp = 0;
+          long long t0 = clock64();
+          while (ok && jp < nt) {
+            const int ks = item + 2 * js, vs = item + 2 * jp + 1, bp = (n + jp) & 1;
+            if (js < nt && js <= jp + 1 && mbar_test(&bars[L::kFull + ks % NS], (uint32_t)((ks / NS) & 1))) {
+              ok = key_tile(js);
+              issue_s(0, js, (n + js) & 1);
+              release(2 * js++);
+            } else if (jp < js && mbar_test(&bars[L::kPFull + bp], (uint32_t)(((n + jp) >> 1) & 1)) &&
+                       mbar_test(&bars[L::kFull + vs % NS], (uint32_t)((vs / NS) & 1)) &&
+                       (jp > 0 || mbar_test(&bars[L::kOFree], (uint32_t)((qn - 1) & 1)))) {
+              tc_fence_after();
+              issue_pv(0, jp, bp);
+              issue_pv(1, jp, bp);
+              release(2 * jp++ + 1);
+              umma_commit(&bars[L::kPV + bp]);
+            } else if (*dead || clock64() - t0 > kWaitLimitCycles) {
+              ok = false;
+              if (!*dead) fail();
+            } else {
+              continue;
             }
-            if (!(ok = full(item + 2 * j + 1) && written(buf, (uint32_t)((n >> 1) & 1)) &&
-                       (j > 0 || wait(L::kOFree, (uint32_t)((qn - 1) & 1)))))
-              break;
-            tc_fence_after();
-            issue_pv(0, j, buf);
-            issue_pv(1, j, buf);
-            release(2 * j + 1);
-            umma_commit(&bars[L::kPV + buf]);
+            t0 = clock64();
           }
+          n += nt;
         }
         item += 2 * nt;
         mbar_arrive(&bars[L::kUEmpty + pb]);
@@ -594,7 +608,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       umma_commit(&bars[L::kDone]);
       mbar_wait(&bars[L::kDone], 0);  // every MMA complete before TMEM is freed
     } else if (warp == kTChecker) {
-      // ------------- value rows of the tiles with a tree, once their scores are there
+      // ------------- value rows of the tiles with a tree
       int u = 0, jall = 0, votes = 0;
       while (true) {
         const int pb = u % kTPosts;
@@ -609,14 +623,19 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         bool ok = true;
         for (int t = max(t0, c / kTN); ok && t < t0 + nt; ++t, ++votes) {
           const int tile = jall + t - t0, item = 2 * tile + 1, key0 = t * kTN;
-          // (what is behind the scores' barrier has left the V tile's slot to it)
+          // (the issuer has seen the K tile: the V tile's slot has nothing before it to wait for)
           if (!(ok = wait_warp(L::kKick + votes % kTVotes, (uint32_t)((votes / kTVotes) & 1)) &&
                      wait_warp(L::kFull + item % NS, (uint32_t)((item / NS) & 1))))
             break;
           const uint32_t pages = pages_of[8 + (tile & 7)];
           uint8_t *vt = smem + L::kOffRing + item % NS * L::kTile;
+#pragma unroll 1
           for (int g = 0; g < kTN / 32; ++g) {
             const int r = g * 32 + lane;
+            if (key0 + g * 32 + 31 < c && pages == kAllPages) {  // the context's
+              if (lane == 0) bad_of[votes % kTVotes * 4 + g] = 0;
+              continue;
+            }
             uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
             bool odd = false;
             if (key0 + r >= c + T || !((pages >> (r / B)) & 1u)) {  // no row attends it
@@ -648,20 +667,11 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       const uint32_t lane_base = tmem + ((uint32_t)(w * 32) << 16);
       const int nl = m / a.G;
       int u = 0, qn = 0, jall = 0;
-      auto clear = [&]() {  // both states, for the next piece
-        uint32_t z[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = 0u;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          tmem_st16(lane_base + kColO + i * 16, z);
-          tmem_st16(lane_base + kColO + 128 + i * 16, z);
-        }
-        tmem_wait_st();
+      auto release = [&]() {  // both states have been read
         tc_fence_before();
         mbar_arrive(&bars[L::kOFree]);
       };
-      clear();
+      release();
       while (true) {
         const int pb = u % kTPosts;
         if (!wait_warp(L::kUFull + pb, (uint32_t)((u / kTPosts) & 1))) break;
@@ -693,55 +703,55 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         const float b0 = M == -INFINITY ? 0.f : M;
         float f0 = s0.y != 0.f ? exp2f(s0.x - b0) : 0.f, f1 = s1.y != 0.f ? exp2f(s1.x - b0) : 0.f;
         const float l = s0.y * f0 + s1.y * f1;
-        auto values = [&](int i, float (&v)[16]) {  // 16 i .. 16 i + 15, of both states
-          uint32_t p0[16], p1[16];
-          tmem_ld16(lane_base + kColO + i * 16, p0);
-          tmem_ld16(lane_base + kColO + 128 + i * 16, p1);
+        auto values = [&](int i, float (&v)[32]) {  // 32 i .. 32 i + 31, of both states
+          uint32_t p0[32], p1[32];
+          tmem_ld32(lane_base + kColO + i * 32, p0);
+          tmem_ld32(lane_base + kColO + 128 + i * 32, p1);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(p0[e]) * f0 + __uint_as_float(p1[e]) * f1;
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(p0[e]) * f0 + __uint_as_float(p1[e]) * f1;
         };
         if (some && slot < 0) {
           const bool empty = l == 0.f || refused;  // (a NaN sum is no empty one)
           const float inv = 1.f / l;
           f0 *= inv, f1 *= inv;
           constexpr int RB = D * 2, CH = RB / 16;  // a row's bytes and 16-byte chunks
-#pragma unroll 2
-          for (int i = 0; i < D / 16; ++i) {
-            float v[16];
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            float v[32];
             values(i, v);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 4; ++k) {
               uint4 y = make_uint4(0u, 0u, 0u, 0u);
               if (!empty)
                 y = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
                                pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
-              *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 2 + k) ^ lane) & (CH - 1)) * 16) = y;
+              *reinterpret_cast<uint4 *>(stage + lane * RB + (((i * 4 + k) ^ lane) & (CH - 1)) * 16) = y;
             }
             __syncwarp();
           }
-          clear();
+          release();
           store_rows<D, RB>(a, stage, row_of(a, row0, nl, h, m, valid), 0, lane);
           fence_proxy_async_smem();  // the next queries come by TMA
         } else {
           if (some) {
             const size_t at = (size_t)blockIdx.x * 2 + slot;
             float4 *o = a.ws_o + at * (D / 4) * a.prow + m;
-#pragma unroll 2
-            for (int i = 0; i < D / 16; ++i) {
-              float v[16];
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float v[32];
               values(i, v);
               if (valid) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  o[(size_t)(i * 4 + k) * a.prow] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                for (int k = 0; k < 8; ++k)
+                  o[(size_t)(i * 8 + k) * a.prow] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
               }
               __syncwarp();
             }
             if (valid) a.ws_ml[at * a.prow + m] = make_float2(M, refused ? -1.f : l);
             __syncwarp();
           }
-          clear();
+          release();
           fence_proxy_async_smem();
         }
         mbar_arrive(&bars[L::kQEmpty + set]);
@@ -792,13 +802,6 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       if (valid && last)  // the chains to be walked behind the last key tile
         asm volatile("prefetch.global.L1 [%0];" ::"l"(a.parents + first + node));
       __syncwarp();
-      if (ROWS2 && some) {
-        uint32_t z[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = 0u;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) tmem_st16(lane_base + o_col + i * 16, z);
-      }
       float m_run = -INFINITY, l_run = 0.f;
       bool refused = false;  // known where the piece has the tree's last key tile
       for (int j = 0; j < nt; ++j, ++jx) {
@@ -829,8 +832,6 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (tree && x == 0 && m == 0) mbar_arrive(&bars[L::kKick + votes % kTVotes]);
-        __syncwarp();
         const uint32_t pages_t = pages_of[(jall + j) & 7];
         const bool masked = tree || pages_t != kAllPages;
         const uint32_t pages = ROWS2 ? pages_t : pages_t >> (x * PAGES / 2);  // of this warpgroup's keys
@@ -875,7 +876,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           const bool grow = valid && m_new > m_run + 8.f;
           const float m_use = grow ? m_new : m_run;
           const float alpha = grow ? exp2f(m_run - m_new) : 1.f;
-          const float lsum = tree_probabilities<FINE>(s, sc, m_use == -INFINITY ? 0.f : m_use, lane_base + s_col);
+          const float lsum = tree_probabilities(s, sc, m_use == -INFINITY ? 0.f : m_use, lane_base + s_col);
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             if (!ROWS2 && !wait_pv(jx - 1)) {  // (two row tiles: S came behind that product)
               ok = false;
@@ -916,22 +917,35 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           }
           const volatile uint32_t *bad = bad_of + votes % kTVotes * 4 + (ROWS2 ? 0 : x * 2);
           ++votes;
-          if (bad[0] | bad[1] | (ROWS2 ? bad[2] | bad[3] : 0u)) {
+          const bool odd = bad[0] | bad[1] | (ROWS2 ? bad[2] | bad[3] : 0u);
+          if (j == 0 && m == 0) put_of[x] = odd;
+          if (odd) {
             // p v added to the rows that attend such a node, then its row cleared
             if (!ROWS2 && !(j > 0 ? wait_pv(jx - 1) : wait_warp(L::kOFree, (uint32_t)((qn - 1) & 1)))) {
               ok = false;
               break;
             }
             tc_fence_after();
+            if (j == 0 && some) {  // the product starts from what is put here, not from nothing
+              uint32_t z[16];
 #pragma unroll
-            for (int w = 0; w < KN / 32; ++w)
+              for (int i = 0; i < 16; ++i) z[i] = 0u;
+#pragma unroll 1
+              for (int i = 0; i < D / 16; ++i) tmem_st16(lane_base + o_col + i * 16, z);
+              tmem_wait_st();
+            }
+#pragma unroll 1
+            for (int w = 0; w < KN / 32; ++w) {
+              uint32_t mine = allow[0];  // (no register array by a running index)
+#pragma unroll
+              for (int i = 1; i < KN / 32; ++i) mine = w == i ? allow[i] : mine;
+#pragma unroll 1
               for (uint32_t todo = some ? bad[w] : 0u; todo; todo &= todo - 1) {
                 const int k = w * 32 + __ffs(todo) - 1;
-                const uint32_t hi = tmem_ld1(lane_base + s_col + (k >> 1));
-                const uint32_t lo = FINE ? tmem_ld1(lane_base + s_col + KN / 2 + (k >> 1)) : 0u;
+                const uint32_t pw = tmem_ld1(lane_base + s_col + (k >> 1));
                 tmem_wait_ld();
-                const float pk = k & 1 ? bf16_hi(hi) + bf16_hi(lo) : bf16_lo(hi) + bf16_lo(lo);
-                const bool attends = (allow[w] >> (k & 31)) & 1u;
+                const float pk = k & 1 ? bf16_hi(pw) : bf16_lo(pw);
+                const bool attends = (mine >> (k & 31)) & 1u;
 #pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
                   uint32_t v[32];
@@ -951,6 +965,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
                 }
                 tmem_wait_st();
               }
+            }
             const int rb = ROWS2 ? live == 1 : x;  // everyone has read them (two row tiles: both warpgroups)
             mbar_arrive(&bars[L::kRead + rb]);
             if (!wait_warp(L::kRead + rb, (uint32_t)(reads[rb]++ & 1))) {
@@ -966,6 +981,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           }
           clear_rows([&](int r) { return !((pages >> (r / B)) & 1u); });
         }
+        if (!tree && j == 0 && m == 0) put_of[x] = 0;
         tc_fence_before();
         mbar_arrive(&bars[L::kPFull + buf]);  // (one row tile: a warp may be at the next key tile while another is here)
       }
@@ -1117,7 +1133,7 @@ TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   p.tiles_x = (max_nodes + p.row_tiles * p.nodes_tile - 1) / (p.row_tiles * p.nodes_tile);
   const long long tiles = std::max<long long>(1, ((long long)d->max_context_len + kTN - 1) / kTN);
   const long long units = std::max<long long>(1, (long long)d->num_seqs * d->num_kv_heads);
-  p.shares = (int)std::max<long long>(1, std::min<long long>(sms / p.tiles_x, units * tiles));
+  p.shares = (int)std::max<long long>(1, std::min<long long>(sms / p.tiles_x, units * (tiles + kTUnitCost)));
   p.split = tiles > 1;  // (a unit of one tile is in one share)
   p.prow = p.row_tiles == 2 ? 2 * kTM : (std::min(kTM, max_nodes * G) + 31) / 32 * 32;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
