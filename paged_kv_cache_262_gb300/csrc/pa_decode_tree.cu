@@ -93,8 +93,10 @@ struct TreeSmem {
   static constexpr int kThreads = ROWS2 ? 384 : 512;
   // Register split (setmaxnreg): the softmax warpgroups take what the others give
   // back.  The sum is within the launch's threads x kRegsLaunch, which the host
-  // checks before every launch (a larger sum would wait forever).
-  static constexpr int kRegsLaunch = ROWS2 ? 168 : 128, kRegsSoftmax = ROWS2 ? 216 : 152, kRegsOther = ROWS2 ? 72 : 104;
+  // checks before every launch (a larger sum would wait forever).  What the issuer
+  // and the producers spill stands in everyone's way: two row tiles with 72 registers
+  // for them 454 us at 8 x 64 nodes over 32K tokens, with 120 422.
+  static constexpr int kRegsLaunch = ROWS2 ? 168 : 128, kRegsSoftmax = ROWS2 ? 192 : 152, kRegsOther = ROWS2 ? 120 : 104;
   static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register split");
   static constexpr int kTile = D / 64 * kTHalf;          // 128 rows
   static constexpr int kSets = ROWS2 ? 1 : 2;            // of query rows
@@ -247,23 +249,23 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[L::kSFull + i], 2);
-      mbar_init(&bars[L::kPFull + i], ROWS2 ? 128 : 256);
+      mbar_init(&bars[L::kPFull + i], ROWS2 ? 4 : 8);  // (an arrival a warp)
       mbar_init(&bars[L::kPV + i], 1);
       mbar_init(&bars[L::kQFull + i], 1);
-      mbar_init(&bars[L::kQEmpty + i], ROWS2 ? 256 : 128);
-      mbar_init(&bars[L::kRead + i], ROWS2 && i == 0 ? 256 : 128);
+      mbar_init(&bars[L::kQEmpty + i], ROWS2 ? 8 : 4);
+      mbar_init(&bars[L::kRead + i], ROWS2 && i == 0 ? 8 : 4);
     }
     for (int i = 0; i < kTPosts; ++i) {
       mbar_init(&bars[L::kUFull + i], 1);
-      mbar_init(&bars[L::kUEmpty + i], 256 + 2 + (ROWS2 ? 0 : 128));
+      mbar_init(&bars[L::kUEmpty + i], 8 + 2 + (ROWS2 ? 0 : 4));
     }
     for (int i = 0; i < kTVotes; ++i) {
       mbar_init(&bars[L::kKick + i], 1);
       mbar_init(&bars[L::kVote + i], 1);
     }
-    mbar_init(&bars[L::kXFull], 256);
-    mbar_init(&bars[L::kXFull + 1], 256);
-    mbar_init(&bars[L::kOFree], 128);
+    mbar_init(&bars[L::kXFull], 8);
+    mbar_init(&bars[L::kXFull + 1], 8);
+    mbar_init(&bars[L::kOFree], 4);
     mbar_init(&bars[L::kDone], 1);
     *dead = 0;
     *start_s = a.S;
@@ -329,6 +331,11 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     return false;
   };
   // uniform over the warp (warp collectives follow)
+  // a warp's arrival: what its lanes did before is before it
+  auto arrive_warp = [&](int b, uint32_t n = 1) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_n(&bars[b], n);
+  };
   auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
   if (warp >= 8) {
@@ -514,22 +521,24 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         const uint32_t sq = smem_u32(smem + set * L::kSet), ring = smem_u32(smem + L::kOffRing);
         // S of the rows at sq + q against the K tile of key tile j, into S columns `buf`
         auto issue_s = [&](int q, int j, int buf) {
-          const uint32_t kb = ring + (item + 2 * j) % NS * L::kTile, qb = sq + q;
+          // (descriptors: the address field counts 16 bytes)
+          const uint64_t qd = umma_desc_sw128(sq + q, 16, 1024);
+          const uint64_t kd = umma_desc_sw128(ring + (item + 2 * j) % NS * L::kTile, 16, kGroup);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(tmem + buf * 128, umma_desc_sw128(qb + (kk >> 2) * kTHalf + (kk & 3) * 32, 16, 1024),
-                      umma_desc_sw128(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, kGroup), kIdS, kk > 0);
+            umma_bf16(tmem + buf * 128, qd + ((kk >> 2) * kTHalf + (kk & 3) * 32) / 16,
+                      kd + ((kk >> 2) * 1024 + (kk & 3) * 32) / 16, kIdS, kk > 0);
           umma_commit(&bars[L::kSFull + buf]);
           mbar_arrive(&bars[L::kSFull + buf]);  // (what the producer wrote with the tile is seen behind it)
         };
         auto issue_pv = [&](int x, int j, int buf) {  // O of warpgroup x += P V
-          const uint32_t vb = ring + (item + 2 * j + 1) % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
+          const uint64_t vd = umma_desc_sw128(
+              ring + (item + 2 * j + 1) % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup), 1024, kGroup);
           const uint32_t pc = tmem + buf * 128 + (ROWS2 ? 0 : x * 64);
           const bool put = j == 0 && put_of[x];  // the first product adds to what is there
 #pragma unroll
           for (int kk = 0; kk < KN / 16; ++kk)
-            umma_bf16_ts(tmem + kColO + x * 128, pc + kk * 8, umma_desc_sw128(vb + kk * 2 * kGroup, 1024, kGroup),
-                         kIdPV, j > 0 || kk > 0 || put);
+            umma_bf16_ts(tmem + kColO + x * 128, pc + kk * 8, vd + kk * 2 * kGroup / 16, kIdPV, j > 0 || kk > 0 || put);
         };
         auto full = [&](int i) {
           if (!wait(L::kFull + i % NS, (uint32_t)((i / NS) & 1))) return false;
@@ -548,29 +557,30 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         };
         auto release = [&](int i) { umma_commit(&bars[L::kEmpty + (item + i) % NS]); };
         if constexpr (ROWS2) {
+          // (A commit waits for its turn among the MMAs, and the issuer with it: none but
+          // those that the softmax waits for.  The tiles are let go by a softmax thread, from
+          // the next scores' commit: FIGURE.)
           if ((ok = key_tile(0))) {
             issue_s(0, 0, 0);
             if (live > 1) issue_s(L::kTile, 0, 1);
-            release(0);
           }
           for (int j = 0; ok && j < nt; ++j) {
             const bool more = j + 1 < nt;
             if (!(ok = full(item + 2 * j + 1) && written(0, (uint32_t)(n++ & 1)))) break;
             issue_pv(0, j, 0);
-            umma_commit(&bars[L::kPV]);
             if (more) {
               if (!(ok = key_tile(j + 1))) break;
               issue_s(0, j + 1, 0);
+            } else {
+              umma_commit(&bars[L::kPV]);
             }
             if (live > 1) {
               if (!(ok = written(1, (uint32_t)(n1++ & 1)))) break;
               issue_pv(1, j, 1);
-              umma_commit(&bars[L::kPV + 1]);
-            }
-            release(2 * j + 1);
-            if (more) {
-              if (live > 1) issue_s(L::kTile, j + 1, 1);
-              release(2 * j + 2);
+              if (more)
+                issue_s(L::kTile, j + 1, 1);
+              else
+                umma_commit(&bars[L::kPV + 1]);
             }
           }
         } else {
@@ -591,7 +601,6 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
               issue_pv(0, jp, bp);
               issue_pv(1, jp, bp);
               release(2 * jp++ + 1);
-              umma_commit(&bars[L::kPV + bp]);
             } else if (*dead || clock64() - t0 > kWaitLimitCycles) {
               ok = false;
               if (!*dead) fail();
@@ -669,7 +678,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       int u = 0, qn = 0, jall = 0;
       auto release = [&]() {  // both states have been read
         tc_fence_before();
-        mbar_arrive(&bars[L::kOFree]);
+        arrive_warp(L::kOFree);
       };
       release();
       while (true) {
@@ -680,7 +689,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         if (kind == kPieceStop) break;
         const int row0 = p[PP_ROW0], T = p[PP_NODES], h = p[PP_HEAD], nt = p[PP_TILES], slot = p[PP_SLOT];
         ++u;
-        mbar_arrive(&bars[L::kUEmpty + pb]);
+        arrive_warp(L::kUEmpty + pb);
         if (kind == kPieceZero) {
           zero_rows<D>(a, row0, T, h, m, 128);
           continue;
@@ -688,12 +697,12 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         const int set = qn % L::kSets;
         ++qn;
         jall += nt;
-        const int last = jall - 1;
+        const int last = 2 * jall - 1;  // its last V tile, let go once its product is done
         const bool valid = nl < a.nodes_tile && nl < T, some = __any_sync(0xffffffffu, valid);
         // the row's states, left in the piece's query rows' room (which nothing reads any more), then the products
         uint8_t *stage = smem + set * L::kSet + w * 32 * D * 2;
         if (!wait_warp(L::kXFull + set, (uint32_t)(((qn - 1) >> 1) & 1)) ||
-            !wait_warp(L::kPV + (last & 1), (uint32_t)((last >> 1) & 1)))
+            !wait_warp(L::kEmpty + last % NS, (uint32_t)((last / NS) & 1)))
           break;
         tc_fence_after();
         const float2 s0 = reinterpret_cast<const float2 *>(stage)[lane], s1 = reinterpret_cast<const float2 *>(stage)[32 + lane];
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           release();
           fence_proxy_async_smem();
         }
-        mbar_arrive(&bars[L::kQEmpty + set]);
+        arrive_warp(L::kQEmpty + set);
       }
     }
   } else {
@@ -767,12 +776,13 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     const int xr = ROWS2 ? x : 0;  // row tile
     const bool positive = a.scale_log2 > 0.f;
     const float sc = positive ? a.scale_log2 : 1.f;
-    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads[2] = {0, 0};  // jx: this warpgroup's key tiles
+    int u = 0, qn = 0, jall = 0, jx = 0, votes = 0, reads[2] = {0, 0}, pieces = 0;  // jx, pieces: this warpgroup's key tiles and pieces
     bool ok = true;
-    // P V of this warpgroup's key tile n (one row tile: the one before it may not
-    // be complete either, so each S buffer has a barrier)
+    // P V of key tile n of the CTA (one row tile), which lets go the V tile.  (Its slot's next
+    // tile but one is not consumed before a later P of these threads.)
     auto wait_pv = [&](int n) -> bool {
-      return ROWS2 ? wait_warp(L::kPV + x, (uint32_t)(n & 1)) : wait_warp(L::kPV + (n & 1), (uint32_t)((n >> 1) & 1));
+      const int i = 2 * n + 1;
+      return wait_warp(L::kEmpty + i % NS, (uint32_t)((i / NS) & 1));
     };
     while (ok) {
       const int pb = u % kTPosts;
@@ -785,7 +795,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       ++u;
       if (kind == kPieceZero) {
         if constexpr (ROWS2) zero_rows<D>(a, first, T, h, tid, 256);
-        mbar_arrive(&bars[L::kUEmpty + pb]);
+        arrive_warp(L::kUEmpty + pb);
         continue;
       }
       const int set = qn % L::kSets, tree0 = c / kTN;  // first key tile with a node
@@ -793,7 +803,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       if (ROWS2 && x >= live) {  // no rows for this warpgroup
         jall += nt;
         votes += max(0, t0 + nt - max(t0, tree0));
-        mbar_arrive(&bars[L::kUEmpty + pb]);
+        arrive_warp(L::kUEmpty + pb);
         continue;
       }
       const int node = base + xr * a.nodes_tile + nl;
@@ -832,6 +842,11 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           break;
         }
         tc_fence_after();
+        if (ROWS2 && x == live - 1 && m == 0) {  // both row tiles' scores, and the products before them, are done
+          mbar_arrive(&bars[L::kEmpty + 2 * (jall + j) % NS]);
+          if (j > 0) mbar_arrive(&bars[L::kEmpty + (2 * (jall + j) - 1) % NS]);
+        }
+        __syncwarp();
         const uint32_t pages_t = pages_of[(jall + j) & 7];
         const bool masked = tree || pages_t != kAllPages;
         const uint32_t pages = ROWS2 ? pages_t : pages_t >> (x * PAGES / 2);  // of this warpgroup's keys
@@ -878,7 +893,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           const float alpha = grow ? exp2f(m_run - m_new) : 1.f;
           const float lsum = tree_probabilities(s, sc, m_use == -INFINITY ? 0.f : m_use, lane_base + s_col);
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
-            if (!ROWS2 && !wait_pv(jx - 1)) {  // (two row tiles: S came behind that product)
+            if (!ROWS2 && !wait_pv(jall + j - 1)) {  // (two row tiles: S came behind that product)
               ok = false;
               break;
             }
@@ -921,7 +936,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           if (j == 0 && m == 0) put_of[x] = odd;
           if (odd) {
             // p v added to the rows that attend such a node, then its row cleared
-            if (!ROWS2 && !(j > 0 ? wait_pv(jx - 1) : wait_warp(L::kOFree, (uint32_t)((qn - 1) & 1)))) {
+            if (!ROWS2 && !(j > 0 ? wait_pv(jall + j - 1) : wait_warp(L::kOFree, (uint32_t)((qn - 1) & 1)))) {
               ok = false;
               break;
             }
@@ -967,7 +982,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
               }
             }
             const int rb = ROWS2 ? live == 1 : x;  // everyone has read them (two row tiles: both warpgroups)
-            mbar_arrive(&bars[L::kRead + rb]);
+            arrive_warp(L::kRead + rb);
             if (!wait_warp(L::kRead + rb, (uint32_t)(reads[rb]++ & 1))) {
               ok = false;
               break;
@@ -983,7 +998,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         }
         if (!tree && j == 0 && m == 0) put_of[x] = 0;
         tc_fence_before();
-        mbar_arrive(&bars[L::kPFull + buf]);  // (one row tile: a warp may be at the next key tile while another is here)
+        arrive_warp(L::kPFull + buf);  // (one row tile: a warp may be at the next key tile while another is here)
       }
       if (!ok) break;
       jall += nt;
@@ -991,9 +1006,11 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       if constexpr (!ROWS2) {  // to the warps that end the piece
         float2 *to = reinterpret_cast<float2 *>(smem + set * L::kSet + (warp & 3) * 32 * D * 2);
         to[x * 32 + lane] = make_float2(m_run, refused && x == 0 ? -1.f : l_run);
-        mbar_arrive(&bars[L::kXFull + set]);  // (the softmax may end the next piece before these have ended this one)
+        arrive_warp(L::kXFull + set);  // (the softmax may end the next piece before these have ended this one)
       } else {
-        if (!wait_pv(jx - 1)) break;
+        if (!wait_warp(L::kPV + x, (uint32_t)(pieces++ & 1))) break;
+        if (x == live - 1 && m == 0) mbar_arrive(&bars[L::kEmpty + (2 * jall - 1) % NS]);  // the last V tile
+        __syncwarp();
         tc_fence_after();
         auto values = [&](int i, float f, float (&v)[16]) {
           uint32_t p0[16];
@@ -1040,9 +1057,9 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           if (valid) a.ws_ml[at * a.prow + x * 128 + m] = make_float2(m_run, refused ? -1.f : l_run);
         }
         tc_fence_before();
-        mbar_arrive_n(&bars[L::kQEmpty + set], live == 1 ? 2u : 1u);  // (for the other row tile's threads too)
+        arrive_warp(L::kQEmpty + set, live == 1 ? 2u : 1u);  // (for the other row tile's threads too)
       }
-      mbar_arrive(&bars[L::kUEmpty + pb]);
+      arrive_warp(L::kUEmpty + pb);
     }
   }
   tc_fence_before();
