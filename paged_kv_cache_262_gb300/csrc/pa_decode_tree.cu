@@ -1087,29 +1087,43 @@ __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
   auto at = [&](int i) { return ((size_t)(share + i) * a.tiles_x + tx) * 2 + (i == 0); };
   float M = -INFINITY, den = 0.f;
   bool refused = false;  // the piece with the tree's last keys says so: a sum below 0
-  for (int i = 0; i < pieces; ++i) {
-    const float2 ml = a.ws_ml[at(i) * a.prow + r];
-    if (ml.y != 0.f) M = fmaxf(M, ml.x);
-    refused |= ml.y < 0.f;
-  }
-  if (M == -INFINITY) M = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = 0; i < pieces; ++i) {
-    const float2 ml = a.ws_ml[at(i) * a.prow + r];
-    const float4 *o = a.ws_o + (at(i) * (D / 4) + warp * 4) * a.prow + r;
-    float4 v[4];
+  constexpr int U = 4;  // pieces on their way at once
+  for (int i0 = 0; i0 < pieces; i0 += U) {
+    float2 ml[U];
+    float4 v[U][4];
+    float Mn = M;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = o[(size_t)k * a.prow];
-    if (ml.y == 0.f) continue;
-    const float w = exp2f(ml.x - M);
-    den += w * ml.y;
+    for (int u = 0; u < U; ++u) {
+      const size_t p = at(min(i0 + u, pieces - 1));
+      ml[u] = a.ws_ml[p * a.prow + r];
+      const float4 *o = a.ws_o + (p * (D / 4) + warp * 4) * a.prow + r;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      acc[k].x += w * v[k].x, acc[k].y += w * v[k].y;
-      acc[k].z += w * v[k].z, acc[k].w += w * v[k].w;
+      for (int k = 0; k < 4; ++k) v[u][k] = o[(size_t)k * a.prow];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= pieces) ml[u].y = 0.f;
+      refused |= ml[u].y < 0.f;
+      if (ml[u].y != 0.f) Mn = fmaxf(Mn, ml[u].x);
+    }
+    const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);  // (nothing so far: nothing to scale)
+    M = Mn;
+    den *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k].x *= f, acc[k].y *= f, acc[k].z *= f, acc[k].w *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].y == 0.f) continue;
+      const float w = M == -INFINITY ? 1.f : exp2f(ml[u].x - M);  // (-infinity: a NaN sum without a maximum)
+      den += w * ml[u].y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[k].x += w * v[u][k].x, acc[k].y += w * v[u][k].y;
+        acc[k].z += w * v[u][k].z, acc[k].w += w * v[u][k].w;
+      }
     }
   }
   const float inv = den != 0.f ? 1.f / den : 0.f;
