@@ -65,15 +65,15 @@ namespace {
 struct TreeArgs {
   const int32_t *bt, *ctx, *cu, *parents;
   __nv_bfloat16 *out;
-  float4 *ws_o;   // [share][row tile][2][D / 4][prow], sums of p v; slot 0 a piece that began before the share, 1 one that goes on past it
-  float2 *ws_ml;  // [share][row tile][2][prow], maximum and sum
-  int4 *ws_next;  // [share][row tile]: of a piece that goes on: first row, kv head, nodes, last share (-1: none)
+  float4 *ws_o;   // [CTA][2][D / 4][prow], sums of p v; slot 0 a piece that began before the CTA's share, 1 one that goes on past it
+  float2 *ws_ml;  // [CTA][2][prow], maximum and sum
+  int4 *ws_next;  // [CTA]: of a piece that goes on: first row, kv head and (from bit 16) CTAs from share to share, nodes, pieces (0: none)
   int32_t *err;
   int S, Hq, Hkv, G, num_blocks, max_blocks, max_ctx, max_nodes, total;
   int nodes_tile;  // nodes of a row tile
   int box;         // nodes of a query load
-  int tiles_x;     // CTAs (of one or two row tiles) a unit's rows take
-  int shares, prow;
+  int tiles_x;     // CTAs (of one or two row tiles) the rows of a largest tree take
+  int prow;
   float scale_log2;
 };
 
@@ -111,8 +111,8 @@ struct TreeSmem {
   static constexpr int kOffPost = kOffBar + kBars * 8;
   static constexpr int kOffPages = kOffPost + kTPosts * kTPostWords * 4;  // [2][8] valid pages of the latest K, V tiles
   static constexpr int kOffBad = kOffPages + 2 * 8 * 4;                   // [votes][4] keys of a tile that are not finite
-  static constexpr int kOffScan = (kOffBad + kTVotes * 16 + 7) & ~7;      // [16] sums of the warps
-  static constexpr int kOffMisc = kOffScan + 16 * 8;                      // TMEM address, dead, first sequence, its tiles' offset, O put by hand [2]
+  static constexpr int kOffScan = (kOffBad + kTVotes * 16 + 7) & ~7;      // [2][16] sums of the warps
+  static constexpr int kOffMisc = kOffScan + 2 * 16 * 8;                    // TMEM address, dead, first sequence, its tiles' offset, O put by hand [2]
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -141,6 +141,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int s, int B) {
 __device__ __forceinline__ int unit_cost(int tiles) { return tiles ? tiles + kTUnitCost : 0; }
 
 __device__ __forceinline__ long long share_begin(long long total, int shares, int i) { return total * i / shares; }
+
+// CTAs (of two row tiles) that a tree's rows take; a refused one's zeros are one's work.
+__device__ __forceinline__ int row_pairs(const TreeArgs &a, int nodes, int why) {
+  return why ? 1 : (nodes + 2 * a.nodes_tile - 1) / (2 * a.nodes_tile);
+}
 
 // The bits of keys [key0, key0 + 128) below `n`.
 __device__ __forceinline__ uint32_t bits_below(int n, int word) {
@@ -173,7 +178,7 @@ __device__ __forceinline__ float tree_probabilities(const float (&s)[KN], float 
 
 // A piece: key tiles t0 .. t0 + nt - 1 of a unit.
 struct TreePiece {
-  int s, first, T, ctx, why, h, tiles, t0, nt;
+  int s, first, T, ctx, why, h, base, tiles, t0, nt;  // base: first node of its rows
   long long unit_end;  // behind the unit, in the shares' count
 };
 
@@ -206,6 +211,13 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const uint8_t *sta
       reinterpret_cast<uint4 *>(a.out + to * D + col)[ch] =
           *reinterpret_cast<const uint4 *>(stage + r * RB + ((ch ^ r) & (CH - 1)) * 16);
   }
+}
+
+// A wait without an end: the first to give up says so.
+__device__ __noinline__ void tree_late(volatile int *dead, int32_t *err) {
+  if (*dead) return;
+  *dead = 1;
+  if (err) atomicOr(err, PA_DEVERR_TIMEOUT);
 }
 
 // ROWS2: the softmax warpgroups have a row tile each, else half of each key tile.
@@ -278,38 +290,53 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
   grid_wait();
   grid_launch_dependents();
 
-  // ---- this CTA's share of all units' key tiles
-  long long mine = 0;
+  // ---- this CTA's share of all units' key tiles.  Trees of several CTAs' rows: CTAs
+  // side by side take the same share of the keys, a pair of row tiles each, and a page
+  // comes from HBM once.  Where that leaves too many without rows (trees much smaller
+  // than the largest may be), the pairs are units by themselves.
+  long long mine[2] = {0, 0};  // side by side; flat
   const int per = (a.S + kThreads - 1) / kThreads;
   for (int s = tid * per; s < min(a.S, (tid + 1) * per); ++s) {
     const TreeSeq q = tree_seq(a, s, B);
-    mine += (long long)unit_cost(q.tiles) * a.Hkv;
+    const long long n = (long long)unit_cost(q.tiles) * a.Hkv;
+    mine[0] += n;
+    if (ROWS2) mine[1] += n * row_pairs(a, q.count, q.why);
     if (q.why && blockIdx.x == 0 && a.err) atomicOr(a.err, q.why);
   }
-  long long incl = mine;
+  long long total[2] = {0, 0}, before[2] = {0, 0};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+  for (int i = 0; i < (ROWS2 ? 2 : 1); ++i) {
+    before[i] = mine[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, before[i], o);
+      if (lane >= o) before[i] += v;
+    }
+    if (lane == 31) scan[i * 16 + warp] = before[i];
+    before[i] -= mine[i];
   }
-  if (lane == 31) scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long total = 0, before = incl - mine;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const int share = blockIdx.x / a.tiles_x, tx = blockIdx.x % a.tiles_x;
-  const int shares = (int)min((long long)a.shares, total);
-  const long long beg = share < shares ? share_begin(total, shares, share) : 0;
-  const long long end = share < shares ? share_begin(total, shares, share + 1) : 0;
-  if (beg < end && beg >= before && beg < before + mine) {
-    long long at = before;
+  for (int i = 0; i < (ROWS2 ? 2 : 1); ++i)
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before[i] += scan[i * 16 + w];
+      total[i] += scan[i * 16 + w];
+    }
+  const int beside = gridDim.x / a.tiles_x;  // shares, with the row tiles side by side
+  const bool flat = ROWS2 && total[1] * beside * 8 < total[0] * gridDim.x * 7;
+  const int step = flat ? 1 : a.tiles_x, share = blockIdx.x / step, tx = blockIdx.x % step;
+  const long long all = flat ? total[1] : total[0], at0 = flat ? before[1] : before[0];
+  const int shares = (int)min((long long)(flat ? gridDim.x : beside), all);
+  const long long beg = share < shares ? share_begin(all, shares, share) : 0;
+  const long long end = share < shares ? share_begin(all, shares, share + 1) : 0;
+  if (beg < end && beg >= at0 && beg < at0 + (flat ? mine[1] : mine[0])) {
+    long long at = at0;
     for (int s = tid * per;; ++s) {
-      const long long n = (long long)unit_cost(tree_seq(a, s, B).tiles) * a.Hkv;
+      const TreeSeq q = tree_seq(a, s, B);
+      const long long n = (long long)unit_cost(q.tiles) * a.Hkv * (flat ? row_pairs(a, q.count, q.why) : 1);
       if (beg < at + n) {
         *start_s = s;
         *start_off = beg - at;
@@ -320,14 +347,10 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
   }
   __syncthreads();
   const uint32_t tmem = *tslot;
-  auto fail = [&]() {
-    *dead = 1;
-    if (a.err) atomicOr(a.err, PA_DEVERR_TIMEOUT);
-  };
   auto wait = [&](int b, uint32_t parity) -> bool {
     if (*dead) return false;
     if (mbar_wait(&bars[b], parity)) return true;
-    fail();
+    tree_late(dead, a.err);
     return false;
   };
   // uniform over the warp (warp collectives follow)
@@ -347,7 +370,6 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       // K tiles are the ring's even items, V tiles the odd ones
       const int kv = warp == kTProducerV;
       const CUtensorMap *map = kv ? &tmV : &tmK;
-      const int base = ROWS2 ? tx * 2 * a.nodes_tile : 0;  // first node of this CTA's rows
       long long pos = beg, off = beg < end ? *start_off : 0;
       int s = *start_s, window = -1;
       TreeSeq near{};  // of sequence window + lane
@@ -372,28 +394,29 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           p.why = __shfl_sync(0xffffffffu, near.why, s & 31);
           p.tiles = tiles;
           // the unit's first kTUnitCost places stand for what it costs besides its tiles
-          const int cost = unit_cost(tiles);
-          p.h = (int)(off / cost);
-          const int from = (int)(off - (long long)p.h * cost), n = (int)min((long long)(cost - from), end - pos);
+          const int cost = unit_cost(tiles), pairs = flat ? row_pairs(a, p.T, p.why) : 1, unit = (int)(off / cost);
+          p.h = flat ? unit / pairs : unit;
+          p.base = ROWS2 ? (flat ? unit - p.h * pairs : tx) * 2 * a.nodes_tile : 0;
+          const int from = (int)(off - (long long)unit * cost), n = (int)min((long long)(cost - from), end - pos);
           p.t0 = max(from - kTUnitCost, 0);
           p.nt = max(from + n - kTUnitCost, 0) - p.t0;
           pos += n;
           off += n;
           p.unit_end = pos + (cost - from - n);
-          if (off == (long long)cost * a.Hkv) {
+          if (off == (long long)cost * a.Hkv * pairs) {
             off = 0;
             ++s;
           }
-          if (p.nt > 0 && (p.why ? tx == 0 : p.T > base)) return p;
+          if (p.nt > 0 && (p.why ? p.base == 0 : p.T > p.base)) return p;
         }
         p.nt = 0;
         return p;
       };
-      auto page_id = [&](const TreePiece &p, int t) {  // this lane's page of key tile t (-1: none)
+      auto page_id = [&](int s, int keys, int t) {  // this lane's page of a sequence's key tile t (-1: none)
         const int i = t * PAGES + lane;
         int pg = -1;
-        if (lane < PAGES && i < (p.ctx + p.T + B - 1) / B) {
-          pg = __ldg(a.bt + (size_t)p.s * a.max_blocks + i);
+        if (lane < PAGES && i < (keys + B - 1) / B) {
+          pg = __ldg(a.bt + (size_t)s * a.max_blocks + i);
           if (pg < 0 || pg >= a.num_blocks) {
             if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
             pg = -1;
@@ -403,20 +426,27 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       };
       int u = 0, qn = 0, jall = 0;
       bool ok = true, goes_on = false;
-      TreePiece p = next_piece();
-      int cur = p.nt > 0 && !p.why ? page_id(p, p.t0) : -1;
-      while (p.nt > 0) {
-        const TreePiece n = next_piece();
-        const int left = p.T - base, live = !ROWS2 || left <= a.nodes_tile ? 1 : 2;
+      TreePiece p{}, n{};  // the piece under way (nt == 0: none yet) and the one behind it
+      int cur = -1;
+      auto keys = [](const TreePiece &p) { return p.nt > 0 && !p.why ? p.ctx + p.T : 0; };
+      while (true) {
+        n = next_piece();
+        if (p.nt == 0) {
+          if (n.nt == 0) break;
+          cur = page_id(n.s, keys(n), n.t0);
+          p = n;
+          continue;
+        }
+        const int left = p.T - p.base, live = !ROWS2 || left <= a.nodes_tile ? 1 : 2;
         if (!kv) {
           const int slot = p.t0 > 0 ? 0 : p.nt < p.tiles ? 1 : -1, pb = u % kTPosts;
           if (u >= kTPosts && !(ok = wait_warp(L::kUEmpty + pb, (uint32_t)((u / kTPosts - 1) & 1)))) break;
           if (lane == 0) {
             int *w = posts + pb * kTPostWords;
             w[PP_KIND] = p.why ? kPieceZero : kPiece;
-            w[PP_ROW0] = p.first + base;
+            w[PP_ROW0] = p.first + p.base;
             w[PP_NODES] = p.T;
-            w[PP_BASE] = base;
+            w[PP_BASE] = p.base;
             w[PP_CTX] = p.ctx;
             w[PP_HEAD] = p.h;
             w[PP_TILE] = p.t0;
@@ -426,9 +456,10 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             w[PP_FIRST] = p.first;
             w[PP_LAST] = p.t0 + p.nt == p.tiles;
             mbar_arrive(&bars[L::kUFull + pb]);
-            // the share that has the unit's last tile
+            // (the last piece is in the share that has the unit's last tile)
             if (slot == 1)
-              a.ws_next[blockIdx.x] = make_int4(p.first + base, p.h, left, (int)((p.unit_end * shares - 1) / total));
+              a.ws_next[blockIdx.x] =
+                  make_int4(p.first + p.base, p.h | step << 16, left, (int)((p.unit_end * shares - 1) / all) - share + 1);
           }
           goes_on |= slot == 1;
           ++u;
@@ -454,16 +485,13 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
               for (int x = 0; x < live; ++x)
                 for (int hf = 0; hf < kHalves; ++hf)
                   tma_load_4d(smem + set * L::kSet + x * L::kTile + hf * kTHalf, &tmQ, hf * 64, 0, p.h,
-                              p.first + base + x * a.nodes_tile, bar);
+                              p.first + p.base + x * a.nodes_tile, bar);
             }
             __syncwarp();
             return true;
           };
           for (int t = p.t0; ok && t < p.t0 + p.nt; ++t, ++jall) {
-            // the next tile's page on its way meanwhile, or that of the next piece's first
-            const int nxt = t + 1 < p.t0 + p.nt ? page_id(p, t + 1) : n.nt > 0 && !n.why ? page_id(n, n.t0) : -1;
             const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0);
-            if (q_due && !(ok = queries(2 * jall + 1 - NS >= 2 * first))) break;
             const int item = 2 * jall + kv, sl = item % NS;
             uint64_t *bar = &bars[L::kFull + sl];
             if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
@@ -478,22 +506,24 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             if (cur >= 0)
               tma_load_4d_hint(smem + L::kOffRing + sl * L::kTile + lane * B * D * 2, map, 0, 0, 0,
                                (cur * a.Hkv + p.h) * (B / 8), bar, pol);
-            cur = nxt;
+            // the next tile's page on its way meanwhile, or that of the next piece's first
+            const bool more = t + 1 < p.t0 + p.nt;
+            cur = page_id(more ? p.s : n.s, keys(more ? p : n), more ? t + 1 : n.t0);
+            if (q_due && !(ok = queries(!more || 2 * jall + 3 - NS >= 2 * first))) break;
           }
-          if (ok && q_due) ok = queries(true);
           if (!q_due) ++qn;
           if (!ok) break;
-        } else {
-          cur = n.nt > 0 && !n.why ? page_id(n, n.t0) : -1;
         }
+        if (p.why) cur = page_id(n.s, keys(n), n.t0);
         p = n;
+        if (p.nt == 0) break;
       }
       if (!kv) {
         if (ok && !(u >= kTPosts && !wait_warp(L::kUEmpty + u % kTPosts, (uint32_t)((u / kTPosts - 1) & 1))) && lane == 0) {
           posts[u % kTPosts * kTPostWords + PP_KIND] = kPieceStop;
           mbar_arrive(&bars[L::kUFull + u % kTPosts]);
         }
-        if (lane == 0 && a.ws_next && !goes_on) a.ws_next[blockIdx.x] = make_int4(0, 0, 0, -1);
+        if (lane == 0 && a.ws_next && !goes_on) a.ws_next[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (int i = max(0, qn - L::kSets); i < qn; ++i)
           mbar_wait(&bars[L::kQFull + i % L::kSets], (uint32_t)((i / L::kSets) & 1));
       }
@@ -603,7 +633,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
               release(2 * jp++ + 1);
             } else if (*dead || clock64() - t0 > kWaitLimitCycles) {
               ok = false;
-              if (!*dead) fail();
+              tree_late(dead, a.err);
             } else {
               continue;
             }
@@ -914,17 +944,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
         }
         const int v_item = 2 * (jall + j) + 1;
         uint8_t *vt = smem + L::kOffRing + v_item % NS * L::kTile + (ROWS2 ? 0 : x * (KN / 8) * kGroup);
-        // clears the value rows r < KN of this warpgroup's keys that `which` says
-        auto clear_rows = [&](auto which) {
-          for (int r = m; r < KN; r += 128)
-            if (which(r)) {
-              uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
-#pragma unroll
-              for (int i = 0; i < kHalves * 8; ++i)
-                *reinterpret_cast<uint4 *>(row + (i >> 3) * 1024 + ((i ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            }
-        };
+        bool clears = false;  // value rows of this warpgroup's keys
         if (tree) {
           if (!wait_warp(L::kVote + votes % kTVotes, (uint32_t)((votes / kTVotes) & 1))) {
             ok = false;
@@ -987,14 +1007,26 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
               ok = false;
               break;
             }
-            clear_rows([&](int r) { return (bad[r >> 5] >> (r & 31)) & 1u; });
+            clears = true;
           }
         } else if (masked) {  // pages outside the pool
           if (!wait_warp(L::kFull + v_item % NS, (uint32_t)((v_item / NS) & 1))) {
             ok = false;
             break;
           }
-          clear_rows([&](int r) { return !((pages >> (r / B)) & 1u); });
+          clears = true;
+        }
+        if (clears) {
+          const volatile uint32_t *bad = bad_of + (votes - 1) % kTVotes * 4 + (ROWS2 ? 0 : x * 2);
+#pragma unroll 1
+          for (int r = m; r < KN; r += 128)
+            if (tree ? (bad[r >> 5] >> (r & 31)) & 1u : !((pages >> (r / B)) & 1u)) {
+              uint8_t *row = vt + (r >> 3) * kGroup + (r & 7) * 128;
+#pragma unroll 4
+              for (int i = 0; i < kHalves * 8; ++i)
+                *reinterpret_cast<uint4 *>(row + (i >> 3) * 1024 + ((i ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
         }
         if (!tree && j == 0 && m == 0) put_of[x] = 0;
         tc_fence_before();
@@ -1070,21 +1102,20 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
   }
 }
 
-// Joins the pieces of units that several shares hold.  grid (32 rows, share and
-// row tile): the CTA of the share that a unit begins in; a lane a row, a warp 16
-// of its values.
+// Joins the pieces of units that several shares hold.  grid (32 rows, CTA of the
+// first kernel): the one whose share a unit begins in; a lane a row, a warp 16 of
+// its values.
 template <int D>
 __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
   grid_wait();
   const int4 next = a.ws_next[blockIdx.y];
-  if (next.w < 0) return;
-  const int share = blockIdx.y / a.tiles_x, tx = blockIdx.y % a.tiles_x;
+  const int pieces = next.w, step = next.y >> 16, h = next.y & 0xffff;
+  if (pieces == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x * 32 + lane;
   const int x = r / 128, m = r % 128, n = m / a.G;
   if (n >= a.nodes_tile || x * a.nodes_tile + n >= next.z) return;
-  const int pieces = next.w - share + 1;
-  // piece i: share + i's, where the unit began (0) or went on
-  auto at = [&](int i) { return ((size_t)(share + i) * a.tiles_x + tx) * 2 + (i == 0); };
+  // piece i, in a later share: where the unit began (0) or went on
+  auto at = [&](int i) { return (blockIdx.y + (size_t)i * step) * 2 + (i == 0); };
   float M = -INFINITY, den = 0.f;
   bool refused = false;  // the piece with the tree's last keys says so: a sum below 0
   float4 acc[4];
@@ -1127,7 +1158,7 @@ __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
     }
   }
   const float inv = den != 0.f ? 1.f / den : 0.f;
-  const size_t row = (size_t)(next.x + x * a.nodes_tile + n) * a.Hq + (size_t)next.y * a.G + (m - n * a.G);
+  const size_t row = (size_t)(next.x + x * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (m - n * a.G);
   uint4 *out = reinterpret_cast<uint4 *>(a.out + row * D + warp * 16);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -1150,7 +1181,7 @@ int validate_tree(const pa_decode_desc *d, int max_nodes) {
 
 // How a call is laid out; the workspace is for pieces, so none where a unit is one tile.
 struct TreePlan {
-  int nodes_tile, row_tiles, tiles_x, shares, prow;
+  int nodes_tile, row_tiles, tiles_x, ctas, prow;
   bool split;
   size_t o_bytes, ml_bytes, next_bytes;
   size_t total() const { return o_bytes + ml_bytes + next_bytes; }
@@ -1163,13 +1194,13 @@ TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   p.row_tiles = max_nodes <= p.nodes_tile ? 1 : 2;
   p.tiles_x = (max_nodes + p.row_tiles * p.nodes_tile - 1) / (p.row_tiles * p.nodes_tile);
   const long long tiles = std::max<long long>(1, ((long long)d->max_context_len + kTN - 1) / kTN);
-  const long long units = std::max<long long>(1, (long long)d->num_seqs * d->num_kv_heads);
-  p.shares = (int)std::max<long long>(1, std::min<long long>(sms / p.tiles_x, units * (tiles + kTUnitCost)));
+  const long long units = std::max<long long>(1, (long long)d->num_seqs * d->num_kv_heads) * p.tiles_x;
+  p.ctas = (int)std::max<long long>(p.tiles_x, std::min<long long>(sms, units * (tiles + kTUnitCost)));
   p.split = tiles > 1;  // (a unit of one tile is in one share)
   p.prow = p.row_tiles == 2 ? 2 * kTM : (std::min(kTM, max_nodes * G) + 31) / 32 * 32;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   if (p.split) {
-    const size_t n = (size_t)p.shares * p.tiles_x;
+    const size_t n = (size_t)p.ctas;
     p.o_bytes = up(n * 2 * p.prow * d->head_dim * sizeof(float));
     p.ml_bytes = up(n * 2 * p.prow * sizeof(float2));
     p.next_bytes = up(n * sizeof(int4));
@@ -1187,9 +1218,9 @@ int launch_tree(const TreePlan &p, const CUtensorMap &tq, const CUtensorMap &tk,
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PA_ERR_CUDA;
   if (fa.numRegs < L::kRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
-  int r = launch_dependent(kern, dim3(p.shares * p.tiles_x), L::kThreads, L::kAlloc, 1, st, tq, tk, tv, a);
+  int r = launch_dependent(kern, dim3(p.ctas), L::kThreads, L::kAlloc, 1, st, tq, tk, tv, a);
   if (r == PA_OK && p.split)
-    r = launch_dependent(tree_join_kernel<D>, dim3(p.prow / 32, p.shares * p.tiles_x), D * 2, 0, 1, st, a);
+    r = launch_dependent(tree_join_kernel<D>, dim3(p.prow / 32, p.ctas), D * 2, 0, 1, st, a);
   return r;
 }
 
@@ -1246,7 +1277,6 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
   a.nodes_tile = p.nodes_tile;
   a.box = std::min(p.nodes_tile, std::min(max_tree_nodes, total_nodes));
   a.tiles_x = p.tiles_x;
-  a.shares = p.shares;
   a.prow = p.prow;
   a.scale_log2 = d->scale * 1.4426950408889634f;
   const uint64_t rows = (uint64_t)d->num_blocks * d->num_kv_heads * d->block_size;
