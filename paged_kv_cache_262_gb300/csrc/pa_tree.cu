@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
     for (int u = 0; u < kVLoads; ++u) w[u] = u < n ? __ldcs(vec + at + lane + u * kVThreads) : make_uint4(0u, 0u, 0u, 0u);
     batch(w, at + lane, n);
   }
-  const int tail = head + words * E + tid;
-  if (part == a.parts - 1 && tail < a.V) one((float)row[tail], tail);
+  const int tail = head + words * E;
+  if (part == a.parts - 1 && tid < a.V - tail) one((float)row[tail + tid], tail + tid);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
