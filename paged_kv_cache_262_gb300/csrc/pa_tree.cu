@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
   grid_launch_dependents();
   const int i = blockIdx.y, s = blockIdx.z, part = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
-  if (r.bad || i >= r.count) return;
+  if (r.bad || i >= r.count) return;  // (the whole cluster)
+  if (a.parts > 1) cluster_arrive();
   const T *row = static_cast<const T *>(a.logits) + (size_t)(r.first + i) * a.stride;
   // this CTA's logits: 16-byte words of the row, and (part 0) the elements before the first, (the last) behind the last
   const int head = min(a.V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
   }
   if (lane == 0) best_w[warp] = best;
   __syncthreads();
+  if (a.parts > 1) cluster_wait();  // the first CTA has begun: its shared memory may be written
   if (tid == 0) {
 #pragma unroll
     for (int w = 1; w < kVThreads / 32; ++w) best = best_w[w] > best ? best_w[w] : best;
