@@ -565,7 +565,7 @@ int pa_paged_attention_decode_tree(const pa_decode_desc *desc, const void *q, co
  * A node range as refused there, or a node 0 with a parent, sets PA_DEVERR_TREE
  * and gives path_lens 0 and next_tokens -1 (and, of a refused range, no targets);
  * another node's bad parent sets it too, and that node is on no path.  No output
- * overlaps another or an input. */
+ * overlaps another or an input (PA_ERR_INVALID). */
 int pa_verify_tree(const void *logits, int logits_type, int64_t logits_stride, int vocab_size,
                    const int32_t *tokens, const int32_t *parents, const int32_t *cu_nodes, int num_seqs,
                    int max_tree_nodes, int total_nodes, int32_t *targets, int32_t *path, int32_t *path_lens,
@@ -577,7 +577,8 @@ int pa_verify_tree(const void *logits, int logits_type, int64_t logits_stride, i
  * bit-exact, and new_lens[s] := c + n.  What the other nodes left behind them
  * stays as it is.  Bounds of the written blocks are stale until
  * pa_block_key_bounds (start_lens = context_lens).
- *   k_pools, v_pools  HOST arrays of num_layers device pointers (1..256 layers)
+ *   k_pools, v_pools  HOST arrays of num_layers device pointers (1..256 layers),
+ *                to 2 num_layers pools that lie apart
  *   path         device int32 [num_seqs][max_path_len], increasing within a row;
  *                max_path_len 1 .. PA_MAX_TREE_NODES
  *   path_lens    device int32 [num_seqs], 0 .. max_path_len

@@ -312,6 +312,22 @@ extern "C" int pa_verify_tree(const void *logits, int logits_type, int64_t logit
       (total_nodes > 0 && (!logits || !tokens || !parents || !targets)))
     return PA_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(logits) % (logits_type == PA_LOGITS_BF16 ? 2 : 4)) return PA_ERR_INVALID;
+  const size_t S = num_seqs, N = total_nodes, paths = S * max_tree_nodes;
+  const struct {
+    const int32_t *p;
+    size_t n;  // in words of 4 bytes; the logits' last row ends with the vocabulary
+  } in[] = {{tokens, N},
+            {parents, N},
+            {cu_nodes, S + 1},
+            {static_cast<const int32_t *>(logits),
+             N == 0 ? 0 : (((N - 1) * (size_t)logits_stride + vocab_size) * (logits_type == PA_LOGITS_BF16 ? 2 : 4) + 3) / 4}},
+    made[] = {{targets, N}, {path, paths}, {path_lens, S}, {next_tokens, S}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto &x : in)
+      if (!apart(made[i].p, made[i].n, x.p, x.n)) return PA_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (!apart(made[i].p, made[i].n, made[j].p, made[j].n)) return PA_ERR_INVALID;
+  }
   const int sms = current_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   VerifyArgs a{};
@@ -357,6 +373,14 @@ extern "C" int pa_commit_tree(const pa_decode_desc *d, void *const *k_pools, voi
       !apart(new_lens, S, path, S * max_path_len) || !apart(new_lens, S, block_tables, S * d->max_blocks_per_seq))
     return PA_ERR_INVALID;
   if (d->num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  // (a pool given twice would move its rows twice, the second time from where the first has put others)
+  uintptr_t pools[512];
+  std::copy_n(reinterpret_cast<const uintptr_t *>(k_pools), num_layers, pools);
+  std::copy_n(reinterpret_cast<const uintptr_t *>(v_pools), num_layers, pools + num_layers);
+  std::sort(pools, pools + 2 * num_layers);
+  const uintptr_t bytes = (uintptr_t)d->num_blocks * d->num_kv_heads * d->block_size * d->head_dim * 2;
+  for (int i = 1; i < 2 * num_layers; ++i)
+    if (pools[i] - pools[i - 1] < bytes) return PA_ERR_INVALID;
   const int sms = current_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   CommitArgs a{};
