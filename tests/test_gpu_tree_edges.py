@@ -39,3 +39,264 @@ def test_verify_largest_vocabulary(pa, torch):
         got = pa.verify_tree(x, *args, max_tree_nodes=1)
         assert [t.flatten().tolist() for t in got] == [[at], [0], [1], [at]]
         x[0, at] = -1
+
+
+def attend(pa, torch, c, **kw):
+    """(out, err) with the rows behind the last tree prefilled."""
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(c["q"], 7.0)
+    pa.paged_attention_decode_tree(c["q"], c["k"], c["v"], c["bt"], c["ctx"], c["cu"], c["parents"], out,
+                                   err_flag=err, **{"max_tree_nodes": c["most"], "scale": c["scale"], **kw})
+    torch.cuda.synchronize()
+    return out, int(err)
+
+
+def whole(pa, torch, c, **kw):
+    out, err = attend(pa, torch, c, **kw)
+    assert err == 0
+    tr.check(out, tr.ref_tree(c))
+    assert bool((out[c["cu_host"][-1]:] == 7.0).all())
+
+
+# trees of up to 2, 4, 8 and 16 CTAs' rows; most much smaller than the largest may be, or all of its size
+@pytest.mark.parametrize("hq,hkv,d,b", [(16, 1, 128, 16), (14, 2, 64, 32), (7, 1, 128, 32), (30, 2, 64, 16)])
+@pytest.mark.parametrize("nodes", [[1, 2, 17, 40, 3, 0, 9], [64] * 5, [256, 1, 1, 1, 1, 1], [60, 61, 62], [1] * 9])
+def test_rows_of_several_ctas(pa, torch, hq, hkv, d, b, nodes):
+    rng = random.Random(len(nodes) + d)
+    ctx = [rng.choice((0, 1, 100, 127, 300, 900, 1500)) for _ in nodes]
+    c = tr.make_case(ctx, nodes, hq, hkv, d, b, seed=31)
+    whole(pa, torch, c)
+    whole(pa, torch, c, max_tree_nodes=256)  # a loose bound
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_batches(pa, torch, seed):
+    rng = random.Random(seed)
+    for _ in range(4):
+        g, hkv = rng.choice((1, 3, 4, 7, 8, 16)), rng.choice((1, 2, 5))
+        most = rng.choice((1, 5, 32, 70))
+        S = rng.choice((1, 3, 20))
+        nodes = [rng.randint(0, most) for _ in range(S)]
+        ctx = [rng.choice((0, rng.randint(0, 200), rng.randint(0, 3000))) for _ in range(S)]
+        c = tr.make_case(ctx, nodes, g * hkv, hkv, rng.choice((64, 128)), rng.choice((16, 32)), seed=rng.randrange(999))
+        whole(pa, torch, c, max_tree_nodes=rng.choice((max(c["most"], most), 256)))
+
+
+def test_many_short_sequences(pa, torch):
+    """More sequences than a CTA has threads."""
+    rng = random.Random(5)
+    S = 1300
+    c = tr.make_case([rng.randrange(40) for _ in range(S)], [rng.randrange(4) for _ in range(S)], 4, 2, 64, 16, seed=33)
+    whole(pa, torch, c)
+
+
+def test_padded_batch(pa, torch):
+    """Sequences of length 0 without nodes behind the real ones, and rows behind the last tree."""
+    c = tr.make_case([300, 17, 0, 0, 0], [9, 30, 0, 0, 0], 8, 2, 128, 16, seed=34)
+    wide = torch.full((9, c["bt"].shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+    wide[:5, :c["bt"].shape[1]] = c["bt"]
+    c["bt"] = wide
+    c["q"] = torch.cat([c["q"], torch.full_like(c["q"][:7], math.nan)])
+    c["parents"] = torch.cat([c["parents"], i32(torch, [99] * 7)])
+    whole(pa, torch, c)
+
+
+def test_calls_from_two_threads(pa, torch):
+    """Each call is two kernels that hand over through a workspace."""
+    cases = [tr.make_case([2500, 64], [9, 40], 16, 2, 128, 16, seed=40 + i) for i in range(2)]
+    alone = [attend(pa, torch, c)[0] for c in cases]
+    n = [c["cu_host"][-1] for c in cases]
+    bad, errors = [0, 0], []
+
+    def work(i, stream):
+        try:
+            c = cases[i]
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    o = pa.paged_attention_decode_tree(c["q"], c["k"], c["v"], c["bt"], c["ctx"], c["cu"], c["parents"],
+                                                       max_tree_nodes=c["most"], scale=c["scale"])
+                    bad[i] += not torch.equal(o[:n[i]], alone[i][:n[i]])
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    for streams in ([torch.cuda.Stream(), torch.cuda.Stream()], [torch.cuda.Stream()] * 2):
+        torch.cuda.synchronize()
+        threads = [threading.Thread(target=work, args=(i, s)) for i, s in enumerate(streams)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert bad == [0, 0] and not errors
+
+
+def setup_steps(pa, torch):
+    c = tr.make_case([100, 40, 7], [6, 11, 3], 8, 2, 64, 16, seed=50)
+    N = c["cu_host"][-1]
+    c["q"], c["parents"] = c["q"][:N].contiguous(), c["parents"][:N].contiguous()
+    g = torch.Generator(device="cuda").manual_seed(51)
+    x = torch.randn(N, 300, generator=g, device="cuda")
+    best = x.argmax(1).tolist()
+    flat, tokens = c["parents"].tolist(), []
+    for s in range(3):
+        base = c["cu_host"][s]
+        tokens += [best[base + p] if p >= 0 else 0 for p in flat[base:c["cu_host"][s + 1]]]
+    pools = [torch.randn(*c["k"].shape, generator=g, device="cuda").to(torch.bfloat16) for _ in range(4)]
+    return c, x, i32(torch, tokens), pools
+
+
+def test_the_ways_into_the_calls_agree(pa, torch, monkeypatch):
+    """The quick way from Python, the one through ctypes, and that on a given stream."""
+    from paged_kv_cache_262_gb300 import _binding as b
+    F = b._FAST if b._FAST is not None else b._fast()
+    assert F, "the extension module is not built"
+    c, x, tokens, pools = setup_steps(pa, torch)
+    taken = []
+
+    class Watch:
+        def __init__(self, name):
+            self.name = name
+
+        def __call__(self, *a):
+            r = getattr(F, self.name)(*a)
+            taken.append((self.name, r is not None))
+            return r
+
+    class Fast:
+        tree, verify, commit = Watch("tree"), Watch("verify"), Watch("commit")
+
+    def run(stream=None, scale=None, most=c["most"], limit=None):
+        k = [p.clone() for p in pools]
+        torch.cuda.synchronize()
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = {} if stream is None else {"stream": stream}
+        torch.cuda.synchronize()
+        o = pa.paged_attention_decode_tree(c["q"], c["k"], c["v"], c["bt"], c["ctx"], c["cu"], c["parents"],
+                                           max_tree_nodes=most, scale=scale, max_context_len=limit, err_flag=err, **kw)
+        v = pa.verify_tree(x, tokens, c["parents"], c["cu"], max_tree_nodes=most, err_flag=err, **kw)
+        new = pa.commit_tree(k[:2], k[2:], c["bt"], c["ctx"], v[1], v[2], max_context_len=limit, err_flag=err, **kw)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        return [o, *v, new, *k]
+
+    monkeypatch.setattr(b, "_FAST", Fast)
+    quick = run()
+    assert taken == [("tree", True), ("verify", True), ("commit", True)]
+    assert int(quick[3].sum()) > 6  # (paths of more than their roots)
+    for kw in (dict(stream=torch.cuda.Stream()), dict(limit=c["bt"].shape[1] * 16), dict(scale=64**-0.5)):
+        assert all(torch.equal(p, q) for p, q in zip(quick, run(**kw)))
+    monkeypatch.setattr(b, "_FAST", False)
+    assert all(torch.equal(p, q) for p, q in zip(quick, run()))
+    # what the quick way does not take goes through ctypes, to the same answer or the same refusal
+    monkeypatch.setattr(b, "_FAST", Fast)
+    taken.clear()
+    assert torch.equal(pa.commit_tree(tuple(p.clone() for p in pools[:2]), tuple(p.clone() for p in pools[2:]), c["bt"],
+                                      c["ctx"], quick[2], quick[3]), quick[5])
+    with pytest.raises(TypeError):
+        pa.verify_tree(x.half(), tokens, c["parents"], c["cu"], max_tree_nodes=c["most"])
+    with pytest.raises((TypeError, ValueError)):
+        pa.paged_attention_decode_tree(c["q"].float(), c["k"], c["v"], c["bt"], c["ctx"], c["cu"], c["parents"],
+                                       max_tree_nodes=c["most"])
+    assert [t for _, t in taken] == [False] * 3
+
+
+def test_a_failed_launch_is_reported_once(pa, torch, monkeypatch):
+    """The quick way raises the library's error and does not call it again through ctypes."""
+    from paged_kv_cache_262_gb300 import _binding as b
+    F = b._FAST if b._FAST is not None else b._fast()
+    lib = pa.load()
+    names = ("pa_decode_tree_workspace_bytes", "pa_paged_attention_decode_tree", "pa_verify_tree", "pa_commit_tree")
+    c, x, tokens, pools = setup_steps(pa, torch)
+    lens = i32(torch, [1, 1, 1])
+    path = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    path[:, 0] = 0
+    calls = [(names[1], lambda: pa.paged_attention_decode_tree(c["q"], c["k"], c["v"], c["bt"], c["ctx"], c["cu"],
+                                                               c["parents"], max_tree_nodes=c["most"])),
+             (names[2], lambda: pa.verify_tree(x, tokens, c["parents"], c["cu"], max_tree_nodes=c["most"])),
+             (names[3], lambda: pa.commit_tree(pools[:2], pools[2:], c["bt"], c["ctx"], path, lens))]
+    made, keep = [], []
+
+    def failing(name):
+        def fail(*_):
+            made.append(name)
+            return pa.PA_ERR_CUDA
+        keep.append(ctypes.CFUNCTYPE(ctypes.c_int, *getattr(lib, name).argtypes)(fail))
+        return ctypes.cast(keep[-1], ctypes.c_void_p).value
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes") or name == "pa_status_string":
+                return getattr(lib, name)
+            return made.append(name) or (lambda *_: 0)
+
+    for _, f in calls:
+        f()
+    real = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names]
+    F.bind_trees(real[0], *(failing(n) for n in names[1:]))
+    try:
+        monkeypatch.setattr(b, "_LIB", Lib())
+        for name, f in calls:
+            made.clear()
+            with pytest.raises(pa.PaError) as e:
+                f()
+            assert made == [name] and e.value.status == pa.PA_ERR_CUDA and name in str(e.value)
+    finally:
+        F.bind_trees(*real)
+    monkeypatch.undo()
+    for _, f in calls:
+        f()
+
+
+def test_tensors_of_another_device_or_layout_are_refused(pa, torch):
+    c, x, tokens, pools = setup_steps(pa, torch)
+    tree = lambda **kw: pa.paged_attention_decode_tree(  # noqa: E731
+        *[kw.get(k, c[k]) for k in ("q", "k", "v", "bt", "ctx", "cu", "parents")], max_tree_nodes=c["most"])
+    for k in ("q", "k", "v", "bt", "ctx", "cu", "parents"):
+        with pytest.raises((TypeError, ValueError)):
+            tree(**{k: c[k].cpu()})
+    with pytest.raises((TypeError, ValueError)):
+        tree(q=c["q"].transpose(0, 1))
+    with pytest.raises((TypeError, ValueError)):
+        tree(k=c["k"].transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises((TypeError, ValueError, pa.PaError)):  # the same pools as K and V of the compaction
+        pa.commit_tree(pools[:2], pools[:2], c["bt"], c["ctx"], torch.zeros(3, 4, dtype=torch.int32, device="cuda"),
+                       i32(torch, [1, 1, 1]))
+
+
+def test_graph_of_a_step(pa, torch):
+    """Attention, verification and compaction captured together, replayed on other trees."""
+    c, x, tokens, pools = setup_steps(pa, torch)
+    most = c["most"]
+    k = [p.clone() for p in pools]
+    par = c["parents"].clone()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        o = pa.paged_attention_decode_tree(c["q"], k[0], k[2], c["bt"], c["ctx"], c["cu"], par, max_tree_nodes=most,
+                                           err_flag=err)
+        v = pa.verify_tree(x, tokens, par, c["cu"], max_tree_nodes=most, err_flag=err)
+        return [o, *v, pa.commit_tree(k[:2], k[2:], c["bt"], c["ctx"], v[1], v[2], err_flag=err)]
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = step()
+    for chain in (False, True, False):
+        par.copy_(c["parents"])
+        if chain:
+            for b, e in zip(c["cu_host"], c["cu_host"][1:]):
+                par[b:e] = torch.arange(-1, e - b - 1, dtype=torch.int32, device="cuda")
+        results = []
+        for replayed in (True, False):
+            for p, q in zip(k, pools):
+                p.copy_(q)
+            torch.cuda.synchronize()
+            if replayed:
+                g.replay()
+            outs = got if replayed else step()
+            torch.cuda.synchronize()
+            results.append([t.clone() for t in outs + k])
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert int(err) == 0
