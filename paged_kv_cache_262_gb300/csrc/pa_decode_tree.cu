@@ -40,6 +40,14 @@
 // nodes 106 us, 94 so).  The running maximum moves only when it grows by more than 8 (2^8), so O is
 // seldom rescaled.
 //
+// Measured: 64 x 5 nodes over 128..2048 tokens 59 us (307 MB, 5.2 TB/s), 32 x 16..32
+// nodes over 512..8192 92.5 (548 MB, 5.9 TB/s), nine trees of 1 to 61 nodes with seven
+// heads a kv head 34, 8 x 64 nodes over 32K tokens 405 (1.36 PFLOP/s), one of 8 nodes
+// over 1000 10.5.  Of the 59, about 4 go by before the first tiles come, 4 are the join
+// and 4 that the CTAs do not end together.  With two row tiles a key tile takes 3600
+// cycles, 2050 of them MMAs: a row tile's scores, softmax (1800) and product follow one
+// another, and TMEM has no room for scores ahead (2 x 128 columns of S, as many of O).
+//
 // Only tiles at and behind the context's end, or with a page outside the pool, are
 // masked.  There a key's value row meets a probability of 0 in the rows that do
 // not attend it: value rows past the tree are cleared in shared memory, and the
@@ -85,8 +93,8 @@ constexpr int kTPostWords = 16;
 constexpr int kTVotes = 4;               // tiles with a tree under way at once
 constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTChecker = 11, kTEnd = 12;  // warps
 // A unit counts as so many key tiles more than it has when the shares are cut:
-// what its pieces cost besides (64 x 5 nodes with 0, 1, 2, 3, 4: 89.9, 81.6, 79.0, 76.0,
-// 75.8 us).
+// what its pieces cost besides (64 x 5 nodes with 1, 2, 3, 4: 61.8, 59.6, 59.4, 60.9 us,
+// one to 61 nodes, seven heads a kv head 34.8, 33.7, 33.8, 34.2).
 constexpr int kTUnitCost = 3;
 
 template <int D, bool ROWS2>
