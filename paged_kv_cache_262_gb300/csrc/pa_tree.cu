@@ -54,33 +54,23 @@ __device__ __forceinline__ float logit(const __nv_bfloat16 *, const uint4 &v, in
 }
 __device__ __forceinline__ float logit(const float *, const uint4 &v, int e) { return __uint_as_float((&v.x)[e]); }
 
-// grid (part of a row, node, sequence), the parts of a row a cluster: the node's
-// target.  A maximum over the tokens is a running one that few values change, so a
-// warp takes that of a batch of 16-byte words first (packed, for bf16) and looks
-// closer, for the token, only at words that hold the warp's new largest: each of its
-// later words lies behind all of its earlier ones, so an equal value there is no
+// The best of logits [0, V) of a row as far as they are in its 16-byte words [w0, w1),
+// before its first word (`head` says so) or behind its last (`tail`); the CTA's THREADS
+// threads, the answer in thread 0.  A maximum over the tokens is a running one that few
+// values change, so a warp takes that of a batch of words first (packed, for bf16) and
+// looks closer, for the token, only at words that hold the warp's new largest: each of
+// its later words lies behind all of its earlier ones, so an equal value there is no
 // better.  (Every thread by its own running maximum instead: 32 of them disagree so
 // often that 426 MB took 137 us; every word of a batch with a larger value: 66.)
-//
-// The bytes bind: 64 trees of 26 nodes against 128000 bf16 logits 64.7 us with the
-// walk, 6.6 TB/s; 16 trees of up to 40 nodes against 50001 fp32 logits (74 MB) 16.6 us,
-// of which the launches and the walk are about 4.
-template <class T>
-__global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
+template <int THREADS, class T>
+__device__ __forceinline__ unsigned long long row_best(const T *row, int V, int part, int parts,
+                                                       unsigned long long (&best_w)[THREADS / 32]) {
   constexpr int E = 16 / sizeof(T);
-  __shared__ unsigned long long best_w[kVThreads / 32];
-  __shared__ uint32_t best_p[kVMaxParts][2];  // of the cluster's parts, in its first CTA
-  grid_wait();
-  grid_launch_dependents();
-  const int i = blockIdx.y, s = blockIdx.z, part = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
-  if (r.bad || i >= r.count) return;  // (the whole cluster)
-  if (a.parts > 1) cluster_arrive();
-  const T *row = static_cast<const T *>(a.logits) + (size_t)(r.first + i) * a.stride;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // this CTA's logits: 16-byte words of the row, and (part 0) the elements before the first, (the last) behind the last
-  const int head = min(a.V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
-  const int words = (a.V - head) / E;
-  const int w0 = (int)((long long)words * part / a.parts), w1 = (int)((long long)words * (part + 1) / a.parts);
+  const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
+  const int words = (V - head) / E;
+  const int w0 = (int)((long long)words * part / parts), w1 = (int)((long long)words * (part + 1) / parts);
   const uint4 *vec = reinterpret_cast<const uint4 *>(row + head);
   unsigned long long best = 0;  // below every logit's rank
   float top = -INFINITY;        // the warp's best logit so far
@@ -98,7 +88,7 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
       return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
   };
-  // words at, at + kVThreads, ... of this thread, `n` of them there (the warp's lanes together)
+  // words at, at + THREADS, ... of this thread, `n` of them there (the warp's lanes together)
   auto batch = [&](const uint4 (&w)[kVLoads], int at, int n) {
     float m[kVLoads], most = -INFINITY;
 #pragma unroll
@@ -116,26 +106,26 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
     for (int u = 0; u < kVLoads; ++u)
       if (u < n && (m[u] == top || m[u] != m[u])) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) one(logit(row, w[u], e), head + (at + u * kVThreads) * E + e);
+        for (int e = 0; e < E; ++e) one(logit(row, w[u], e), head + (at + u * THREADS) * E + e);
       }
   };
   if (part == 0 && tid < head) one((float)row[tid], tid);
   int at = w0 + warp * 32;  // the warp's first word
-  for (; at + 31 + (kVLoads - 1) * kVThreads < w1 && !nan; at += kVLoads * kVThreads) {
+  for (; at + 31 + (kVLoads - 1) * THREADS < w1 && !nan; at += kVLoads * THREADS) {
     uint4 w[kVLoads];
 #pragma unroll
-    for (int u = 0; u < kVLoads; ++u) w[u] = __ldcs(vec + at + lane + u * kVThreads);
+    for (int u = 0; u < kVLoads; ++u) w[u] = __ldcs(vec + at + lane + u * THREADS);
     batch(w, at + lane, kVLoads);
   }
-  for (; at < w1 && !nan; at += kVLoads * kVThreads) {
+  for (; at < w1 && !nan; at += kVLoads * THREADS) {
     uint4 w[kVLoads];
-    const int left = w1 - at - lane, n = left <= 0 ? 0 : min(kVLoads, (left + kVThreads - 1) / kVThreads);
+    const int left = w1 - at - lane, n = left <= 0 ? 0 : min(kVLoads, (left + THREADS - 1) / THREADS);
 #pragma unroll
-    for (int u = 0; u < kVLoads; ++u) w[u] = u < n ? __ldcs(vec + at + lane + u * kVThreads) : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < kVLoads; ++u) w[u] = u < n ? __ldcs(vec + at + lane + u * THREADS) : make_uint4(0u, 0u, 0u, 0u);
     batch(w, at + lane, n);
   }
   const int tail = head + words * E;
-  if (part == a.parts - 1 && tid < a.V - tail) one((float)row[tail + tid], tail + tid);
+  if (part == parts - 1 && tid < V - tail) one((float)row[tail + tid], tail + tid);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
@@ -143,17 +133,37 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
   }
   if (lane == 0) best_w[warp] = best;
   __syncthreads();
-  if (a.parts > 1) cluster_wait();  // the first CTA has begun: its shared memory may be written
   if (tid == 0) {
 #pragma unroll
-    for (int w = 1; w < kVThreads / 32; ++w) best = best_w[w] > best ? best_w[w] : best;
-    if (a.parts > 1) {
+    for (int w = 1; w < THREADS / 32; ++w) best = best_w[w] > best ? best_w[w] : best;
+  }
+  return best;
+}
+
+// grid (part of a row, node, sequence), the parts of a row a cluster: the node's target.
+//
+// The bytes bind: 64 trees of 26 nodes against 128000 bf16 logits 64.7 us with the
+// walk, 6.6 TB/s; 16 trees of up to 40 nodes against 50001 fp32 logits (74 MB) 16.6 us,
+// of which the launches and the walk are about 4.
+template <class T>
+__global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
+  __shared__ unsigned long long best_w[kVThreads / 32];
+  __shared__ uint32_t best_p[kVMaxParts][2];  // of the cluster's parts, in its first CTA
+  grid_wait();
+  grid_launch_dependents();
+  const int i = blockIdx.y, s = blockIdx.z, part = blockIdx.x, tid = threadIdx.x;
+  const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
+  if (r.bad || i >= r.count) return;  // (the whole cluster)
+  if (a.parts > 1) cluster_arrive();
+  const T *row = static_cast<const T *>(a.logits) + (size_t)(r.first + i) * a.stride;
+  unsigned long long best = row_best<kVThreads>(row, a.V, part, a.parts, best_w);
+  if (a.parts > 1) {
+    cluster_wait();  // the first CTA has begun: its shared memory may be written
+    if (tid == 0) {
       const uint32_t to = cluster_addr(smem_u32(&best_p[part][0]), 0);
       cluster_store(to, (uint32_t)best);
       cluster_store(to + 4, (uint32_t)(best >> 32));
     }
-  }
-  if (a.parts > 1) {
     cluster_arrive();
     cluster_wait();
     if (part > 0) return;
@@ -166,34 +176,34 @@ __global__ void __launch_bounds__(kVThreads) target_kernel(const VerifyArgs a) {
   if (tid == 0) a.targets[r.first + i] = (int32_t)~(unsigned int)best;
 }
 
-// One CTA a sequence: the walk, by one warp in shared memory.
-__global__ void __launch_bounds__(PA_MAX_TREE_NODES) walk_kernel(const VerifyArgs a) {
-  __shared__ int32_t par[PA_MAX_TREE_NODES], tok[PA_MAX_TREE_NODES], tgt[PA_MAX_TREE_NODES];
-  const int s = blockIdx.x, k = threadIdx.x, lane = k & 31;
-  grid_wait();  // the targets are there (and what the caller's own kernels wrote)
-  grid_launch_dependents();
-  const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
-  const int n = r.bad ? 0 : r.count;
+// A tree in shared memory.
+struct TreeNodes {
+  int32_t par[PA_MAX_TREE_NODES], tok[PA_MAX_TREE_NODES], tgt[PA_MAX_TREE_NODES];
+};
+
+// Node `k`'s parent and token, by a thread each; what is wrong is reported.
+__device__ __forceinline__ void load_nodes(const VerifyArgs &a, const TreeRange &r, int k, TreeNodes &t) {
   bool bad = r.bad;
-  if (k < n) {
-    tgt[k] = a.targets[r.first + k];
-    par[k] = __ldg(a.parents + r.first + k);
-    tok[k] = __ldg(a.tokens + r.first + k);
-    bad = !good_parent(k, par[k]);
+  if (k < (r.bad ? 0 : r.count)) {
+    t.par[k] = __ldg(a.parents + r.first + k);
+    t.tok[k] = __ldg(a.tokens + r.first + k);
+    bad = !good_parent(k, t.par[k]);
   }
   if (bad && a.err) atomicOr(a.err, PA_DEVERR_TREE);
-  __syncthreads();
-  if (k >= 32) return;
+}
+
+// The path of sequence s's tree of n nodes, by one warp.
+__device__ __forceinline__ void walk(const VerifyArgs &a, int s, int n, const TreeNodes &t, int lane) {
   int32_t *path = a.path + (size_t)s * a.max_nodes;
-  int len = 0, next = -1, node = n > 0 && par[0] == -1 ? 0 : -1;
+  int len = 0, next = -1, node = n > 0 && t.par[0] == -1 ? 0 : -1;
   while (node >= 0) {
     if (lane == 0) path[len] = node;
     ++len;
-    next = tgt[node];
+    next = t.tgt[node];
     int found = -1;
     for (int base = node + 1; base < n && found < 0; base += 32) {
       const int c = base + lane;
-      const unsigned fits = __ballot_sync(0xffffffffu, c < n && par[c] == node && tok[c] == next);
+      const unsigned fits = __ballot_sync(0xffffffffu, c < n && t.par[c] == node && t.tok[c] == next);
       if (fits) found = base + __ffs(fits) - 1;
     }
     node = found;
@@ -203,6 +213,67 @@ __global__ void __launch_bounds__(PA_MAX_TREE_NODES) walk_kernel(const VerifyArg
     a.path_lens[s] = len;
     a.next[s] = next;
   }
+}
+
+// One CTA a sequence.
+__global__ void __launch_bounds__(PA_MAX_TREE_NODES) walk_kernel(const VerifyArgs a) {
+  __shared__ TreeNodes t;
+  const int s = blockIdx.x, k = threadIdx.x;
+  grid_wait();  // the targets are there (and what the caller's own kernels wrote)
+  grid_launch_dependents();
+  const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
+  const int n = r.bad ? 0 : r.count;
+  if (k < n) t.tgt[k] = a.targets[r.first + k];
+  load_nodes(a, r, k, t);
+  __syncthreads();
+  if (k < 32) walk(a, s, n, t, k);
+}
+
+// Both at once where a tree's logits are few: a cluster a tree, its CTAs whole rows in
+// turn, then the walk by the first.  One launch instead of two, and no wait between
+// them: one tree of 8 nodes against 32000 bf16 logits 4.3 us in a graph (5.4 with two
+// kernels) and 8.9 by calls from Python (11.5); 16 of them 5.2 (6.7).  Where its CTAs
+// are more than the SMs or read much each, the two kernels: 64 of them 9.6 (11.9 so), 64
+// of 5 against 8000 logits 5.8 (8.1), one of 26 against 32000, 256 KB a CTA, 5.4 (9.5).
+constexpr int kWThreads = 512;
+constexpr int kWBytes = 128 << 10;  // logits of a CTA, at most
+
+template <class T>
+__global__ void __launch_bounds__(kWThreads) verify_kernel(const VerifyArgs a) {
+  __shared__ unsigned long long best_w[kWThreads / 32];
+  __shared__ TreeNodes t;
+  const int s = blockIdx.y, part = blockIdx.x, k = threadIdx.x;
+  grid_wait();
+  grid_launch_dependents();
+  if (a.parts > 1) cluster_arrive();
+  const TreeRange r = tree_range(a.cu, s, a.total, a.max_nodes);
+  const int n = r.bad ? 0 : r.count;
+  if (part == 0 && k < PA_MAX_TREE_NODES) load_nodes(a, r, k, t);
+  const uint32_t tgt = a.parts > 1 ? cluster_addr(smem_u32(t.tgt), 0) : 0;
+  bool begun = a.parts == 1;
+  for (int i = part; i < n; i += a.parts) {
+    const T *row = static_cast<const T *>(a.logits) + (size_t)(r.first + i) * a.stride;
+    const unsigned long long best = row_best<kWThreads>(row, a.V, 0, 1, best_w);
+    if (!begun) cluster_wait();  // the first CTA has: its shared memory may be written
+    begun = true;
+    if (k == 0) {
+      const int32_t target = (int32_t)~(unsigned int)best;
+      a.targets[r.first + i] = target;
+      if (a.parts > 1)
+        cluster_store(tgt + i * 4, (uint32_t)target);
+      else
+        t.tgt[i] = target;
+    }
+    __syncthreads();  // (best_w again)
+  }
+  if (a.parts > 1) {
+    if (!begun) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (part == 0 && k < 32) walk(a, s, n, t, k);
 }
 
 // Parts of a row: two CTAs for every SM, of 2048 logits at least, in one cluster.
@@ -364,9 +435,16 @@ extern "C" int pa_verify_tree(const void *logits, int logits_type, int64_t logit
   a.total = total_nodes;
   a.parts = verify_parts(num_seqs, max_tree_nodes, total_nodes, vocab_size, sms);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = logits_type == PA_LOGITS_F32;
+  const int rows = std::min(max_tree_nodes, total_nodes), ctas = std::max(1, std::min(rows, kVMaxParts));
+  if ((int64_t)num_seqs * ctas <= sms && (int64_t)((rows + ctas - 1) / ctas) * vocab_size * (f32 ? 4 : 2) <= kWBytes) {
+    a.parts = ctas;
+    return launch_dependent(f32 ? verify_kernel<float> : verify_kernel<__nv_bfloat16>, dim3(ctas, num_seqs), kWThreads, 0,
+                            ctas, st, a);
+  }
   if (total_nodes > 0) {
-    auto kern = logits_type == PA_LOGITS_BF16 ? target_kernel<__nv_bfloat16> : target_kernel<float>;
-    const int r = launch_dependent(kern, dim3(a.parts, max_tree_nodes, num_seqs), kVThreads, 0, a.parts, st, a);
+    const int r = launch_dependent(f32 ? target_kernel<float> : target_kernel<__nv_bfloat16>,
+                                   dim3(a.parts, max_tree_nodes, num_seqs), kVThreads, 0, a.parts, st, a);
     if (r != PA_OK) return r;
   }
   return launch_dependent(walk_kernel, dim3(num_seqs), PA_MAX_TREE_NODES, 0, 1, st, a);

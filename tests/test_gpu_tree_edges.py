@@ -300,3 +300,52 @@ def test_graph_of_a_step(pa, torch):
             results.append([t.clone() for t in outs + k])
         assert all(torch.equal(a, b) for a, b in zip(*results))
     assert int(err) == 0
+
+
+# a CTA's whole rows with the walk behind them, and rows in parts with a walk of their own
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("V,S", [(300, 1), (5003, 9), (5003, 200), (70001, 1), (70001, 3), (300001, 1)])
+def test_verify_either_way(pa, torch, dtype, V, S):
+    rng = random.Random(V + S)
+    t = getattr(torch, dtype)
+    trees = [tr.make_tree(rng.choice((0, 1, 3, 9)) if s else 9, "any", rng) for s in range(S)]
+    cu = [0]
+    for tree in trees:
+        cu.append(cu[-1] + len(tree))
+    N = cu[-1] + 1
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(N, V + 3, generator=g, device="cuda") * 2).round().to(t)  # ties
+    x[:, V:] = math.inf
+    x[0] = -math.inf
+    x[1, V // 3], x[1, V // 2], x[1, 5] = math.nan, math.nan, math.inf
+    x[2] = 0.0
+    x[2, ::2] = -0.0
+    x[3, V - 1] = math.inf
+    x[4] = -math.inf
+    x[4, V - 2] = torch.finfo(t).min
+    x[5] = -x[5].abs() - 1
+    flat = [p for tree in trees for p in tree]
+    best = x[:, :V].float().nan_to_num(nan=math.inf).argmax(1).tolist()
+    tokens = [best[c + p] if p >= 0 and rng.random() < 0.8 else rng.randrange(V) for c, tree in zip(cu, trees)
+              for p in tree] + [0]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    targets = torch.full((N,), -5, dtype=torch.int32, device="cuda")
+    got = pa.verify_tree(x[:, :V], i32(torch, tokens), i32(torch, flat + [7]), i32(torch, cu), max_tree_nodes=9,
+                         targets=targets, err_flag=err)
+    rt, rp, rn = tr.ref_verify(x, tokens, trees, cu, V)
+    assert int(err) == 0
+    assert got[0].tolist() == rt[:cu[-1]] + [-5]
+    assert got[1].tolist() == [p + [-1] * (9 - len(p)) for p in rp]
+    assert got[2].tolist() == [len(p) for p in rp] and got[3].tolist() == rn
+    # a range outside the arrays, one of too many nodes, a bad parent: as in either way
+    bad = list(cu)
+    bad[-1] = N + 5
+    got = pa.verify_tree(x[:, :V], i32(torch, tokens), i32(torch, flat + [7]), i32(torch, bad), max_tree_nodes=9,
+                         targets=targets.fill_(-5), err_flag=err)
+    assert int(err) == pa.DEVERR_TREE and got[0][cu[-2]:].tolist() == [-5] * (N - cu[-2])
+    assert got[2][-1] == 0 and got[3][-1] == -1 and got[1][-1].tolist() == [-1] * 9
+    assert got[1][:-1].tolist() == [p + [-1] * (9 - len(p)) for p in rp[:-1]]
+    err.zero_()
+    got = pa.verify_tree(x[:, :V], i32(torch, tokens), i32(torch, flat + [7]), i32(torch, cu), max_tree_nodes=8,
+                         targets=targets.fill_(-5), err_flag=err)
+    assert int(err) == pa.DEVERR_TREE and got[0][:9].tolist() == [-5] * 9 and got[2][0] == 0 and got[3][0] == -1
