@@ -82,6 +82,7 @@ struct TreeArgs {
   int box;         // nodes of a query load
   int tiles_x;     // CTAs (of one or two row tiles) the rows of a largest tree take
   int prow;
+  int cluster;     // 0: shares; else the CTAs of a unit, a cluster
   float scale_log2;
 };
 
@@ -96,6 +97,8 @@ constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTChecker = 11, k
 // what its pieces cost besides (64 x 5 nodes with 1, 2, 3, 4: 61.8, 59.6, 59.4, 60.9 us,
 // one to 61 nodes, seven heads a kv head 34.8, 33.7, 33.8, 34.2).
 constexpr int kTUnitCost = 3;
+constexpr int kTCluster = 8;       // CTAs of a unit, at most, where a cluster does one
+constexpr int kTClusterTiles = 8;  // key tiles of such a CTA, at most
 
 template <int D, bool ROWS2>
 struct TreeSmem {
@@ -185,6 +188,17 @@ __device__ __forceinline__ float tree_probabilities(const float (&s)[KN], float 
   return x.x + x.y;
 }
 
+// Which unit a CTA works on where a cluster does one, and as which of its CTAs (each
+// has unit_share() of the tiles, in order, as long as there are any).
+struct TreeUnit {
+  int s, h, base, part;  // base: first node of its rows
+};
+__device__ __forceinline__ int unit_share(const TreeArgs &a, int tiles) { return (tiles + a.cluster - 1) / a.cluster; }
+__device__ __forceinline__ TreeUnit unit_of(const TreeArgs &a, int cta) {
+  const int u = cta / a.cluster, sh = u / a.tiles_x;
+  return {sh / a.Hkv, sh % a.Hkv, (u - sh * a.tiles_x) * 2 * a.nodes_tile, cta - u * a.cluster};
+}
+
 // A piece: key tiles t0 .. t0 + nt - 1 of a unit.
 struct TreePiece {
   int s, first, T, ctx, why, h, base, tiles, t0, nt;  // base: first node of its rows
@@ -222,6 +236,72 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const uint8_t *sta
   }
 }
 
+// Values 16 chunk .. 16 chunk + 15 of a unit's row r (a lane's), from its pieces: the first in
+// CTA `first` and one in every `step`-th behind it.  row0, h, left: the first row's place in q, the
+// kv head, the nodes from there on.
+template <int D>
+__device__ __forceinline__ void join_rows(const TreeArgs &a, int first, int step, int pieces, int row0, int h, int left,
+                                          int r, int chunk) {
+  const int x = r / 128, m = r % 128, n = m / a.G;
+  if (n >= a.nodes_tile || x * a.nodes_tile + n >= left) return;
+  // where the unit began (0) or went on
+  auto at = [&](int i) { return (first + (size_t)i * step) * 2 + (i == 0); };
+  float M = -INFINITY, den = 0.f;
+  bool refused = false;  // the piece with the tree's last keys says so: a sum below 0
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = 4;  // pieces on their way at once
+  for (int i0 = 0; i0 < pieces; i0 += U) {
+    float2 ml[U];
+    float4 v[U][4];
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t p = at(min(i0 + u, pieces - 1));
+      ml[u] = __ldcg(a.ws_ml + p * a.prow + r);
+      const float4 *o = a.ws_o + (p * (D / 4) + chunk * 4) * a.prow + r;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[u][k] = __ldcg(o + (size_t)k * a.prow);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= pieces) ml[u].y = 0.f;
+      refused |= ml[u].y < 0.f;
+      if (ml[u].y != 0.f) Mn = fmaxf(Mn, ml[u].x);
+    }
+    const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);  // (nothing so far: nothing to scale)
+    M = Mn;
+    den *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k].x *= f, acc[k].y *= f, acc[k].z *= f, acc[k].w *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].y == 0.f) continue;
+      const float w = M == -INFINITY ? 1.f : exp2f(ml[u].x - M);  // (-infinity: a NaN sum without a maximum)
+      den += w * ml[u].y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[k].x += w * v[u][k].x, acc[k].y += w * v[u][k].y;
+        acc[k].z += w * v[u][k].z, acc[k].w += w * v[u][k].w;
+      }
+    }
+  }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  const size_t row = (size_t)(row0 + x * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (m - n * a.G);
+  uint4 *out = reinterpret_cast<uint4 *>(a.out + row * D + chunk * 16);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (den != 0.f && !refused) {
+      const float4 p = acc[2 * k], q = acc[2 * k + 1];
+      y = make_uint4(pack_bf16(p.x * inv, p.y * inv), pack_bf16(p.z * inv, p.w * inv), pack_bf16(q.x * inv, q.y * inv),
+                     pack_bf16(q.z * inv, q.w * inv));
+    }
+    out[k] = y;
+  }
+}
+
 // A wait without an end: the first to give up says so.
 __device__ __noinline__ void tree_late(volatile int *dead, int32_t *err) {
   if (*dead) return;
@@ -230,7 +310,8 @@ __device__ __noinline__ void tree_late(volatile int *dead, int32_t *err) {
 }
 
 // ROWS2: the softmax warpgroups have a row tile each, else half of each key tile.
-template <int D, int B, bool ROWS2>
+// CLUSTER: a cluster does a unit, else shares.
+template <int D, int B, bool ROWS2, bool CLUSTER>
 __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
@@ -296,67 +377,88 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
+  // where a cluster does a unit: which, and (the producers) its tree and this CTA's first pages
+  TreeUnit unit{};
+  if constexpr (CLUSTER) unit = unit_of(a, blockIdx.x);
   grid_wait();
   grid_launch_dependents();
-
+  TreeSeq seq{};
+  int page = -1;
   // ---- this CTA's share of all units' key tiles.  Trees of several CTAs' rows: CTAs
   // side by side take the same share of the keys, a pair of row tiles each, and a page
   // comes from HBM once.  Where that leaves too many without rows (trees much smaller
   // than the largest may be), the pairs are units by themselves: nine trees of 1 to 61
   // nodes, seven heads a kv head, 34.0 us, 36.9 side by side; eight of 64 nodes over 32K
   // tokens 426, side by side 412.
-  long long mine[2] = {0, 0};  // side by side; flat
+  long long mine[2] = {0, 0}, before[2] = {0, 0};  // side by side; flat
+  long long all = 0, beg = 0, end = 0;
+  bool flat = false;
+  int step = 1, share = 0, shares = 0, tx = 0;
   const int per = (a.S + kThreads - 1) / kThreads;
-  for (int s = tid * per; s < min(a.S, (tid + 1) * per); ++s) {
-    const TreeSeq q = tree_seq(a, s, B);
-    const long long n = (long long)unit_cost(q.tiles) * a.Hkv;
-    mine[0] += n;
-    if (ROWS2) mine[1] += n * row_pairs(a, q.count, q.why);
-    if (q.why && blockIdx.x == 0 && a.err) atomicOr(a.err, q.why);
-  }
-  long long total[2] = {0, 0}, before[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < (ROWS2 ? 2 : 1); ++i) {
-    before[i] = mine[i];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, before[i], o);
-      if (lane >= o) before[i] += v;
+  if constexpr (CLUSTER) {
+    if (warp == kTProducerK || warp == kTProducerV) {
+      seq = tree_seq(a, unit.s, B);
+      const int i = unit.part * unit_share(a, seq.tiles) * PAGES + lane;
+      if (!seq.why && lane < PAGES && i < (seq.ctx + seq.count + B - 1) / B)
+        page = __ldg(a.bt + (size_t)unit.s * a.max_blocks + i);
     }
-    if (lane == 31) scan[i * 16 + warp] = before[i];
-    before[i] -= mine[i];
+  } else {
+    for (int s = tid * per; s < min(a.S, (tid + 1) * per); ++s) {
+      const TreeSeq q = tree_seq(a, s, B);
+      const long long n = (long long)unit_cost(q.tiles) * a.Hkv;
+      mine[0] += n;
+      if (ROWS2) mine[1] += n * row_pairs(a, q.count, q.why);
+      if (q.why && blockIdx.x == 0 && a.err) atomicOr(a.err, q.why);
+    }
+#pragma unroll
+    for (int i = 0; i < (ROWS2 ? 2 : 1); ++i) {
+      before[i] = mine[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before[i], o);
+        if (lane >= o) before[i] += v;
+      }
+      if (lane == 31) scan[i * 16 + warp] = before[i];
+      before[i] -= mine[i];
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (!CLUSTER) {
+    long long total[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < (ROWS2 ? 2 : 1); ++i)
+    for (int i = 0; i < (ROWS2 ? 2 : 1); ++i)
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before[i] += scan[i * 16 + w];
-      total[i] += scan[i * 16 + w];
-    }
-  const int beside = gridDim.x / a.tiles_x;  // shares, with the row tiles side by side
-  const bool flat = ROWS2 && total[1] * beside * 8 < total[0] * gridDim.x * 7;
-  const int step = flat ? 1 : a.tiles_x, share = blockIdx.x / step, tx = blockIdx.x % step;
-  const long long all = flat ? total[1] : total[0], at0 = flat ? before[1] : before[0];
-  const int shares = (int)min((long long)(flat ? gridDim.x : beside), all);
-  const long long beg = share < shares ? share_begin(all, shares, share) : 0;
-  const long long end = share < shares ? share_begin(all, shares, share + 1) : 0;
-  if (beg < end && beg >= at0 && beg < at0 + (flat ? mine[1] : mine[0])) {
-    long long at = at0;
-    for (int s = tid * per;; ++s) {
-      const TreeSeq q = tree_seq(a, s, B);
-      const long long n = (long long)unit_cost(q.tiles) * a.Hkv * (flat ? row_pairs(a, q.count, q.why) : 1);
-      if (beg < at + n) {
-        *start_s = s;
-        *start_off = beg - at;
-        break;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before[i] += scan[i * 16 + w];
+        total[i] += scan[i * 16 + w];
       }
-      at += n;
+    const int beside = gridDim.x / a.tiles_x;  // shares, with the row tiles side by side
+    flat = ROWS2 && total[1] * beside * 8 < total[0] * gridDim.x * 7;
+    step = flat ? 1 : a.tiles_x, share = blockIdx.x / step, tx = blockIdx.x % step;
+    const long long at0 = flat ? before[1] : before[0];
+    all = flat ? total[1] : total[0];
+    shares = (int)min((long long)(flat ? gridDim.x : beside), all);
+    if (share < shares) {
+      beg = share_begin(all, shares, share);
+      end = share_begin(all, shares, share + 1);
     }
+    if (beg < end && beg >= at0 && beg < at0 + (flat ? mine[1] : mine[0])) {
+      long long at = at0;
+      for (int s = tid * per;; ++s) {
+        const TreeSeq q = tree_seq(a, s, B);
+        const long long n = (long long)unit_cost(q.tiles) * a.Hkv * (flat ? row_pairs(a, q.count, q.why) : 1);
+        if (beg < at + n) {
+          *start_s = s;
+          *start_off = beg - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const uint32_t tmem = *tslot;
   auto wait = [&](int b, uint32_t parity) -> bool {
     if (*dead) return false;
@@ -387,64 +489,70 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       // the share's next piece of a unit that has rows for this CTA (nt == 0: no more)
       auto next_piece = [&]() {
         TreePiece p{};
-        while (pos < end) {
-          if (s >> 5 != window) {
-            window = s >> 5;
-            near = TreeSeq{};
-            if (window * 32 + lane < a.S) near = tree_seq(a, window * 32 + lane, B);
+        if constexpr (CLUSTER) {  // the unit's part for this CTA of its cluster
+          if (pos++ > 0) return p;
+          p.s = unit.s, p.first = seq.first, p.T = seq.count, p.ctx = seq.ctx, p.why = seq.why, p.h = unit.h;
+          p.base = unit.base, p.tiles = seq.tiles;
+          const int n = unit_share(a, seq.tiles);
+          p.t0 = unit.part * n;
+          p.nt = seq.why ? seq.tiles > 0 && unit.part == 0 && unit.base == 0
+                         : seq.count > unit.base ? max(min(n, seq.tiles - p.t0), 0) : 0;
+          if (seq.why && a.err && kv && unit.part == 0 && unit.h == 0 && unit.base == 0 && lane == 0)
+            atomicOr(a.err, seq.why);
+          return p;
+        } else {
+          while (pos < end) {
+            if (s >> 5 != window) {
+              window = s >> 5;
+              near = TreeSeq{};
+              if (window * 32 + lane < a.S) near = tree_seq(a, window * 32 + lane, B);
+            }
+            const int tiles = __shfl_sync(0xffffffffu, near.tiles, s & 31);
+            if (tiles == 0) {
+              ++s;
+              continue;
+            }
+            p.s = s;
+            p.first = __shfl_sync(0xffffffffu, near.first, s & 31);
+            p.T = __shfl_sync(0xffffffffu, near.count, s & 31);
+            p.ctx = __shfl_sync(0xffffffffu, near.ctx, s & 31);
+            p.why = __shfl_sync(0xffffffffu, near.why, s & 31);
+            p.tiles = tiles;
+            // the unit's first kTUnitCost places stand for what it costs besides its tiles
+            const int cost = unit_cost(tiles), pairs = flat ? row_pairs(a, p.T, p.why) : 1, unit = (int)(off / cost);
+            p.h = flat ? unit / pairs : unit;
+            p.base = ROWS2 ? (flat ? unit - p.h * pairs : tx) * 2 * a.nodes_tile : 0;
+            const int from = (int)(off - (long long)unit * cost), n = (int)min((long long)(cost - from), end - pos);
+            p.t0 = max(from - kTUnitCost, 0);
+            p.nt = max(from + n - kTUnitCost, 0) - p.t0;
+            pos += n;
+            off += n;
+            p.unit_end = pos + (cost - from - n);
+            if (off == (long long)cost * a.Hkv * pairs) {
+              off = 0;
+              ++s;
+            }
+            if (p.nt > 0 && (p.why ? p.base == 0 : p.T > p.base)) return p;
           }
-          const int tiles = __shfl_sync(0xffffffffu, near.tiles, s & 31);
-          if (tiles == 0) {
-            ++s;
-            continue;
-          }
-          p.s = s;
-          p.first = __shfl_sync(0xffffffffu, near.first, s & 31);
-          p.T = __shfl_sync(0xffffffffu, near.count, s & 31);
-          p.ctx = __shfl_sync(0xffffffffu, near.ctx, s & 31);
-          p.why = __shfl_sync(0xffffffffu, near.why, s & 31);
-          p.tiles = tiles;
-          // the unit's first kTUnitCost places stand for what it costs besides its tiles
-          const int cost = unit_cost(tiles), pairs = flat ? row_pairs(a, p.T, p.why) : 1, unit = (int)(off / cost);
-          p.h = flat ? unit / pairs : unit;
-          p.base = ROWS2 ? (flat ? unit - p.h * pairs : tx) * 2 * a.nodes_tile : 0;
-          const int from = (int)(off - (long long)unit * cost), n = (int)min((long long)(cost - from), end - pos);
-          p.t0 = max(from - kTUnitCost, 0);
-          p.nt = max(from + n - kTUnitCost, 0) - p.t0;
-          pos += n;
-          off += n;
-          p.unit_end = pos + (cost - from - n);
-          if (off == (long long)cost * a.Hkv * pairs) {
-            off = 0;
-            ++s;
-          }
-          if (p.nt > 0 && (p.why ? p.base == 0 : p.T > p.base)) return p;
+          p.nt = 0;
+          return p;
         }
-        p.nt = 0;
-        return p;
       };
-      auto page_id = [&](int s, int keys, int t) {  // this lane's page of a sequence's key tile t (-1: none)
-        const int i = t * PAGES + lane;
-        int pg = -1;
-        if (lane < PAGES && i < (keys + B - 1) / B) {
-          pg = __ldg(a.bt + (size_t)s * a.max_blocks + i);
-          if (pg < 0 || pg >= a.num_blocks) {
-            if (a.err) atomicOr(a.err, PA_DEVERR_PAGE);
-            pg = -1;
-          }
-        }
-        return pg;
+      // this lane's page of a sequence's key tile t, if it has one (what is there is looked at later)
+      auto has_page = [&](int keys, int t) { return lane < PAGES && t * PAGES + lane < (keys + B - 1) / B; };
+      auto page_of = [&](int s, int keys, int t) {
+        return has_page(keys, t) ? __ldg(a.bt + (size_t)s * a.max_blocks + t * PAGES + lane) : -1;
       };
       int u = 0, qn = 0, jall = 0;
       bool ok = true, goes_on = false;
       TreePiece p{}, n{};  // the piece under way (nt == 0: none yet) and the one behind it
-      int cur = -1;
+      int next = page;  // of the key tile to come
       auto keys = [](const TreePiece &p) { return p.nt > 0 && !p.why ? p.ctx + p.T : 0; };
       while (true) {
         n = next_piece();
         if (p.nt == 0) {
           if (n.nt == 0) break;
-          cur = page_id(n.s, keys(n), n.t0);
+          if (!CLUSTER) next = page_of(n.s, keys(n), n.t0);
           p = n;
           continue;
         }
@@ -468,7 +576,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             w[PP_LAST] = p.t0 + p.nt == p.tiles;
             mbar_arrive(&bars[L::kUFull + pb]);
             // (the last piece is in the share that has the unit's last tile)
-            if (slot == 1)
+            if (!CLUSTER && slot == 1)
               a.ws_next[blockIdx.x] =
                   make_int4(p.first + p.base, p.h | step << 16, left, (int)((p.unit_end * shares - 1) / all) - share + 1);
           }
@@ -502,10 +610,12 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             return true;
           };
           for (int t = p.t0; ok && t < p.t0 + p.nt; ++t, ++jall) {
-            const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0);
             const int item = 2 * jall + kv, sl = item % NS;
             uint64_t *bar = &bars[L::kFull + sl];
             if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
+            const bool has = has_page(p.ctx + p.T, t), good = has && next >= 0 && next < a.num_blocks;
+            if (has && !good && a.err) atomicOr(a.err, PA_DEVERR_PAGE);
+            const uint32_t have = __ballot_sync(0xffffffffu, good);
             if (lane == 0) {
               pages_of[kv * 8 + (jall & 7)] = have;
               if (have)
@@ -514,18 +624,18 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
                 mbar_arrive(bar);
             }
             __syncwarp();
-            if (cur >= 0)
+            if (good)
               tma_load_4d_hint(smem + L::kOffRing + sl * L::kTile + lane * B * D * 2, map, 0, 0, 0,
-                               (cur * a.Hkv + p.h) * (B / 8), bar, pol);
+                               (next * a.Hkv + p.h) * (B / 8), bar, pol);
             // the next tile's page on its way meanwhile, or that of the next piece's first
             const bool more = t + 1 < p.t0 + p.nt;
-            cur = page_id(more ? p.s : n.s, keys(more ? p : n), more ? t + 1 : n.t0);
+            next = page_of(more ? p.s : n.s, keys(more ? p : n), more ? t + 1 : n.t0);
             if (q_due && !(ok = queries(!more || 2 * jall + 3 - NS >= 2 * first))) break;
           }
           if (!q_due) ++qn;
           if (!ok) break;
         }
-        if (p.why) cur = page_id(n.s, keys(n), n.t0);
+        if (p.why) next = page_of(n.s, keys(n), n.t0);
         p = n;
         if (p.nt == 0) break;
       }
@@ -1114,76 +1224,30 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (CLUSTER && a.cluster > 1) {  // the pieces are in the workspace: joined by all of the cluster
+    cluster_arrive();
+    if (warp < 8) {
+      const TreeUnit u = unit_of(a, blockIdx.x);
+      const TreeSeq q = tree_seq(a, u.s, B);
+      const int n = unit_share(a, q.tiles);
+      cluster_wait();
+      if (!q.why && q.count > u.base && q.tiles > n)
+        for (int i = u.part * 8 + warp; i < a.prow / 32 * (D / 16); i += a.cluster * 8)
+          join_rows<D>(a, blockIdx.x - u.part, 1, (q.tiles + n - 1) / n, q.first + u.base, u.h, q.count - u.base,
+                       i / (D / 16) * 32 + lane, i % (D / 16));
+    }
+  }
 }
 
 // Joins the pieces of units that several shares hold.  grid (32 rows, CTA of the
-// first kernel): the one whose share a unit begins in; a lane a row, a warp 16 of
-// its values.
+// first kernel): the one whose share a unit begins in; a warp 16 values of the rows.
 template <int D>
 __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
   grid_wait();
   const int4 next = a.ws_next[blockIdx.y];
-  const int pieces = next.w, step = next.y >> 16, h = next.y & 0xffff;
-  if (pieces == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x * 32 + lane;
-  const int x = r / 128, m = r % 128, n = m / a.G;
-  if (n >= a.nodes_tile || x * a.nodes_tile + n >= next.z) return;
-  // piece i, in a later share: where the unit began (0) or went on
-  auto at = [&](int i) { return (blockIdx.y + (size_t)i * step) * 2 + (i == 0); };
-  float M = -INFINITY, den = 0.f;
-  bool refused = false;  // the piece with the tree's last keys says so: a sum below 0
-  float4 acc[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int U = 4;  // pieces on their way at once
-  for (int i0 = 0; i0 < pieces; i0 += U) {
-    float2 ml[U];
-    float4 v[U][4];
-    float Mn = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const size_t p = at(min(i0 + u, pieces - 1));
-      ml[u] = a.ws_ml[p * a.prow + r];
-      const float4 *o = a.ws_o + (p * (D / 4) + warp * 4) * a.prow + r;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[u][k] = o[(size_t)k * a.prow];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u >= pieces) ml[u].y = 0.f;
-      refused |= ml[u].y < 0.f;
-      if (ml[u].y != 0.f) Mn = fmaxf(Mn, ml[u].x);
-    }
-    const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);  // (nothing so far: nothing to scale)
-    M = Mn;
-    den *= f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k].x *= f, acc[k].y *= f, acc[k].z *= f, acc[k].w *= f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (ml[u].y == 0.f) continue;
-      const float w = M == -INFINITY ? 1.f : exp2f(ml[u].x - M);  // (-infinity: a NaN sum without a maximum)
-      den += w * ml[u].y;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[k].x += w * v[u][k].x, acc[k].y += w * v[u][k].y;
-        acc[k].z += w * v[u][k].z, acc[k].w += w * v[u][k].w;
-      }
-    }
-  }
-  const float inv = den != 0.f ? 1.f / den : 0.f;
-  const size_t row = (size_t)(next.x + x * a.nodes_tile + n) * a.Hq + (size_t)h * a.G + (m - n * a.G);
-  uint4 *out = reinterpret_cast<uint4 *>(a.out + row * D + warp * 16);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    uint4 y = make_uint4(0u, 0u, 0u, 0u);
-    if (den != 0.f && !refused) {
-      const float4 p = acc[2 * k], q = acc[2 * k + 1];
-      y = make_uint4(pack_bf16(p.x * inv, p.y * inv), pack_bf16(p.z * inv, p.w * inv), pack_bf16(q.x * inv, q.y * inv),
-                     pack_bf16(q.z * inv, q.w * inv));
-    }
-    out[k] = y;
-  }
+  if (next.w > 0)
+    join_rows<D>(a, blockIdx.y, next.y >> 16, next.w, next.x, next.y & 0xffff, next.z, blockIdx.x * 32 + (threadIdx.x & 31),
+                 threadIdx.x >> 5);
 }
 
 int validate_tree(const pa_decode_desc *d, int max_nodes) {
@@ -1195,7 +1259,7 @@ int validate_tree(const pa_decode_desc *d, int max_nodes) {
 
 // How a call is laid out; the workspace is for pieces, so none where a unit is one tile.
 struct TreePlan {
-  int nodes_tile, row_tiles, tiles_x, ctas, prow;
+  int nodes_tile, row_tiles, tiles_x, ctas, cluster, prow;
   bool split;
   size_t o_bytes, ml_bytes, next_bytes;
   size_t total() const { return o_bytes + ml_bytes + next_bytes; }
@@ -1211,29 +1275,38 @@ TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   const long long units = std::max<long long>(1, (long long)d->num_seqs * d->num_kv_heads) * p.tiles_x;
   p.ctas = (int)std::max<long long>(p.tiles_x, std::min<long long>(sms, units * (tiles + kTUnitCost)));
   p.split = tiles > 1;  // (a unit of one tile is in one share)
+  if (units <= sms) {
+    int c = 1;
+    while (c < kTCluster && c < tiles && units * 2 * c <= sms) c *= 2;
+    if ((tiles + c - 1) / c <= kTClusterTiles) {
+      p.cluster = c;
+      p.ctas = (int)units * c;
+      p.split = c > 1;
+    }
+  }
   p.prow = p.row_tiles == 2 ? 2 * kTM : (std::min(kTM, max_nodes * G) + 31) / 32 * 32;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   if (p.split) {
     const size_t n = (size_t)p.ctas;
     p.o_bytes = up(n * 2 * p.prow * d->head_dim * sizeof(float));
     p.ml_bytes = up(n * 2 * p.prow * sizeof(float2));
-    p.next_bytes = up(n * sizeof(int4));
+    p.next_bytes = p.cluster ? 0 : up(n * sizeof(int4));
   }
   return p;
 }
 
-template <int D, int B, bool ROWS2>
+template <int D, int B, bool ROWS2, bool CLUSTER>
 int launch_tree(const TreePlan &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                 const TreeArgs &a, cudaStream_t st) {
   using L = TreeSmem<D, ROWS2>;
-  auto kern = tree_kernel<D, B, ROWS2>;
+  auto kern = tree_kernel<D, B, ROWS2, CLUSTER>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
     return PA_ERR_CUDA;
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PA_ERR_CUDA;
   if (fa.numRegs < L::kRegsLaunch) return PA_ERR_UNSUPPORTED;  // the register split would not fit
-  int r = launch_dependent(kern, dim3(p.ctas), L::kThreads, L::kAlloc, 1, st, tq, tk, tv, a);
-  if (r == PA_OK && p.split)
+  int r = launch_dependent(kern, dim3(p.ctas), L::kThreads, L::kAlloc, std::max(1, p.cluster), st, tq, tk, tv, a);
+  if (r == PA_OK && p.split && !CLUSTER)
     r = launch_dependent(tree_join_kernel<D>, dim3(p.prow / 32, p.ctas), D * 2, 0, 1, st, a);
   return r;
 }
@@ -1276,7 +1349,7 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.ws_o = reinterpret_cast<float4 *>(ws);
     a.ws_ml = reinterpret_cast<float2 *>(ws + p.o_bytes);
-    a.ws_next = reinterpret_cast<int4 *>(ws + p.o_bytes + p.ml_bytes);
+    if (!p.cluster) a.ws_next = reinterpret_cast<int4 *>(ws + p.o_bytes + p.ml_bytes);
   }
   a.err = err_flag;
   a.S = d->num_seqs;
@@ -1292,6 +1365,7 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
   a.box = std::min(p.nodes_tile, std::min(max_tree_nodes, total_nodes));
   a.tiles_x = p.tiles_x;
   a.prow = p.prow;
+  a.cluster = p.cluster;
   a.scale_log2 = d->scale * 1.4426950408889634f;
   const uint64_t rows = (uint64_t)d->num_blocks * d->num_kv_heads * d->block_size;
   CUtensorMap tq, tk, tv;
@@ -1304,8 +1378,11 @@ extern "C" int pa_paged_attention_decode_tree(const pa_decode_desc *d, const voi
   // call may come between the two on the stream, whatever thread makes it.
   static std::mutex both;
   const std::lock_guard<std::mutex> lock(both);
-#define PA_TREE(D_, B_)                                                            \
-  (p.row_tiles == 1 ? launch_tree<D_, B_, false>(p, tq, tk, tv, a, st) : launch_tree<D_, B_, true>(p, tq, tk, tv, a, st))
+#define PA_TREE(D_, B_)                                                                    \
+  (p.cluster ? p.row_tiles == 1 ? launch_tree<D_, B_, false, true>(p, tq, tk, tv, a, st)    \
+                                : launch_tree<D_, B_, true, true>(p, tq, tk, tv, a, st)     \
+   : p.row_tiles == 1 ? launch_tree<D_, B_, false, false>(p, tq, tk, tv, a, st)             \
+                      : launch_tree<D_, B_, true, false>(p, tq, tk, tv, a, st))
   if (d->head_dim == 128) return d->block_size == 16 ? PA_TREE(128, 16) : PA_TREE(128, 32);
   return d->block_size == 16 ? PA_TREE(64, 16) : PA_TREE(64, 32);
 #undef PA_TREE
