@@ -12,7 +12,8 @@
 // A unit is (sequence, kv head) with its keys in tiles of 128; the units' tiles,
 // one unit after another, are cut into equal shares, one for each CTA (persistent,
 // one an SM), whatever the lengths.  A share's pieces of units that other shares
-// go on with leave partial softmax states, which a second kernel joins.  The rows
+// go on with leave partial softmax states, which a second kernel joins.  (Few short
+// units: a cluster each, which joins them itself.)  The rows
 // are the MMA's M side: a row tile is 128 rows (floor(128 / G) nodes).  Trees of
 // one row tile have the CTA's two softmax warpgroups take half of every key tile
 // each, with a running state of its own, joined at the piece's end (so that a
@@ -43,7 +44,7 @@
 // Measured: 64 x 5 nodes over 128..2048 tokens 59 us (307 MB, 5.2 TB/s), 32 x 16..32
 // nodes over 512..8192 92.5 (548 MB, 5.9 TB/s), nine trees of 1 to 61 nodes with seven
 // heads a kv head 34, 8 x 64 nodes over 32K tokens 405 (1.36 PFLOP/s), one of 8 nodes
-// over 1000 10.5.  Of the 59, about 4 go by before the first tiles come, 4 are the join
+// over 1000 9.1.  Of the 59, about 4 go by before the first tiles come, 4 are the join
 // and 4 that the CTAs do not end together.  With two row tiles a key tile takes 3600
 // cycles, 2050 of them MMAs: a row tile's scores, softmax (1800) and product follow one
 // another, and TMEM has no room for scores ahead (2 x 128 columns of S, as many of O).
@@ -97,8 +98,13 @@ constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTChecker = 11, k
 // what its pieces cost besides (64 x 5 nodes with 1, 2, 3, 4: 61.8, 59.6, 59.4, 60.9 us,
 // one to 61 nodes, seven heads a kv head 34.8, 33.7, 33.8, 34.2).
 constexpr int kTUnitCost = 3;
-constexpr int kTCluster = 8;       // CTAs of a unit, at most, where a cluster does one
-constexpr int kTClusterTiles = 8;  // key tiles of such a CTA, at most
+// Few short units: each a cluster's, which joins its pieces itself, in one launch and
+// without the search for a share.  Of the SMs that a unit then may take (8 at most), none
+// has more than 8 key tiles of the longest context: 8 nodes, 8 kv heads, one sequence of
+// 100, 1000, 4000, 8000 tokens 7.5, 10.5, 14.0, 17.9 us, by shares 9.2, 12.1, 17.4, 20.4
+// (of 16000, with 16 tiles a CTA, 26.9 and 25.1), 16 of up to 1000 18.5 and 23.9.
+constexpr int kTCluster = 8;
+constexpr int kTClusterTiles = 8;
 
 template <int D, bool ROWS2>
 struct TreeSmem {
