@@ -102,7 +102,9 @@ constexpr int kTUnitCost = 3;
 // without the search for a share.  Of the SMs that a unit then may take (8 at most), none
 // has more than 8 key tiles of the longest context: 8 nodes, 8 kv heads, one sequence of
 // 100, 1000, 4000, 8000 tokens 7.5, 10.5, 14.0, 17.9 us, by shares 9.2, 12.1, 17.4, 20.4
-// (of 16000, with 16 tiles a CTA, 26.9 and 25.1), 16 of up to 1000 18.5 and 23.9.
+// (of 16000, with 16 tiles a CTA, 26.9 and 25.1), 16 of up to 1000 18.5 and 23.9.  The
+// pieces go through the workspace here too: out of the other CTAs' shared memory 64
+// nodes over 4000 tokens took 22.2 us, so 18.3.
 constexpr int kTCluster = 8;
 constexpr int kTClusterTiles = 8;
 
@@ -563,9 +565,10 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           continue;
         }
         const int left = p.T - p.base, live = !ROWS2 || left <= a.nodes_tile ? 1 : 2;
-        if (!kv) {
+        // the piece to the other roles (behind its first K tile's copies, which take longest)
+        auto post = [&]() -> bool {
           const int slot = p.t0 > 0 ? 0 : p.nt < p.tiles ? 1 : -1, pb = u % kTPosts;
-          if (u >= kTPosts && !(ok = wait_warp(L::kUEmpty + pb, (uint32_t)((u / kTPosts - 1) & 1)))) break;
+          if (u >= kTPosts && !wait_warp(L::kUEmpty + pb, (uint32_t)((u / kTPosts - 1) & 1))) return false;
           if (lane == 0) {
             int *w = posts + pb * kTPostWords;
             w[PP_KIND] = p.why ? kPieceZero : kPiece;
@@ -588,34 +591,35 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
           }
           goes_on |= slot == 1;
           ++u;
-        }
-        if (!p.why) {
-          const int set = qn % L::kSets, first = jall;
-          bool q_due = !kv;
-          // the piece's query rows, as soon as the set is free; at the latest when a K or V
-          // tile would have to wait for this piece's own
-          auto queries = [&](bool now) -> bool {
-            if (qn >= L::kSets) {
-              const uint32_t par = (uint32_t)((qn / L::kSets - 1) & 1);
-              if (now) {
-                if (!wait_warp(L::kQEmpty + set, par)) return false;
-              } else if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[L::kQEmpty + set], par))) {
-                return true;
-              }
+          return true;
+        };
+        const int set = qn % L::kSets, first = jall;
+        bool q_due = !kv && !p.why;
+        // the piece's query rows, as soon as the set is free; at the latest when a K or V
+        // tile would have to wait for this piece's own
+        auto queries = [&](bool now) -> bool {
+          if (qn >= L::kSets) {
+            const uint32_t par = (uint32_t)((qn / L::kSets - 1) & 1);
+            if (now) {
+              if (!wait_warp(L::kQEmpty + set, par)) return false;
+            } else if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[L::kQEmpty + set], par))) {
+              return true;
             }
-            q_due = false;
-            if (lane == 0) {
-              uint64_t *bar = &bars[L::kQFull + set];
-              mbar_arrive_expect_tx(bar, (uint32_t)(live * kHalves * a.box * a.G * 128));
-              for (int x = 0; x < live; ++x)
-                for (int hf = 0; hf < kHalves; ++hf)
-                  tma_load_4d(smem + set * L::kSet + x * L::kTile + hf * kTHalf, &tmQ, hf * 64, 0, p.h,
-                              p.first + p.base + x * a.nodes_tile, bar);
-            }
-            __syncwarp();
-            return true;
-          };
-          for (int t = p.t0; ok && t < p.t0 + p.nt; ++t, ++jall) {
+          }
+          q_due = false;
+          if (lane == 0) {
+            uint64_t *bar = &bars[L::kQFull + set];
+            mbar_arrive_expect_tx(bar, (uint32_t)(live * kHalves * a.box * a.G * 128));
+            for (int x = 0; x < live; ++x)
+              for (int hf = 0; hf < kHalves; ++hf)
+                tma_load_4d(smem + set * L::kSet + x * L::kTile + hf * kTHalf, &tmQ, hf * 64, 0, p.h,
+                            p.first + p.base + x * a.nodes_tile, bar);
+          }
+          __syncwarp();
+          return true;
+        };
+        for (int t = p.t0; t < p.t0 + p.nt; ++t) {
+          if (!p.why) {
             const int item = 2 * jall + kv, sl = item % NS;
             uint64_t *bar = &bars[L::kFull + sl];
             if (item >= NS && !(ok = wait_warp(L::kEmpty + sl, (uint32_t)((item / NS - 1) & 1)))) break;
@@ -633,15 +637,16 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
             if (good)
               tma_load_4d_hint(smem + L::kOffRing + sl * L::kTile + lane * B * D * 2, map, 0, 0, 0,
                                (next * a.Hkv + p.h) * (B / 8), bar, pol);
-            // the next tile's page on its way meanwhile, or that of the next piece's first
-            const bool more = t + 1 < p.t0 + p.nt;
-            next = page_of(more ? p.s : n.s, keys(more ? p : n), more ? t + 1 : n.t0);
-            if (q_due && !(ok = queries(!more || 2 * jall + 3 - NS >= 2 * first))) break;
+            ++jall;
           }
-          if (!q_due) ++qn;
-          if (!ok) break;
+          if (!kv && t == p.t0 && !(ok = post())) break;
+          // the next tile's page on its way meanwhile, or that of the next piece's first
+          const bool more = t + 1 < p.t0 + p.nt;
+          next = page_of(more ? p.s : n.s, keys(more ? p : n), more ? t + 1 : n.t0);
+          if (q_due && !(ok = queries(!more || 2 * jall + 1 - NS >= 2 * first))) break;
         }
-        if (p.why) next = page_of(n.s, keys(n), n.t0);
+        if (!p.why && !q_due) ++qn;
+        if (!ok) break;
         p = n;
         if (p.nt == 0) break;
       }
