@@ -93,7 +93,7 @@ constexpr int kTHalf = kTM * 128;        // 64 columns of a row tile
 constexpr int kTPosts = 4;               // pieces posted ahead
 constexpr int kTPostWords = 16;
 constexpr int kTVotes = 4;               // tiles with a tree under way at once
-constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTChecker = 11, kTEnd = 12;  // warps
+constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTFinite = 11, kTEnd = 12;  // warps
 // A unit counts as so many key tiles more than it has when the shares are cut:
 // what its pieces cost besides (64 x 5 nodes with 1, 2, 3, 4: 61.8, 59.6, 59.4, 60.9 us,
 // one to 61 nodes, seven heads a kv head 34.8, 33.7, 33.8, 34.2).
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
       }
       umma_commit(&bars[L::kDone]);
       mbar_wait(&bars[L::kDone], 0);  // every MMA complete before TMEM is freed
-    } else if (warp == kTChecker) {
+    } else if (warp == kTFinite) {
       // ------------- value rows of the tiles with a tree
       int u = 0, jall = 0, votes = 0;
       while (true) {

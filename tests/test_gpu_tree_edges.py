@@ -9,6 +9,7 @@ import threading
 import pytest
 
 import gpu_util
+import test_gpu_decode_tree as base
 import tree_ref as tr
 
 pytestmark = pytest.mark.gpu
@@ -349,3 +350,61 @@ def test_verify_either_way(pa, torch, dtype, V, S):
     got = pa.verify_tree(x[:, :V], i32(torch, tokens), i32(torch, flat + [7]), i32(torch, cu), max_tree_nodes=8,
                          targets=targets.fill_(-5), err_flag=err)
     assert int(err) == pa.DEVERR_TREE and got[0][:9].tolist() == [-5] * 9 and got[2][0] == 0 and got[3][0] == -1
+
+
+# A call with a wide bound on the contexts cuts them into shares for the CTAs, one with a narrow one gives each
+# (sequence, kv head) a cluster: the same cases by shares.
+@pytest.fixture
+def by_shares(monkeypatch):
+    call = base.call
+    monkeypatch.setattr(base, "call", lambda pa, torch, c, **kw: call(pa, torch, c, **{"max_context_len": 1 << 20, **kw}))
+
+
+@pytest.mark.parametrize("shape", base.SHAPES)
+def test_shapes_by_shares(pa, torch, by_shares, shape):
+    base.test_small(pa, torch, *shape)
+
+
+@pytest.mark.parametrize("d,nodes,bad,which", [(64, 12, math.nan, "v"), (128, 12, -math.inf, "v"), (128, 60, math.inf, "v"),
+                                               (64, 140, math.nan, "v"), (128, 140, math.nan, "k"), (64, 12, math.inf, "k")])
+def test_values_that_are_not_finite_by_shares(pa, torch, by_shares, d, nodes, bad, which):
+    base.test_values_that_are_not_finite_reach_only_the_nodes_that_attend_them(pa, torch, d, nodes, bad, which)
+
+
+@pytest.mark.parametrize("b", [16, 32])
+def test_unwritten_slots_by_shares(pa, torch, by_shares, b):
+    base.test_unwritten_slots_do_not_reach_the_output(pa, torch, math.nan, b)
+
+
+@pytest.mark.parametrize("name", ["bad_sequences_are_zeros_and_the_others_stay", "bad_node_ranges", "bad_parents",
+                                  "every_page_outside_the_pool", "logits_of_minus_infinity", "large_logits",
+                                  "growing_logits_rescale"])
+def test_edges_by_shares(pa, torch, by_shares, name):
+    getattr(base, "test_" + name)(pa, torch)
+
+
+@pytest.mark.parametrize("nodes", [4, 60])
+def test_pages_outside_the_pool_by_shares(pa, torch, by_shares, nodes):
+    base.test_pages_outside_the_pool_are_left_out(pa, torch, nodes)
+
+
+@pytest.mark.parametrize("hq,nodes", [(8, [9, 0, 3]), (32, [20, 31, 1]), (16, [64, 70, 2])])
+def test_bounds_change_the_cut_not_the_answer(pa, torch, hq, nodes):
+    """Clusters of one to eight CTAs a unit, and shares; pieces of a unit joined or not."""
+    c = tr.make_case([700, 250, 90], nodes, hq, 2, 128, 16, seed=60)
+    ref = tr.ref_tree(c)
+    wide = torch.full((3, 8192), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c["bt"].shape[1]] = c["bt"]
+    c["bt"] = wide
+    for limit in (770, 1024, 2000, 4000, 8000, 16000, 100000):
+        out, err = attend(pa, torch, c, max_context_len=limit)
+        assert err == 0
+        tr.check(out, ref)
+    # more sequences, without trees: fewer CTAs a unit
+    for more in (7, 20, 60, 200):
+        d = dict(c, ctx=torch.cat([c["ctx"], torch.zeros(more, dtype=torch.int32, device="cuda")]),
+                 cu=torch.cat([c["cu"], c["cu"][-1:].expand(more)]),
+                 bt=torch.cat([c["bt"], torch.full((more, 8192), -1, dtype=torch.int32, device="cuda")]))
+        out, err = attend(pa, torch, d, max_context_len=1000)
+        assert err == 0
+        tr.check(out, ref)
