@@ -61,6 +61,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "pa_internal.h"
@@ -99,8 +100,9 @@ constexpr int kTProducerK = 8, kTIssuer = 9, kTProducerV = 10, kTFinite = 11, kT
 // one to 61 nodes, seven heads a kv head 34.8, 33.7, 33.8, 34.2).
 constexpr int kTUnitCost = 3;
 // Few short units: each a cluster's, which joins its pieces itself, in one launch and
-// without the search for a share.  Of the SMs that a unit then may take (8 at most), none
-// has more than 8 key tiles of the longest context: 8 nodes, 8 kv heads, one sequence of
+// without the search for a share.  All clusters run at once (16 of 8 CTAs did not: 24.9 us
+// where shares take 18.1), and of a cluster's CTAs, 8 at most, none has more than 8 key
+// tiles of the longest context: 8 nodes, 8 kv heads, one sequence of
 // 100, 1000, 4000, 8000 tokens 7.5, 10.5, 14.0, 17.9 us, by shares 9.2, 12.1, 17.4, 20.4
 // (of 16000, with 16 tiles a CTA, 26.9 and 25.1), 16 of up to 1000 18.5 and 23.9.  The
 // pieces go through the workspace here too: out of the other CTAs' shared memory 64
@@ -1276,6 +1278,38 @@ struct TreePlan {
   size_t total() const { return o_bytes + ml_bytes + next_bytes; }
 };
 
+// Clusters of 2^log2 CTAs of the tree kernel that the current device runs at once (the
+// SMs come in groups that no cluster crosses); 0 where that is not to be had.  One CTA
+// takes an SM in every form of the kernel, so one form tells.
+int clusters_at_once(int log2) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][4];  // + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  const int k = known[dev][log2].load(std::memory_order_relaxed);
+  if (k > 0) return k - 1;
+  using L = TreeSmem<128, false>;
+  auto kern = tree_kernel<128, 16, false, true>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1u << log2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(1u << log2);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev][log2].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   TreePlan p{};
   const int G = d->num_q_heads / d->num_kv_heads;
@@ -1288,7 +1322,7 @@ TreePlan make_tree_plan(const pa_decode_desc *d, int max_nodes, int sms) {
   p.split = tiles > 1;  // (a unit of one tile is in one share)
   if (units <= sms) {
     int c = 1;
-    while (c < kTCluster && c < tiles && units * 2 * c <= sms) c *= 2;
+    for (int i = 1; c < kTCluster && c < tiles && units <= clusters_at_once(i); ++i) c *= 2;
     if ((tiles + c - 1) / c <= kTClusterTiles) {
       p.cluster = c;
       p.ctas = (int)units * c;
