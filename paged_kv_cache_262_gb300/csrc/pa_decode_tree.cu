@@ -43,7 +43,7 @@
 //
 // Measured: 64 x 5 nodes over 128..2048 tokens 59 us (307 MB, 5.2 TB/s), 32 x 16..32
 // nodes over 512..8192 92.5 (548 MB, 5.9 TB/s), nine trees of 1 to 61 nodes with seven
-// heads a kv head 34, 8 x 64 nodes over 32K tokens 405 (1.36 PFLOP/s), one of 8 nodes
+// heads a kv head 33, 8 x 64 nodes over 32K tokens 405 (1.36 PFLOP/s), one of 8 nodes
 // over 1000 9.1.  Of the 59, about 4 go by before the first tiles come, 4 are the join
 // and 4 that the CTAs do not end together.  With two row tiles a key tile takes 3600
 // cycles, 2050 of them MMAs: a row tile's scores, softmax (1800) and product follow one
@@ -1257,6 +1257,7 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(D * 2) tree_join_kernel(const TreeArgs a) {
   grid_wait();
+  grid_launch_dependents();
   const int4 next = a.ws_next[blockIdx.y];
   if (next.w > 0)
     join_rows<D>(a, blockIdx.y, next.y >> 16, next.w, next.x, next.y & 0xffff, next.z, blockIdx.x * 32 + (threadIdx.x & 31),
