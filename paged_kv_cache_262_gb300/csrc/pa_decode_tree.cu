@@ -476,12 +476,12 @@ __global__ void __launch_bounds__(TreeSmem<D, ROWS2>::kThreads, 1)
     tree_late(dead, a.err);
     return false;
   };
-  // uniform over the warp (warp collectives follow)
   // a warp's arrival: what its lanes did before is before it
   auto arrive_warp = [&](int b, uint32_t n = 1) {
     __syncwarp();
     if (lane == 0) mbar_arrive_n(&bars[b], n);
   };
+  // uniform over the warp (warp collectives follow)
   auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
   if (warp >= 8) {
@@ -1271,7 +1271,7 @@ int validate_tree(const pa_decode_desc *d, int max_nodes) {
   return max_nodes > PA_MAX_TREE_NODES ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
-// How a call is laid out; the workspace is for pieces, so none where a unit is one tile.
+// How a call is laid out; the workspace is for pieces, so none where a unit is one tile or one CTA's.
 struct TreePlan {
   int nodes_tile, row_tiles, tiles_x, ctas, cluster, prow;
   bool split;
